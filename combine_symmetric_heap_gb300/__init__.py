@@ -42,6 +42,7 @@ SYM_HEAP_WINDOWS = 13
 _u64 = ctypes.c_uint64
 _u32 = ctypes.c_uint32
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 
 
@@ -58,6 +59,32 @@ class SymHeapDesc(ctypes.Structure):
                 ("off_status", _u64), ("off_ready", _u64), ("off_hist", _u64),
                 ("off_ctrl", _u64), ("num_ready", _u32), ("epoch", _u32),
                 ("wait_timeout_us", _u32), ("reserved", _u32), ("s", MoeShape)]
+
+
+class SymRows(ctypes.Structure):
+    _fields_ = [("ptr", _u64), ("ld", _i64), ("slot_stride", _i64), ("rows", _i64), ("slots", _i32),
+                ("cols", _i32)]
+
+
+class SymGroups(ctypes.Structure):
+    _fields_ = [("cnt", _u64), ("off", _u64), ("cnt_slot_stride", _i64), ("off_slot_stride", _i64),
+                ("status", _u64), ("groups", _i32), ("slots", _i32), ("wait_timeout_us", _u32),
+                ("reserved", _u32)]
+
+
+class SymBlockNorm(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i32), ("dtype", _i32), ("x", _u64), ("o", _u64), ("w_post", _u64),
+                ("gate", _u64), ("w_pre", _u64), ("y", _u64), ("h", _u64), ("rstd_post", _u64),
+                ("rstd_pre", _u64), ("ld_x", _i64), ("ld_o", _i64), ("ld_gate", _i64), ("ld_y", _i64),
+                ("ld_h", _i64), ("gate_rows", _i64), ("gate_act", _i32), ("flags", _i32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("p", ctypes.c_double), ("seed", _u64),
+                ("offset", _u64)]
+
+
+class SymBlockNormGrad(ctypes.Structure):
+    _fields_ = [("dy", _u64), ("dh", _u64), ("dx", _u64), ("d_o", _u64), ("dw_pre", _u64), ("dw_post", _u64),
+                ("dgate", _u64), ("ld_dy", _i64), ("ld_dh", _i64), ("ld_dx", _i64), ("ld_do", _i64),
+                ("ld_dgate", _i64), ("work", _u64), ("work_bytes", _u64)]
 
 
 class SymmoeError(RuntimeError):
@@ -99,6 +126,15 @@ def lib() -> ctypes.CDLL:
         L.sym_gemm_a2a.argtypes = [P(SymHeapDesc), _vp, _vp, ctypes.c_int, _vp]
         L.sym_a2a_gemm.argtypes = [P(SymHeapDesc), _vp, _vp, ctypes.c_int, _vp]
         L.moe_dispatch_layout_noalloc.argtypes = [P(MoeShape), _vp, _vp, _vp, _vp, _vp, _vp]
+        R, G = P(SymRows), P(SymGroups)
+        L.moe_grouped_matmul.argtypes = [G, ctypes.c_int, R, _vp, _i64, _i64, ctypes.c_int, R, _vp]
+        L.moe_grouped_wgrad.argtypes = [G, ctypes.c_int, R, R, _vp, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]
+        L.moe_swiglu_rows.argtypes = [ctypes.c_int, R, R, _vp, _i64, _vp, _i64, R, _vp]
+        L.moe_swiglu_rows_bwd.argtypes = [ctypes.c_int, R, R, R, _vp, _i64, _vp, _i64, R, R, _vp, _i64, _vp]
+        L.moe_dropout.argtypes = [ctypes.c_int, R, R, R, ctypes.c_double, _u64, _u64, _vp]
+        L.moe_block_norm.argtypes = [P(SymBlockNorm), _vp]
+        L.moe_block_norm_bwd.argtypes = [P(SymBlockNorm), P(SymBlockNormGrad), _vp]
+        L.moe_block_norm_workspace.argtypes = [_i64, _i32, _i64, P(_u64)]
         L.sym_strerror.argtypes = [ctypes.c_int]
         L.sym_strerror.restype = ctypes.c_char_p
         _lib = L
@@ -275,6 +311,241 @@ def sym_heap_status(heap: SymHeapDesc, clear: bool = False, stream=None) -> int:
     return st.value
 
 
+# ------------------------------------------------------------------ training through an MoE block
+# Tensors in, shapes and strides read from them.  A mismatch raises
+# SymmoeError(SYM_EINVAL) before anything is launched.
+
+SYM_BF16, SYM_FP16, SYM_FP32 = 0, 1, 2
+SYM_GM_TRANS_W = 1
+SYM_GM_ACCUMULATE = 1
+SYM_GATE_NONE, SYM_GATE_SIGMOID, SYM_GATE_TANH = 0, 1, 2
+SYM_NORM_NO_POST = 1
+_DTYPES = {torch.bfloat16: SYM_BF16, torch.float16: SYM_FP16, torch.float32: SYM_FP32}
+_GATE_ACTS = {"none": SYM_GATE_NONE, "sigmoid": SYM_GATE_SIGMOID, "tanh": SYM_GATE_TANH}
+
+
+def _need(ok: bool, where: str, why: str) -> None:
+    if not ok:
+        e = SymmoeError(SYM_EINVAL, where)
+        e.args = (f"{e.args[0]}: {why}",)
+        raise e
+
+
+def _on_device(where: str, *tensors) -> None:
+    for t in tensors:
+        if t is not None:
+            _need(isinstance(t, torch.Tensor) and t.is_cuda and t.device.index == torch.cuda.current_device(),
+                  where, "tensors of the current CUDA device are wanted")
+
+
+def _rows(t, where: str, dtype=None) -> SymRows:
+    """[rows, cols], or [slots, rows, cols] such as a heap's windows."""
+    _need(t.dim() in (2, 3) and (dtype is None or t.dtype == dtype), where,
+          "rows [R, C] or [slots, R, C] of one type are wanted")
+    slots, slot_stride = (1, 0) if t.dim() == 2 else (t.shape[0], t.stride(0))
+    rows, cols = t.shape[-2:]
+    _need(cols == 1 or t.stride(-1) == 1, where, "the last dimension has to be contiguous")
+    ld = t.stride(-2) if rows > 1 else (cols + 7) // 8 * 8
+    return SymRows(t.data_ptr(), ld, slot_stride, rows, slots, cols)
+
+
+def _per_slot(t, slots: int, n: int, dtype, where: str) -> int:
+    """Slot stride of a [slots, n] (or, with one slot, [n]) tensor."""
+    _need(t.dtype == dtype and t.shape in ((slots, n), (n,) if slots == 1 else (slots, n)) and
+          (n == 1 or t.stride(-1) == 1), where, f"[{slots}, {n}] {dtype} is wanted")
+    return t.stride(0) if t.dim() == 2 else 0
+
+
+def _groups(cnt, off, rows: SymRows, status, where: str) -> SymGroups:
+    g = cnt.numel()
+    _need(g > 0 and g % rows.slots == 0, where, "the slots have equally many groups")
+    each = g // rows.slots
+    cs = _per_slot(cnt, rows.slots, each, torch.int32, where)
+    os_ = _per_slot(off, rows.slots, each, torch.int32, where)
+    _need(status is None or (status.dtype == torch.int32 and status.numel() >= 1), where, "status is an int32 word")
+    return SymGroups(cnt.data_ptr(), off.data_ptr(), cs, os_, 0 if status is None else status.data_ptr(), g,
+                     rows.slots, 0, 0)
+
+
+def _matrices(w, groups: int, shape, where: str):
+    _need(w.dim() == 3 and tuple(w.shape) == (groups, *shape) and (w.shape[2] == 1 or w.stride(2) == 1), where,
+          f"one matrix for each group, [{groups}, {shape[0]}, {shape[1]}], is wanted")
+    return w.stride(0), (w.stride(1) if w.shape[1] > 1 else (w.shape[2] + 7) // 8 * 8)
+
+
+def moe_grouped_matmul(x, w, cnt, off, out, trans_w: bool = False, status=None, stream=None) -> None:
+    """out[r] = w[e] @ x[r] for the rows r of group e (w [E, F, C]), or with
+    trans_w x[r] @ w[e] (w [E, C, F]: on a forward product's weights, its data
+    gradient).  x [R, C] or [slots, R, C]; cnt, off: int32 rows and first row
+    of each group, [E] or [slots, E / slots]; bf16 or fp16."""
+    where = "moe_grouped_matmul"
+    _on_device(where, x, w, cnt, off, out, status)
+    rx, ro = _rows(x, where), _rows(out, where, x.dtype)
+    g = _groups(cnt, off, rx, status, where)
+    _need(w.dtype == x.dtype, where, "x, w and out have one type")
+    ws, wl = _matrices(w, g.groups, (rx.cols, ro.cols) if trans_w else (ro.cols, rx.cols), where)
+    _check(lib().moe_grouped_matmul(ctypes.byref(g), _DTYPES.get(x.dtype, -1), ctypes.byref(rx), w.data_ptr(), ws, wl,
+                                    SYM_GM_TRANS_W if trans_w else 0, ctypes.byref(ro), _stream(stream)), where)
+
+
+def moe_grouped_wgrad(dy, x, cnt, off, dw, accumulate: bool = False, status=None, stream=None) -> None:
+    """dw[e] = dy_e^T x_e over the rows of group e (added to dw with
+    accumulate); dw [E, F, C] of the inputs' type or float32."""
+    where = "moe_grouped_wgrad"
+    _on_device(where, dy, x, cnt, off, dw, status)
+    ry, rx = _rows(dy, where, x.dtype), _rows(x, where)
+    g = _groups(cnt, off, rx, status, where)
+    ws, wl = _matrices(dw, g.groups, (ry.cols, rx.cols), where)
+    _check(lib().moe_grouped_wgrad(ctypes.byref(g), _DTYPES.get(x.dtype, -1), ctypes.byref(ry), ctypes.byref(rx),
+                                   dw.data_ptr(), ws, wl, _DTYPES.get(dw.dtype, -1),
+                                   SYM_GM_ACCUMULATE if accumulate else 0, _stream(stream)), where)
+
+
+def _row_words(t, rows: SymRows, dtype, where: str):
+    """(address, slot stride) of one word for each row, or none."""
+    return (None, 0) if t is None else (t.data_ptr(), _per_slot(t, rows.slots, rows.rows, dtype, where))
+
+
+def _totals(total, rows: SymRows, where: str):
+    if total is None:
+        return None, 0
+    _need(total.dtype == torch.int32 and total.numel() == rows.slots and total.dim() <= 2, where,
+          "total is one int32 for each slot")
+    return total.data_ptr(), (total.stride(0) if total.dim() and rows.slots > 1 else 0)
+
+
+def moe_swiglu_rows(g, u, h, row_w=None, total=None, stream=None) -> None:
+    """h = row_w * silu(g) * u; row_w float32 [R] or [slots, R]; total: int32
+    rows to do in each slot (all without it)."""
+    where = "moe_swiglu_rows"
+    _on_device(where, g, u, h, row_w, total)
+    rg, ru, rh = _rows(g, where), _rows(u, where, g.dtype), _rows(h, where, g.dtype)
+    rw, rws = _row_words(row_w, rg, torch.float32, where)
+    tt, ts = _totals(total, rg, where)
+    _check(lib().moe_swiglu_rows(_DTYPES.get(g.dtype, -1), ctypes.byref(rg), ctypes.byref(ru), rw, rws, tt, ts,
+                                 ctypes.byref(rh), _stream(stream)), where)
+
+
+def moe_swiglu_rows_bwd(g, u, dh, dg, du, row_w=None, d_row_w=None, total=None, stream=None) -> None:
+    """Gradients of moe_swiglu_rows: dg, du and, where given, d_row_w."""
+    where = "moe_swiglu_rows_bwd"
+    _on_device(where, g, u, dh, dg, du, row_w, d_row_w, total)
+    rg, ru, rh = _rows(g, where), _rows(u, where, g.dtype), _rows(dh, where, g.dtype)
+    r1, r2 = _rows(dg, where, g.dtype), _rows(du, where, g.dtype)
+    rw, rws = _row_words(row_w, rg, torch.float32, where)
+    dw, dws = _row_words(d_row_w, rg, torch.float32, where)
+    tt, ts = _totals(total, rg, where)
+    _check(lib().moe_swiglu_rows_bwd(_DTYPES.get(g.dtype, -1), ctypes.byref(rg), ctypes.byref(ru), ctypes.byref(rh),
+                                     rw, rws, tt, ts, ctypes.byref(r1), ctypes.byref(r2), dw, dws, _stream(stream)),
+           where)
+
+
+def moe_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, stream=None) -> None:
+    """y = residual + x * keep / (1 - p); element i is kept by word i of the
+    counter-based stream (seed, offset).  On y's gradient the same call is the
+    backward pass."""
+    where = "moe_dropout"
+    _on_device(where, x, y, residual)
+    rx, ry = _rows(x, where), _rows(y, where, x.dtype)
+    rr = None if residual is None else ctypes.byref(_rows(residual, where, x.dtype))
+    _check(lib().moe_dropout(_DTYPES.get(x.dtype, -1), ctypes.byref(rx), rr, ctypes.byref(ry), p, seed, offset,
+                             _stream(stream)), where)
+
+
+def _block(where: str, stream_t, rows: int, cols: int, *, o, w_post, gate, gate_act, scale, p, seed, offset, w_pre,
+           rstd_post, rstd_pre, post_norm, eps, x=None, y=None, h=None) -> SymBlockNorm:
+    dt = stream_t.dtype
+
+    def rows_of(t, n=rows):
+        if t is None:
+            return 0, 0
+        r = _rows(t, where, dt)
+        _need(t.dim() == 2 and r.rows == n and r.cols == cols, where, f"[{n}, {cols}] is wanted")
+        return r.ptr, r.ld
+
+    def vector(t, n, dtype):
+        _need(t is None or (t.dtype == dtype and tuple(t.shape) == (n,) and (n <= 1 or t.stride(0) == 1)), where,
+              f"[{n}] {dtype} is wanted")
+        return 0 if t is None else t.data_ptr()
+
+    a = SymBlockNorm(rows=rows, cols=cols, dtype=_DTYPES.get(dt, -1), w_post=vector(w_post, cols, dt),
+                     w_pre=vector(w_pre, cols, dt), rstd_post=vector(rstd_post, rows, torch.float32),
+                     rstd_pre=vector(rstd_pre, rows, torch.float32), gate_act=_GATE_ACTS.get(gate_act, -1),
+                     flags=0 if post_norm else SYM_NORM_NO_POST, scale=scale, eps=eps, p=p, seed=seed, offset=offset)
+    a.x, a.ld_x = rows_of(x)
+    a.o, a.ld_o = rows_of(o)
+    a.y, a.ld_y = rows_of(y)
+    a.h, a.ld_h = rows_of(h)
+    if gate is not None:
+        _need(gate.dim() == 2, where, "gate is [gate_rows, cols]")
+        a.gate_rows = gate.shape[0]
+        a.gate, a.ld_gate = rows_of(gate, gate.shape[0])
+    return a
+
+
+def moe_block_norm(x, o=None, w_post=None, gate=None, gate_act="none", scale: float = 1.0, p: float = 0.0,
+                   seed: int = 0, offset: int = 0, y=None, w_pre=None, h=None, rstd_post=None, rstd_pre=None,
+                   post_norm: bool = True, eps: float = 1e-6, stream=None) -> None:
+    """y = x + scale * drop(act(gate) * norm(o) * w_post), h = norm(y) * w_pre,
+    in one pass over the rows [R, C].  Without o only h = norm(x) * w_pre;
+    without h only y; post_norm False: o enters as it is.  gate [G, C]: row r
+    uses gate row r // (R / G), through gate_act "none", "sigmoid" or "tanh".
+    rstd_post, rstd_pre: float32 [R], kept for the backward."""
+    where = "moe_block_norm"
+    _on_device(where, x, o, w_post, gate, y, w_pre, h, rstd_post, rstd_pre)
+    _need(x.dim() == 2, where, "x is [rows, cols]")
+    a = _block(where, x, x.shape[0], x.shape[1], o=o, w_post=w_post, gate=gate, gate_act=gate_act, scale=scale, p=p,
+               seed=seed, offset=offset, w_pre=w_pre, rstd_post=rstd_post, rstd_pre=rstd_pre, post_norm=post_norm,
+               eps=eps, x=x, y=y, h=h)
+    _check(lib().moe_block_norm(ctypes.byref(a), _stream(stream)), where)
+
+
+def moe_block_norm_workspace(rows: int, cols: int, gate_rows: int = 0) -> int:
+    """Workspace bytes of moe_block_norm_bwd."""
+    out = _u64()
+    _check(lib().moe_block_norm_workspace(rows, cols, gate_rows, ctypes.byref(out)), "moe_block_norm_workspace")
+    return out.value
+
+
+def moe_block_norm_bwd(dy=None, dh=None, y=None, o=None, w_post=None, gate=None, gate_act="none", scale: float = 1.0,
+                       p: float = 0.0, seed: int = 0, offset: int = 0, w_pre=None, rstd_post=None, rstd_pre=None,
+                       post_norm: bool = True, dx=None, do=None, dw_pre=None, dw_post=None, dgate=None, work=None,
+                       stream=None) -> None:
+    """Gradients of moe_block_norm from dy (of y) and dh (of h), with the
+    forward's arguments and its y, rstd_post and rstd_pre.  Every output may
+    be left out.  work: a uint8 tensor of moe_block_norm_workspace bytes."""
+    where = "moe_block_norm_bwd"
+    _on_device(where, dy, dh, y, o, w_post, gate, w_pre, rstd_post, rstd_pre, dx, do, dw_pre, dw_post, dgate, work)
+    lead = dy if dy is not None else dh
+    _need(lead is not None and lead.dim() == 2, where, "dy or dh, [rows, cols], is wanted")
+    rows, cols = lead.shape
+    a = _block(where, lead, rows, cols, o=o, w_post=w_post, gate=gate, gate_act=gate_act, scale=scale, p=p, seed=seed,
+               offset=offset, w_pre=w_pre, rstd_post=rstd_post, rstd_pre=rstd_pre, post_norm=post_norm, eps=0.0, y=y)
+    g = SymBlockNormGrad()
+
+    def put(name, ld, t, n):
+        if t is not None:
+            r = _rows(t, where, lead.dtype)
+            _need(t.dim() == 2 and r.rows == n and r.cols == cols, where, f"{name}: [{n}, {cols}] is wanted")
+            setattr(g, name, r.ptr)
+            setattr(g, ld, r.ld)
+
+    put("dy", "ld_dy", dy, rows)
+    put("dh", "ld_dh", dh, rows)
+    put("dx", "ld_dx", dx, rows)
+    put("d_o", "ld_do", do, rows)
+    put("dgate", "ld_dgate", dgate, a.gate_rows)
+    for name, t in (("dw_pre", dw_pre), ("dw_post", dw_post)):
+        if t is not None:
+            _need(t.dtype == lead.dtype and tuple(t.shape) == (cols,) and (cols == 1 or t.stride(0) == 1), where,
+                  f"{name}: [{cols}] of the rows' type is wanted")
+            setattr(g, name, t.data_ptr())
+    if work is not None:
+        _need(work.is_contiguous(), where, "work is contiguous")
+        g.work, g.work_bytes = work.data_ptr(), work.numel() * work.element_size()
+    _check(lib().moe_block_norm_bwd(ctypes.byref(a), ctypes.byref(g), _stream(stream)), where)
+
+
 # ------------------------------------------------------------------ heap owner
 
 class SymHeap:
@@ -345,6 +616,28 @@ class SymHeap:
         W = self.shape["world"]
         base = self.buf[self.desc.off_y:].view(torch.bfloat16)
         return base.as_strided((W, self.cap, H), (self.desc.per_rank_size // 2, H, 1))
+
+    def window(self, name: str) -> torch.Tensor:
+        """A per-slot window as one tensor over all slots (strided by the slot
+        size, zero copy), for the calls that take rows or groups: "recv_x",
+        "y" [W, cap, H]; "h" [W, cap, I]; "recv_w" [W, cap]; "cnt", "recv_off"
+        [W, E/W]; "total" [W]."""
+        W, H, I = self.shape["world"], self.shape["hidden"], self.shape["inter"]
+        el, cap = self.shape["num_experts"] // W, self.cap
+        tail, dtype, off = {"recv_x": ((cap, H), torch.bfloat16, self.desc.off_recv_x),
+                            "y": ((cap, H), torch.bfloat16, self.desc.off_y),
+                            "h": ((cap, I), torch.bfloat16, self.desc.off_h),
+                            "recv_w": ((cap,), torch.float32, self.desc.off_recv_w),
+                            "cnt": ((el,), torch.int32, self.desc.off_cnt),
+                            "recv_off": ((el,), torch.int32, self.desc.off_recv_off),
+                            "total": ((), torch.int32, self.desc.off_total)}[name]
+        base = self.buf[off:].narrow(0, 0, (self.buf.numel() - off) // 4 * 4).view(dtype)
+        inner = (tail[1], 1) if len(tail) == 2 else (1,) * len(tail)
+        return base.as_strided((W, *tail), (self.desc.per_rank_size // base.element_size(), *inner))
+
+    def status_word(self) -> torch.Tensor:
+        """The heap's status word as a tensor (for the grouped products' status)."""
+        return self._win(0, self.desc.off_status, 4, torch.int32)
 
     def status(self, clear: bool = False, stream=None) -> int:
         return sym_heap_status(self.desc, clear, stream)

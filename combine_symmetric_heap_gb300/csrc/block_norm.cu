@@ -1,0 +1,589 @@
+// block_norm.cu -- the norms before and after a block, fused with the block's
+// gate, dropout and residual scale; forward and backward.
+//
+//   n = o * rstd_o * w_post          rstd_o = (mean(o^2) + eps)^-1/2
+//   y = x + scale * drop(act(gate) * n)
+//   h = y * rstd_y * w_pre           rstd_y = (mean(y^2) + eps)^-1/2
+//
+// o is the block's output, x the residual stream, y the stream after the
+// block, h the input of the next block.  Backward, with the stream's gradient
+// dy and h's gradient dh, yn = y rstd_y, on = o rstd_o, m = scale * drop:
+//   dx = dy + rstd_y (dh w_pre - yn mean(dh w_pre yn))
+//   dn = m act(gate) dx;   do = rstd_o (dn w_post - on mean(dn w_post on))
+//   dw_pre = sum dh yn,  dw_post = sum dn on,  dgate = act'(gate) sum m dx on w_post
+// (sums over rows; the gate's over the rows that share it).
+//
+// Both are bound by their bytes: every row tensor is read once and written
+// once, one pass per row with the row held in registers (rows beyond the
+// register budget are walked again out of L2).  The dropout mask is recomputed
+// from its counter.  The backward's two row means are taken with one block
+// reduction: mean(dn w_post on) is linear in the first mean.
+#include <algorithm>
+
+#include "rows_dev.cuh"
+
+namespace symmoe {
+namespace norm {
+
+using namespace rows;
+
+enum Act : int { ACT_NONE = 0, ACT_SIGMOID = 1, ACT_TANH = 2 };
+
+struct Fwd {
+  const void *x, *o, *w_post, *w_pre, *gate;
+  void *y, *h;
+  float *rstd_post, *rstd_pre;
+  int64_t ldx, ldo, ldy, ldh, ldg;  // elements
+  int64_t rows, per_gate;           // rows that share a gate row
+  int cols, act, post_norm;
+  float scale, eps;
+  int drop;
+  Random rnd;
+};
+
+struct Bwd {
+  const void *dy, *dh, *y, *o, *w_post, *w_pre, *gate;
+  const float *rstd_post, *rstd_pre;
+  void *dx, *dout, *dw_pre, *dw_post, *dgate;
+  float *ws;  // partial sums
+  int64_t ld_dy, ld_dh, ldy, ldo, ldg, ld_dx, ld_do, ld_dg;
+  int64_t rows, per_gate;
+  int gates, cols, act, post_norm;
+  float scale;
+  int drop;
+  Random rnd;
+  // work items: `per_item` rows of a gate's rows; items = gates * split
+  int split;
+  int64_t per_item;
+};
+
+__device__ __forceinline__ float activate(int act, float g) {
+  if (act == ACT_SIGMOID) return __fdividef(1.f, 1.f + __expf(-g));
+  if (act == ACT_TANH) return tanhf(g);
+  return g;
+}
+__device__ __forceinline__ float slope(int act, float g) {
+  if (act == ACT_SIGMOID) {
+    const float s = __fdividef(1.f, 1.f + __expf(-g));
+    return s * (1.f - s);
+  }
+  if (act == ACT_TANH) {
+    const float t = tanhf(g);
+    return 1.f - t * t;
+  }
+  return 1.f;
+}
+
+// The stream after the block for V columns of a row: x + scale * drop(gate * n)
+template <typename T, int V>
+__device__ __forceinline__ void stream_after(const Fwd &p, const T *x, const float (&ov)[V], float rstd, const T *gate,
+                                             int64_t row, int c, float (&yv)[V]) {
+  float f[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = ov[i] * rstd;
+  if (p.w_post) {
+    float w[V];
+    load<T, V>(reinterpret_cast<const T *>(p.w_post) + c, w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] *= w[i];
+  }
+  if (gate) {
+    float g[V];
+    load<T, V>(gate + c, g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] *= activate(p.act, g[i]);
+  }
+  if (p.drop) {
+    float k[V];
+    keep_factors<V>(p.rnd, (uint64_t)row * p.cols + c, k);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = k[i] != 0.f ? f[i] * k[i] : 0.f;
+  }
+  load<T, V>(x + c, yv);
+#pragma unroll
+  for (int i = 0; i < V; ++i) yv[i] += p.scale * f[i];
+}
+
+// Forward.  NV > 0: a thread keeps its NV vectors of the row in registers;
+// NV = 0: any row length, the row is walked once per sum and once to write.
+// blockDim (threads of a row, rows of a block).
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(1024) block_norm_kernel(const Fwd p) {
+  extern __shared__ float buf[];
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  float *mine = buf + threadIdx.y * 64;
+  int turn = 0;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const float inv = 1.f / p.cols;
+  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.rows; r0 += step) {
+    const int64_t want = r0 + threadIdx.y;
+    const bool live = want < p.rows;
+    const int64_t r = live ? want : p.rows - 1;  // idle row groups follow along without writing
+    const T *x = reinterpret_cast<const T *>(p.x) + r * p.ldx;
+    const T *o = p.o ? reinterpret_cast<const T *>(p.o) + r * p.ldo : nullptr;
+    const T *gate = p.gate ? reinterpret_cast<const T *>(p.gate) + (r / p.per_gate) * p.ldg : nullptr;
+    T *y = p.y ? reinterpret_cast<T *>(p.y) + r * p.ldy : nullptr;
+    T *h = p.h ? reinterpret_cast<T *>(p.h) + r * p.ldh : nullptr;
+    constexpr int N = NV ? NV : 1;
+    float yv[N][V];
+    float rstd_o = 1.f;
+    if (o && p.post_norm) {
+      float s[1] = {0.f};
+      if (NV) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+          if (c < p.cols) {
+            load<T, V>(o + c, yv[j]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[0] += yv[j][i] * yv[j][i];
+          }
+        }
+      } else {
+        for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
+          float ov[V];
+          load<T, V>(o + c, ov);
+#pragma unroll
+          for (int i = 0; i < V; ++i) s[0] += ov[i] * ov[i];
+        }
+      }
+      group_sums<1>(s, mine, warp, warps, turn);
+      rstd_o = rsqrtf(s[0] * inv + p.eps);
+      if (live && threadIdx.x == 0 && p.rstd_post) p.rstd_post[r] = rstd_o;
+    }
+    // V columns of y from c on, o's values in ov where the row is in registers
+    auto stream = [&](int c, const float(&ov)[V], float(&out)[V]) {
+      if (!o) load<T, V>(x + c, out);
+      else if (NV && p.post_norm) stream_after<T, V>(p, x, ov, rstd_o, gate, r, c, out);
+      else {
+        float fresh[V];
+        load<T, V>(o + c, fresh);
+        stream_after<T, V>(p, x, fresh, rstd_o, gate, r, c, out);
+      }
+    };
+    float s[1] = {0.f};
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+        if (c < p.cols) {
+          float t[V];
+          stream(c, yv[j], t);
+          if (y && live) store<T, V>(y + c, t);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            yv[j][i] = t[i];
+            s[0] += t[i] * t[i];
+          }
+        }
+      }
+    } else if (h || p.rstd_pre) {
+      for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
+        float t[V];
+        stream(c, t, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[0] += t[i] * t[i];
+      }
+    }
+    float rstd_y = 0.f;
+    if (h || p.rstd_pre) {
+      group_sums<1>(s, mine, warp, warps, turn);
+      rstd_y = rsqrtf(s[0] * inv + p.eps);
+      if (live && threadIdx.x == 0 && p.rstd_pre) p.rstd_pre[r] = rstd_y;
+    }
+    auto finish = [&](int c, float(&t)[V]) {
+      if (!h || !live) return;
+      if (p.w_pre) {
+        float w[V];
+        load<T, V>(reinterpret_cast<const T *>(p.w_pre) + c, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = t[i] * rstd_y * w[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] *= rstd_y;
+      }
+      store<T, V>(h + c, t);
+    };
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+        if (c < p.cols) finish(c, yv[j]);
+      }
+    } else {
+      for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
+        float t[V];
+        stream(c, t, t);  // each column is read before it is written: y may be x
+        if (y && live) store<T, V>(y + c, t);
+        finish(c, t);
+      }
+    }
+  }
+}
+
+// Backward.  A block takes work items (a run of rows that share a gate row),
+// one row at a time; the column sums stay in registers over its rows (NV > 0)
+// or in the block's partial sums in the workspace (NV = 0), and are joined by
+// sum_partials_kernel in a fixed order.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
+  __shared__ float buf[2 * 32 * 3];
+  constexpr int N = NV ? NV : 1;
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  const int items = p.gates * p.split;
+  const float inv = 1.f / p.cols;
+  int turn = 0;
+  // workspace: [gridDim][cols] dw_pre, the same for dw_post, [items][cols] gate
+  float *ws_pre = p.ws + (int64_t)blockIdx.x * p.cols;
+  float *ws_post = p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.cols;
+  float *ws_gate = p.ws + 2 * (int64_t)gridDim.x * p.cols;
+  float a_pre[N][V], a_post[N][V], a_gate[N][V];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) a_pre[j][i] = a_post[j][i] = 0.f;
+  const T *w_pre = reinterpret_cast<const T *>(p.w_pre), *w_post = reinterpret_cast<const T *>(p.w_post);
+
+  auto each = [&](auto &&f) {  // f(j, c) for this thread's vectors
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+        if (c < p.cols) f(j, c);
+      }
+    } else {
+      for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) f(0, c);
+    }
+  };
+  if (!NV)
+    each([&](int, int c) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) ws_pre[c + i] = ws_post[c + i] = 0.f;
+    });
+
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t gi = item / p.split, first = gi * p.per_gate;
+    const int64_t begin = first + (item % p.split) * p.per_item;
+    const int64_t end = min(begin + p.per_item, first + p.per_gate);
+    const T *gate = p.gate ? reinterpret_cast<const T *>(p.gate) + gi * p.ldg : nullptr;
+    float *gate_sum = ws_gate + (int64_t)item * p.cols;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) a_gate[j][i] = 0.f;
+    if (!NV && p.dgate)
+      each([&](int, int c) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) gate_sum[c + i] = 0.f;
+      });
+
+    for (int64_t r = begin; r < end; ++r) {
+      const T *dy = p.dy ? reinterpret_cast<const T *>(p.dy) + r * p.ld_dy : nullptr;
+      const T *dh = p.dh ? reinterpret_cast<const T *>(p.dh) + r * p.ld_dh : nullptr;
+      const T *y = p.dh ? reinterpret_cast<const T *>(p.y) + r * p.ldy : nullptr;
+      const T *o = p.o ? reinterpret_cast<const T *>(p.o) + r * p.ldo : nullptr;
+      const float ry = p.dh ? p.rstd_pre[r] : 0.f;
+      const float ro = p.o && p.post_norm ? p.rstd_post[r] : 1.f;
+      // per column: yn, dx without its mean term (g0), on, the factor m * act
+      // from dx to dn, and m alone (for the gate's gradient)
+      auto columns = [&](int c, float(&yn)[V], float(&g0)[V], float(&hv)[V], float(&on)[V], float(&fa)[V],
+                         float(&fm)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) yn[i] = g0[i] = hv[i] = on[i] = fa[i] = fm[i] = 0.f;
+        if (dy) load<T, V>(dy + c, g0);
+        if (dh) {
+          load<T, V>(y + c, yn);
+          load<T, V>(dh + c, hv);
+          float w[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) w[i] = 1.f;
+          if (w_pre) load<T, V>(w_pre + c, w);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            yn[i] *= ry;
+            g0[i] += ry * hv[i] * w[i];
+          }
+        }
+        if (o) {
+          load<T, V>(o + c, on);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            on[i] *= ro;
+            fm[i] = p.scale;
+          }
+          if (p.drop) {
+            float k[V];
+            keep_factors<V>(p.rnd, (uint64_t)r * p.cols + c, k);
+#pragma unroll
+            for (int i = 0; i < V; ++i) fm[i] *= k[i];
+          }
+          if (gate) {
+            float g[V];
+            load<T, V>(gate + c, g);
+#pragma unroll
+            for (int i = 0; i < V; ++i) fa[i] = fm[i] * activate(p.act, g[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) fa[i] = fm[i];
+          }
+        }
+      };
+      auto post_weight = [&](int c, float(&w)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] = 1.f;
+        if (w_post) load<T, V>(w_post + c, w);
+      };
+      // sums over the row: dh w_pre yn;  g0 q;  yn q  with q = m act w_post on
+      float s[3] = {0.f, 0.f, 0.f};
+      each([&](int, int c) {
+        float yn[V], g0[V], hv[V], on[V], fa[V], fm[V], w[V];
+        columns(c, yn, g0, hv, on, fa, fm);
+        post_weight(c, w);
+        float wp[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) wp[i] = 1.f;
+        if (dh && w_pre) load<T, V>(w_pre + c, wp);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float q = fa[i] * w[i] * on[i];
+          s[0] += hv[i] * wp[i] * yn[i];
+          s[1] += g0[i] * q;
+          s[2] += yn[i] * q;
+        }
+      });
+      group_sums<3>(s, buf, warp, warps, turn);
+      const float m1 = ry * s[0] * inv;                                  // dx = g0 - yn * m1
+      const float m2 = p.post_norm ? (s[1] - m1 * s[2]) * inv : 0.f;     // mean(dn w_post on)
+      each([&](int j, int c) {
+        float yn[V], g0[V], hv[V], on[V], fa[V], fm[V], w[V];
+        columns(c, yn, g0, hv, on, fa, fm);
+        post_weight(c, w);
+        float dov[V], dxv[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float dx = g0[i] - yn[i] * m1;
+          // a dropped element passes nothing on, whatever its values
+          const float dn = fa[i] != 0.f ? dx * fa[i] : 0.f;
+          const float dg = fm[i] != 0.f ? dx * fm[i] * on[i] * w[i] : 0.f;
+          dxv[i] = dx;
+          dov[i] = ro * (dn * w[i] - on[i] * m2);
+          hv[i] *= yn[i];
+          fa[i] = dn * on[i];
+          fm[i] = dg;
+        }
+        if (p.dx) store<T, V>(reinterpret_cast<T *>(p.dx) + r * p.ld_dx + c, dxv);
+        if (p.dout) store<T, V>(reinterpret_cast<T *>(p.dout) + r * p.ld_do + c, dov);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (NV) {
+            a_pre[j][i] += hv[i];
+            a_post[j][i] += fa[i];
+            a_gate[j][i] += fm[i];
+          } else {
+            ws_pre[c + i] += hv[i];
+            ws_post[c + i] += fa[i];
+            if (p.dgate) gate_sum[c + i] += fm[i];
+          }
+        }
+      });
+    }
+    if (p.dgate)
+      each([&](int j, int c) {
+        float t[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = NV ? a_gate[j][i] : gate_sum[c + i];
+        if (p.split == 1) {  // this block saw all rows of the gate row
+          float g[V];
+          load<T, V>(gate + c, g);
+#pragma unroll
+          for (int i = 0; i < V; ++i) t[i] *= slope(p.act, g[i]);
+          store<T, V>(reinterpret_cast<T *>(p.dgate) + gi * p.ld_dg + c, t);
+        } else if (NV) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) gate_sum[c + i] = t[i];
+        }
+      });
+  }
+  if (NV)
+    each([&](int j, int c) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (p.dw_pre) ws_pre[c + i] = a_pre[j][i];
+        if (p.dw_post) ws_post[c + i] = a_post[j][i];
+      }
+    });
+}
+
+// Column sums of the partials: y 0 dw_pre, 1 dw_post, 2 + g the gate rows.
+// A block adds 32 columns: warp w takes partials w, w + 8, ..., then the eight
+// sums are added in order.
+template <typename T>
+__global__ void __launch_bounds__(256) sum_partials_kernel(const Bwd p, int blocks) {
+  __shared__ float part[8][33];
+  const int which = blockIdx.y;
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x / 32;
+  const bool is_gate = which >= 2;
+  void *out = which == 0 ? p.dw_pre : which == 1 ? p.dw_post : p.dgate;
+  if (!out || (is_gate && p.split == 1)) return;
+  const float *from = p.ws + (which == 0 ? 0 : which == 1 ? (int64_t)blocks * p.cols
+                                                          : 2 * (int64_t)blocks * p.cols +
+                                                                (int64_t)(which - 2) * p.split * p.cols);
+  const int n = is_gate ? p.split : blocks;
+  float s = 0.f;
+  if (c < p.cols)
+    for (int i = w; i < n; i += 8) s += from[(int64_t)i * p.cols + c];
+  part[w][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (w != 0 || c >= p.cols) return;
+  s = 0.f;
+  for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
+  if (is_gate) {
+    const int64_t gi = which - 2;
+    s *= slope(p.act, Elem<T>::get(reinterpret_cast<const T *>(p.gate)[gi * p.ldg + c]));
+    reinterpret_cast<T *>(p.dgate)[gi * p.ld_dg + c] = Elem<T>::put(s);
+  } else {
+    reinterpret_cast<T *>(out)[c] = Elem<T>::put(s);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// Threads of a row for rows of `cols` elements in vectors of V: whole warps,
+// at most `most`, each with at most `nv` vectors (0: the row does not fit)
+static int threads_of(int cols, int V, int nv, int most) {
+  const int vecs = (cols + V - 1) / V;
+  const int t = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+  return t <= most ? t : 0;
+}
+
+template <typename T, int V, int NV>
+static void run_fwd(const Fwd &p, int tpr, int num_sms, cudaStream_t st) {
+  const int rpb = std::max(1, 128 / tpr);
+  const int64_t blocks = std::min<int64_t>((p.rows + rpb - 1) / rpb, (int64_t)num_sms * 64);
+  block_norm_kernel<T, V, NV><<<(unsigned)blocks, dim3(tpr, rpb), rpb * 64 * sizeof(float), st>>>(p);
+}
+// NV vectors a thread: two where they fit 512 threads, more for wider rows
+template <typename T, int V>
+static void fwd(const Fwd &p, int num_sms, cudaStream_t st) {
+  constexpr int N = V == 1 ? 8 : 2;
+  if (const int t = threads_of(p.cols, V, N / 2, 256)) return run_fwd<T, V, N / 2>(p, t, num_sms, st);
+  if (const int t = threads_of(p.cols, V, N, 1024)) return run_fwd<T, V, N>(p, t, num_sms, st);
+  run_fwd<T, V, 0>(p, 1024, num_sms, st);
+}
+
+static int bwd_threads(int cols, int V, int *nv) {
+  const int n = V == 1 ? 8 : V == 4 ? 4 : 2;
+  if (const int t = threads_of(cols, V, n, 512)) {
+    *nv = n;
+    return t;
+  }
+  *nv = 0;
+  return 512;
+}
+// blocks that share the rows: about two thousand threads an SM
+static int64_t bwd_blocks(int64_t rows, int threads, int num_sms) {
+  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * std::max(1, 1024 / threads)));
+}
+// Split of a gate row's rows so that all items together give every block one
+static int64_t bwd_split(int64_t gates, int64_t per_gate, int64_t blocks) {
+  if (gates >= blocks) return 1;
+  return std::max<int64_t>(1, std::min<int64_t>(per_gate, blocks / gates));
+}
+
+template <typename T, int V, int NV>
+static cudaError_t run_bwd(Bwd p, int threads, int num_sms, cudaStream_t st) {
+  const int64_t most = bwd_blocks(p.rows, threads, num_sms);
+  p.split = (int)bwd_split(p.gates, p.per_gate, most);
+  p.per_item = (p.per_gate + p.split - 1) / p.split;
+  const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split);
+  block_norm_bwd_kernel<T, V, NV><<<blocks, threads, 0, st>>>(p);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  const bool gates = p.dgate && p.split > 1;
+  if (p.dw_pre || p.dw_post || gates) {
+    sum_partials_kernel<T><<<dim3((p.cols + 31) / 32, 2 + (gates ? p.gates : 0)), 256, 0, st>>>(p, blocks);
+    err = cudaGetLastError();
+  }
+  return err;
+}
+template <typename T, int V>
+static cudaError_t bwd(const Bwd &p, int num_sms, cudaStream_t st) {
+  int nv;
+  const int t = bwd_threads(p.cols, V, &nv);
+  constexpr int N = V == 1 ? 8 : V == 4 ? 4 : 2;
+  return nv ? run_bwd<T, V, N>(p, t, num_sms, st) : run_bwd<T, V, 0>(p, t, num_sms, st);
+}
+
+// 16-byte vectors where every row of every tensor starts on their boundary
+static bool vec_ok(std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> lds, int cols, int64_t es) {
+  for (const void *q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) % 16) return false;
+  for (int64_t l : lds)
+    if (l * es % 16) return false;
+  return cols * es % 16 == 0;
+}
+
+}  // namespace norm
+
+// bytes of partial sums, an upper bound over the types and alignments
+size_t block_norm_workspace(int64_t rows, int cols, int64_t gates, int num_sms) {
+  using namespace norm;
+  size_t best = 0;
+  for (int V : {1, 4, 8}) {
+    int nv;
+    const int64_t blocks = bwd_blocks(rows, bwd_threads(cols, V, &nv), num_sms);
+    const int64_t split = gates ? bwd_split(gates, rows / gates, blocks) : 1;
+    // gate partials: where several blocks share a gate row, or (rows beyond
+    // the register budget) the sums live in memory
+    const int64_t items = gates && (split > 1 || nv == 0) ? gates * split : 0;
+    best = std::max(best, (size_t)(2 * blocks + items) * cols * sizeof(float));
+  }
+  return best;
+}
+
+cudaError_t launch_block_norm(const sym_block_norm &a, int num_sms, cudaStream_t st) {
+  using namespace norm;
+  Fwd p = {};
+  p.x = a.x, p.o = a.o, p.w_post = a.w_post, p.w_pre = a.w_pre, p.gate = a.gate, p.y = a.y, p.h = a.h;
+  p.rstd_post = a.rstd_post, p.rstd_pre = a.rstd_pre;
+  p.ldx = a.ld_x, p.ldo = a.ld_o, p.ldy = a.ld_y, p.ldh = a.ld_h, p.ldg = a.ld_gate;
+  p.rows = a.rows, p.per_gate = a.gate ? a.rows / a.gate_rows : a.rows;
+  p.cols = a.cols, p.act = a.gate_act, p.post_norm = !(a.flags & SYM_NORM_NO_POST);
+  p.scale = a.scale, p.eps = a.eps, p.drop = a.p > 0;
+  p.rnd = Random{a.seed, a.offset, (uint32_t)(a.p * 4294967296.0), (float)(1.0 / (1.0 - a.p))};
+  const int64_t es = a.dtype == SYM_FP32 ? 4 : 2;
+  const bool vec = vec_ok({p.x, p.o, p.w_post, p.w_pre, p.gate, p.y, p.h},
+                          {p.ldx, p.o ? p.ldo : 0, p.y ? p.ldy : 0, p.h ? p.ldh : 0, p.gate ? p.ldg : 0}, p.cols, es);
+  if (a.dtype == SYM_BF16) vec ? fwd<__nv_bfloat16, 8>(p, num_sms, st) : fwd<__nv_bfloat16, 1>(p, num_sms, st);
+  else if (a.dtype == SYM_FP16) vec ? fwd<__half, 8>(p, num_sms, st) : fwd<__half, 1>(p, num_sms, st);
+  else vec ? fwd<float, 4>(p, num_sms, st) : fwd<float, 1>(p, num_sms, st);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_block_norm_bwd(const sym_block_norm &a, const sym_block_norm_grad &b, int num_sms,
+                                  cudaStream_t st) {
+  using namespace norm;
+  Bwd p = {};
+  p.dy = b.dy, p.dh = b.dh, p.y = a.y, p.o = a.o, p.w_post = a.w_post, p.w_pre = a.w_pre, p.gate = a.gate;
+  p.rstd_post = a.rstd_post, p.rstd_pre = a.rstd_pre;
+  p.dx = b.dx, p.dout = b.d_o, p.dw_pre = b.dw_pre, p.dw_post = b.dw_post, p.dgate = b.dgate;
+  p.ws = reinterpret_cast<float *>(b.work);
+  p.ld_dy = b.ld_dy, p.ld_dh = b.ld_dh, p.ldy = a.ld_y, p.ldo = a.ld_o, p.ldg = a.ld_gate;
+  p.ld_dx = b.ld_dx, p.ld_do = b.ld_do, p.ld_dg = b.ld_dgate;
+  p.rows = a.rows, p.gates = a.gate ? (int)a.gate_rows : 1;
+  p.per_gate = p.rows / p.gates;
+  p.cols = a.cols, p.act = a.gate_act, p.post_norm = !(a.flags & SYM_NORM_NO_POST);
+  p.scale = a.scale, p.drop = a.p > 0;
+  p.rnd = Random{a.seed, a.offset, (uint32_t)(a.p * 4294967296.0), (float)(1.0 / (1.0 - a.p))};
+  const int64_t es = a.dtype == SYM_FP32 ? 4 : 2;
+  const bool vec = vec_ok({p.dy, p.dh, p.dh ? p.y : nullptr, p.o, p.w_post, p.w_pre, p.gate, p.dx, p.dout, p.dgate},
+                          {p.dy ? p.ld_dy : 0, p.dh ? p.ld_dh : 0, p.dh ? p.ldy : 0, p.o ? p.ldo : 0,
+                           p.gate ? p.ldg : 0, p.dx ? p.ld_dx : 0, p.dout ? p.ld_do : 0, p.dgate ? p.ld_dg : 0},
+                          p.cols, es);
+  if (a.dtype == SYM_BF16) return vec ? bwd<__nv_bfloat16, 8>(p, num_sms, st) : bwd<__nv_bfloat16, 1>(p, num_sms, st);
+  if (a.dtype == SYM_FP16) return vec ? bwd<__half, 8>(p, num_sms, st) : bwd<__half, 1>(p, num_sms, st);
+  return vec ? bwd<float, 4>(p, num_sms, st) : bwd<float, 1>(p, num_sms, st);
+}
+
+}  // namespace symmoe

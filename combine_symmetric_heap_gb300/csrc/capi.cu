@@ -36,6 +36,24 @@ cudaError_t launch_fused(const sym_heap &h, const float *logits, const uint16_t 
                          const uint16_t *wg, const uint16_t *wu, const uint16_t *wd,
                          int32_t *idx, float *w, uint16_t *out, int weights_in_ffn, int num_sms,
                          cudaStream_t st);
+cudaError_t launch_grouped_matmul(const sym_groups &g, int fp16, const sym_rows &x, const void *w, int64_t w_group,
+                                  int64_t w_ld, int trans, const sym_rows &out, int num_sms, cudaStream_t st);
+cudaError_t launch_grouped_wgrad(const sym_groups &g, int fp16, const sym_rows &dy, const sym_rows &x, void *dw,
+                                 int64_t dw_group, int64_t dw_ld, int out_type, int add, int num_sms,
+                                 cudaStream_t st);
+cudaError_t launch_swiglu_rows(int dtype, const sym_rows &g, const sym_rows &u, const sym_rows &h, const float *rw,
+                               int64_t rw_slot, const int32_t *total, int64_t total_slot, int num_sms,
+                               cudaStream_t st);
+cudaError_t launch_swiglu_rows_bwd(int dtype, const sym_rows &g, const sym_rows &u, const sym_rows &dh,
+                                   const sym_rows &dg, const sym_rows &du, const float *rw, int64_t rw_slot,
+                                   float *drw, int64_t drw_slot, const int32_t *total, int64_t total_slot,
+                                   int num_sms, cudaStream_t st);
+cudaError_t launch_dropout(int dtype, const sym_rows &x, const sym_rows *res, const sym_rows &y, uint64_t seed,
+                           uint64_t offset, uint32_t threshold, float keep_scale, int num_sms, cudaStream_t st);
+size_t block_norm_workspace(int64_t rows, int cols, int64_t gates, int num_sms);
+cudaError_t launch_block_norm(const sym_block_norm &a, int num_sms, cudaStream_t st);
+cudaError_t launch_block_norm_bwd(const sym_block_norm &a, const sym_block_norm_grad &b, int num_sms,
+                                  cudaStream_t st);
 }  // namespace symmoe
 
 using namespace symmoe;
@@ -339,6 +357,180 @@ int sym_heap_status(const sym_heap *h, int32_t *status, int clear, symmoe_stream
     return SYM_ECUDA;
   if (clear && cudaMemset(dev, 0, sizeof(int32_t)) != cudaSuccess) return SYM_ECUDA;
   return SYM_OK;
+}
+
+// ---------------------------------------------------------------------------
+// training through an MoE block
+// ---------------------------------------------------------------------------
+// rows of a tensor or a window: extents in range, rows that do not overlap
+static bool rows_ok(const sym_rows *r, uint64_t align) {
+  if (!r || r->slots < 1 || r->slots > 1024 || r->rows < 0 || r->cols < 1 || r->cols > 65536) return false;
+  if (r->rows * r->slots >= (int64_t(1) << 30)) return false;
+  if (r->rows > 0 && (r->ptr == 0 || r->ptr % align != 0)) return false;
+  if (r->rows > 1 && r->ld < r->cols) return false;
+  if (r->slots > 1 && r->rows > 0 && r->slot_stride < (r->rows - 1) * r->ld + r->cols) return false;
+  return true;
+}
+// the tensor copies' rule: 16-byte aligned rows
+static bool rows_tma_ok(const sym_rows *r) {
+  return rows_ok(r, 16) && r->ld % 8 == 0 && r->ld >= r->cols && (r->slots == 1 || r->slot_stride % 8 == 0);
+}
+static bool same_rows(const sym_rows *a, const sym_rows *b) { return a->slots == b->slots && a->rows == b->rows; }
+static bool groups_ok(const sym_groups *g, const sym_rows *r) {
+  return g && aligned4(g->cnt) && aligned4(g->off) && g->groups >= 1 && g->groups <= 1024 && g->slots == r->slots &&
+         g->groups % g->slots == 0 && (reinterpret_cast<uintptr_t>(g->status) & 3u) == 0;
+}
+static sym_groups with_timeout(const sym_groups *g) {
+  sym_groups c = *g;
+  if (c.wait_timeout_us == 0) c.wait_timeout_us = kDefaultTimeoutUs;
+  return c;
+}
+
+int moe_grouped_matmul(const sym_groups *g, int dtype, const sym_rows *x, const void *w, int64_t w_group_stride,
+                       int64_t w_ld, int flags, const sym_rows *out, symmoe_stream_t stream) {
+  if ((dtype != SYM_BF16 && dtype != SYM_FP16) || (flags & ~SYM_GM_TRANS_W) || !rows_tma_ok(x) || !rows_ok(out, 2) ||
+      !same_rows(x, out) || !groups_ok(g, x) || !aligned16(w))
+    return SYM_EINVAL;
+  const int trans = flags & SYM_GM_TRANS_W;
+  if (w_ld % 8 != 0 || w_ld < (trans ? out->cols : x->cols) || (g->groups > 1 && w_group_stride % 8 != 0) ||
+      (g->groups > 1 && w_group_stride < 0))
+    return SYM_EINVAL;
+  if (x->rows == 0) return SYM_OK;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  return from_cuda(launch_grouped_matmul(with_timeout(g), dtype == SYM_FP16, *x, w, w_group_stride, w_ld, trans, *out,
+                                         sms, (cudaStream_t)stream));
+}
+
+int moe_grouped_wgrad(const sym_groups *g, int dtype, const sym_rows *dy, const sym_rows *x, void *dw,
+                      int64_t dw_group_stride, int64_t dw_ld, int out_dtype, int flags, symmoe_stream_t stream) {
+  if ((dtype != SYM_BF16 && dtype != SYM_FP16) || (out_dtype != dtype && out_dtype != SYM_FP32) ||
+      (flags & ~SYM_GM_ACCUMULATE) || !rows_tma_ok(dy) || !rows_tma_ok(x) || !same_rows(dy, x) || !groups_ok(g, x) ||
+      !dw || reinterpret_cast<uintptr_t>(dw) % (out_dtype == SYM_FP32 ? 4 : 2) != 0 || dw_ld < x->cols ||
+      (g->groups > 1 && dw_group_stride < 0))
+    return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  return from_cuda(launch_grouped_wgrad(with_timeout(g), dtype == SYM_FP16, *dy, *x, dw, dw_group_stride, dw_ld,
+                                        out_dtype, flags & SYM_GM_ACCUMULATE, sms, (cudaStream_t)stream));
+}
+
+static bool dtype_ok(int dtype) { return dtype == SYM_BF16 || dtype == SYM_FP16 || dtype == SYM_FP32; }
+static uint64_t size_of(int dtype) { return dtype == SYM_FP32 ? 4 : 2; }
+static bool like_ok(const sym_rows *r, const sym_rows *first, int dtype) {
+  return rows_ok(r, size_of(dtype)) && same_rows(r, first) && r->cols == first->cols;
+}
+static bool opt4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int moe_swiglu_rows(int dtype, const sym_rows *g, const sym_rows *u, const float *row_w, int64_t row_w_slot_stride,
+                    const int32_t *total, int64_t total_slot_stride, const sym_rows *h, symmoe_stream_t stream) {
+  if (!dtype_ok(dtype) || !rows_ok(g, size_of(dtype)) || !like_ok(u, g, dtype) || !like_ok(h, g, dtype) ||
+      !opt4(row_w) || !opt4(total))
+    return SYM_EINVAL;
+  if (g->rows == 0) return SYM_OK;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  return from_cuda(launch_swiglu_rows(dtype, *g, *u, *h, row_w, row_w_slot_stride, total, total_slot_stride, sms,
+                                      (cudaStream_t)stream));
+}
+
+int moe_swiglu_rows_bwd(int dtype, const sym_rows *g, const sym_rows *u, const sym_rows *dh, const float *row_w,
+                        int64_t row_w_slot_stride, const int32_t *total, int64_t total_slot_stride,
+                        const sym_rows *dg, const sym_rows *du, float *d_row_w, int64_t d_row_w_slot_stride,
+                        symmoe_stream_t stream) {
+  if (!dtype_ok(dtype) || !rows_ok(g, size_of(dtype)) || !like_ok(u, g, dtype) || !like_ok(dh, g, dtype) ||
+      !like_ok(dg, g, dtype) || !like_ok(du, g, dtype) || !opt4(row_w) || !opt4(total) || !opt4(d_row_w))
+    return SYM_EINVAL;
+  if (g->rows == 0) return SYM_OK;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  return from_cuda(launch_swiglu_rows_bwd(dtype, *g, *u, *dh, *dg, *du, row_w, row_w_slot_stride, d_row_w,
+                                          d_row_w_slot_stride, total, total_slot_stride, sms, (cudaStream_t)stream));
+}
+
+int moe_dropout(int dtype, const sym_rows *x, const sym_rows *residual, const sym_rows *y, double p, uint64_t seed,
+                uint64_t offset, symmoe_stream_t stream) {
+  if (!dtype_ok(dtype) || !rows_ok(x, size_of(dtype)) || !like_ok(y, x, dtype) ||
+      (residual && !like_ok(residual, x, dtype)) || !(p >= 0.0 && p < 1.0))
+    return SYM_EINVAL;
+  if (x->rows == 0) return SYM_OK;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  return from_cuda(launch_dropout(dtype, *x, residual, *y, seed, offset, (uint32_t)(p * 4294967296.0),
+                                  (float)(1.0 / (1.0 - p)), sms, (cudaStream_t)stream));
+}
+
+// a tensor of the call: aligned to its type, rows that do not overlap
+static bool tensor_ok(const void *p, int64_t ld, int64_t rows, int cols, int dtype) {
+  return reinterpret_cast<uintptr_t>(p) % size_of(dtype) == 0 && (!p || rows <= 1 || ld >= cols);
+}
+static bool block_ok(const sym_block_norm *a) {
+  if (!a || !dtype_ok(a->dtype) || a->rows < 0 || a->rows >= (int64_t(1) << 30) || a->cols < 1 || a->cols > 65536)
+    return false;
+  if ((a->flags & ~SYM_NORM_NO_POST) || a->gate_act < SYM_GATE_NONE || a->gate_act > SYM_GATE_TANH) return false;
+  if (!(a->p >= 0.0 && a->p < 1.0) || !(a->eps >= 0.f)) return false;
+  if ((a->flags & SYM_NORM_NO_POST) && (a->w_post || a->rstd_post)) return false;
+  // (an empty tensor may have no address)
+  if (a->rows > 0 && !a->o && (a->w_post || a->gate || a->rstd_post)) return false;
+  if (a->gate && (a->gate_rows < 1 || a->gate_rows >= (int64_t(1) << 31) ||
+                  (a->rows > 0 && (a->gate_rows > a->rows || a->rows % a->gate_rows != 0))))
+    return false;
+  return tensor_ok(a->o, a->ld_o, a->rows, a->cols, a->dtype) && tensor_ok(a->y, a->ld_y, a->rows, a->cols, a->dtype) &&
+         tensor_ok(a->gate, a->ld_gate, a->gate_rows, a->cols, a->dtype) &&
+         tensor_ok(a->w_post, 0, 1, a->cols, a->dtype) && tensor_ok(a->w_pre, 0, 1, a->cols, a->dtype) &&
+         opt4(a->rstd_post) && opt4(a->rstd_pre);
+}
+
+int moe_block_norm(const sym_block_norm *a, symmoe_stream_t stream) {
+  if (!block_ok(a) || !tensor_ok(a->x, a->ld_x, a->rows, a->cols, a->dtype) ||
+      !tensor_ok(a->h, a->ld_h, a->rows, a->cols, a->dtype))
+    return SYM_EINVAL;
+  if (a->rows == 0) return SYM_OK;
+  if (!a->x || (a->o && !a->y) || (!a->o && a->y) || (!a->o && !a->h && !a->rstd_pre)) return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  return from_cuda(launch_block_norm(*a, sms, (cudaStream_t)stream));
+}
+
+int moe_block_norm_workspace(int64_t rows, int32_t cols, int64_t gate_rows, uint64_t *bytes) {
+  if (!bytes || rows < 0 || rows >= (int64_t(1) << 30) || cols < 1 || cols > 65536 || gate_rows < 0 ||
+      (gate_rows > 0 && rows > 0 && (gate_rows > rows || rows % gate_rows != 0)))
+    return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  *bytes = rows == 0 ? 0 : block_norm_workspace(rows, cols, gate_rows, sms);
+  return SYM_OK;
+}
+
+int moe_block_norm_bwd(const sym_block_norm *a, const sym_block_norm_grad *g, symmoe_stream_t stream) {
+  if (!block_ok(a) || !g) return SYM_EINVAL;
+  const int64_t R = a->rows;
+  const int C = a->cols, t = a->dtype;
+  if (!tensor_ok(g->dy, g->ld_dy, R, C, t) || !tensor_ok(g->dh, g->ld_dh, R, C, t) ||
+      !tensor_ok(g->dx, g->ld_dx, R, C, t) || !tensor_ok(g->d_o, g->ld_do, R, C, t) ||
+      !tensor_ok(g->dw_pre, 0, 1, C, t) || !tensor_ok(g->dw_post, 0, 1, C, t) ||
+      !tensor_ok(g->dgate, g->ld_dgate, a->gate_rows, C, t) || (reinterpret_cast<uintptr_t>(g->work) & 15u))
+    return SYM_EINVAL;
+  if ((!a->gate && g->dgate) || ((a->flags & SYM_NORM_NO_POST) && g->dw_post)) return SYM_EINVAL;
+  if (R == 0) {  // sums over no rows
+    const cudaStream_t st = (cudaStream_t)stream;
+    const size_t row = C * size_of(t);
+    cudaError_t e = cudaSuccess;
+    if (g->dw_pre) e = cudaMemsetAsync(g->dw_pre, 0, row, st);
+    if (e == cudaSuccess && g->dw_post) e = cudaMemsetAsync(g->dw_post, 0, row, st);
+    if (e == cudaSuccess && g->dgate) {
+      const size_t pitch = a->gate_rows > 1 ? g->ld_dgate * size_of(t) : row;
+      e = cudaMemset2DAsync(g->dgate, pitch, 0, row, (size_t)a->gate_rows, st);
+    }
+    return from_cuda(e);
+  }
+  if ((!a->o && (g->d_o || g->dw_post)) || (!g->dy && !g->dh) || (g->dh && (!a->y || !a->rstd_pre)) || (!g->dh && g->dw_pre) ||
+      (a->o && !(a->flags & SYM_NORM_NO_POST) && !a->rstd_post))
+    return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  if (!g->work || g->work_bytes < block_norm_workspace(R, C, g->dgate ? a->gate_rows : 0, sms)) return SYM_ENOSPACE;
+  return from_cuda(launch_block_norm_bwd(*a, *g, sms, (cudaStream_t)stream));
 }
 
 const char *sym_strerror(int code) {

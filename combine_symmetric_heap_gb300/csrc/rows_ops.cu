@@ -1,0 +1,244 @@
+// rows_ops.cu -- row-wise operators between and after the grouped products:
+// SwiGLU of expert rows with the row's routing weight, forward and backward,
+// and dropout whose mask is recomputed from a counter instead of stored.
+//
+//   h  = rw * silu(g) * u            silu(g) = g * s, s = 1 / (1 + exp(-g))
+//   dg = rw * dh * u * s * (1 + g * (1 - s)),  du = rw * dh * silu(g),
+//   d_rw = sum over the row of dh * silu(g) * u
+//   y  = residual + x * [word(i) >= p * 2^32] / (1 - p)
+//
+// All are bound by their bytes.  A row is walked in 16-byte vectors; where the
+// rows start off a 16-byte boundary (odd row lengths) all tensors of a call
+// are off by the same amount, and only the vectors cut by the row's ends are
+// moved element by element.
+#include <algorithm>
+
+#include "rows_dev.cuh"
+
+namespace symmoe {
+namespace rows {
+
+constexpr int THREADS = 256;
+
+struct View {
+  char *ptr;
+  int64_t ld, slot;  // bytes
+};
+
+struct RowArgs {
+  View a, b, c, d, e;  // swiglu: g u h; backward: g u dh dg du; dropout: x residual y
+  const float *rw;
+  float *drw;
+  int64_t rw_slot, drw_slot;
+  const int32_t *total;
+  int64_t total_slot;
+  int64_t rows;
+  int slots, cols;
+};
+
+template <typename T>
+__device__ __forceinline__ T *row_of(const View &v, int d, int64_t r) {
+  return reinterpret_cast<T *>(v.ptr + d * v.slot + r * v.ld);
+}
+// elements between the 16-byte boundary at or before p and p (V = 1: none)
+template <typename T, int V>
+__device__ __forceinline__ int skew(const T *p) {
+  return V == 1 ? 0 : (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
+
+// rows a slot holds: total[slot] where given (values outside [0, rows] are cut)
+__device__ __forceinline__ int64_t live_rows(const RowArgs &p, int d) {
+  if (!p.total) return p.rows;
+  const int64_t t = p.total[d * p.total_slot];
+  return t < 0 ? 0 : t > p.rows ? p.rows : t;
+}
+
+// (1 + exp(-g) may overflow: the quotient is then 0, the limit)
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+// blockDim (threads of a row, rows of a block); grid (blocks, slots)
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS) swiglu_kernel(const RowArgs p) {
+  const int d = blockIdx.y;
+  const int64_t rows = live_rows(p, d);
+  for (int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; r < rows; r += (int64_t)gridDim.x * blockDim.y) {
+    const T *g = row_of<T>(p.a, d, r), *u = row_of<T>(p.b, d, r);
+    T *h = row_of<T>(p.c, d, r);
+    const float w = p.rw ? p.rw[d * p.rw_slot + r] : 1.f;
+    for (int c = (int)threadIdx.x * V - skew<T, V>(g); c < p.cols; c += blockDim.x * V) {
+      float gv[V], uv[V];
+      load_part<T, V>(g, c, p.cols, gv);
+      load_part<T, V>(u, c, p.cols, uv);
+#pragma unroll
+      for (int i = 0; i < V; ++i) gv[i] = w * (gv[i] * sigmoid(gv[i])) * uv[i];
+      store_part<T, V>(h, c, p.cols, gv);
+    }
+  }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS) swiglu_bwd_kernel(const RowArgs p) {
+  __shared__ float buf[2][32];
+  const int d = blockIdx.y;
+  const int64_t rows = live_rows(p, d);
+  const int warps_row = blockDim.x / 32, warp = threadIdx.x / 32, base = threadIdx.y * warps_row;
+  int turn = 0;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < rows; r0 += step) {
+    const int64_t r = r0 + threadIdx.y;
+    float sum = 0.f;
+    if (r < rows) {
+      const T *g = row_of<T>(p.a, d, r), *u = row_of<T>(p.b, d, r), *dh = row_of<T>(p.c, d, r);
+      T *dg = row_of<T>(p.d, d, r), *du = row_of<T>(p.e, d, r);
+      const float w = p.rw ? p.rw[d * p.rw_slot + r] : 1.f;
+      for (int c = (int)threadIdx.x * V - skew<T, V>(g); c < p.cols; c += blockDim.x * V) {
+        float gv[V], uv[V], hv[V];
+        load_part<T, V>(g, c, p.cols, gv);
+        load_part<T, V>(u, c, p.cols, uv);
+        load_part<T, V>(dh, c, p.cols, hv);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float s = sigmoid(gv[i]), silu = gv[i] * s, wh = w * hv[i];
+          sum += hv[i] * silu * uv[i];
+          gv[i] = wh * uv[i] * (s * (1.f + gv[i] * (1.f - s)));
+          uv[i] = wh * silu;
+        }
+        store_part<T, V>(dg, c, p.cols, gv);
+        store_part<T, V>(du, c, p.cols, uv);
+      }
+    }
+    if (!p.drw) continue;
+    float v[1] = {sum};
+    warp_sums<1>(v);
+    if (warps_row > 1) {
+      if ((threadIdx.x & 31) == 0) buf[turn][base + warp] = v[0];
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        v[0] = 0.f;
+        for (int i = 0; i < warps_row; ++i) v[0] += buf[turn][base + i];
+      }
+      turn ^= 1;
+    }
+    if (threadIdx.x == 0 && r < rows) p.drw[d * p.drw_slot + r] = v[0];
+  }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS) dropout_kernel(const RowArgs p, const Random rnd) {
+  const int d = blockIdx.y;
+  for (int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; r < p.rows; r += (int64_t)gridDim.x * blockDim.y) {
+    const T *x = row_of<T>(p.a, d, r);
+    T *y = row_of<T>(p.c, d, r);
+    const uint64_t first = ((uint64_t)d * p.rows + r) * p.cols;  // index of the row's first element
+    for (int64_t c = (int64_t)threadIdx.x * V - skew<T, V>(x); c < p.cols; c += blockDim.x * V) {
+      float xv[V], k[V];
+      load_part<T, V>(x, (int)c, p.cols, xv);
+      keep_factors<V>(rnd, first + c, k);
+      if (p.b.ptr) {
+        float rv[V];
+        load_part<T, V>(row_of<T>(p.b, d, r), (int)c, p.cols, rv);
+#pragma unroll
+        for (int i = 0; i < V; ++i) xv[i] = k[i] != 0.f ? rv[i] + xv[i] * k[i] : rv[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) xv[i] = k[i] != 0.f ? xv[i] * k[i] : 0.f;
+      }
+      store_part<T, V>(y, (int)c, p.cols, xv);
+    }
+  }
+}
+
+static View view_of(const sym_rows *r, int64_t es) {
+  if (!r) return View{nullptr, 0, 0};
+  return View{reinterpret_cast<char *>(r->ptr), r->ld * es, r->slots > 1 ? r->slot_stride * es : 0};
+}
+
+struct Shape {
+  dim3 grid, block;
+};
+// Threads of a row: enough for one vector each up to a block of 256, in powers
+// of two from a warp on; the block's other threads take further rows.
+static Shape shape_of(int64_t rows, int slots, int cols, int vec, int num_sms) {
+  int tpr = 32;
+  while (tpr < THREADS && tpr * vec < cols) tpr *= 2;
+  const int rpb = THREADS / tpr;
+  const int64_t blocks = std::min<int64_t>((rows + rpb - 1) / rpb, (int64_t)num_sms * 32);
+  return Shape{dim3((unsigned)std::max<int64_t>(1, blocks), slots), dim3(tpr, rpb)};
+}
+
+// Do all tensors of a call start their rows at the same place of a 16-byte
+// line, so that they can be walked in the same vectors?
+static bool same_skew(std::initializer_list<const sym_rows *> all, int64_t es) {
+  const sym_rows *f = *all.begin();
+  for (const sym_rows *r : all) {
+    if (!r) continue;
+    if ((r->ptr - f->ptr) % 16 || ((r->ld - f->ld) * es) % 16 ||
+        (r->slots > 1 && ((r->slot_stride - f->slot_stride) * es) % 16))
+      return false;
+  }
+  return true;
+}
+
+}  // namespace rows
+
+#define SYM_ROWS_LAUNCH(KERNEL, ...)                                                                      \
+  switch (dtype) {                                                                                        \
+    case SYM_BF16:                                                                                        \
+      if (vec) rows::KERNEL<__nv_bfloat16, 8><<<s.grid, s.block, 0, st>>>(__VA_ARGS__);                   \
+      else rows::KERNEL<__nv_bfloat16, 1><<<s.grid, s.block, 0, st>>>(__VA_ARGS__);                       \
+      break;                                                                                              \
+    case SYM_FP16:                                                                                        \
+      if (vec) rows::KERNEL<__half, 8><<<s.grid, s.block, 0, st>>>(__VA_ARGS__);                          \
+      else rows::KERNEL<__half, 1><<<s.grid, s.block, 0, st>>>(__VA_ARGS__);                              \
+      break;                                                                                              \
+    default:                                                                                              \
+      if (vec) rows::KERNEL<float, 4><<<s.grid, s.block, 0, st>>>(__VA_ARGS__);                           \
+      else rows::KERNEL<float, 1><<<s.grid, s.block, 0, st>>>(__VA_ARGS__);                               \
+  }                                                                                                       \
+  return cudaGetLastError();
+
+static int64_t elem_size(int dtype) { return dtype == SYM_FP32 ? 4 : 2; }
+
+cudaError_t launch_swiglu_rows(int dtype, const sym_rows &g, const sym_rows &u, const sym_rows &h, const float *rw,
+                               int64_t rw_slot, const int32_t *total, int64_t total_slot, int num_sms,
+                               cudaStream_t st) {
+  using namespace rows;
+  const int64_t es = elem_size(dtype);
+  const bool vec = same_skew({&g, &u, &h}, es);
+  RowArgs a = {};
+  a.a = view_of(&g, es), a.b = view_of(&u, es), a.c = view_of(&h, es);
+  a.rw = rw, a.rw_slot = rw_slot, a.total = total, a.total_slot = total_slot;
+  a.rows = g.rows, a.slots = g.slots, a.cols = g.cols;
+  const Shape s = shape_of(g.rows, g.slots, g.cols, vec ? (int)(16 / es) : 1, num_sms);
+  SYM_ROWS_LAUNCH(swiglu_kernel, a)
+}
+
+cudaError_t launch_swiglu_rows_bwd(int dtype, const sym_rows &g, const sym_rows &u, const sym_rows &dh,
+                                   const sym_rows &dg, const sym_rows &du, const float *rw, int64_t rw_slot,
+                                   float *drw, int64_t drw_slot, const int32_t *total, int64_t total_slot,
+                                   int num_sms, cudaStream_t st) {
+  using namespace rows;
+  const int64_t es = elem_size(dtype);
+  const bool vec = same_skew({&g, &u, &dh, &dg, &du}, es);
+  RowArgs a = {};
+  a.a = view_of(&g, es), a.b = view_of(&u, es), a.c = view_of(&dh, es), a.d = view_of(&dg, es), a.e = view_of(&du, es);
+  a.rw = rw, a.rw_slot = rw_slot, a.drw = drw, a.drw_slot = drw_slot, a.total = total, a.total_slot = total_slot;
+  a.rows = g.rows, a.slots = g.slots, a.cols = g.cols;
+  const Shape s = shape_of(g.rows, g.slots, g.cols, vec ? (int)(16 / es) : 1, num_sms);
+  SYM_ROWS_LAUNCH(swiglu_bwd_kernel, a)
+}
+
+cudaError_t launch_dropout(int dtype, const sym_rows &x, const sym_rows *res, const sym_rows &y, uint64_t seed,
+                           uint64_t offset, uint32_t threshold, float keep_scale, int num_sms, cudaStream_t st) {
+  using namespace rows;
+  const int64_t es = elem_size(dtype);
+  const bool vec = same_skew({&x, &y, res}, es);
+  const Random rnd{seed, offset, threshold, keep_scale};
+  RowArgs a = {};
+  a.a = view_of(&x, es), a.b = view_of(res, es), a.c = view_of(&y, es);
+  a.rows = x.rows, a.slots = x.slots, a.cols = x.cols;
+  const Shape s = shape_of(x.rows, x.slots, x.cols, vec ? (int)(16 / es) : 1, num_sms);
+  SYM_ROWS_LAUNCH(dropout_kernel, a, rnd)
+}
+
+}  // namespace symmoe

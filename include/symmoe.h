@@ -448,6 +448,206 @@ int moe_dispatch_layout_noalloc(const moe_shape *s, const int32_t *idx, int32_t 
                                 int32_t *recv_off, int32_t *total_recv, int32_t *pos,
                                 symmoe_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Training through an MoE block.  The calls below work on plain tensors or on
+ * a heap's windows alike (a sym_rows over a window); none needs a heap.  They
+ * allocate nothing, keep no state between calls and may run on any streams at
+ * the same time as long as their outputs (and workspaces) differ.
+ *
+ * Types: SYM_BF16, SYM_FP16 (the products), and SYM_FP32 (the other calls
+ * too).  Sums, norms and products accumulate in 32 bits; every result is
+ * rounded once, to its tensor's type.
+ * ---------------------------------------------------------------------------
+ */
+#define SYM_BF16 0
+#define SYM_FP16 1
+#define SYM_FP32 2
+
+/*
+ * sym_rows: `slots` x `rows` rows of `cols` contiguous elements; row r of slot
+ * d starts at element d * slot_stride + r * ld (slot_stride is not read when
+ * slots == 1).  A plain [R][cols] tensor has slots = 1; the recv_x window of a
+ * heap has slots = W, rows = cap, ld = H, slot_stride = per_rank_size / 2.
+ */
+typedef struct sym_rows {
+  uint64_t ptr;
+  int64_t ld;
+  int64_t slot_stride;
+  int64_t rows;
+  int32_t slots;
+  int32_t cols;
+} sym_rows;
+
+/*
+ * sym_groups: the row ranges of the experts (groups).  Group e belongs to slot
+ * d = e / (groups / slots) and owns rows [off, off + cnt) of it, with cnt =
+ * cnt[d * cnt_slot_stride + e mod (groups / slots)] and off likewise, int32 in
+ * device memory (read by the kernels; no host sync).  Ranges may leave gaps
+ * but must not overlap.  A group whose range does not lie in [0, rows) of its
+ * slot is taken as empty and SYM_STATUS_OVERFLOW is raised.
+ *   status: device word that SYM_STATUS_* bits are OR-ed into, or NULL;
+ *   wait_timeout_us: bound on the kernels' internal waits (0: 2,000,000).
+ */
+typedef struct sym_groups {
+  const int32_t *cnt, *off;
+  int64_t cnt_slot_stride, off_slot_stride;
+  int32_t *status;
+  int32_t groups;
+  int32_t slots;
+  uint32_t wait_timeout_us;
+  uint32_t reserved;
+} sym_groups;
+
+/*
+ * moe_grouped_matmul: the product of every group's rows with its own matrix:
+ *   out[r][f] = sum_c x[r][c] * w[e][f][c]                     flags 0
+ *   out[r][f] = sum_c x[r][c] * w[e][c][f]                     SYM_GM_TRANS_W
+ * for the rows r of group e (F = out->cols, C = x->cols).  With w [E][F][C]
+ * the first form is a linear layer's forward product and, on the same weights
+ * with the sizes exchanged, the second its data gradient.
+ *   dtype: SYM_BF16 or SYM_FP16, of x, w and out; accumulated in fp32 in
+ *   tensor memory, rounded once.
+ *   w: device, 16-byte aligned; matrix e at element e * w_group_stride, its
+ *   rows w_ld elements apart, both multiples of 8.
+ *   x: 16-byte aligned, ld (and slot_stride) multiples of 8.  out: any ld.
+ *   slots, rows of x and out are equal.  Any C, F in [1, 65536], any number of
+ *   rows per group; at most 1024 groups.
+ * Rows of out outside every group are not written.  out must not overlap x
+ * or w.  Returns SYM_OK, SYM_EINVAL or SYM_ECUDA; asynchronous.
+ */
+#define SYM_GM_TRANS_W 1
+int moe_grouped_matmul(const sym_groups *g, int dtype, const sym_rows *x, const void *w,
+                       int64_t w_group_stride, int64_t w_ld, int flags, const sym_rows *out,
+                       symmoe_stream_t stream);
+
+/*
+ * moe_grouped_wgrad: the weight gradient of moe_grouped_matmul,
+ *   dw[e][f][c] = sum over the rows r of group e of dy[r][f] * x[r][c],
+ * zeros for a group without rows.  SYM_GM_ACCUMULATE: added to what dw holds
+ * (a group without rows is left as it is).
+ *   dtype: SYM_BF16 or SYM_FP16, of dy and x; out_dtype: that, or SYM_FP32.
+ *   dy, x: as x above, equal slots and rows.  dw: device; matrix e at element
+ *   e * dw_group_stride, its rows dw_ld elements apart (any strides; 16-byte
+ *   aligned ones are stored faster).
+ * The contraction runs over the group's rows in order, one work item per
+ * output tile: the result does not depend on the schedule.  The tensor
+ * cores' additions into the fp32 accumulator truncate: relative error about
+ * 1e-8 per 16 rows of a group on top of the result's rounding.
+ */
+#define SYM_GM_ACCUMULATE 1
+int moe_grouped_wgrad(const sym_groups *g, int dtype, const sym_rows *dy, const sym_rows *x,
+                      void *dw, int64_t dw_group_stride, int64_t dw_ld, int out_dtype, int flags,
+                      symmoe_stream_t stream);
+
+/*
+ * moe_swiglu_rows: what stands between the grouped products of a SwiGLU
+ * expert, h = row_w * silu(g) * u per row, with the row's routing weight (or
+ * 1): with the weight here, the combine that follows is the unweighted one and
+ * the weight's gradient a sum over the row.
+ *   dtype: SYM_BF16, SYM_FP16 or SYM_FP32, of g, u and h (equal slots, rows,
+ *   cols; any strides: rows that all start at the same place of a 16-byte line
+ *   in every tensor move in 16-byte vectors).
+ *   row_w: device fp32, row r of slot d at d * row_w_slot_stride + r; or NULL.
+ *   total: device int32, total[d * total_slot_stride] = rows of slot d to do
+ *   (read by the kernel, cut to [0, rows]); NULL: all.  Other rows are not
+ *   read or written.
+ * h may be g or u.  Returns SYM_OK, SYM_EINVAL or SYM_ECUDA; asynchronous.
+ */
+int moe_swiglu_rows(int dtype, const sym_rows *g, const sym_rows *u, const float *row_w,
+                    int64_t row_w_slot_stride, const int32_t *total, int64_t total_slot_stride,
+                    const sym_rows *h, symmoe_stream_t stream);
+
+/*
+ * moe_swiglu_rows_bwd: the gradients of moe_swiglu_rows from dh:
+ *   dg = row_w * dh * u * silu'(g),  du = row_w * dh * silu(g),
+ *   d_row_w[r] = sum_c dh * silu(g) * u   (fp32, strided like row_w; or NULL).
+ * dg may be g or dh, du may be u.
+ */
+int moe_swiglu_rows_bwd(int dtype, const sym_rows *g, const sym_rows *u, const sym_rows *dh,
+                        const float *row_w, int64_t row_w_slot_stride, const int32_t *total,
+                        int64_t total_slot_stride, const sym_rows *dg, const sym_rows *du,
+                        float *d_row_w, int64_t d_row_w_slot_stride, symmoe_stream_t stream);
+
+/*
+ * moe_dropout: y = residual + x * keep / (1 - p) (residual may be NULL), where
+ * the element with index i = (slot * rows + row) * cols + column is kept iff
+ * word(i) >= floor(p * 2^32).  word(i) is word i mod 4 of block i / 4 of
+ * Philox 4x32-10 under the key `seed` and the upper counter half `offset`: the
+ * mask is a function of (seed, offset, i) and never stored; the same call on
+ * the output's gradient is the backward pass.  A dropped element contributes
+ * exactly 0, whatever x holds there (infinities and NaN too).
+ *   dtype: SYM_BF16, SYM_FP16 or SYM_FP32.  0 <= p < 1.
+ * y may be x or residual.  Returns SYM_OK, SYM_EINVAL or SYM_ECUDA; async.
+ */
+int moe_dropout(int dtype, const sym_rows *x, const sym_rows *residual, const sym_rows *y,
+                double p, uint64_t seed, uint64_t offset, symmoe_stream_t stream);
+
+/*
+ * moe_block_norm: the norms before and after a block in one pass over the
+ * rows, with the block's gate, dropout and residual scale:
+ *   n = o * rstd_post * w_post       rstd_post = 1 / sqrt(mean(o^2) + eps)
+ *   y = x + scale * drop(act(gate) * n)
+ *   h = y * rstd_pre * w_pre         rstd_pre = 1 / sqrt(mean(y^2) + eps)
+ * o: the block's output; x: the residual stream; y: the stream after the
+ * block; h: the next block's input, from the unrounded y.
+ *   o NULL: the norm before a first block only (y = x; y is not written).
+ *   SYM_NORM_NO_POST: no norm after the block (n = o; w_post, rstd_post NULL).
+ *   h NULL: no norm before a next one.
+ *   w_post, w_pre [cols]: NULL = ones.  gate [gate_rows][cols], row r uses gate
+ *   row r / (rows / gate_rows): one gate for all rows, one for each sequence
+ *   or one for each row; NULL = ones.  gate_act: SYM_GATE_*.
+ *   p, seed, offset: dropout as in moe_dropout, element index row * cols + col.
+ *   rstd_post, rstd_pre: device fp32 [rows], out (kept for the backward), each
+ *   may be NULL.
+ * All tensors have the type dtype; rows ld_* elements apart; vectors of 16
+ * bytes are used when every base, stride and cols allow.  y may be x.
+ * cols <= 65536; gate_rows divides rows; 0 <= p < 1; eps >= 0.
+ */
+#define SYM_GATE_NONE 0
+#define SYM_GATE_SIGMOID 1
+#define SYM_GATE_TANH 2
+#define SYM_NORM_NO_POST 1
+typedef struct sym_block_norm {
+  int64_t rows;
+  int32_t cols, dtype;
+  const void *x, *o, *w_post, *gate, *w_pre;
+  void *y, *h;
+  float *rstd_post, *rstd_pre;
+  int64_t ld_x, ld_o, ld_gate, ld_y, ld_h;
+  int64_t gate_rows;
+  int32_t gate_act, flags;
+  float scale, eps;
+  double p;
+  uint64_t seed, offset;
+} sym_block_norm;
+int moe_block_norm(const sym_block_norm *a, symmoe_stream_t stream);
+
+/*
+ * moe_block_norm_bwd: gradients of moe_block_norm.  Of `a` it reads o, w_post,
+ * gate, w_pre, y (the stream after the block; with o NULL the stream itself)
+ * and rstd_post, rstd_pre as the forward left them; x, h and eps are not used.
+ *   dy: gradient of y from elsewhere (NULL: none); dh: gradient of h (NULL:
+ *   none; then y, w_pre, rstd_pre are not read).
+ *   dx: gradient of x (= of y; may be dy); d_o, dw_pre, dw_post, dgate: each
+ *   of the type of what it is the gradient of, each may be NULL.
+ *   work: device, 16-byte aligned, at least moe_block_norm_workspace(...)
+ *   bytes; contents do not matter before or after.
+ * Column sums are taken in 32 bits in an order that depends on the sizes and
+ * the device's SM count only.
+ */
+typedef struct sym_block_norm_grad {
+  const void *dy, *dh;
+  void *dx, *d_o, *dw_pre, *dw_post, *dgate;
+  int64_t ld_dy, ld_dh, ld_dx, ld_do, ld_dgate;
+  void *work;
+  uint64_t work_bytes;
+} sym_block_norm_grad;
+int moe_block_norm_bwd(const sym_block_norm *a, const sym_block_norm_grad *g, symmoe_stream_t stream);
+
+/* Workspace bytes of moe_block_norm_bwd (gate_rows 0: no gate gradient).  Host only. */
+int moe_block_norm_workspace(int64_t rows, int32_t cols, int64_t gate_rows, uint64_t *bytes);
+
 /* Static description of a SYM_* code (never NULL). */
 const char *sym_strerror(int code);
 
