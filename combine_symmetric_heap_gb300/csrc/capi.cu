@@ -407,7 +407,7 @@ int moe_grouped_wgrad(const sym_groups *g, int dtype, const sym_rows *dy, const 
   if ((dtype != SYM_BF16 && dtype != SYM_FP16) || (out_dtype != dtype && out_dtype != SYM_FP32) ||
       (flags & ~SYM_GM_ACCUMULATE) || !rows_tma_ok(dy) || !rows_tma_ok(x) || !same_rows(dy, x) || !groups_ok(g, x) ||
       !dw || reinterpret_cast<uintptr_t>(dw) % (out_dtype == SYM_FP32 ? 4 : 2) != 0 || dw_ld < x->cols ||
-      (g->groups > 1 && dw_group_stride < 0))
+      (g->groups > 1 && dw_group_stride < (dy->cols - 1) * dw_ld + x->cols))
     return SYM_EINVAL;
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return SYM_ECUDA;

@@ -32,10 +32,13 @@ namespace grouped {
 using namespace gemm2;
 
 constexpr int PRODUCT_THREADS = 192;  // producer, MMA issuer, 4 epilogue warps
-constexpr int WGRAD_THREADS = 224;    // ... and the warp that zeroes rows past a group's end
+constexpr int WG_EPI_WARPS = 4;       // one per TMEM lane quarter
+constexpr int WGRAD_THREADS = 32 * (3 + WG_EPI_WARPS);  // ... and the warp that zeroes rows past a group's end
 constexpr int CTRL_BYTES = 512;
 constexpr int CHUNK_BYTES = BK * 64 * 2;  // 64 contraction rows x 64 features (MN-major tiles)
 constexpr int WG_STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int WG_STAGES = 6;
+constexpr int WG_OUT_BYTES = 32 * 128;  // staged output of a warp: 32 rows of 128 bytes
 
 struct Groups {
   const int32_t *cnt, *off;
@@ -142,7 +145,7 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
 }
 
 // ---------------------------------------------------------------------------
-// group tables: rows, first row and prefix of row tiles of every group.  A
+// group tables: rows, first row and (product) prefix of row tiles of every group.  A
 // group whose range does not lie in its slot is taken as empty and flagged.
 // ---------------------------------------------------------------------------
 __device__ inline void build_tables(const Groups &g, const TokTables &tb, bool report) {
@@ -157,6 +160,7 @@ __device__ inline void build_tables(const Groups &g, const TokTables &tb, bool r
     tb.cnt[e] = c;
     tb.roff[e] = o;
   }
+  if (!tb.tokprefix) return;
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
@@ -208,18 +212,20 @@ __device__ inline Tile decode_product(const Groups &g, const TokTables &tb, int 
 // ---------------------------------------------------------------------------
 // product kernel
 // ---------------------------------------------------------------------------
-struct Ring {
+template <int N>
+struct RingOf {
   uint8_t *base;
   uint64_t *full, *empty;
   int stage = 0;
   uint32_t phase = 0;
   __device__ __forceinline__ void next() {
-    if (++stage == STAGES) {
+    if (++stage == N) {
       stage = 0;
       phase ^= 1u;
     }
   }
 };
+using Ring = RingOf<STAGES>;
 
 // K loop of the producer for one tile; TWO: with a remainder part
 template <bool TRANS, bool TWO>
@@ -267,13 +273,16 @@ __device__ __forceinline__ bool product_mma(Ring &rg, const Ctl &ctl, uint32_t d
   return true;
 }
 
-// hand an accumulator (or its head) back to the leader's MMA
+// Hand an accumulator (or its head) back to the leader's MMA.  What the arrival
+// orders is the warp's finished TMEM reads, nothing in memory, so the peer's
+// remote arrival releases at CTA scope: a release at cluster scope waits for
+// the warp's stores (a third of the weight gradient's epilogue, 1900 cycles a tile).
 __device__ __forceinline__ void give_back(uint64_t *bar, uint32_t rank, int lane) {
   tc_fence_before();
   __syncwarp();
   if (lane == 0) {
     if (rank == 0) mbar_arrive(bar);
-    else mbar_arrive_remote(map_to(bar, 0));
+    else asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(map_to(bar, 0)) : "memory");
   }
 }
 
@@ -486,40 +495,100 @@ __device__ __forceinline__ void wgrad_store(void *row, const uint32_t (&v)[32], 
   }
 }
 
+// shared -> global tensor copies of the calling thread's bulk group: a box as
+// it is, or added to what is there (fp32); elements past the extents are cut
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, const void *src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap *m, const void *src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+// all but the newest N groups of this thread have read their shared memory
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// Order this thread's stores to shared memory before later tensor copies out
+// of it.  The unrestricted proxy fence also waits for global accesses: with it
+// the weight gradient of the prefill shape took 3.49 ms, with this one 2.99.
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// This lane's row of a staged box (128 bytes: 32 floats or 64 16-bit values),
+// in the 128-byte swizzle: 16-byte word j of row r sits at word j ^ (r mod 8).
+template <int OT>
+__device__ __forceinline__ void stage_row(uint8_t *box, int lane, const uint32_t *v) {
+  uint8_t *row = box + lane * 128;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint4 w;
+    if (OT == OUT_FP32) {
+      w = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+      constexpr bool H = OT == OUT_FP16;
+      const uint32_t *s = v + 8 * j;
+      w = make_uint4(narrow2<H>(__uint_as_float(s[0]), __uint_as_float(s[1])),
+                     narrow2<H>(__uint_as_float(s[2]), __uint_as_float(s[3])),
+                     narrow2<H>(__uint_as_float(s[4]), __uint_as_float(s[5])),
+                     narrow2<H>(__uint_as_float(s[6]), __uint_as_float(s[7])));
+    }
+    *reinterpret_cast<uint4 *>(row + ((j ^ (lane & 7)) << 4)) = w;
+  }
+}
+
+// by_tma: the output's rows are 16-byte aligned and written (fp32: or added)
+// by tensor copies from a staged box per warp.  Direct stores of each lane's
+// row touch 32 lines per instruction with half a sector each: the prefill
+// shape (256 experts, 2048 x 7168, bf16) took 4.57 ms that way.
 template <int OT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
-    grouped_wgrad_kernel(const Groups g, const Out o, int F, int C, int fp16, int add,
-                         const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x) {
+    grouped_wgrad_kernel(const Groups g, const Out o, int F, int C, int fp16, int add, int by_tma,
+                         const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x,
+                         const __grid_constant__ CUtensorMap tm_dw) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *ctrl = smem + (size_t)STAGES * WG_STAGE_BYTES;
+  uint8_t *boxes = smem + (size_t)WG_STAGES * WG_STAGE_BYTES;
+  uint8_t *ctrl = boxes + WG_EPI_WARPS * WG_OUT_BYTES;
   uint64_t *bars = reinterpret_cast<uint64_t *>(ctrl);
-  uint64_t *tail = bars + 2 * STAGES;  // [STAGES] this CTA's copies of a cut K block
-  uint64_t *acc_full = tail + STAGES, *acc_empty = acc_full + 2;
+  uint64_t *tail = bars + 2 * WG_STAGES;  // [WG_STAGES] this CTA's copies of a cut K block
+  uint64_t *peer_cut = tail + WG_STAGES;  // [WG_STAGES] (the leader's) the peer's half of a cut block is ready
+  uint64_t *acc_full = peer_cut + WG_STAGES, *acc_empty = acc_full + 2;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(acc_full + 4);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base_s + 1);
   int *tab = reinterpret_cast<int *>(ctrl + CTRL_BYTES);
-  const TokTables tb{tab, tab + g.G, tab + 2 * g.G};
+  const TokTables tb{tab, tab + g.G, nullptr};
   const int wid = warp_id(), lane = lane_id();
   const uint32_t rank = cta_rank();
   const int pair = (int)cluster_id_x(), npairs = (int)num_clusters_x();
   const Ctl ctl{abort_flag, g.status, g.tmo};
-  Ring rg{smem, bars, bars + STAGES};
+  RingOf<WG_STAGES> rg{smem, bars, bars + WG_STAGES};
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&rg.full[s], 2);  // used on the leader: one arrival per CTA
+    for (int s = 0; s < WG_STAGES; ++s) {
+      // full (the leader's is used): its producer's arrival with both CTAs'
+      // bytes, or for a cut block its zeroing warp's arrival
+      mbar_init(&rg.full[s], 1);
       mbar_init(&rg.empty[s], 1);
       mbar_init(&tail[s], 1);
+      mbar_init(&peer_cut[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);
+      mbar_init(&acc_empty[b], 2 * WG_EPI_WARPS);
     }
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_dy);
     tma_prefetch_desc(&tm_x);
+    if (by_tma) tma_prefetch_desc(&tm_dw);
   }
   if (wid == 1) {
     tmem_alloc2(tmem_base_s, TMEM_COLS);
@@ -548,8 +617,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
           uint8_t *sb = rg.base + (size_t)rg.stage * WG_STAGE_BYTES;
           const int row = ti.row0 + kb * BK;
           if (kb == nk - 1 && (ti.cnt & (UK - 1))) {
-            // the block's last MMA step runs past the group: this CTA's zeroing
-            // warp takes the copies and reports the stage to the leader
+            // the block's last MMA step runs past the group: the CTAs' zeroing
+            // warps take the copies and report the stage
             mbar_arrive_expect_tx(&tail[rg.stage], WG_STAGE_BYTES);
             for (int h = 0; h < 2; ++h) {
               tma_load_3d(sb + h * CHUNK_BYTES, &tm_dy, &tail[rg.stage], f0 + h * 64, row, ti.d);
@@ -558,7 +627,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
           } else {
             const uint32_t bar = full_leader + (uint32_t)(rg.stage * sizeof(uint64_t));
             if (rank == 0) mbar_arrive_expect_tx(&rg.full[rg.stage], 2 * WG_STAGE_BYTES);
-            else mbar_arrive_remote(bar);
             for (int h = 0; h < 2; ++h) {
               tma_load_3d_pair(sb + h * CHUNK_BYTES, &tm_dy, bar, f0 + h * 64, row, ti.d);
               tma_load_3d_pair(sb + A_BYTES + h * CHUNK_BYTES, &tm_x, bar, c0 + h * 64, row, ti.d);
@@ -599,59 +667,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
         b ^= 1;
       }
     }
-  } else if (wid == 6) {
+  } else if (wid == 2 + WG_EPI_WARPS) {
     // ------------------------------------ zeroing of rows past a group's end
+    // (Only cut blocks cross the pair here: a release at cluster scope in the
+    // peer's producer, one per K block, held every block to 0.8 us.)
     uint32_t uses = 0;  // bit s: parity of stage s's next cut block
     int stage = 0;
     for (int i = 0, t; (t = pair_tile(i, pair, npairs)) < total; ++i) {
       const WTile ti = decode_wgrad(g, tb.cnt, tb.roff, nf, nc, t);
       const int nk = (ti.cnt + BK - 1) / BK;
       if (nk && (ti.cnt & (UK - 1))) {
-        const int s = (stage + nk - 1) % STAGES;
+        const int s = (stage + nk - 1) % WG_STAGES;
         if (!__all_sync(0xffffffffu, bar_wait(&tail[s], (uses >> s) & 1u, ctl))) break;
-        uses ^= 1u << s;
         const int v = ti.cnt - (nk - 1) * BK, rows = ((v + UK - 1) & ~(UK - 1)) - v;
         uint8_t *sb = smem + (size_t)s * WG_STAGE_BYTES + v * 128;
         for (int j = lane; j < rows * 32; j += 32)  // 4 chunks x rows x 8 16-byte words
           *reinterpret_cast<uint4 *>(sb + (j / (rows * 8)) * CHUNK_BYTES + (j % (rows * 8)) * 16) =
               make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async();  // the zeros before the tensor core's reads
+        fence_proxy_async_shared();  // the zeros before the tensor core's reads
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_to(&rg.full[s], 0));
+        if (rank != 0) {
+          if (lane == 0) mbar_arrive_remote(map_to(&peer_cut[s], 0));
+        } else {
+          if (!__all_sync(0xffffffffu, bar_wait(&peer_cut[s], (uses >> s) & 1u, ctl))) break;
+          if (lane == 0) mbar_arrive(&rg.full[s]);
+        }
+        uses ^= 1u << s;
       }
-      stage = (stage + nk) % STAGES;
+      stage = (stage + nk) % WG_STAGES;
     }
   } else {
     // -------------------------------------------------------------- epilogue
     const int q = wid & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    constexpr int OB = OT == OUT_FP32 ? 4 : 2;
+    constexpr int OB = OT == OUT_FP32 ? 4 : 2, BOX = 128 / OB;  // bytes of an element, columns of a box
     const bool aligned = ((reinterpret_cast<uintptr_t>(o.ptr) | (uintptr_t)(o.ld * OB) | (uintptr_t)(o.stride * OB)) & 15u) == 0;
+    uint8_t *box = boxes + (size_t)(wid - 2) * WG_OUT_BYTES;
     uint32_t used[2] = {0, 0};
     int b = 0;
     for (int i = 0, t; (t = pair_tile(i, pair, npairs)) < total; ++i) {
       const WTile ti = decode_wgrad(g, tb.cnt, tb.roff, nf, nc, t);
-      const int f = ti.f * 256 + (int)rank * 128 + q * 32 + lane, c0 = ti.c * 256;
+      const int fw = ti.f * 256 + (int)rank * 128 + q * 32, f = fw + lane, c0 = ti.c * 256;  // the warp's rows
       const int cols = min(256, C - c0);
-      uint8_t *row = reinterpret_cast<uint8_t *>(o.ptr) + ((int64_t)ti.e * o.stride + (int64_t)f * o.ld + c0) * OB;
-      if (ti.cnt == 0) {  // a group without rows: zeros, or nothing to add
-        if (add) continue;
-        const uint32_t z[32] = {};
-        for (int c = 0; c < cols; c += 32)
-          if (f < F) wgrad_store<OT>(row + c * OB, z, cols - c, aligned && c + 32 <= cols, false);
-        continue;
-      }
-      if (!__all_sync(0xffffffffu, bar_wait(&acc_full[b], used[b]++ & 1u, ctl))) break;
+      const bool empty = ti.cnt == 0;  // zeros, or nothing to add
+      if (empty && add) continue;
+      if (!empty && !__all_sync(0xffffffffu, bar_wait(&acc_full[b], used[b]++ & 1u, ctl))) break;
       tc_fence_after();
-      for (int c = 0; c < cols; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(lanes + (uint32_t)(b * ACC_COLS + c), v);
-        tmem_ld_wait();
-        if (f < F) wgrad_store<OT>(row + c * OB, v, cols - c, aligned && c + 32 <= cols, add != 0);
+      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS);
+      if (by_tma) {
+#pragma unroll 1
+        for (int c = 0; c < cols; c += BOX) {
+          uint32_t v[BOX];
+          if (empty) {
+#pragma unroll
+            for (int j = 0; j < BOX; ++j) v[j] = 0u;
+          } else {
+#pragma unroll
+            for (int j = 0; j < BOX; j += 32)
+              tmem_ld32(acc + (uint32_t)(c + j), *reinterpret_cast<uint32_t(*)[32]>(v + j));
+            tmem_ld_wait();
+          }
+          if (lane == 0) bulk_wait_read<0>();  // the last copy has left the box
+          __syncwarp();
+          stage_row<OT>(box, lane, v);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            if (fw < F) {
+              if (OT == OUT_FP32 && add) tma_add_3d(&tm_dw, box, c0 + c, fw, ti.e);
+              else tma_store_3d(&tm_dw, box, c0 + c, fw, ti.e);
+            }
+            bulk_commit();
+          }
+        }
+      } else {
+        uint8_t *row = reinterpret_cast<uint8_t *>(o.ptr) + ((int64_t)ti.e * o.stride + (int64_t)f * o.ld + c0) * OB;
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t v[32] = {};
+          if (!empty) {
+            tmem_ld32(acc + (uint32_t)c, v);
+            tmem_ld_wait();
+          }
+          if (f < F) wgrad_store<OT>(row + c * OB, v, cols - c, aligned && c + 32 <= cols, add != 0);
+        }
       }
+      if (empty) continue;
       give_back(&acc_empty[b], rank, lane);
       b ^= 1;
     }
+    if (lane == 0) bulk_wait_all();  // the copies have read their shared memory before the block ends
   }
 
   tc_fence_before();
@@ -664,10 +768,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// 16-bit elements [d2][d1][d0], strides in elements, box [1][b1][b0], 128-byte
+// 16-bit (or fp32) elements [d2][d1][d0], strides in elements, box [1][b1][b0], 128-byte
 // swizzle; elements outside the extents read as zeros
 static bool encode(CUtensorMap *m, uint64_t ptr, uint64_t d0, uint64_t d1, uint64_t d2, int64_t s1, int64_t s2,
-                   uint32_t b0, uint32_t b1) {
+                   uint32_t b0, uint32_t b1, bool fp32 = false) {
   typedef CUresult (*Fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                          const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                          CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -678,9 +782,9 @@ static bool encode(CUtensorMap *m, uint64_t ptr, uint64_t d0, uint64_t d1, uint6
     return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<Fn>(p) : nullptr;
   }();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {(cuuint64_t)s1 * (fp32 ? 4 : 2), (cuuint64_t)s2 * (fp32 ? 4 : 2)};
   const cuuint32_t box[3] = {b0, b1, 1}, step[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, reinterpret_cast<void *>(ptr), dims, strides, box, step,
+  return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, reinterpret_cast<void *>(ptr), dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -740,17 +844,23 @@ cudaError_t launch_grouped_wgrad(const sym_groups &sg, int fp16, const sym_rows 
     ry.rows = rx.rows = 1;
   }
   if (!encode_rows(&md, ry, BK) || !encode_rows(&mx, rx, BK)) return cudaErrorInvalidValue;
-  const size_t smem = 1024 + (size_t)STAGES * WG_STAGE_BYTES + CTRL_BYTES + tok_tables_bytes(sg.groups);
+  const size_t smem = 1024 + (size_t)WG_STAGES * WG_STAGE_BYTES + WG_EPI_WARPS * WG_OUT_BYTES + CTRL_BYTES +
+                      2 * sizeof(int) * sg.groups;
   const Groups g = groups_of(sg, x);
   const Out o{dw, dw_ld, dw_group};
-  switch (out_type) {
-    case OUT_BF16:
-      return launch(grouped_wgrad_kernel<OUT_BF16>, WGRAD_THREADS, smem, num_sms, st, g, o, dy.cols, x.cols, fp16, add, md, mx);
-    case OUT_FP16:
-      return launch(grouped_wgrad_kernel<OUT_FP16>, WGRAD_THREADS, smem, num_sms, st, g, o, dy.cols, x.cols, fp16, add, md, mx);
-    default:
-      return launch(grouped_wgrad_kernel<OUT_FP32>, WGRAD_THREADS, smem, num_sms, st, g, o, dy.cols, x.cols, fp16, add, md, mx);
-  }
+  // Tensor copies need 16-byte aligned rows.  16-bit sums onto old values are
+  // stored directly: they are rounded once, a copy would add rounded values.
+  const bool fp32 = out_type == OUT_FP32;
+  const int64_t per16 = fp32 ? 4 : 8, gs = sg.groups > 1 ? dw_group : dw_ld * dy.cols;
+  const int by_tma = reinterpret_cast<uintptr_t>(dw) % 16 == 0 && dw_ld % per16 == 0 && gs % per16 == 0 && (fp32 || !add);
+  CUtensorMap mo = md;
+  if (by_tma && !encode(&mo, reinterpret_cast<uint64_t>(dw), x.cols, dy.cols, sg.groups, dw_ld, gs, fp32 ? 32 : 64, 32, fp32))
+    return cudaErrorInvalidValue;
+  auto go = [&](auto kern) {
+    return launch(kern, WGRAD_THREADS, smem, num_sms, st, g, o, dy.cols, x.cols, fp16, add, by_tma, md, mx, mo);
+  };
+  return fp32 ? go(grouped_wgrad_kernel<OUT_FP32>)
+              : fp16 ? go(grouped_wgrad_kernel<OUT_FP16>) : go(grouped_wgrad_kernel<OUT_BF16>);
 }
 
 }  // namespace symmoe
