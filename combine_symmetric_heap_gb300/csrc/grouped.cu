@@ -14,9 +14,10 @@
 // of both count on the leader's full barrier, its commits free the stage in
 // both).  The product keeps weights on the M side and rows on N, so a ragged
 // group shortens N; wgrad has features on both sides and the ragged axis is
-// K, where a K block that runs past the group's end is cut to whole MMA steps
-// of 16 rows and the rows of the last step beyond the end are zeroed in shared
-// memory (they belong to another group, or to nobody, and may hold anything).
+// K: whole MMA steps of 16 rows stream through the ring, and the last cnt mod
+// 16 rows of a group take a step of their own from a side buffer, where the
+// rows past the group's end (they belong to another group, or to nobody, and
+// may hold anything) are zeroed first.
 //
 // An operand whose contraction index is the outer one in memory (trans
 // weights, both operands of wgrad) is staged as it lies: boxes of 64
@@ -32,13 +33,13 @@ namespace grouped {
 using namespace gemm2;
 
 constexpr int PRODUCT_THREADS = 192;  // producer, MMA issuer, 4 epilogue warps
-constexpr int WG_EPI_WARPS = 4;       // one per TMEM lane quarter
-constexpr int WGRAD_THREADS = 32 * (3 + WG_EPI_WARPS);  // ... and the warp that zeroes rows past a group's end
+constexpr int WG_EPI_WARPS = 8;       // two per TMEM lane quarter, each with half of a tile's columns
+constexpr int WGRAD_THREADS = 32 * (3 + WG_EPI_WARPS);  // ... and the warp of the groups' last rows
 constexpr int CTRL_BYTES = 512;
 constexpr int CHUNK_BYTES = BK * 64 * 2;  // 64 contraction rows x 64 features (MN-major tiles)
 constexpr int WG_STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int WG_STAGES = 6;
-constexpr int WG_OUT_BYTES = 32 * 128;  // staged output of a warp: 32 rows of 128 bytes
+constexpr int WG_OUT_BYTES = 32 * 64;  // staged output of a warp: 32 rows of 64 bytes
 
 struct Groups {
   const int32_t *cnt, *off;
@@ -86,10 +87,10 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, const C
 // Matrix descriptor of an MN-major tile with the 128-byte swizzle: chunks of
 // 64 features, each [64 contraction rows][128 bytes]; the leading offset steps
 // over chunks, the stride offset over groups of 8 contraction rows.
-__device__ __forceinline__ uint64_t smem_desc_mn(const void *tile) {
+__device__ __forceinline__ uint64_t smem_desc_mn(const void *tile, int chunk = CHUNK_BYTES) {
   uint64_t d = 0;
   d |= (smem_u32(tile) >> 4) & 0x3FFFull;
-  d |= (uint64_t)(CHUNK_BYTES >> 4) << 16;
+  d |= (uint64_t)(chunk >> 4) << 16;
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= 1ull << 46;
   d |= 2ull << 61;
@@ -145,7 +146,7 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
 }
 
 // ---------------------------------------------------------------------------
-// group tables: rows, first row and (product) prefix of row tiles of every group.  A
+// group tables: rows, first row and prefix of row tiles of every group.  A
 // group whose range does not lie in its slot is taken as empty and flagged.
 // ---------------------------------------------------------------------------
 __device__ inline void build_tables(const Groups &g, const TokTables &tb, bool report) {
@@ -160,7 +161,6 @@ __device__ inline void build_tables(const Groups &g, const TokTables &tb, bool r
     tb.cnt[e] = c;
     tb.roff[e] = o;
   }
-  if (!tb.tokprefix) return;
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
@@ -427,20 +427,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PRODUCT_THREADS, 1)
 // ---------------------------------------------------------------------------
 // weight gradient kernel: tile (e, f, c) = 256 x 256 of dw[e], K = cnt_e rows
 // ---------------------------------------------------------------------------
+// Row boxes of a K block: a group's last block loads 16, 32 or 64 rows,
+// whichever holds what is left of its whole steps.
+constexpr int WG_BOXES = 3;
+// The side buffer of a group's last cnt mod 16 rows: 16 rows of the CTA's four
+// chunks.  Cutting the last K block in the ring instead held its slot through
+// copy, zeroing and two barriers: 0.3 of 1.98 ms on the prefill shape.
+constexpr int REST_CHUNK = UK * 128;
+constexpr int REST_BYTES = 4 * REST_CHUNK;
+struct WMaps {
+  CUtensorMap m[WG_BOXES];
+};
+
 struct WTile {
   int e, d, f, c, row0, cnt;
 };
-__device__ inline WTile decode_wgrad(const Groups &g, const int *cnt, const int *roff, int nf, int nc, int t) {
+// Tile t, with the group's range read (and checked) when the group changes:
+// one role's walk of the tiles.
+struct WWalk {
+  const Groups &g;
+  int nf, nc;
   WTile ti;
-  ti.e = t / (nf * nc);
-  const int r = t - ti.e * nf * nc;
-  ti.f = r / nc;  // the x tiles of a group pass under each dy tile
-  ti.c = r - ti.f * nc;
-  ti.d = ti.e / g.per_slot;
-  ti.row0 = roff[ti.e];
-  ti.cnt = cnt[ti.e];
-  return ti;
-}
+  __device__ WWalk(const Groups &g_, int nf_, int nc_) : g(g_), nf(nf_), nc(nc_) { ti.e = -1; }
+  __device__ __forceinline__ const WTile &at(int t) {
+    const int e = t / (nf * nc), r = t - e * nf * nc;
+    ti.f = r / nc;  // the x tiles of a group pass under each dy tile
+    ti.c = r - ti.f * nc;
+    if (e != ti.e) {
+      ti.e = e;
+      ti.d = e / g.per_slot;
+      const int l = e - ti.d * g.per_slot;
+      const int c = __ldg(g.cnt + ti.d * g.cnt_ss + l), o = __ldg(g.off + ti.d * g.off_ss + l);
+      const bool ok = c >= 0 && o >= 0 && (int64_t)o + c <= g.cap;
+      ti.cnt = ok ? c : 0;
+      ti.row0 = ok ? o : 0;
+    }
+    return ti;
+  }
+};
 
 enum OutType { OUT_BF16, OUT_FP16, OUT_FP32 };
 
@@ -522,13 +546,13 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// This lane's row of a staged box (128 bytes: 32 floats or 64 16-bit values),
-// in the 128-byte swizzle: 16-byte word j of row r sits at word j ^ (r mod 8).
+// This lane's row of a staged box (64 bytes: 16 floats or 32 16-bit values), in
+// the 64-byte swizzle: 16-byte word j of row r sits at word j ^ (r / 2 mod 4).
 template <int OT>
 __device__ __forceinline__ void stage_row(uint8_t *box, int lane, const uint32_t *v) {
-  uint8_t *row = box + lane * 128;
+  uint8_t *row = box + lane * 64;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     uint4 w;
     if (OT == OUT_FP32) {
       w = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -540,7 +564,7 @@ __device__ __forceinline__ void stage_row(uint8_t *box, int lane, const uint32_t
                      narrow2<H>(__uint_as_float(s[4]), __uint_as_float(s[5])),
                      narrow2<H>(__uint_as_float(s[6]), __uint_as_float(s[7])));
     }
-    *reinterpret_cast<uint4 *>(row + ((j ^ (lane & 7)) << 4)) = w;
+    *reinterpret_cast<uint4 *>(row + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
   }
 }
 
@@ -551,20 +575,20 @@ __device__ __forceinline__ void stage_row(uint8_t *box, int lane, const uint32_t
 template <int OT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
     grouped_wgrad_kernel(const Groups g, const Out o, int F, int C, int fp16, int add, int by_tma,
-                         const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x,
+                         const __grid_constant__ WMaps tm_dy, const __grid_constant__ WMaps tm_x,
                          const __grid_constant__ CUtensorMap tm_dw) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *boxes = smem + (size_t)WG_STAGES * WG_STAGE_BYTES;
-  uint8_t *ctrl = boxes + WG_EPI_WARPS * WG_OUT_BYTES;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(ctrl);
-  uint64_t *tail = bars + 2 * WG_STAGES;  // [WG_STAGES] this CTA's copies of a cut K block
-  uint64_t *peer_cut = tail + WG_STAGES;  // [WG_STAGES] (the leader's) the peer's half of a cut block is ready
-  uint64_t *acc_full = peer_cut + WG_STAGES, *acc_empty = acc_full + 2;
+  uint8_t *rest = smem + (size_t)WG_STAGES * WG_STAGE_BYTES;  // [2]
+  uint8_t *boxes = rest + 2 * REST_BYTES;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(boxes + WG_EPI_WARPS * WG_OUT_BYTES);
+  uint64_t *rest_in = bars + 2 * WG_STAGES;  // [2] this CTA's copies of a group's last rows have landed
+  uint64_t *rest_peer = rest_in + 2;         // [2] (the leader's) the peer's half is zeroed past the end
+  uint64_t *rest_full = rest_in + 4;         // [2] (the leader's) both halves are
+  uint64_t *rest_empty = rest_in + 6;        // [2] the MMA has read it
+  uint64_t *acc_full = rest_in + 8, *acc_empty = acc_full + 2;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(acc_full + 4);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base_s + 1);
-  int *tab = reinterpret_cast<int *>(ctrl + CTRL_BYTES);
-  const TokTables tb{tab, tab + g.G, nullptr};
   const int wid = warp_id(), lane = lane_id();
   const uint32_t rank = cta_rank();
   const int pair = (int)cluster_id_x(), npairs = (int)num_clusters_x();
@@ -573,28 +597,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < WG_STAGES; ++s) {
-      // full (the leader's is used): its producer's arrival with both CTAs'
-      // bytes, or for a cut block its zeroing warp's arrival
       mbar_init(&rg.full[s], 1);
       mbar_init(&rg.empty[s], 1);
-      mbar_init(&tail[s], 1);
-      mbar_init(&peer_cut[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
+      for (int k = 0; k < 8; k += 2) mbar_init(&rest_in[k + b], 1);
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * WG_EPI_WARPS);
     }
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_dy);
-    tma_prefetch_desc(&tm_x);
+    for (int i = 0; i < WG_BOXES; ++i) {
+      tma_prefetch_desc(&tm_dy.m[i]);
+      tma_prefetch_desc(&tm_x.m[i]);
+    }
     if (by_tma) tma_prefetch_desc(&tm_dw);
   }
   if (wid == 1) {
     tmem_alloc2(tmem_base_s, TMEM_COLS);
     tmem_relinquish2();
   }
-  build_tables(g, tb, blockIdx.x == 0);
+  if (blockIdx.x == 0 && g.status)  // groups outside their slot: taken as empty, and flagged
+    for (int e = threadIdx.x; e < g.G; e += blockDim.x) {
+      const int d = e / g.per_slot, l = e - d * g.per_slot;
+      const int c = g.cnt[d * g.cnt_ss + l], o = g.off[d * g.off_ss + l];
+      if (c < 0 || o < 0 || (int64_t)o + c > g.cap) raise(g.status, SYM_STATUS_OVERFLOW);
+    }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -602,35 +630,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
   const uint32_t tmem = *tmem_base_s;
   const int nf = (F + 255) / 256, nc = (C + 255) / 256;
   const int total = g.G * nf * nc;
+  WWalk walk(g, nf, nc);
 
   if (wid == 0) {
     if (lane == 0) {
-      // ------------------------------------------------------------ producer
+      // ------------------------------------------- producer of the whole steps
       const uint32_t full_leader = map_to(rg.full, 0);
       bool ok = true;
       for (int i = 0, t; ok && (t = pair_tile(i, pair, npairs)) < total; ++i) {
-        const WTile ti = decode_wgrad(g, tb.cnt, tb.roff, nf, nc, t);
-        const int nk = (ti.cnt + BK - 1) / BK;
+        const WTile &ti = walk.at(t);
+        const int whole = ti.cnt & ~(UK - 1);
         const int f0 = ti.f * 256 + (int)rank * 128, c0 = ti.c * 256 + (int)rank * 128;
-        for (int kb = 0; kb < nk; ++kb) {
+        for (int k0 = 0; k0 < whole; k0 += BK) {
           if (!(ok = bar_wait(&rg.empty[rg.stage], rg.phase ^ 1u, ctl))) break;
           uint8_t *sb = rg.base + (size_t)rg.stage * WG_STAGE_BYTES;
-          const int row = ti.row0 + kb * BK;
-          if (kb == nk - 1 && (ti.cnt & (UK - 1))) {
-            // the block's last MMA step runs past the group: the CTAs' zeroing
-            // warps take the copies and report the stage
-            mbar_arrive_expect_tx(&tail[rg.stage], WG_STAGE_BYTES);
-            for (int h = 0; h < 2; ++h) {
-              tma_load_3d(sb + h * CHUNK_BYTES, &tm_dy, &tail[rg.stage], f0 + h * 64, row, ti.d);
-              tma_load_3d(sb + A_BYTES + h * CHUNK_BYTES, &tm_x, &tail[rg.stage], c0 + h * 64, row, ti.d);
-            }
-          } else {
-            const uint32_t bar = full_leader + (uint32_t)(rg.stage * sizeof(uint64_t));
-            if (rank == 0) mbar_arrive_expect_tx(&rg.full[rg.stage], 2 * WG_STAGE_BYTES);
-            for (int h = 0; h < 2; ++h) {
-              tma_load_3d_pair(sb + h * CHUNK_BYTES, &tm_dy, bar, f0 + h * 64, row, ti.d);
-              tma_load_3d_pair(sb + A_BYTES + h * CHUNK_BYTES, &tm_x, bar, c0 + h * 64, row, ti.d);
-            }
+          const int row = ti.row0 + k0, left = whole - k0;
+          const int box = left > 32 ? 2 : left > 16 ? 1 : 0;
+          const CUtensorMap *my = &tm_dy.m[box], *mx = &tm_x.m[box];
+          const uint32_t bar = full_leader + (uint32_t)(rg.stage * sizeof(uint64_t));
+          if (rank == 0) mbar_arrive_expect_tx(&rg.full[rg.stage], 8u * 128u * (16u << box));  // both CTAs' chunks
+          for (int h = 0; h < 2; ++h) {
+            tma_load_3d_pair(sb + h * CHUNK_BYTES, my, bar, f0 + h * 64, row, ti.d);
+            tma_load_3d_pair(sb + A_BYTES + h * CHUNK_BYTES, mx, bar, c0 + h * 64, row, ti.d);
           }
           rg.next();
         }
@@ -639,105 +660,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
   } else if (wid == 1) {
     if (lane == 0 && rank == 0) {
       // ---------------------------------------------------- MMA issuer (leader)
-      uint32_t ne[2] = {0, 0};
+      uint32_t ne[2] = {0, 0}, nr = 0;  // accumulators acquired, side buffers read
       const uint32_t id = idesc(fp16, true, true, 256);
       int b = 0;
       bool ok = true;
       for (int i = 0, t; ok && (t = pair_tile(i, pair, npairs)) < total; ++i) {
-        const WTile ti = decode_wgrad(g, tb.cnt, tb.roff, nf, nc, t);
-        const int nk = (ti.cnt + BK - 1) / BK;
-        if (nk == 0) continue;
+        const WTile &ti = walk.at(t);
+        if (ti.cnt == 0) continue;
+        const int whole = ti.cnt & ~(UK - 1);
         if (!(ok = bar_wait(&acc_empty[b], (ne[b]++ & 1u) ^ 1u, ctl))) break;
         tc_fence_after();
         const uint32_t d0 = tmem + (uint32_t)(b * ACC_COLS);
-        for (int kb = 0; kb < nk; ++kb) {
+        for (int k0 = 0; k0 < whole; k0 += BK) {
           if (!(ok = bar_wait(&rg.full[rg.stage], rg.phase, ctl))) break;
           tc_fence_after();
           uint8_t *sb = rg.base + (size_t)rg.stage * WG_STAGE_BYTES;
           const uint64_t da = smem_desc_mn(sb), db = smem_desc_mn(sb + A_BYTES);
-          const int steps = min(BK / UK, (ti.cnt - kb * BK + UK - 1) / UK);
+          const int steps = min(BK, whole - k0) / UK;
 #pragma unroll
           for (int kk = 0; kk < BK / UK; ++kk)
-            if (kk < steps) mma2(d0, da + kk * MN_STEP, db + kk * MN_STEP, id, (kb > 0 || kk > 0) ? 1u : 0u);
+            if (kk < steps) mma2(d0, da + kk * MN_STEP, db + kk * MN_STEP, id, (k0 > 0 || kk > 0) ? 1u : 0u);
           commit2_both(&rg.empty[rg.stage]);
           rg.next();
         }
         if (!ok) break;
+        if (ti.cnt != whole) {
+          const int j = nr & 1;
+          if (!(ok = bar_wait(&rest_full[j], (nr >> 1) & 1u, ctl))) break;
+          ++nr;
+          tc_fence_after();
+          uint8_t *sb = rest + j * REST_BYTES;
+          mma2(d0, smem_desc_mn(sb, REST_CHUNK), smem_desc_mn(sb + 2 * REST_CHUNK, REST_CHUNK), id, whole ? 1u : 0u);
+          commit2_both(&rest_empty[j]);
+        }
         commit2_both(&acc_full[b]);
         b ^= 1;
       }
     }
   } else if (wid == 2 + WG_EPI_WARPS) {
-    // ------------------------------------ zeroing of rows past a group's end
-    // (Only cut blocks cross the pair here: a release at cluster scope in the
-    // peer's producer, one per K block, held every block to 0.8 us.)
-    uint32_t uses = 0;  // bit s: parity of stage s's next cut block
-    int stage = 0;
-    for (int i = 0, t; (t = pair_tile(i, pair, npairs)) < total; ++i) {
-      const WTile ti = decode_wgrad(g, tb.cnt, tb.roff, nf, nc, t);
-      const int nk = (ti.cnt + BK - 1) / BK;
-      if (nk && (ti.cnt & (UK - 1))) {
-        const int s = (stage + nk - 1) % WG_STAGES;
-        if (!__all_sync(0xffffffffu, bar_wait(&tail[s], (uses >> s) & 1u, ctl))) break;
-        const int v = ti.cnt - (nk - 1) * BK, rows = ((v + UK - 1) & ~(UK - 1)) - v;
-        uint8_t *sb = smem + (size_t)s * WG_STAGE_BYTES + v * 128;
-        for (int j = lane; j < rows * 32; j += 32)  // 4 chunks x rows x 8 16-byte words
-          *reinterpret_cast<uint4 *>(sb + (j / (rows * 8)) * CHUNK_BYTES + (j % (rows * 8)) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_shared();  // the zeros before the tensor core's reads
-        __syncwarp();
-        if (rank != 0) {
-          if (lane == 0) mbar_arrive_remote(map_to(&peer_cut[s], 0));
-        } else {
-          if (!__all_sync(0xffffffffu, bar_wait(&peer_cut[s], (uses >> s) & 1u, ctl))) break;
-          if (lane == 0) mbar_arrive(&rg.full[s]);
+    // --------------------------------------------- the groups' last cnt mod 16
+    // rows: loaded one tile ahead, zeroed past the end, reported to the leader.
+    // Only these steps cross the pair by a release at cluster scope (as part
+    // of every K block it held each to 0.8 us).
+    auto load = [&](int i, uint32_t n) {  // tile i's rows as use n of the side buffers
+      const WTile &ti = walk.at(pair_tile(i, pair, npairs));
+      const int j = n & 1, row = ti.row0 + (ti.cnt & ~(UK - 1));
+      const int f0 = ti.f * 256 + (int)rank * 128, c0 = ti.c * 256 + (int)rank * 128;
+      if (!__all_sync(0xffffffffu, bar_wait(&rest_empty[j], ((n >> 1) & 1u) ^ 1u, ctl))) return false;
+      if (lane == 0) {
+        uint8_t *sb = rest + j * REST_BYTES;
+        mbar_arrive_expect_tx(&rest_in[j], REST_BYTES);
+        for (int h = 0; h < 2; ++h) {
+          tma_load_3d(sb + h * REST_CHUNK, &tm_dy.m[0], &rest_in[j], f0 + h * 64, row, ti.d);
+          tma_load_3d(sb + (2 + h) * REST_CHUNK, &tm_x.m[0], &rest_in[j], c0 + h * 64, row, ti.d);
         }
-        uses ^= 1u << s;
       }
-      stage = (stage + nk) % WG_STAGES;
+      return true;
+    };
+    // the next tile from i on that has such rows
+    auto next = [&](int i) {
+      for (int t; (t = pair_tile(i, pair, npairs)) < total; ++i)
+        if (walk.at(t).cnt & (UK - 1)) return i;
+      return -1;
+    };
+    int i = next(0);
+    uint32_t n = 0;
+    bool ok = i < 0 || load(i, 0);
+    while (ok && i >= 0) {
+      const int r = walk.at(pair_tile(i, pair, npairs)).cnt & (UK - 1), j = n & 1;
+      const uint32_t parity = (n >> 1) & 1u;
+      const int after = next(i + 1);
+      if (after >= 0 && !(ok = load(after, n + 1))) break;
+      if (!(ok = __all_sync(0xffffffffu, bar_wait(&rest_in[j], parity, ctl)))) break;
+      // a row past the end: 8 lanes x 16 bytes in each of the four chunks
+      uint8_t *sb = rest + j * REST_BYTES + (lane >> 3) * REST_CHUNK + (lane & 7) * 16;
+      for (int row = r; row < UK; ++row) *reinterpret_cast<uint4 *>(sb + row * 128) = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_shared();  // the zeros before the tensor core's reads
+      __syncwarp();
+      if (rank != 0) {
+        if (lane == 0) mbar_arrive_remote(map_to(&rest_peer[j], 0));
+      } else {
+        if (!(ok = __all_sync(0xffffffffu, bar_wait(&rest_peer[j], parity, ctl)))) break;
+        if (lane == 0) mbar_arrive(&rest_full[j]);
+      }
+      i = after;
+      ++n;
     }
   } else {
     // -------------------------------------------------------------- epilogue
     const int q = wid & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    constexpr int OB = OT == OUT_FP32 ? 4 : 2, BOX = 128 / OB;  // bytes of an element, columns of a box
+    constexpr int OB = OT == OUT_FP32 ? 4 : 2, BOX = 64 / OB;  // bytes of an element, columns of a box
     const bool aligned = ((reinterpret_cast<uintptr_t>(o.ptr) | (uintptr_t)(o.ld * OB) | (uintptr_t)(o.stride * OB)) & 15u) == 0;
+    const int half = (wid - 2) / 4;
     uint8_t *box = boxes + (size_t)(wid - 2) * WG_OUT_BYTES;
     uint32_t used[2] = {0, 0};
     int b = 0;
     for (int i = 0, t; (t = pair_tile(i, pair, npairs)) < total; ++i) {
-      const WTile ti = decode_wgrad(g, tb.cnt, tb.roff, nf, nc, t);
-      const int fw = ti.f * 256 + (int)rank * 128 + q * 32, f = fw + lane, c0 = ti.c * 256;  // the warp's rows
-      const int cols = min(256, C - c0);
+      const WTile &ti = walk.at(t);
+      const int fw = ti.f * 256 + (int)rank * 128 + q * 32, f = fw + lane, c0 = ti.c * 256 + half * 128;  // the warp's rows, columns
+      const int cols = min(128, C - c0);
       const bool empty = ti.cnt == 0;  // zeros, or nothing to add
       if (empty && add) continue;
       if (!empty && !__all_sync(0xffffffffu, bar_wait(&acc_full[b], used[b]++ & 1u, ctl))) break;
       tc_fence_after();
-      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS);
+      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS + half * 128);
       if (by_tma) {
 #pragma unroll 1
-        for (int c = 0; c < cols; c += BOX) {
-          uint32_t v[BOX];
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t v[32];
           if (empty) {
 #pragma unroll
-            for (int j = 0; j < BOX; ++j) v[j] = 0u;
+            for (int j = 0; j < 32; ++j) v[j] = 0u;
           } else {
-#pragma unroll
-            for (int j = 0; j < BOX; j += 32)
-              tmem_ld32(acc + (uint32_t)(c + j), *reinterpret_cast<uint32_t(*)[32]>(v + j));
+            tmem_ld32(acc + (uint32_t)c, v);
             tmem_ld_wait();
           }
-          if (lane == 0) bulk_wait_read<0>();  // the last copy has left the box
-          __syncwarp();
-          stage_row<OT>(box, lane, v);
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            if (fw < F) {
-              if (OT == OUT_FP32 && add) tma_add_3d(&tm_dw, box, c0 + c, fw, ti.e);
-              else tma_store_3d(&tm_dw, box, c0 + c, fw, ti.e);
+#pragma unroll
+          for (int j = 0; j < 32; j += BOX) {
+            if (lane == 0) bulk_wait_read<0>();  // the last copy has left the box
+            __syncwarp();
+            stage_row<OT>(box, lane, v + j);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              if (fw < F && c + j < cols) {
+                if (OT == OUT_FP32 && add) tma_add_3d(&tm_dw, box, c0 + c + j, fw, ti.e);
+                else tma_store_3d(&tm_dw, box, c0 + c + j, fw, ti.e);
+              }
+              bulk_commit();
             }
-            bulk_commit();
           }
         }
       } else {
@@ -768,10 +820,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// 16-bit (or fp32) elements [d2][d1][d0], strides in elements, box [1][b1][b0], 128-byte
-// swizzle; elements outside the extents read as zeros
+// 16-bit (or fp32) elements [d2][d1][d0], strides in elements, box [1][b1][b0]; elements outside the extents read as zeros
 static bool encode(CUtensorMap *m, uint64_t ptr, uint64_t d0, uint64_t d1, uint64_t d2, int64_t s1, int64_t s2,
-                   uint32_t b0, uint32_t b1, bool fp32 = false) {
+                   uint32_t b0, uint32_t b1, bool fp32 = false,
+                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   typedef CUresult (*Fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                          const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                          CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -785,7 +837,7 @@ static bool encode(CUtensorMap *m, uint64_t ptr, uint64_t d0, uint64_t d1, uint6
   const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {(cuuint64_t)s1 * (fp32 ? 4 : 2), (cuuint64_t)s2 * (fp32 ? 4 : 2)};
   const cuuint32_t box[3] = {b0, b1, 1}, step[3] = {1, 1, 1};
   return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, reinterpret_cast<void *>(ptr), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // rows of a sym_rows, boxes of [box_rows][64]
@@ -837,15 +889,15 @@ cudaError_t launch_grouped_wgrad(const sym_groups &sg, int fp16, const sym_rows 
                                  int64_t dw_group, int64_t dw_ld, int out_type, int add, int num_sms,
                                  cudaStream_t st) {
   using namespace grouped;
-  CUtensorMap md, mx;
+  WMaps md, mx;
   sym_rows ry = dy, rx = x;
   if (x.rows == 0) {  // no rows at all: nothing is loaded; maps over the output keep the encoder content
     ry.ptr = rx.ptr = reinterpret_cast<uint64_t>(dw) & ~uint64_t(15);
     ry.rows = rx.rows = 1;
   }
-  if (!encode_rows(&md, ry, BK) || !encode_rows(&mx, rx, BK)) return cudaErrorInvalidValue;
-  const size_t smem = 1024 + (size_t)WG_STAGES * WG_STAGE_BYTES + WG_EPI_WARPS * WG_OUT_BYTES + CTRL_BYTES +
-                      2 * sizeof(int) * sg.groups;
+  for (int i = 0; i < WG_BOXES; ++i)
+    if (!encode_rows(&md.m[i], ry, 16u << i) || !encode_rows(&mx.m[i], rx, 16u << i)) return cudaErrorInvalidValue;
+  const size_t smem = 1024 + (size_t)WG_STAGES * WG_STAGE_BYTES + 2 * REST_BYTES + WG_EPI_WARPS * WG_OUT_BYTES + CTRL_BYTES;
   const Groups g = groups_of(sg, x);
   const Out o{dw, dw_ld, dw_group};
   // Tensor copies need 16-byte aligned rows.  16-bit sums onto old values are
@@ -853,8 +905,9 @@ cudaError_t launch_grouped_wgrad(const sym_groups &sg, int fp16, const sym_rows 
   const bool fp32 = out_type == OUT_FP32;
   const int64_t per16 = fp32 ? 4 : 8, gs = sg.groups > 1 ? dw_group : dw_ld * dy.cols;
   const int by_tma = reinterpret_cast<uintptr_t>(dw) % 16 == 0 && dw_ld % per16 == 0 && gs % per16 == 0 && (fp32 || !add);
-  CUtensorMap mo = md;
-  if (by_tma && !encode(&mo, reinterpret_cast<uint64_t>(dw), x.cols, dy.cols, sg.groups, dw_ld, gs, fp32 ? 32 : 64, 32, fp32))
+  CUtensorMap mo = md.m[0];
+  if (by_tma && !encode(&mo, reinterpret_cast<uint64_t>(dw), x.cols, dy.cols, sg.groups, dw_ld, gs, fp32 ? 16 : 32, 32, fp32,
+                        CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   auto go = [&](auto kern) {
     return launch(kern, WGRAD_THREADS, smem, num_sms, st, g, o, dy.cols, x.cols, fp16, add, by_tma, md, mx, mo);
