@@ -331,21 +331,44 @@ def _need(ok: bool, where: str, why: str) -> None:
         raise e
 
 
-def _on_device(where: str, *tensors) -> None:
+# These calls are made many times a step on small tensors: the helpers touch
+# each tensor attribute once.
+def _on_device(where: str, *tensors) -> int:
+    """The current device, which every tensor has to be on."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
     for t in tensors:
-        if t is not None:
-            _need(isinstance(t, torch.Tensor) and t.is_cuda and t.device.index == torch.cuda.current_device(),
-                  where, "tensors of the current CUDA device are wanted")
+        if t is not None and not (isinstance(t, torch.Tensor) and t.get_device() == dev):
+            _need(False, where, "tensors of the current CUDA device are wanted")
+    return dev
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, dev: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def _rows(t, where: str, dtype=None) -> SymRows:
     """[rows, cols], or [slots, rows, cols] such as a heap's windows."""
-    _need(t.dim() in (2, 3) and (dtype is None or t.dtype == dtype), where,
-          "rows [R, C] or [slots, R, C] of one type are wanted")
-    slots, slot_stride = (1, 0) if t.dim() == 2 else (t.shape[0], t.stride(0))
-    rows, cols = t.shape[-2:]
-    _need(cols == 1 or t.stride(-1) == 1, where, "the last dimension has to be contiguous")
-    ld = t.stride(-2) if rows > 1 else (cols + 7) // 8 * 8
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        slots, slot_stride = 1, 0
+        rows, cols = shape
+        ld, inner = stride
+    elif len(shape) == 3:
+        slots, rows, cols = shape
+        slot_stride, ld, inner = stride
+    else:
+        _need(False, where, "rows [R, C] or [slots, R, C] are wanted")
+    if dtype is not None and t.dtype != dtype:
+        _need(False, where, "tensors of one type are wanted")
+    if inner != 1 and cols != 1:
+        _need(False, where, "the last dimension has to be contiguous")
+    if rows <= 1:
+        ld = (cols + 7) // 8 * 8
     return SymRows(t.data_ptr(), ld, slot_stride, rows, slots, cols)
 
 
@@ -379,26 +402,26 @@ def moe_grouped_matmul(x, w, cnt, off, out, trans_w: bool = False, status=None, 
     gradient).  x [R, C] or [slots, R, C]; cnt, off: int32 rows and first row
     of each group, [E] or [slots, E / slots]; bf16 or fp16."""
     where = "moe_grouped_matmul"
-    _on_device(where, x, w, cnt, off, out, status)
+    dev = _on_device(where, x, w, cnt, off, out, status)
     rx, ro = _rows(x, where), _rows(out, where, x.dtype)
     g = _groups(cnt, off, rx, status, where)
     _need(w.dtype == x.dtype, where, "x, w and out have one type")
     ws, wl = _matrices(w, g.groups, (rx.cols, ro.cols) if trans_w else (ro.cols, rx.cols), where)
     _check(lib().moe_grouped_matmul(ctypes.byref(g), _DTYPES.get(x.dtype, -1), ctypes.byref(rx), w.data_ptr(), ws, wl,
-                                    SYM_GM_TRANS_W if trans_w else 0, ctypes.byref(ro), _stream(stream)), where)
+                                    SYM_GM_TRANS_W if trans_w else 0, ctypes.byref(ro), _stream_of(stream, dev)), where)
 
 
 def moe_grouped_wgrad(dy, x, cnt, off, dw, accumulate: bool = False, status=None, stream=None) -> None:
     """dw[e] = dy_e^T x_e over the rows of group e (added to dw with
     accumulate); dw [E, F, C] of the inputs' type or float32."""
     where = "moe_grouped_wgrad"
-    _on_device(where, dy, x, cnt, off, dw, status)
+    dev = _on_device(where, dy, x, cnt, off, dw, status)
     ry, rx = _rows(dy, where, x.dtype), _rows(x, where)
     g = _groups(cnt, off, rx, status, where)
     ws, wl = _matrices(dw, g.groups, (ry.cols, rx.cols), where)
     _check(lib().moe_grouped_wgrad(ctypes.byref(g), _DTYPES.get(x.dtype, -1), ctypes.byref(ry), ctypes.byref(rx),
                                    dw.data_ptr(), ws, wl, _DTYPES.get(dw.dtype, -1),
-                                   SYM_GM_ACCUMULATE if accumulate else 0, _stream(stream)), where)
+                                   SYM_GM_ACCUMULATE if accumulate else 0, _stream_of(stream, dev)), where)
 
 
 def _row_words(t, rows: SymRows, dtype, where: str):
@@ -418,25 +441,25 @@ def moe_swiglu_rows(g, u, h, row_w=None, total=None, stream=None) -> None:
     """h = row_w * silu(g) * u; row_w float32 [R] or [slots, R]; total: int32
     rows to do in each slot (all without it)."""
     where = "moe_swiglu_rows"
-    _on_device(where, g, u, h, row_w, total)
+    dev = _on_device(where, g, u, h, row_w, total)
     rg, ru, rh = _rows(g, where), _rows(u, where, g.dtype), _rows(h, where, g.dtype)
     rw, rws = _row_words(row_w, rg, torch.float32, where)
     tt, ts = _totals(total, rg, where)
     _check(lib().moe_swiglu_rows(_DTYPES.get(g.dtype, -1), ctypes.byref(rg), ctypes.byref(ru), rw, rws, tt, ts,
-                                 ctypes.byref(rh), _stream(stream)), where)
+                                 ctypes.byref(rh), _stream_of(stream, dev)), where)
 
 
 def moe_swiglu_rows_bwd(g, u, dh, dg, du, row_w=None, d_row_w=None, total=None, stream=None) -> None:
     """Gradients of moe_swiglu_rows: dg, du and, where given, d_row_w."""
     where = "moe_swiglu_rows_bwd"
-    _on_device(where, g, u, dh, dg, du, row_w, d_row_w, total)
+    dev = _on_device(where, g, u, dh, dg, du, row_w, d_row_w, total)
     rg, ru, rh = _rows(g, where), _rows(u, where, g.dtype), _rows(dh, where, g.dtype)
     r1, r2 = _rows(dg, where, g.dtype), _rows(du, where, g.dtype)
     rw, rws = _row_words(row_w, rg, torch.float32, where)
     dw, dws = _row_words(d_row_w, rg, torch.float32, where)
     tt, ts = _totals(total, rg, where)
     _check(lib().moe_swiglu_rows_bwd(_DTYPES.get(g.dtype, -1), ctypes.byref(rg), ctypes.byref(ru), ctypes.byref(rh),
-                                     rw, rws, tt, ts, ctypes.byref(r1), ctypes.byref(r2), dw, dws, _stream(stream)),
+                                     rw, rws, tt, ts, ctypes.byref(r1), ctypes.byref(r2), dw, dws, _stream_of(stream, dev)),
            where)
 
 
@@ -445,42 +468,43 @@ def moe_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, strea
     counter-based stream (seed, offset).  On y's gradient the same call is the
     backward pass."""
     where = "moe_dropout"
-    _on_device(where, x, y, residual)
+    dev = _on_device(where, x, y, residual)
     rx, ry = _rows(x, where), _rows(y, where, x.dtype)
     rr = None if residual is None else ctypes.byref(_rows(residual, where, x.dtype))
     _check(lib().moe_dropout(_DTYPES.get(x.dtype, -1), ctypes.byref(rx), rr, ctypes.byref(ry), p, seed, offset,
-                             _stream(stream)), where)
+                             _stream_of(stream, dev)), where)
 
 
-def _block(where: str, stream_t, rows: int, cols: int, *, o, w_post, gate, gate_act, scale, p, seed, offset, w_pre,
-           rstd_post, rstd_pre, post_norm, eps, x=None, y=None, h=None) -> SymBlockNorm:
-    dt = stream_t.dtype
+def _plain(t, rows: int, cols: int, dtype, where: str):
+    """(address, row stride) of a [rows, cols] tensor; (0, 0) for none."""
+    if t is None:
+        return 0, 0
+    stride = t.stride()
+    if t.shape != (rows, cols) or t.dtype != dtype or (stride[1] != 1 and cols != 1):
+        _need(False, where, f"[{rows}, {cols}] with contiguous rows, of one type, is wanted")
+    return t.data_ptr(), stride[0] if rows > 1 else (cols + 7) // 8 * 8
 
-    def rows_of(t, n=rows):
-        if t is None:
-            return 0, 0
-        r = _rows(t, where, dt)
-        _need(t.dim() == 2 and r.rows == n and r.cols == cols, where, f"[{n}, {cols}] is wanted")
-        return r.ptr, r.ld
 
-    def vector(t, n, dtype):
-        _need(t is None or (t.dtype == dtype and tuple(t.shape) == (n,) and (n <= 1 or t.stride(0) == 1)), where,
-              f"[{n}] {dtype} is wanted")
-        return 0 if t is None else t.data_ptr()
+def _vector(t, n: int, dtype, where: str) -> int:
+    if t is None:
+        return 0
+    if t.shape != (n,) or t.dtype != dtype or (n > 1 and t.stride()[0] != 1):
+        _need(False, where, f"[{n}] {dtype} is wanted")
+    return t.data_ptr()
 
-    a = SymBlockNorm(rows=rows, cols=cols, dtype=_DTYPES.get(dt, -1), w_post=vector(w_post, cols, dt),
-                     w_pre=vector(w_pre, cols, dt), rstd_post=vector(rstd_post, rows, torch.float32),
-                     rstd_pre=vector(rstd_pre, rows, torch.float32), gate_act=_GATE_ACTS.get(gate_act, -1),
-                     flags=0 if post_norm else SYM_NORM_NO_POST, scale=scale, eps=eps, p=p, seed=seed, offset=offset)
-    a.x, a.ld_x = rows_of(x)
-    a.o, a.ld_o = rows_of(o)
-    a.y, a.ld_y = rows_of(y)
-    a.h, a.ld_h = rows_of(h)
-    if gate is not None:
-        _need(gate.dim() == 2, where, "gate is [gate_rows, cols]")
-        a.gate_rows = gate.shape[0]
-        a.gate, a.ld_gate = rows_of(gate, gate.shape[0])
-    return a
+
+def _block(where: str, dt, rows: int, cols: int, x, o, w_post, gate, gate_act, scale, p, seed, offset, w_pre, y, h,
+           rstd_post, rstd_pre, post_norm, eps) -> SymBlockNorm:
+    xp, xl = _plain(x, rows, cols, dt, where)
+    op, ol = _plain(o, rows, cols, dt, where)
+    yp, yl = _plain(y, rows, cols, dt, where)
+    hp, hl = _plain(h, rows, cols, dt, where)
+    gates = 0 if gate is None else gate.shape[0]
+    gp, gl = _plain(gate, gates, cols, dt, where)
+    return SymBlockNorm(rows, cols, _DTYPES.get(dt, -1), xp, op, _vector(w_post, cols, dt, where), gp,
+                        _vector(w_pre, cols, dt, where), yp, hp, _vector(rstd_post, rows, torch.float32, where),
+                        _vector(rstd_pre, rows, torch.float32, where), xl, ol, gl, yl, hl, gates,
+                        _GATE_ACTS.get(gate_act, -1), 0 if post_norm else SYM_NORM_NO_POST, scale, eps, p, seed, offset)
 
 
 def moe_block_norm(x, o=None, w_post=None, gate=None, gate_act="none", scale: float = 1.0, p: float = 0.0,
@@ -492,12 +516,11 @@ def moe_block_norm(x, o=None, w_post=None, gate=None, gate_act="none", scale: fl
     uses gate row r // (R / G), through gate_act "none", "sigmoid" or "tanh".
     rstd_post, rstd_pre: float32 [R], kept for the backward."""
     where = "moe_block_norm"
-    _on_device(where, x, o, w_post, gate, y, w_pre, h, rstd_post, rstd_pre)
+    dev = _on_device(where, x, o, w_post, gate, y, w_pre, h, rstd_post, rstd_pre)
     _need(x.dim() == 2, where, "x is [rows, cols]")
-    a = _block(where, x, x.shape[0], x.shape[1], o=o, w_post=w_post, gate=gate, gate_act=gate_act, scale=scale, p=p,
-               seed=seed, offset=offset, w_pre=w_pre, rstd_post=rstd_post, rstd_pre=rstd_pre, post_norm=post_norm,
-               eps=eps, x=x, y=y, h=h)
-    _check(lib().moe_block_norm(ctypes.byref(a), _stream(stream)), where)
+    a = _block(where, x.dtype, *x.shape, x, o, w_post, gate, gate_act, scale, p, seed, offset, w_pre, y, h, rstd_post,
+               rstd_pre, post_norm, eps)
+    _check(lib().moe_block_norm(ctypes.byref(a), _stream_of(stream, dev)), where)
 
 
 def moe_block_norm_workspace(rows: int, cols: int, gate_rows: int = 0) -> int:
@@ -515,35 +538,23 @@ def moe_block_norm_bwd(dy=None, dh=None, y=None, o=None, w_post=None, gate=None,
     forward's arguments and its y, rstd_post and rstd_pre.  Every output may
     be left out.  work: a uint8 tensor of moe_block_norm_workspace bytes."""
     where = "moe_block_norm_bwd"
-    _on_device(where, dy, dh, y, o, w_post, gate, w_pre, rstd_post, rstd_pre, dx, do, dw_pre, dw_post, dgate, work)
+    dev = _on_device(where, dy, dh, y, o, w_post, gate, w_pre, rstd_post, rstd_pre, dx, do, dw_pre, dw_post, dgate, work)
     lead = dy if dy is not None else dh
     _need(lead is not None and lead.dim() == 2, where, "dy or dh, [rows, cols], is wanted")
-    rows, cols = lead.shape
-    a = _block(where, lead, rows, cols, o=o, w_post=w_post, gate=gate, gate_act=gate_act, scale=scale, p=p, seed=seed,
-               offset=offset, w_pre=w_pre, rstd_post=rstd_post, rstd_pre=rstd_pre, post_norm=post_norm, eps=0.0, y=y)
-    g = SymBlockNormGrad()
-
-    def put(name, ld, t, n):
-        if t is not None:
-            r = _rows(t, where, lead.dtype)
-            _need(t.dim() == 2 and r.rows == n and r.cols == cols, where, f"{name}: [{n}, {cols}] is wanted")
-            setattr(g, name, r.ptr)
-            setattr(g, ld, r.ld)
-
-    put("dy", "ld_dy", dy, rows)
-    put("dh", "ld_dh", dh, rows)
-    put("dx", "ld_dx", dx, rows)
-    put("d_o", "ld_do", do, rows)
-    put("dgate", "ld_dgate", dgate, a.gate_rows)
-    for name, t in (("dw_pre", dw_pre), ("dw_post", dw_post)):
-        if t is not None:
-            _need(t.dtype == lead.dtype and tuple(t.shape) == (cols,) and (cols == 1 or t.stride(0) == 1), where,
-                  f"{name}: [{cols}] of the rows' type is wanted")
-            setattr(g, name, t.data_ptr())
+    (rows, cols), dt = lead.shape, lead.dtype
+    a = _block(where, dt, rows, cols, None, o, w_post, gate, gate_act, scale, p, seed, offset, w_pre, y, None,
+               rstd_post, rstd_pre, post_norm, 0.0)
+    dyp, dyl = _plain(dy, rows, cols, dt, where)
+    dhp, dhl = _plain(dh, rows, cols, dt, where)
+    dxp, dxl = _plain(dx, rows, cols, dt, where)
+    dop, dol = _plain(do, rows, cols, dt, where)
+    dgp, dgl = _plain(dgate, a.gate_rows, cols, dt, where)
+    g = SymBlockNormGrad(dyp, dhp, dxp, dop, _vector(dw_pre, cols, dt, where), _vector(dw_post, cols, dt, where), dgp,
+                         dyl, dhl, dxl, dol, dgl)
     if work is not None:
         _need(work.is_contiguous(), where, "work is contiguous")
         g.work, g.work_bytes = work.data_ptr(), work.numel() * work.element_size()
-    _check(lib().moe_block_norm_bwd(ctypes.byref(a), ctypes.byref(g), _stream(stream)), where)
+    _check(lib().moe_block_norm_bwd(ctypes.byref(a), ctypes.byref(g), _stream_of(stream, dev)), where)
 
 
 # ------------------------------------------------------------------ heap owner
