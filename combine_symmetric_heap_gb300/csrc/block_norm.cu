@@ -35,10 +35,12 @@ struct Fwd {
   float *rstd_post, *rstd_pre;
   int64_t ldx, ldo, ldy, ldh, ldg;  // elements
   int64_t rows, per_gate;           // rows that share a gate row
-  int cols, act, post_norm;
+  int gates, cols, act, post_norm;
   float scale, eps;
   int drop;
   Random rnd;
+  int split;  // work items, as in Bwd
+  int64_t per_item;
 };
 
 struct Bwd {
@@ -414,12 +416,413 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
     });
 }
 
+// ---------------------------------------------------------------------------
+// Staged kernels: rows in 16-byte vectors, at most 8192 columns.  A block walks
+// work items (runs of rows that share a gate row) with 8 or 16 columns a
+// thread; a thread copies its own vectors of the next rows into its own shared
+// memory (cp.async, a few rows deep), so no barrier guards the copies.  What a
+// column needs for every row stays with its thread for the item's rows: the
+// activated gate in registers, the weights in shared memory.
+// ---------------------------------------------------------------------------
+constexpr int STAGED_COLS = 8192;
+constexpr int STAGED_SMEM = 220 * 1024;
+// A gate row shared by this few rows is copied along with each of them.
+constexpr int GATE_WITH_ROWS = 4;
+
+// A block's rows in the order of its work items
+struct Walk {
+  int64_t per_gate, per_item, row, end;
+  int item, items, split, step;
+  __device__ Walk(int64_t per_gate_, int64_t per_item_, int gates, int split_)
+      : per_gate(per_gate_), per_item(per_item_), item(blockIdx.x), items(gates * split_), split(split_),
+        step(gridDim.x) {
+    open();
+  }
+  __device__ void open() {  // the item's rows; items without rows are passed over
+    for (; item < items; item += step) {
+      const int g = item / split;
+      const int64_t first = g * per_gate;
+      row = first + (item - g * split) * per_item;
+      end = min(row + per_item, first + per_gate);
+      if (row < end) return;
+    }
+  }
+  __device__ bool live() const { return item < items; }
+  __device__ void next() {
+    if (++row < end) return;
+    item += step;
+    open();
+  }
+};
+
+// A thread's share of the row buffers: `ahead` rows of `arrays` x NV vectors
+template <int NV>
+struct Stage {
+  uint4 *mine;
+  int threads, arrays, ahead;
+  int turn = 0;
+  __device__ __forceinline__ uint4 *at(int a, int j) const { return mine + ((turn * arrays + a) * NV + j) * threads; }
+  __device__ __forceinline__ void next() { turn = turn + 1 == ahead ? 0 : turn + 1; }
+  // the oldest row in flight has landed
+  __device__ __forceinline__ void wait() const {
+    if (ahead == 3) cp_async_wait<2>();
+    else if (ahead == 2) cp_async_wait<1>();
+    else cp_async_wait<0>();
+  }
+};
+
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512) block_norm_staged_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float buf[2 * 32];
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  // x, o and, where it changes from row to row, the gate; then w_pre
+  Stage<NV> st{reinterpret_cast<uint4 *>(smem) + threadIdx.x, (int)blockDim.x, 2 + gate_with_rows, ahead_rows};
+  uint4 *wp = reinterpret_cast<uint4 *>(smem) + (size_t)ahead_rows * (2 + gate_with_rows) * NV * blockDim.x + threadIdx.x;
+  const float inv = 1.f / p.cols;
+  const T *w_post = reinterpret_cast<const T *>(p.w_post), *w_pre = reinterpret_cast<const T *>(p.w_pre);
+  auto col = [&](int j) { return ((int)threadIdx.x + j * (int)blockDim.x) * V; };
+  Walk ahead(p.per_gate, p.per_item, p.gates, p.split), now = ahead;
+  auto fetch = [&]() {  // the next row, into the slot just read
+    if (ahead.live()) {
+      const int64_t r = ahead.row;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (col(j) < p.cols) {
+          cp_async16(st.at(0, j), reinterpret_cast<const T *>(p.x) + r * p.ldx + col(j));
+          if (p.o) cp_async16(st.at(1, j), reinterpret_cast<const T *>(p.o) + r * p.ldo + col(j));
+          if (gate_with_rows)
+            cp_async16(st.at(2, j),
+                       reinterpret_cast<const T *>(p.gate) + (ahead.item / p.split) * p.ldg + col(j));
+        }
+      ahead.next();
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < ahead_rows; ++i, st.next()) fetch();
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (w_pre && col(j) < p.cols) wp[j * blockDim.x] = *reinterpret_cast<const uint4 *>(w_pre + col(j));
+  float factor[NV][V];  // scale * act(gate) * w_post
+  auto make_factor = [&](int j, const uint4 &gate) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) factor[j][i] = p.scale;
+    if (p.gate) {
+      float g[V];
+      unpack<T, V>(gate, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) factor[j][i] *= activate(p.act, g[i]);
+    }
+    if (w_post) {
+      float w[V];
+      load<T, V>(w_post + col(j), w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) factor[j][i] *= w[i];
+    }
+  };
+  int half = 0, item = -1;
+  for (; now.live(); now.next()) {
+    const int64_t r = now.row;
+    if (now.item != item && !gate_with_rows) {
+      item = now.item;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (p.o && col(j) < p.cols) {
+          uint4 g = make_uint4(0, 0, 0, 0);
+          if (p.gate)
+            g = *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.gate) + (item / p.split) * p.ldg + col(j));
+          make_factor(j, g);
+        }
+    }
+    st.wait();
+    uint4 xq[NV], oq[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (col(j) < p.cols) {
+        xq[j] = *st.at(0, j);
+        if (p.o) oq[j] = *st.at(1, j);
+        if (gate_with_rows) make_factor(j, *st.at(2, j));
+      }
+    fetch();
+    st.next();
+
+    float rstd_o = 1.f;
+    if (p.o && p.post_norm) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (col(j) < p.cols) {
+          float ov[V];
+          unpack<T, V>(oq[j], ov);
+#pragma unroll
+          for (int i = 0; i < V; ++i) s[0] += ov[i] * ov[i];
+        }
+      group_sums<1>(s, buf, warp, warps, half);
+      rstd_o = rsqrtf(s[0] * inv + p.eps);
+      if (threadIdx.x == 0 && p.rstd_post) p.rstd_post[r] = rstd_o;
+    }
+    float y[NV][V], s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (col(j) < p.cols) {
+        unpack<T, V>(xq[j], y[j]);
+        if (p.o) {
+          float ov[V];
+          unpack<T, V>(oq[j], ov);
+#pragma unroll
+          for (int i = 0; i < V; ++i) ov[i] *= rstd_o * factor[j][i];
+          if (p.drop) {
+            float k[V];
+            keep_factors<V>(p.rnd, (uint64_t)r * p.cols + col(j), k);
+#pragma unroll
+            for (int i = 0; i < V; ++i) ov[i] = k[i] != 0.f ? ov[i] * k[i] : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) y[j][i] += ov[i];
+          store<T, V>(reinterpret_cast<T *>(p.y) + r * p.ldy + col(j), y[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[0] += y[j][i] * y[j][i];
+      }
+    if (!p.h && !p.rstd_pre) continue;
+    group_sums<1>(s, buf, warp, warps, half);
+    const float rstd_y = rsqrtf(s[0] * inv + p.eps);
+    if (threadIdx.x == 0 && p.rstd_pre) p.rstd_pre[r] = rstd_y;
+    if (!p.h) continue;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (col(j) < p.cols) {
+        float w[V];
+        if (w_pre) unpack<T, V>(wp[j * blockDim.x], w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[j][i] *= w_pre ? rstd_y * w[i] : rstd_y;
+        store<T, V>(reinterpret_cast<T *>(p.h) + r * p.ldh + col(j), y[j]);
+      }
+  }
+}
+
+// Backward.  Per column the block keeps two sums: of dh yn (dw_pre), and over
+// an item's rows S = sum drop dx on, from which both dw_post = sum over gates
+// of scale act S and dgate = scale act' w_post S follow.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512) block_norm_bwd_staged_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float buf[2 * 32 * 3];
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  // dy, dh, y, o and, where it changes from row to row, the gate; then w_pre,
+  // then this thread's columns of dw_post, summed over the items
+  Stage<NV> st{reinterpret_cast<uint4 *>(smem) + threadIdx.x, (int)blockDim.x, 4 + gate_with_rows, ahead_rows};
+  uint4 *wp = reinterpret_cast<uint4 *>(smem) + (size_t)ahead_rows * (4 + gate_with_rows) * NV * blockDim.x + threadIdx.x;
+  float *post = reinterpret_cast<float *>(reinterpret_cast<uint4 *>(smem) +
+                                          ((size_t)ahead_rows * (4 + gate_with_rows) + 1) * NV * blockDim.x) + threadIdx.x;
+  const float inv = 1.f / p.cols;
+  const T *w_post = reinterpret_cast<const T *>(p.w_post), *w_pre = reinterpret_cast<const T *>(p.w_pre);
+  float *ws_pre = p.ws + (int64_t)blockIdx.x * p.cols;
+  float *ws_post = p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.cols;
+  float *ws_gate = p.ws + 2 * (int64_t)gridDim.x * p.cols;
+  auto col = [&](int j) { return ((int)threadIdx.x + j * (int)blockDim.x) * V; };
+  Walk ahead(p.per_gate, p.per_item, p.gates, p.split), now = ahead;
+  auto fetch = [&]() {  // the next row, into the slot that is free
+    if (ahead.live()) {
+      const int64_t r = ahead.row;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (col(j) < p.cols) {
+          if (p.dy) cp_async16(st.at(0, j), reinterpret_cast<const T *>(p.dy) + r * p.ld_dy + col(j));
+          if (p.dh) {
+            cp_async16(st.at(1, j), reinterpret_cast<const T *>(p.dh) + r * p.ld_dh + col(j));
+            cp_async16(st.at(2, j), reinterpret_cast<const T *>(p.y) + r * p.ldy + col(j));
+          }
+          if (p.o) cp_async16(st.at(3, j), reinterpret_cast<const T *>(p.o) + r * p.ldo + col(j));
+          if (gate_with_rows)
+            cp_async16(st.at(4, j),
+                       reinterpret_cast<const T *>(p.gate) + (ahead.item / p.split) * p.ldg + col(j));
+        }
+      ahead.next();
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < ahead_rows; ++i, st.next()) fetch();
+  float a_pre[NV][V], a_s[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (w_pre && col(j) < p.cols) wp[j * blockDim.x] = *reinterpret_cast<const uint4 *>(w_pre + col(j));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      a_pre[j][i] = a_s[j][i] = 0.f;
+      post[(j * V + i) * blockDim.x] = 0.f;
+    }
+  }
+  float factor[NV][V];  // scale * act(gate) * w_post
+  auto make_factor = [&](int j, const uint4 &gate) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) factor[j][i] = p.scale;
+    if (p.gate) {
+      float g[V];
+      unpack<T, V>(gate, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) factor[j][i] *= activate(p.act, g[i]);
+    }
+    if (w_post) {
+      float w[V];
+      load<T, V>(w_post + col(j), w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) factor[j][i] *= w[i];
+    }
+  };
+  auto gate_of = [&](int item, int j) {
+    return p.gate ? *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.gate) + (item / p.split) * p.ldg + col(j))
+                  : make_uint4(0, 0, 0, 0);
+  };
+  // an item's S goes to dw_post's sums and to the gate's gradient (directly
+  // where the item is all of the gate row's rows)
+  auto flush = [&](int item) {
+    if (!p.o || item < 0) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (col(j) < p.cols) {
+        float g[V], w[V], d[V];
+        unpack<T, V>(gate_of(item, j), g);
+        if (w_post) load<T, V>(w_post + col(j), w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float s = p.scale * a_s[j][i];
+          post[(j * V + i) * blockDim.x] += p.gate ? activate(p.act, g[i]) * s : s;
+          d[i] = w_post ? s * w[i] : s;
+          a_s[j][i] = 0.f;
+        }
+        if (!p.dgate) continue;
+        if (p.split == 1) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) d[i] *= slope(p.act, g[i]);
+          store<T, V>(reinterpret_cast<T *>(p.dgate) + item * p.ld_dg + col(j), d);
+        } else {
+          float *to = ws_gate + (int64_t)item * p.cols + col(j);
+#pragma unroll
+          for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(to + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+        }
+      }
+  };
+  int half = 0, item = -1;
+  for (; now.live(); now.next()) {
+    const int64_t r = now.row;
+    const float ry = p.dh ? p.rstd_pre[r] : 0.f;
+    const float ro = p.o && p.post_norm ? p.rstd_post[r] : 1.f;
+    if (now.item != item) {
+      flush(item);
+      item = now.item;
+      if (p.o && !gate_with_rows)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (col(j) < p.cols) make_factor(j, gate_of(item, j));
+    }
+    st.wait();
+    if (p.o && gate_with_rows)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (col(j) < p.cols) make_factor(j, *st.at(4, j));
+
+    // yn, dx without its mean term, and q = scale drop act w_post on
+    uint32_t kept[NV];
+    auto front = [&](int j, float(&yn)[V], float(&g0)[V], float(&hv)[V], float &s0) {
+      float w[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) yn[i] = g0[i] = hv[i] = 0.f;
+      if (p.dy) unpack<T, V>(*st.at(0, j), g0);
+      if (!p.dh) return;
+      unpack<T, V>(*st.at(1, j), hv);
+      unpack<T, V>(*st.at(2, j), yn);
+      if (w_pre) unpack<T, V>(wp[j * blockDim.x], w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        yn[i] *= ry;
+        const float t = w_pre ? hv[i] * w[i] : hv[i];
+        g0[i] += ry * t;
+        s0 += t * yn[i];
+      }
+    };
+    float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (col(j) < p.cols) {
+        float yn[V], g0[V], hv[V], ov[V];
+        front(j, yn, g0, hv, s[0]);
+        if (p.o) {
+          kept[j] = ~0u;
+          if (p.drop) {
+            float k[V];
+            keep_factors<V>(p.rnd, (uint64_t)r * p.cols + col(j), k);
+            kept[j] = 0u;
+#pragma unroll
+            for (int i = 0; i < V; ++i) kept[j] |= k[i] != 0.f ? 1u << i : 0u;
+          }
+          if (p.post_norm) {
+            unpack<T, V>(*st.at(3, j), ov);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float q = (kept[j] >> i) & 1u ? factor[j][i] * ov[i] : 0.f;
+              s[1] += g0[i] * q;
+              s[2] += yn[i] * q;
+            }
+          }
+        }
+      }
+    group_sums<3>(s, buf, warp, warps, half);
+    const float m1 = ry * s[0] * inv;  // dx = g0 - yn * m1
+    const float ks = p.drop ? p.rnd.keep_scale : 1.f;
+    const float m2 = p.post_norm ? ks * ro * (s[1] - m1 * s[2]) * inv : 0.f;  // mean(dn w_post on)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (col(j) < p.cols) {
+        float yn[V], g0[V], hv[V], unused = 0.f;
+        front(j, yn, g0, hv, unused);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          a_pre[j][i] += hv[i] * yn[i];
+          g0[i] -= yn[i] * m1;  // dx
+        }
+        if (p.dx) store<T, V>(reinterpret_cast<T *>(p.dx) + r * p.ld_dx + col(j), g0);
+        if (p.o) {
+          float ov[V];
+          unpack<T, V>(*st.at(3, j), ov);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float on = ov[i] * ro;
+            // a dropped element passes nothing on, whatever its values
+            const float d = (kept[j] >> i) & 1u ? g0[i] * ks : 0.f;
+            a_s[j][i] += d * on;
+            ov[i] = ro * (d * factor[j][i] - on * m2);
+          }
+          if (p.dout) store<T, V>(reinterpret_cast<T *>(p.dout) + r * p.ld_do + col(j), ov);
+        }
+      }
+    fetch();
+    st.next();
+  }
+  flush(item);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (col(j) < p.cols) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        if (p.dw_pre)
+          *reinterpret_cast<float4 *>(ws_pre + col(j) + i) =
+              make_float4(a_pre[j][i], a_pre[j][i + 1], a_pre[j][i + 2], a_pre[j][i + 3]);
+        if (p.dw_post)
+          *reinterpret_cast<float4 *>(ws_post + col(j) + i) =
+              make_float4(post[(j * V + i) * blockDim.x], post[(j * V + i + 1) * blockDim.x],
+                          post[(j * V + i + 2) * blockDim.x], post[(j * V + i + 3) * blockDim.x]);
+      }
+    }
+}
+
 // Column sums of the partials: y 0 dw_pre, 1 dw_post, 2 + g the gate rows.
 // A block adds 32 columns: warp w takes partials w, w + 8, ..., then the eight
 // sums are added in order.
 template <typename T>
 __global__ void __launch_bounds__(256) sum_partials_kernel(const Bwd p, int blocks) {
   __shared__ float part[8][33];
+  pdl_wait();  // the partials
   const int which = blockIdx.y;
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x / 32;
   const bool is_gate = which >= 2;
@@ -457,62 +860,112 @@ static int threads_of(int cols, int V, int nv, int most) {
   return t <= most ? t : 0;
 }
 
-template <typename T, int V, int NV>
-static void run_fwd(const Fwd &p, int tpr, int num_sms, cudaStream_t st) {
-  const int rpb = std::max(1, 128 / tpr);
-  const int64_t blocks = std::min<int64_t>((p.rows + rpb - 1) / rpb, (int64_t)num_sms * 64);
-  block_norm_kernel<T, V, NV><<<(unsigned)blocks, dim3(tpr, rpb), rpb * 64 * sizeof(float), st>>>(p);
+// Resident blocks of a staged kernel with `resident` threads an SM
+static int64_t staged_blocks(int64_t rows, int threads, int resident, int num_sms) {
+  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * std::max(1, resident / threads)));
 }
-// NV vectors a thread: two where they fit 512 threads, more for wider rows
-template <typename T, int V>
-static void fwd(const Fwd &p, int num_sms, cudaStream_t st) {
-  constexpr int N = V == 1 ? 8 : 2;
-  if (const int t = threads_of(p.cols, V, N / 2, 256)) return run_fwd<T, V, N / 2>(p, t, num_sms, st);
-  if (const int t = threads_of(p.cols, V, N, 1024)) return run_fwd<T, V, N>(p, t, num_sms, st);
-  run_fwd<T, V, 0>(p, 1024, num_sms, st);
-}
-
-static int bwd_threads(int cols, int V, int *nv) {
-  const int n = V == 1 ? 8 : V == 4 ? 4 : 2;
-  if (const int t = threads_of(cols, V, n, 512)) {
-    *nv = n;
-    return t;
-  }
-  *nv = 0;
-  return 512;
-}
-// blocks that share the rows: about two thousand threads an SM
-static int64_t bwd_blocks(int64_t rows, int threads, int num_sms) {
-  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * std::max(1, 1024 / threads)));
+// Rows to copy ahead: up to three, as many as leave room for `blocks` blocks an SM
+static int ahead_of(size_t arrays, size_t fixed, size_t vectors, int blocks) {
+  const size_t room = STAGED_SMEM / std::max(1, blocks) / vectors;
+  return room < fixed + 2 * arrays ? 1 : room < fixed + 3 * arrays ? 2 : 3;
 }
 // Split of a gate row's rows so that all items together give every block one
-static int64_t bwd_split(int64_t gates, int64_t per_gate, int64_t blocks) {
+static int64_t split_of(int64_t gates, int64_t per_gate, int64_t blocks) {
   if (gates >= blocks) return 1;
   return std::max<int64_t>(1, std::min<int64_t>(per_gate, blocks / gates));
 }
+// Columns of a thread: 8 in rows of up to 2048, else 16 (what a thread keeps
+// beside its columns -- addresses, the generator's words -- is spent on twice
+// as many)
+static int staged_cols(int cols) { return cols <= 2048 ? 8 : 16; }
 
 template <typename T, int V, int NV>
-static cudaError_t run_bwd(Bwd p, int threads, int num_sms, cudaStream_t st) {
-  const int64_t most = bwd_blocks(p.rows, threads, num_sms);
-  p.split = (int)bwd_split(p.gates, p.per_gate, most);
-  p.per_item = (p.per_gate + p.split - 1) / p.split;
-  const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split);
-  block_norm_bwd_kernel<T, V, NV><<<blocks, threads, 0, st>>>(p);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  const bool gates = p.dgate && p.split > 1;
-  if (p.dw_pre || p.dw_post || gates) {
-    sum_partials_kernel<T><<<dim3((p.cols + 31) / 32, 2 + (gates ? p.gates : 0)), 256, 0, st>>>(p, blocks);
-    err = cudaGetLastError();
-  }
-  return err;
+static cudaError_t run_fwd(const Fwd &p, int tpr, int num_sms, cudaStream_t st) {
+  const int rpb = std::max(1, 128 / tpr);
+  const int64_t blocks = std::min<int64_t>((p.rows + rpb - 1) / rpb, (int64_t)num_sms * 64);
+  block_norm_kernel<T, V, NV><<<(unsigned)blocks, dim3(tpr, rpb), rpb * 64 * sizeof(float), st>>>(p);
+  return cudaGetLastError();
 }
 template <typename T, int V>
-static cudaError_t bwd(const Bwd &p, int num_sms, cudaStream_t st) {
-  int nv;
-  const int t = bwd_threads(p.cols, V, &nv);
-  constexpr int N = V == 1 ? 8 : V == 4 ? 4 : 2;
-  return nv ? run_bwd<T, V, N>(p, t, num_sms, st) : run_bwd<T, V, 0>(p, t, num_sms, st);
+static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
+  if constexpr (V > 1) {
+    if (p.cols <= STAGED_COLS) {
+      const int nv = staged_cols(p.cols) / V;
+      const int threads = threads_of(p.cols, V, nv, 512);
+      const int64_t most = staged_blocks(p.rows, threads, 512, num_sms);
+      p.split = (int)split_of(p.gates, p.per_gate, most);
+      p.per_item = (p.per_gate + p.split - 1) / p.split;
+      const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split);
+      const int with_rows = p.gate && p.per_gate <= GATE_WITH_ROWS;
+      const size_t vectors = (size_t)nv * threads * 16;  // a row's of one array
+      const int ahead = ahead_of(2 + with_rows, 1, vectors, 512 / threads);
+      const size_t smem = ((size_t)ahead * (2 + with_rows) + 1) * vectors;
+      auto kern = nv * V == 8 ? block_norm_staged_kernel<T, V, 8 / V> : block_norm_staged_kernel<T, V, 16 / V>;
+      const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (err != cudaSuccess) return err;
+      kern<<<blocks, threads, smem, st>>>(p, with_rows, ahead);
+      return cudaGetLastError();
+    }
+    if (const int t = threads_of(p.cols, V, 2, 1024)) return run_fwd<T, V, 2>(p, t, num_sms, st);
+  } else {
+    // single elements: 4 or 8 a thread
+    if (const int t = threads_of(p.cols, 1, 4, 256)) return run_fwd<T, 1, 4>(p, t, num_sms, st);
+    if (const int t = threads_of(p.cols, 1, 8, 1024)) return run_fwd<T, 1, 8>(p, t, num_sms, st);
+  }
+  return run_fwd<T, V, 0>(p, 1024, num_sms, st);
+}
+
+// The backward's launch: threads and blocks for rows in vectors of V
+struct BwdPlan {
+  bool staged;
+  int threads, nv;  // nv: registers' vectors of the plain kernel (0: none)
+  int64_t blocks;
+};
+static BwdPlan plan_bwd(int64_t rows, int cols, int V, int num_sms) {
+  if (V > 1 && cols <= STAGED_COLS) {
+    const int nv = staged_cols(cols) / V, t = threads_of(cols, V, nv, 512);
+    return BwdPlan{true, t, nv, staged_blocks(rows, t, 512, num_sms)};
+  }
+  const int n = V == 1 ? 8 : 0;
+  const int t = n ? threads_of(cols, V, n, 512) : 0;
+  const int threads = t ? t : 512;
+  return BwdPlan{false, threads, t ? n : 0,
+                 std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * std::max(1, 1024 / threads)))};
+}
+
+template <typename T, int V>
+static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
+  const BwdPlan plan = plan_bwd(p.rows, p.cols, V, num_sms);
+  p.split = (int)split_of(p.gates, p.per_gate, plan.blocks);
+  p.per_item = (p.per_gate + p.split - 1) / p.split;
+  const int blocks = (int)std::min<int64_t>(plan.blocks, (int64_t)p.gates * p.split);
+  cudaError_t err = cudaSuccess;
+  if constexpr (V > 1) {
+    if (plan.staged) {
+      const int with_rows = p.gate && p.per_gate <= GATE_WITH_ROWS;
+      const size_t vectors = (size_t)plan.nv * plan.threads * 16;
+      const size_t sums = V * sizeof(float) / 16;  // dw_post's sums, in vectors
+      const int ahead = ahead_of(4 + with_rows, 1 + sums, vectors, 512 / plan.threads);
+      const size_t smem = ((size_t)ahead * (4 + with_rows) + 1 + sums) * vectors;
+      auto kern = plan.nv * V == 8 ? block_norm_bwd_staged_kernel<T, V, 8 / V>
+                                   : block_norm_bwd_staged_kernel<T, V, 16 / V>;
+      err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (err != cudaSuccess) return err;
+      kern<<<blocks, plan.threads, smem, st>>>(p, with_rows, ahead);
+    } else {
+      block_norm_bwd_kernel<T, V, 0><<<blocks, plan.threads, 0, st>>>(p);
+    }
+  } else {
+    if (plan.nv) block_norm_bwd_kernel<T, 1, 8><<<blocks, plan.threads, 0, st>>>(p);
+    else block_norm_bwd_kernel<T, 1, 0><<<blocks, plan.threads, 0, st>>>(p);
+  }
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  const bool gates = p.dgate && p.split > 1;
+  if (p.dw_pre || p.dw_post || gates)
+    err = launch_pdl(sum_partials_kernel<T>, dim3((p.cols + 31) / 32, 2 + (gates ? p.gates : 0)), dim3(256), 0, st, p,
+                     blocks);
+  return err;
 }
 
 // 16-byte vectors where every row of every tensor starts on their boundary
@@ -531,13 +984,12 @@ size_t block_norm_workspace(int64_t rows, int cols, int64_t gates, int num_sms) 
   using namespace norm;
   size_t best = 0;
   for (int V : {1, 4, 8}) {
-    int nv;
-    const int64_t blocks = bwd_blocks(rows, bwd_threads(cols, V, &nv), num_sms);
-    const int64_t split = gates ? bwd_split(gates, rows / gates, blocks) : 1;
+    const BwdPlan plan = plan_bwd(rows, cols, V, num_sms);
+    const int64_t split = gates ? split_of(gates, rows / gates, plan.blocks) : 1;
     // gate partials: where several blocks share a gate row, or (rows beyond
     // the register budget) the sums live in memory
-    const int64_t items = gates && (split > 1 || nv == 0) ? gates * split : 0;
-    best = std::max(best, (size_t)(2 * blocks + items) * cols * sizeof(float));
+    const int64_t items = gates && (split > 1 || (!plan.staged && plan.nv == 0)) ? gates * split : 0;
+    best = std::max(best, (size_t)(2 * plan.blocks + items) * cols * sizeof(float));
   }
   return best;
 }
@@ -548,17 +1000,17 @@ cudaError_t launch_block_norm(const sym_block_norm &a, int num_sms, cudaStream_t
   p.x = a.x, p.o = a.o, p.w_post = a.w_post, p.w_pre = a.w_pre, p.gate = a.gate, p.y = a.y, p.h = a.h;
   p.rstd_post = a.rstd_post, p.rstd_pre = a.rstd_pre;
   p.ldx = a.ld_x, p.ldo = a.ld_o, p.ldy = a.ld_y, p.ldh = a.ld_h, p.ldg = a.ld_gate;
-  p.rows = a.rows, p.per_gate = a.gate ? a.rows / a.gate_rows : a.rows;
+  p.rows = a.rows, p.gates = a.gate ? (int)a.gate_rows : 1;
+  p.per_gate = p.rows / p.gates;
   p.cols = a.cols, p.act = a.gate_act, p.post_norm = !(a.flags & SYM_NORM_NO_POST);
   p.scale = a.scale, p.eps = a.eps, p.drop = a.p > 0;
-  p.rnd = Random{a.seed, a.offset, (uint32_t)(a.p * 4294967296.0), (float)(1.0 / (1.0 - a.p))};
+  p.rnd = make_random(a.seed, a.offset, a.p);
   const int64_t es = a.dtype == SYM_FP32 ? 4 : 2;
   const bool vec = vec_ok({p.x, p.o, p.w_post, p.w_pre, p.gate, p.y, p.h},
                           {p.ldx, p.o ? p.ldo : 0, p.y ? p.ldy : 0, p.h ? p.ldh : 0, p.gate ? p.ldg : 0}, p.cols, es);
-  if (a.dtype == SYM_BF16) vec ? fwd<__nv_bfloat16, 8>(p, num_sms, st) : fwd<__nv_bfloat16, 1>(p, num_sms, st);
-  else if (a.dtype == SYM_FP16) vec ? fwd<__half, 8>(p, num_sms, st) : fwd<__half, 1>(p, num_sms, st);
-  else vec ? fwd<float, 4>(p, num_sms, st) : fwd<float, 1>(p, num_sms, st);
-  return cudaGetLastError();
+  if (a.dtype == SYM_BF16) return vec ? fwd<__nv_bfloat16, 8>(p, num_sms, st) : fwd<__nv_bfloat16, 1>(p, num_sms, st);
+  if (a.dtype == SYM_FP16) return vec ? fwd<__half, 8>(p, num_sms, st) : fwd<__half, 1>(p, num_sms, st);
+  return vec ? fwd<float, 4>(p, num_sms, st) : fwd<float, 1>(p, num_sms, st);
 }
 
 cudaError_t launch_block_norm_bwd(const sym_block_norm &a, const sym_block_norm_grad &b, int num_sms,
@@ -575,7 +1027,7 @@ cudaError_t launch_block_norm_bwd(const sym_block_norm &a, const sym_block_norm_
   p.per_gate = p.rows / p.gates;
   p.cols = a.cols, p.act = a.gate_act, p.post_norm = !(a.flags & SYM_NORM_NO_POST);
   p.scale = a.scale, p.drop = a.p > 0;
-  p.rnd = Random{a.seed, a.offset, (uint32_t)(a.p * 4294967296.0), (float)(1.0 / (1.0 - a.p))};
+  p.rnd = make_random(a.seed, a.offset, a.p);
   const int64_t es = a.dtype == SYM_FP32 ? 4 : 2;
   const bool vec = vec_ok({p.dy, p.dh, p.dh ? p.y : nullptr, p.o, p.w_post, p.w_pre, p.gate, p.dx, p.dout, p.dgate},
                           {p.dy ? p.ld_dy : 0, p.dh ? p.ld_dh : 0, p.dh ? p.ldy : 0, p.o ? p.ldo : 0,

@@ -49,7 +49,7 @@ cudaError_t launch_swiglu_rows_bwd(int dtype, const sym_rows &g, const sym_rows 
                                    float *drw, int64_t drw_slot, const int32_t *total, int64_t total_slot,
                                    int num_sms, cudaStream_t st);
 cudaError_t launch_dropout(int dtype, const sym_rows &x, const sym_rows *res, const sym_rows &y, uint64_t seed,
-                           uint64_t offset, uint32_t threshold, float keep_scale, int num_sms, cudaStream_t st);
+                           uint64_t offset, double drop, int num_sms, cudaStream_t st);
 size_t block_norm_workspace(int64_t rows, int cols, int64_t gates, int num_sms);
 cudaError_t launch_block_norm(const sym_block_norm &a, int num_sms, cudaStream_t st);
 cudaError_t launch_block_norm_bwd(const sym_block_norm &a, const sym_block_norm_grad &b, int num_sms,
@@ -456,8 +456,7 @@ int moe_dropout(int dtype, const sym_rows *x, const sym_rows *residual, const sy
   if (x->rows == 0) return SYM_OK;
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return SYM_ECUDA;
-  return from_cuda(launch_dropout(dtype, *x, residual, *y, seed, offset, (uint32_t)(p * 4294967296.0),
-                                  (float)(1.0 / (1.0 - p)), sms, (cudaStream_t)stream));
+  return from_cuda(launch_dropout(dtype, *x, residual, *y, seed, offset, p, sms, (cudaStream_t)stream));
 }
 
 // a tensor of the call: aligned to its type, rows that do not overlap

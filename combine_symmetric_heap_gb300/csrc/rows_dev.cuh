@@ -17,12 +17,21 @@ struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int VEC = 8;
+  static __device__ __forceinline__ float2 get2(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
+  static __device__ __forceinline__ uint32_t put2(float a, float b) { return pack_bf16x2(a, b); }
   static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
 };
 template <>
 struct Elem<__half> {
   static constexpr int VEC = 8;
+  static __device__ __forceinline__ float2 get2(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  }
+  static __device__ __forceinline__ uint32_t put2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
   static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
   static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
 };
@@ -33,24 +42,45 @@ struct Elem<float> {
   static __device__ __forceinline__ float put(float v) { return v; }
 };
 
+// A 16-byte vector of T as floats and back, pairs converted together
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const uint4 &q, float (&f)[V]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = Elem<T>::get2(w[i]);
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ uint4 pack(const float (&f)[V]) {
+  uint32_t w[4];
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = Elem<T>::put2(f[2 * i], f[2 * i + 1]);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 // V consecutive elements as floats: one 16-byte access when V is the vector
 // length, one element when V is 1
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-  T v[V];
-};
-template <typename T, int V>
 __device__ __forceinline__ void load(const T *p, float (&f)[V]) {
-  const Pack<T, V> k = *reinterpret_cast<const Pack<T, V> *>(p);
-#pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = Elem<T>::get(k.v[i]);
+  if constexpr (V == 1) f[0] = Elem<T>::get(*p);
+  else unpack<T, V>(*reinterpret_cast<const uint4 *>(p), f);
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(T *p, const float (&f)[V]) {
-  Pack<T, V> k;
-#pragma unroll
-  for (int i = 0; i < V; ++i) k.v[i] = Elem<T>::put(f[i]);
-  *reinterpret_cast<Pack<T, V> *>(p) = k;
+  if constexpr (V == 1) *p = Elem<T>::put(f[0]);
+  else *reinterpret_cast<uint4 *>(p) = pack<T, V>(f);
 }
 
 // Columns [c, c + V) of a row, of which those outside [0, cols) do not exist
@@ -84,23 +114,33 @@ __device__ __forceinline__ void store_part(T *p, int c, int cols, const float (&
 // (seed mod 2^32, seed >> 32); word j of it belongs to element 4b + j.
 // ---------------------------------------------------------------------------
 struct Random {
-  uint64_t seed, offset;
-  uint32_t threshold;  // an element is kept where its word >= threshold
-  float keep_scale;    // 1 / (1 - p)
+  uint64_t offset;
+  uint32_t key[10][2];  // the rounds' keys
+  uint32_t threshold;   // an element is kept where its word >= threshold
+  float keep_scale;     // 1 / (1 - p)
 };
+inline Random make_random(uint64_t seed, uint64_t offset, double p) {
+  Random r;
+  r.offset = offset;
+  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+  for (int i = 0; i < 10; ++i, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) {
+    r.key[i][0] = k0;
+    r.key[i][1] = k1;
+  }
+  r.threshold = (uint32_t)(p * 4294967296.0);
+  r.keep_scale = (float)(1.0 / (1.0 - p));
+  return r;
+}
 __device__ __forceinline__ uint4 random_block(const Random &r, uint64_t block) {
   uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32);
   uint32_t c2 = (uint32_t)r.offset, c3 = (uint32_t)(r.offset >> 32);
-  uint32_t k0 = (uint32_t)r.seed, k1 = (uint32_t)(r.seed >> 32);
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ r.key[i][0];
     c1 = (uint32_t)b;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ r.key[i][1];
     c3 = (uint32_t)a;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }

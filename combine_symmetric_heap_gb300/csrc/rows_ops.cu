@@ -229,11 +229,11 @@ cudaError_t launch_swiglu_rows_bwd(int dtype, const sym_rows &g, const sym_rows 
 }
 
 cudaError_t launch_dropout(int dtype, const sym_rows &x, const sym_rows *res, const sym_rows &y, uint64_t seed,
-                           uint64_t offset, uint32_t threshold, float keep_scale, int num_sms, cudaStream_t st) {
+                           uint64_t offset, double drop, int num_sms, cudaStream_t st) {
   using namespace rows;
   const int64_t es = elem_size(dtype);
   const bool vec = same_skew({&x, &y, res}, es);
-  const Random rnd{seed, offset, threshold, keep_scale};
+  const Random rnd = make_random(seed, offset, drop);
   RowArgs a = {};
   a.a = view_of(&x, es), a.b = view_of(res, es), a.c = view_of(&y, es);
   a.rows = x.rows, a.slots = x.slots, a.cols = x.cols;
