@@ -29,18 +29,28 @@ using namespace rows;
 
 enum Act : int { ACT_NONE = 0, ACT_SIGMOID = 1, ACT_TANH = 2 };
 
+// A row's address: rows and strides are 32-bit (one multiply-add of 64 bits)
+template <typename T>
+__device__ __forceinline__ const T *at(const void *p, int row, int ld) {
+  return reinterpret_cast<const T *>(p) + (int64_t)row * ld;
+}
+template <typename T>
+__device__ __forceinline__ T *at(void *p, int row, int ld) {
+  return reinterpret_cast<T *>(p) + (int64_t)row * ld;
+}
+
 struct Fwd {
   const void *x, *o, *w_post, *w_pre, *gate;
   void *y, *h;
   float *rstd_post, *rstd_pre;
-  int64_t ldx, ldo, ldy, ldh, ldg;  // elements
-  int64_t rows, per_gate;           // rows that share a gate row
+  int ldx, ldo, ldy, ldh, ldg;  // elements
+  int rows, per_gate;           // per_gate: rows that share a gate row
   int gates, cols, act, post_norm;
   float scale, eps;
   int drop;
   Random rnd;
   int split;  // work items, as in Bwd
-  int64_t per_item;
+  int per_item;
 };
 
 struct Bwd {
@@ -48,15 +58,15 @@ struct Bwd {
   const float *rstd_post, *rstd_pre;
   void *dx, *dout, *dw_pre, *dw_post, *dgate;
   float *ws;  // partial sums
-  int64_t ld_dy, ld_dh, ldy, ldo, ldg, ld_dx, ld_do, ld_dg;
-  int64_t rows, per_gate;
+  int ld_dy, ld_dh, ldy, ldo, ldg, ld_dx, ld_do, ld_dg;
+  int rows, per_gate;
   int gates, cols, act, post_norm;
   float scale;
   int drop;
   Random rnd;
   // work items: `per_item` rows of a gate's rows; items = gates * split
   int split;
-  int64_t per_item;
+  int per_item;
 };
 
 __device__ __forceinline__ float activate(int act, float g) {
@@ -418,30 +428,31 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
 
 // ---------------------------------------------------------------------------
 // Staged kernels: rows in 16-byte vectors, at most 8192 columns.  A block walks
-// work items (runs of rows that share a gate row) with 8 or 16 columns a
-// thread; a thread copies its own vectors of the next rows into its own shared
-// memory (cp.async, a few rows deep), so no barrier guards the copies.  What a
-// column needs for every row stays with its thread for the item's rows: the
-// activated gate in registers, the weights in shared memory.
+// work items (runs of rows that share a gate row) with 8 columns a thread,
+// worked on as two quads so that 64 registers do and 1024 threads an SM hide
+// the generator's and the reductions' latencies (16 columns a thread at 128
+// registers: train 162, gradient 258 us).  A thread copies its own vectors of the
+// next rows into its own shared memory (cp.async, a few rows deep), so no
+// barrier guards the copies.  What a column needs for every row stays with its
+// thread for the item's rows: the activated gate in registers, the weights in
+// shared memory.
 // ---------------------------------------------------------------------------
 constexpr int STAGED_COLS = 8192;
+constexpr int FWD_QUADS = 4, BWD_QUADS = 4;
 constexpr int STAGED_SMEM = 220 * 1024;
 // A gate row shared by this few rows is copied along with each of them.
 constexpr int GATE_WITH_ROWS = 4;
 
 // A block's rows in the order of its work items
 struct Walk {
-  int64_t per_gate, per_item, row, end;
-  int item, items, split, step;
-  __device__ Walk(int64_t per_gate_, int64_t per_item_, int gates, int split_)
-      : per_gate(per_gate_), per_item(per_item_), item(blockIdx.x), items(gates * split_), split(split_),
-        step(gridDim.x) {
+  int per_gate, per_item, row, end, item, items, split;
+  __device__ Walk(int per_gate_, int per_item_, int gates, int split_)
+      : per_gate(per_gate_), per_item(per_item_), item(blockIdx.x), items(gates * split_), split(split_) {
     open();
   }
   __device__ void open() {  // the item's rows; items without rows are passed over
-    for (; item < items; item += step) {
-      const int g = item / split;
-      const int64_t first = g * per_gate;
+    for (; item < items; item += gridDim.x) {
+      const int g = item / split, first = g * per_gate;
       row = first + (item - g * split) * per_item;
       end = min(row + per_item, first + per_gate);
       if (row < end) return;
@@ -450,18 +461,34 @@ struct Walk {
   __device__ bool live() const { return item < items; }
   __device__ void next() {
     if (++row < end) return;
-    item += step;
+    item += gridDim.x;
     open();
   }
 };
 
-// A thread's share of the row buffers: `ahead` rows of `arrays` x NV vectors
-template <int NV>
-struct Stage {
-  uint4 *mine;
-  int threads, arrays, ahead;
-  int turn = 0;
-  __device__ __forceinline__ uint4 *at(int a, int j) const { return mine + ((turn * arrays + a) * NV + j) * threads; }
+// A thread's NQ quads of columns and its share of the row buffers.  16-bit
+// types: quads 2j and 2j + 1 are vector j; fp32: quad k is vector k.  A thread's
+// vectors are a block's width apart.
+template <typename T, int NQ>
+struct Mine {
+  static constexpr int PER = sizeof(T) == 4 ? 1 : 2;  // quads of a vector
+  static constexpr int NV = NQ / PER;
+  int threads, arrays, ahead, turn;
+  char *buf;
+  __device__ Mine(char *smem, int arrays_, int ahead_)
+      : threads(blockDim.x), arrays(arrays_), ahead(ahead_), turn(0), buf(smem + threadIdx.x * 16) {}
+  // first column of vector j and of quad k
+  __device__ __forceinline__ int vector(int j) const {
+    return ((int)threadIdx.x + j * threads) * (16 / (int)sizeof(T));
+  }
+  __device__ __forceinline__ int quad(int k) const { return vector(k / PER) + 4 * (k % PER); }
+  // vector j / quad k of `slot`, one of the 16-byte-per-thread planes
+  __device__ __forceinline__ char *plane(int slot, int j) const { return buf + (size_t)(slot * NV + j) * threads * 16; }
+  __device__ __forceinline__ char *plane_quad(int slot, int k) const {
+    return plane(slot, k / PER) + 8 * (k % PER);
+  }
+  __device__ __forceinline__ char *row_vector(int a, int j) const { return plane(turn * arrays + a, j); }
+  __device__ __forceinline__ char *row_quad(int a, int k) const { return plane_quad(turn * arrays + a, k); }
   __device__ __forceinline__ void next() { turn = turn + 1 == ahead ? 0 : turn + 1; }
   // the oldest row in flight has landed
   __device__ __forceinline__ void wait() const {
@@ -470,133 +497,146 @@ struct Stage {
     else cp_async_wait<0>();
   }
 };
+// Quads' results as whole 16-byte stores
+template <typename T>
+struct Writer {
+  typename Quad<T>::Word first;
+  __device__ __forceinline__ void put(int k, T *row, int col, const float (&f)[4]) {
+    const typename Quad<T>::Word w = Quad<T>::put(f);
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<uint4 *>(row + col) = w;
+    } else {
+      if (k % 2 == 0) first = w;
+      else *reinterpret_cast<uint4 *>(row + col - 4) = make_uint4(first.x, first.y, w.x, w.y);
+    }
+  }
+};
+// scale * act(gate) * w_post of a quad
+template <typename T>
+__device__ __forceinline__ void factor_of(float scale, int act, const void *gate, const T *w_post, float (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = scale;
+  if (gate) {
+    float g[4];
+    Quad<T>::get(gate, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] *= activate(act, g[i]);
+  }
+  if (w_post) {
+    float w[4];
+    Quad<T>::get(w_post, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] *= w[i];
+  }
+}
 
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(512) block_norm_staged_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
-  extern __shared__ __align__(16) uint8_t smem[];
+template <typename T, int NQ>
+__global__ void __launch_bounds__(NQ == 2 ? 1024 : 512) block_norm_staged_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
+  extern __shared__ __align__(16) char smem[];
   __shared__ float buf[2 * 32];
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
   // x, o and, where it changes from row to row, the gate; then w_pre
-  Stage<NV> st{reinterpret_cast<uint4 *>(smem) + threadIdx.x, (int)blockDim.x, 2 + gate_with_rows, ahead_rows};
-  uint4 *wp = reinterpret_cast<uint4 *>(smem) + (size_t)ahead_rows * (2 + gate_with_rows) * NV * blockDim.x + threadIdx.x;
+  using M = Mine<T, NQ>;
+  M my(smem, 2 + gate_with_rows, ahead_rows);
+  const int w_slot = ahead_rows * my.arrays;
   const float inv = 1.f / p.cols;
   const T *w_post = reinterpret_cast<const T *>(p.w_post), *w_pre = reinterpret_cast<const T *>(p.w_pre);
-  auto col = [&](int j) { return ((int)threadIdx.x + j * (int)blockDim.x) * V; };
   Walk ahead(p.per_gate, p.per_item, p.gates, p.split), now = ahead;
-  auto fetch = [&]() {  // the next row, into the slot just read
+  auto fetch = [&]() {  // the next row, into the slot that is free
     if (ahead.live()) {
-      const int64_t r = ahead.row;
+      const int r = ahead.row;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (col(j) < p.cols) {
-          cp_async16(st.at(0, j), reinterpret_cast<const T *>(p.x) + r * p.ldx + col(j));
-          if (p.o) cp_async16(st.at(1, j), reinterpret_cast<const T *>(p.o) + r * p.ldo + col(j));
+      for (int j = 0; j < M::NV; ++j) {
+        const int c = my.vector(j);
+        if (c < p.cols) {
+          cp_async16(my.row_vector(0, j), at<T>(p.x, r, p.ldx) + c);
+          if (p.o) cp_async16(my.row_vector(1, j), at<T>(p.o, r, p.ldo) + c);
           if (gate_with_rows)
-            cp_async16(st.at(2, j),
-                       reinterpret_cast<const T *>(p.gate) + (ahead.item / p.split) * p.ldg + col(j));
+            cp_async16(my.row_vector(2, j), at<T>(p.gate, ahead.item / p.split, p.ldg) + c);
         }
+      }
       ahead.next();
     }
     cp_async_commit();
   };
-  for (int i = 0; i < ahead_rows; ++i, st.next()) fetch();
+  for (int i = 0; i < ahead_rows; ++i, my.next()) fetch();
+  if (w_pre)
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (w_pre && col(j) < p.cols) wp[j * blockDim.x] = *reinterpret_cast<const uint4 *>(w_pre + col(j));
-  float factor[NV][V];  // scale * act(gate) * w_post
-  auto make_factor = [&](int j, const uint4 &gate) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) factor[j][i] = p.scale;
-    if (p.gate) {
-      float g[V];
-      unpack<T, V>(gate, g);
-#pragma unroll
-      for (int i = 0; i < V; ++i) factor[j][i] *= activate(p.act, g[i]);
-    }
-    if (w_post) {
-      float w[V];
-      load<T, V>(w_post + col(j), w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) factor[j][i] *= w[i];
-    }
-  };
+    for (int j = 0; j < M::NV; ++j)
+      if (my.vector(j) < p.cols)
+        *reinterpret_cast<uint4 *>(my.plane(w_slot, j)) = *reinterpret_cast<const uint4 *>(w_pre + my.vector(j));
+  float factor[NQ][4];
   int half = 0, item = -1;
   for (; now.live(); now.next()) {
-    const int64_t r = now.row;
-    if (now.item != item && !gate_with_rows) {
+    const int r = now.row;
+    if (p.o && (now.item != item) && !gate_with_rows) {
       item = now.item;
+      const T *gate = p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (p.o && col(j) < p.cols) {
-          uint4 g = make_uint4(0, 0, 0, 0);
-          if (p.gate)
-            g = *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.gate) + (item / p.split) * p.ldg + col(j));
-          make_factor(j, g);
-        }
-    }
-    st.wait();
-    uint4 xq[NV], oq[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (col(j) < p.cols) {
-        xq[j] = *st.at(0, j);
-        if (p.o) oq[j] = *st.at(1, j);
-        if (gate_with_rows) make_factor(j, *st.at(2, j));
+      for (int k = 0; k < NQ; ++k) {
+        const int c = my.quad(k);
+        if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[k]);
       }
-    fetch();
-    st.next();
-
+    }
+    my.wait();
+    if (p.o && gate_with_rows)
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) {
+        const int c = my.quad(k);
+        if (c < p.cols) factor_of<T>(p.scale, p.act, my.row_quad(2, k), w_post ? w_post + c : nullptr, factor[k]);
+      }
     float rstd_o = 1.f;
     if (p.o && p.post_norm) {
       float s[1] = {0.f};
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (col(j) < p.cols) {
-          float ov[V];
-          unpack<T, V>(oq[j], ov);
+      for (int k = 0; k < NQ; ++k)
+        if (my.quad(k) < p.cols) {
+          float ov[4];
+          Quad<T>::get(my.row_quad(1, k), ov);
 #pragma unroll
-          for (int i = 0; i < V; ++i) s[0] += ov[i] * ov[i];
+          for (int i = 0; i < 4; ++i) s[0] += ov[i] * ov[i];
         }
       group_sums<1>(s, buf, warp, warps, half);
       rstd_o = rsqrtf(s[0] * inv + p.eps);
       if (threadIdx.x == 0 && p.rstd_post) p.rstd_post[r] = rstd_o;
     }
-    float y[NV][V], s[1] = {0.f};
+    float y[NQ][4], s[1] = {0.f};
+    Writer<T> out;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (col(j) < p.cols) {
-        unpack<T, V>(xq[j], y[j]);
+    for (int k = 0; k < NQ; ++k) {
+      const int c = my.quad(k);
+      if (c < p.cols) {
+        Quad<T>::get(my.row_quad(0, k), y[k]);
         if (p.o) {
-          float ov[V];
-          unpack<T, V>(oq[j], ov);
+          float ov[4];
+          Quad<T>::get(my.row_quad(1, k), ov);
+          const float ks = p.drop ? rstd_o * p.rnd.keep_scale : rstd_o;
+          uint32_t word[4] = {~0u, ~0u, ~0u, ~0u};
+          if (p.drop) random_words(p.rnd, ((uint64_t)r * p.cols + c) >> 2, word);
 #pragma unroll
-          for (int i = 0; i < V; ++i) ov[i] *= rstd_o * factor[j][i];
-          if (p.drop) {
-            float k[V];
-            keep_factors<V>(p.rnd, (uint64_t)r * p.cols + col(j), k);
-#pragma unroll
-            for (int i = 0; i < V; ++i) ov[i] = k[i] != 0.f ? ov[i] * k[i] : 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) y[j][i] += ov[i];
-          store<T, V>(reinterpret_cast<T *>(p.y) + r * p.ldy + col(j), y[j]);
+          for (int i = 0; i < 4; ++i)
+            if (word[i] >= p.rnd.threshold) y[k][i] += ov[i] * ks * factor[k][i];
+          out.put(k, at<T>(p.y, r, p.ldy), c, y[k]);
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[0] += y[j][i] * y[j][i];
+        for (int i = 0; i < 4; ++i) s[0] += y[k][i] * y[k][i];
       }
+    }
+    fetch();
+    my.next();
     if (!p.h && !p.rstd_pre) continue;
     group_sums<1>(s, buf, warp, warps, half);
     const float rstd_y = rsqrtf(s[0] * inv + p.eps);
     if (threadIdx.x == 0 && p.rstd_pre) p.rstd_pre[r] = rstd_y;
     if (!p.h) continue;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (col(j) < p.cols) {
-        float w[V];
-        if (w_pre) unpack<T, V>(wp[j * blockDim.x], w);
+    for (int k = 0; k < NQ; ++k)
+      if (my.quad(k) < p.cols) {
+        float w[4] = {1.f, 1.f, 1.f, 1.f};
+        if (w_pre) Quad<T>::get(my.plane_quad(w_slot, k), w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) y[j][i] *= w_pre ? rstd_y * w[i] : rstd_y;
-        store<T, V>(reinterpret_cast<T *>(p.h) + r * p.ldh + col(j), y[j]);
+        for (int i = 0; i < 4; ++i) y[k][i] *= rstd_y * w[i];
+        out.put(k, at<T>(p.h, r, p.ldh), my.quad(k), y[k]);
       }
   }
 }
@@ -604,216 +644,201 @@ __global__ void __launch_bounds__(512) block_norm_staged_kernel(const Fwd p, int
 // Backward.  Per column the block keeps two sums: of dh yn (dw_pre), and over
 // an item's rows S = sum drop dx on, from which both dw_post = sum over gates
 // of scale act S and dgate = scale act' w_post S follow.
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(512) block_norm_bwd_staged_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
-  extern __shared__ __align__(16) uint8_t smem[];
+template <typename T, int NQ>
+__global__ void __launch_bounds__(NQ == 2 ? 1024 : 512) block_norm_bwd_staged_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
+  extern __shared__ __align__(16) char smem[];
   __shared__ float buf[2 * 32 * 3];
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
   // dy, dh, y, o and, where it changes from row to row, the gate; then w_pre,
   // then this thread's columns of dw_post, summed over the items
-  Stage<NV> st{reinterpret_cast<uint4 *>(smem) + threadIdx.x, (int)blockDim.x, 4 + gate_with_rows, ahead_rows};
-  uint4 *wp = reinterpret_cast<uint4 *>(smem) + (size_t)ahead_rows * (4 + gate_with_rows) * NV * blockDim.x + threadIdx.x;
-  float *post = reinterpret_cast<float *>(reinterpret_cast<uint4 *>(smem) +
-                                          ((size_t)ahead_rows * (4 + gate_with_rows) + 1) * NV * blockDim.x) + threadIdx.x;
+  using M = Mine<T, NQ>;
+  M my(smem, 4 + gate_with_rows, ahead_rows);
+  const int w_slot = ahead_rows * my.arrays;
+  float *post = reinterpret_cast<float *>(smem + (size_t)(w_slot + 1) * M::NV * blockDim.x * 16) + threadIdx.x;
   const float inv = 1.f / p.cols;
   const T *w_post = reinterpret_cast<const T *>(p.w_post), *w_pre = reinterpret_cast<const T *>(p.w_pre);
-  float *ws_pre = p.ws + (int64_t)blockIdx.x * p.cols;
-  float *ws_post = p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.cols;
-  float *ws_gate = p.ws + 2 * (int64_t)gridDim.x * p.cols;
-  auto col = [&](int j) { return ((int)threadIdx.x + j * (int)blockDim.x) * V; };
   Walk ahead(p.per_gate, p.per_item, p.gates, p.split), now = ahead;
   auto fetch = [&]() {  // the next row, into the slot that is free
     if (ahead.live()) {
-      const int64_t r = ahead.row;
+      const int r = ahead.row;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (col(j) < p.cols) {
-          if (p.dy) cp_async16(st.at(0, j), reinterpret_cast<const T *>(p.dy) + r * p.ld_dy + col(j));
+      for (int j = 0; j < M::NV; ++j) {
+        const int c = my.vector(j);
+        if (c < p.cols) {
+          if (p.dy) cp_async16(my.row_vector(0, j), at<T>(p.dy, r, p.ld_dy) + c);
           if (p.dh) {
-            cp_async16(st.at(1, j), reinterpret_cast<const T *>(p.dh) + r * p.ld_dh + col(j));
-            cp_async16(st.at(2, j), reinterpret_cast<const T *>(p.y) + r * p.ldy + col(j));
+            cp_async16(my.row_vector(1, j), at<T>(p.dh, r, p.ld_dh) + c);
+            cp_async16(my.row_vector(2, j), at<T>(p.y, r, p.ldy) + c);
           }
-          if (p.o) cp_async16(st.at(3, j), reinterpret_cast<const T *>(p.o) + r * p.ldo + col(j));
+          if (p.o) cp_async16(my.row_vector(3, j), at<T>(p.o, r, p.ldo) + c);
           if (gate_with_rows)
-            cp_async16(st.at(4, j),
-                       reinterpret_cast<const T *>(p.gate) + (ahead.item / p.split) * p.ldg + col(j));
+            cp_async16(my.row_vector(4, j), at<T>(p.gate, ahead.item / p.split, p.ldg) + c);
         }
+      }
       ahead.next();
     }
     cp_async_commit();
   };
-  for (int i = 0; i < ahead_rows; ++i, st.next()) fetch();
-  float a_pre[NV][V], a_s[NV][V];
+  for (int i = 0; i < ahead_rows; ++i, my.next()) fetch();
+  if (w_pre)
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (w_pre && col(j) < p.cols) wp[j * blockDim.x] = *reinterpret_cast<const uint4 *>(w_pre + col(j));
+    for (int j = 0; j < M::NV; ++j)
+      if (my.vector(j) < p.cols)
+        *reinterpret_cast<uint4 *>(my.plane(w_slot, j)) = *reinterpret_cast<const uint4 *>(w_pre + my.vector(j));
+  float factor[NQ][4], a_pre[NQ][4], a_s[NQ][4];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      a_pre[j][i] = a_s[j][i] = 0.f;
-      post[(j * V + i) * blockDim.x] = 0.f;
+  for (int k = 0; k < NQ; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      factor[k][i] = a_pre[k][i] = a_s[k][i] = 0.f;
+      post[(k * 4 + i) * blockDim.x] = 0.f;
     }
-  }
-  float factor[NV][V];  // scale * act(gate) * w_post
-  auto make_factor = [&](int j, const uint4 &gate) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) factor[j][i] = p.scale;
-    if (p.gate) {
-      float g[V];
-      unpack<T, V>(gate, g);
-#pragma unroll
-      for (int i = 0; i < V; ++i) factor[j][i] *= activate(p.act, g[i]);
-    }
-    if (w_post) {
-      float w[V];
-      load<T, V>(w_post + col(j), w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) factor[j][i] *= w[i];
-    }
-  };
-  auto gate_of = [&](int item, int j) {
-    return p.gate ? *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.gate) + (item / p.split) * p.ldg + col(j))
-                  : make_uint4(0, 0, 0, 0);
+  auto gate_row = [&](int item) {
+    return p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
   };
   // an item's S goes to dw_post's sums and to the gate's gradient (directly
   // where the item is all of the gate row's rows)
   auto flush = [&](int item) {
     if (!p.o || item < 0) return;
+    const T *gate = gate_row(item);
+    Writer<T> out;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (col(j) < p.cols) {
-        float g[V], w[V], d[V];
-        unpack<T, V>(gate_of(item, j), g);
-        if (w_post) load<T, V>(w_post + col(j), w);
+    for (int k = 0; k < NQ; ++k) {
+      const int c = my.quad(k);
+      if (c < p.cols) {
+        float g[4], w[4] = {1.f, 1.f, 1.f, 1.f}, d[4];
+        if (gate) Quad<T>::get(gate + c, g);
+        if (w_post) Quad<T>::get(w_post + c, w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float s = p.scale * a_s[j][i];
-          post[(j * V + i) * blockDim.x] += p.gate ? activate(p.act, g[i]) * s : s;
-          d[i] = w_post ? s * w[i] : s;
-          a_s[j][i] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const float s = p.scale * a_s[k][i];
+          post[(k * 4 + i) * blockDim.x] += gate ? activate(p.act, g[i]) * s : s;
+          d[i] = s * w[i];
+          a_s[k][i] = 0.f;
         }
         if (!p.dgate) continue;
         if (p.split == 1) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) d[i] *= slope(p.act, g[i]);
-          store<T, V>(reinterpret_cast<T *>(p.dgate) + item * p.ld_dg + col(j), d);
+          for (int i = 0; i < 4; ++i) d[i] *= slope(p.act, g[i]);
+          out.put(k, at<T>(p.dgate, item, p.ld_dg), c, d);
         } else {
-          float *to = ws_gate + (int64_t)item * p.cols + col(j);
-#pragma unroll
-          for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(to + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+          float *sums = p.ws + 2 * (int64_t)gridDim.x * p.cols + (int64_t)item * p.cols;
+          *reinterpret_cast<float4 *>(sums + c) = make_float4(d[0], d[1], d[2], d[3]);
         }
       }
+    }
+  };
+  // yn, dx without its mean term and dh of a quad; s0 += dh w_pre yn
+  auto front = [&](int k, float ry, float (&yn)[4], float (&g0)[4], float (&hv)[4], float &s0) {
+    float w[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) yn[i] = g0[i] = hv[i] = 0.f;
+    if (p.dy) Quad<T>::get(my.row_quad(0, k), g0);
+    if (!p.dh) return;
+    Quad<T>::get(my.row_quad(1, k), hv);
+    Quad<T>::get(my.row_quad(2, k), yn);
+    if (w_pre) Quad<T>::get(my.plane_quad(w_slot, k), w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      yn[i] *= ry;
+      const float t = hv[i] * w[i];
+      g0[i] += ry * t;
+      s0 += t * yn[i];
+    }
   };
   int half = 0, item = -1;
   for (; now.live(); now.next()) {
-    const int64_t r = now.row;
+    const int r = now.row;
     const float ry = p.dh ? p.rstd_pre[r] : 0.f;
     const float ro = p.o && p.post_norm ? p.rstd_post[r] : 1.f;
     if (now.item != item) {
       flush(item);
       item = now.item;
+      const T *gate = gate_row(item);
       if (p.o && !gate_with_rows)
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (col(j) < p.cols) make_factor(j, gate_of(item, j));
+        for (int k = 0; k < NQ; ++k) {
+          const int c = my.quad(k);
+          if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[k]);
+        }
     }
-    st.wait();
-    if (p.o && gate_with_rows)
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (col(j) < p.cols) make_factor(j, *st.at(4, j));
-
-    // yn, dx without its mean term, and q = scale drop act w_post on
-    uint32_t kept[NV];
-    auto front = [&](int j, float(&yn)[V], float(&g0)[V], float(&hv)[V], float &s0) {
-      float w[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) yn[i] = g0[i] = hv[i] = 0.f;
-      if (p.dy) unpack<T, V>(*st.at(0, j), g0);
-      if (!p.dh) return;
-      unpack<T, V>(*st.at(1, j), hv);
-      unpack<T, V>(*st.at(2, j), yn);
-      if (w_pre) unpack<T, V>(wp[j * blockDim.x], w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        yn[i] *= ry;
-        const float t = w_pre ? hv[i] * w[i] : hv[i];
-        g0[i] += ry * t;
-        s0 += t * yn[i];
-      }
-    };
+    my.wait();
+    uint32_t kept = 0u;  // bit 4k + i: element i of quad k is kept
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (col(j) < p.cols) {
-        float yn[V], g0[V], hv[V], ov[V];
-        front(j, yn, g0, hv, s[0]);
-        if (p.o) {
-          kept[j] = ~0u;
-          if (p.drop) {
-            float k[V];
-            keep_factors<V>(p.rnd, (uint64_t)r * p.cols + col(j), k);
-            kept[j] = 0u;
+    for (int k = 0; k < NQ; ++k) {
+      const int c = my.quad(k);
+      if (c < p.cols) {
+        if (p.o && gate_with_rows)
+          factor_of<T>(p.scale, p.act, my.row_quad(4, k), w_post ? w_post + c : nullptr, factor[k]);
+        uint32_t word[4] = {~0u, ~0u, ~0u, ~0u};
+        if (p.o && p.drop) random_words(p.rnd, ((uint64_t)r * p.cols + c) >> 2, word);
 #pragma unroll
-            for (int i = 0; i < V; ++i) kept[j] |= k[i] != 0.f ? 1u << i : 0u;
-          }
-          if (p.post_norm) {
-            unpack<T, V>(*st.at(3, j), ov);
+        for (int i = 0; i < 4; ++i)
+          if (word[i] >= p.rnd.threshold) kept |= 1u << (4 * k + i);
+        float yn[4], g0[4], hv[4];
+        front(k, ry, yn, g0, hv, s[0]);
+        if (p.o && p.post_norm) {
+          float ov[4];
+          Quad<T>::get(my.row_quad(3, k), ov);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float q = (kept[j] >> i) & 1u ? factor[j][i] * ov[i] : 0.f;
-              s[1] += g0[i] * q;
-              s[2] += yn[i] * q;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float q = word[i] >= p.rnd.threshold ? factor[k][i] * ov[i] : 0.f;
+            s[1] += g0[i] * q;
+            s[2] += yn[i] * q;
           }
         }
       }
+    }
     group_sums<3>(s, buf, warp, warps, half);
     const float m1 = ry * s[0] * inv;  // dx = g0 - yn * m1
     const float ks = p.drop ? p.rnd.keep_scale : 1.f;
     const float m2 = p.post_norm ? ks * ro * (s[1] - m1 * s[2]) * inv : 0.f;  // mean(dn w_post on)
+    Writer<T> out_x, out_o;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (col(j) < p.cols) {
-        float yn[V], g0[V], hv[V], unused = 0.f;
-        front(j, yn, g0, hv, unused);
+    for (int k = 0; k < NQ; ++k) {
+      const int c = my.quad(k);
+      if (c < p.cols) {
+        float yn[4], g0[4], hv[4], unused = 0.f;
+        front(k, ry, yn, g0, hv, unused);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          a_pre[j][i] += hv[i] * yn[i];
+        for (int i = 0; i < 4; ++i) {
+          a_pre[k][i] += hv[i] * yn[i];
           g0[i] -= yn[i] * m1;  // dx
         }
-        if (p.dx) store<T, V>(reinterpret_cast<T *>(p.dx) + r * p.ld_dx + col(j), g0);
+        if (p.dx) out_x.put(k, at<T>(p.dx, r, p.ld_dx), c, g0);
         if (p.o) {
-          float ov[V];
-          unpack<T, V>(*st.at(3, j), ov);
+          float ov[4];
+          Quad<T>::get(my.row_quad(3, k), ov);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
+          for (int i = 0; i < 4; ++i) {
             const float on = ov[i] * ro;
             // a dropped element passes nothing on, whatever its values
-            const float d = (kept[j] >> i) & 1u ? g0[i] * ks : 0.f;
-            a_s[j][i] += d * on;
-            ov[i] = ro * (d * factor[j][i] - on * m2);
+            const float d = (kept >> (4 * k + i)) & 1u ? g0[i] * ks : 0.f;
+            a_s[k][i] += d * on;
+            ov[i] = ro * (d * factor[k][i] - on * m2);
           }
-          if (p.dout) store<T, V>(reinterpret_cast<T *>(p.dout) + r * p.ld_do + col(j), ov);
+          if (p.dout) out_o.put(k, at<T>(p.dout, r, p.ld_do), c, ov);
         }
       }
+    }
     fetch();
-    st.next();
+    my.next();
   }
   flush(item);
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (col(j) < p.cols) {
-#pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        if (p.dw_pre)
-          *reinterpret_cast<float4 *>(ws_pre + col(j) + i) =
-              make_float4(a_pre[j][i], a_pre[j][i + 1], a_pre[j][i + 2], a_pre[j][i + 3]);
-        if (p.dw_post)
-          *reinterpret_cast<float4 *>(ws_post + col(j) + i) =
-              make_float4(post[(j * V + i) * blockDim.x], post[(j * V + i + 1) * blockDim.x],
-                          post[(j * V + i + 2) * blockDim.x], post[(j * V + i + 3) * blockDim.x]);
-      }
+  for (int k = 0; k < NQ; ++k) {
+    const int c = my.quad(k);
+    if (c < p.cols) {
+      if (p.dw_pre)
+        *reinterpret_cast<float4 *>(p.ws + (int64_t)blockIdx.x * p.cols + c) =
+            make_float4(a_pre[k][0], a_pre[k][1], a_pre[k][2], a_pre[k][3]);
+      if (p.dw_post)
+        *reinterpret_cast<float4 *>(p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.cols + c) =
+            make_float4(post[(k * 4) * blockDim.x], post[(k * 4 + 1) * blockDim.x], post[(k * 4 + 2) * blockDim.x],
+                        post[(k * 4 + 3) * blockDim.x]);
     }
+  }
 }
 
 // Column sums of the partials: y 0 dw_pre, 1 dw_post, 2 + g the gate rows.
@@ -860,9 +885,10 @@ static int threads_of(int cols, int V, int nv, int most) {
   return t <= most ? t : 0;
 }
 
-// Resident blocks of a staged kernel with `resident` threads an SM
-static int64_t staged_blocks(int64_t rows, int threads, int resident, int num_sms) {
-  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * std::max(1, resident / threads)));
+// Resident blocks of a staged kernel: 1024 threads an SM at 2 quads, 512 or 768 at 4
+static int staged_per_sm(int threads, int nq) { return std::max(1, (nq == 2 ? 1024 : 512) / threads); }
+static int64_t staged_blocks(int64_t rows, int threads, int nq, int num_sms) {
+  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * staged_per_sm(threads, nq)));
 }
 // Rows to copy ahead: up to three, as many as leave room for `blocks` blocks an SM
 static int ahead_of(size_t arrays, size_t fixed, size_t vectors, int blocks) {
@@ -874,10 +900,9 @@ static int64_t split_of(int64_t gates, int64_t per_gate, int64_t blocks) {
   if (gates >= blocks) return 1;
   return std::max<int64_t>(1, std::min<int64_t>(per_gate, blocks / gates));
 }
-// Columns of a thread: 8 in rows of up to 2048, else 16 (what a thread keeps
-// beside its columns -- addresses, the generator's words -- is spent on twice
-// as many)
-static int staged_cols(int cols) { return cols <= 2048 ? 8 : 16; }
+// Quads of a thread's columns, and the threads of a staged block
+static int staged_quads(int cols, int quads) { return cols <= 2048 ? 2 : quads; }
+static int staged_threads(int cols, int nq) { return (cols / 4 + 32 * nq - 1) / (32 * nq) * 32; }
 
 template <typename T, int V, int NV>
 static cudaError_t run_fwd(const Fwd &p, int tpr, int num_sms, cudaStream_t st) {
@@ -890,17 +915,16 @@ template <typename T, int V>
 static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
   if constexpr (V > 1) {
     if (p.cols <= STAGED_COLS) {
-      const int nv = staged_cols(p.cols) / V;
-      const int threads = threads_of(p.cols, V, nv, 512);
-      const int64_t most = staged_blocks(p.rows, threads, 512, num_sms);
+      const int nq = staged_quads(p.cols, FWD_QUADS), threads = staged_threads(p.cols, nq);
+      const int64_t most = staged_blocks(p.rows, threads, nq, num_sms);
       p.split = (int)split_of(p.gates, p.per_gate, most);
       p.per_item = (p.per_gate + p.split - 1) / p.split;
       const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split);
       const int with_rows = p.gate && p.per_gate <= GATE_WITH_ROWS;
-      const size_t vectors = (size_t)nv * threads * 16;  // a row's of one array
-      const int ahead = ahead_of(2 + with_rows, 1, vectors, 512 / threads);
+      const size_t vectors = 4 * nq * sizeof(T) * threads;  // a row's bytes of one array
+      const int ahead = ahead_of(2 + with_rows, 1, vectors, staged_per_sm(threads, nq));
       const size_t smem = ((size_t)ahead * (2 + with_rows) + 1) * vectors;
-      auto kern = nv * V == 8 ? block_norm_staged_kernel<T, V, 8 / V> : block_norm_staged_kernel<T, V, 16 / V>;
+      auto kern = nq == 2 ? block_norm_staged_kernel<T, 2> : block_norm_staged_kernel<T, FWD_QUADS>;
       const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (err != cudaSuccess) return err;
       kern<<<blocks, threads, smem, st>>>(p, with_rows, ahead);
@@ -918,13 +942,13 @@ static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
 // The backward's launch: threads and blocks for rows in vectors of V
 struct BwdPlan {
   bool staged;
-  int threads, nv;  // nv: registers' vectors of the plain kernel (0: none)
+  int threads, nv;  // a thread's quads, or the plain kernel's vectors in registers (0: none)
   int64_t blocks;
 };
 static BwdPlan plan_bwd(int64_t rows, int cols, int V, int num_sms) {
   if (V > 1 && cols <= STAGED_COLS) {
-    const int nv = staged_cols(cols) / V, t = threads_of(cols, V, nv, 512);
-    return BwdPlan{true, t, nv, staged_blocks(rows, t, 512, num_sms)};
+    const int nq = staged_quads(cols, BWD_QUADS), t = staged_threads(cols, nq);
+    return BwdPlan{true, t, nq, staged_blocks(rows, t, nq, num_sms)};
   }
   const int n = V == 1 ? 8 : 0;
   const int t = n ? threads_of(cols, V, n, 512) : 0;
@@ -943,12 +967,11 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
   if constexpr (V > 1) {
     if (plan.staged) {
       const int with_rows = p.gate && p.per_gate <= GATE_WITH_ROWS;
-      const size_t vectors = (size_t)plan.nv * plan.threads * 16;
-      const size_t sums = V * sizeof(float) / 16;  // dw_post's sums, in vectors
-      const int ahead = ahead_of(4 + with_rows, 1 + sums, vectors, 512 / plan.threads);
+      const size_t vectors = 4 * plan.nv * sizeof(T) * plan.threads;
+      const size_t sums = sizeof(float) / sizeof(T);  // dw_post's sums, in rows
+      const int ahead = ahead_of(4 + with_rows, 1 + sums, vectors, staged_per_sm(plan.threads, plan.nv));
       const size_t smem = ((size_t)ahead * (4 + with_rows) + 1 + sums) * vectors;
-      auto kern = plan.nv * V == 8 ? block_norm_bwd_staged_kernel<T, V, 8 / V>
-                                   : block_norm_bwd_staged_kernel<T, V, 16 / V>;
+      auto kern = plan.nv == 2 ? block_norm_bwd_staged_kernel<T, 2> : block_norm_bwd_staged_kernel<T, BWD_QUADS>;
       err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (err != cudaSuccess) return err;
       kern<<<blocks, plan.threads, smem, st>>>(p, with_rows, ahead);
@@ -999,8 +1022,8 @@ cudaError_t launch_block_norm(const sym_block_norm &a, int num_sms, cudaStream_t
   Fwd p = {};
   p.x = a.x, p.o = a.o, p.w_post = a.w_post, p.w_pre = a.w_pre, p.gate = a.gate, p.y = a.y, p.h = a.h;
   p.rstd_post = a.rstd_post, p.rstd_pre = a.rstd_pre;
-  p.ldx = a.ld_x, p.ldo = a.ld_o, p.ldy = a.ld_y, p.ldh = a.ld_h, p.ldg = a.ld_gate;
-  p.rows = a.rows, p.gates = a.gate ? (int)a.gate_rows : 1;
+  p.ldx = (int)a.ld_x, p.ldo = (int)a.ld_o, p.ldy = (int)a.ld_y, p.ldh = (int)a.ld_h, p.ldg = (int)a.ld_gate;
+  p.rows = (int)a.rows, p.gates = a.gate ? (int)a.gate_rows : 1;
   p.per_gate = p.rows / p.gates;
   p.cols = a.cols, p.act = a.gate_act, p.post_norm = !(a.flags & SYM_NORM_NO_POST);
   p.scale = a.scale, p.eps = a.eps, p.drop = a.p > 0;
@@ -1021,9 +1044,9 @@ cudaError_t launch_block_norm_bwd(const sym_block_norm &a, const sym_block_norm_
   p.rstd_post = a.rstd_post, p.rstd_pre = a.rstd_pre;
   p.dx = b.dx, p.dout = b.d_o, p.dw_pre = b.dw_pre, p.dw_post = b.dw_post, p.dgate = b.dgate;
   p.ws = reinterpret_cast<float *>(b.work);
-  p.ld_dy = b.ld_dy, p.ld_dh = b.ld_dh, p.ldy = a.ld_y, p.ldo = a.ld_o, p.ldg = a.ld_gate;
-  p.ld_dx = b.ld_dx, p.ld_do = b.ld_do, p.ld_dg = b.ld_dgate;
-  p.rows = a.rows, p.gates = a.gate ? (int)a.gate_rows : 1;
+  p.ld_dy = (int)b.ld_dy, p.ld_dh = (int)b.ld_dh, p.ldy = (int)a.ld_y, p.ldo = (int)a.ld_o, p.ldg = (int)a.ld_gate;
+  p.ld_dx = (int)b.ld_dx, p.ld_do = (int)b.ld_do, p.ld_dg = (int)b.ld_dgate;
+  p.rows = (int)a.rows, p.gates = a.gate ? (int)a.gate_rows : 1;
   p.per_gate = p.rows / p.gates;
   p.cols = a.cols, p.act = a.gate_act, p.post_norm = !(a.flags & SYM_NORM_NO_POST);
   p.scale = a.scale, p.drop = a.p > 0;

@@ -461,7 +461,8 @@ int moe_dropout(int dtype, const sym_rows *x, const sym_rows *residual, const sy
 
 // a tensor of the call: aligned to its type, rows that do not overlap
 static bool tensor_ok(const void *p, int64_t ld, int64_t rows, int cols, int dtype) {
-  return reinterpret_cast<uintptr_t>(p) % size_of(dtype) == 0 && (!p || rows <= 1 || ld >= cols);
+  return reinterpret_cast<uintptr_t>(p) % size_of(dtype) == 0 &&
+         (!p || rows <= 1 || (ld >= cols && ld < (int64_t(1) << 31)));
 }
 static bool block_ok(const sym_block_norm *a) {
   if (!a || !dtype_ok(a->dtype) || a->rows < 0 || a->rows >= (int64_t(1) << 30) || a->cols < 1 || a->cols > 65536)

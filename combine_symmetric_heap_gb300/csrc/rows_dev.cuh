@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "symmoe_dev.cuh"
 
 namespace symmoe {
@@ -83,6 +85,27 @@ __device__ __forceinline__ void store(T *p, const float (&f)[V]) {
   else *reinterpret_cast<uint4 *>(p) = pack<T, V>(f);
 }
 
+// Four elements: 8 or 16 bytes
+template <typename T>
+struct Quad {
+  using Word = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;
+  static __device__ __forceinline__ void get(const void *p, float (&f)[4]) {
+    const Word w = *reinterpret_cast<const Word *>(p);
+    if constexpr (sizeof(T) == 4) {
+      f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y), f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
+    } else {
+      const float2 a = Elem<T>::get2(w.x), b = Elem<T>::get2(w.y);
+      f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+    }
+  }
+  static __device__ __forceinline__ Word put(const float (&f)[4]) {
+    if constexpr (sizeof(T) == 4)
+      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    else
+      return make_uint2(Elem<T>::put2(f[0], f[1]), Elem<T>::put2(f[2], f[3]));
+  }
+};
+
 // Columns [c, c + V) of a row, of which those outside [0, cols) do not exist
 // (zeros on a load, skipped on a store); whole vectors are 16-byte accesses,
 // so c places p + c on a 16-byte boundary.
@@ -116,9 +139,13 @@ __device__ __forceinline__ void store_part(T *p, int c, int cols, const float (&
 struct Random {
   uint64_t offset;
   uint32_t key[10][2];  // the rounds' keys
-  uint32_t threshold;   // an element is kept where its word >= threshold
-  float keep_scale;     // 1 / (1 - p)
+  // The first two rounds multiply two words that are the same for all blocks
+  // below 2^32: what they leave behind (see random_block).
+  uint32_t first[4];
+  uint32_t threshold;  // an element is kept where its word >= threshold
+  float keep_scale;    // 1 / (1 - p)
 };
+constexpr uint32_t PHILOX_A = 0xD2511F53u, PHILOX_B = 0xCD9E8D57u;
 inline Random make_random(uint64_t seed, uint64_t offset, double p) {
   Random r;
   r.offset = offset;
@@ -127,22 +154,44 @@ inline Random make_random(uint64_t seed, uint64_t offset, double p) {
     r.key[i][0] = k0;
     r.key[i][1] = k1;
   }
+  const uint64_t b = (uint64_t)(uint32_t)offset * PHILOX_B;  // round 1, of the counter's third word
+  const uint64_t a = (uint64_t)((uint32_t)(b >> 32) ^ r.key[0][0]) * PHILOX_A;  // round 2, of the first
+  r.first[0] = (uint32_t)(offset >> 32) ^ r.key[0][1];  // round 1: third word = high(a) ^ this
+  r.first[1] = (uint32_t)b ^ r.key[1][0];               // round 2: first word = high(b) ^ this
+  r.first[2] = (uint32_t)(a >> 32) ^ r.key[1][1];       // round 2: third word = low(a of round 1) ^ this
+  r.first[3] = (uint32_t)a;                             // round 2: fourth word
   r.threshold = (uint32_t)(p * 4294967296.0);
   r.keep_scale = (float)(1.0 / (1.0 - p));
   return r;
 }
 __device__ __forceinline__ uint4 random_block(const Random &r, uint64_t block) {
-  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32);
-  uint32_t c2 = (uint32_t)r.offset, c3 = (uint32_t)(r.offset >> 32);
-#pragma unroll
-  for (int i = 0; i < 10; ++i) {
-    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2, c3;
+  auto round = [&](int i) {
+    const uint64_t a = (uint64_t)c0 * PHILOX_A, b = (uint64_t)c2 * PHILOX_B;
     c0 = (uint32_t)(b >> 32) ^ c1 ^ r.key[i][0];
     c1 = (uint32_t)b;
     c2 = (uint32_t)(a >> 32) ^ c3 ^ r.key[i][1];
     c3 = (uint32_t)a;
+  };
+  if (c1 == 0) {
+    const uint64_t a = (uint64_t)c0 * PHILOX_A;
+    const uint64_t b = (uint64_t)((uint32_t)(a >> 32) ^ r.first[0]) * PHILOX_B;
+    c0 = (uint32_t)(b >> 32) ^ r.first[1];
+    c1 = (uint32_t)b;
+    c2 = (uint32_t)a ^ r.first[2];
+    c3 = r.first[3];
+  } else {
+    c2 = (uint32_t)r.offset, c3 = (uint32_t)(r.offset >> 32);
+    round(0);
+    round(1);
   }
+#pragma unroll
+  for (int i = 2; i < 10; ++i) round(i);
   return make_uint4(c0, c1, c2, c3);
+}
+__device__ __forceinline__ void random_words(const Random &r, uint64_t block, uint32_t (&u)[4]) {
+  const uint4 w = random_block(r, block);
+  u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
 }
 // keep factors (0 or 1 / (1 - p)) of the V elements from element `at` on
 template <int V>

@@ -148,6 +148,52 @@ __global__ void __launch_bounds__(THREADS) dropout_kernel(const RowArgs p, const
   }
 }
 
+// The same over one run of n contiguous elements (element i is number i of the
+// stream): no rows to address, two vectors in flight a thread.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) dropout_flat_kernel(const T *x, const T *res, T *y, int64_t n,
+                                                               const Random rnd) {
+  constexpr int V = Elem<T>::VEC, U = 2;
+  const int64_t vecs = n / V, step = (int64_t)gridDim.x * THREADS;
+  const uint4 *xv = reinterpret_cast<const uint4 *>(x), *rv = reinterpret_cast<const uint4 *>(res);
+  for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < vecs; i += U * step) {
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * step < vecs) {
+        a[u] = xv[i + u * step];
+        if (res) b[u] = rv[i + u * step];
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * step < vecs) {
+        const int64_t at = i + u * step;
+        float f[V], r[V];
+        unpack<T, V>(a[u], f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) r[j] = 0.f;
+        if (res) unpack<T, V>(b[u], r);
+#pragma unroll
+        for (int q = 0; q < V; q += 4) {
+          uint32_t word[4];
+          random_words(rnd, (uint64_t)(at * V + q) >> 2, word);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (word[j] >= rnd.threshold) r[q + j] += f[q + j] * rnd.keep_scale;
+        }
+        reinterpret_cast<uint4 *>(y)[at] = pack<T, V>(r);
+      }
+  }
+  if (blockIdx.x == 0 && threadIdx.x < n % V) {
+    const int64_t at = vecs * V + threadIdx.x;
+    uint32_t word[4];
+    random_words(rnd, (uint64_t)at >> 2, word);
+    const bool kept = word[at & 3] >= rnd.threshold;
+    const float r = res ? Elem<T>::get(res[at]) : 0.f;
+    y[at] = Elem<T>::put(kept ? r + Elem<T>::get(x[at]) * rnd.keep_scale : r);
+  }
+}
+
 static View view_of(const sym_rows *r, int64_t es) {
   if (!r) return View{nullptr, 0, 0};
   return View{reinterpret_cast<char *>(r->ptr), r->ld * es, r->slots > 1 ? r->slot_stride * es : 0};
@@ -237,6 +283,25 @@ cudaError_t launch_dropout(int dtype, const sym_rows &x, const sym_rows *res, co
   RowArgs a = {};
   a.a = view_of(&x, es), a.b = view_of(res, es), a.c = view_of(&y, es);
   a.rows = x.rows, a.slots = x.slots, a.cols = x.cols;
+  // rows that follow each other without gaps, on 16-byte boundaries: one run
+  auto run = [&](const sym_rows *r) {
+    return !r || (r->ptr % 16 == 0 && (r->rows == 1 || r->ld == r->cols) &&
+                  (r->slots == 1 || r->slot_stride == r->rows * r->cols));
+  };
+  if (run(&x) && run(&y) && run(res)) {
+    const int64_t n = x.rows * x.slots * x.cols, per = THREADS * 2 * (16 / es);
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + per - 1) / per, (int64_t)num_sms * 32);
+    auto go = [&](auto zero) {
+      using T = decltype(zero);
+      dropout_flat_kernel<T><<<blocks, THREADS, 0, st>>>(reinterpret_cast<const T *>(x.ptr),
+                                                         res ? reinterpret_cast<const T *>(res->ptr) : nullptr,
+                                                         reinterpret_cast<T *>(y.ptr), n, rnd);
+    };
+    if (dtype == SYM_BF16) go(__nv_bfloat16{});
+    else if (dtype == SYM_FP16) go(__half{});
+    else go(float{});
+    return cudaGetLastError();
+  }
   const Shape s = shape_of(x.rows, x.slots, x.cols, vec ? (int)(16 / es) : 1, num_sms);
   SYM_ROWS_LAUNCH(dropout_kernel, a, rnd)
 }
