@@ -428,17 +428,19 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
 
 // ---------------------------------------------------------------------------
 // Staged kernels: rows in 16-byte vectors, at most 8192 columns.  A block walks
-// work items (runs of rows that share a gate row) with 8 columns a thread,
-// worked on as two quads so that 64 registers do and 1024 threads an SM hide
-// the generator's and the reductions' latencies (16 columns a thread at 128
-// registers: train 162, gradient 258 us).  A thread copies its own vectors of the
-// next rows into its own shared memory (cp.async, a few rows deep), so no
-// barrier guards the copies.  What a column needs for every row stays with its
-// thread for the item's rows: the activated gate in registers, the weights in
-// shared memory.
+// work items (runs of rows that share a gate row); a thread holds 8 or 16
+// columns and copies its own vectors of the next rows into its own shared
+// memory (cp.async, a few rows deep), so no barrier guards the copies.  What a
+// column needs for every row stays with its thread for the item's rows: the
+// activated gate in registers, the weights in shared memory.
+//
+// With rows of a few thousand columns these kernels are bound by the latency
+// of a row's chain (read, reduce, finish) as much as by bytes: one reduction a
+// row, four sums at a time; no branches in the inner loops (tensors that are
+// not there, and columns past the row's end, are zeros in shared memory, the
+// weights ones); addresses that are constants from a row's start.
 // ---------------------------------------------------------------------------
 constexpr int STAGED_COLS = 8192;
-constexpr int FWD_QUADS = 4, BWD_QUADS = 4;
 constexpr int STAGED_SMEM = 220 * 1024;
 // A gate row shared by this few rows is copied along with each of them.
 constexpr int GATE_WITH_ROWS = 4;
@@ -466,48 +468,49 @@ struct Walk {
   }
 };
 
-// A thread's NQ quads of columns and its share of the row buffers.  16-bit
-// types: quads 2j and 2j + 1 are vector j; fp32: quad k is vector k.  A thread's
-// vectors are a block's width apart.
-template <typename T, int NQ>
-struct Mine {
-  static constexpr int PER = sizeof(T) == 4 ? 1 : 2;  // quads of a vector
-  static constexpr int NV = NQ / PER;
-  int threads, arrays, ahead, turn;
-  char *buf;
-  __device__ Mine(char *smem, int arrays_, int ahead_)
-      : threads(blockDim.x), arrays(arrays_), ahead(ahead_), turn(0), buf(smem + threadIdx.x * 16) {}
-  // first column of vector j and of quad k
-  __device__ __forceinline__ int vector(int j) const {
-    return ((int)threadIdx.x + j * threads) * (16 / (int)sizeof(T));
+// A thread's columns: NG groups of 8.  16-bit types: a group is one 16-byte
+// vector; fp32: two.  A thread's vectors lie a block's width apart in a row, and
+// MAXT words of 16 bytes apart in shared memory.
+template <typename T, int NG_, int MAXT_>
+struct Columns {
+  static constexpr int NG = NG_, MAXT = MAXT_;
+  static constexpr int PER = sizeof(T) / 2;  // vectors of a group
+  static constexpr int NV = NG * PER;
+  static constexpr int W = 16 / sizeof(T);   // columns of a vector
+  static __device__ __forceinline__ int vector(int j) { return ((int)threadIdx.x + j * (int)blockDim.x) * W; }
+  static __device__ __forceinline__ int quad(int g, int k) { return vector(g * PER + k / (W / 4)) + 4 * (k % (W / 4)); }
+  // place of vector j of array a in a row's shared memory, in bytes
+  static __device__ __forceinline__ constexpr int place(int a, int j) { return (a * NV + j) * MAXT * 16; }
+  static __host__ __device__ constexpr int row_bytes(int arrays) { return arrays * NV * MAXT * 16; }
+};
+// A group's 8 values of one array: two quads
+template <typename C, typename T>
+struct Eight {
+  uint4 v[C::PER];
+  __device__ __forceinline__ Eight(const char *p, int g) {
+#pragma unroll
+    for (int j = 0; j < C::PER; ++j) v[j] = *reinterpret_cast<const uint4 *>(p + C::place(0, g * C::PER + j));
   }
-  __device__ __forceinline__ int quad(int k) const { return vector(k / PER) + 4 * (k % PER); }
-  // vector j / quad k of `slot`, one of the 16-byte-per-thread planes
-  __device__ __forceinline__ char *plane(int slot, int j) const { return buf + (size_t)(slot * NV + j) * threads * 16; }
-  __device__ __forceinline__ char *plane_quad(int slot, int k) const {
-    return plane(slot, k / PER) + 8 * (k % PER);
-  }
-  __device__ __forceinline__ char *row_vector(int a, int j) const { return plane(turn * arrays + a, j); }
-  __device__ __forceinline__ char *row_quad(int a, int k) const { return plane_quad(turn * arrays + a, k); }
-  __device__ __forceinline__ void next() { turn = turn + 1 == ahead ? 0 : turn + 1; }
-  // the oldest row in flight has landed
-  __device__ __forceinline__ void wait() const {
-    if (ahead == 3) cp_async_wait<2>();
-    else if (ahead == 2) cp_async_wait<1>();
-    else cp_async_wait<0>();
+  __device__ __forceinline__ void quad(int k, float (&f)[4]) const {
+    if constexpr (sizeof(T) == 4) {
+      unpack<T, 4>(v[k], f);
+    } else {
+      const float2 a = Elem<T>::get2(k ? v[0].z : v[0].x), b = Elem<T>::get2(k ? v[0].w : v[0].y);
+      f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+    }
   }
 };
 // Quads' results as whole 16-byte stores
 template <typename T>
 struct Writer {
   typename Quad<T>::Word first;
-  __device__ __forceinline__ void put(int k, T *row, int col, const float (&f)[4]) {
+  __device__ __forceinline__ void put(int k, T *row, int col, int cols, const float (&f)[4]) {
     const typename Quad<T>::Word w = Quad<T>::put(f);
     if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<uint4 *>(row + col) = w;
+      if (col < cols) *reinterpret_cast<uint4 *>(row + col) = w;
     } else {
-      if (k % 2 == 0) first = w;
-      else *reinterpret_cast<uint4 *>(row + col - 4) = make_uint4(first.x, first.y, w.x, w.y);
+      if (k == 0) first = w;
+      else if (col < cols) *reinterpret_cast<uint4 *>(row + col - 4) = make_uint4(first.x, first.y, w.x, w.y);
     }
   }
 };
@@ -529,173 +532,213 @@ __device__ __forceinline__ void factor_of(float scale, int act, const void *gate
     for (int i = 0; i < 4; ++i) f[i] *= w[i];
   }
 }
+// zeros in a thread's part of the rows, w_pre (or ones) in its fixed part
+template <typename C, typename T>
+__device__ __forceinline__ void prepare_rows(char *row0, char *end, char *fixed, const T *w_pre, int cols) {
+  for (char *q = row0; q < end; q += C::MAXT * 16) *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
+  float one[Elem<T>::VEC];
+#pragma unroll
+  for (int i = 0; i < Elem<T>::VEC; ++i) one[i] = 1.f;
+#pragma unroll
+  for (int j = 0; j < C::NV; ++j)
+    *reinterpret_cast<uint4 *>(fixed + C::place(0, j)) =
+        w_pre && C::vector(j) < cols ? *reinterpret_cast<const uint4 *>(w_pre + C::vector(j)) : pack<T, Elem<T>::VEC>(one);
+}
+__device__ __forceinline__ void wait_oldest(int ahead) {
+  if (ahead == 3) cp_async_wait<2>();
+  else if (ahead == 2) cp_async_wait<1>();
+  else cp_async_wait<0>();
+}
 
-template <typename T, int NQ>
-__global__ void __launch_bounds__(NQ == 2 ? 1024 : 512) block_norm_staged_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
+// Forward.  With q = scale drop act(gate) w_post o, y = x + rstd_o q, so the sum
+// of y^2 comes from the same reduction as rstd_o's: it is the sum of x^2 + 2
+// rstd_o x q + rstd_o^2 q^2.  Where those cancel (y shorter than a third of its
+// parts) y^2 is summed over again.
+template <typename T, bool DROP, int NG, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
+  using C = Columns<T, NG, MAXT>;
   extern __shared__ __align__(16) char smem[];
-  __shared__ float buf[2 * 32];
+  __shared__ float buf[2 * 128];
+  enum { X, O, GATE };
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
-  // x, o and, where it changes from row to row, the gate; then w_pre
-  using M = Mine<T, NQ>;
-  M my(smem, 2 + gate_with_rows, ahead_rows);
-  const int w_slot = ahead_rows * my.arrays;
+  const int row_step = C::row_bytes(2 + gate_with_rows);
+  char *const row0 = smem + threadIdx.x * 16, *const row_end = row0 + ahead_rows * row_step, *const fixed = row_end;
   const float inv = 1.f / p.cols;
-  const T *w_post = reinterpret_cast<const T *>(p.w_post), *w_pre = reinterpret_cast<const T *>(p.w_pre);
+  const T *w_post = reinterpret_cast<const T *>(p.w_post);
+  prepare_rows<C, T>(row0, row_end, fixed, reinterpret_cast<const T *>(p.w_pre), p.cols);
   Walk ahead(p.per_gate, p.per_item, p.gates, p.split), now = ahead;
-  auto fetch = [&]() {  // the next row, into the slot that is free
+  auto fetch = [&](char *to) {  // the next row
     if (ahead.live()) {
       const int r = ahead.row;
 #pragma unroll
-      for (int j = 0; j < M::NV; ++j) {
-        const int c = my.vector(j);
+      for (int j = 0; j < C::NV; ++j) {
+        const int c = C::vector(j);
         if (c < p.cols) {
-          cp_async16(my.row_vector(0, j), at<T>(p.x, r, p.ldx) + c);
-          if (p.o) cp_async16(my.row_vector(1, j), at<T>(p.o, r, p.ldo) + c);
-          if (gate_with_rows)
-            cp_async16(my.row_vector(2, j), at<T>(p.gate, ahead.item / p.split, p.ldg) + c);
+          cp_async16(to + C::place(X, j), at<T>(p.x, r, p.ldx) + c);
+          if (p.o) cp_async16(to + C::place(O, j), at<T>(p.o, r, p.ldo) + c);
+          if (gate_with_rows) cp_async16(to + C::place(GATE, j), at<T>(p.gate, ahead.item / p.split, p.ldg) + c);
         }
       }
       ahead.next();
     }
     cp_async_commit();
   };
-  for (int i = 0; i < ahead_rows; ++i, my.next()) fetch();
-  if (w_pre)
+  for (char *to = row0; to != row_end; to += row_step) fetch(to);
+  char *row = row0;
+  float factor[NG][2][4];
 #pragma unroll
-    for (int j = 0; j < M::NV; ++j)
-      if (my.vector(j) < p.cols)
-        *reinterpret_cast<uint4 *>(my.plane(w_slot, j)) = *reinterpret_cast<const uint4 *>(w_pre + my.vector(j));
-  float factor[NQ][4];
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) factor[g][i / 4][i % 4] = 0.f;
   int half = 0, item = -1;
   for (; now.live(); now.next()) {
     const int r = now.row;
-    if (p.o && (now.item != item) && !gate_with_rows) {
+    if (now.item != item && !gate_with_rows) {
       item = now.item;
       const T *gate = p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
 #pragma unroll
-      for (int k = 0; k < NQ; ++k) {
-        const int c = my.quad(k);
-        if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[k]);
-      }
-    }
-    my.wait();
-    if (p.o && gate_with_rows)
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int k = 0; k < NQ; ++k) {
-        const int c = my.quad(k);
-        if (c < p.cols) factor_of<T>(p.scale, p.act, my.row_quad(2, k), w_post ? w_post + c : nullptr, factor[k]);
-      }
-    float rstd_o = 1.f;
-    if (p.o && p.post_norm) {
-      float s[1] = {0.f};
-#pragma unroll
-      for (int k = 0; k < NQ; ++k)
-        if (my.quad(k) < p.cols) {
-          float ov[4];
-          Quad<T>::get(my.row_quad(1, k), ov);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[0] += ov[i] * ov[i];
+        for (int k = 0; k < 2; ++k) {
+          const int c = C::quad(g, k);
+          if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[g][k]);
         }
-      group_sums<1>(s, buf, warp, warps, half);
-      rstd_o = rsqrtf(s[0] * inv + p.eps);
-      if (threadIdx.x == 0 && p.rstd_post) p.rstd_post[r] = rstd_o;
     }
-    float y[NQ][4], s[1] = {0.f};
+    wait_oldest(ahead_rows);
+    if (gate_with_rows)
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = C::quad(g, k);
+          const char *gate = row + C::place(GATE, g * C::PER + k / (C::W / 4)) + 4 * (k % (C::W / 4)) * (int)sizeof(T);
+          if (c < p.cols) factor_of<T>(p.scale, p.act, gate, w_post ? w_post + c : nullptr, factor[g][k]);
+        }
+    // sums of o^2, x^2, x q, q^2
+    float x[NG][2][4], q[NG][2][4], s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const Eight<C, T> x8(row + C::place(X, 0), g), o8(row + C::place(O, 0), g);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float ov[4];
+        x8.quad(k, x[g][k]);
+        o8.quad(k, ov);
+        uint32_t word[4];
+        if (DROP) random_words(p.rnd, ((uint64_t)r * p.cols + C::quad(g, k)) >> 2, word);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float xv = x[g][k][i], qv = !DROP || word[i] >= p.rnd.threshold ? ov[i] * factor[g][k][i] : 0.f;
+          q[g][k][i] = qv;
+          s[0] += ov[i] * ov[i];
+          s[1] += xv * xv;
+          s[2] += xv * qv;
+          s[3] += qv * qv;
+        }
+      }
+    }
+    fetch(row);
+    row = row + row_step == row_end ? row0 : row + row_step;
+    block_sums4(s, buf, warp, warps, half);
+    const float rstd_o = p.post_norm ? rsqrtf(s[0] * inv + p.eps) : 1.f;
+    const float f = DROP ? rstd_o * p.rnd.keep_scale : rstd_o;
+    float yy = s[1] + f * (2.f * s[2] + f * s[3]);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[g][i / 4][i % 4] += f * q[g][i / 4][i % 4];  // y
+    if (!(yy >= 0.1f * (s[1] + f * f * s[3]))) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[0] += x[g][i / 4][i % 4] * x[g][i / 4][i % 4];
+      block_sums4(t, buf, warp, warps, half);
+      yy = t[0];
+    }
+    const float rstd_y = rsqrtf(yy * inv + p.eps);
+    if (threadIdx.x == 0) {
+      if (p.rstd_post) p.rstd_post[r] = rstd_o;
+      if (p.rstd_pre) p.rstd_pre[r] = rstd_y;
+    }
     Writer<T> out;
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-      const int c = my.quad(k);
-      if (c < p.cols) {
-        Quad<T>::get(my.row_quad(0, k), y[k]);
-        if (p.o) {
-          float ov[4];
-          Quad<T>::get(my.row_quad(1, k), ov);
-          const float ks = p.drop ? rstd_o * p.rnd.keep_scale : rstd_o;
-          uint32_t word[4] = {~0u, ~0u, ~0u, ~0u};
-          if (p.drop) random_words(p.rnd, ((uint64_t)r * p.cols + c) >> 2, word);
+    for (int g = 0; g < NG; ++g) {
+      if (p.y)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (word[i] >= p.rnd.threshold) y[k][i] += ov[i] * ks * factor[k][i];
-          out.put(k, at<T>(p.y, r, p.ldy), c, y[k]);
-        }
+        for (int k = 0; k < 2; ++k) out.put(k, at<T>(p.y, r, p.ldy), C::quad(g, k), p.cols, x[g][k]);
+      if (!p.h) continue;
+      const Eight<C, T> w8(fixed, g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[0] += y[k][i] * y[k][i];
+      for (int k = 0; k < 2; ++k) {
+        float w[4];
+        w8.quad(k, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] *= x[g][k][i] * rstd_y;
+        out.put(k, at<T>(p.h, r, p.ldh), C::quad(g, k), p.cols, w);
       }
     }
-    fetch();
-    my.next();
-    if (!p.h && !p.rstd_pre) continue;
-    group_sums<1>(s, buf, warp, warps, half);
-    const float rstd_y = rsqrtf(s[0] * inv + p.eps);
-    if (threadIdx.x == 0 && p.rstd_pre) p.rstd_pre[r] = rstd_y;
-    if (!p.h) continue;
-#pragma unroll
-    for (int k = 0; k < NQ; ++k)
-      if (my.quad(k) < p.cols) {
-        float w[4] = {1.f, 1.f, 1.f, 1.f};
-        if (w_pre) Quad<T>::get(my.plane_quad(w_slot, k), w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[k][i] *= rstd_y * w[i];
-        out.put(k, at<T>(p.h, r, p.ldh), my.quad(k), y[k]);
-      }
   }
 }
 
 // Backward.  Per column the block keeps two sums: of dh yn (dw_pre), and over
 // an item's rows S = sum drop dx on, from which both dw_post = sum over gates
 // of scale act S and dgate = scale act' w_post S follow.
-template <typename T, int NQ>
-__global__ void __launch_bounds__(NQ == 2 ? 1024 : 512) block_norm_bwd_staged_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
+template <typename T, bool DROP, int NG, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
+  using C = Columns<T, NG, MAXT>;
   extern __shared__ __align__(16) char smem[];
-  __shared__ float buf[2 * 32 * 3];
+  __shared__ float buf[2 * 128];
+  enum { DY, DH, Y, O, GATE };
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
-  // dy, dh, y, o and, where it changes from row to row, the gate; then w_pre,
-  // then this thread's columns of dw_post, summed over the items
-  using M = Mine<T, NQ>;
-  M my(smem, 4 + gate_with_rows, ahead_rows);
-  const int w_slot = ahead_rows * my.arrays;
-  float *post = reinterpret_cast<float *>(smem + (size_t)(w_slot + 1) * M::NV * blockDim.x * 16) + threadIdx.x;
+  const int row_step = C::row_bytes(4 + gate_with_rows);
+  char *const row0 = smem + threadIdx.x * 16, *const row_end = row0 + ahead_rows * row_step, *const fixed = row_end;
+  // dw_post's sums over the items: quad k of group g at post[(2g + k) * MAXT]
+  float4 *const post = reinterpret_cast<float4 *>(fixed + C::row_bytes(1));
   const float inv = 1.f / p.cols;
-  const T *w_post = reinterpret_cast<const T *>(p.w_post), *w_pre = reinterpret_cast<const T *>(p.w_pre);
-  Walk ahead(p.per_gate, p.per_item, p.gates, p.split), now = ahead;
-  auto fetch = [&]() {  // the next row, into the slot that is free
+  const T *w_post = reinterpret_cast<const T *>(p.w_post);
+  prepare_rows<C, T>(row0, row_end, fixed, reinterpret_cast<const T *>(p.w_pre), p.cols);
+  Walk ahead(p.per_gate, p.per_item, p.gates, p.split), now = ahead, soon = ahead;
+  auto fetch = [&](char *to) {  // the next row
     if (ahead.live()) {
       const int r = ahead.row;
 #pragma unroll
-      for (int j = 0; j < M::NV; ++j) {
-        const int c = my.vector(j);
+      for (int j = 0; j < C::NV; ++j) {
+        const int c = C::vector(j);
         if (c < p.cols) {
-          if (p.dy) cp_async16(my.row_vector(0, j), at<T>(p.dy, r, p.ld_dy) + c);
+          if (p.dy) cp_async16(to + C::place(DY, j), at<T>(p.dy, r, p.ld_dy) + c);
           if (p.dh) {
-            cp_async16(my.row_vector(1, j), at<T>(p.dh, r, p.ld_dh) + c);
-            cp_async16(my.row_vector(2, j), at<T>(p.y, r, p.ldy) + c);
+            cp_async16(to + C::place(DH, j), at<T>(p.dh, r, p.ld_dh) + c);
+            cp_async16(to + C::place(Y, j), at<T>(p.y, r, p.ldy) + c);
           }
-          if (p.o) cp_async16(my.row_vector(3, j), at<T>(p.o, r, p.ldo) + c);
-          if (gate_with_rows)
-            cp_async16(my.row_vector(4, j), at<T>(p.gate, ahead.item / p.split, p.ldg) + c);
+          if (p.o) cp_async16(to + C::place(O, j), at<T>(p.o, r, p.ldo) + c);
+          if (gate_with_rows) cp_async16(to + C::place(GATE, j), at<T>(p.gate, ahead.item / p.split, p.ldg) + c);
         }
       }
       ahead.next();
     }
     cp_async_commit();
   };
-  for (int i = 0; i < ahead_rows; ++i, my.next()) fetch();
-  if (w_pre)
-#pragma unroll
-    for (int j = 0; j < M::NV; ++j)
-      if (my.vector(j) < p.cols)
-        *reinterpret_cast<uint4 *>(my.plane(w_slot, j)) = *reinterpret_cast<const uint4 *>(w_pre + my.vector(j));
-  float factor[NQ][4], a_pre[NQ][4], a_s[NQ][4];
-#pragma unroll
-  for (int k = 0; k < NQ; ++k)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      factor[k][i] = a_pre[k][i] = a_s[k][i] = 0.f;
-      post[(k * 4 + i) * blockDim.x] = 0.f;
-    }
-  auto gate_row = [&](int item) {
-    return p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
+  // 1 / rms of the next row, read one row ahead
+  float ry = 0.f, ro = 1.f;
+  auto read_rstd = [&](const Walk &w) {
+    if (!w.live()) return;
+    if (p.dh) ry = p.rstd_pre[w.row];
+    if (p.o && p.post_norm) ro = p.rstd_post[w.row];
   };
+  for (char *to = row0; to != row_end; to += row_step) fetch(to);
+  read_rstd(soon);
+  char *row = row0;
+  float factor[NG][2][4], a_pre[NG][2][4], a_s[NG][2][4];
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      post[(2 * g + k) * MAXT] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) factor[g][k][i] = a_pre[g][k][i] = a_s[g][k][i] = 0.f;
+    }
+  auto gate_row = [&](int item) { return p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr; };
   // an item's S goes to dw_post's sums and to the gate's gradient (directly
   // where the item is all of the gate row's rows)
   auto flush = [&](int item) {
@@ -703,142 +746,156 @@ __global__ void __launch_bounds__(NQ == 2 ? 1024 : 512) block_norm_bwd_staged_ke
     const T *gate = gate_row(item);
     Writer<T> out;
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-      const int c = my.quad(k);
-      if (c < p.cols) {
-        float g[4], w[4] = {1.f, 1.f, 1.f, 1.f}, d[4];
-        if (gate) Quad<T>::get(gate + c, g);
-        if (w_post) Quad<T>::get(w_post + c, w);
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float s = p.scale * a_s[k][i];
-          post[(k * 4 + i) * blockDim.x] += gate ? activate(p.act, g[i]) * s : s;
-          d[i] = s * w[i];
-          a_s[k][i] = 0.f;
-        }
-        if (!p.dgate) continue;
-        if (p.split == 1) {
+      for (int k = 0; k < 2; ++k) {
+        const int c = C::quad(g, k);
+        if (c < p.cols) {
+          float gv[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {1.f, 1.f, 1.f, 1.f}, s[4];
+          if (gate) Quad<T>::get(gate + c, gv);
+          if (w_post) Quad<T>::get(w_post + c, w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] *= slope(p.act, g[i]);
-          out.put(k, at<T>(p.dgate, item, p.ld_dg), c, d);
-        } else {
-          float *sums = p.ws + 2 * (int64_t)gridDim.x * p.cols + (int64_t)item * p.cols;
-          *reinterpret_cast<float4 *>(sums + c) = make_float4(d[0], d[1], d[2], d[3]);
+          for (int i = 0; i < 4; ++i) {
+            s[i] = p.scale * a_s[g][k][i];
+            a_s[g][k][i] = 0.f;
+            w[i] *= s[i];
+            if (gate) s[i] *= activate(p.act, gv[i]);
+          }
+          float4 sum = post[(2 * g + k) * MAXT];
+          sum.x += s[0], sum.y += s[1], sum.z += s[2], sum.w += s[3];
+          post[(2 * g + k) * MAXT] = sum;
+          if (!p.dgate) continue;
+          if (p.split == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] *= slope(p.act, gv[i]);
+            out.put(k, at<T>(p.dgate, item, p.ld_dg), c, p.cols, w);
+          } else {
+            float *sums = p.ws + 2 * (int64_t)gridDim.x * p.cols + (int64_t)item * p.cols;
+            *reinterpret_cast<float4 *>(sums + c) = make_float4(w[0], w[1], w[2], w[3]);
+          }
         }
+      }
+  };
+  // a group's values of a row; yn, dx without its mean term and dh of a quad
+  // (s0 += dh w_pre yn)
+  struct Row {
+    Eight<C, T> dy, dh, y, o, w;
+    __device__ __forceinline__ Row(const char *row, const char *fixed, int g)
+        : dy(row + C::place(DY, 0), g), dh(row + C::place(DH, 0), g), y(row + C::place(Y, 0), g),
+          o(row + C::place(O, 0), g), w(fixed, g) {}
+    __device__ __forceinline__ void front(int k, float ry, float (&yn)[4], float (&g0)[4], float (&hv)[4],
+                                          float &s0) const {
+      float wv[4];
+      dy.quad(k, g0);
+      dh.quad(k, hv);
+      y.quad(k, yn);
+      w.quad(k, wv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        yn[i] *= ry;
+        const float t = hv[i] * wv[i];
+        g0[i] += ry * t;
+        s0 += t * yn[i];
       }
     }
   };
-  // yn, dx without its mean term and dh of a quad; s0 += dh w_pre yn
-  auto front = [&](int k, float ry, float (&yn)[4], float (&g0)[4], float (&hv)[4], float &s0) {
-    float w[4] = {1.f, 1.f, 1.f, 1.f};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) yn[i] = g0[i] = hv[i] = 0.f;
-    if (p.dy) Quad<T>::get(my.row_quad(0, k), g0);
-    if (!p.dh) return;
-    Quad<T>::get(my.row_quad(1, k), hv);
-    Quad<T>::get(my.row_quad(2, k), yn);
-    if (w_pre) Quad<T>::get(my.plane_quad(w_slot, k), w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      yn[i] *= ry;
-      const float t = hv[i] * w[i];
-      g0[i] += ry * t;
-      s0 += t * yn[i];
-    }
-  };
+  const float ks = DROP ? p.rnd.keep_scale : 1.f;
   int half = 0, item = -1;
   for (; now.live(); now.next()) {
     const int r = now.row;
-    const float ry = p.dh ? p.rstd_pre[r] : 0.f;
-    const float ro = p.o && p.post_norm ? p.rstd_post[r] : 1.f;
+    const float cy = ry, co = ro;  // this row's
+    soon.next();
+    read_rstd(soon);
     if (now.item != item) {
       flush(item);
       item = now.item;
       const T *gate = gate_row(item);
-      if (p.o && !gate_with_rows)
+      if (!gate_with_rows)
 #pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-          const int c = my.quad(k);
-          if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[k]);
-        }
-    }
-    my.wait();
-    uint32_t kept = 0u;  // bit 4k + i: element i of quad k is kept
-    float s[3] = {0.f, 0.f, 0.f};
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-      const int c = my.quad(k);
-      if (c < p.cols) {
-        if (p.o && gate_with_rows)
-          factor_of<T>(p.scale, p.act, my.row_quad(4, k), w_post ? w_post + c : nullptr, factor[k]);
-        uint32_t word[4] = {~0u, ~0u, ~0u, ~0u};
-        if (p.o && p.drop) random_words(p.rnd, ((uint64_t)r * p.cols + c) >> 2, word);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (word[i] >= p.rnd.threshold) kept |= 1u << (4 * k + i);
-        float yn[4], g0[4], hv[4];
-        front(k, ry, yn, g0, hv, s[0]);
-        if (p.o && p.post_norm) {
-          float ov[4];
-          Quad<T>::get(my.row_quad(3, k), ov);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float q = word[i] >= p.rnd.threshold ? factor[k][i] * ov[i] : 0.f;
-            s[1] += g0[i] * q;
-            s[2] += yn[i] * q;
+          for (int k = 0; k < 2; ++k) {
+            const int c = C::quad(g, k);
+            if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[g][k]);
           }
-        }
-      }
     }
-    group_sums<3>(s, buf, warp, warps, half);
-    const float m1 = ry * s[0] * inv;  // dx = g0 - yn * m1
-    const float ks = p.drop ? p.rnd.keep_scale : 1.f;
-    const float m2 = p.post_norm ? ks * ro * (s[1] - m1 * s[2]) * inv : 0.f;  // mean(dn w_post on)
-    Writer<T> out_x, out_o;
+    wait_oldest(ahead_rows);
+    if (gate_with_rows)
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-      const int c = my.quad(k);
-      if (c < p.cols) {
-        float yn[4], g0[4], hv[4], unused = 0.f;
-        front(k, ry, yn, g0, hv, unused);
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = C::quad(g, k);
+          const char *gate = row + C::place(GATE, g * C::PER + k / (C::W / 4)) + 4 * (k % (C::W / 4)) * (int)sizeof(T);
+          if (c < p.cols) factor_of<T>(p.scale, p.act, gate, w_post ? w_post + c : nullptr, factor[g][k]);
+        }
+    uint32_t kept = 0u;  // bit 8g + 4k + i
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const Row in(row, fixed, g);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t word[4];
+        if (DROP) random_words(p.rnd, ((uint64_t)r * p.cols + C::quad(g, k)) >> 2, word);
+        float yn[4], g0[4], hv[4], ov[4];
+        in.front(k, cy, yn, g0, hv, s[0]);
+        in.o.quad(k, ov);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          a_pre[k][i] += hv[i] * yn[i];
-          g0[i] -= yn[i] * m1;  // dx
-        }
-        if (p.dx) out_x.put(k, at<T>(p.dx, r, p.ld_dx), c, g0);
-        if (p.o) {
-          float ov[4];
-          Quad<T>::get(my.row_quad(3, k), ov);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float on = ov[i] * ro;
-            // a dropped element passes nothing on, whatever its values
-            const float d = (kept >> (4 * k + i)) & 1u ? g0[i] * ks : 0.f;
-            a_s[k][i] += d * on;
-            ov[i] = ro * (d * factor[k][i] - on * m2);
-          }
-          if (p.dout) out_o.put(k, at<T>(p.dout, r, p.ld_do), c, ov);
+          if (DROP && word[i] < p.rnd.threshold) continue;
+          kept |= 1u << (8 * g + 4 * k + i);
+          const float q = factor[g][k][i] * ov[i];
+          s[1] += g0[i] * q;
+          s[2] += yn[i] * q;
         }
       }
     }
-    fetch();
-    my.next();
+    block_sums4(s, buf, warp, warps, half);
+    const float m1 = cy * s[0] * inv;  // dx = g0 - yn * m1
+    // mean(dn w_post on), times on's and do's rstd
+    const float m2 = p.post_norm ? ks * co * co * co * (s[1] - m1 * s[2]) * inv : 0.f;
+    const float kr = ks * co;
+    Writer<T> out_x, out_o;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const Row in(row, fixed, g);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c = C::quad(g, k);
+        float yn[4], g0[4], hv[4], ov[4], unused = 0.f;
+        in.front(k, cy, yn, g0, hv, unused);
+        in.o.quad(k, ov);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a_pre[g][k][i] += hv[i] * yn[i];
+          g0[i] -= yn[i] * m1;  // dx
+          // a dropped element passes nothing on, whatever its values
+          const float d = !DROP || ((kept >> (8 * g + 4 * k + i)) & 1u) ? g0[i] * kr : 0.f;  // drop dx rstd_o
+          a_s[g][k][i] += d * ov[i];
+          ov[i] = d * factor[g][k][i] - ov[i] * m2;
+        }
+        if (p.dx) out_x.put(k, at<T>(p.dx, r, p.ld_dx), c, p.cols, g0);
+        if (p.dout) out_o.put(k, at<T>(p.dout, r, p.ld_do), c, p.cols, ov);
+      }
+    }
+    fetch(row);
+    row = row + row_step == row_end ? row0 : row + row_step;
   }
   flush(item);
 #pragma unroll
-  for (int k = 0; k < NQ; ++k) {
-    const int c = my.quad(k);
-    if (c < p.cols) {
-      if (p.dw_pre)
-        *reinterpret_cast<float4 *>(p.ws + (int64_t)blockIdx.x * p.cols + c) =
-            make_float4(a_pre[k][0], a_pre[k][1], a_pre[k][2], a_pre[k][3]);
-      if (p.dw_post)
-        *reinterpret_cast<float4 *>(p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.cols + c) =
-            make_float4(post[(k * 4) * blockDim.x], post[(k * 4 + 1) * blockDim.x], post[(k * 4 + 2) * blockDim.x],
-                        post[(k * 4 + 3) * blockDim.x]);
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = C::quad(g, k);
+      if (c < p.cols) {
+        const float(&a)[4] = a_pre[g][k];
+        if (p.dw_pre)
+          *reinterpret_cast<float4 *>(p.ws + (int64_t)blockIdx.x * p.cols + c) = make_float4(a[0], a[1], a[2], a[3]);
+        if (p.dw_post)
+          *reinterpret_cast<float4 *>(p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.cols + c) = post[(2 * g + k) * MAXT];
+      }
     }
-  }
 }
 
 // Column sums of the partials: y 0 dw_pre, 1 dw_post, 2 + g the gate rows.
@@ -885,25 +942,50 @@ static int threads_of(int cols, int V, int nv, int most) {
   return t <= most ? t : 0;
 }
 
-// Resident blocks of a staged kernel: 1024 threads an SM at 2 quads, 512 or 768 at 4
-static int staged_per_sm(int threads, int nq) { return std::max(1, (nq == 2 ? 1024 : 512) / threads); }
-static int64_t staged_blocks(int64_t rows, int threads, int nq, int num_sms) {
-  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * staged_per_sm(threads, nq)));
+// A staged block: 8 columns a thread in rows of up to 2048 columns (blocks of up
+// to 64 or 256 threads, which sets the shared memory's layout), 16 beyond.
+struct StagedShape {
+  int groups, max_threads, threads, per_sm;
+};
+static StagedShape staged_shape(int cols) {
+  StagedShape s;
+  s.groups = cols <= 2048 ? 1 : 2;
+  s.max_threads = cols <= 512 ? 64 : cols <= 2048 ? 256 : 512;
+  s.threads = (cols + 256 * s.groups - 1) / (256 * s.groups) * 32;
+  // resident blocks an SM: by their registers, 768 threads of small blocks, else 512
+  s.per_sm = std::max(1, (s.groups == 1 ? 768 : 512) / s.threads);
+  return s;
 }
-// Rows to copy ahead: up to three, as many as leave room for `blocks` blocks an SM
-static int ahead_of(size_t arrays, size_t fixed, size_t vectors, int blocks) {
-  const size_t room = STAGED_SMEM / std::max(1, blocks) / vectors;
-  return room < fixed + 2 * arrays ? 1 : room < fixed + 3 * arrays ? 2 : 3;
+static int64_t staged_blocks(int64_t rows, const StagedShape &s, int num_sms) {
+  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * s.per_sm));
+}
+// f(group count, threads' limit) as types
+template <typename F>
+static auto with_shape(const StagedShape &s, F f) {
+  using std::integral_constant;
+  if (s.max_threads == 64) return f(integral_constant<int, 1>{}, integral_constant<int, 64>{});
+  if (s.max_threads == 256) return f(integral_constant<int, 1>{}, integral_constant<int, 256>{});
+  return f(integral_constant<int, 2>{}, integral_constant<int, 512>{});
+}
+// Launch with rows copied ahead (up to three, as many as leave room for the
+// resident blocks) and, where it fits, the gate copied with them
+template <typename C, typename P>
+static cudaError_t launch_staged(void (*kern)(P, int, int), const P &p, int arrays, size_t fixed, bool gate, int blocks,
+                                 const StagedShape &s, cudaStream_t st) {
+  const int with_rows = gate && fixed + C::row_bytes(arrays + 1) <= STAGED_SMEM;
+  const size_t row = C::row_bytes(arrays + with_rows), room = STAGED_SMEM / s.per_sm;
+  const int ahead = room < fixed + 2 * row ? 1 : room < fixed + 3 * row ? 2 : 3;
+  const size_t bytes = fixed + ahead * row;
+  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (err != cudaSuccess) return err;
+  kern<<<blocks, s.threads, bytes, st>>>(p, with_rows, ahead);
+  return cudaGetLastError();
 }
 // Split of a gate row's rows so that all items together give every block one
 static int64_t split_of(int64_t gates, int64_t per_gate, int64_t blocks) {
   if (gates >= blocks) return 1;
   return std::max<int64_t>(1, std::min<int64_t>(per_gate, blocks / gates));
 }
-// Quads of a thread's columns, and the threads of a staged block
-static int staged_quads(int cols, int quads) { return cols <= 2048 ? 2 : quads; }
-static int staged_threads(int cols, int nq) { return (cols / 4 + 32 * nq - 1) / (32 * nq) * 32; }
-
 template <typename T, int V, int NV>
 static cudaError_t run_fwd(const Fwd &p, int tpr, int num_sms, cudaStream_t st) {
   const int rpb = std::max(1, 128 / tpr);
@@ -915,20 +997,17 @@ template <typename T, int V>
 static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
   if constexpr (V > 1) {
     if (p.cols <= STAGED_COLS) {
-      const int nq = staged_quads(p.cols, FWD_QUADS), threads = staged_threads(p.cols, nq);
-      const int64_t most = staged_blocks(p.rows, threads, nq, num_sms);
+      const StagedShape s = staged_shape(p.cols);
+      const int64_t most = staged_blocks(p.rows, s, num_sms);
       p.split = (int)split_of(p.gates, p.per_gate, most);
       p.per_item = (p.per_gate + p.split - 1) / p.split;
       const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split);
-      const int with_rows = p.gate && p.per_gate <= GATE_WITH_ROWS;
-      const size_t vectors = 4 * nq * sizeof(T) * threads;  // a row's bytes of one array
-      const int ahead = ahead_of(2 + with_rows, 1, vectors, staged_per_sm(threads, nq));
-      const size_t smem = ((size_t)ahead * (2 + with_rows) + 1) * vectors;
-      auto kern = nq == 2 ? block_norm_staged_kernel<T, 2> : block_norm_staged_kernel<T, FWD_QUADS>;
-      const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (err != cudaSuccess) return err;
-      kern<<<blocks, threads, smem, st>>>(p, with_rows, ahead);
-      return cudaGetLastError();
+      return with_shape(s, [&](auto groups, auto threads) {
+        using C = Columns<T, decltype(groups)::value, decltype(threads)::value>;
+        return launch_staged<C, Fwd>(p.drop ? block_norm_staged_kernel<T, true, C::NG, C::MAXT>
+                                            : block_norm_staged_kernel<T, false, C::NG, C::MAXT>,
+                                     p, 2, C::row_bytes(1), p.gate && p.per_gate <= GATE_WITH_ROWS, blocks, s, st);
+      });
     }
     if (const int t = threads_of(p.cols, V, 2, 1024)) return run_fwd<T, V, 2>(p, t, num_sms, st);
   } else {
@@ -942,13 +1021,13 @@ static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
 // The backward's launch: threads and blocks for rows in vectors of V
 struct BwdPlan {
   bool staged;
-  int threads, nv;  // a thread's quads, or the plain kernel's vectors in registers (0: none)
+  int threads, nv;  // nv: the plain kernel's vectors in registers (0: none)
   int64_t blocks;
 };
 static BwdPlan plan_bwd(int64_t rows, int cols, int V, int num_sms) {
   if (V > 1 && cols <= STAGED_COLS) {
-    const int nq = staged_quads(cols, BWD_QUADS), t = staged_threads(cols, nq);
-    return BwdPlan{true, t, nq, staged_blocks(rows, t, nq, num_sms)};
+    const StagedShape s = staged_shape(cols);
+    return BwdPlan{true, s.threads, 0, staged_blocks(rows, s, num_sms)};
   }
   const int n = V == 1 ? 8 : 0;
   const int t = n ? threads_of(cols, V, n, 512) : 0;
@@ -966,15 +1045,15 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
   cudaError_t err = cudaSuccess;
   if constexpr (V > 1) {
     if (plan.staged) {
-      const int with_rows = p.gate && p.per_gate <= GATE_WITH_ROWS;
-      const size_t vectors = 4 * plan.nv * sizeof(T) * plan.threads;
-      const size_t sums = sizeof(float) / sizeof(T);  // dw_post's sums, in rows
-      const int ahead = ahead_of(4 + with_rows, 1 + sums, vectors, staged_per_sm(plan.threads, plan.nv));
-      const size_t smem = ((size_t)ahead * (4 + with_rows) + 1 + sums) * vectors;
-      auto kern = plan.nv == 2 ? block_norm_bwd_staged_kernel<T, 2> : block_norm_bwd_staged_kernel<T, BWD_QUADS>;
-      err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      const StagedShape s = staged_shape(p.cols);
+      err = with_shape(s, [&](auto groups, auto threads) {
+        using C = Columns<T, decltype(groups)::value, decltype(threads)::value>;
+        return launch_staged<C, Bwd>(p.drop ? block_norm_bwd_staged_kernel<T, true, C::NG, C::MAXT>
+                                            : block_norm_bwd_staged_kernel<T, false, C::NG, C::MAXT>,
+                                     p, 4, C::row_bytes(1) + 2 * C::NG * C::MAXT * 16,
+                                     p.gate && p.per_gate <= GATE_WITH_ROWS, blocks, s, st);
+      });
       if (err != cudaSuccess) return err;
-      kern<<<blocks, plan.threads, smem, st>>>(p, with_rows, ahead);
     } else {
       block_norm_bwd_kernel<T, V, 0><<<blocks, plan.threads, 0, st>>>(p);
     }

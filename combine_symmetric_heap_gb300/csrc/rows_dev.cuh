@@ -249,5 +249,37 @@ __device__ __forceinline__ void group_sums(float (&v)[K], float *buf, int warp, 
   warp_sums<K>(v);
 }
 
+// Four sums at once for a block of one row.  Inside a warp the lanes trade
+// values for halves of the lanes first (6 shuffles instead of 20), so that lane
+// 8k ends with sum k; then every warp adds the warps' sums.  buf: 2 * 128
+// floats, its halves used in turn.
+__device__ __forceinline__ void block_sums4(float (&v)[4], float *buf, int warp, int warps, int &turn) {
+  const int lane = threadIdx.x & 31;
+  const bool h16 = lane & 16, h8 = lane & 8;
+  float a = h16 ? v[2] : v[0], b = h16 ? v[3] : v[1];
+  a += __shfl_xor_sync(0xffffffffu, h16 ? v[0] : v[2], 16);
+  b += __shfl_xor_sync(0xffffffffu, h16 ? v[1] : v[3], 16);
+  float s = h8 ? b : a;
+  s += __shfl_xor_sync(0xffffffffu, h8 ? a : b, 8);
+#pragma unroll
+  for (int i = 4; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+  if (warps == 1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(0xffffffffu, s, 8 * k);
+    return;
+  }
+  float *p = buf + turn * 128;
+  turn ^= 1;
+  if ((lane & 7) == 0) p[warp * 4 + (lane >> 3)] = s;
+  __syncthreads();
+  // lane l: sum l mod 4 of warps l / 4, l / 4 + 8, ...
+  s = 0.f;
+  for (int w = lane >> 2; w < warps; w += 8) s += p[w * 4 + (lane & 3)];
+#pragma unroll
+  for (int i = 16; i > 2; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(0xffffffffu, s, k);
+}
+
 }  // namespace rows
 }  // namespace symmoe
