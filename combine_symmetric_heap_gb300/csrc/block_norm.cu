@@ -89,7 +89,7 @@ __device__ __forceinline__ float slope(int act, float g) {
 // The stream after the block for V columns of a row: x + scale * drop(gate * n)
 template <typename T, int V>
 __device__ __forceinline__ void stream_after(const Fwd &p, const T *x, const float (&ov)[V], float rstd, const T *gate,
-                                             int64_t row, int c, float (&yv)[V]) {
+                                             int64_t row, int c, const uint8_t *mask, float (&yv)[V]) {
   float f[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) f[i] = ov[i] * rstd;
@@ -106,10 +106,14 @@ __device__ __forceinline__ void stream_after(const Fwd &p, const T *x, const flo
     for (int i = 0; i < V; ++i) f[i] *= activate(p.act, g[i]);
   }
   if (p.drop) {
-    float k[V];
-    keep_factors<V>(p.rnd, (uint64_t)row * p.cols + c, k);
+    if (V == 1) {
+      f[0] = mask[c] ? f[0] * p.rnd.keep_scale : 0.f;
+    } else {
+      float k[V];
+      keep_factors<V>(p.rnd, (uint64_t)row * p.cols + c, k);
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = k[i] != 0.f ? f[i] * k[i] : 0.f;
+      for (int i = 0; i < V; ++i) f[i] = k[i] != 0.f ? f[i] * k[i] : 0.f;
+    }
   }
   load<T, V>(x + c, yv);
 #pragma unroll
@@ -124,6 +128,8 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const Fwd p) {
   extern __shared__ float buf[];
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
   float *mine = buf + threadIdx.y * 64;
+  // V = 1: which elements of the row are kept
+  uint8_t *mask = reinterpret_cast<uint8_t *>(buf + blockDim.y * 64) + threadIdx.y * p.cols;
   int turn = 0;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const float inv = 1.f / p.cols;
@@ -138,6 +144,11 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const Fwd p) {
     T *h = p.h ? reinterpret_cast<T *>(p.h) + r * p.ldh : nullptr;
     constexpr int N = NV ? NV : 1;
     float yv[N][V];
+    if (V == 1 && p.drop) {
+      __syncthreads();  // the last row's mask has been read
+      fill_mask(p.rnd, (uint64_t)r * p.cols, p.cols, mask, threadIdx.x, blockDim.x);
+      __syncthreads();
+    }
     float rstd_o = 1.f;
     if (o && p.post_norm) {
       float s[1] = {0.f};
@@ -166,11 +177,11 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const Fwd p) {
     // V columns of y from c on, o's values in ov where the row is in registers
     auto stream = [&](int c, const float(&ov)[V], float(&out)[V]) {
       if (!o) load<T, V>(x + c, out);
-      else if (NV && p.post_norm) stream_after<T, V>(p, x, ov, rstd_o, gate, r, c, out);
+      else if (NV && p.post_norm) stream_after<T, V>(p, x, ov, rstd_o, gate, r, c, mask, out);
       else {
         float fresh[V];
         load<T, V>(o + c, fresh);
-        stream_after<T, V>(p, x, fresh, rstd_o, gate, r, c, out);
+        stream_after<T, V>(p, x, fresh, rstd_o, gate, r, c, mask, out);
       }
     };
     float s[1] = {0.f};
@@ -240,6 +251,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const Fwd p) {
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
   __shared__ float buf[2 * 32 * 3];
+  extern __shared__ uint8_t mask[];  // V = 1: which elements of the row are kept
   constexpr int N = NV ? NV : 1;
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
   const int items = p.gates * p.split;
@@ -296,6 +308,11 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
       const T *o = p.o ? reinterpret_cast<const T *>(p.o) + r * p.ldo : nullptr;
       const float ry = p.dh ? p.rstd_pre[r] : 0.f;
       const float ro = p.o && p.post_norm ? p.rstd_post[r] : 1.f;
+      if (V == 1 && p.drop) {
+        __syncthreads();  // the last row's mask has been read
+        fill_mask(p.rnd, (uint64_t)r * p.cols, p.cols, mask, threadIdx.x, blockDim.x);
+        __syncthreads();
+      }
       // per column: yn, dx without its mean term (g0), on, the factor m * act
       // from dx to dn, and m alone (for the gate's gradient)
       auto columns = [&](int c, float(&yn)[V], float(&g0)[V], float(&hv)[V], float(&on)[V], float(&fa)[V],
@@ -325,7 +342,8 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
           }
           if (p.drop) {
             float k[V];
-            keep_factors<V>(p.rnd, (uint64_t)r * p.cols + c, k);
+            if (V == 1) k[0] = mask[c] ? p.rnd.keep_scale : 0.f;
+            else keep_factors<V>(p.rnd, (uint64_t)r * p.cols + c, k);
 #pragma unroll
             for (int i = 0; i < V; ++i) fm[i] *= k[i];
           }
@@ -890,10 +908,16 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p
       const int c = C::quad(g, k);
       if (c < p.cols) {
         const float(&a)[4] = a_pre[g][k];
+        const float4 sum = post[(2 * g + k) * MAXT];
+        if (gridDim.x == 1) {  // the sums are whole: no launch to add partials
+          const float b[4] = {sum.x, sum.y, sum.z, sum.w};
+          if (p.dw_pre) *reinterpret_cast<typename Quad<T>::Word *>(reinterpret_cast<T *>(p.dw_pre) + c) = Quad<T>::put(a);
+          if (p.dw_post) *reinterpret_cast<typename Quad<T>::Word *>(reinterpret_cast<T *>(p.dw_post) + c) = Quad<T>::put(b);
+          continue;
+        }
         if (p.dw_pre)
           *reinterpret_cast<float4 *>(p.ws + (int64_t)blockIdx.x * p.cols + c) = make_float4(a[0], a[1], a[2], a[3]);
-        if (p.dw_post)
-          *reinterpret_cast<float4 *>(p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.cols + c) = post[(2 * g + k) * MAXT];
+        if (p.dw_post) *reinterpret_cast<float4 *>(p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.cols + c) = sum;
       }
     }
 }
@@ -990,7 +1014,11 @@ template <typename T, int V, int NV>
 static cudaError_t run_fwd(const Fwd &p, int tpr, int num_sms, cudaStream_t st) {
   const int rpb = std::max(1, 128 / tpr);
   const int64_t blocks = std::min<int64_t>((p.rows + rpb - 1) / rpb, (int64_t)num_sms * 64);
-  block_norm_kernel<T, V, NV><<<(unsigned)blocks, dim3(tpr, rpb), rpb * 64 * sizeof(float), st>>>(p);
+  auto kern = block_norm_kernel<T, V, NV>;
+  const size_t smem = rpb * (64 * sizeof(float) + (V == 1 && p.drop ? p.cols : 0));
+  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  kern<<<(unsigned)blocks, dim3(tpr, rpb), smem, st>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int V>
@@ -1058,13 +1086,16 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
       block_norm_bwd_kernel<T, V, 0><<<blocks, plan.threads, 0, st>>>(p);
     }
   } else {
-    if (plan.nv) block_norm_bwd_kernel<T, 1, 8><<<blocks, plan.threads, 0, st>>>(p);
-    else block_norm_bwd_kernel<T, 1, 0><<<blocks, plan.threads, 0, st>>>(p);
+    auto kern = plan.nv ? block_norm_bwd_kernel<T, 1, 8> : block_norm_bwd_kernel<T, 1, 0>;
+    const size_t smem = p.drop ? p.cols : 0;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    kern<<<blocks, plan.threads, smem, st>>>(p);
   }
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   const bool gates = p.dgate && p.split > 1;
-  if (p.dw_pre || p.dw_post || gates)
+  if (!(plan.staged && blocks == 1) && (p.dw_pre || p.dw_post || gates))
     err = launch_pdl(sum_partials_kernel<T>, dim3((p.cols + 31) / 32, 2 + (gates ? p.gates : 0)), dim3(256), 0, st, p,
                      blocks);
   return err;
@@ -1131,7 +1162,8 @@ cudaError_t launch_block_norm_bwd(const sym_block_norm &a, const sym_block_norm_
   p.scale = a.scale, p.drop = a.p > 0;
   p.rnd = make_random(a.seed, a.offset, a.p);
   const int64_t es = a.dtype == SYM_FP32 ? 4 : 2;
-  const bool vec = vec_ok({p.dy, p.dh, p.dh ? p.y : nullptr, p.o, p.w_post, p.w_pre, p.gate, p.dx, p.dout, p.dgate},
+  const bool vec = vec_ok({p.dy, p.dh, p.dh ? p.y : nullptr, p.o, p.w_post, p.w_pre, p.gate, p.dx, p.dout, p.dgate, p.dw_pre,
+                           p.dw_post},
                           {p.dy ? p.ld_dy : 0, p.dh ? p.ld_dh : 0, p.dh ? p.ldy : 0, p.o ? p.ldo : 0,
                            p.gate ? p.ldg : 0, p.dx ? p.ld_dx : 0, p.dout ? p.ld_do : 0, p.dgate ? p.ld_dg : 0},
                           p.cols, es);

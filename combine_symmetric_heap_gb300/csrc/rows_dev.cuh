@@ -221,6 +221,22 @@ __device__ __forceinline__ void keep_factors(const Random &r, uint64_t at, float
   }
 }
 
+// Which of the n elements from element `first` on are kept, one byte each: for
+// rows walked element by element, where every block of words would otherwise be
+// made four times
+__device__ __forceinline__ void fill_mask(const Random &r, uint64_t first, int n, uint8_t *mask, int thread,
+                                          int threads) {
+  for (uint64_t b = (first >> 2) + thread; 4 * b < first + n; b += threads) {
+    uint32_t word[4];
+    random_words(r, b, word);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t i = (int64_t)(4 * b + j - first);
+      if (i >= 0 && i < n) mask[i] = word[j] >= r.threshold;
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Sums of K values over the `warps` warps of a row group; every thread gets
 // the totals, added in a fixed order.  buf holds 2 * 32 * K floats per group;
