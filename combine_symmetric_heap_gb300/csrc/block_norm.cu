@@ -86,64 +86,23 @@ __device__ __forceinline__ float slope(int act, float g) {
   return 1.f;
 }
 
-// The stream after the block for V columns of a row: x + scale * drop(gate * n)
+// Forward for rows of any length: the row is walked once for each sum and once
+// to write (out of L2 after the first time).  V = 1: single elements, the row's
+// dropout mask made once into shared memory.
 template <typename T, int V>
-__device__ __forceinline__ void stream_after(const Fwd &p, const T *x, const float (&ov)[V], float rstd, const T *gate,
-                                             int64_t row, int c, const uint8_t *mask, float (&yv)[V]) {
-  float f[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = ov[i] * rstd;
-  if (p.w_post) {
-    float w[V];
-    load<T, V>(reinterpret_cast<const T *>(p.w_post) + c, w);
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] *= w[i];
-  }
-  if (gate) {
-    float g[V];
-    load<T, V>(gate + c, g);
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] *= activate(p.act, g[i]);
-  }
-  if (p.drop) {
-    if (V == 1) {
-      f[0] = mask[c] ? f[0] * p.rnd.keep_scale : 0.f;
-    } else {
-      float k[V];
-      keep_factors<V>(p.rnd, (uint64_t)row * p.cols + c, k);
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = k[i] != 0.f ? f[i] * k[i] : 0.f;
-    }
-  }
-  load<T, V>(x + c, yv);
-#pragma unroll
-  for (int i = 0; i < V; ++i) yv[i] += p.scale * f[i];
-}
-
-// Forward.  NV > 0: a thread keeps its NV vectors of the row in registers;
-// NV = 0: any row length, the row is walked once per sum and once to write.
-// blockDim (threads of a row, rows of a block).
-template <typename T, int V, int NV>
 __global__ void __launch_bounds__(1024) block_norm_kernel(const Fwd p) {
-  extern __shared__ float buf[];
+  extern __shared__ uint8_t mask[];
+  __shared__ float buf[64];
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
-  float *mine = buf + threadIdx.y * 64;
-  // V = 1: which elements of the row are kept
-  uint8_t *mask = reinterpret_cast<uint8_t *>(buf + blockDim.y * 64) + threadIdx.y * p.cols;
-  int turn = 0;
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const float inv = 1.f / p.cols;
-  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.rows; r0 += step) {
-    const int64_t want = r0 + threadIdx.y;
-    const bool live = want < p.rows;
-    const int64_t r = live ? want : p.rows - 1;  // idle row groups follow along without writing
-    const T *x = reinterpret_cast<const T *>(p.x) + r * p.ldx;
-    const T *o = p.o ? reinterpret_cast<const T *>(p.o) + r * p.ldo : nullptr;
-    const T *gate = p.gate ? reinterpret_cast<const T *>(p.gate) + (r / p.per_gate) * p.ldg : nullptr;
-    T *y = p.y ? reinterpret_cast<T *>(p.y) + r * p.ldy : nullptr;
-    T *h = p.h ? reinterpret_cast<T *>(p.h) + r * p.ldh : nullptr;
-    constexpr int N = NV ? NV : 1;
-    float yv[N][V];
+  int turn = 0;
+  auto each = [&](auto &&f) {  // f(c) for this thread's vectors
+    for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) f(c);
+  };
+  for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    const T *x = at<T>(p.x, r, p.ldx), *o = p.o ? at<T>(p.o, r, p.ldo) : nullptr;
+    const T *gate = p.gate ? at<T>(p.gate, r / p.per_gate, p.ldg) : nullptr;
+    const T *w_post = reinterpret_cast<const T *>(p.w_post), *w_pre = reinterpret_cast<const T *>(p.w_pre);
     if (V == 1 && p.drop) {
       __syncthreads();  // the last row's mask has been read
       fill_mask(p.rnd, (uint64_t)r * p.cols, p.cols, mask, threadIdx.x, blockDim.x);
@@ -152,107 +111,77 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const Fwd p) {
     float rstd_o = 1.f;
     if (o && p.post_norm) {
       float s[1] = {0.f};
-      if (NV) {
+      each([&](int c) {
+        float v[V];
+        load<T, V>(o + c, v);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-          if (c < p.cols) {
-            load<T, V>(o + c, yv[j]);
-#pragma unroll
-            for (int i = 0; i < V; ++i) s[0] += yv[j][i] * yv[j][i];
-          }
-        }
-      } else {
-        for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
-          float ov[V];
-          load<T, V>(o + c, ov);
-#pragma unroll
-          for (int i = 0; i < V; ++i) s[0] += ov[i] * ov[i];
-        }
-      }
-      group_sums<1>(s, mine, warp, warps, turn);
+        for (int i = 0; i < V; ++i) s[0] += v[i] * v[i];
+      });
+      group_sums<1>(s, buf, warp, warps, turn);
       rstd_o = rsqrtf(s[0] * inv + p.eps);
-      if (live && threadIdx.x == 0 && p.rstd_post) p.rstd_post[r] = rstd_o;
+      if (threadIdx.x == 0 && p.rstd_post) p.rstd_post[r] = rstd_o;
     }
-    // V columns of y from c on, o's values in ov where the row is in registers
-    auto stream = [&](int c, const float(&ov)[V], float(&out)[V]) {
-      if (!o) load<T, V>(x + c, out);
-      else if (NV && p.post_norm) stream_after<T, V>(p, x, ov, rstd_o, gate, r, c, mask, out);
-      else {
-        float fresh[V];
-        load<T, V>(o + c, fresh);
-        stream_after<T, V>(p, x, fresh, rstd_o, gate, r, c, mask, out);
+    // y = x + scale * drop(act(gate) * n) for V columns
+    auto stream = [&](int c, float(&y)[V]) {
+      load<T, V>(x + c, y);
+      if (!o) return;
+      float f[V], t[V];
+      load<T, V>(o + c, f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] *= rstd_o * p.scale;
+      if (w_post) {
+        load<T, V>(w_post + c, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] *= t[i];
       }
+      if (gate) {
+        load<T, V>(gate + c, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] *= activate(p.act, t[i]);
+      }
+      if (p.drop) {
+        if (V == 1) t[0] = mask[c] ? p.rnd.keep_scale : 0.f;
+        else keep_factors<V>(p.rnd, (uint64_t)r * p.cols + c, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = t[i] != 0.f ? f[i] * t[i] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[i] += f[i];
     };
-    float s[1] = {0.f};
-    if (NV) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-        if (c < p.cols) {
-          float t[V];
-          stream(c, yv[j], t);
-          if (y && live) store<T, V>(y + c, t);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            yv[j][i] = t[i];
-            s[0] += t[i] * t[i];
-          }
-        }
-      }
-    } else if (h || p.rstd_pre) {
-      for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
-        float t[V];
-        stream(c, t, t);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[0] += t[i] * t[i];
-      }
-    }
     float rstd_y = 0.f;
-    if (h || p.rstd_pre) {
-      group_sums<1>(s, mine, warp, warps, turn);
+    if (p.h || p.rstd_pre) {
+      float s[1] = {0.f};
+      each([&](int c) {
+        float v[V];
+        stream(c, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[0] += v[i] * v[i];
+      });
+      group_sums<1>(s, buf, warp, warps, turn);
       rstd_y = rsqrtf(s[0] * inv + p.eps);
-      if (live && threadIdx.x == 0 && p.rstd_pre) p.rstd_pre[r] = rstd_y;
+      if (threadIdx.x == 0 && p.rstd_pre) p.rstd_pre[r] = rstd_y;
     }
-    auto finish = [&](int c, float(&t)[V]) {
-      if (!h || !live) return;
-      if (p.w_pre) {
-        float w[V];
-        load<T, V>(reinterpret_cast<const T *>(p.w_pre) + c, w);
+    each([&](int c) {  // each column is read before it is written: y may be x
+      float v[V], w[V];
+      stream(c, v);
+      if (p.y) store<T, V>(at<T>(p.y, r, p.ldy) + c, v);
+      if (!p.h) return;
+      if (w_pre) load<T, V>(w_pre + c, w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) t[i] = t[i] * rstd_y * w[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) t[i] *= rstd_y;
-      }
-      store<T, V>(h + c, t);
-    };
-    if (NV) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-        if (c < p.cols) finish(c, yv[j]);
-      }
-    } else {
-      for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
-        float t[V];
-        stream(c, t, t);  // each column is read before it is written: y may be x
-        if (y && live) store<T, V>(y + c, t);
-        finish(c, t);
-      }
-    }
+      for (int i = 0; i < V; ++i) v[i] *= w_pre ? rstd_y * w[i] : rstd_y;
+      store<T, V>(at<T>(p.h, r, p.ldh) + c, v);
+    });
   }
 }
 
-// Backward.  A block takes work items (a run of rows that share a gate row),
-// one row at a time; the column sums stay in registers over its rows (NV > 0)
-// or in the block's partial sums in the workspace (NV = 0), and are joined by
-// sum_partials_kernel in a fixed order.
-template <typename T, int V, int NV>
+// Backward for rows of any length: a block takes work items (a run of rows that
+// share a gate row), one row at a time, walking it once for the sums and once
+// for the results; the column sums live in the block's partial sums in the
+// workspace and are joined by sum_partials_kernel in a fixed order.
+template <typename T, int V>
 __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
   __shared__ float buf[2 * 32 * 3];
   extern __shared__ uint8_t mask[];  // V = 1: which elements of the row are kept
-  constexpr int N = NV ? NV : 1;
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
   const int items = p.gates * p.split;
   const float inv = 1.f / p.cols;
@@ -261,29 +190,15 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
   float *ws_pre = p.ws + (int64_t)blockIdx.x * p.cols;
   float *ws_post = p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.cols;
   float *ws_gate = p.ws + 2 * (int64_t)gridDim.x * p.cols;
-  float a_pre[N][V], a_post[N][V], a_gate[N][V];
-#pragma unroll
-  for (int j = 0; j < N; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i) a_pre[j][i] = a_post[j][i] = 0.f;
   const T *w_pre = reinterpret_cast<const T *>(p.w_pre), *w_post = reinterpret_cast<const T *>(p.w_post);
 
-  auto each = [&](auto &&f) {  // f(j, c) for this thread's vectors
-    if (NV) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-        if (c < p.cols) f(j, c);
-      }
-    } else {
-      for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) f(0, c);
-    }
+  auto each = [&](auto &&f) {  // f(c) for this thread's vectors
+    for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) f(c);
   };
-  if (!NV)
-    each([&](int, int c) {
+  each([&](int c) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) ws_pre[c + i] = ws_post[c + i] = 0.f;
-    });
+    for (int i = 0; i < V; ++i) ws_pre[c + i] = ws_post[c + i] = 0.f;
+  });
 
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t gi = item / p.split, first = gi * p.per_gate;
@@ -291,12 +206,8 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
     const int64_t end = min(begin + p.per_item, first + p.per_gate);
     const T *gate = p.gate ? reinterpret_cast<const T *>(p.gate) + gi * p.ldg : nullptr;
     float *gate_sum = ws_gate + (int64_t)item * p.cols;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) a_gate[j][i] = 0.f;
-    if (!NV && p.dgate)
-      each([&](int, int c) {
+    if (p.dgate)
+      each([&](int c) {
 #pragma unroll
         for (int i = 0; i < V; ++i) gate_sum[c + i] = 0.f;
       });
@@ -365,7 +276,7 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
       };
       // sums over the row: dh w_pre yn;  g0 q;  yn q  with q = m act w_post on
       float s[3] = {0.f, 0.f, 0.f};
-      each([&](int, int c) {
+      each([&](int c) {
         float yn[V], g0[V], hv[V], on[V], fa[V], fm[V], w[V];
         columns(c, yn, g0, hv, on, fa, fm);
         post_weight(c, w);
@@ -384,7 +295,7 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
       group_sums<3>(s, buf, warp, warps, turn);
       const float m1 = ry * s[0] * inv;                                  // dx = g0 - yn * m1
       const float m2 = p.post_norm ? (s[1] - m1 * s[2]) * inv : 0.f;     // mean(dn w_post on)
-      each([&](int j, int c) {
+      each([&](int c) {
         float yn[V], g0[V], hv[V], on[V], fa[V], fm[V], w[V];
         columns(c, yn, g0, hv, on, fa, fm);
         post_weight(c, w);
@@ -405,43 +316,26 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
         if (p.dout) store<T, V>(reinterpret_cast<T *>(p.dout) + r * p.ld_do + c, dov);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if (NV) {
-            a_pre[j][i] += hv[i];
-            a_post[j][i] += fa[i];
-            a_gate[j][i] += fm[i];
-          } else {
-            ws_pre[c + i] += hv[i];
-            ws_post[c + i] += fa[i];
-            if (p.dgate) gate_sum[c + i] += fm[i];
-          }
+          ws_pre[c + i] += hv[i];
+          ws_post[c + i] += fa[i];
+          if (p.dgate) gate_sum[c + i] += fm[i];
         }
       });
     }
     if (p.dgate)
-      each([&](int j, int c) {
+      each([&](int c) {
         float t[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) t[i] = NV ? a_gate[j][i] : gate_sum[c + i];
+        for (int i = 0; i < V; ++i) t[i] = gate_sum[c + i];
         if (p.split == 1) {  // this block saw all rows of the gate row
           float g[V];
           load<T, V>(gate + c, g);
 #pragma unroll
           for (int i = 0; i < V; ++i) t[i] *= slope(p.act, g[i]);
           store<T, V>(reinterpret_cast<T *>(p.dgate) + gi * p.ld_dg + c, t);
-        } else if (NV) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) gate_sum[c + i] = t[i];
         }
       });
   }
-  if (NV)
-    each([&](int j, int c) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (p.dw_pre) ws_pre[c + i] = a_pre[j][i];
-        if (p.dw_post) ws_post[c + i] = a_post[j][i];
-      }
-    });
 }
 
 // ---------------------------------------------------------------------------
@@ -470,13 +364,10 @@ struct Walk {
       : per_gate(per_gate_), per_item(per_item_), item(blockIdx.x), items(gates * split_), split(split_) {
     open();
   }
-  __device__ void open() {  // the item's rows; items without rows are passed over
-    for (; item < items; item += gridDim.x) {
-      const int g = item / split, first = g * per_gate;
-      row = first + (item - g * split) * per_item;
-      end = min(row + per_item, first + per_gate);
-      if (row < end) return;
-    }
+  __device__ void open() {  // the item's rows (every item has some)
+    const int g = item / split, first = g * per_gate;
+    row = first + (item - g * split) * per_item;
+    end = min(row + per_item, first + per_gate);
   }
   __device__ bool live() const { return item < items; }
   __device__ void next() {
@@ -922,6 +813,228 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p
     }
 }
 
+// ---------------------------------------------------------------------------
+// Rows that start off a 16-byte boundary (odd lengths, sliced tensors): the
+// staged kernels' work with NE single elements a thread, a block's width apart.
+// The next row's elements are loaded into registers while a row is worked on,
+// and its dropout mask is made, once a block of words, into shared memory: by
+// the time it is read the row's reduction has been a barrier.  Up to NE * 512
+// columns.
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float single_factor(float scale, int act, const T *gate, const T *w_post, int c) {
+  float f = scale;
+  if (gate) f *= activate(act, Elem<T>::get(gate[c]));
+  if (w_post) f *= Elem<T>::get(w_post[c]);
+  return f;
+}
+
+template <typename T, int NE>
+__global__ void __launch_bounds__(512) block_norm_odd_kernel(const Fwd p) {
+  extern __shared__ uint8_t masks[];  // [2][cols]
+  __shared__ float buf[2 * 128];
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  const float inv = 1.f / p.cols;
+  const T *w_pre = reinterpret_cast<const T *>(p.w_pre), *w_post = reinterpret_cast<const T *>(p.w_post);
+  auto col = [&](int e) { return (int)threadIdx.x + e * (int)blockDim.x; };
+  float w[NE], factor[NE];
+  T nx[NE], no[NE];  // the next row's elements, as they lie
+#pragma unroll
+  for (int e = 0; e < NE; ++e) {
+    w[e] = w_pre && col(e) < p.cols ? Elem<T>::get(w_pre[col(e)]) : 1.f;
+    factor[e] = 0.f;
+    nx[e] = no[e] = Elem<T>::put(0.f);
+  }
+  Walk now(p.per_gate, p.per_item, p.gates, p.split), soon = now;
+  auto read = [&]() {
+    if (!soon.live()) return;
+    const T *px = at<T>(p.x, soon.row, p.ldx), *po = p.o ? at<T>(p.o, soon.row, p.ldo) : nullptr;
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+      if (col(e) < p.cols) {
+        nx[e] = px[col(e)];
+        if (po) no[e] = po[col(e)];
+      }
+  };
+  auto mask_of = [&](int side) {
+    if (p.drop && soon.live())
+      fill_mask(p.rnd, (uint64_t)soon.row * p.cols, p.cols, masks + side * p.cols, threadIdx.x, blockDim.x);
+  };
+  read();
+  mask_of(0);
+  if (p.drop) __syncthreads();
+  int half = 0, item = -1, side = 0;
+  for (; now.live(); now.next()) {
+    const int r = now.row;
+    if (now.item != item) {
+      item = now.item;
+      const T *gate = p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+        if (col(e) < p.cols) factor[e] = single_factor(p.scale, p.act, gate, w_post, col(e));
+    }
+    float y[NE], q[NE], s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      const bool keep = !p.drop || (col(e) < p.cols && masks[side * p.cols + col(e)]);
+      const float o = Elem<T>::get(no[e]);
+      y[e] = Elem<T>::get(nx[e]);
+      q[e] = keep ? o * factor[e] : 0.f;
+      s[0] += o * o;
+      s[1] += y[e] * y[e];
+      s[2] += y[e] * q[e];
+      s[3] += q[e] * q[e];
+    }
+    soon.next();
+    read();
+    side ^= 1;
+    mask_of(side);
+    block_sums4(s, buf, warp, warps, half);
+    if (warps == 1) __syncwarp();
+    const float rstd_o = p.post_norm ? rsqrtf(s[0] * inv + p.eps) : 1.f;
+    const float f = p.drop ? rstd_o * p.rnd.keep_scale : rstd_o;
+    float yy = s[1] + f * (2.f * s[2] + f * s[3]);
+#pragma unroll
+    for (int e = 0; e < NE; ++e) y[e] += f * q[e];
+    if (!(yy >= 0.1f * (s[1] + f * f * s[3]))) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < NE; ++e) t[0] += y[e] * y[e];
+      block_sums4(t, buf, warp, warps, half);
+      yy = t[0];
+    }
+    const float rstd_y = rsqrtf(yy * inv + p.eps);
+    if (threadIdx.x == 0) {
+      if (p.rstd_post) p.rstd_post[r] = rstd_o;
+      if (p.rstd_pre) p.rstd_pre[r] = rstd_y;
+    }
+    T *py = p.y ? at<T>(p.y, r, p.ldy) : nullptr, *ph = p.h ? at<T>(p.h, r, p.ldh) : nullptr;
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+      if (col(e) < p.cols) {
+        if (py) py[col(e)] = Elem<T>::put(y[e]);
+        if (ph) ph[col(e)] = Elem<T>::put(y[e] * rstd_y * w[e]);
+      }
+  }
+}
+
+template <typename T, int NE>
+__global__ void __launch_bounds__(512) block_norm_bwd_odd_kernel(const Bwd p) {
+  extern __shared__ uint8_t masks[];  // [2][cols]
+  __shared__ float buf[2 * 128];
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  const float inv = 1.f / p.cols;
+  const T *w_pre = reinterpret_cast<const T *>(p.w_pre), *w_post = reinterpret_cast<const T *>(p.w_post);
+  auto col = [&](int e) { return (int)threadIdx.x + e * (int)blockDim.x; };
+  float w[NE], factor[NE], a_pre[NE], a_s[NE], a_post[NE];
+  T ndy[NE], ndh[NE], ny[NE], no[NE];  // the next row's elements, as they lie
+#pragma unroll
+  for (int e = 0; e < NE; ++e) {
+    w[e] = w_pre && col(e) < p.cols ? Elem<T>::get(w_pre[col(e)]) : 1.f;
+    factor[e] = a_pre[e] = a_s[e] = a_post[e] = 0.f;
+    ndy[e] = ndh[e] = ny[e] = no[e] = Elem<T>::put(0.f);
+  }
+  Walk now(p.per_gate, p.per_item, p.gates, p.split), soon = now;
+  float ry = 0.f, ro = 1.f;
+  auto read = [&]() {
+    if (!soon.live()) return;
+    const int r = soon.row;
+    if (p.dh) ry = p.rstd_pre[r];
+    if (p.o && p.post_norm) ro = p.rstd_post[r];
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+      if (col(e) < p.cols) {
+        if (p.dy) ndy[e] = at<T>(p.dy, r, p.ld_dy)[col(e)];
+        if (p.dh) {
+          ndh[e] = at<T>(p.dh, r, p.ld_dh)[col(e)];
+          ny[e] = at<T>(p.y, r, p.ldy)[col(e)];
+        }
+        if (p.o) no[e] = at<T>(p.o, r, p.ldo)[col(e)];
+      }
+  };
+  auto mask_of = [&](int side) {
+    if (p.drop && soon.live())
+      fill_mask(p.rnd, (uint64_t)soon.row * p.cols, p.cols, masks + side * p.cols, threadIdx.x, blockDim.x);
+  };
+  auto flush = [&](int item) {  // as in the staged kernel
+    if (!p.o || item < 0) return;
+    const T *gate = p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      const int c = col(e);
+      if (c >= p.cols) continue;
+      const float s = p.scale * a_s[e], g = gate ? Elem<T>::get(gate[c]) : 0.f;
+      a_s[e] = 0.f;
+      a_post[e] += gate ? activate(p.act, g) * s : s;
+      if (!p.dgate) continue;
+      const float d = w_post ? s * Elem<T>::get(w_post[c]) : s;
+      if (p.split == 1) at<T>(p.dgate, item, p.ld_dg)[c] = Elem<T>::put(d * slope(p.act, g));
+      else p.ws[2 * (int64_t)gridDim.x * p.cols + (int64_t)item * p.cols + c] = d;
+    }
+  };
+  read();
+  mask_of(0);
+  if (p.drop) __syncthreads();
+  const float ks = p.drop ? p.rnd.keep_scale : 1.f;
+  int half = 0, item = -1, side = 0;
+  for (; now.live(); now.next()) {
+    const int r = now.row;
+    const float cy = ry, co = ro;
+    if (now.item != item) {
+      flush(item);
+      item = now.item;
+      const T *gate = p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+        if (col(e) < p.cols) factor[e] = single_factor(p.scale, p.act, gate, w_post, col(e));
+    }
+    float g0[NE], yn[NE], hv[NE], ov[NE], s[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t kept = 0u;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      hv[e] = Elem<T>::get(ndh[e]);
+      yn[e] = Elem<T>::get(ny[e]) * cy;
+      ov[e] = Elem<T>::get(no[e]);
+      const float t = hv[e] * w[e];
+      g0[e] = Elem<T>::get(ndy[e]) + cy * t;
+      s[0] += t * yn[e];
+      if (!p.drop || (col(e) < p.cols && masks[side * p.cols + col(e)])) {
+        kept |= 1u << e;
+        const float q = factor[e] * ov[e];
+        s[1] += g0[e] * q;
+        s[2] += yn[e] * q;
+      }
+    }
+    soon.next();
+    read();
+    side ^= 1;
+    mask_of(side);
+    block_sums4(s, buf, warp, warps, half);
+    if (warps == 1) __syncwarp();
+    const float m1 = cy * s[0] * inv;
+    const float m2 = p.post_norm ? ks * co * co * co * (s[1] - m1 * s[2]) * inv : 0.f;
+    const float kr = ks * co;
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+      if (col(e) < p.cols) {
+        const int c = col(e);
+        a_pre[e] += hv[e] * yn[e];
+        const float dx = g0[e] - yn[e] * m1;
+        const float d = (kept >> e) & 1u ? dx * kr : 0.f;
+        a_s[e] += d * ov[e];
+        if (p.dx) at<T>(p.dx, r, p.ld_dx)[c] = Elem<T>::put(dx);
+        if (p.dout) at<T>(p.dout, r, p.ld_do)[c] = Elem<T>::put(d * factor[e] - ov[e] * m2);
+      }
+  }
+  flush(item);
+#pragma unroll
+  for (int e = 0; e < NE; ++e)
+    if (col(e) < p.cols) {
+      if (p.dw_pre) p.ws[(int64_t)blockIdx.x * p.cols + col(e)] = a_pre[e];
+      if (p.dw_post) p.ws[((int64_t)gridDim.x + blockIdx.x) * p.cols + col(e)] = a_post[e];
+    }
+}
+
 // Column sums of the partials: y 0 dw_pre, 1 dw_post, 2 + g the gate rows.
 // A block adds 32 columns with 32 warps: warp w takes partials w, w + 32, ...,
 // four in flight, then the warps' sums are added in order.  (Eight warps, one
@@ -967,13 +1080,8 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) sum_partials_kernel(const Bwd 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// Threads of a row for rows of `cols` elements in vectors of V: whole warps,
-// at most `most`, each with at most `nv` vectors (0: the row does not fit)
-static int threads_of(int cols, int V, int nv, int most) {
-  const int vecs = (cols + V - 1) / V;
-  const int t = ((vecs + nv - 1) / nv + 31) / 32 * 32;
-  return t <= most ? t : 0;
-}
+// Threads for rows of `cols` elements, `each` a thread: whole warps
+static int threads_of(int cols, int each) { return ((cols + each - 1) / each + 31) / 32 * 32; }
 
 // A staged block: 8 columns a thread in rows of up to 2048 columns (blocks of up
 // to 64 or 256 threads, which sets the shared memory's layout), 16 beyond.
@@ -991,6 +1099,11 @@ static StagedShape staged_shape(int cols) {
 }
 static int64_t staged_blocks(int64_t rows, const StagedShape &s, int num_sms) {
   return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * s.per_sm));
+}
+// Single elements: columns that fit 512 threads, and resident blocks (512 threads an SM)
+constexpr int ODD_BWD_COLS = 8 * 512, ODD_FWD_COLS = 16 * 512;
+static int64_t odd_blocks(int64_t rows, int threads, int num_sms) {
+  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * std::max(1, 512 / threads)));
 }
 // f(group count, threads' limit) as types
 template <typename F>
@@ -1014,22 +1127,15 @@ static cudaError_t launch_staged(void (*kern)(P, int, int), const P &p, int arra
   kern<<<blocks, s.threads, bytes, st>>>(p, with_rows, ahead);
   return cudaGetLastError();
 }
-// Split of a gate row's rows so that all items together give every block one
+// Split of a gate row's rows into items, about one for each block and none
+// without rows (each leaves a partial sum that is added)
 static int64_t split_of(int64_t gates, int64_t per_gate, int64_t blocks) {
   if (gates >= blocks) return 1;
-  return std::max<int64_t>(1, std::min<int64_t>(per_gate, blocks / gates));
+  const int64_t split = std::max<int64_t>(1, std::min<int64_t>(per_gate, blocks / gates));
+  const int64_t per_item = (per_gate + split - 1) / split;
+  return (per_gate + per_item - 1) / per_item;
 }
-template <typename T, int V, int NV>
-static cudaError_t run_fwd(const Fwd &p, int tpr, int num_sms, cudaStream_t st) {
-  const int rpb = std::max(1, 128 / tpr);
-  const int64_t blocks = std::min<int64_t>((p.rows + rpb - 1) / rpb, (int64_t)num_sms * 64);
-  auto kern = block_norm_kernel<T, V, NV>;
-  const size_t smem = rpb * (64 * sizeof(float) + (V == 1 && p.drop ? p.cols : 0));
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (err != cudaSuccess) return err;
-  kern<<<(unsigned)blocks, dim3(tpr, rpb), smem, st>>>(p);
-  return cudaGetLastError();
-}
+
 template <typename T, int V>
 static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
   if constexpr (V > 1) {
@@ -1046,19 +1152,31 @@ static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
                                      p, 2, C::row_bytes(1), p.gate && p.per_gate <= GATE_WITH_ROWS, blocks, s, st);
       });
     }
-    if (const int t = threads_of(p.cols, V, 2, 1024)) return run_fwd<T, V, 2>(p, t, num_sms, st);
   } else {
-    // single elements: 4 or 8 a thread
-    if (const int t = threads_of(p.cols, 1, 4, 256)) return run_fwd<T, 1, 4>(p, t, num_sms, st);
-    if (const int t = threads_of(p.cols, 1, 8, 1024)) return run_fwd<T, 1, 8>(p, t, num_sms, st);
+    if (p.cols <= ODD_FWD_COLS) {
+      const int ne = p.cols <= ODD_BWD_COLS ? 8 : 16, t = threads_of(p.cols, ne);
+      const int64_t most = odd_blocks(p.rows, t, num_sms);
+      p.split = (int)split_of(p.gates, p.per_gate, most);
+      p.per_item = (p.per_gate + p.split - 1) / p.split;
+      const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split);
+      const size_t smem = p.drop ? 2 * p.cols : 0;
+      auto kern = ne == 8 ? block_norm_odd_kernel<T, 8> : block_norm_odd_kernel<T, 16>;
+      kern<<<blocks, t, smem, st>>>(p);
+      return cudaGetLastError();
+    }
   }
-  return run_fwd<T, V, 0>(p, 1024, num_sms, st);
+  auto kern = block_norm_kernel<T, V>;
+  const size_t smem = V == 1 && p.drop ? p.cols : 0;
+  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  kern<<<std::min(p.rows, num_sms * 2), 1024, smem, st>>>(p);
+  return cudaGetLastError();
 }
 
 // The backward's launch: threads and blocks for rows in vectors of V
 struct BwdPlan {
   bool staged;
-  int threads, nv;  // nv: the plain kernel's vectors in registers (0: none)
+  int threads, nv;  // nv: single elements a thread of the odd rows' kernel (0: the general one)
   int64_t blocks;
 };
 static BwdPlan plan_bwd(int64_t rows, int cols, int V, int num_sms) {
@@ -1066,11 +1184,11 @@ static BwdPlan plan_bwd(int64_t rows, int cols, int V, int num_sms) {
     const StagedShape s = staged_shape(cols);
     return BwdPlan{true, s.threads, 0, staged_blocks(rows, s, num_sms)};
   }
-  const int n = V == 1 ? 8 : 0;
-  const int t = n ? threads_of(cols, V, n, 512) : 0;
-  const int threads = t ? t : 512;
-  return BwdPlan{false, threads, t ? n : 0,
-                 std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * std::max(1, 1024 / threads)))};
+  if (V == 1 && cols <= ODD_BWD_COLS) {
+    const int t = threads_of(cols, 8);
+    return BwdPlan{false, t, 8, odd_blocks(rows, t, num_sms)};
+  }
+  return BwdPlan{false, 512, 0, std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * 2))};
 }
 
 template <typename T, int V>
@@ -1092,14 +1210,17 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
       });
       if (err != cudaSuccess) return err;
     } else {
-      block_norm_bwd_kernel<T, V, 0><<<blocks, plan.threads, 0, st>>>(p);
+      block_norm_bwd_kernel<T, V><<<blocks, plan.threads, 0, st>>>(p);
     }
   } else {
-    auto kern = plan.nv ? block_norm_bwd_kernel<T, 1, 8> : block_norm_bwd_kernel<T, 1, 0>;
-    const size_t smem = p.drop ? p.cols : 0;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-    kern<<<blocks, plan.threads, smem, st>>>(p);
+    if (plan.nv) {
+      block_norm_bwd_odd_kernel<T, 8><<<blocks, plan.threads, p.drop ? 2 * p.cols : 0, st>>>(p);
+    } else {
+      const size_t smem = p.drop ? p.cols : 0;
+      err = cudaFuncSetAttribute(block_norm_bwd_kernel<T, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (err != cudaSuccess) return err;
+      block_norm_bwd_kernel<T, 1><<<blocks, plan.threads, smem, st>>>(p);
+    }
   }
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;

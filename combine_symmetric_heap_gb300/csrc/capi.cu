@@ -378,7 +378,8 @@ static bool rows_tma_ok(const sym_rows *r) {
 static bool same_rows(const sym_rows *a, const sym_rows *b) { return a->slots == b->slots && a->rows == b->rows; }
 static bool groups_ok(const sym_groups *g, const sym_rows *r) {
   return g && aligned4(g->cnt) && aligned4(g->off) && g->groups >= 1 && g->groups <= 1024 && g->slots == r->slots &&
-         g->groups % g->slots == 0 && (reinterpret_cast<uintptr_t>(g->status) & 3u) == 0;
+         g->groups % g->slots == 0 && (reinterpret_cast<uintptr_t>(g->status) & 3u) == 0 &&
+         (g->slots == 1 || (g->cnt_slot_stride >= g->groups / g->slots && g->off_slot_stride >= g->groups / g->slots));
 }
 static sym_groups with_timeout(const sym_groups *g) {
   sym_groups c = *g;
@@ -392,8 +393,9 @@ int moe_grouped_matmul(const sym_groups *g, int dtype, const sym_rows *x, const 
       !same_rows(x, out) || !groups_ok(g, x) || !aligned16(w))
     return SYM_EINVAL;
   const int trans = flags & SYM_GM_TRANS_W;
-  if (w_ld % 8 != 0 || w_ld < (trans ? out->cols : x->cols) || (g->groups > 1 && w_group_stride % 8 != 0) ||
-      (g->groups > 1 && w_group_stride < 0))
+  const int64_t w_rows = trans ? x->cols : out->cols, w_cols = trans ? out->cols : x->cols;
+  if (w_ld % 8 != 0 || w_ld < w_cols ||
+      (g->groups > 1 && (w_group_stride % 8 != 0 || w_group_stride < (w_rows - 1) * w_ld + w_cols)))
     return SYM_EINVAL;
   if (x->rows == 0) return SYM_OK;
   const int sms = num_sms_of_current_device();

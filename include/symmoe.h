@@ -509,7 +509,7 @@ typedef struct sym_groups {
  *   dtype: SYM_BF16 or SYM_FP16, of x, w and out; accumulated in fp32 in
  *   tensor memory, rounded once.
  *   w: device, 16-byte aligned; matrix e at element e * w_group_stride, its
- *   rows w_ld elements apart, both multiples of 8.
+ *   rows w_ld elements apart, both multiples of 8; matrices do not overlap.
  *   x: 16-byte aligned, ld (and slot_stride) multiples of 8.  out: any ld.
  *   slots, rows of x and out are equal.  Any C, F in [1, 65536], any number of
  *   rows per group; at most 1024 groups.

@@ -202,6 +202,11 @@ NORMS = [
     (40, 333, 4, "sigmoid", 0.2, True, True, True, True, True),
     (6, 1, 1, "tanh", 0.0, True, True, True, True, True),
     (3, 9001, 1, "none", 0.1, True, True, True, True, True),
+    (4, 5001, 2, "tanh", 0.1, True, True, True, True, True),
+    (350, 1023, 7, "sigmoid", 0.1, True, True, True, True, True),
+    (1200, 512, 300, "tanh", 0.1, True, True, True, True, True),
+    (900, 264, 900, "sigmoid", 0.0, True, True, True, True, True),
+    (310, 8192, 5, "tanh", 0.1, True, True, True, True, True),
 ]
 
 
@@ -290,6 +295,23 @@ def test_block_norm_gradient_against_differences(act, p, G):
         return (ref["y"] * dy.double()).sum() + (ref["h"] * dh.double()).sum()
 
     directional(loss, (x, o, wp, wo, gate), (dx, do, dwp, dwo, dg), gen)
+
+
+def test_block_norm_where_the_block_cancels_the_stream():
+    """x + scale * norm(o) nearly 0: y's norm is far below its parts' (the sum of
+    y^2 may not come from their sums)."""
+    gen = gen_of(12)
+    for rows, cols in ((5, 1024), (3, 4096), (4, 333), (2, 10000)):
+        o = randn(gen, (rows, cols), FP32)
+        n = o.double() * (o.double().square().mean(1, keepdim=True) + 1e-6).rsqrt()
+        x = (-0.5 * n + 1e-3 * torch.randn(n.shape, generator=gen, device="cuda", dtype=torch.float64)).float()
+        y, h, ry = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device="cuda")
+        sm.moe_block_norm(x, o=o, y=y, h=h, scale=0.5, rstd_pre=ry)
+        ref, mag = ref_norm(x, o=o, scale=0.5)
+        assert_within(y, ref["y"], mag["y"], "y")
+        # y itself is off by EVAL of its parts (about 0.5), 500 times its size;
+        # its norm by that much less the square root of the row's length
+        assert float((ry.double() / ref["rstd_pre"] - 1).abs().max()) < 500 * EVAL / 10
 
 
 def test_block_norm_rows_of_zeros_and_parts():

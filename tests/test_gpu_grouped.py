@@ -36,6 +36,7 @@ PRODUCTS = [
     ([0, 0, 3, 0], 2, 0, 72, 136, 0, torch.bfloat16),
     ([700, 0, 2, 30], 4, 5, 136, 264, 8, torch.float16),
     ([1100], 1, 0, 320, 640, 0, torch.bfloat16),
+    ([(7 * i) % 41 for i in range(1024)], 64, 0, 64, 72, 0, torch.bfloat16),
 ]
 
 
@@ -69,6 +70,7 @@ WGRADS = [
     ([0, 0, 3, 0], 2, 0, 1032, 136, 0, torch.float16),
     ([700, 0, 2, 30], 4, 5, 264, 520, 8, torch.bfloat16),
     ([0, 0], 1, 4, 64, 64, 0, torch.bfloat16),
+    ([(7 * i) % 41 for i in range(1024)], 64, 0, 64, 72, 0, torch.bfloat16),
 ]
 
 
@@ -251,6 +253,7 @@ def _args(**over):
     dict(x=torch.zeros(16 * 64 + 4, dtype=torch.bfloat16)[4:].view(16, 64)),          # base not 16-byte aligned
     dict(x=torch.zeros(1, 64, dtype=torch.bfloat16).expand(16, 64)),                  # rows overlap
     dict(x=torch.zeros(16, 64), w=torch.zeros(2, 64, 64), out=torch.zeros(16, 64)),   # fp32 operands
+    dict(w=torch.zeros(1, 64, 64, dtype=torch.bfloat16).expand(2, 64, 64)),           # one matrix for two groups
 ])
 def test_refusals(bad):
     device = lambda k, t: t if k == "x" and tuple(t.shape) == (16, 64) and t.dtype == torch.bfloat16 and t.is_contiguous() \
