@@ -453,6 +453,16 @@ __device__ __forceinline__ void prepare_rows(char *row0, char *end, char *fixed,
     *reinterpret_cast<uint4 *>(fixed + C::place(0, j)) =
         w_pre && C::vector(j) < cols ? *reinterpret_cast<const uint4 *>(w_pre + C::vector(j)) : pack<T, Elem<T>::VEC>(one);
 }
+// Bit 8g + 4k + i: is element i of quad k of group g of row r kept?
+template <typename C>
+__device__ __forceinline__ uint32_t row_mask(const Random &rnd, int r, int cols) {
+  uint64_t block[2 * C::NG];
+#pragma unroll
+  for (int g = 0; g < C::NG; ++g)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) block[2 * g + k] = ((uint64_t)r * cols + C::quad(g, k)) >> 2;
+  return kept_bits<2 * C::NG>(rnd, block);
+}
 __device__ __forceinline__ void wait_oldest(int ahead) {
   if (ahead == 3) cp_async_wait<2>();
   else if (ahead == 2) cp_async_wait<1>();
@@ -513,6 +523,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, in
           if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[g][k]);
         }
     }
+    const uint32_t kept = DROP ? row_mask<C>(p.rnd, r, p.cols) : 0u;
     wait_oldest(ahead_rows);
     if (gate_with_rows)
 #pragma unroll
@@ -533,11 +544,10 @@ __global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, in
         float ov[4];
         x8.quad(k, x[g][k]);
         o8.quad(k, ov);
-        uint32_t word[4];
-        if (DROP) random_words(p.rnd, ((uint64_t)r * p.cols + C::quad(g, k)) >> 2, word);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float xv = x[g][k][i], qv = !DROP || word[i] >= p.rnd.threshold ? ov[i] * factor[g][k][i] : 0.f;
+          const bool keep = !DROP || ((kept >> (8 * g + 4 * k + i)) & 1u);
+          const float xv = x[g][k][i], qv = keep ? ov[i] * factor[g][k][i] : 0.f;
           q[g][k][i] = qv;
           s[0] += ov[i] * ov[i];
           s[1] += xv * xv;
@@ -728,6 +738,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p
             if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[g][k]);
           }
     }
+    const uint32_t kept = DROP ? row_mask<C>(p.rnd, r, p.cols) : 0u;  // bit 8g + 4k + i
     wait_oldest(ahead_rows);
     if (gate_with_rows)
 #pragma unroll
@@ -738,23 +749,19 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p
           const char *gate = row + C::place(GATE, g * C::PER + k / (C::W / 4)) + 4 * (k % (C::W / 4)) * (int)sizeof(T);
           if (c < p.cols) factor_of<T>(p.scale, p.act, gate, w_post ? w_post + c : nullptr, factor[g][k]);
         }
-    uint32_t kept = 0u;  // bit 8g + 4k + i
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const Row in(row, fixed, g);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        uint32_t word[4];
-        if (DROP) random_words(p.rnd, ((uint64_t)r * p.cols + C::quad(g, k)) >> 2, word);
         float yn[4], g0[4], hv[4], ov[4];
         in.front(k, cy, yn, g0, hv, s[0]);
         in.o.quad(k, ov);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (DROP && word[i] < p.rnd.threshold) continue;
-          kept |= 1u << (8 * g + 4 * k + i);
-          const float q = factor[g][k][i] * ov[i];
+          const bool keep = !DROP || ((kept >> (8 * g + 4 * k + i)) & 1u);
+          const float q = keep ? factor[g][k][i] * ov[i] : 0.f;
           s[1] += g0[i] * q;
           s[2] += yn[i] * q;
         }
@@ -1084,7 +1091,10 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) sum_partials_kernel(const Bwd 
 static int threads_of(int cols, int each) { return ((cols + each - 1) / each + 31) / 32 * 32; }
 
 // A staged block: 8 columns a thread in rows of up to 2048 columns (blocks of up
-// to 64 or 256 threads, which sets the shared memory's layout), 16 beyond.
+// to 64 or 256 threads, which sets the shared memory's layout), 16 beyond.  At
+// 4096 columns, forward, three resident blocks of 256 threads instead of two
+// were slower (102 against 88 us without dropout, the same 131 with it), so
+// were 8 columns a thread (94 and 145).
 struct StagedShape {
   int groups, max_threads, threads, per_sm;
 };

@@ -193,6 +193,61 @@ __device__ __forceinline__ void random_words(const Random &r, uint64_t block, ui
   const uint4 w = random_block(r, block);
   u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
 }
+// Bit 4b + j: is element j of block first[b] kept?  The blocks' rounds run side
+// by side: a round is a chain of two dependent instructions, and one block at a
+// time would leave the pipes waiting on it.
+template <int NB>
+__device__ __forceinline__ uint32_t kept_bits(const Random &r, const uint64_t (&block)[NB]) {
+  uint32_t c0[NB], c1[NB], c2[NB], c3[NB];
+  bool small = true;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) small = small && (block[b] >> 32) == 0;
+  if (small) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint64_t x = (uint64_t)(uint32_t)block[b] * PHILOX_A;
+      const uint64_t y = (uint64_t)((uint32_t)(x >> 32) ^ r.first[0]) * PHILOX_B;
+      c0[b] = (uint32_t)(y >> 32) ^ r.first[1];
+      c1[b] = (uint32_t)y;
+      c2[b] = (uint32_t)x ^ r.first[2];
+      c3[b] = r.first[3];
+    }
+  } else {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      c0[b] = (uint32_t)block[b], c1[b] = (uint32_t)(block[b] >> 32);
+      c2[b] = (uint32_t)r.offset, c3[b] = (uint32_t)(r.offset >> 32);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t x = (uint64_t)c0[b] * PHILOX_A, y = (uint64_t)c2[b] * PHILOX_B;
+        c0[b] = (uint32_t)(y >> 32) ^ c1[b] ^ r.key[i][0];
+        c1[b] = (uint32_t)y;
+        c2[b] = (uint32_t)(x >> 32) ^ c3[b] ^ r.key[i][1];
+        c3[b] = (uint32_t)x;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 2; i < 10; ++i)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint64_t x = (uint64_t)c0[b] * PHILOX_A, y = (uint64_t)c2[b] * PHILOX_B;
+      c0[b] = (uint32_t)(y >> 32) ^ c1[b] ^ r.key[i][0];
+      c1[b] = (uint32_t)y;
+      c2[b] = (uint32_t)(x >> 32) ^ c3[b] ^ r.key[i][1];
+      c3[b] = (uint32_t)x;
+    }
+  uint32_t kept = 0u;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (c0[b] >= r.threshold) kept |= 1u << (4 * b);
+    if (c1[b] >= r.threshold) kept |= 2u << (4 * b);
+    if (c2[b] >= r.threshold) kept |= 4u << (4 * b);
+    if (c3[b] >= r.threshold) kept |= 8u << (4 * b);
+  }
+  return kept;
+}
+
 // keep factors (0 or 1 / (1 - p)) of the V elements from element `at` on
 template <int V>
 __device__ __forceinline__ void keep_factors(const Random &r, uint64_t at, float (&k)[V]) {

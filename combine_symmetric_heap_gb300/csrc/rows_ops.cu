@@ -149,40 +149,29 @@ __global__ void __launch_bounds__(THREADS) dropout_kernel(const RowArgs p, const
 }
 
 // The same over one run of n contiguous elements (element i is number i of the
-// stream): no rows to address, two vectors in flight a thread.
+// stream): no rows to address.  One vector a thread at a time with its blocks of
+// words side by side and many warps: 66 us at 16384 x 4096 (bf16, residual; 6.1
+// TB/s), against 71 and 76 with two and four vectors.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) dropout_flat_kernel(const T *x, const T *res, T *y, int64_t n,
                                                                const Random rnd) {
-  constexpr int V = Elem<T>::VEC, U = 2;
+  constexpr int V = Elem<T>::VEC;
   const int64_t vecs = n / V, step = (int64_t)gridDim.x * THREADS;
-  const uint4 *xv = reinterpret_cast<const uint4 *>(x), *rv = reinterpret_cast<const uint4 *>(res);
-  for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < vecs; i += U * step) {
-    uint4 a[U], b[U];
+  for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < vecs; i += step) {
+    const uint4 a = reinterpret_cast<const uint4 *>(x)[i];
+    uint4 b = make_uint4(0, 0, 0, 0);
+    if (res) b = reinterpret_cast<const uint4 *>(res)[i];
+    uint64_t block[V / 4];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * step < vecs) {
-        a[u] = xv[i + u * step];
-        if (res) b[u] = rv[i + u * step];
-      }
+    for (int q = 0; q < V / 4; ++q) block[q] = (uint64_t)i * (V / 4) + q;
+    const uint32_t kept = kept_bits<V / 4>(rnd, block);
+    float f[V], r[V];
+    unpack<T, V>(a, f);
+    unpack<T, V>(b, r);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * step < vecs) {
-        const int64_t at = i + u * step;
-        float f[V], r[V];
-        unpack<T, V>(a[u], f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) r[j] = 0.f;
-        if (res) unpack<T, V>(b[u], r);
-#pragma unroll
-        for (int q = 0; q < V; q += 4) {
-          uint32_t word[4];
-          random_words(rnd, (uint64_t)(at * V + q) >> 2, word);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (word[j] >= rnd.threshold) r[q + j] += f[q + j] * rnd.keep_scale;
-        }
-        reinterpret_cast<uint4 *>(y)[at] = pack<T, V>(r);
-      }
+    for (int j = 0; j < V; ++j)
+      if ((kept >> j) & 1u) r[j] += f[j] * rnd.keep_scale;
+    reinterpret_cast<uint4 *>(y)[i] = pack<T, V>(r);
   }
   if (blockIdx.x == 0 && threadIdx.x < n % V) {
     const int64_t at = vecs * V + threadIdx.x;
@@ -293,7 +282,7 @@ cudaError_t launch_dropout(int dtype, const sym_rows &x, const sym_rows *res, co
                   (r->slots == 1 || r->slot_stride == r->rows * r->cols));
   };
   if (run(&x) && run(&y) && run(res)) {
-    const int64_t n = x.rows * x.slots * x.cols, per = THREADS * 2 * (16 / es);
+    const int64_t n = x.rows * x.slots * x.cols, per = THREADS * (16 / es);
     const unsigned blocks = (unsigned)std::min<int64_t>((n + per - 1) / per, (int64_t)num_sms * 32);
     auto go = [&](auto zero) {
       using T = decltype(zero);
