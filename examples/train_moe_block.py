@@ -1,6 +1,6 @@
 """Training steps of one MoE block on the symmetric heap.
 
-    python examples/train_moe_block.py [--steps 20] [--config tiny|mixtral]
+    python examples/train_moe_block.py [--steps 20] [--config tiny|mixtral] [--tokens-per-slot 512] [--inter 4096]
 
 The block is  y = x + scale * drop(tanh(gate) * norm(MoE(norm(x)))).  Its
 forward dispatches the normalised tokens over the heap, runs the experts as
@@ -120,9 +120,12 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--config", default="tiny", choices=("tiny", "mixtral"))
+    ap.add_argument("--tokens-per-slot", type=int, help="instead of the configuration's")
+    ap.add_argument("--inter", type=int, help="expert intermediate size, instead of the configuration's")
     ap.add_argument("--lr", type=float, default=0.5)
     a = ap.parse_args()
     cfg = ms.shape_of(ms.CONFIGS[a.config])
+    cfg.update({k: v for k, v in (("tokens_per_slot", a.tokens_per_slot), ("inter", a.inter)) if v})
     dev = torch.device("cuda", torch.cuda.current_device())
     block = MoeBlock(cfg, device=dev)
     x = ms.x_torch(cfg, dev)
@@ -131,14 +134,17 @@ def main():
     y, dx = torch.empty_like(x), torch.empty_like(x)
     first = None
     for step in range(a.steps):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
         block.forward(x, y)
         diff = y.float() - target.float()
         loss = diff.square().mean()
         # the gradient of the mean, times the tokens: one learning rate for every size
         block.backward((2 / x.shape[1] * diff).bfloat16(), dx)
+        end.record()
         block.update(a.lr / x.shape[0])
         first = float(loss) if first is None else first
-        print(f"step {step}: loss {float(loss):.5f}")
+        print(f"step {step}: loss {float(loss):.5f}, forward and backward {start.elapsed_time(end):.3f} ms")
     assert block.heap.status() == 0 and block.grad_heap.status() == 0
     return first, float(loss)
 

@@ -37,6 +37,13 @@ PRODUCTS = [
     ([700, 0, 2, 30], 4, 5, 136, 264, 8, torch.float16),
     ([1100], 1, 0, 320, 640, 0, torch.bfloat16),
     ([(7 * i) % 41 for i in range(1024)], 64, 0, 64, 72, 0, torch.bfloat16),
+    # few rows in all
+    ([1, 0, 2, 0, 1], 1, 0, 1003, 300, 8, torch.bfloat16),
+    ([0, 3, 5], 1, 0, 264, 520, 0, torch.float16),
+    ([2, 1], 1, 1, 4099, 77, 0, torch.bfloat16),
+    ([4], 1, 0, 16384, 200, 0, torch.float16),
+    ([0, 8], 1, 0, 72, 20000, 0, torch.bfloat16),
+    ([1], 1, 1, 3, 5, 0, torch.bfloat16),
 ]
 
 
@@ -131,6 +138,20 @@ def test_groups_outside_their_slot_are_empty_and_flagged():
     assert int(status) == sm.SYM_STATUS_OVERFLOW
     assert bool((out[10:] == 7.0).all()) and not bool((out[:10] == 7.0).all())
     assert bool((dw[1:] == 0).all()) and bool(dw[0].isfinite().all())
+
+
+@pytest.mark.parametrize("rows,trans", [(4, False), (4, True), (9, False)])
+def test_bad_groups_among_few_rows(rows, trans):
+    gen = gen_of(4)
+    x = torch.randn(rows, 64, generator=gen, device="cuda").bfloat16()
+    w = torch.randn(3, 64, 64, generator=gen, device="cuda").bfloat16()
+    cnt = torch.tensor([2, rows, -2], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((rows, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+    sm.moe_grouped_matmul(x, w, cnt, off, out, trans_w=trans, status=status)
+    assert int(status) == sm.SYM_STATUS_OVERFLOW
+    assert bool((out[2:] == 7.0).all()) and not bool((out[:2] == 7.0).any(1).all())
 
 
 def test_empty_tensors():
