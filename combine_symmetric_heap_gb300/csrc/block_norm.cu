@@ -13,11 +13,19 @@
 //   dw_pre = sum dh yn,  dw_post = sum dn on,  dgate = act'(gate) sum m dx on w_post
 // (sums over rows; the gate's over the rows that share it).
 //
-// Both are bound by their bytes: every row tensor is read once and written
-// once, one pass per row with the row held in registers (rows beyond the
-// register budget are walked again out of L2).  The dropout mask is recomputed
-// from its counter.  The backward's two row means are taken with one block
-// reduction: mean(dn w_post on) is linear in the first mean.
+// Every row tensor is read once and written once; the dropout mask is recomputed
+// from its counter; a row's sums come from one block reduction (the backward's
+// two row means too: mean(dn w_post on) is linear in the first mean).  Three
+// kernels each way, by the rows' length and alignment: staged (16-byte vectors,
+// up to 8192 columns), odd (single elements, up to 8192 forward, 4096 backward)
+// and general (any length, the row walked again out of L2).
+//
+// Measured (bf16, dropout 0.1, a GB300 whose copy rate is 6.69 TB/s): forward
+// with both norms, 16384 x 4096, 133 us (4.0 TB/s; 88 us and 6.1 TB/s without
+// dropout), bound by the generator's multiplies on top of the bytes; backward,
+// 8192 x 7168, 197 us (3.6 TB/s; 151 us and 4.7 TB/s without dropout), bound by
+// the latency of a row's chain: its 57 KB a row and 16 columns' sums a thread
+// leave an SM one block.  Single elements: 304 us forward at 16384 x 4095.
 #include <algorithm>
 
 #include "rows_dev.cuh"
@@ -453,15 +461,15 @@ __device__ __forceinline__ void prepare_rows(char *row0, char *end, char *fixed,
     *reinterpret_cast<uint4 *>(fixed + C::place(0, j)) =
         w_pre && C::vector(j) < cols ? *reinterpret_cast<const uint4 *>(w_pre + C::vector(j)) : pack<T, Elem<T>::VEC>(one);
 }
-// Bit 8g + 4k + i: is element i of quad k of group g of row r kept?
-template <typename C>
-__device__ __forceinline__ uint32_t row_mask(const Random &rnd, int r, int cols) {
-  uint64_t block[2 * C::NG];
+// Bit 8g + 4k + i: is element i of quad k of group first + g of row r kept?
+template <typename C, int N>
+__device__ __forceinline__ uint32_t row_mask(const Random &rnd, int r, int cols, int first) {
+  uint64_t block[2 * N];
 #pragma unroll
-  for (int g = 0; g < C::NG; ++g)
+  for (int g = 0; g < N; ++g)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) block[2 * g + k] = ((uint64_t)r * cols + C::quad(g, k)) >> 2;
-  return kept_bits<2 * C::NG>(rnd, block);
+    for (int k = 0; k < 2; ++k) block[2 * g + k] = ((uint64_t)r * cols + C::quad(first + g, k)) >> 2;
+  return kept_bits<2 * N>(rnd, block);
 }
 __device__ __forceinline__ void wait_oldest(int ahead) {
   if (ahead == 3) cp_async_wait<2>();
@@ -523,7 +531,6 @@ __global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, in
           if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[g][k]);
         }
     }
-    const uint32_t kept = DROP ? row_mask<C>(p.rnd, r, p.cols) : 0u;
     wait_oldest(ahead_rows);
     if (gate_with_rows)
 #pragma unroll
@@ -538,6 +545,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, in
     float x[NG][2][4], q[NG][2][4], s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
+      const uint32_t kept = DROP ? row_mask<C, 1>(p.rnd, r, p.cols, g) : 0u;
       const Eight<C, T> x8(row + C::place(X, 0), g), o8(row + C::place(O, 0), g);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -546,7 +554,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, in
         o8.quad(k, ov);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool keep = !DROP || ((kept >> (8 * g + 4 * k + i)) & 1u);
+          const bool keep = !DROP || ((kept >> (4 * k + i)) & 1u);
           const float xv = x[g][k][i], qv = keep ? ov[i] * factor[g][k][i] : 0.f;
           q[g][k][i] = qv;
           s[0] += ov[i] * ov[i];
@@ -738,7 +746,6 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p
             if (c < p.cols) factor_of<T>(p.scale, p.act, gate ? gate + c : nullptr, w_post ? w_post + c : nullptr, factor[g][k]);
           }
     }
-    const uint32_t kept = DROP ? row_mask<C>(p.rnd, r, p.cols) : 0u;  // bit 8g + 4k + i
     wait_oldest(ahead_rows);
     if (gate_with_rows)
 #pragma unroll
@@ -749,6 +756,9 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p
           const char *gate = row + C::place(GATE, g * C::PER + k / (C::W / 4)) + 4 * (k % (C::W / 4)) * (int)sizeof(T);
           if (c < p.cols) factor_of<T>(p.scale, p.act, gate, w_post ? w_post + c : nullptr, factor[g][k]);
         }
+    // all groups' blocks of words side by side (a group at a time: 203 against
+    // 197 us; the forward, with fewer registers to spare, gains from that)
+    const uint32_t kept = DROP ? row_mask<C, C::NG>(p.rnd, r, p.cols, 0) : 0u;  // bit 8g + 4k + i
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -1093,8 +1103,8 @@ static int threads_of(int cols, int each) { return ((cols + each - 1) / each + 3
 // A staged block: 8 columns a thread in rows of up to 2048 columns (blocks of up
 // to 64 or 256 threads, which sets the shared memory's layout), 16 beyond.  At
 // 4096 columns, forward, three resident blocks of 256 threads instead of two
-// were slower (102 against 88 us without dropout, the same 131 with it), so
-// were 8 columns a thread (94 and 145).
+// were slower (102 against 88 us without dropout, the same with it), so were 8
+// columns a thread (94 against 88, 145 against 133).
 struct StagedShape {
   int groups, max_threads, threads, per_sm;
 };

@@ -532,8 +532,10 @@ int moe_grouped_matmul(const sym_groups *g, int dtype, const sym_rows *x, const 
  *   aligned ones are stored faster).
  * The contraction runs over the group's rows in order, one work item per
  * output tile: the result does not depend on the schedule.  The tensor
- * cores' additions into the fp32 accumulator truncate: relative error about
- * 1e-8 per 16 rows of a group on top of the result's rounding.
+ * cores' additions into the fp32 accumulator truncate: an fp32 result is off by
+ * about 1e-9 of its norm for every row of the group (measured relative L2: 2.3e-7
+ * at 256 rows, 1.0e-6 at 1024, 4.4e-6 at 4096), far below a 16-bit result's
+ * rounding (2e-3).
  */
 #define SYM_GM_ACCUMULATE 1
 int moe_grouped_wgrad(const sym_groups *g, int dtype, const sym_rows *dy, const sym_rows *x,
