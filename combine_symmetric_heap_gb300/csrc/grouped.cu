@@ -24,7 +24,7 @@
 // contraction rows x 64 features, a tile the tensor core reads in its
 // "MN-major" form, so no operand is ever transposed by a copy.
 //
-// Measured (bf16; copy rate 6.69 TB/s, cuBLAS 1867 TFLOP/s in a burst, 1710 under
+// Measured (bf16; measured rates: copy 6.69 TB/s, library GEMM 1867 TFLOP/s in a burst, 1710 under
 // the power cap): product of 8192 rows in 256 groups, 7168 -> 2048, 1.17 ms (6.57
 // TB/s, bound by the weights' read); of 65536 rows 1.43 ms in a few launches, 1.65
 // ms back to back under the power cap (the narrow second MMA of groups of 257..288

@@ -8,8 +8,6 @@
 // counts are on the device: the block of a row that starts a run of NR rows of
 // its group takes the run, blocks of the other rows leave.  Sums run in fp32 in
 // a fixed order.
-#include <algorithm>
-
 #include "rows_dev.cuh"
 
 namespace symmoe {
@@ -221,7 +219,8 @@ cudaError_t launch_few_rows(const sym_groups &g, int fp16, const sym_rows &x, co
   const Args p{g.cnt, g.off, g.groups, g.status, reinterpret_cast<const uint16_t *>(x.ptr),
                reinterpret_cast<const uint16_t *>(w), reinterpret_cast<uint16_t *>(out.ptr), x.ld, w_group, w_ld, out.ld,
                (int)x.rows, out.cols, x.cols};
-  const size_t smem = trans ? (size_t)std::min<int64_t>(RUN, x.rows) * ((x.cols + 7) & ~7) * 2 : 0;
+  // rows of x a block reads: 1, 2 or RUN (a run of three reads a fourth that is not stored)
+  const size_t smem = trans ? (size_t)(x.rows <= 2 ? x.rows : RUN) * ((x.cols + 7) & ~7) * 2 : 0;
   auto go = [&](auto kern, int threads, int features) {
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;

@@ -44,6 +44,8 @@ PRODUCTS = [
     ([4], 1, 0, 16384, 200, 0, torch.float16),
     ([0, 8], 1, 0, 72, 20000, 0, torch.bfloat16),
     ([1], 1, 1, 3, 5, 0, torch.bfloat16),
+    ([0, 3], 1, 0, 136, 72, 0, torch.bfloat16),
+    ([2], 1, 0, 136, 72, 0, torch.float16),
 ]
 
 
