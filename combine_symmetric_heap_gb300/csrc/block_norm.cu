@@ -17,15 +17,16 @@
 // from its counter; a row's sums come from one block reduction (the backward's
 // two row means too: mean(dn w_post on) is linear in the first mean).  Three
 // kernels each way, by the rows' length and alignment: staged (16-byte vectors,
-// up to 8192 columns), odd (single elements, up to 8192 forward, 4096 backward)
-// and general (any length, the row walked again out of L2).
+// up to 8192 columns), odd (rows off 16-byte boundaries, up to 8192 columns) and
+// general (any length, the row walked again out of L2).
 //
 // Measured (bf16, dropout 0.1, a GB300 whose copy rate is 6.69 TB/s): forward
 // with both norms, 16384 x 4096, 133 us (4.0 TB/s; 88 us and 6.1 TB/s without
 // dropout), bound by the generator's multiplies on top of the bytes; backward,
 // 8192 x 7168, 197 us (3.6 TB/s; 151 us and 4.7 TB/s without dropout), bound by
 // the latency of a row's chain: its 57 KB a row and 16 columns' sums a thread
-// leave an SM one block.  Single elements: 304 us forward at 16384 x 4095.
+// leave an SM one block.  Rows off 16-byte boundaries: forward 16384 x 4095
+// 218 us, backward 8192 x 7167 294 us.
 #include <algorithm>
 
 #include "rows_dev.cuh"
@@ -831,85 +832,162 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p
 }
 
 // ---------------------------------------------------------------------------
-// Rows that start off a 16-byte boundary (odd lengths, sliced tensors): the
-// staged kernels' work with NE single elements a thread, a block's width apart.
-// The next row's elements are loaded into registers while a row is worked on,
-// and its dropout mask is made, once a block of words, into shared memory: by
-// the time it is read the row's reduction has been a barrier.  Up to NE * 512
-// columns.
+// Rows that start off a 16-byte boundary (odd lengths, sliced tensors), up to
+// 8192 columns: the staged kernels' work with 8 single elements a thread, 32
+// apart (a warp's are 256 in a row, their offsets constants).  A row is copied as the 16-byte words that it lies in,
+// up to three rows ahead, and lies in shared memory as far from a boundary as
+// in memory; here any thread may read what another one copied, so a thread's
+// copies of the next row are waited for before a barrier of this row.  A row's
+// dropout mask is made a row ahead too, each block of words once.  Columns past
+// the row's end are zeros in shared memory, as in the staged kernels.
+//
+// Bound by instructions: an element at a time, bf16 and fp32 take the same time
+// (218 and 229 us forward at 16384 x 4095, 144 and 174 without dropout).  With
+// the next row's elements loaded into registers instead, 307 us, and 757 against
+// 325 backward; columns a block's width apart, whose addresses are computed, 250
+// and 423.
 // ---------------------------------------------------------------------------
+constexpr int ODD_EACH = 8, ODD_COLS = ODD_EACH * 1024;
+// This thread's first column; the others follow 32 apart
+__device__ __forceinline__ int odd_first() {
+  return (int)threadIdx.x / 32 * (32 * ODD_EACH) + ((int)threadIdx.x & 31);
+}
+// A row of any alignment in shared memory, and a row's mask bytes, for `threads` threads
 template <typename T>
-__device__ __forceinline__ float single_factor(float scale, int act, const T *gate, const T *w_post, int c) {
-  float f = scale;
-  if (gate) f *= activate(act, Elem<T>::get(gate[c]));
-  if (w_post) f *= Elem<T>::get(w_post[c]);
-  return f;
+__host__ __device__ constexpr int odd_pitch(int threads) {
+  return ODD_EACH * threads * (int)sizeof(T) + 16;
+}
+__host__ __device__ constexpr int odd_mask_pitch(int threads) { return ODD_EACH * threads + 8; }
+// How far from a 16-byte boundary row r starts
+template <typename T>
+__device__ __forceinline__ int odd_shift(const void *p, int r, int ld) {
+  return p ? (int)(reinterpret_cast<uintptr_t>(at<T>(p, r, ld)) & 15) : 0;
+}
+// 16 bytes to shared memory, of which `n` are read and the rest are zeros
+__device__ __forceinline__ void cp_async16_part(char *to, const char *from, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(n) : "memory");
+}
+// Copy row r of `cols` elements to `to` + its shift.  The first word begins up to
+// 15 bytes before the row: memory of the same allocation, since those begin on
+// 16-byte boundaries (it is read, never used).  The last word is cut at the row's
+// end, and zeros follow where a row of another shift may have ended.
+template <typename T>
+__device__ __forceinline__ void odd_copy(char *to, const void *p, int r, int ld, int cols, int pitch) {
+  if (!p) return;
+  const int shift = odd_shift<T>(p, r, ld), bytes = shift + cols * (int)sizeof(T);
+  const char *from = reinterpret_cast<const char *>(at<T>(p, r, ld)) - shift;
+  for (int i = 16 * (int)threadIdx.x; i < min(bytes + 16, pitch); i += 16 * (int)blockDim.x) {
+    const int n = max(0, min(16, bytes - i));
+    cp_async16_part(to + i, n ? from + i : from, n);
+  }
+}
+// Which elements of row r are kept, a byte each: element c at mask[(r cols) mod 4 + c]
+__device__ __forceinline__ void odd_mask(const Random &rnd, int r, int cols, uint8_t *mask) {
+  const uint64_t first = (uint64_t)r * cols;
+  const int blocks = ((int)(first & 3) + cols + 3) / 4, T = blockDim.x;
+  for (int b = threadIdx.x; b < blocks; b += 2 * T) {
+    const uint64_t block[2] = {(first >> 2) + b, (first >> 2) + b + T};
+    const uint32_t kept = kept_bits<2>(rnd, block);
+    // bit i of four to byte i
+    reinterpret_cast<uint32_t *>(mask)[b] = ((kept & 15u) * 0x00204081u) & 0x01010101u;
+    if (b + T < blocks) reinterpret_cast<uint32_t *>(mask)[b + T] = ((kept >> 4) * 0x00204081u) & 0x01010101u;
+  }
+}
+template <typename T>
+__device__ __forceinline__ float odd_get(const char *row, int c) {
+  return Elem<T>::get(*reinterpret_cast<const T *>(row + c * (int)sizeof(T)));
+}
+// Zeros in the rows, w_pre (or ones) behind them
+template <typename T>
+__device__ __forceinline__ void odd_prepare(char *rows, T *w, const T *w_pre, int cols) {
+  for (char *q = rows + 16 * threadIdx.x; q < reinterpret_cast<char *>(w); q += 16 * blockDim.x)
+    *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
+  for (int c = threadIdx.x; c < ODD_EACH * (int)blockDim.x; c += blockDim.x)
+    w[c] = w_pre && c < cols ? w_pre[c] : Elem<T>::put(1.f);
+  __syncthreads();
+}
+// scale * act(gate) * w_post of this thread's columns (`gate`: in memory, or with the row)
+template <typename T>
+__device__ __forceinline__ void odd_factors(float scale, int act, const T *gate, const T *w_post, int cols,
+                                            float (&f)[ODD_EACH]) {
+  float g[ODD_EACH], w[ODD_EACH];
+#pragma unroll
+  for (int e = 0; e < ODD_EACH; ++e) {
+    const int c = odd_first() + 32 * e;
+    g[e] = gate && c < cols ? Elem<T>::get(gate[c]) : 0.f;
+    w[e] = w_post && c < cols ? Elem<T>::get(w_post[c]) : 1.f;
+  }
+#pragma unroll
+  for (int e = 0; e < ODD_EACH; ++e) f[e] = scale * (gate ? activate(act, g[e]) : 1.f) * w[e];
 }
 
-template <typename T, int NE>
-__global__ void __launch_bounds__(512) block_norm_odd_kernel(const Fwd p) {
-  extern __shared__ uint8_t masks[];  // [2][cols]
+template <typename T, bool DROP>
+__global__ void __launch_bounds__(1024) block_norm_odd_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
+  constexpr int NE = ODD_EACH;
+  extern __shared__ __align__(16) char smem[];
   __shared__ float buf[2 * 128];
-  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  enum { X, O, GATE };
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, pitch = odd_pitch<T>(blockDim.x);
+  const int row_step = (2 + gate_with_rows) * pitch;
+  char *const row_end = smem + ahead_rows * row_step;
+  T *const w = reinterpret_cast<T *>(row_end);
+  uint8_t *const masks = reinterpret_cast<uint8_t *>(row_end + pitch);
+  const int mask_pitch = odd_mask_pitch(blockDim.x);
   const float inv = 1.f / p.cols;
-  const T *w_pre = reinterpret_cast<const T *>(p.w_pre), *w_post = reinterpret_cast<const T *>(p.w_post);
-  auto col = [&](int e) { return (int)threadIdx.x + e * (int)blockDim.x; };
-  float w[NE], factor[NE];
-  T nx[NE], no[NE];  // the next row's elements, as they lie
-#pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    w[e] = w_pre && col(e) < p.cols ? Elem<T>::get(w_pre[col(e)]) : 1.f;
-    factor[e] = 0.f;
-    nx[e] = no[e] = Elem<T>::put(0.f);
-  }
-  Walk now(p.per_gate, p.per_item, p.gates, p.split), soon = now;
-  auto read = [&]() {
-    if (!soon.live()) return;
-    const T *px = at<T>(p.x, soon.row, p.ldx), *po = p.o ? at<T>(p.o, soon.row, p.ldo) : nullptr;
-#pragma unroll
-    for (int e = 0; e < NE; ++e)
-      if (col(e) < p.cols) {
-        nx[e] = px[col(e)];
-        if (po) no[e] = po[col(e)];
-      }
+  const T *w_post = reinterpret_cast<const T *>(p.w_post);
+  auto col = [&](int e) { return odd_first() + 32 * e; };
+  Walk now(p.per_gate, p.per_item, p.gates, p.split), soon = now, ahead = now;
+  odd_prepare<T>(smem, w, reinterpret_cast<const T *>(p.w_pre), p.cols);
+  auto fetch = [&](char *to) {  // the next row
+    if (ahead.live()) {
+      odd_copy<T>(to + X * pitch, p.x, ahead.row, p.ldx, p.cols, pitch);
+      odd_copy<T>(to + O * pitch, p.o, ahead.row, p.ldo, p.cols, pitch);
+      if (gate_with_rows) odd_copy<T>(to + GATE * pitch, p.gate, ahead.item / p.split, p.ldg, p.cols, pitch);
+      ahead.next();
+    }
+    cp_async_commit();
   };
-  auto mask_of = [&](int side) {
-    if (p.drop && soon.live())
-      fill_mask(p.rnd, (uint64_t)soon.row * p.cols, p.cols, masks + side * p.cols, threadIdx.x, blockDim.x);
-  };
-  read();
-  mask_of(0);
-  if (p.drop) __syncthreads();
+  for (char *to = smem; to != row_end; to += row_step) fetch(to);
+  if (DROP) odd_mask(p.rnd, soon.row, p.cols, masks);
+  float factor[NE];
+#pragma unroll
+  for (int e = 0; e < NE; ++e) factor[e] = 0.f;
+  wait_oldest(ahead_rows);
+  __syncthreads();
+  char *row = smem;
   int half = 0, item = -1, side = 0;
   for (; now.live(); now.next()) {
     const int r = now.row;
-    if (now.item != item) {
+    if (now.item != item || gate_with_rows) {
       item = now.item;
       const T *gate = p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
-#pragma unroll
-      for (int e = 0; e < NE; ++e)
-        if (col(e) < p.cols) factor[e] = single_factor(p.scale, p.act, gate, w_post, col(e));
+      if (gate_with_rows)
+        gate = reinterpret_cast<const T *>(row + GATE * pitch + odd_shift<T>(p.gate, item / p.split, p.ldg));
+      odd_factors<T>(p.scale, p.act, gate, w_post, p.cols, factor);
     }
+    const char *rx = row + X * pitch + odd_shift<T>(p.x, r, p.ldx), *ro = row + O * pitch + odd_shift<T>(p.o, r, p.ldo);
+    const uint8_t *mask = masks + side * mask_pitch + (((uint32_t)r * (uint32_t)p.cols) & 3u);
     float y[NE], q[NE], s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
-      const bool keep = !p.drop || (col(e) < p.cols && masks[side * p.cols + col(e)]);
-      const float o = Elem<T>::get(no[e]);
-      y[e] = Elem<T>::get(nx[e]);
-      q[e] = keep ? o * factor[e] : 0.f;
+      const float o = odd_get<T>(ro, col(e));
+      y[e] = odd_get<T>(rx, col(e));
+      q[e] = !DROP || mask[col(e)] ? o * factor[e] : 0.f;
       s[0] += o * o;
       s[1] += y[e] * y[e];
       s[2] += y[e] * q[e];
       s[3] += q[e] * q[e];
     }
     soon.next();
-    read();
     side ^= 1;
-    mask_of(side);
+    if (DROP && soon.live()) odd_mask(p.rnd, soon.row, p.cols, masks + side * mask_pitch);
+    if (ahead_rows > 1) wait_oldest(ahead_rows - 1);  // the next row
     block_sums4(s, buf, warp, warps, half);
     if (warps == 1) __syncwarp();
+    fetch(row);
+    row = row + row_step == row_end ? smem : row + row_step;
     const float rstd_o = p.post_norm ? rsqrtf(s[0] * inv + p.eps) : 1.f;
-    const float f = p.drop ? rstd_o * p.rnd.keep_scale : rstd_o;
+    const float f = DROP ? rstd_o * p.rnd.keep_scale : rstd_o;
     float yy = s[1] + f * (2.f * s[2] + f * s[3]);
 #pragma unroll
     for (int e = 0; e < NE; ++e) y[e] += f * q[e];
@@ -925,130 +1003,176 @@ __global__ void __launch_bounds__(512) block_norm_odd_kernel(const Fwd p) {
       if (p.rstd_post) p.rstd_post[r] = rstd_o;
       if (p.rstd_pre) p.rstd_pre[r] = rstd_y;
     }
-    T *py = p.y ? at<T>(p.y, r, p.ldy) : nullptr, *ph = p.h ? at<T>(p.h, r, p.ldh) : nullptr;
+    if (p.y) {
+      T *py = at<T>(p.y, r, p.ldy);
 #pragma unroll
-    for (int e = 0; e < NE; ++e)
-      if (col(e) < p.cols) {
-        if (py) py[col(e)] = Elem<T>::put(y[e]);
-        if (ph) ph[col(e)] = Elem<T>::put(y[e] * rstd_y * w[e]);
+      for (int e = 0; e < NE; ++e)
+        if (col(e) < p.cols) py[col(e)] = Elem<T>::put(y[e]);
+    }
+    if (p.h) {
+      T *ph = at<T>(p.h, r, p.ldh);
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        const T v = Elem<T>::put(y[e] * rstd_y * Elem<T>::get(w[col(e)]));
+        if (col(e) < p.cols) ph[col(e)] = v;
       }
+    }
+    if (ahead_rows == 1) {
+      cp_async_wait<0>();
+      __syncthreads();
+    }
   }
 }
 
-template <typename T, int NE>
-__global__ void __launch_bounds__(512) block_norm_bwd_odd_kernel(const Bwd p) {
-  extern __shared__ uint8_t masks[];  // [2][cols]
+template <typename T, bool DROP>
+__global__ void __launch_bounds__(1024) block_norm_bwd_odd_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
+  constexpr int NE = ODD_EACH;
+  extern __shared__ __align__(16) char smem[];
   __shared__ float buf[2 * 128];
-  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  enum { DY, DH, Y, O, GATE };
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, pitch = odd_pitch<T>(blockDim.x);
+  const int row_step = (4 + gate_with_rows) * pitch;
+  char *const row_end = smem + ahead_rows * row_step;
+  T *const w = reinterpret_cast<T *>(row_end);
+  float *const post = reinterpret_cast<float *>(row_end + pitch);  // dw_post's sums over the items
+  uint8_t *const masks = reinterpret_cast<uint8_t *>(post + NE * blockDim.x);
+  const int mask_pitch = odd_mask_pitch(blockDim.x);
   const float inv = 1.f / p.cols;
-  const T *w_pre = reinterpret_cast<const T *>(p.w_pre), *w_post = reinterpret_cast<const T *>(p.w_post);
-  auto col = [&](int e) { return (int)threadIdx.x + e * (int)blockDim.x; };
-  float w[NE], factor[NE], a_pre[NE], a_s[NE], a_post[NE];
-  T ndy[NE], ndh[NE], ny[NE], no[NE];  // the next row's elements, as they lie
-#pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    w[e] = w_pre && col(e) < p.cols ? Elem<T>::get(w_pre[col(e)]) : 1.f;
-    factor[e] = a_pre[e] = a_s[e] = a_post[e] = 0.f;
-    ndy[e] = ndh[e] = ny[e] = no[e] = Elem<T>::put(0.f);
-  }
-  Walk now(p.per_gate, p.per_item, p.gates, p.split), soon = now;
-  float ry = 0.f, ro = 1.f;
-  auto read = [&]() {
-    if (!soon.live()) return;
-    const int r = soon.row;
-    if (p.dh) ry = p.rstd_pre[r];
-    if (p.o && p.post_norm) ro = p.rstd_post[r];
-#pragma unroll
-    for (int e = 0; e < NE; ++e)
-      if (col(e) < p.cols) {
-        if (p.dy) ndy[e] = at<T>(p.dy, r, p.ld_dy)[col(e)];
-        if (p.dh) {
-          ndh[e] = at<T>(p.dh, r, p.ld_dh)[col(e)];
-          ny[e] = at<T>(p.y, r, p.ldy)[col(e)];
-        }
-        if (p.o) no[e] = at<T>(p.o, r, p.ldo)[col(e)];
+  const T *w_post = reinterpret_cast<const T *>(p.w_post);
+  auto col = [&](int e) { return odd_first() + 32 * e; };
+  Walk now(p.per_gate, p.per_item, p.gates, p.split), soon = now, ahead = now;
+  odd_prepare<T>(smem, w, reinterpret_cast<const T *>(p.w_pre), p.cols);
+  auto fetch = [&](char *to) {  // the next row
+    if (ahead.live()) {
+      const int r = ahead.row;
+      odd_copy<T>(to + DY * pitch, p.dy, r, p.ld_dy, p.cols, pitch);
+      if (p.dh) {
+        odd_copy<T>(to + DH * pitch, p.dh, r, p.ld_dh, p.cols, pitch);
+        odd_copy<T>(to + Y * pitch, p.y, r, p.ldy, p.cols, pitch);
       }
+      odd_copy<T>(to + O * pitch, p.o, r, p.ldo, p.cols, pitch);
+      if (gate_with_rows) odd_copy<T>(to + GATE * pitch, p.gate, ahead.item / p.split, p.ldg, p.cols, pitch);
+      ahead.next();
+    }
+    cp_async_commit();
   };
-  auto mask_of = [&](int side) {
-    if (p.drop && soon.live())
-      fill_mask(p.rnd, (uint64_t)soon.row * p.cols, p.cols, masks + side * p.cols, threadIdx.x, blockDim.x);
+  float ry = 0.f, ro = 1.f;  // 1 / rms of the next row
+  auto read_rstd = [&]() {
+    if (!soon.live()) return;
+    if (p.dh) ry = p.rstd_pre[soon.row];
+    if (p.o && p.post_norm) ro = p.rstd_post[soon.row];
   };
+  for (char *to = smem; to != row_end; to += row_step) fetch(to);
+  read_rstd();
+  if (DROP) odd_mask(p.rnd, soon.row, p.cols, masks);
+  float factor[NE], a_pre[NE], a_s[NE];
+#pragma unroll
+  for (int e = 0; e < NE; ++e) factor[e] = a_pre[e] = a_s[e] = post[col(e)] = 0.f;
   auto flush = [&](int item) {  // as in the staged kernel
     if (!p.o || item < 0) return;
     const T *gate = p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
+    float g[NE], d[NE];
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
-      const int c = col(e);
-      if (c >= p.cols) continue;
-      const float s = p.scale * a_s[e], g = gate ? Elem<T>::get(gate[c]) : 0.f;
+      g[e] = gate && col(e) < p.cols ? Elem<T>::get(gate[col(e)]) : 0.f;
+      d[e] = w_post && col(e) < p.cols ? Elem<T>::get(w_post[col(e)]) : 1.f;
+    }
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      const float s = p.scale * a_s[e];
       a_s[e] = 0.f;
-      a_post[e] += gate ? activate(p.act, g) * s : s;
-      if (!p.dgate) continue;
-      const float d = w_post ? s * Elem<T>::get(w_post[c]) : s;
-      if (p.split == 1) at<T>(p.dgate, item, p.ld_dg)[c] = Elem<T>::put(d * slope(p.act, g));
-      else p.ws[2 * (int64_t)gridDim.x * p.cols + (int64_t)item * p.cols + c] = d;
+      d[e] *= s;
+      post[col(e)] += gate ? activate(p.act, g[e]) * s : s;
+    }
+    if (!p.dgate) return;
+    if (p.split == 1) {
+      T *to = at<T>(p.dgate, item, p.ld_dg);
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+        if (col(e) < p.cols) to[col(e)] = Elem<T>::put(d[e] * slope(p.act, g[e]));
+    } else {
+      float *to = p.ws + 2 * (int64_t)gridDim.x * p.cols + (int64_t)item * p.cols;
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+        if (col(e) < p.cols) to[col(e)] = d[e];
     }
   };
-  read();
-  mask_of(0);
-  if (p.drop) __syncthreads();
-  const float ks = p.drop ? p.rnd.keep_scale : 1.f;
+  wait_oldest(ahead_rows);
+  __syncthreads();
+  const float ks = DROP ? p.rnd.keep_scale : 1.f;
+  char *row = smem;
   int half = 0, item = -1, side = 0;
   for (; now.live(); now.next()) {
     const int r = now.row;
     const float cy = ry, co = ro;
-    if (now.item != item) {
-      flush(item);
+    soon.next();
+    read_rstd();
+    if (now.item != item) flush(item);
+    if (now.item != item || gate_with_rows) {
       item = now.item;
       const T *gate = p.gate ? at<T>(p.gate, item / p.split, p.ldg) : nullptr;
-#pragma unroll
-      for (int e = 0; e < NE; ++e)
-        if (col(e) < p.cols) factor[e] = single_factor(p.scale, p.act, gate, w_post, col(e));
+      if (gate_with_rows)
+        gate = reinterpret_cast<const T *>(row + GATE * pitch + odd_shift<T>(p.gate, item / p.split, p.ldg));
+      odd_factors<T>(p.scale, p.act, gate, w_post, p.cols, factor);
     }
-    float g0[NE], yn[NE], hv[NE], ov[NE], s[4] = {0.f, 0.f, 0.f, 0.f};
+    const char *rdy = row + DY * pitch + odd_shift<T>(p.dy, r, p.ld_dy), *rdh = row + DH * pitch;
+    const char *ryy = row + Y * pitch, *rov = row + O * pitch + odd_shift<T>(p.o, r, p.ldo);
+    if (p.dh) rdh += odd_shift<T>(p.dh, r, p.ld_dh), ryy += odd_shift<T>(p.y, r, p.ldy);
+    const uint8_t *mask = masks + side * mask_pitch + (((uint32_t)r * (uint32_t)p.cols) & 3u);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
     uint32_t kept = 0u;
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
-      hv[e] = Elem<T>::get(ndh[e]);
-      yn[e] = Elem<T>::get(ny[e]) * cy;
-      ov[e] = Elem<T>::get(no[e]);
-      const float t = hv[e] * w[e];
-      g0[e] = Elem<T>::get(ndy[e]) + cy * t;
-      s[0] += t * yn[e];
-      if (!p.drop || (col(e) < p.cols && masks[side * p.cols + col(e)])) {
-        kept |= 1u << e;
-        const float q = factor[e] * ov[e];
-        s[1] += g0[e] * q;
-        s[2] += yn[e] * q;
-      }
+      const int c = col(e);
+      const float yn = odd_get<T>(ryy, c) * cy, t = odd_get<T>(rdh, c) * Elem<T>::get(w[c]);
+      const float g0 = odd_get<T>(rdy, c) + cy * t;
+      if (DROP) kept |= (uint32_t)mask[c] << e;
+      const float q = !DROP || ((kept >> e) & 1u) ? factor[e] * odd_get<T>(rov, c) : 0.f;
+      s[0] += t * yn;
+      s[1] += g0 * q;
+      s[2] += yn * q;
     }
-    soon.next();
-    read();
     side ^= 1;
-    mask_of(side);
+    if (DROP && soon.live()) odd_mask(p.rnd, soon.row, p.cols, masks + side * mask_pitch);
     block_sums4(s, buf, warp, warps, half);
-    if (warps == 1) __syncwarp();
     const float m1 = cy * s[0] * inv;
     const float m2 = p.post_norm ? ks * co * co * co * (s[1] - m1 * s[2]) * inv : 0.f;
     const float kr = ks * co;
+    T *const dx_row = p.dx ? at<T>(p.dx, r, p.ld_dx) : nullptr, *const do_row = p.dout ? at<T>(p.dout, r, p.ld_do) : nullptr;
 #pragma unroll
-    for (int e = 0; e < NE; ++e)
-      if (col(e) < p.cols) {
-        const int c = col(e);
-        a_pre[e] += hv[e] * yn[e];
-        const float dx = g0[e] - yn[e] * m1;
-        const float d = (kept >> e) & 1u ? dx * kr : 0.f;
-        a_s[e] += d * ov[e];
-        if (p.dx) at<T>(p.dx, r, p.ld_dx)[c] = Elem<T>::put(dx);
-        if (p.dout) at<T>(p.dout, r, p.ld_do)[c] = Elem<T>::put(d * factor[e] - ov[e] * m2);
-      }
+    for (int e = 0; e < NE; ++e) {
+      const int c = col(e);
+      const bool in = c < p.cols;
+      const float hv = odd_get<T>(rdh, c), yn = odd_get<T>(ryy, c) * cy, ov = odd_get<T>(rov, c);
+      const float dx = odd_get<T>(rdy, c) + cy * (hv * Elem<T>::get(w[c])) - yn * m1;
+      a_pre[e] += hv * yn;
+      const float d = !DROP || ((kept >> e) & 1u) ? dx * kr : 0.f;
+      a_s[e] += d * ov;
+      const T vx = Elem<T>::put(dx), vo = Elem<T>::put(d * factor[e] - ov * m2);
+      if (in && dx_row) dx_row[c] = vx;
+      if (in && do_row) do_row[c] = vo;
+    }
+    if (ahead_rows > 1) wait_oldest(ahead_rows - 1);  // the next row
+    __syncthreads();  // it has come, and this one has been read
+    fetch(row);
+    row = row + row_step == row_end ? smem : row + row_step;
+    if (ahead_rows == 1) {
+      cp_async_wait<0>();
+      __syncthreads();
+    }
   }
   flush(item);
 #pragma unroll
   for (int e = 0; e < NE; ++e)
     if (col(e) < p.cols) {
-      if (p.dw_pre) p.ws[(int64_t)blockIdx.x * p.cols + col(e)] = a_pre[e];
-      if (p.dw_post) p.ws[((int64_t)gridDim.x + blockIdx.x) * p.cols + col(e)] = a_post[e];
+      const int c = col(e);
+      if (gridDim.x == 1) {  // the sums are whole: no launch to add partials
+        if (p.dw_pre) reinterpret_cast<T *>(p.dw_pre)[c] = Elem<T>::put(a_pre[e]);
+        if (p.dw_post) reinterpret_cast<T *>(p.dw_post)[c] = Elem<T>::put(post[c]);
+        continue;
+      }
+      if (p.dw_pre) p.ws[(int64_t)blockIdx.x * p.cols + c] = a_pre[e];
+      if (p.dw_post) p.ws[((int64_t)gridDim.x + blockIdx.x) * p.cols + c] = post[c];
     }
 }
 
@@ -1120,10 +1244,25 @@ static StagedShape staged_shape(int cols) {
 static int64_t staged_blocks(int64_t rows, const StagedShape &s, int num_sms) {
   return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * s.per_sm));
 }
-// Single elements: columns that fit 512 threads, and resident blocks (512 threads an SM)
-constexpr int ODD_BWD_COLS = 8 * 512, ODD_FWD_COLS = 16 * 512;
+// An odd rows' blocks: 64 registers a thread, so up to 1024 threads an SM
+static int odd_threads(int cols) { return threads_of(cols, ODD_EACH); }
+static int odd_per_sm(int threads) { return std::max(1, 1024 / threads); }
 static int64_t odd_blocks(int64_t rows, int threads, int num_sms) {
-  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * std::max(1, 512 / threads)));
+  return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * odd_per_sm(threads)));
+}
+// As launch_staged; a block also has its 1 KB for the sums and 1 KB reserved
+template <typename P>
+static cudaError_t launch_odd(void (*kern)(P, int, int), const P &p, int arrays, int pitch, size_t fixed, int blocks,
+                              int threads, cudaStream_t st) {
+  const size_t room = STAGED_SMEM / odd_per_sm(threads) - 2048;
+  const int with_rows = p.gate && p.per_gate <= GATE_WITH_ROWS && fixed + (size_t)pitch * (arrays + 1) <= room;
+  const size_t row = (size_t)pitch * (arrays + with_rows);
+  const int ahead = room < fixed + 2 * row ? 1 : room < fixed + 3 * row ? 2 : 3;
+  const size_t bytes = fixed + ahead * row;
+  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (err != cudaSuccess) return err;
+  kern<<<blocks, threads, bytes, st>>>(p, with_rows, ahead);
+  return cudaGetLastError();
 }
 // f(group count, threads' limit) as types
 template <typename F>
@@ -1173,16 +1312,14 @@ static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
       });
     }
   } else {
-    if (p.cols <= ODD_FWD_COLS) {
-      const int ne = p.cols <= ODD_BWD_COLS ? 8 : 16, t = threads_of(p.cols, ne);
-      const int64_t most = odd_blocks(p.rows, t, num_sms);
+    if (p.cols <= ODD_COLS) {
+      const int threads = odd_threads(p.cols);
+      const int64_t most = odd_blocks(p.rows, threads, num_sms);
       p.split = (int)split_of(p.gates, p.per_gate, most);
       p.per_item = (p.per_gate + p.split - 1) / p.split;
-      const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split);
-      const size_t smem = p.drop ? 2 * p.cols : 0;
-      auto kern = ne == 8 ? block_norm_odd_kernel<T, 8> : block_norm_odd_kernel<T, 16>;
-      kern<<<blocks, t, smem, st>>>(p);
-      return cudaGetLastError();
+      const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split), pitch = odd_pitch<T>(threads);
+      return launch_odd(p.drop ? block_norm_odd_kernel<T, true> : block_norm_odd_kernel<T, false>, p, 2, pitch,
+                        pitch + (p.drop ? 2 * odd_mask_pitch(threads) : 0), blocks, threads, st);
     }
   }
   auto kern = block_norm_kernel<T, V>;
@@ -1195,20 +1332,20 @@ static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
 
 // The backward's launch: threads and blocks for rows in vectors of V
 struct BwdPlan {
-  bool staged;
-  int threads, nv;  // nv: single elements a thread of the odd rows' kernel (0: the general one)
+  bool staged, odd;  // neither: the general kernel
+  int threads;
   int64_t blocks;
 };
 static BwdPlan plan_bwd(int64_t rows, int cols, int V, int num_sms) {
   if (V > 1 && cols <= STAGED_COLS) {
     const StagedShape s = staged_shape(cols);
-    return BwdPlan{true, s.threads, 0, staged_blocks(rows, s, num_sms)};
+    return BwdPlan{true, false, s.threads, staged_blocks(rows, s, num_sms)};
   }
-  if (V == 1 && cols <= ODD_BWD_COLS) {
-    const int t = threads_of(cols, 8);
-    return BwdPlan{false, t, 8, odd_blocks(rows, t, num_sms)};
+  if (V == 1 && cols <= ODD_COLS) {
+    const int threads = odd_threads(cols);
+    return BwdPlan{false, true, threads, odd_blocks(rows, threads, num_sms)};
   }
-  return BwdPlan{false, 512, 0, std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * 2))};
+  return BwdPlan{false, false, 512, std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms * 2))};
 }
 
 template <typename T, int V>
@@ -1233,8 +1370,12 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
       block_norm_bwd_kernel<T, V><<<blocks, plan.threads, 0, st>>>(p);
     }
   } else {
-    if (plan.nv) {
-      block_norm_bwd_odd_kernel<T, 8><<<blocks, plan.threads, p.drop ? 2 * p.cols : 0, st>>>(p);
+    if (plan.odd) {
+      const int pitch = odd_pitch<T>(plan.threads);
+      err = launch_odd(p.drop ? block_norm_bwd_odd_kernel<T, true> : block_norm_bwd_odd_kernel<T, false>, p, 4, pitch,
+                       pitch + 4 * ODD_EACH * plan.threads + (p.drop ? 2 * odd_mask_pitch(plan.threads) : 0), blocks,
+                       plan.threads, st);
+      if (err != cudaSuccess) return err;
     } else {
       const size_t smem = p.drop ? p.cols : 0;
       err = cudaFuncSetAttribute(block_norm_bwd_kernel<T, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -1245,7 +1386,7 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   const bool gates = p.dgate && p.split > 1;
-  if (!(plan.staged && blocks == 1) && (p.dw_pre || p.dw_post || gates))
+  if (!((plan.staged || plan.odd) && blocks == 1) && (p.dw_pre || p.dw_post || gates))
     err = launch_pdl(sum_partials_kernel<T>, dim3((p.cols + 31) / 32, 2 + (gates ? p.gates : 0)),
                      dim3(32 * SUM_WARPS), 0, st, p,
                      blocks);
@@ -1272,7 +1413,7 @@ size_t block_norm_workspace(int64_t rows, int cols, int64_t gates, int num_sms) 
     const int64_t split = gates ? split_of(gates, rows / gates, plan.blocks) : 1;
     // gate partials: where several blocks share a gate row, or (rows beyond
     // the register budget) the sums live in memory
-    const int64_t items = gates && (split > 1 || (!plan.staged && plan.nv == 0)) ? gates * split : 0;
+    const int64_t items = gates && (split > 1 || (!plan.staged && !plan.odd)) ? gates * split : 0;
     best = std::max(best, (size_t)(2 * plan.blocks + items) * cols * sizeof(float));
   }
   return best;

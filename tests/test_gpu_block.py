@@ -207,6 +207,14 @@ NORMS = [
     (1200, 512, 300, "tanh", 0.1, True, True, True, True, True),
     (900, 264, 900, "sigmoid", 0.0, True, True, True, True, True),
     (310, 8192, 5, "tanh", 0.1, True, True, True, True, True),
+    # many rows a block, of changing alignment
+    (1300, 4095, 1, "tanh", 0.1, True, True, True, True, True),
+    (640, 8191, 2, "sigmoid", 0.1, True, True, True, True, True),
+    (700, 6001, 700, "tanh", 0.2, True, False, True, True, True),
+    (3000, 1001, 750, "none", 0.1, True, True, True, True, True),
+    (20000, 31, 4, "sigmoid", 0.5, False, True, True, True, True),
+    (500, 7167, 0, "none", 0.0, True, True, True, False, True),
+    (810, 2047, 0, "none", 0.1, True, True, False, True, False),
 ]
 
 
