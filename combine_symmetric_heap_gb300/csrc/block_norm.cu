@@ -387,15 +387,21 @@ struct Walk {
 };
 
 // A thread's columns: NG groups of 8.  16-bit types: a group is one 16-byte
-// vector; fp32: two.  A thread's vectors lie a block's width apart in a row, and
-// MAXT words of 16 bytes apart in shared memory.
-template <typename T, int NG_, int MAXT_>
+// vector; fp32: two.  A thread's vectors lie a warp's width apart in a row
+// (NEAR: constant offsets) or a block's, and MAXT words of 16 bytes apart in
+// shared memory.  Near is faster where instructions count (16384 x 4096 forward
+// 133 -> 129 us, 8192 x 7168 backward 198 -> 192, 150 -> 144 without dropout), but
+// not in the forward without dropout, which is bound by memory (89 -> 94 us).
+template <typename T, int NG_, int MAXT_, bool NEAR>
 struct Columns {
   static constexpr int NG = NG_, MAXT = MAXT_;
   static constexpr int PER = sizeof(T) / 2;  // vectors of a group
   static constexpr int NV = NG * PER;
   static constexpr int W = 16 / sizeof(T);   // columns of a vector
-  static __device__ __forceinline__ int vector(int j) { return ((int)threadIdx.x + j * (int)blockDim.x) * W; }
+  static __device__ __forceinline__ int vector(int j) {
+    const int t = threadIdx.x;
+    return (NEAR ? t / 32 * (32 * NV) + (t & 31) + 32 * j : t + j * (int)blockDim.x) * W;
+  }
   static __device__ __forceinline__ int quad(int g, int k) { return vector(g * PER + k / (W / 4)) + 4 * (k % (W / 4)); }
   // place of vector j of array a in a row's shared memory, in bytes
   static __device__ __forceinline__ constexpr int place(int a, int j) { return (a * NV + j) * MAXT * 16; }
@@ -484,7 +490,7 @@ __device__ __forceinline__ void wait_oldest(int ahead) {
 // parts) y^2 is summed over again.
 template <typename T, bool DROP, int NG, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
-  using C = Columns<T, NG, MAXT>;
+  using C = Columns<T, NG, MAXT, DROP>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float buf[2 * 128];
   enum { X, O, GATE };
@@ -614,7 +620,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, in
 // of scale act S and dgate = scale act' w_post S follow.
 template <typename T, bool DROP, int NG, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
-  using C = Columns<T, NG, MAXT>;
+  using C = Columns<T, NG, MAXT, true>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float buf[2 * 128];
   enum { DY, DH, Y, O, GATE };
@@ -1305,7 +1311,7 @@ static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
       p.per_item = (p.per_gate + p.split - 1) / p.split;
       const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split);
       return with_shape(s, [&](auto groups, auto threads) {
-        using C = Columns<T, decltype(groups)::value, decltype(threads)::value>;
+        using C = Columns<T, decltype(groups)::value, decltype(threads)::value, true>;  // (for the sizes)
         return launch_staged<C, Fwd>(p.drop ? block_norm_staged_kernel<T, true, C::NG, C::MAXT>
                                             : block_norm_staged_kernel<T, false, C::NG, C::MAXT>,
                                      p, 2, C::row_bytes(1), p.gate && p.per_gate <= GATE_WITH_ROWS, blocks, s, st);
@@ -1359,7 +1365,7 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
     if (plan.staged) {
       const StagedShape s = staged_shape(p.cols);
       err = with_shape(s, [&](auto groups, auto threads) {
-        using C = Columns<T, decltype(groups)::value, decltype(threads)::value>;
+        using C = Columns<T, decltype(groups)::value, decltype(threads)::value, true>;  // (for the sizes)
         return launch_staged<C, Bwd>(p.drop ? block_norm_bwd_staged_kernel<T, true, C::NG, C::MAXT>
                                             : block_norm_bwd_staged_kernel<T, false, C::NG, C::MAXT>,
                                      p, 4, C::row_bytes(1) + 2 * C::NG * C::MAXT * 16,
