@@ -21,9 +21,9 @@
 // general (any length, the row walked again out of L2).
 //
 // Measured (bf16, dropout 0.1, a GB300 whose copy rate is 6.69 TB/s): forward
-// with both norms, 16384 x 4096, 133 us (4.0 TB/s; 88 us and 6.1 TB/s without
+// with both norms, 16384 x 4096, 129 us (4.2 TB/s; 89 us and 6.1 TB/s without
 // dropout), bound by the generator's multiplies on top of the bytes; backward,
-// 8192 x 7168, 197 us (3.6 TB/s; 151 us and 4.7 TB/s without dropout), bound by
+// 8192 x 7168, 192 us (3.7 TB/s; 134 us and 5.3 TB/s without dropout), bound by
 // the latency of a row's chain: its 57 KB a row and 16 columns' sums a thread
 // leave an SM one block.  Rows off 16-byte boundaries: forward 16384 x 4095
 // 218 us, backward 8192 x 7167 294 us.
@@ -489,7 +489,8 @@ __device__ __forceinline__ void wait_oldest(int ahead) {
 // rstd_o x q + rstd_o^2 q^2.  Where those cancel (y shorter than a third of its
 // parts) y^2 is summed over again.
 template <typename T, bool DROP, int NG, int MAXT>
-__global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
+__global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 0)
+    block_norm_staged_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
   using C = Columns<T, NG, MAXT, DROP>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float buf[2 * 128];
@@ -617,9 +618,12 @@ __global__ void __launch_bounds__(MAXT) block_norm_staged_kernel(const Fwd p, in
 
 // Backward.  Per column the block keeps two sums: of dh yn (dw_pre), and over
 // an item's rows S = sum drop dx on, from which both dw_post = sum over gates
-// of scale act S and dgate = scale act' w_post S follow.
+// of scale act S and dgate = scale act' w_post S follow.  (One block an SM, said
+// to the compiler: it takes all registers and reads further ahead, 134 against 144
+// us at 8192 x 7168 without dropout.  With dropout it had them anyway.)
 template <typename T, bool DROP, int NG, int MAXT>
-__global__ void __launch_bounds__(MAXT) block_norm_bwd_staged_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
+__global__ void __launch_bounds__(MAXT, !DROP && NG == 2 ? 1 : 0)
+    block_norm_bwd_staged_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
   using C = Columns<T, NG, MAXT, true>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float buf[2 * 128];
@@ -1234,17 +1238,21 @@ static int threads_of(int cols, int each) { return ((cols + each - 1) / each + 3
 // to 64 or 256 threads, which sets the shared memory's layout), 16 beyond.  At
 // 4096 columns, forward, three resident blocks of 256 threads instead of two
 // were slower (102 against 88 us without dropout, the same with it), so were 8
-// columns a thread (94 against 88, 145 against 133).
+// columns a thread (94 against 88, 145 against 133).  Beyond 4096 columns, two
+// blocks of up to 384 threads at 80 registers instead of one, in the forward of
+// 16-bit types (`two`): 8192 x 5120 92 against 107 us, 61 against 74 without
+// dropout; 8192 x 6144 101 against 109.  fp32 loses (6144: 145 against 137), the
+// backward too (5120: 170 against 158): too few registers.
 struct StagedShape {
   int groups, max_threads, threads, per_sm;
 };
-static StagedShape staged_shape(int cols) {
+static StagedShape staged_shape(int cols, bool two) {
   StagedShape s;
   s.groups = cols <= 2048 ? 1 : 2;
-  s.max_threads = cols <= 512 ? 64 : cols <= 2048 ? 256 : 512;
+  s.max_threads = cols <= 512 ? 64 : cols <= 2048 ? 256 : two && cols > 4096 && cols <= 6144 ? 384 : 512;
   s.threads = (cols + 256 * s.groups - 1) / (256 * s.groups) * 32;
   // resident blocks an SM: by their registers, 768 threads of small blocks, else 512
-  s.per_sm = std::max(1, (s.groups == 1 ? 768 : 512) / s.threads);
+  s.per_sm = std::max(1, (s.groups == 1 || s.max_threads == 384 ? 768 : 512) / s.threads);
   return s;
 }
 static int64_t staged_blocks(int64_t rows, const StagedShape &s, int num_sms) {
@@ -1271,11 +1279,13 @@ static cudaError_t launch_odd(void (*kern)(P, int, int), const P &p, int arrays,
   return cudaGetLastError();
 }
 // f(group count, threads' limit) as types
-template <typename F>
+template <bool TWO, typename F>
 static auto with_shape(const StagedShape &s, F f) {
   using std::integral_constant;
   if (s.max_threads == 64) return f(integral_constant<int, 1>{}, integral_constant<int, 64>{});
   if (s.max_threads == 256) return f(integral_constant<int, 1>{}, integral_constant<int, 256>{});
+  if constexpr (TWO)
+    if (s.max_threads == 384) return f(integral_constant<int, 2>{}, integral_constant<int, 384>{});
   return f(integral_constant<int, 2>{}, integral_constant<int, 512>{});
 }
 // Launch with rows copied ahead (up to three, as many as leave room for the
@@ -1305,12 +1315,13 @@ template <typename T, int V>
 static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
   if constexpr (V > 1) {
     if (p.cols <= STAGED_COLS) {
-      const StagedShape s = staged_shape(p.cols);
+      constexpr bool two = sizeof(T) == 2;
+      const StagedShape s = staged_shape(p.cols, two);
       const int64_t most = staged_blocks(p.rows, s, num_sms);
       p.split = (int)split_of(p.gates, p.per_gate, most);
       p.per_item = (p.per_gate + p.split - 1) / p.split;
       const int blocks = (int)std::min<int64_t>(most, (int64_t)p.gates * p.split);
-      return with_shape(s, [&](auto groups, auto threads) {
+      return with_shape<two>(s, [&](auto groups, auto threads) {
         using C = Columns<T, decltype(groups)::value, decltype(threads)::value, true>;  // (for the sizes)
         return launch_staged<C, Fwd>(p.drop ? block_norm_staged_kernel<T, true, C::NG, C::MAXT>
                                             : block_norm_staged_kernel<T, false, C::NG, C::MAXT>,
@@ -1344,7 +1355,7 @@ struct BwdPlan {
 };
 static BwdPlan plan_bwd(int64_t rows, int cols, int V, int num_sms) {
   if (V > 1 && cols <= STAGED_COLS) {
-    const StagedShape s = staged_shape(cols);
+    const StagedShape s = staged_shape(cols, false);
     return BwdPlan{true, false, s.threads, staged_blocks(rows, s, num_sms)};
   }
   if (V == 1 && cols <= ODD_COLS) {
@@ -1363,8 +1374,8 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
   cudaError_t err = cudaSuccess;
   if constexpr (V > 1) {
     if (plan.staged) {
-      const StagedShape s = staged_shape(p.cols);
-      err = with_shape(s, [&](auto groups, auto threads) {
+      const StagedShape s = staged_shape(p.cols, false);
+      err = with_shape<false>(s, [&](auto groups, auto threads) {
         using C = Columns<T, decltype(groups)::value, decltype(threads)::value, true>;  // (for the sizes)
         return launch_staged<C, Bwd>(p.drop ? block_norm_bwd_staged_kernel<T, true, C::NG, C::MAXT>
                                             : block_norm_bwd_staged_kernel<T, false, C::NG, C::MAXT>,
