@@ -435,7 +435,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PRODUCT_THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// weight gradient kernel: tile (e, f, c) = 256 x 256 of dw[e], K = cnt_e rows
+// weight gradient kernel: tile (e, f, c) = 256 x tile_c of dw[e], K = cnt_e rows.
+// tile_c is 256, or 128 where every pair still has one tile at most: the time is
+// then one tile's K axis, whose blocks take less (one group of 56548 rows, 1096 x
+// 872: 371 -> 285 us; 8 groups, 4096 rows, 512 x 512: 18.4 -> 15.4; the wide
+// tile's are bound by the pair's tensor cores, the narrow one's by six loads in
+// flight).  With more tiles the wide one's operands are read less often.
 // ---------------------------------------------------------------------------
 // Row boxes of a K block: a group's last block loads 16, 32 or 64 rows,
 // whichever holds what is left of its whole steps.
@@ -584,7 +589,7 @@ __device__ __forceinline__ void stage_row(uint8_t *box, int lane, const uint32_t
 // shape (256 experts, 2048 x 7168, bf16) took 4.57 ms that way.
 template <int OT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
-    grouped_wgrad_kernel(const Groups g, const Out o, int F, int C, int fp16, int add, int by_tma,
+    grouped_wgrad_kernel(const Groups g, const Out o, int F, int C, int fp16, int add, int by_tma, int tile_c,
                          const __grid_constant__ WMaps tm_dy, const __grid_constant__ WMaps tm_x,
                          const __grid_constant__ CUtensorMap tm_dw) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -638,8 +643,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
-  const int nf = (F + 255) / 256, nc = (C + 255) / 256;
+  const int nf = (F + 255) / 256, nc = (C + tile_c - 1) / tile_c;
   const int total = g.G * nf * nc;
+  const int own_c = tile_c / 2;  // columns of x that this CTA stages: one or two chunks
   WWalk walk(g, nf, nc);
 
   if (wid == 0) {
@@ -650,7 +656,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
       for (int i = 0, t; ok && (t = pair_tile(i, pair, npairs)) < total; ++i) {
         const WTile &ti = walk.at(t);
         const int whole = ti.cnt & ~(UK - 1);
-        const int f0 = ti.f * 256 + (int)rank * 128, c0 = ti.c * 256 + (int)rank * 128;
+        const int f0 = ti.f * 256 + (int)rank * 128, c0 = ti.c * tile_c + (int)rank * own_c;
         for (int k0 = 0; k0 < whole; k0 += BK) {
           if (!(ok = bar_wait(&rg.empty[rg.stage], rg.phase ^ 1u, ctl))) break;
           uint8_t *sb = rg.base + (size_t)rg.stage * WG_STAGE_BYTES;
@@ -658,10 +664,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
           const int box = left > 32 ? 2 : left > 16 ? 1 : 0;
           const CUtensorMap *my = &tm_dy.m[box], *mx = &tm_x.m[box];
           const uint32_t bar = full_leader + (uint32_t)(rg.stage * sizeof(uint64_t));
-          if (rank == 0) mbar_arrive_expect_tx(&rg.full[rg.stage], 8u * 128u * (16u << box));  // both CTAs' chunks
+          if (rank == 0) mbar_arrive_expect_tx(&rg.full[rg.stage], (4u + (uint32_t)tile_c / 64u) * 128u * (16u << box));  // both CTAs' chunks
           for (int h = 0; h < 2; ++h) {
             tma_load_3d_pair(sb + h * CHUNK_BYTES, my, bar, f0 + h * 64, row, ti.d);
-            tma_load_3d_pair(sb + A_BYTES + h * CHUNK_BYTES, mx, bar, c0 + h * 64, row, ti.d);
+            if (h * 64 < own_c) tma_load_3d_pair(sb + A_BYTES + h * CHUNK_BYTES, mx, bar, c0 + h * 64, row, ti.d);
           }
           rg.next();
         }
@@ -671,7 +677,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
     if (lane == 0 && rank == 0) {
       // ---------------------------------------------------- MMA issuer (leader)
       uint32_t ne[2] = {0, 0}, nr = 0;  // accumulators acquired, side buffers read
-      const uint32_t id = idesc(fp16, true, true, 256);
+      const uint32_t id = idesc(fp16, true, true, tile_c);
       int b = 0;
       bool ok = true;
       for (int i = 0, t; ok && (t = pair_tile(i, pair, npairs)) < total; ++i) {
@@ -715,14 +721,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
     auto load = [&](int i, uint32_t n) {  // tile i's rows as use n of the side buffers
       const WTile &ti = walk.at(pair_tile(i, pair, npairs));
       const int j = n & 1, row = ti.row0 + (ti.cnt & ~(UK - 1));
-      const int f0 = ti.f * 256 + (int)rank * 128, c0 = ti.c * 256 + (int)rank * 128;
+      const int f0 = ti.f * 256 + (int)rank * 128, c0 = ti.c * tile_c + (int)rank * own_c;
       if (!__all_sync(0xffffffffu, bar_wait(&rest_empty[j], ((n >> 1) & 1u) ^ 1u, ctl))) return false;
       if (lane == 0) {
         uint8_t *sb = rest + j * REST_BYTES;
-        mbar_arrive_expect_tx(&rest_in[j], REST_BYTES);
+        mbar_arrive_expect_tx(&rest_in[j], (2u + (uint32_t)own_c / 64u) * REST_CHUNK);
         for (int h = 0; h < 2; ++h) {
           tma_load_3d(sb + h * REST_CHUNK, &tm_dy.m[0], &rest_in[j], f0 + h * 64, row, ti.d);
-          tma_load_3d(sb + (2 + h) * REST_CHUNK, &tm_x.m[0], &rest_in[j], c0 + h * 64, row, ti.d);
+          if (h * 64 < own_c) tma_load_3d(sb + (2 + h) * REST_CHUNK, &tm_x.m[0], &rest_in[j], c0 + h * 64, row, ti.d);
         }
       }
       return true;
@@ -768,13 +774,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
     int b = 0;
     for (int i = 0, t; (t = pair_tile(i, pair, npairs)) < total; ++i) {
       const WTile &ti = walk.at(t);
-      const int fw = ti.f * 256 + (int)rank * 128 + q * 32, f = fw + lane, c0 = ti.c * 256 + half * 128;  // the warp's rows, columns
-      const int cols = min(128, C - c0);
+      const int fw = ti.f * 256 + (int)rank * 128 + q * 32, f = fw + lane, c0 = ti.c * tile_c + half * own_c;  // the warp's rows, columns
+      const int cols = min(own_c, C - c0);
       const bool empty = ti.cnt == 0;  // zeros, or nothing to add
       if (empty && add) continue;
       if (!empty && !__all_sync(0xffffffffu, bar_wait(&acc_full[b], used[b]++ & 1u, ctl))) break;
       tc_fence_after();
-      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS + half * 128);
+      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS + half * own_c);
       if (by_tma) {
 #pragma unroll 1
         for (int c = 0; c < cols; c += 32) {
@@ -919,8 +925,10 @@ cudaError_t launch_grouped_wgrad(const sym_groups &sg, int fp16, const sym_rows 
   if (by_tma && !encode(&mo, reinterpret_cast<uint64_t>(dw), x.cols, dy.cols, sg.groups, dw_ld, gs, fp32 ? 16 : 32, 32, fp32,
                         CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
+  const int64_t narrow = (int64_t)sg.groups * ((dy.cols + 255) / 256) * ((x.cols + 127) / 128);
+  const int tile_c = narrow <= num_sms / 2 ? 128 : 256;
   auto go = [&](auto kern) {
-    return launch(kern, WGRAD_THREADS, smem, num_sms, st, g, o, dy.cols, x.cols, fp16, add, by_tma, md, mx, mo);
+    return launch(kern, WGRAD_THREADS, smem, num_sms, st, g, o, dy.cols, x.cols, fp16, add, by_tma, tile_c, md, mx, mo);
   };
   return fp32 ? go(grouped_wgrad_kernel<OUT_FP32>)
               : fp16 ? go(grouped_wgrad_kernel<OUT_FP16>) : go(grouped_wgrad_kernel<OUT_BF16>);

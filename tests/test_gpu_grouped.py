@@ -80,6 +80,11 @@ WGRADS = [
     ([700, 0, 2, 30], 4, 5, 264, 520, 8, torch.bfloat16),
     ([0, 0], 1, 4, 64, 64, 0, torch.bfloat16),
     ([(7 * i) % 41 for i in range(1024)], 64, 0, 64, 72, 0, torch.bfloat16),
+    # tiles of 256 columns (more than one for each pair at 128), and of 128 with long and ragged groups
+    (RAGGED * 3, 2, 3, 712, 520, 8, torch.bfloat16),
+    ([300, 5, 0, 77, 130, 64, 9, 16], 4, 2, 1096, 776, 0, torch.float16),
+    ([2000, 1999], 1, 0, 392, 264, 0, torch.bfloat16),
+    ([150, 33, 0, 401], 1, 2, 840, 136, 8, torch.float16),
 ]
 
 
