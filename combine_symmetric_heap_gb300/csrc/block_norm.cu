@@ -907,13 +907,10 @@ template <typename T>
 __device__ __forceinline__ float odd_get(const char *row, int c) {
   return Elem<T>::get(*reinterpret_cast<const T *>(row + c * (int)sizeof(T)));
 }
-// Zeros in the rows, w_pre (or ones) behind them
-template <typename T>
-__device__ __forceinline__ void odd_prepare(char *rows, T *w, const T *w_pre, int cols) {
-  for (char *q = rows + 16 * threadIdx.x; q < reinterpret_cast<char *>(w); q += 16 * blockDim.x)
+// Zeros in the rows
+__device__ __forceinline__ void odd_clear(char *rows, const char *end) {
+  for (char *q = rows + 16 * threadIdx.x; q < end; q += 16 * blockDim.x)
     *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
-  for (int c = threadIdx.x; c < ODD_EACH * (int)blockDim.x; c += blockDim.x)
-    w[c] = w_pre && c < cols ? w_pre[c] : Elem<T>::put(1.f);
   __syncthreads();
 }
 // scale * act(gate) * w_post of this thread's columns (`gate`: in memory, or with the row)
@@ -947,7 +944,7 @@ __global__ void __launch_bounds__(1024) block_norm_odd_kernel(const Fwd p, int g
   const T *w_post = reinterpret_cast<const T *>(p.w_post);
   auto col = [&](int e) { return odd_first() + 32 * e; };
   Walk now(p.per_gate, p.per_item, p.gates, p.split), soon = now, ahead = now;
-  odd_prepare<T>(smem, w, reinterpret_cast<const T *>(p.w_pre), p.cols);
+  odd_clear(smem, row_end);
   auto fetch = [&](char *to) {  // the next row
     if (ahead.live()) {
       odd_copy<T>(to + X * pitch, p.x, ahead.row, p.ldx, p.cols, pitch);
@@ -962,6 +959,9 @@ __global__ void __launch_bounds__(1024) block_norm_odd_kernel(const Fwd p, int g
   float factor[NE];
 #pragma unroll
   for (int e = 0; e < NE; ++e) factor[e] = 0.f;
+  const T *w_pre = reinterpret_cast<const T *>(p.w_pre);
+#pragma unroll
+  for (int e = 0; e < NE; ++e) w[col(e)] = w_pre && col(e) < p.cols ? w_pre[col(e)] : Elem<T>::put(1.f);
   wait_oldest(ahead_rows);
   __syncthreads();
   char *row = smem;
@@ -1051,7 +1051,10 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_odd_kernel(const Bwd p, i
   const T *w_post = reinterpret_cast<const T *>(p.w_post);
   auto col = [&](int e) { return odd_first() + 32 * e; };
   Walk now(p.per_gate, p.per_item, p.gates, p.split), soon = now, ahead = now;
-  odd_prepare<T>(smem, w, reinterpret_cast<const T *>(p.w_pre), p.cols);
+  odd_clear(smem, row_end);
+  const T *w_pre = reinterpret_cast<const T *>(p.w_pre);
+  for (int c = threadIdx.x; c < NE * (int)blockDim.x; c += blockDim.x)
+    w[c] = w_pre && c < p.cols ? w_pre[c] : Elem<T>::put(1.f);
   auto fetch = [&](char *to) {  // the next row
     if (ahead.live()) {
       const int r = ahead.row;
