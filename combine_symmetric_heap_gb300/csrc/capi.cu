@@ -41,6 +41,9 @@ cudaError_t launch_grouped_matmul(const sym_groups &g, int fp16, const sym_rows 
 bool few_rows_product(const sym_groups &g, const sym_rows &x, int trans);
 cudaError_t launch_few_rows(const sym_groups &g, int fp16, const sym_rows &x, const void *w, int64_t w_group,
                             int64_t w_ld, int trans, const sym_rows &out, int num_sms, cudaStream_t st);
+bool thin_product(const sym_groups &g, const sym_rows &x, const sym_rows &out, int trans, int num_sms);
+cudaError_t launch_thin_product(const sym_groups &g, int fp16, const sym_rows &x, const void *w, int64_t w_group,
+                                int64_t w_ld, int trans, const sym_rows &out, int num_sms, cudaStream_t st);
 cudaError_t launch_grouped_wgrad(const sym_groups &g, int fp16, const sym_rows &dy, const sym_rows &x, void *dw,
                                  int64_t dw_group, int64_t dw_ld, int out_type, int add, int num_sms,
                                  cudaStream_t st);
@@ -403,7 +406,9 @@ int moe_grouped_matmul(const sym_groups *g, int dtype, const sym_rows *x, const 
   if (x->rows == 0) return SYM_OK;
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return SYM_ECUDA;
-  const auto launch = few_rows_product(*g, *x, trans) ? launch_few_rows : launch_grouped_matmul;
+  const auto launch = few_rows_product(*g, *x, trans)                ? launch_few_rows
+                      : thin_product(*g, *x, *out, trans, sms) ? launch_thin_product
+                                                               : launch_grouped_matmul;
   return from_cuda(launch(with_timeout(g), dtype == SYM_FP16, *x, w, w_group_stride, w_ld, trans, *out, sms,
                           (cudaStream_t)stream));
 }

@@ -161,6 +161,60 @@ def test_bad_groups_among_few_rows(rows, trans):
     assert bool((out[2:] == 7.0).all()) and not bool((out[:2] == 7.0).any(1).all())
 
 
+TENS = [  # counts, C, F
+    ([9], 7168, 2048),
+    ([16], 64, 16),
+    ([13], 1001, 70),
+    ([0, 12, 0], 37, 1000),
+    ([17, 0, 0, 15], 520, 264),
+    ([1, 9, 8, 4, 10], 136, 130),
+    ([3, 0, 2, 2, 1, 1, 0, 3], 328, 9),
+    ([0, 0, 31, 0], 2056, 4096),
+    ([10], 96, 5000),
+    ([0] * 60 + [5, 0, 7, 1], 200, 152),
+]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("case", range(len(TENS)))
+def test_tens_of_rows(case, dt, trans):
+    counts, C, F = TENS[case]
+    gen = gen_of(300 + case)
+    cnt, off, rows = groups_of(counts, 1, 0)
+    G, pad = len(counts), lambda n: (n + 15) // 8 * 8  # noqa: E731
+    x = torch.full((1, rows, pad(C)), NAN, device="cuda", dtype=dt)[..., :C]
+    x.copy_(torch.randn(1, rows, C, generator=gen, device="cuda"))
+    w = torch.full((G, C, pad(F)) if trans else (G, F, pad(C)), NAN, device="cuda", dtype=dt)[..., :F if trans else C]
+    w.copy_(0.05 * torch.randn(w.shape, generator=gen, device="cuda"))
+    wide = torch.full((1, rows, F + 3), 7.0, device="cuda", dtype=dt)
+    out = wide[..., :F]
+    out.fill_(NAN)
+    sm.moe_grouped_matmul(x, w, cnt, off, out, trans_w=trans)
+    ref, mag, _ = ref_product(x, w, cnt, off, trans)
+    assert_within(out, ref, mag, "product", product_bound(C))
+    assert bool((wide[..., F:] == 7.0).all())
+    again = torch.empty_like(wide)[..., :F]
+    sm.moe_grouped_matmul(x, w, cnt, off, again, trans_w=trans)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+def test_bad_groups_and_infinities_among_tens_of_rows(trans):
+    gen = gen_of(6)
+    x = torch.randn(15, 64, generator=gen, device="cuda").bfloat16()
+    x[4] = float("inf")
+    w = torch.randn(4, 64, 64, generator=gen, device="cuda").bfloat16()
+    cnt = torch.tensor([4, 15, -2, 5], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 1, 3, 5], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((15, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+    sm.moe_grouped_matmul(x, w, cnt, off, out, trans_w=trans, status=status)
+    assert int(status) == sm.SYM_STATUS_OVERFLOW
+    assert bool((out[[4] + list(range(10, 15))] == 7.0).all()) and bool(out.isfinite().all())
+    assert not bool((out[:4] == 7.0).any(1).all()) and not bool((out[5:10] == 7.0).any(1).all())
+
+
 def test_empty_tensors():
     cnt = torch.zeros(2, dtype=torch.int32, device="cuda")
     x = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
