@@ -20,8 +20,10 @@ constexpr int RUN = 4;  // rows of a group that share one read of the weights
 // tensor-core kernel (us, 2 of 8 groups with a row each, cold weights): w [F][C]
 // 4096 -> 14336 36.4 / 50.5 (0.96 of the copy rate), 14336 -> 4096 38.7 / 67.7; w
 // [C][F] 14336 -> 4096 41.3 / 67.9.  8 groups with a row: 38.2 / 47.4, but w
-// [C][F] 46.7 / 44.1.  Where rows share a group the weights are read again every
-// RUN rows: 8 rows of one group of 7168 x 7168 take 45.2 / 37.0.
+// [C][F] 46.7 / 44.1.  Where rows share a group the arithmetic counts: 4 rows of
+// one group, 7168 -> 2048, take 25.2 (w [C][F] 49.8) against 15.0 (25.2) in warp-wide
+// products (grouped_thin.cu), so a group has two rows (one) on average at most; 8
+// groups with a row each, 51.9 / 62.1.
 constexpr int64_t FEW_ROWS = 8, FEW_ROWS_TRANS = 4;
 
 struct Args {
@@ -207,10 +209,10 @@ __global__ void __launch_bounds__(T_THREADS) few_rows_trans_kernel(const Args p)
 }  // namespace few
 
 // Does the call go to these kernels?  One slot, so that the rows there are bound
-// the live ones; not more rows than one run a group; a run of x fits shared memory.
+// the live ones; a run of x fits shared memory.
 bool few_rows_product(const sym_groups &g, const sym_rows &x, int trans) {
   return x.slots == 1 && x.rows <= (trans ? few::FEW_ROWS_TRANS : few::FEW_ROWS) &&
-         x.rows <= (int64_t)few::RUN * g.groups && x.cols <= 16384;
+         x.rows <= (int64_t)(trans ? 1 : 2) * g.groups && x.cols <= 16384;
 }
 
 cudaError_t launch_few_rows(const sym_groups &g, int fp16, const sym_rows &x, const void *w, int64_t w_group,

@@ -172,6 +172,10 @@ TENS = [  # counts, C, F
     ([0, 0, 31, 0], 2056, 4096),
     ([10], 96, 5000),
     ([0] * 60 + [5, 0, 7, 1], 200, 152),
+    # fewer: runs of three and four rows of a group
+    ([0, 3, 0, 1], 1001, 200),
+    ([4, 0, 0, 0], 136, 72),
+    ([0, 0, 0, 7, 1], 264, 1000),
 ]
 
 
