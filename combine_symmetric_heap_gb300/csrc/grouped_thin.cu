@@ -12,6 +12,8 @@
 // A warp-wide product m16n8k16 wants pairs of contraction elements from each lane;
 // which ones is free as long as both operands agree.  Lane 4g + t takes the eight
 // at 8t of every 32 (a 16-byte load), as two products' four each.
+#include <algorithm>
+
 #include "rows_dev.cuh"
 
 namespace symmoe {
@@ -143,17 +145,21 @@ __device__ __forceinline__ void by_features(const Args &p, int r, int n, int e, 
   join<T, 8 * NB, NF>(p, part, r, n, f0);
 }
 
-// grid (feature blocks, groups)
-template <typename T, int MT>
-__global__ void __launch_bounds__(32 * WARPS) thin_kernel(const Args p) {
+// grid (feature blocks, groups).  Two blocks an SM with two steps' loads in flight
+// each, or (DEEP) one with four, for grids that leave an SM one block: 16 rows of
+// four groups, 7168 -> 2048, 35.5 / 39.6 us; of one group 19.1 / 15.0.
+template <typename T, int MT, bool DEEP>
+__global__ void __launch_bounds__(32 * WARPS, DEEP ? 1 : 2) thin_kernel(const Args p) {
   extern __shared__ __align__(16) float part[];
   const int e = blockIdx.y, f0 = blockIdx.x * 16 * MT;
   const int2 rows = group_rows(p, e);
-  for (int i = 0; i < rows.y; i += 32) {
-    const int r = rows.x + i, n = min(32, rows.y - i);
-    if (n <= 8) by_features<T, MT, 1, 4>(p, r, n, e, f0, part);
-    else if (n <= 16) by_features<T, MT, 2, 4 / MT>(p, r, n, e, f0, part);
-    else by_features<T, MT, 4, 2 / MT>(p, r, n, e, f0, part);
+  // rows of a pass: with 32 features, 32 rows' sums would not fit 64 registers
+  constexpr int PASS = MT == 2 ? 16 : 32, U = DEEP ? 2 : 1;
+  for (int i = 0; i < rows.y; i += PASS) {
+    const int r = rows.x + i, n = min(PASS, rows.y - i);
+    if (n <= 8) by_features<T, MT, 1, 2 * U>(p, r, n, e, f0, part);
+    else if (n <= 16) by_features<T, MT, 2, 2 * U / MT>(p, r, n, e, f0, part);
+    else if constexpr (PASS == 32) by_features<T, MT, 4, U>(p, r, n, e, f0, part);
   }
 }
 
@@ -233,12 +239,12 @@ __global__ void __launch_bounds__(32 * WARPS) thin_trans_kernel(const Args p) {
 // of a single call on cold weights against that kernel's (us, some 8 of them the
 // call's own; 16 rows):
 //   groups, live   C -> F           w [F][C]      w [C][F]
-//   1, 1         7168 -> 2048     17.0 /  41.6  27.3 /  41.6   taken
-//   1, 1        14336 -> 4096     43.6 /  72.3  45.7 /  70.3   taken
-//   4, 4         7168 -> 2048     39.6 /  47.7  33.4 /  45.7   taken
-//   8, 2         7168 -> 2048     23.3 /  41.6  27.3 /  41.6   taken
-//   8, 8         7168 -> 2048     64.2 /  60.2  56.0 /  57.0   taken
-//   8, 8        14336 -> 4096    170.7 / 176.8 178.8 / 164.5   taken / not
+//   1, 1         7168 -> 2048     15.0 /  41.6  25.2 /  41.6   taken
+//   1, 1        14336 -> 4096     41.6 /  72.3  45.7 /  70.3   taken
+//   4, 4         7168 -> 2048     35.5 /  47.7  33.4 /  45.7   taken
+//   8, 2         7168 -> 2048     21.1 /  41.6  27.3 /  41.6   taken
+//   8, 8         7168 -> 2048     56.0 /  60.2  56.0 /  57.0   taken
+//   8, 8        14336 -> 4096    160.4 / 176.8 178.8 / 164.5   taken / not
 //   32, 32       7168 -> 2048    189   / 183     (32 rows)     not
 // 32 rows of one group: 31.4 / 41.6, but 14336 -> 4096 94.8 / 72.3.
 bool thin_product(const sym_groups &g, const sym_rows &x, const sym_rows &out, int trans, int num_sms) {
@@ -263,8 +269,12 @@ cudaError_t launch_thin_product(const sym_groups &g, int fp16, const sym_rows &x
     return fp16 ? go(thin_trans_kernel<__half>, T_FEATURES, 16) : go(thin_trans_kernel<__nv_bfloat16>, T_FEATURES, 16);
   const int rows = x.rows <= 8 ? 8 : x.rows <= 16 ? 16 : 32;  // that a pass takes
   // 32 features a block (x is read half as often) where that still gives every SM one
-  if (out.cols >= 32 * num_sms) return fp16 ? go(thin_kernel<__half, 2>, 32, rows) : go(thin_kernel<__nv_bfloat16, 2>, 32, rows);
-  return fp16 ? go(thin_kernel<__half, 1>, 16, rows) : go(thin_kernel<__nv_bfloat16, 1>, 16, rows);
+  if (out.cols >= 32 * num_sms)
+    return fp16 ? go(thin_kernel<__half, 2, false>, 32, std::min(rows, 16))
+                : go(thin_kernel<__nv_bfloat16, 2, false>, 32, std::min(rows, 16));
+  if ((int64_t)g.groups * ((out.cols + 15) / 16) <= num_sms)
+    return fp16 ? go(thin_kernel<__half, 1, true>, 16, rows) : go(thin_kernel<__nv_bfloat16, 1, true>, 16, rows);
+  return fp16 ? go(thin_kernel<__half, 1, false>, 16, rows) : go(thin_kernel<__nv_bfloat16, 1, false>, 16, rows);
 }
 
 }  // namespace symmoe

@@ -171,6 +171,7 @@ TENS = [  # counts, C, F
     ([3, 0, 2, 2, 1, 1, 0, 3], 328, 9),
     ([0, 0, 31, 0], 2056, 4096),
     ([10], 96, 5000),
+    ([20, 0, 3, 0], 200, 5000),
     ([0] * 60 + [5, 0, 7, 1], 200, 152),
     # fewer: runs of three and four rows of a group
     ([0, 3, 0, 1], 1001, 200),
