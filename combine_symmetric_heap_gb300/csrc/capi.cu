@@ -142,10 +142,26 @@ bool heap_ok(const sym_heap *h) {
 bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// A host thread that has made no CUDA call yet has no current context, and the
+// tensor-map encoder (a driver call) refuses without one: make the device's
+// primary context current there.  A context the caller chose stays.
+bool have_context(int dev) {
+  typedef CUresult (*Fn)(CUcontext *);
+  static const Fn current = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<Fn>(p) : nullptr;
+  }();
+  CUcontext c = nullptr;
+  if (current && current(&c) == CUDA_SUCCESS && c) return true;
+  return cudaSetDevice(dev) == cudaSuccess;
+}
+
 int num_sms_of_current_device() {
   static int cache[64] = {0};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || !have_context(dev)) return 0;
   if (dev < 64 && cache[dev]) return cache[dev];
   int n = 0;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
