@@ -1447,7 +1447,9 @@ cudaError_t launch_block_norm(const sym_block_norm &a, int num_sms, cudaStream_t
   p.ldx = (int)a.ld_x, p.ldo = (int)a.ld_o, p.ldy = (int)a.ld_y, p.ldh = (int)a.ld_h, p.ldg = (int)a.ld_gate;
   p.rows = (int)a.rows, p.gates = a.gate ? (int)a.gate_rows : 1;
   p.per_gate = p.rows / p.gates;
-  p.cols = a.cols, p.act = a.gate_act, p.post_norm = !(a.flags & SYM_NORM_NO_POST);
+  // no norm after a block that is not there (its rstd would be 1 / sqrt(eps),
+  // infinite at eps = 0)
+  p.cols = a.cols, p.act = a.gate_act, p.post_norm = a.o && !(a.flags & SYM_NORM_NO_POST);
   p.scale = a.scale, p.eps = a.eps, p.drop = a.p > 0;
   p.rnd = make_random(a.seed, a.offset, a.p);
   const int64_t es = a.dtype == SYM_FP32 ? 4 : 2;
