@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
         if (dh && w_pre) load<T, V>(w_pre + c, wp);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float q = fa[i] * w[i] * on[i];
+          const float q = fa[i] != 0.f ? fa[i] * w[i] * on[i] : 0.f;
           s[0] += hv[i] * wp[i] * yn[i];
           s[1] += g0[i] * q;
           s[2] += yn[i] * q;
@@ -316,9 +316,9 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
           const float dn = fa[i] != 0.f ? dx * fa[i] : 0.f;
           const float dg = fm[i] != 0.f ? dx * fm[i] * on[i] * w[i] : 0.f;
           dxv[i] = dx;
-          dov[i] = ro * (dn * w[i] - on[i] * m2);
+          dov[i] = ro * (dn * w[i] - (p.post_norm ? on[i] * m2 : 0.f));
           hv[i] *= yn[i];
-          fa[i] = dn * on[i];
+          fa[i] = fa[i] != 0.f ? dn * on[i] : 0.f;
           fm[i] = dg;
         }
         if (p.dx) store<T, V>(reinterpret_cast<T *>(p.dx) + r * p.ld_dx + c, dxv);
@@ -807,10 +807,12 @@ __global__ void __launch_bounds__(MAXT, !DROP && NG == 2 ? 1 : 0)
         for (int i = 0; i < 4; ++i) {
           a_pre[g][k][i] += hv[i] * yn[i];
           g0[i] -= yn[i] * m1;  // dx
-          // a dropped element passes nothing on, whatever its values
-          const float d = !DROP || ((kept >> (8 * g + 4 * k + i)) & 1u) ? g0[i] * kr : 0.f;  // drop dx rstd_o
-          a_s[g][k][i] += d * ov[i];
-          ov[i] = d * factor[g][k][i] - ov[i] * m2;
+          // a dropped element passes nothing on, whatever its values (an infinite o
+          // reaches do through the norm only)
+          const bool keep = !DROP || ((kept >> (8 * g + 4 * k + i)) & 1u);
+          const float d = keep ? g0[i] * kr : 0.f;  // drop dx rstd_o
+          if (keep) a_s[g][k][i] += d * ov[i];
+          ov[i] = d * factor[g][k][i] - (p.post_norm ? ov[i] * m2 : 0.f);
         }
         if (p.dx) out_x.put(k, at<T>(p.dx, r, p.ld_dx), c, p.cols, g0);
         if (p.dout) out_o.put(k, at<T>(p.dout, r, p.ld_do), c, p.cols, ov);
@@ -1159,9 +1161,10 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_odd_kernel(const Bwd p, i
       const float hv = odd_get<T>(rdh, c), yn = odd_get<T>(ryy, c) * cy, ov = odd_get<T>(rov, c);
       const float dx = odd_get<T>(rdy, c) + cy * (hv * Elem<T>::get(w[c])) - yn * m1;
       a_pre[e] += hv * yn;
-      const float d = !DROP || ((kept >> e) & 1u) ? dx * kr : 0.f;
-      a_s[e] += d * ov;
-      const T vx = Elem<T>::put(dx), vo = Elem<T>::put(d * factor[e] - ov * m2);
+      const bool keep = !DROP || ((kept >> e) & 1u);
+      const float d = keep ? dx * kr : 0.f;
+      if (keep) a_s[e] += d * ov;
+      const T vx = Elem<T>::put(dx), vo = Elem<T>::put(d * factor[e] - (p.post_norm ? ov * m2 : 0.f));
       if (in && dx_row) dx_row[c] = vx;
       if (in && do_row) do_row[c] = vo;
     }

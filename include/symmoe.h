@@ -600,6 +600,8 @@ int moe_dropout(int dtype, const sym_rows *x, const sym_rows *residual, const sy
  *   row r / (rows / gate_rows): one gate for all rows, one for each sequence
  *   or one for each row; NULL = ones.  gate_act: SYM_GATE_*.
  *   p, seed, offset: dropout as in moe_dropout, element index row * cols + col.
+ *   (A dropped element passes nothing on, whatever it holds, forward or backward;
+ *   the norm after the block takes rstd_post from all of o's row, though.)
  *   rstd_post, rstd_pre: device fp32 [rows], out (kept for the backward), each
  *   may be NULL.
  * All tensors have the type dtype; rows ld_* elements apart; vectors of 16
