@@ -23,10 +23,10 @@
 // Measured (bf16, dropout 0.1, a GB300 whose copy rate is 6.69 TB/s): forward
 // with both norms, 16384 x 4096, 129 us (4.2 TB/s; 89 us and 6.1 TB/s without
 // dropout), bound by the generator's multiplies on top of the bytes; backward,
-// 8192 x 7168, 192 us (3.7 TB/s; 134 us and 5.3 TB/s without dropout), bound by
+// 8192 x 7168, 197 us (3.6 TB/s; 136 us and 5.2 TB/s without dropout), bound by
 // the latency of a row's chain: its 57 KB a row and 16 columns' sums a thread
 // leave an SM one block.  Rows off 16-byte boundaries: forward 16384 x 4095
-// 218 us, backward 8192 x 7167 294 us.
+// 219 us, backward 8192 x 7167 300 us.
 #include <algorithm>
 
 #include "rows_dev.cuh"
@@ -485,9 +485,15 @@ __device__ __forceinline__ void wait_oldest(int ahead) {
 }
 
 // Forward.  With q = scale drop act(gate) w_post o, y = x + rstd_o q, so the sum
-// of y^2 comes from the same reduction as rstd_o's: it is the sum of x^2 + 2
-// rstd_o x q + rstd_o^2 q^2.  Where those cancel (y shorter than a third of its
-// parts) y^2 is summed over again.
+// of y^2 comes from the same reduction as rstd_o's: with f = rstd_o (and the
+// kept elements' scale), y^2 sums to s1 + f (2 s2 + f s3) of the sums of x^2, x q
+// and q^2.  That does not hold where the parts cancel (y shorter than a third of
+// them), where a product of values not yet normalised left the range of fp32, or
+// where so small ones vanished (each by less than 2^-149) that f^2 brings back.
+// Such a row is read again and taken in the definition's order.
+__device__ __forceinline__ bool sums_hold(float yy, const float (&s)[4], float f, float inv, float eps) {
+  return yy <= 3e38f && yy >= 0.1f * (s[1] + f * (f * s[3])) && f * (f + 2.f) * 1.5e-38f <= yy * inv + eps;
+}
 template <typename T, bool DROP, int NG, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 0)
     block_norm_staged_kernel(const Fwd p, int gate_with_rows, int ahead_rows) {
@@ -578,16 +584,33 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 0)
     const float rstd_o = p.post_norm ? rsqrtf(s[0] * inv + p.eps) : 1.f;
     const float f = DROP ? rstd_o * p.rnd.keep_scale : rstd_o;
     float yy = s[1] + f * (2.f * s[2] + f * s[3]);
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[g][i / 4][i % 4] += f * q[g][i / 4][i % 4];  // y
-    if (!(yy >= 0.1f * (s[1] + f * f * s[3]))) {
-      float t[4] = {0.f, 0.f, 0.f, 0.f};
+    if (sums_hold(yy, s, f, inv, p.eps)) {
 #pragma unroll
       for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[0] += x[g][i / 4][i % 4] * x[g][i / 4][i % 4];
+        for (int i = 0; i < 8; ++i) x[g][i / 4][i % 4] += f * q[g][i / 4][i % 4];  // y
+    } else {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t kept = DROP ? row_mask<C, 1>(p.rnd, r, p.cols, g) : 0u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = C::quad(g, k);
+          float xv[4] = {0.f, 0.f, 0.f, 0.f}, ov[4] = {0.f, 0.f, 0.f, 0.f};
+          if (c < p.cols) {
+            Quad<T>::get(at<T>(p.x, r, p.ldx) + c, xv);
+            if (p.o) Quad<T>::get(at<T>(p.o, r, p.ldo) + c, ov);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool keep = !DROP || ((kept >> (4 * k + i)) & 1u);
+            const float y = xv[i] + (keep ? ov[i] * f * factor[g][k][i] : 0.f);
+            x[g][k][i] = y;
+            t[0] += y * y;
+          }
+        }
+      }
       block_sums4(t, buf, warp, warps, half);
       yy = t[0];
     }
@@ -618,10 +641,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 0)
 
 // Backward.  Per column the block keeps two sums: of dh yn (dw_pre), and over
 // an item's rows S = sum drop dx on, from which both dw_post = sum over gates
-// of scale act S and dgate = scale act' w_post S follow.  (One block an SM, said
+// of scale act S and dgate = scale act' w_post S follow.  o is normalised before
+// anything else multiplies it, so that rows of any size stay in range; without
+// the norm after the block (POST) o is in S only.  (One block an SM, said
 // to the compiler: it takes all registers and reads further ahead, 134 against 144
 // us at 8192 x 7168 without dropout.  With dropout it had them anyway.)
-template <typename T, bool DROP, int NG, int MAXT>
+template <typename T, bool DROP, bool POST, int NG, int MAXT>
 __global__ void __launch_bounds__(MAXT, !DROP && NG == 2 ? 1 : 0)
     block_norm_bwd_staged_kernel(const Bwd p, int gate_with_rows, int ahead_rows) {
   using C = Columns<T, NG, MAXT, true>;
@@ -662,7 +687,7 @@ __global__ void __launch_bounds__(MAXT, !DROP && NG == 2 ? 1 : 0)
   auto read_rstd = [&](const Walk &w) {
     if (!w.live()) return;
     if (p.dh) ry = p.rstd_pre[w.row];
-    if (p.o && p.post_norm) ro = p.rstd_post[w.row];
+    if (POST && p.o) ro = p.rstd_post[w.row];
   };
   for (char *to = row0; to != row_end; to += row_step) fetch(to);
   read_rstd(soon);
@@ -782,17 +807,21 @@ __global__ void __launch_bounds__(MAXT, !DROP && NG == 2 ? 1 : 0)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool keep = !DROP || ((kept >> (8 * g + 4 * k + i)) & 1u);
-          const float q = keep ? factor[g][k][i] * ov[i] : 0.f;
-          s[1] += g0[i] * q;
-          s[2] += yn[i] * q;
+          if (POST) {
+            const float q = keep ? factor[g][k][i] * (ov[i] * co) : 0.f;
+            s[1] += g0[i] * q;
+            s[2] += yn[i] * q;
+          }
         }
       }
     }
     block_sums4(s, buf, warp, warps, half);
+    // The row is read from shared memory again: without this the compiler keeps its
+    // values in registers over the reduction (100 instead of 76 a thread at 8 columns,
+    // 8192 x 1024 44 us instead of 33; at 8192 x 7168 152 instead of 136).
+    asm volatile("" ::: "memory");
     const float m1 = cy * s[0] * inv;  // dx = g0 - yn * m1
-    // mean(dn w_post on), times on's and do's rstd
-    const float m2 = p.post_norm ? ks * co * co * co * (s[1] - m1 * s[2]) * inv : 0.f;
-    const float kr = ks * co;
+    const float m2 = ks * (s[1] - m1 * s[2]) * inv;  // mean(dn w_post on)
     Writer<T> out_x, out_o;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -807,12 +836,17 @@ __global__ void __launch_bounds__(MAXT, !DROP && NG == 2 ? 1 : 0)
         for (int i = 0; i < 4; ++i) {
           a_pre[g][k][i] += hv[i] * yn[i];
           g0[i] -= yn[i] * m1;  // dx
-          // a dropped element passes nothing on, whatever its values (an infinite o
-          // reaches do through the norm only)
+          // a dropped element passes nothing on, whatever its values
           const bool keep = !DROP || ((kept >> (8 * g + 4 * k + i)) & 1u);
-          const float d = keep ? g0[i] * kr : 0.f;  // drop dx rstd_o
-          if (keep) a_s[g][k][i] += d * ov[i];
-          ov[i] = d * factor[g][k][i] - (p.post_norm ? ov[i] * m2 : 0.f);
+          const float d = keep ? g0[i] * ks : 0.f;  // drop dx
+          if constexpr (POST) {
+            const float on = ov[i] * co;
+            a_s[g][k][i] += d * on;
+            ov[i] = co * (d * factor[g][k][i] - on * m2);
+          } else {
+            a_s[g][k][i] += d * (keep ? ov[i] : 0.f);
+            ov[i] = d * factor[g][k][i];
+          }
         }
         if (p.dx) out_x.put(k, at<T>(p.dx, r, p.ld_dx), c, p.cols, g0);
         if (p.dout) out_o.put(k, at<T>(p.dout, r, p.ld_do), c, p.cols, ov);
@@ -1001,12 +1035,23 @@ __global__ void __launch_bounds__(1024) block_norm_odd_kernel(const Fwd p, int g
     const float rstd_o = p.post_norm ? rsqrtf(s[0] * inv + p.eps) : 1.f;
     const float f = DROP ? rstd_o * p.rnd.keep_scale : rstd_o;
     float yy = s[1] + f * (2.f * s[2] + f * s[3]);
+    if (sums_hold(yy, s, f, inv, p.eps)) {
 #pragma unroll
-    for (int e = 0; e < NE; ++e) y[e] += f * q[e];
-    if (!(yy >= 0.1f * (s[1] + f * f * s[3]))) {
+      for (int e = 0; e < NE; ++e) y[e] += f * q[e];
+    } else {
+      // (the row's mask bytes may be the next row's by now: its words are made again)
       float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < NE; ++e) t[0] += y[e] * y[e];
+      for (int e = 0; e < NE; ++e) {
+        const int c = col(e);
+        const bool in = c < p.cols;
+        const float xv = in ? Elem<T>::get(at<T>(p.x, r, p.ldx)[c]) : 0.f;
+        const float ov = in && p.o ? Elem<T>::get(at<T>(p.o, r, p.ldo)[c]) : 0.f;
+        float k[1] = {1.f};
+        if (DROP) keep_factors<1>(p.rnd, (uint64_t)r * p.cols + c, k);
+        y[e] = xv + (k[0] != 0.f ? ov * f * factor[e] : 0.f);
+        t[0] += y[e] * y[e];
+      }
       block_sums4(t, buf, warp, warps, half);
       yy = t[0];
     }
@@ -1142,7 +1187,7 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_odd_kernel(const Bwd p, i
       const float yn = odd_get<T>(ryy, c) * cy, t = odd_get<T>(rdh, c) * Elem<T>::get(w[c]);
       const float g0 = odd_get<T>(rdy, c) + cy * t;
       if (DROP) kept |= (uint32_t)mask[c] << e;
-      const float q = !DROP || ((kept >> e) & 1u) ? factor[e] * odd_get<T>(rov, c) : 0.f;
+      const float q = !DROP || ((kept >> e) & 1u) ? factor[e] * (odd_get<T>(rov, c) * co) : 0.f;
       s[0] += t * yn;
       s[1] += g0 * q;
       s[2] += yn * q;
@@ -1151,20 +1196,19 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_odd_kernel(const Bwd p, i
     if (DROP && soon.live()) odd_mask(p.rnd, soon.row, p.cols, masks + side * mask_pitch);
     block_sums4(s, buf, warp, warps, half);
     const float m1 = cy * s[0] * inv;
-    const float m2 = p.post_norm ? ks * co * co * co * (s[1] - m1 * s[2]) * inv : 0.f;
-    const float kr = ks * co;
+    const float m2 = p.post_norm ? ks * (s[1] - m1 * s[2]) * inv : 0.f;
     T *const dx_row = p.dx ? at<T>(p.dx, r, p.ld_dx) : nullptr, *const do_row = p.dout ? at<T>(p.dout, r, p.ld_do) : nullptr;
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
       const int c = col(e);
       const bool in = c < p.cols;
-      const float hv = odd_get<T>(rdh, c), yn = odd_get<T>(ryy, c) * cy, ov = odd_get<T>(rov, c);
+      const float hv = odd_get<T>(rdh, c), yn = odd_get<T>(ryy, c) * cy, on = odd_get<T>(rov, c) * co;
       const float dx = odd_get<T>(rdy, c) + cy * (hv * Elem<T>::get(w[c])) - yn * m1;
       a_pre[e] += hv * yn;
       const bool keep = !DROP || ((kept >> e) & 1u);
-      const float d = keep ? dx * kr : 0.f;
-      if (keep) a_s[e] += d * ov;
-      const T vx = Elem<T>::put(dx), vo = Elem<T>::put(d * factor[e] - (p.post_norm ? ov * m2 : 0.f));
+      const float d = keep ? dx * ks : 0.f;
+      if (keep) a_s[e] += d * on;
+      const T vx = Elem<T>::put(dx), vo = Elem<T>::put(co * (d * factor[e] - (p.post_norm ? on * m2 : 0.f)));
       if (in && dx_row) dx_row[c] = vx;
       if (in && do_row) do_row[c] = vo;
     }
@@ -1383,9 +1427,11 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
       const StagedShape s = staged_shape(p.cols, false);
       err = with_shape<false>(s, [&](auto groups, auto threads) {
         using C = Columns<T, decltype(groups)::value, decltype(threads)::value, true>;  // (for the sizes)
-        return launch_staged<C, Bwd>(p.drop ? block_norm_bwd_staged_kernel<T, true, C::NG, C::MAXT>
-                                            : block_norm_bwd_staged_kernel<T, false, C::NG, C::MAXT>,
-                                     p, 4, C::row_bytes(1) + 2 * C::NG * C::MAXT * 16,
+        auto kern = p.post_norm ? (p.drop ? block_norm_bwd_staged_kernel<T, true, true, C::NG, C::MAXT>
+                                          : block_norm_bwd_staged_kernel<T, false, true, C::NG, C::MAXT>)
+                                : (p.drop ? block_norm_bwd_staged_kernel<T, true, false, C::NG, C::MAXT>
+                                          : block_norm_bwd_staged_kernel<T, false, false, C::NG, C::MAXT>);
+        return launch_staged<C, Bwd>(kern, p, 4, C::row_bytes(1) + 2 * C::NG * C::MAXT * 16,
                                      p.gate && p.per_gate <= GATE_WITH_ROWS, blocks, s, st);
       });
       if (err != cudaSuccess) return err;
