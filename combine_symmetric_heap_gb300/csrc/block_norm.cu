@@ -265,7 +265,10 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
             if (V == 1) k[0] = mask[c] ? p.rnd.keep_scale : 0.f;
             else keep_factors<V>(p.rnd, (uint64_t)r * p.cols + c, k);
 #pragma unroll
-            for (int i = 0; i < V; ++i) fm[i] *= k[i];
+            for (int i = 0; i < V; ++i) {
+              fm[i] *= k[i];
+              if (k[i] == 0.f && !(ro > 0.f)) on[i] = 0.f;  // as clear_dropped does
+            }
           }
           if (gate) {
             float g[V];
@@ -639,6 +642,16 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 0)
   }
 }
 
+// An infinite o makes its row's rstd 0 and itself NaN when normalised: where it is
+// dropped, a zero in its place (this thread's elements of the row's copy)
+template <typename C, typename T>
+__device__ __forceinline__ void clear_dropped(char *p, uint32_t kept) {
+#pragma unroll 1
+  for (int e = 0; e < 8 * C::NG; ++e)
+    if (!((kept >> e) & 1u))
+      *reinterpret_cast<T *>(p + C::place(0, e / C::W) + e % C::W * (int)sizeof(T)) = Elem<T>::put(0.f);
+}
+
 // Backward.  Per column the block keeps two sums: of dh yn (dw_pre), and over
 // an item's rows S = sum drop dx on, from which both dw_post = sum over gates
 // of scale act S and dgate = scale act' w_post S follow.  o is normalised before
@@ -795,6 +808,7 @@ __global__ void __launch_bounds__(MAXT, !DROP && NG == 2 ? 1 : 0)
     // all groups' blocks of words side by side (a group at a time: 203 against
     // 197 us; the forward, with fewer registers to spare, gains from that)
     const uint32_t kept = DROP ? row_mask<C, C::NG>(p.rnd, r, p.cols, 0) : 0u;  // bit 8g + 4k + i
+    if (DROP && POST && !(co > 0.f)) clear_dropped<C, T>(row + C::place(O, 0), kept);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -1181,6 +1195,9 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_odd_kernel(const Bwd p, i
     const uint8_t *mask = masks + side * mask_pitch + (((uint32_t)r * (uint32_t)p.cols) & 3u);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     uint32_t kept = 0u;
+    if (DROP && !(co > 0.f))  // as clear_dropped does; no other thread reads these elements
+      for (int e = 0; e < NE; ++e)
+        if (!mask[col(e)]) *reinterpret_cast<T *>(const_cast<char *>(rov) + col(e) * (int)sizeof(T)) = Elem<T>::put(0.f);
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
       const int c = col(e);

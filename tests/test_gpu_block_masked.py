@@ -44,6 +44,39 @@ def test_dropped_garbage_passes_nothing_on(cols, dt, gates):
             assert bool(t.isfinite().all()) and torch.equal(t, dirty[name]), name
 
 
+@pytest.mark.parametrize("gates", [0, 1, 6])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", COLS)
+def test_a_dropped_infinity_before_the_norm(cols, dt, gates):
+    """The norm after the block makes zeros of the row with the infinity; the other
+    rows, and what is summed over rows, do not see it."""
+    gen = torch.Generator(device="cuda").manual_seed(cols + gates)
+    randn = lambda *s: torch.randn(s, generator=gen, device="cuda").to(dt)  # noqa: E731
+    rows, row = 6, 2
+    o, x, dy = (randn(rows, cols) for _ in range(3))
+    gate, like = randn(gates, cols) if gates else None, torch.empty_like
+    at = int((~kept(SEED, OFFSET, o.shape, P))[row].nonzero()[-1])
+    got = []
+    for dirty in (True, False):
+        o[row] = randn(cols) if dirty else 0
+        if dirty:
+            o[row, at] = -float("inf")
+        kw = dict(o=o, gate=gate, gate_act="tanh" if gates else "none", scale=0.7, p=P, seed=SEED, offset=OFFSET)
+        y, h, ro = like(x), like(x), torch.empty(rows, device="cuda")
+        sm.moe_block_norm(x, y=y, h=h, rstd_post=ro, **kw)
+        assert dirty == (float(ro[row]) == 0)
+        ro[row] = 0
+        grads = dict(dx=like(x), do=like(x), dw_post=torch.empty(cols, device="cuda", dtype=dt),
+                     dgate=None if gate is None else like(gate))
+        work = torch.empty(sm.moe_block_norm_workspace(rows, cols, gates), dtype=torch.uint8, device="cuda")
+        sm.moe_block_norm_bwd(dy=dy, rstd_post=ro, work=work, **grads, **kw)
+        got.append(dict(y=y, h=h, rstd_post=ro, **grads))
+    assert torch.equal(got[0]["y"][row], x[row]) and bool((got[0]["do"][row] == 0).all())
+    for name, t in got[1].items():
+        if t is not None:
+            assert bool(t.isfinite().all()) and torch.equal(t, got[0][name]), name
+
+
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("cols", COLS)
 def test_without_a_norm_the_gradient_does_not_depend_on_the_block_output(cols, dt):
