@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const Bwd p) {
 // weights ones); addresses that are constants from a row's start.
 // ---------------------------------------------------------------------------
 constexpr int STAGED_COLS = 8192;
-constexpr int STAGED_SMEM = 220 * 1024;
+constexpr int STAGED_SMEM = 220 * 1024;  // of a block, at most (the odd kernels too)
+constexpr int MASK_SMEM = 65536;         // a row's mask bytes in the general kernels, at most
 // A gate row shared by this few rows is copied along with each of them.
 constexpr int GATE_WITH_ROWS = 4;
 
@@ -1340,7 +1341,7 @@ static cudaError_t launch_odd(void (*kern)(P, int, int), const P &p, int arrays,
   const size_t row = (size_t)pitch * (arrays + with_rows);
   const int ahead = room < fixed + 2 * row ? 1 : room < fixed + 3 * row ? 2 : 3;
   const size_t bytes = fixed + ahead * row;
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  const cudaError_t err = allow_smem(kern, STAGED_SMEM);
   if (err != cudaSuccess) return err;
   kern<<<blocks, threads, bytes, st>>>(p, with_rows, ahead);
   return cudaGetLastError();
@@ -1364,7 +1365,7 @@ static cudaError_t launch_staged(void (*kern)(P, int, int), const P &p, int arra
   const size_t row = C::row_bytes(arrays + with_rows), room = STAGED_SMEM / s.per_sm;
   const int ahead = room < fixed + 2 * row ? 1 : room < fixed + 3 * row ? 2 : 3;
   const size_t bytes = fixed + ahead * row;
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  const cudaError_t err = allow_smem(kern, STAGED_SMEM);
   if (err != cudaSuccess) return err;
   kern<<<blocks, s.threads, bytes, st>>>(p, with_rows, ahead);
   return cudaGetLastError();
@@ -1408,7 +1409,7 @@ static cudaError_t fwd(Fwd p, int num_sms, cudaStream_t st) {
   }
   auto kern = block_norm_kernel<T, V>;
   const size_t smem = V == 1 && p.drop ? p.cols : 0;
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t err = allow_smem(kern, MASK_SMEM);
   if (err != cudaSuccess) return err;
   kern<<<std::min(p.rows, num_sms * 2), 1024, smem, st>>>(p);
   return cudaGetLastError();
@@ -1464,7 +1465,7 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
       if (err != cudaSuccess) return err;
     } else {
       const size_t smem = p.drop ? p.cols : 0;
-      err = cudaFuncSetAttribute(block_norm_bwd_kernel<T, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      err = allow_smem(block_norm_bwd_kernel<T, 1>, MASK_SMEM);
       if (err != cudaSuccess) return err;
       block_norm_bwd_kernel<T, 1><<<blocks, plan.threads, smem, st>>>(p);
     }

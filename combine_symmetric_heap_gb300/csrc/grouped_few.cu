@@ -25,6 +25,7 @@ constexpr int RUN = 4;  // rows of a group that share one read of the weights
 // products (grouped_thin.cu), so a group has two rows (one) on average at most; 8
 // groups with a row each, 51.9 / 62.1.
 constexpr int64_t FEW_ROWS = 8, FEW_ROWS_TRANS = 4;
+constexpr int MOST_COLS = 16384;  // of x: a run fits shared memory
 
 struct Args {
   const int32_t *cnt, *off;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(T_THREADS) few_rows_trans_kernel(const Args p)
 // the live ones; a run of x fits shared memory.
 bool few_rows_product(const sym_groups &g, const sym_rows &x, int trans) {
   return x.slots == 1 && x.rows <= (trans ? few::FEW_ROWS_TRANS : few::FEW_ROWS) &&
-         x.rows <= (int64_t)(trans ? 1 : 2) * g.groups && x.cols <= 16384;
+         x.rows <= (int64_t)(trans ? 1 : 2) * g.groups && x.cols <= few::MOST_COLS;
 }
 
 cudaError_t launch_few_rows(const sym_groups &g, int fp16, const sym_rows &x, const void *w, int64_t w_group,
@@ -224,7 +225,7 @@ cudaError_t launch_few_rows(const sym_groups &g, int fp16, const sym_rows &x, co
   // rows of x a block reads: 1, 2 or RUN (a run of three reads a fourth that is not stored)
   const size_t smem = trans ? (size_t)(x.rows <= 2 ? x.rows : RUN) * ((x.cols + 7) & ~7) * 2 : 0;
   auto go = [&](auto kern, int threads, int features) {
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t err = allow_smem(kern, trans ? RUN * MOST_COLS * 2 : 0);
     if (err != cudaSuccess) return err;
     kern<<<dim3((out.cols + features - 1) / features, (unsigned)x.rows), threads, smem, st>>>(p);
     return cudaGetLastError();

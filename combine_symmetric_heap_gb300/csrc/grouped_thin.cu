@@ -24,6 +24,7 @@ using namespace rows;
 constexpr int WARPS = 16;
 constexpr int K_STEP = 32;         // contraction elements of a warp's step
 constexpr int T_FEATURES = 64;     // of a block, w [C][F]
+constexpr int MOST_SMEM = 4 * WARPS * T_FEATURES * 16;  // the warps' sums, at most
 
 struct Args {
   const int32_t *cnt, *off;
@@ -260,7 +261,7 @@ cudaError_t launch_thin_product(const sym_groups &g, int fp16, const sym_rows &x
                (int)x.rows, out.cols, x.cols};
   auto go = [&](auto kern, int features, int rows) {
     const size_t smem = sizeof(float) * WARPS * features * rows;
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t err = allow_smem(kern, MOST_SMEM);
     if (err != cudaSuccess) return err;
     kern<<<dim3((out.cols + features - 1) / features, (unsigned)g.groups), 32 * WARPS, smem, st>>>(p);
     return cudaGetLastError();

@@ -352,5 +352,14 @@ __device__ __forceinline__ void block_sums4(float (&v)[4], float *buf, int warp,
   for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(0xffffffffu, s, k);
 }
 
+// Let launches of `kern` take up to `most` bytes of dynamic shared memory.  The
+// limit is one per kernel for the whole process, so every call gives the kernel's
+// largest size, whatever its own: with that, a call in another host thread cannot
+// lower it between this call and its launch.
+template <typename Kern>
+inline cudaError_t allow_smem(Kern kern, int most) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 }  // namespace rows
 }  // namespace symmoe

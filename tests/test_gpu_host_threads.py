@@ -65,6 +65,69 @@ def ffn():
     return lambda: heap.expert_ffn(*weights), (heap.window("h"), heap, idx, w, weights)
 
 
+def norm(rows, cols, dt):
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x, o = (torch.randn(rows, cols, generator=gen, device="cuda").to(dt) for _ in range(2))
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    return lambda: sm.moe_block_norm(x, o=o, y=y, h=h, p=0.1, seed=1), (y, h, x, o)
+
+
+def norm_bwd(rows, cols, dt):
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    dy, o = (torch.randn(rows, cols, generator=gen, device="cuda").to(dt) for _ in range(2))
+    ro = o.double().square().mean(1).rsqrt().float()
+    do = torch.empty_like(o)
+    work = torch.empty(sm.moe_block_norm_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+    return lambda: sm.moe_block_norm_bwd(dy=dy, o=o, rstd_post=ro, do=do, p=0.1, seed=1, work=work), (do, dy, o, ro, work)
+
+
+BF16, FP32 = torch.bfloat16, torch.float32
+# two sizes that take different amounts of shared memory of the same kernel
+SIZES = {
+    "vectors": (norm, (2, 8192, FP32), (2, 2056, FP32)),
+    "vectors, gradient": (norm_bwd, (2, 8192, FP32), (2, 2056, FP32)),
+    "off boundaries": (norm, (2, 8191, FP32), (2, 33, FP32)),
+    "off boundaries, gradient": (norm_bwd, (2, 8191, FP32), (2, 33, FP32)),
+    "long rows": (norm, (2, 65535, BF16), (2, 8201, BF16)),
+    "long rows, gradient": (norm_bwd, (2, 65535, BF16), (2, 8201, BF16)),
+    "few rows": (product, ([1, 1, 1, 1], 16384, 64, True), ([1], 64, 64, True)),
+    "tens of rows": (product, ([12, 0, 10, 9], 256, 64, False), ([9, 0, 0, 0], 256, 64, False)),
+}
+
+
+@pytest.mark.parametrize("name", SIZES)
+def test_threads_with_different_sizes(name):
+    """Six threads at once, each on a stream and outputs of its own: a call that sets
+    a kernel up for its size must not undo what another one has just set up."""
+    make, *sizes = SIZES[name]
+    made = [make(*sizes[i % 2]) for i in range(6)]
+    calls = [recorded(call) for call, _ in made]
+    torch.cuda.synchronize()
+    outs = [kept[0] for _, kept in made]
+    want = [t.clone() for t in outs]
+    streams = [torch.cuda.Stream() for _ in made]
+    for t in outs:
+        t.fill_(float("nan"))
+    torch.cuda.synchronize()
+    start, codes = threading.Barrier(len(made)), [set() for _ in made]
+
+    def work(i):
+        (fn, args), handle = calls[i], streams[i].cuda_stream
+        args = (*args[:-1], handle)
+        start.wait()
+        for _ in range(3000):
+            codes[i].add(fn(*args))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(made))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{sm.SYM_OK}] * len(made)
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 @pytest.mark.parametrize("make", [lambda: product([100, 3], 64, 64, False), lambda: product([1], 64, 64, True),
                                   lambda: wgrad([100, 3], 64, 64), ffn],
                          ids=["product", "product of one row", "weight gradient", "expert ffn"])
