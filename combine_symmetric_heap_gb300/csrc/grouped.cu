@@ -46,6 +46,10 @@ constexpr int PRODUCT_THREADS = 192;  // producer, MMA issuer, 4 epilogue warps
 constexpr int WG_EPI_WARPS = 8;       // two per TMEM lane quarter, each with half of a tile's columns
 constexpr int WGRAD_THREADS = 32 * (3 + WG_EPI_WARPS);  // ... and the warp of the groups' last rows
 constexpr int CTRL_BYTES = 512;
+// A call's most groups.  The product's tables take their 12 KB whatever the call's
+// number: one shared-memory size for the kernel, so that calls from several host
+// threads set the same limit and the resident pairs are looked up once.
+constexpr int MAX_GROUPS = 1024;
 constexpr int CHUNK_BYTES = BK * 64 * 2;  // 64 contraction rows x 64 features (MN-major tiles)
 constexpr int WG_STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int WG_STAGES = 6;
@@ -891,7 +895,7 @@ cudaError_t launch_grouped_matmul(const sym_groups &sg, int fp16, const sym_rows
     return cudaErrorInvalidValue;
   for (int i = 0; i < NBOX; ++i)
     if (!encode_rows(&mx.m[i], x, (uint32_t)(BOX_MIN_ROWS << i))) return cudaErrorInvalidValue;
-  const size_t smem = 1024 + (size_t)STAGES * STAGE_BYTES + CTRL_BYTES + tok_tables_bytes(sg.groups);
+  const size_t smem = 1024 + (size_t)STAGES * STAGE_BYTES + CTRL_BYTES + tok_tables_bytes(MAX_GROUPS);
   // row tiles of a run: their rows fit 64 MB, so a wave's rows stay in L2
   // while the feature tiles pass (the expert FFN's budget for wide rows)
   const int run = (int)std::max<int64_t>(1, GROUP_H_BYTES / ((int64_t)BN * C * 2));

@@ -92,6 +92,7 @@ SIZES = {
     "long rows, gradient": (norm_bwd, (2, 65535, BF16), (2, 8201, BF16)),
     "few rows": (product, ([1, 1, 1, 1], 16384, 64, True), ([1], 64, 64, True)),
     "tens of rows": (product, ([12, 0, 10, 9], 256, 64, False), ([9, 0, 0, 0], 256, 64, False)),
+    "many rows": (product, ([1] * 1000, 64, 64, False), ([100], 64, 64, False)),
 }
 
 
