@@ -432,9 +432,10 @@ def _row_words(t, rows: SymRows, dtype, where: str):
 def _totals(total, rows: SymRows, where: str):
     if total is None:
         return None, 0
-    _need(total.dtype == torch.int32 and total.numel() == rows.slots and total.dim() <= 2, where,
-          "total is one int32 for each slot")
-    return total.data_ptr(), (total.stride(0) if total.dim() and rows.slots > 1 else 0)
+    n = rows.slots
+    _need(total.dtype == torch.int32 and (total.shape in ((n,), (n, 1)) or n == 1 and total.dim() == 0), where,
+          "total is one int32 for each slot, [slots] or [slots, 1]")
+    return total.data_ptr(), (total.stride(0) if n > 1 else 0)
 
 
 def moe_swiglu_rows(g, u, h, row_w=None, total=None, stream=None) -> None:
