@@ -381,7 +381,7 @@ def _per_slot(t, slots: int, n: int, dtype, where: str) -> int:
 
 def _groups(cnt, off, rows: SymRows, status, where: str) -> SymGroups:
     g = cnt.numel()
-    _need(g > 0 and g % rows.slots == 0, where, "the slots have equally many groups")
+    _need(g > 0 and rows.slots > 0 and g % rows.slots == 0, where, "the slots have equally many groups")
     each = g // rows.slots
     cs = _per_slot(cnt, rows.slots, each, torch.int32, where)
     os_ = _per_slot(off, rows.slots, each, torch.int32, where)

@@ -27,3 +27,8 @@ def test_totals_are_one_word_for_each_slot():
     for t in (words[1], words[1:2], words[1:2].view(1, 1)):
         assert sm._totals(t, one, "t") == (t.data_ptr(), 0)
     refused(sm._totals, words[:2], one, "t")
+
+
+def test_no_slots():
+    words = torch.zeros(2, dtype=torch.int32)
+    refused(sm._groups, words, words, sm._rows(torch.zeros(0, 4, 8), "t"), None, "t")
