@@ -501,6 +501,8 @@ def _block(where: str, dt, rows: int, cols: int, x, o, w_post, gate, gate_act, s
     yp, yl = _plain(y, rows, cols, dt, where)
     hp, hl = _plain(h, rows, cols, dt, where)
     gates = 0 if gate is None else gate.shape[0]
+    # (an empty tensor has no address, which would read as no gate)
+    _need(gate is None or gates > 0 or rows == 0, where, "a gate has at least one row")
     gp, gl = _plain(gate, gates, cols, dt, where)
     return SymBlockNorm(rows, cols, _DTYPES.get(dt, -1), xp, op, _vector(w_post, cols, dt, where), gp,
                         _vector(w_pre, cols, dt, where), yp, hp, _vector(rstd_post, rows, torch.float32, where),

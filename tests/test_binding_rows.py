@@ -32,3 +32,15 @@ def test_totals_are_one_word_for_each_slot():
 def test_no_slots():
     words = torch.zeros(2, dtype=torch.int32)
     refused(sm._groups, words, words, sm._rows(torch.zeros(0, 4, 8), "t"), None, "t")
+
+
+def norm_args(rows, gate):
+    x = torch.zeros(rows, 8)
+    return ("t", x.dtype, rows, 8, x, x, None, gate, "none", 1.0, 0.0, 0, 0, None, x, None, None, None, True, 1e-6)
+
+
+def test_gate_without_rows():
+    """An empty gate is no gate row for rows that are there (and not the absence of a gate)."""
+    refused(sm._block, *norm_args(4, torch.zeros(0, 8)))
+    assert sm._block(*norm_args(0, torch.zeros(0, 8))).gate_rows == 0
+    assert sm._block(*norm_args(4, torch.zeros(2, 8))).gate_rows == 2
