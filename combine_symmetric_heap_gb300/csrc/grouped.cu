@@ -98,6 +98,21 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, const C
   }
 }
 
+// A wait of this CTA has run out and all its threads have stopped: before its
+// shared memory and TMEM are given up, wait (10 ms at most) for the MMAs in
+// flight, and 10 ms for the copies.  No barrier this CTA may wait on counts all of
+// those (the peer's are counted by the leader, a stage that one CTA did not load
+// never completes); a copy takes some microseconds.
+__device__ __forceinline__ void settle(uint64_t *drained, bool issuer) {
+  constexpr uint32_t LIMIT_US = 10000;
+  const uint64_t t0 = globaltimer_ns();
+  if (issuer) {
+    commit2_both(drained);
+    mbar_wait(drained, 0, LIMIT_US, nullptr);
+  }
+  while (globaltimer_ns() - t0 < LIMIT_US * 1000ull) __nanosleep(1000);
+}
+
 // Matrix descriptor of an MN-major tile with the 128-byte swizzle: chunks of
 // 64 features, each [64 contraction rows][128 bytes]; the leading offset steps
 // over chunks, the stride offset over groups of 8 contraction rows.
@@ -323,7 +338,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PRODUCT_THREADS, 1)
   uint8_t *ctrl = smem + (size_t)STAGES * STAGE_BYTES;
   uint64_t *bars = reinterpret_cast<uint64_t *>(ctrl);
   uint64_t *acc_full = bars + 2 * STAGES, *acc_empty = acc_full + 2, *acc_head = acc_full + 4;
-  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(acc_full + 6);
+  uint64_t *drained = acc_full + 6;
+  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base_s + 1);
   int *tab = reinterpret_cast<int *>(ctrl + CTRL_BYTES);
   const TokTables tb{tab, tab + g.G, tab + 2 * g.G};
@@ -343,6 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PRODUCT_THREADS, 1)
       mbar_init(&acc_empty[b], 8);  // 4 epilogue warps of each CTA
       mbar_init(&acc_head[b], 8);
     }
+    mbar_init(drained, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_w);
@@ -433,6 +450,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PRODUCT_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) settle(drained, wid == 1 && lane == 0 && rank == 0);
+  __syncwarp();
   cluster_sync();  // no remote arrive or MMA of the pair is still in flight
   tc_fence_after();
   if (wid == 1) tmem_dealloc2(tmem, TMEM_COLS);
@@ -606,7 +625,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
   uint64_t *rest_full = rest_in + 4;         // [2] (the leader's) both halves are
   uint64_t *rest_empty = rest_in + 6;        // [2] the MMA has read it
   uint64_t *acc_full = rest_in + 8, *acc_empty = acc_full + 2;
-  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(acc_full + 4);
+  uint64_t *drained = acc_full + 4;
+  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base_s + 1);
   const int wid = warp_id(), lane = lane_id();
   const uint32_t rank = cta_rank();
@@ -624,6 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * WG_EPI_WARPS);
     }
+    mbar_init(drained, 1);
     *abort_flag = 0;
     fence_mbar_init();
     for (int i = 0; i < WG_BOXES; ++i) {
@@ -832,6 +853,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) settle(drained, wid == 1 && lane == 0 && rank == 0);
+  __syncwarp();
   cluster_sync();
   tc_fence_after();
   if (wid == 1) tmem_dealloc2(tmem, TMEM_COLS);
