@@ -22,10 +22,11 @@
 //
 // Measured (bf16, dropout 0.1, a GB300 whose copy rate is 6.69 TB/s): forward
 // with both norms, 16384 x 4096, 129 us (4.2 TB/s; 89 us and 6.1 TB/s without
-// dropout), bound by the generator's multiplies on top of the bytes; backward,
-// 8192 x 7168, 197 us (3.6 TB/s; 136 us and 5.2 TB/s without dropout), bound by
-// the latency of a row's chain: its 57 KB a row and 16 columns' sums a thread
-// leave an SM one block.  Rows off 16-byte boundaries: forward 16384 x 4095
+// dropout): a row's mask is made between its arrival and its sums, on the row's
+// critical path (the dropout kernel, which has no such path, makes as many words
+// in 67 us); backward, 8192 x 7168, 197 us (3.6 TB/s; 136 us and 5.2 TB/s without
+// dropout), for the same reason and by the latency of a row's chain: its 57 KB a
+// row and 16 columns' sums a thread leave an SM one block.  Rows off 16-byte boundaries: forward 16384 x 4095
 // 219 us, backward 8192 x 7167 300 us.
 #include <algorithm>
 

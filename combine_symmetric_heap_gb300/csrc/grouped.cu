@@ -26,13 +26,17 @@
 //
 // Measured (bf16; measured rates: copy 6.69 TB/s, library GEMM 1867 TFLOP/s in a burst, 1710 under
 // the power cap): product of 8192 rows in 256 groups, 7168 -> 2048, 1.17 ms (6.57
-// TB/s, bound by the weights' read); of 65536 rows 1.43 ms in a few launches, 1.65
-// ms back to back under the power cap (the narrow second MMA of groups of 257..288
+// TB/s, bound by the weights' read); of 65536 rows 1.49 ms for a pass by itself, 1.64 to
+// 1.68 ms back to back under the power cap (the narrow second MMA of groups of 257..288
 // rows then bounds half the tiles); data gradient 32768 rows, 8 groups, 4096 ->
-// 14336, 2.41 ms (1600 TFLOP/s, the power cap).  Weight gradient of the 65536 rows
-// (7.5 GB written) 1.96 ms, 1.67 ms where every count is a multiple of 16: bound by
-// shared memory, which the MMA's operands fill at full rate (128 bytes a clock)
-// and the output's staging shares; 8 groups of 4096 rows 2.0 ms (1.9 PFLOP/s).
+// 14336, 2.41 to 2.49 ms (1540 to 1600 TFLOP/s, the power cap).  Weight gradient of the
+// 65536 rows (7.5 GB written) 1.95 to 1.99 ms; where every count is a multiple of 16 1.65
+// ms in runs of three, 1.83 under the power cap.  No single unit bounds it: at 64 of these
+// groups DRAM is 65% busy, L1 and shared memory 76%, the tensor pipe 49% (58, 68 and 45
+// with ragged counts), and the same bytes written by themselves take 1.10 ms.  Into
+// fp32 2.73 ms, added to what is there 6.2 ms (15 GB read, 15 written).  8 groups of
+// 4096 rows, 4096 x 14336: 2.02 ms in runs of three (1.91 PFLOP/s), 2.31 ms
+// back to back (1.67 PFLOP/s at the 1.54 GHz that the power cap leaves).
 #include <algorithm>
 
 #include "gemm2sm.cuh"

@@ -148,7 +148,9 @@ __device__ __forceinline__ void by_features(const Args &p, int r, int n, int e, 
 
 // grid (feature blocks, groups).  Two blocks an SM with two steps' loads in flight
 // each, or (DEEP) one with four, for grids that leave an SM one block: 16 rows of
-// four groups, 7168 -> 2048, 35.5 / 39.6 us; of one group 19.1 / 15.0.
+// four groups, 7168 -> 2048, 35.5 / 39.6 us; of one group 19.1 / 15.0.  (The
+// two-block form's 64 registers spill: 52 bytes stored and 152 loaded a thread with
+// 32 features, 28 and 68 with 16.)
 template <typename T, int MT, bool DEEP>
 __global__ void __launch_bounds__(32 * WARPS, DEEP ? 1 : 2) thin_kernel(const Args p) {
   extern __shared__ __align__(16) float part[];

@@ -506,8 +506,9 @@ typedef struct sym_groups {
  * for the rows r of group e (F = out->cols, C = x->cols).  With w [E][F][C]
  * the first form is a linear layer's forward product and, on the same weights
  * with the sizes exchanged, the second its data gradient.
- *   dtype: SYM_BF16 or SYM_FP16, of x, w and out; accumulated in fp32 in
- *   tensor memory, rounded once.
+ *   dtype: SYM_BF16 or SYM_FP16, of x, w and out; accumulated in fp32 (few rows
+ *   on the CUDA cores or by warp-wide products, more in tensor memory) in an order
+ *   that depends on the sizes, the groups and the device's SM count, rounded once.
  *   w: device, 16-byte aligned; matrix e at element e * w_group_stride, its
  *   rows w_ld elements apart, both multiples of 8; matrices do not overlap.
  *   x: 16-byte aligned, ld (and slot_stride) multiples of 8.  out: any ld.
@@ -554,6 +555,8 @@ int moe_grouped_wgrad(const sym_groups *g, int dtype, const sym_rows *dy, const 
  *   total: device int32, total[d * total_slot_stride] = rows of slot d to do
  *   (read by the kernel, cut to [0, rows]); NULL: all.  Other rows are not
  *   read or written.
+ * The exponential is the fast one for every type: silu is off by 2e-7 relative
+ * for positive g, 1e-6 at g = -20 and 2e-6 at -30 (the norms' sigmoid gates too).
  * h may be g or u.  Returns SYM_OK, SYM_EINVAL or SYM_ECUDA; asynchronous.
  */
 int moe_swiglu_rows(int dtype, const sym_rows *g, const sym_rows *u, const float *row_w,
@@ -637,8 +640,9 @@ int moe_block_norm(const sym_block_norm *a, symmoe_stream_t stream);
  *   of the type of what it is the gradient of, each may be NULL.
  *   work: device, 16-byte aligned, at least moe_block_norm_workspace(...)
  *   bytes; contents do not matter before or after.
- * Column sums are taken in 32 bits in an order that depends on the sizes and
- * the device's SM count only.
+ * Column sums are taken in 32 bits in an order that depends on the sizes, the
+ * type, on whether every base, stride and cols allow 16-byte vectors, and on the
+ * device's SM count only.
  */
 typedef struct sym_block_norm_grad {
   const void *dy, *dh;
