@@ -85,12 +85,13 @@ __device__ __forceinline__ void raise(int32_t *status, int bits) {
 }
 
 // Bounded wait (cluster-scope acquire: some arrivals come from the pair's
-// other CTA after generic stores); a timeout sets the CTA's abort flag.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, const Ctl &c) {
+// other CTA after generic stores); a timeout sets the CTA's abort flag.  A wait
+// that may outlast several of the pair's tiles has the limit for each of them.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, const Ctl &c, uint32_t tiles = 1) {
   const uint32_t a = smem_u32(bar);
   if (mbar_try_wait_cluster(a, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  const uint64_t limit = (uint64_t)c.tmo * 1000ull;
+  const uint64_t limit = (uint64_t)c.tmo * tiles * 1000ull;
   for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait_cluster(a, parity)) return true;
     if (*c.abort) return false;
@@ -745,13 +746,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
   } else if (wid == 2 + WG_EPI_WARPS) {
     // --------------------------------------------- the groups' last cnt mod 16
     // rows: loaded one tile ahead, zeroed past the end, reported to the leader.
+    // This warp runs ahead over the tiles without such rows, so what it waits for
+    // may come only after all of the pair's tiles so far.
     // Only these steps cross the pair by a release at cluster scope (as part
     // of every K block it held each to 0.8 us).
     auto load = [&](int i, uint32_t n) {  // tile i's rows as use n of the side buffers
       const WTile &ti = walk.at(pair_tile(i, pair, npairs));
       const int j = n & 1, row = ti.row0 + (ti.cnt & ~(UK - 1));
       const int f0 = ti.f * 256 + (int)rank * 128, c0 = ti.c * tile_c + (int)rank * own_c;
-      if (!__all_sync(0xffffffffu, bar_wait(&rest_empty[j], ((n >> 1) & 1u) ^ 1u, ctl))) return false;
+      if (!__all_sync(0xffffffffu, bar_wait(&rest_empty[j], ((n >> 1) & 1u) ^ 1u, ctl, i + 1))) return false;
       if (lane == 0) {
         uint8_t *sb = rest + j * REST_BYTES;
         mbar_arrive_expect_tx(&rest_in[j], (2u + (uint32_t)own_c / 64u) * REST_CHUNK);
@@ -785,7 +788,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
       if (rank != 0) {
         if (lane == 0) mbar_arrive_remote(map_to(&rest_peer[j], 0));
       } else {
-        if (!(ok = __all_sync(0xffffffffu, bar_wait(&rest_peer[j], parity, ctl)))) break;
+        if (!(ok = __all_sync(0xffffffffu, bar_wait(&rest_peer[j], parity, ctl, i + 1)))) break;
         if (lane == 0) mbar_arrive(&rest_full[j]);
       }
       i = after;

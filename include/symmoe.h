@@ -487,7 +487,8 @@ typedef struct sym_rows {
  * but must not overlap.  A group whose range does not lie in [0, rows) of its
  * slot is taken as empty and SYM_STATUS_OVERFLOW is raised.
  *   status: device word that SYM_STATUS_* bits are OR-ed into, or NULL;
- *   wait_timeout_us: bound on the kernels' internal waits (0: 2,000,000).
+ *   wait_timeout_us: bound on each of the kernels' internal waits, for every output
+ *   tile that it may span (0: 2,000,000); SYM_STATUS_TIMEOUT where one runs out.
  */
 typedef struct sym_groups {
   const int32_t *cnt, *off;

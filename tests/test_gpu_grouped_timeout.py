@@ -80,3 +80,28 @@ def test_product_under_a_short_limit(flags):
     sm.moe_grouped_matmul(x, w, cnt, off, want, trans_w=bool(flags))
     assert int(status) != 0 or torch.equal(out, want)
     small_calls_are_right()
+
+
+def test_weight_gradient_that_outlasts_the_limit_of_one_wait():
+    """The limit is for a wait, not for the launch: a long group without a remainder
+    between short ones with one takes several times the limit, each of its tiles a
+    fraction of it."""
+    big, C = 200_000, 8192  # about 14 tiles of a millisecond for each pair
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    cnt, off, n = groups_of([3, big, 5])
+    x, dy = (torch.randn(1, n, C, generator=gen, device="cuda", dtype=torch.bfloat16)[0] for _ in range(2))
+    dw = torch.empty(3, C, C, device="cuda", dtype=torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    start.record()
+    assert wgrad(dy, x, dw, groups(cnt, off, status, 4000)) == sm.SYM_OK
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) > 8, "not the long launch that this is about"
+    assert int(status) == 0
+    for e, (at, rows_) in enumerate(((0, 3), (3 + big, 5))):
+        g = [0, 2][e]
+        ref = dy[at:at + rows_].double().T @ x[at:at + rows_].double()
+        mag = dy[at:at + rows_].double().abs().T @ x[at:at + rows_].double().abs()
+        assert_within(dw[g], ref, mag, "wgrad", product_bound(rows_))
