@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(MAXT, !DROP && NG == 2 ? 1 : 0)
 // Bound by instructions: an element at a time, bf16 and fp32 take the same time
 // (218 and 229 us forward at 16384 x 4095, 144 and 174 without dropout).  With
 // the next row's elements loaded into registers instead, 307 us, and 757 against
-// 325 backward; columns a block's width apart, whose addresses are computed, 250
+// 335 backward; columns a block's width apart, whose addresses are computed, 250
 // and 423.
 // ---------------------------------------------------------------------------
 constexpr int ODD_EACH = 8, ODD_COLS = ODD_EACH * 1024;
