@@ -87,6 +87,33 @@ class SymBlockNormGrad(ctypes.Structure):
                 ("ld_dgate", _i64), ("work", _u64), ("work_bytes", _u64)]
 
 
+class SymLayerNorm(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i32), ("dtype", _i32), ("x", _u64), ("add", _u64), ("w", _u64), ("b", _u64),
+                ("sum", _u64), ("h", _u64), ("mean", _u64), ("rstd", _u64), ("ld_x", _i64), ("ld_add", _i64),
+                ("ld_sum", _i64), ("ld_h", _i64), ("eps", ctypes.c_float), ("reserved", _u32)]
+
+
+class SymLayerNormGrad(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i32), ("dtype", _i32), ("dh", _u64), ("s", _u64), ("dsum", _u64), ("w", _u64),
+                ("mean", _u64), ("rstd", _u64), ("dx", _u64), ("dw", _u64), ("db", _u64), ("ld_dh", _i64),
+                ("ld_s", _i64), ("ld_dsum", _i64), ("ld_dx", _i64), ("work", _u64), ("work_bytes", _u64)]
+
+
+class SymOrthogonalize(ctypes.Structure):
+    _fields_ = [("count", _i32), ("rows", _i32), ("cols", _i32), ("steps", _i32), ("g_dtype", _i32), ("out_dtype", _i32),
+                ("coeffs", ctypes.c_float * 3), ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("reserved", _u32),
+                ("g", _u64), ("out", _u64), ("g_stride", _i64), ("ld_g", _i64), ("out_stride", _i64), ("ld_out", _i64),
+                ("work", _u64), ("work_bytes", _u64)]
+
+
+class SymFewTokens(ctypes.Structure):
+    _fields_ = [("tokens", _i32), ("hidden", _i32), ("inter", _i32), ("num_experts", _i32), ("topk", _i32),
+                ("dtype", _i32), ("x", _u64), ("w_gate", _u64), ("w_up", _u64), ("w_down", _u64), ("w_router", _u64),
+                ("logits", _u64), ("idx", _u64), ("w", _u64), ("out", _u64), ("ld_x", _i64), ("ld_out", _i64),
+                ("gate_group", _i64), ("gate_ld", _i64), ("up_group", _i64), ("up_ld", _i64), ("down_group", _i64),
+                ("down_ld", _i64), ("router_ld", _i64), ("work", _u64), ("work_bytes", _u64)]
+
+
 class SymmoeError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -135,6 +162,13 @@ def lib() -> ctypes.CDLL:
         L.moe_block_norm.argtypes = [P(SymBlockNorm), _vp]
         L.moe_block_norm_bwd.argtypes = [P(SymBlockNorm), P(SymBlockNormGrad), _vp]
         L.moe_block_norm_workspace.argtypes = [_i64, _i32, _i64, P(_u64)]
+        L.moe_layer_norm.argtypes = [P(SymLayerNorm), _vp]
+        L.moe_layer_norm_bwd.argtypes = [P(SymLayerNormGrad), _vp]
+        L.moe_layer_norm_workspace.argtypes = [_i64, _i32, P(_u64)]
+        L.moe_orthogonalize.argtypes = [P(SymOrthogonalize), _vp]
+        L.moe_orthogonalize_workspace.argtypes = [_i32, _i32, _i32, P(_u64), P(_u64)]
+        L.moe_few_tokens.argtypes = [P(SymFewTokens), _vp]
+        L.moe_few_tokens_workspace.argtypes = [_i32, _i32, _i32, P(_u64)]
         L.sym_strerror.argtypes = [ctypes.c_int]
         L.sym_strerror.restype = ctypes.c_char_p
         _lib = L
@@ -558,6 +592,131 @@ def moe_block_norm_bwd(dy=None, dh=None, y=None, o=None, w_post=None, gate=None,
         _need(work.is_contiguous(), where, "work is contiguous")
         g.work, g.work_bytes = work.data_ptr(), work.numel() * work.element_size()
     _check(lib().moe_block_norm_bwd(ctypes.byref(a), ctypes.byref(g), _stream_of(stream, dev)), where)
+
+
+# ------------------------------------------------------------------ layer norm
+
+def moe_layer_norm(x, h=None, w=None, b=None, add=None, sum=None, mean=None, rstd=None, eps: float = 1e-5,
+                   stream=None) -> None:
+    """h = (s - mean) * rstd * w + b over the rows [R, C] of s = x + add (or x);
+    sum takes s.  mean, rstd: float32 [R], kept for the backward."""
+    where = "moe_layer_norm"
+    dev = _on_device(where, x, h, w, b, add, sum, mean, rstd)
+    _need(x.dim() == 2, where, "x is [rows, cols]")
+    (rows, cols), dt = x.shape, x.dtype
+    xp, xl = _plain(x, rows, cols, dt, where)
+    ap, al = _plain(add, rows, cols, dt, where)
+    sp, sl = _plain(sum, rows, cols, dt, where)
+    hp, hl = _plain(h, rows, cols, dt, where)
+    a = SymLayerNorm(rows, cols, _DTYPES.get(dt, -1), xp, ap, _vector(w, cols, dt, where), _vector(b, cols, dt, where), sp,
+                     hp, _vector(mean, rows, torch.float32, where), _vector(rstd, rows, torch.float32, where), xl, al, sl,
+                     hl, eps, 0)
+    _check(lib().moe_layer_norm(ctypes.byref(a), _stream_of(stream, dev)), where)
+
+
+def moe_layer_norm_workspace(rows: int, cols: int) -> int:
+    """Workspace bytes of moe_layer_norm_bwd."""
+    out = _u64()
+    _check(lib().moe_layer_norm_workspace(rows, cols, ctypes.byref(out)), "moe_layer_norm_workspace")
+    return out.value
+
+
+def _work(work, where: str):
+    if work is None:
+        return 0, 0
+    _need(work.is_contiguous(), where, "work is contiguous")
+    return work.data_ptr(), work.numel() * work.element_size()
+
+
+def moe_layer_norm_bwd(dh, s, mean, rstd, dx=None, w=None, dsum=None, dw=None, db=None, work=None, stream=None) -> None:
+    """Gradients of moe_layer_norm from dh (of h) and dsum (of s, from elsewhere),
+    with the forward's s, mean and rstd.  Every output may be left out.  work (for
+    dw and db): a uint8 tensor of moe_layer_norm_workspace bytes."""
+    where = "moe_layer_norm_bwd"
+    dev = _on_device(where, dh, s, mean, rstd, dx, w, dsum, dw, db, work)
+    _need(dh is not None and dh.dim() == 2 and s is not None, where, "dh and s, [rows, cols], are wanted")
+    (rows, cols), dt = dh.shape, dh.dtype
+    hp, hl = _plain(dh, rows, cols, dt, where)
+    sp, sl = _plain(s, rows, cols, dt, where)
+    dp, dl = _plain(dsum, rows, cols, dt, where)
+    xp, xl = _plain(dx, rows, cols, dt, where)
+    wp, wn = _work(work, where)
+    a = SymLayerNormGrad(rows, cols, _DTYPES.get(dt, -1), hp, sp, dp, _vector(w, cols, dt, where),
+                         _vector(mean, rows, torch.float32, where), _vector(rstd, rows, torch.float32, where), xp,
+                         _vector(dw, cols, dt, where), _vector(db, cols, dt, where), hl, sl, dl, xl, wp, wn)
+    _check(lib().moe_layer_norm_bwd(ctypes.byref(a), _stream_of(stream, dev)), where)
+
+
+# ------------------------------------------------------------------ updates of the experts' matrices
+
+def _batch(t, where: str):
+    """(matrices, rows, columns, stride of a matrix, of a row) of [F, C] or [E, F, C]."""
+    _need(t.dim() in (2, 3), where, "matrices [F, C] or [E, F, C] are wanted")
+    count = t.shape[0] if t.dim() == 3 else 1
+    f, c = t.shape[-2:]
+    _need(c <= 1 or t.stride(-1) == 1, where, "the last dimension has to be contiguous")
+    return count, f, c, (t.stride(0) if count > 1 else f * c), (t.stride(-2) if f > 1 else c)
+
+
+def moe_orthogonalize_workspace(count: int, rows: int, cols: int, least: bool = False) -> int:
+    """Workspace bytes of moe_orthogonalize: what it runs best with, or the least it takes."""
+    best, low = _u64(), _u64()
+    _check(lib().moe_orthogonalize_workspace(count, rows, cols, ctypes.byref(best), ctypes.byref(low)),
+           "moe_orthogonalize_workspace")
+    return low.value if least else best.value
+
+
+def moe_orthogonalize(g, out, work, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                      scale: float = 1.0, stream=None) -> None:
+    """out = scale * X after `steps` Newton-Schulz products, X = a X + (b A + c A A) X
+    with A = X X^T, from X = g / (norm of g + eps), for every matrix of g [F, C] or
+    [E, F, C] (bf16, fp16 or float32; out bf16 or fp16).  work: a uint8 tensor."""
+    where = "moe_orthogonalize"
+    dev = _on_device(where, g, out, work)
+    _need(g.shape == out.shape, where, "g and out have one shape")
+    _need(len(coeffs) == 3, where, "three coefficients are wanted")
+    count, f, c, gs, gl = _batch(g, where)
+    os_, ol = _batch(out, where)[3:]
+    wp, wn = _work(work, where)
+    a = SymOrthogonalize(count, f, c, steps, _DTYPES.get(g.dtype, -1), _DTYPES.get(out.dtype, -1),
+                         (ctypes.c_float * 3)(*coeffs), eps, scale, 0, g.data_ptr(), out.data_ptr(), gs, gl, os_, ol, wp, wn)
+    _check(lib().moe_orthogonalize(ctypes.byref(a), _stream_of(stream, dev)), where)
+
+
+# ------------------------------------------------------------------ a few tokens
+
+def moe_few_tokens_workspace(tokens: int, inter: int, topk: int) -> int:
+    """Workspace bytes of moe_few_tokens."""
+    out = _u64()
+    _check(lib().moe_few_tokens_workspace(tokens, inter, topk, ctypes.byref(out)), "moe_few_tokens_workspace")
+    return out.value
+
+
+def moe_few_tokens(x, w_gate, w_up, w_down, logits, idx, w, out, work, w_router=None, stream=None) -> None:
+    """A whole MoE layer for up to 32 tokens x [T, H]: logits [T, E] (float32; made
+    from w_router [E, H] where that is given), idx and w [T, k] of each token's k
+    experts, out = their SwiGLU's sum.  w_gate, w_up [E, I, H], w_down [E, H, I];
+    bf16 or fp16.  work: a uint8 tensor of moe_few_tokens_workspace bytes."""
+    where = "moe_few_tokens"
+    dev = _on_device(where, x, w_gate, w_up, w_down, logits, idx, w, out, work, w_router)
+    _need(x.dim() == 2 and logits.dim() == 2 and idx.dim() == 2 and w_gate.dim() == 3, where,
+          "x [T, H], logits [T, E], idx [T, k] and w_gate [E, I, H] are wanted")
+    (tokens, hidden), experts, topk, inter, dt = x.shape, logits.shape[1], idx.shape[1], w_gate.shape[1], x.dtype
+    xp, xl = _plain(x, tokens, hidden, dt, where)
+    op, ol = _plain(out, tokens, hidden, dt, where)
+    for t, n, kind in ((logits, experts, torch.float32), (idx, topk, torch.int32), (w, topk, torch.float32)):
+        _need(t.shape == (tokens, n) and t.dtype == kind and t.is_contiguous(), where,
+              f"[{tokens}, {n}] {kind}, contiguous, is wanted")
+    _need(w_gate.dtype == dt and w_up.dtype == dt and w_down.dtype == dt, where, "x and the weights have one type")
+    gg, gl = _matrices(w_gate, experts, (inter, hidden), where)
+    ug, ul = _matrices(w_up, experts, (inter, hidden), where)
+    dg, dl = _matrices(w_down, experts, (hidden, inter), where)
+    rp, rl = _plain(w_router, experts, hidden, dt, where)
+    wp, wn = _work(work, where)
+    a = SymFewTokens(tokens, hidden, inter, experts, topk, _DTYPES.get(dt, -1), xp, w_gate.data_ptr(), w_up.data_ptr(),
+                     w_down.data_ptr(), rp, logits.data_ptr(), idx.data_ptr(), w.data_ptr(), op, xl, ol, gg, gl, ug, ul, dg,
+                     dl, rl, wp, wn)
+    _check(lib().moe_few_tokens(ctypes.byref(a), _stream_of(stream, dev)), where)
 
 
 # ------------------------------------------------------------------ heap owner

@@ -58,6 +58,13 @@ cudaError_t launch_dropout(int dtype, const sym_rows &x, const sym_rows *res, co
                            uint64_t offset, double drop, int num_sms, cudaStream_t st);
 size_t block_norm_workspace(int64_t rows, int cols, int64_t gates, int num_sms);
 cudaError_t launch_block_norm(const sym_block_norm &a, int num_sms, cudaStream_t st);
+size_t layer_norm_workspace(int64_t rows, int cols, int num_sms);
+cudaError_t launch_layer_norm(const sym_layer_norm &a, int num_sms, cudaStream_t st);
+cudaError_t launch_layer_norm_bwd(const sym_layer_norm_grad &a, int num_sms, cudaStream_t st);
+void orthogonalize_workspace(int count, int rows, int cols, int num_sms, size_t *least, size_t *best);
+cudaError_t launch_orthogonalize(const sym_orthogonalize &a, int num_sms, cudaStream_t st);
+size_t few_tokens_workspace(int tokens, int inter, int topk);
+cudaError_t launch_few_tokens(const sym_few_tokens &a, int num_sms, cudaStream_t st);
 cudaError_t launch_block_norm_bwd(const sym_block_norm &a, const sym_block_norm_grad &b, int num_sms,
                                   cudaStream_t st);
 }  // namespace symmoe
@@ -448,6 +455,7 @@ static bool like_ok(const sym_rows *r, const sym_rows *first, int dtype) {
   return rows_ok(r, size_of(dtype)) && same_rows(r, first) && r->cols == first->cols;
 }
 static bool opt4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool opt16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int moe_swiglu_rows(int dtype, const sym_rows *g, const sym_rows *u, const float *row_w, int64_t row_w_slot_stride,
                     const int32_t *total, int64_t total_slot_stride, const sym_rows *h, symmoe_stream_t stream) {
@@ -558,6 +566,126 @@ int moe_block_norm_bwd(const sym_block_norm *a, const sym_block_norm_grad *g, sy
   if (sms <= 0) return SYM_ECUDA;
   if (!g->work || g->work_bytes < block_norm_workspace(R, C, g->dgate ? a->gate_rows : 0, sms)) return SYM_ENOSPACE;
   return from_cuda(launch_block_norm_bwd(*a, *g, sms, (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// layer norm, updates of the experts' matrices, a few tokens
+// ---------------------------------------------------------------------------
+static bool norm_shape_ok(int64_t rows, int cols) { return rows >= 0 && rows < (int64_t(1) << 30) && cols >= 1 && cols <= 65536; }
+
+int moe_layer_norm(const sym_layer_norm *a, symmoe_stream_t stream) {
+  if (!a || !dtype_ok(a->dtype) || !norm_shape_ok(a->rows, a->cols) || !(a->eps >= 0.f)) return SYM_EINVAL;
+  const int64_t R = a->rows;
+  const int C = a->cols, t = a->dtype;
+  if (!tensor_ok(a->x, a->ld_x, R, C, t) || !tensor_ok(a->add, a->ld_add, R, C, t) || !tensor_ok(a->sum, a->ld_sum, R, C, t) ||
+      !tensor_ok(a->h, a->ld_h, R, C, t) || !tensor_ok(a->w, 0, 1, C, t) || !tensor_ok(a->b, 0, 1, C, t) || !opt4(a->mean) ||
+      !opt4(a->rstd))
+    return SYM_EINVAL;
+  if (R == 0) return SYM_OK;
+  if (!a->x || (!a->h && !a->sum && !a->mean && !a->rstd) || (a->h && a->h == a->sum)) return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  return from_cuda(launch_layer_norm(*a, sms, (cudaStream_t)stream));
+}
+
+int moe_layer_norm_workspace(int64_t rows, int32_t cols, uint64_t *bytes) {
+  if (!bytes || !norm_shape_ok(rows, cols)) return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  *bytes = rows == 0 ? 0 : layer_norm_workspace(rows, cols, sms);
+  return SYM_OK;
+}
+
+int moe_layer_norm_bwd(const sym_layer_norm_grad *a, symmoe_stream_t stream) {
+  if (!a || !dtype_ok(a->dtype) || !norm_shape_ok(a->rows, a->cols)) return SYM_EINVAL;
+  const int64_t R = a->rows;
+  const int C = a->cols, t = a->dtype;
+  if (!tensor_ok(a->dh, a->ld_dh, R, C, t) || !tensor_ok(a->s, a->ld_s, R, C, t) || !tensor_ok(a->dsum, a->ld_dsum, R, C, t) ||
+      !tensor_ok(a->dx, a->ld_dx, R, C, t) || !tensor_ok(a->w, 0, 1, C, t) || !tensor_ok(a->dw, 0, 1, C, t) ||
+      !tensor_ok(a->db, 0, 1, C, t) || !opt4(a->mean) || !opt4(a->rstd) || !opt16(a->work))
+    return SYM_EINVAL;
+  if (!a->dx && !a->dw && !a->db) return SYM_EINVAL;
+  if (R == 0) {  // sums over no rows
+    const cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = cudaSuccess;
+    if (a->dw) e = cudaMemsetAsync(a->dw, 0, C * size_of(t), st);
+    if (e == cudaSuccess && a->db) e = cudaMemsetAsync(a->db, 0, C * size_of(t), st);
+    return from_cuda(e);
+  }
+  if (!a->dh || !a->s || !a->mean || !a->rstd) return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  if ((a->dw || a->db) && (!a->work || a->work_bytes < layer_norm_workspace(R, C, sms))) return SYM_ENOSPACE;
+  return from_cuda(launch_layer_norm_bwd(*a, sms, (cudaStream_t)stream));
+}
+
+static bool orth_shape_ok(int count, int rows, int cols) {
+  return count >= 0 && count <= 65535 && rows >= 1 && rows <= 65536 && cols >= 1 && cols <= 65536;
+}
+// matrices of a batch: aligned to their type, rows and matrices that do not overlap
+static bool matrices_ok(const void *p, int count, int rows, int cols, int64_t stride, int64_t ld, int dtype) {
+  return p && reinterpret_cast<uintptr_t>(p) % size_of(dtype) == 0 && (rows == 1 || ld >= cols) &&
+         (count == 1 || stride >= (rows - 1) * (rows == 1 ? 0 : ld) + cols);
+}
+
+int moe_orthogonalize_workspace(int32_t count, int32_t rows, int32_t cols, uint64_t *work_bytes, uint64_t *least_bytes) {
+  if (!orth_shape_ok(count, rows, cols) || (!work_bytes && !least_bytes)) return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  size_t least = 0, best = 0;
+  orthogonalize_workspace(count, rows, cols, sms, &least, &best);
+  if (work_bytes) *work_bytes = best;
+  if (least_bytes) *least_bytes = least;
+  return SYM_OK;
+}
+
+int moe_orthogonalize(const sym_orthogonalize *a, symmoe_stream_t stream) {
+  if (!a || !orth_shape_ok(a->count, a->rows, a->cols) || a->steps < 0 || a->steps > 64 || !dtype_ok(a->g_dtype) ||
+      (a->out_dtype != SYM_BF16 && a->out_dtype != SYM_FP16) || !(a->eps >= 0.f) || (reinterpret_cast<uintptr_t>(a->work) & 255u))
+    return SYM_EINVAL;
+  if (a->count == 0) return SYM_OK;
+  if (!matrices_ok(a->g, a->count, a->rows, a->cols, a->g_stride, a->ld_g, a->g_dtype) ||
+      !matrices_ok(a->out, a->count, a->rows, a->cols, a->out_stride, a->ld_out, a->out_dtype))
+    return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  size_t least = 0, best = 0;
+  orthogonalize_workspace(a->count, a->rows, a->cols, sms, &least, &best);
+  if (!a->work || a->work_bytes < least) return SYM_ENOSPACE;
+  return from_cuda(launch_orthogonalize(*a, sms, (cudaStream_t)stream));
+}
+
+static bool few_shape_ok(int tokens, int inter, int topk) {
+  return tokens >= 0 && tokens <= 32 && inter >= 8 && inter <= 65536 && inter % 8 == 0 && topk >= 1 && topk <= 32;
+}
+// an expert's matrices: 16-byte aligned rows, none over another
+static bool expert_ok(const void *p, int experts, int rows, int cols, int64_t group, int64_t ld) {
+  return aligned16(p) && ld % 8 == 0 && ld >= cols && (experts == 1 || (group % 8 == 0 && group >= (rows - 1) * ld + cols));
+}
+
+int moe_few_tokens_workspace(int32_t tokens, int32_t inter, int32_t topk, uint64_t *bytes) {
+  if (!bytes || !few_shape_ok(tokens, inter, topk)) return SYM_EINVAL;
+  *bytes = few_tokens_workspace(tokens, inter, topk);
+  return SYM_OK;
+}
+
+int moe_few_tokens(const sym_few_tokens *a, symmoe_stream_t stream) {
+  if (!a || !few_shape_ok(a->tokens, a->inter, a->topk) || a->hidden < 8 || a->hidden > 65536 || a->hidden % 8 != 0 ||
+      a->num_experts < 1 || a->num_experts > 1024 || a->topk > a->num_experts || (a->dtype != SYM_BF16 && a->dtype != SYM_FP16))
+    return SYM_EINVAL;
+  const int T = a->tokens, H = a->hidden, I = a->inter, E = a->num_experts;
+  if (!expert_ok(a->w_gate, E, I, H, a->gate_group, a->gate_ld) || !expert_ok(a->w_up, E, I, H, a->up_group, a->up_ld) ||
+      !expert_ok(a->w_down, E, H, I, a->down_group, a->down_ld) || (a->w_router && !expert_ok(a->w_router, 1, E, H, 0, a->router_ld)) ||
+      !opt16(a->work))
+    return SYM_EINVAL;
+  if (T == 0) return SYM_OK;
+  if (!aligned16(a->x) || (T > 1 && (a->ld_x % 8 != 0 || a->ld_x < H)) || !a->out || (reinterpret_cast<uintptr_t>(a->out) & 1u) ||
+      (T > 1 && a->ld_out < H) || !aligned4(a->logits) || !aligned4(a->idx) || !aligned4(a->w))
+    return SYM_EINVAL;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return SYM_ECUDA;
+  if (!a->work || a->work_bytes < few_tokens_workspace(T, I, a->topk)) return SYM_ENOSPACE;
+  return from_cuda(launch_few_tokens(*a, sms, (cudaStream_t)stream));
 }
 
 const char *sym_strerror(int code) {

@@ -1,0 +1,331 @@
+// layer_norm.cu -- layer norm of rows with the residual sum in the same pass,
+// and its gradient with the reductions of the weight's and the bias'.
+//
+//   s = x + add;  h = (s - mean) * rstd * w + b     rstd = (mean((s - mean)^2) + eps)^-1/2
+//
+// Backward, with n = (s - mean) * rstd and g = dh * w:
+//   dx = dsum + rstd * (g - mean(g) - n * mean(g * n)),  dw = sum dh * n,  db = sum dh
+// (means over a row's columns, sums over the rows).
+//
+// Both are bound by the tensors' bytes.  The variance is the mean of squared
+// distances from the mean, a second walk of the row: the difference of the mean
+// square and the squared mean would lose what a row far from zero has left.
+#include <algorithm>
+#include <initializer_list>
+
+#include "rows_dev.cuh"
+
+namespace symmoe {
+namespace layer {
+
+using namespace rows;
+
+struct Fwd {
+  const void *x, *add, *w, *b;
+  void *sum, *h;
+  float *mean, *rstd;
+  int64_t ldx, ld_add, ld_sum, ldh;  // elements
+  int rows, cols;
+  float eps;
+};
+struct Bwd {
+  const void *dh, *s, *dsum, *w;
+  const float *mean, *rstd;
+  void *dx, *dw, *db;
+  float *ws;  // partial sums, [parts][2][cols]
+  int64_t ld_dh, ld_s, ld_dsum, ld_dx;
+  int rows, cols, parts;
+};
+
+template <typename T>
+__device__ __forceinline__ const T *at(const void *p, int row, int64_t ld) {
+  return reinterpret_cast<const T *>(p) + row * ld;
+}
+template <typename T>
+__device__ __forceinline__ T *at(void *p, int row, int64_t ld) {
+  return reinterpret_cast<T *>(p) + row * ld;
+}
+
+// A row's variance by its sum of squares v holds where v neither left the range of
+// fp32 nor is so small that squares vanished from it.
+__device__ __forceinline__ bool squares_hold(float v, float inv, float eps) {
+  return v <= 3e38f && v * inv + eps >= 1e-30f;
+}
+// Otherwise the row is taken again times a power of two that brings its largest
+// element to [1, 2): the exponent of it, from the group's largest.
+__device__ __forceinline__ int row_exponent(float largest, float *buf, int warp, int warps, int &turn) {
+  float m[1] = {largest};
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], s));
+  if (warps > 1) {
+    float *b = buf + turn * 32;
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) b[warp] = m[0];
+    __syncthreads();
+    m[0] = (threadIdx.x & 31) < warps ? b[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], s));
+  }
+  return m[0] > 0.f && m[0] <= 3.4028235e38f ? ilogbf(m[0]) : 0;
+}
+// rstd of a row whose scaled squares sum to v
+__device__ __forceinline__ float scaled_rstd(float v, int e, float inv, float eps) {
+  return (float)(1.0 / sqrt(ldexp((double)v * inv, 2 * e) + (double)eps));
+}
+
+// Forward for rows of any length: walked for the mean, the variance and the result
+// (out of L2 after the first time).
+template <typename T, int V>
+__global__ void __launch_bounds__(512) layer_norm_kernel(const Fwd p) {
+  __shared__ float buf[2 * 32];
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  const float inv = 1.f / p.cols;
+  int turn = 0;
+  for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    const T *x = at<T>(p.x, r, p.ldx), *add = p.add ? at<T>(p.add, r, p.ld_add) : nullptr;
+    auto each = [&](auto &&f) {  // f(c, s) for this thread's vectors
+      for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
+        float s[V], t[V];
+        load<T, V>(x + c, s);
+        if (add) {
+          load<T, V>(add + c, t);
+#pragma unroll
+          for (int i = 0; i < V; ++i) s[i] += t[i];
+        }
+        f(c, s);
+      }
+    };
+    float m[1] = {0.f}, v[1] = {0.f};
+    each([&](int, float(&s)[V]) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) m[0] += s[i];
+    });
+    group_sums<1>(m, buf, warp, warps, turn);
+    const float first = m[0] * inv;
+    each([&](int, float(&s)[V]) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[0] += (s[i] - first) * (s[i] - first);
+    });
+    group_sums<1>(v, buf, warp, warps, turn);
+    float mean = m[0] * inv, rstd = rsqrtf(v[0] * inv + p.eps);
+    if (!squares_hold(v[0], inv, p.eps)) {
+      float largest = 0.f;
+      each([&](int, float(&s)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) largest = fmaxf(largest, fabsf(s[i]));
+      });
+      const int e = row_exponent(largest, buf, warp, warps, turn);
+      m[0] = v[0] = 0.f;
+      each([&](int, float(&s)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) m[0] += ldexpf(s[i], -e);
+      });
+      group_sums<1>(m, buf, warp, warps, turn);
+      const float scaled = m[0] * inv;
+      each([&](int, float(&s)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float d = ldexpf(s[i], -e) - scaled;
+          v[0] += d * d;
+        }
+      });
+      group_sums<1>(v, buf, warp, warps, turn);
+      mean = ldexpf(scaled, e);
+      rstd = scaled_rstd(v[0], e, inv, p.eps);
+    }
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
+    }
+    each([&](int c, float(&s)[V]) {  // each column is read before it is written: h or sum may be x or add
+      if (p.sum) store<T, V>(at<T>(p.sum, r, p.ld_sum) + c, s);
+      if (!p.h) return;
+      float t[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = (s[i] - mean) * rstd;
+      if (p.w) {
+        load<T, V>(reinterpret_cast<const T *>(p.w) + c, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] *= t[i];
+      }
+      if (p.b) {
+        load<T, V>(reinterpret_cast<const T *>(p.b) + c, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] += t[i];
+      }
+      store<T, V>(at<T>(p.h, r, p.ldh) + c, s);
+    });
+  }
+}
+
+// dx for rows of any length
+template <typename T, int V>
+__global__ void __launch_bounds__(512) layer_norm_dx_kernel(const Bwd p) {
+  __shared__ float buf[2 * 32 * 2];
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  const float inv = 1.f / p.cols;
+  int turn = 0;
+  for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    const float mean = p.mean[r], rstd = p.rstd[r];
+    const T *dh = at<T>(p.dh, r, p.ld_dh), *sr = at<T>(p.s, r, p.ld_s);
+    auto each = [&](auto &&f) {  // f(c, g, n)
+      for (int c = (int)threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
+        float g[V], n[V], t[V];
+        load<T, V>(dh + c, g);
+        load<T, V>(sr + c, n);
+        if (p.w) {
+          load<T, V>(reinterpret_cast<const T *>(p.w) + c, t);
+#pragma unroll
+          for (int i = 0; i < V; ++i) g[i] *= t[i];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) n[i] = (n[i] - mean) * rstd;
+        f(c, g, n);
+      }
+    };
+    float v[2] = {0.f, 0.f};
+    each([&](int, float(&g)[V], float(&n)[V]) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[0] += g[i];
+        v[1] += g[i] * n[i];
+      }
+    });
+    group_sums<2>(v, buf, warp, warps, turn);
+    const float mg = v[0] * inv, mgn = v[1] * inv;
+    each([&](int c, float(&g)[V], float(&n)[V]) {
+      float t[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] = rstd * (g[i] - mg - n[i] * mgn);
+      if (p.dsum) {
+        load<T, V>(at<T>(p.dsum, r, p.ld_dsum) + c, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] += t[i];
+      }
+      store<T, V>(at<T>(p.dx, r, p.ld_dx) + c, g);
+    });
+  }
+}
+
+// Column sums of dh n and dh over a part of the rows: grid (column tiles, parts).
+// A thread has a vector of columns, the block's 8 warps every eighth row.
+constexpr int SUM_WARPS = 8;
+template <typename T, int V>
+__global__ void __launch_bounds__(32 * SUM_WARPS) layer_norm_columns_kernel(const Bwd p) {
+  __shared__ float part[SUM_WARPS][2][32 * V];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int c = (blockIdx.x * 32 + lane) * V;
+  float a[V], b[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) a[i] = b[i] = 0.f;
+  if (c < p.cols)
+    for (int r = blockIdx.y * SUM_WARPS + warp; r < p.rows; r += gridDim.y * SUM_WARPS) {
+      const float mean = p.mean[r], rstd = p.rstd[r];
+      float g[V], n[V];
+      load<T, V>(at<T>(p.dh, r, p.ld_dh) + c, g);
+      load<T, V>(at<T>(p.s, r, p.ld_s) + c, n);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        a[i] += g[i] * ((n[i] - mean) * rstd);
+        b[i] += g[i];
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    part[warp][0][lane * V + i] = a[i];
+    part[warp][1][lane * V + i] = b[i];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * 32 * V; i += blockDim.x) {
+    const int k = i / (32 * V), j = i % (32 * V), col = blockIdx.x * 32 * V + j;
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < SUM_WARPS; ++v) s += part[v][k][j];
+    if (col < p.cols) p.ws[((int64_t)blockIdx.y * 2 + k) * p.cols + col] = s;
+  }
+}
+// The parts' sums added in order: grid (columns / 32, 2), every warp takes every 32nd part
+template <typename T>
+__global__ void __launch_bounds__(1024) layer_norm_join_kernel(const Bwd p) {
+  __shared__ float part[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane, k = blockIdx.y;
+  T *to = reinterpret_cast<T *>(k ? p.db : p.dw);
+  if (!to) return;
+  pdl_wait();
+  float s = 0.f;
+  if (c < p.cols)
+    for (int i = warp; i < p.parts; i += 32) s += p.ws[((int64_t)i * 2 + k) * p.cols + c];
+  part[warp][lane] = s;
+  __syncthreads();
+  float v[1] = {part[lane][warp]};
+  warp_sums<1>(v);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane == 0 && col < p.cols) to[col] = Elem<T>::put(v[0]);
+}
+
+static bool vec_ok(std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> lds, int cols, int64_t es) {
+  for (const void *q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) % 16) return false;
+  for (int64_t l : lds)
+    if (l * es % 16) return false;
+  return cols * es % 16 == 0;
+}
+static int threads_of(int cols, int v) { return std::min(512, std::max(32, (cols / v + 31) / 32 * 32)); }
+// rows' parts of the column sums
+static int parts_of(int64_t rows, int num_sms) { return (int)std::max<int64_t>(1, std::min<int64_t>((rows + 63) / 64, num_sms)); }
+
+template <typename T, int V>
+static cudaError_t fwd(const Fwd &p, int num_sms, cudaStream_t st) {
+  layer_norm_kernel<T, V><<<std::min(p.rows, num_sms * 8), threads_of(p.cols, V), 0, st>>>(p);
+  return cudaGetLastError();
+}
+template <typename T, int V>
+static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
+  // (the column sums first: dx may be dh or s)
+  if (p.dw || p.db) {
+    p.parts = parts_of(p.rows, num_sms);
+    layer_norm_columns_kernel<T, V><<<dim3((p.cols + 32 * V - 1) / (32 * V), p.parts), 32 * SUM_WARPS, 0, st>>>(p);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(layer_norm_join_kernel<T>, dim3((p.cols + 31) / 32, 2), dim3(1024), 0, st, p);
+    if (err != cudaSuccess) return err;
+  }
+  if (!p.dx) return cudaSuccess;
+  layer_norm_dx_kernel<T, V><<<std::min(p.rows, num_sms * 8), threads_of(p.cols, V), 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace layer
+
+size_t layer_norm_workspace(int64_t rows, int cols, int num_sms) {
+  return (size_t)layer::parts_of(rows, num_sms) * 2 * cols * sizeof(float);
+}
+
+cudaError_t launch_layer_norm(const sym_layer_norm &a, int num_sms, cudaStream_t st) {
+  using namespace layer;
+  const Fwd p{a.x, a.add, a.w, a.b, a.sum, a.h, a.mean, a.rstd, a.ld_x, a.ld_add, a.ld_sum, a.ld_h, (int)a.rows, a.cols, a.eps};
+  const int64_t es = a.dtype == SYM_FP32 ? 4 : 2;
+  const bool one = a.rows <= 1;  // (a single row has no stride)
+  const bool vec = vec_ok({p.x, p.add, p.w, p.b, p.sum, p.h},
+                          {one ? 0 : p.ldx, p.add && !one ? p.ld_add : 0, p.sum && !one ? p.ld_sum : 0, p.h && !one ? p.ldh : 0},
+                          p.cols, es);
+  if (a.dtype == SYM_BF16) return vec ? fwd<__nv_bfloat16, 8>(p, num_sms, st) : fwd<__nv_bfloat16, 1>(p, num_sms, st);
+  if (a.dtype == SYM_FP16) return vec ? fwd<__half, 8>(p, num_sms, st) : fwd<__half, 1>(p, num_sms, st);
+  return vec ? fwd<float, 4>(p, num_sms, st) : fwd<float, 1>(p, num_sms, st);
+}
+
+cudaError_t launch_layer_norm_bwd(const sym_layer_norm_grad &a, int num_sms, cudaStream_t st) {
+  using namespace layer;
+  const Bwd p{a.dh, a.s, a.dsum, a.w, a.mean, a.rstd, a.dx, a.dw, a.db, reinterpret_cast<float *>(a.work), a.ld_dh, a.ld_s,
+              a.ld_dsum, a.ld_dx, (int)a.rows, a.cols, 0};
+  const int64_t es = a.dtype == SYM_FP32 ? 4 : 2;
+  const bool one = a.rows <= 1;
+  const bool vec = vec_ok({p.dh, p.s, p.dsum, p.w, p.dx, p.dw, p.db},
+                          {one ? 0 : p.ld_dh, one ? 0 : p.ld_s, p.dsum && !one ? p.ld_dsum : 0, p.dx && !one ? p.ld_dx : 0},
+                          p.cols, es);
+  if (a.dtype == SYM_BF16) return vec ? bwd<__nv_bfloat16, 8>(p, num_sms, st) : bwd<__nv_bfloat16, 1>(p, num_sms, st);
+  if (a.dtype == SYM_FP16) return vec ? bwd<__half, 8>(p, num_sms, st) : bwd<__half, 1>(p, num_sms, st);
+  return vec ? bwd<float, 4>(p, num_sms, st) : bwd<float, 1>(p, num_sms, st);
+}
+
+}  // namespace symmoe

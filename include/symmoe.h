@@ -657,6 +657,143 @@ int moe_block_norm_bwd(const sym_block_norm *a, const sym_block_norm_grad *g, sy
 /* Workspace bytes of moe_block_norm_bwd (gate_rows 0: no gate gradient).  Host only. */
 int moe_block_norm_workspace(int64_t rows, int32_t cols, int64_t gate_rows, uint64_t *bytes);
 
+/*
+ * moe_layer_norm: layer norm of rows, with the residual sum in the same pass:
+ *   s = x + add                      (add NULL: s = x)
+ *   h = (s - mean) * rstd * w + b    mean, rstd = 1 / sqrt(mean((s - mean)^2) + eps) of the row
+ *   sum, if not NULL: s, rounded; h and the statistics come from the unrounded s.
+ *   w, b [cols]: NULL = ones, zeros.  mean, rstd: device fp32 [rows], out (kept
+ *   for the backward), each may be NULL.  h may be NULL.
+ * All tensors have the type dtype; rows ld_* elements apart; 16-byte vectors are
+ * used where a row of every tensor starts on a 16-byte boundary.  h or sum may be
+ * x or add, but sum is not h.
+ * The variance is the mean of the squared distances from the mean, all in fp32.
+ * rows < 2^30, cols <= 65536; eps >= 0.  A row whose s holds an infinity or NaN,
+ * and only that row, has results that are NaN.
+ */
+typedef struct sym_layer_norm {
+  int64_t rows;
+  int32_t cols, dtype;
+  const void *x, *add, *w, *b;
+  void *sum, *h;
+  float *mean, *rstd;
+  int64_t ld_x, ld_add, ld_sum, ld_h;
+  float eps;
+  uint32_t reserved;
+} sym_layer_norm;
+int moe_layer_norm(const sym_layer_norm *a, symmoe_stream_t stream);
+
+/*
+ * moe_layer_norm_bwd: gradients of moe_layer_norm, n = (s - mean) * rstd:
+ *   g = dh * w;   dx = dsum + rstd * (g - mean(g) - n * mean(g * n))
+ *   dw = sum over the rows of dh * n,   db = sum over the rows of dh.
+ *   s: the forward's s (x, or sum where something was added); mean, rstd as the
+ *   forward left them; dsum: gradient of s from elsewhere, or NULL.
+ *   dx is the gradient of x and of add; may be dh, dsum or s.  dx, dw, db: each may be NULL.
+ *   work: device, 16-byte aligned, at least moe_layer_norm_workspace(...) bytes;
+ *   contents do not matter before or after; not read where dw and db are NULL.
+ * The column sums are taken in 32 bits in an order that depends on the sizes, the
+ * type, the alignment and the device's SM count only.
+ */
+typedef struct sym_layer_norm_grad {
+  int64_t rows;
+  int32_t cols, dtype;
+  const void *dh, *s, *dsum, *w;
+  const float *mean, *rstd;
+  void *dx, *dw, *db;
+  int64_t ld_dh, ld_s, ld_dsum, ld_dx;
+  void *work;
+  uint64_t work_bytes;
+} sym_layer_norm_grad;
+int moe_layer_norm_bwd(const sym_layer_norm_grad *a, symmoe_stream_t stream);
+
+/* Workspace bytes of moe_layer_norm_bwd.  Host only. */
+int moe_layer_norm_workspace(int64_t rows, int32_t cols, uint64_t *bytes);
+
+/*
+ * moe_orthogonalize: a batch of updates with their singular values brought
+ * towards one by Newton-Schulz products (the experts' weight gradients of
+ * moe_grouped_wgrad, or momentum made of them):
+ *   X = g / (|g| + eps)              |g|: the square root of the sum of squares of a matrix
+ *   `steps` times   X = a X + (b A + c A A) X,  A = X X^T    (rows <= cols;
+ *                   X = a X + X (b A + c A A),  A = X^T X     otherwise: the same X)
+ *   out = scale * X
+ * with (a, b, c) = coeffs.  A matrix of zeros gives zeros; one that holds an
+ * infinity or NaN, and only that one, gives NaN.
+ *   g: device, count matrices of rows x cols, matrix i at element i * g_stride,
+ *   its rows ld_g elements apart, of type g_dtype (SYM_BF16, SYM_FP16, SYM_FP32).
+ *   out: likewise, of type out_dtype (SYM_BF16 or SYM_FP16); may be g where type
+ *   and strides are equal.
+ *   Any strides; rows, cols in [1, 65536], count in [0, 65535], steps in [0, 64].
+ *   work: device, 256-byte aligned.  moe_orthogonalize_workspace gives what lets
+ *   all matrices go side by side where they are small, and enough of them at a
+ *   time to fill the device where they are large (work_bytes), and the least the
+ *   call takes (least_bytes): the matrices go through in as many turns as the
+ *   workspace makes them.  Contents do not matter before or after.
+ * X is held in 22 bits (two fp16 numbers) and enters the products as its first
+ * 11; a Gram matrix is held as its diagonal in fp32 and the rest in fp16;
+ * products accumulate in fp32.  Against exact arithmetic the result is off by a few
+ * times 1e-4 of its norm before its rounding, whatever g's scale.
+ */
+typedef struct sym_orthogonalize {
+  int32_t count, rows, cols, steps;
+  int32_t g_dtype, out_dtype;
+  float coeffs[3];
+  float eps, scale;
+  uint32_t reserved;
+  const void *g;
+  void *out;
+  int64_t g_stride, ld_g, out_stride, ld_out;
+  void *work;
+  uint64_t work_bytes;
+} sym_orthogonalize;
+int moe_orthogonalize(const sym_orthogonalize *a, symmoe_stream_t stream);
+int moe_orthogonalize_workspace(int32_t count, int32_t rows, int32_t cols, uint64_t *work_bytes,
+                                uint64_t *least_bytes);
+
+/*
+ * moe_few_tokens: a whole MoE layer for a few tokens (what a decode step of a
+ * few users asks of it), without a heap, in two launches (three with the router):
+ *   logits[t] = w_router x[t]                     (w_router NULL: logits are given)
+ *   idx[t], w[t]: the top-k of the logits (descending, equal ones to the lower
+ *   expert) and the softmax over them
+ *   out[t] = sum_j w[t][j] * (silu(x Wg^T) * (x Wu^T)) Wd^T   of expert idx[t][j]
+ * A chosen expert whose logit is -infinity has the weight 0 and takes no part; a
+ * token without any other has a row of zeros.  A logit that is NaN ranks below
+ * all numbers; where one is chosen, or +infinity is, the token's weights and row
+ * are NaN.
+ *   dtype: SYM_BF16 or SYM_FP16, of x, the weights and out.
+ *   x [tokens][hidden], 16-byte aligned, ld_x a multiple of 8; may be out.
+ *   logits [tokens][num_experts] fp32 (in, or out with w_router); idx int32, w fp32
+ *   [tokens][topk] (out).
+ *   w_gate, w_up: [num_experts][inter][hidden], w_down: [num_experts][hidden][inter],
+ *   w_router: [num_experts][hidden]: 16-byte aligned, expert e at element
+ *   e * *_group, rows *_ld elements apart (multiples of 8), so that w_gate and w_up
+ *   may be the halves of one tensor.
+ *   work: device, 16-byte aligned, moe_few_tokens_workspace(...) bytes; contents do
+ *   not matter before or after.
+ * tokens in [0, 32], hidden and inter multiples of 8 up to 65536, num_experts <= 1024,
+ * topk <= min(num_experts, 32).  Products accumulate in fp32; h is held in two
+ * numbers of dtype (bf16: 16 bits; fp16: 22, and infinite beyond its range); out is
+ * rounded once.  Only the chosen experts' weights are read, once for every 32 rows
+ * of an expert in the first product and every 16 in the second.
+ */
+typedef struct sym_few_tokens {
+  int32_t tokens, hidden, inter, num_experts, topk, dtype;
+  const void *x, *w_gate, *w_up, *w_down, *w_router;
+  float *logits;
+  int32_t *idx;
+  float *w;
+  void *out;
+  int64_t ld_x, ld_out, gate_group, gate_ld, up_group, up_ld, down_group, down_ld, router_ld;
+  void *work;
+  uint64_t work_bytes;
+} sym_few_tokens;
+int moe_few_tokens(const sym_few_tokens *a, symmoe_stream_t stream);
+
+/* Workspace bytes of moe_few_tokens.  Host only. */
+int moe_few_tokens_workspace(int32_t tokens, int32_t inter, int32_t topk, uint64_t *bytes);
+
 /* Static description of a SYM_* code (never NULL). */
 const char *sym_strerror(int code);
 
