@@ -101,8 +101,8 @@ class SymLayerNormGrad(ctypes.Structure):
 
 class SymOrthogonalize(ctypes.Structure):
     _fields_ = [("count", _i32), ("rows", _i32), ("cols", _i32), ("steps", _i32), ("g_dtype", _i32), ("out_dtype", _i32),
-                ("coeffs", ctypes.c_float * 3), ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("reserved", _u32),
-                ("g", _u64), ("out", _u64), ("g_stride", _i64), ("ld_g", _i64), ("out_stride", _i64), ("ld_out", _i64),
+                ("coeffs", ctypes.c_float * 3), ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("wait_timeout_us", _u32),
+                ("status", _u64), ("g", _u64), ("out", _u64), ("g_stride", _i64), ("ld_g", _i64), ("out_stride", _i64), ("ld_out", _i64),
                 ("work", _u64), ("work_bytes", _u64)]
 
 
@@ -667,19 +667,22 @@ def moe_orthogonalize_workspace(count: int, rows: int, cols: int, least: bool = 
 
 
 def moe_orthogonalize(g, out, work, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
-                      scale: float = 1.0, stream=None) -> None:
+                      scale: float = 1.0, status=None, stream=None) -> None:
     """out = scale * X after `steps` Newton-Schulz products, X = a X + (b A + c A A) X
     with A = X X^T, from X = g / (norm of g + eps), for every matrix of g [F, C] or
-    [E, F, C] (bf16, fp16 or float32; out bf16 or fp16).  work: a uint8 tensor."""
+    [E, F, C] (bf16, fp16 or float32; out bf16 or fp16).  work: a uint8 tensor; status: an
+    int32 word that SYM_STATUS_TIMEOUT is set in if an internal wait runs out."""
     where = "moe_orthogonalize"
-    dev = _on_device(where, g, out, work)
+    dev = _on_device(where, g, out, work, status)
+    _need(status is None or (status.dtype == torch.int32 and status.numel() >= 1), where, "status is an int32 word")
     _need(g.shape == out.shape, where, "g and out have one shape")
     _need(len(coeffs) == 3, where, "three coefficients are wanted")
     count, f, c, gs, gl = _batch(g, where)
     os_, ol = _batch(out, where)[3:]
     wp, wn = _work(work, where)
     a = SymOrthogonalize(count, f, c, steps, _DTYPES.get(g.dtype, -1), _DTYPES.get(out.dtype, -1),
-                         (ctypes.c_float * 3)(*coeffs), eps, scale, 0, g.data_ptr(), out.data_ptr(), gs, gl, os_, ol, wp, wn)
+                         (ctypes.c_float * 3)(*coeffs), eps, scale, 0,
+                         0 if status is None else status.data_ptr(), g.data_ptr(), out.data_ptr(), gs, gl, os_, ol, wp, wn)
     _check(lib().moe_orthogonalize(ctypes.byref(a), _stream_of(stream, dev)), where)
 
 

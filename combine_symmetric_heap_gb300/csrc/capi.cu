@@ -641,7 +641,7 @@ int moe_orthogonalize_workspace(int32_t count, int32_t rows, int32_t cols, uint6
 
 int moe_orthogonalize(const sym_orthogonalize *a, symmoe_stream_t stream) {
   if (!a || !orth_shape_ok(a->count, a->rows, a->cols) || a->steps < 0 || a->steps > 64 || !dtype_ok(a->g_dtype) ||
-      (a->out_dtype != SYM_BF16 && a->out_dtype != SYM_FP16) || !(a->eps >= 0.f) || (reinterpret_cast<uintptr_t>(a->work) & 255u))
+      (a->out_dtype != SYM_BF16 && a->out_dtype != SYM_FP16) || !(a->eps >= 0.f) || (reinterpret_cast<uintptr_t>(a->work) & 255u) || !opt4(a->status))
     return SYM_EINVAL;
   if (a->count == 0) return SYM_OK;
   if (!matrices_ok(a->g, a->count, a->rows, a->cols, a->g_stride, a->ld_g, a->g_dtype) ||

@@ -39,12 +39,12 @@
 // back to back (1.67 PFLOP/s at the 1.54 GHz that the power cap leaves).
 #include <algorithm>
 
-#include "gemm2sm.cuh"
+#include "pair_ops.cuh"
 
 namespace symmoe {
 namespace grouped {
 
-using namespace gemm2;
+using namespace pair;
 
 constexpr int PRODUCT_THREADS = 192;  // producer, MMA issuer, 4 epilogue warps
 constexpr int WG_EPI_WARPS = 8;       // two per TMEM lane quarter, each with half of a tile's columns
@@ -54,7 +54,6 @@ constexpr int CTRL_BYTES = 512;
 // number: one shared-memory size for the kernel, so that calls from several host
 // threads set the same limit and the resident pairs are looked up once.
 constexpr int MAX_GROUPS = 1024;
-constexpr int CHUNK_BYTES = BK * 64 * 2;  // 64 contraction rows x 64 features (MN-major tiles)
 constexpr int WG_STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int WG_STAGES = 6;
 constexpr int WG_OUT_BYTES = 32 * 64;  // staged output of a warp: 32 rows of 64 bytes
@@ -72,98 +71,6 @@ struct Out {
   void *ptr;
   int64_t ld, stride;  // elements between rows, and between slots (product) or groups (wgrad)
 };
-
-// Role-local view of the CTA's give-up flag and the wait limit
-struct Ctl {
-  volatile int *abort;
-  int32_t *status;
-  uint32_t tmo;
-};
-
-__device__ __forceinline__ void raise(int32_t *status, int bits) {
-  if (status) atomicOr(status, bits);
-}
-
-// Bounded wait (cluster-scope acquire: some arrivals come from the pair's
-// other CTA after generic stores); a timeout sets the CTA's abort flag.  A wait
-// that may outlast several of the pair's tiles has the limit for each of them.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, const Ctl &c, uint32_t tiles = 1) {
-  const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait_cluster(a, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  const uint64_t limit = (uint64_t)c.tmo * tiles * 1000ull;
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait_cluster(a, parity)) return true;
-    if (*c.abort) return false;
-    if ((it & 15u) == 15u && globaltimer_ns() - t0 > limit) {
-      *c.abort = 1;
-      raise(c.status, SYM_STATUS_TIMEOUT);
-      return false;
-    }
-  }
-}
-
-// A wait of this CTA has run out and all its threads have stopped: before its
-// shared memory and TMEM are given up, wait (10 ms at most) for the MMAs in
-// flight, and 10 ms for the copies.  No barrier this CTA may wait on counts all of
-// those (the peer's are counted by the leader, a stage that one CTA did not load
-// never completes); a copy takes some microseconds.
-__device__ __forceinline__ void settle(uint64_t *drained, bool issuer) {
-  constexpr uint32_t LIMIT_US = 10000;
-  const uint64_t t0 = globaltimer_ns();
-  if (issuer) {
-    commit2_both(drained);
-    mbar_wait(drained, 0, LIMIT_US, nullptr);
-  }
-  while (globaltimer_ns() - t0 < LIMIT_US * 1000ull) __nanosleep(1000);
-}
-
-// Matrix descriptor of an MN-major tile with the 128-byte swizzle: chunks of
-// 64 features, each [64 contraction rows][128 bytes]; the leading offset steps
-// over chunks, the stride offset over groups of 8 contraction rows.
-__device__ __forceinline__ uint64_t smem_desc_mn(const void *tile, int chunk = CHUNK_BYTES) {
-  uint64_t d = 0;
-  d |= (smem_u32(tile) >> 4) & 0x3FFFull;
-  d |= (uint64_t)(chunk >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= 1ull << 46;
-  d |= 2ull << 61;
-  return d;
-}
-constexpr uint64_t MN_STEP = UK * 128 / 16;  // 16 contraction rows, in 16-byte units
-constexpr uint64_t K_STEP = UK * 2 / 16;     // 16 contraction columns of a K-major row
-
-// kind::f16 instruction descriptor (idesc_bf16_f32 with the operand type and
-// majors as arguments): bits 7-9 / 10-12 operand formats (0 fp16, 1 bf16),
-// bits 15 / 16 A / B major (1 = MN).
-__device__ __forceinline__ uint32_t idesc(bool fp16, bool a_mn, bool b_mn, int n) {
-  const uint32_t fmt = fp16 ? 0u : (1u << 7) | (1u << 10);
-  return (1u << 4) | fmt | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
-         ((256u >> 4) << 24);
-}
-
-__device__ __forceinline__ uint16_t to_half(float v) {
-  uint16_t r;
-  asm("cvt.rn.f16.f32 %0, %1;" : "=h"(r) : "f"(v));
-  return r;
-}
-template <bool FP16>
-__device__ __forceinline__ uint16_t narrow(float v) {
-  return FP16 ? to_half(v) : to_bf16(v);
-}
-template <bool FP16>
-__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
-  if (!FP16) return pack_bf16x2(lo, hi);
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float widen(bool fp16, uint16_t v) {
-  if (!fp16) return __uint_as_float((uint32_t)v << 16);
-  float r;
-  asm("cvt.f32.f16 %0, %1;" : "=f"(r) : "h"(v));
-  return r;
-}
 
 __device__ __forceinline__ void tma_load_3d_pair_hint(void *dst, const CUtensorMap *m, uint32_t bar_cluster, int x,
                                                       int y, int z, uint64_t policy) {
@@ -246,19 +153,6 @@ __device__ inline Tile decode_product(const Groups &g, const TokTables &tb, int 
 // ---------------------------------------------------------------------------
 // product kernel
 // ---------------------------------------------------------------------------
-template <int N>
-struct RingOf {
-  uint8_t *base;
-  uint64_t *full, *empty;
-  int stage = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++stage == N) {
-      stage = 0;
-      phase ^= 1u;
-    }
-  }
-};
 using Ring = RingOf<STAGES>;
 
 // K loop of the producer for one tile; TWO: with a remainder part
@@ -305,19 +199,6 @@ __device__ __forceinline__ bool product_mma(Ring &rg, const Ctl &ctl, uint32_t d
     rg.next();
   }
   return true;
-}
-
-// Hand an accumulator (or its head) back to the leader's MMA.  What the arrival
-// orders is the warp's finished TMEM reads, nothing in memory, so the peer's
-// remote arrival releases at CTA scope: a release at cluster scope waits for
-// the warp's stores (a third of the weight gradient's epilogue, 1900 cycles a tile).
-__device__ __forceinline__ void give_back(uint64_t *bar, uint32_t rank, int lane) {
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) {
-    if (rank == 0) mbar_arrive(bar);
-    else asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(map_to(bar, 0)) : "memory");
-  }
 }
 
 // Rows [row, row + n) of a tile: this lane's feature of each
@@ -560,33 +441,6 @@ __device__ __forceinline__ void wgrad_store(void *row, const uint32_t (&v)[32], 
     for (int i = 0; i < 32; ++i)
       if (i < n) p[i] = narrow<H>(add ? a[i] + widen(H, p[i]) : a[i]);
   }
-}
-
-// shared -> global tensor copies of the calling thread's bulk group: a box as
-// it is, or added to what is there (fp32); elements past the extents are cut
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, const void *src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-__device__ __forceinline__ void tma_add_3d(const CUtensorMap *m, const void *src, int x, int y, int z) {
-  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-// all but the newest N groups of this thread have read their shared memory
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
-// Order this thread's stores to shared memory before later tensor copies out
-// of it.  The unrestricted proxy fence also waits for global accesses: with it
-// the weight gradient of the prefill shape took 3.49 ms, with this one 2.99.
-__device__ __forceinline__ void fence_proxy_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // This lane's row of a staged box (64 bytes: 16 floats or 32 16-bit values), in
@@ -870,26 +724,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WGRAD_THREADS, 1)
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// 16-bit (or fp32) elements [d2][d1][d0], strides in elements, box [1][b1][b0]; elements outside the extents read as zeros
-static bool encode(CUtensorMap *m, uint64_t ptr, uint64_t d0, uint64_t d1, uint64_t d2, int64_t s1, int64_t s2,
-                   uint32_t b0, uint32_t b1, bool fp32 = false,
-                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
-  typedef CUresult (*Fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                         const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                         CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static const Fn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
-    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<Fn>(p) : nullptr;
-  }();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {(cuuint64_t)s1 * (fp32 ? 4 : 2), (cuuint64_t)s2 * (fp32 ? 4 : 2)};
-  const cuuint32_t box[3] = {b0, b1, 1}, step[3] = {1, 1, 1};
-  return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, reinterpret_cast<void *>(ptr), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 // rows of a sym_rows, boxes of [box_rows][64]
 static bool encode_rows(CUtensorMap *m, const sym_rows &r, uint32_t box_rows) {
   const int64_t slot = r.slots > 1 ? r.slot_stride : r.ld * r.rows;
@@ -899,16 +733,6 @@ static bool encode_rows(CUtensorMap *m, const sym_rows &r, uint32_t box_rows) {
 static Groups groups_of(const sym_groups &g, const sym_rows &rows) {
   return Groups{g.cnt, g.off, g.cnt_slot_stride, g.off_slot_stride, g.groups, g.groups / g.slots, rows.rows,
                 g.status, g.wait_timeout_us};
-}
-
-template <typename Kern, typename... Args>
-static cudaError_t launch(Kern kern, int threads, size_t smem, int num_sms, cudaStream_t st, Args... args) {
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (err != cudaSuccess) return err;
-  const int grid = 2 * max_resident_pairs((const void *)kern, threads, smem, num_sms);
-  if (grid <= 0) return cudaErrorInvalidConfiguration;
-  kern<<<grid, threads, smem, st>>>(args...);
-  return cudaGetLastError();
 }
 
 }  // namespace grouped
@@ -931,8 +755,8 @@ cudaError_t launch_grouped_matmul(const sym_groups &sg, int fp16, const sym_rows
   const int run = (int)std::max<int64_t>(1, GROUP_H_BYTES / ((int64_t)BN * C * 2));
   const Groups g = groups_of(sg, x);
   const Out o{reinterpret_cast<void *>(out.ptr), out.ld, out.slots > 1 ? out.slot_stride : 0};
-  return trans ? launch(grouped_product_kernel<true>, PRODUCT_THREADS, smem, num_sms, st, g, o, F, C, fp16, run, mw, mx)
-               : launch(grouped_product_kernel<false>, PRODUCT_THREADS, smem, num_sms, st, g, o, F, C, fp16, run, mw, mx);
+  return trans ? launch_pairs(grouped_product_kernel<true>, PRODUCT_THREADS, smem, num_sms, st, g, o, F, C, fp16, run, mw, mx)
+               : launch_pairs(grouped_product_kernel<false>, PRODUCT_THREADS, smem, num_sms, st, g, o, F, C, fp16, run, mw, mx);
 }
 
 cudaError_t launch_grouped_wgrad(const sym_groups &sg, int fp16, const sym_rows &dy, const sym_rows &x, void *dw,
@@ -962,7 +786,7 @@ cudaError_t launch_grouped_wgrad(const sym_groups &sg, int fp16, const sym_rows 
   const int64_t narrow = (int64_t)sg.groups * ((dy.cols + 255) / 256) * ((x.cols + 127) / 128);
   const int tile_c = narrow <= num_sms / 2 ? 128 : 256;
   auto go = [&](auto kern) {
-    return launch(kern, WGRAD_THREADS, smem, num_sms, st, g, o, dy.cols, x.cols, fp16, add, by_tma, tile_c, md, mx, mo);
+    return launch_pairs(kern, WGRAD_THREADS, smem, num_sms, st, g, o, dy.cols, x.cols, fp16, add, by_tma, tile_c, md, mx, mo);
   };
   return fp32 ? go(grouped_wgrad_kernel<OUT_FP32>)
               : fp16 ? go(grouped_wgrad_kernel<OUT_FP16>) : go(grouped_wgrad_kernel<OUT_BF16>);

@@ -21,20 +21,27 @@
 // times 2^8.
 #include <algorithm>
 
+#include "pair_ops.cuh"
 #include "rows_dev.cuh"
 
 namespace symmoe {
 namespace orth {
 
 using namespace rows;
+using namespace pair;
 
+// A bf16 result rounds by 1.7e-3 of its norm; products of 11-bit operands add 4e-4 to
+// 5e-4.  An fp16 result rounds by 2.1e-4: there the last steps' products are taken of
+// both parts (hi hi + hi lo + lo hi), which leaves the first steps' 1e-4 or less.
+constexpr int PRECISE_STEPS = 3;
 constexpr float X_SCALE = 8192.f, A_SCALE = 1024.f, B_SCALE = 256.f;
 
 // A matrix' part of the workspace
 struct Layout {
   int64_t ld_x, ld_a;                      // rows of X, of A and B: multiples of 64 elements
   size_t x_bytes, a_bytes;                 // one copy of X's hi or lo, of A or B
-  size_t hi, lo, a, b, diag_a, diag_b, sums, total;  // offsets; hi, lo: two copies each
+  // offsets: two copies of X's hi and lo; A's and B's (b: B's, a: A's, each hi, lo)
+  size_t hi, lo, a, b, diag_a, diag_b, sums, total;
 };
 constexpr int SUMS = 64;  // partial sums of squares
 static Layout layout_of(int rows, int cols) {
@@ -43,8 +50,8 @@ static Layout layout_of(int rows, int cols) {
   auto up = [](size_t v, size_t to) { return (v + to - 1) / to * to; };
   l.ld_x = up(cols, 64), l.ld_a = up(m, 64);
   l.x_bytes = up((size_t)rows * l.ld_x * 2, 256), l.a_bytes = up((size_t)m * l.ld_a * 2, 256);
-  l.hi = 0, l.lo = 2 * l.x_bytes, l.a = 4 * l.x_bytes, l.b = l.a + l.a_bytes;
-  l.diag_a = l.b + l.a_bytes, l.diag_b = l.diag_a + up((size_t)m * 4, 256);
+  l.hi = 0, l.lo = 2 * l.x_bytes, l.a = 4 * l.x_bytes, l.b = l.a + 2 * l.a_bytes;
+  l.diag_a = l.b + 2 * l.a_bytes, l.diag_b = l.diag_a + up((size_t)m * 4, 256);
   l.sums = l.diag_b + up((size_t)m * 4, 256), l.total = l.sums + SUMS * 8;
   return l;
 }
@@ -58,16 +65,12 @@ struct Call {
   int rows, cols, m, tall;
   float a, b, c, eps, scale;
 };
-// what a step reads and writes: copy `turn` of X to the other
 struct State {
-  __half *hi, *lo, *A, *B;
-  float *da, *db;
+  __half *hi, *lo;
 };
 __device__ __forceinline__ State state_of(const Call &p, int matrix, int copy) {
   char *w = p.work + matrix * p.l.total;
-  return State{reinterpret_cast<__half *>(w + p.l.hi + copy * p.l.x_bytes), reinterpret_cast<__half *>(w + p.l.lo + copy * p.l.x_bytes),
-               reinterpret_cast<__half *>(w + p.l.a), reinterpret_cast<__half *>(w + p.l.b),
-               reinterpret_cast<float *>(w + p.l.diag_a), reinterpret_cast<float *>(w + p.l.diag_b)};
+  return State{reinterpret_cast<__half *>(w + p.l.hi + copy * p.l.x_bytes), reinterpret_cast<__half *>(w + p.l.lo + copy * p.l.x_bytes)};
 }
 
 // Partial sums of squares, grid (SUMS, matrices), in 64 bits: any fp32 values
@@ -129,60 +132,337 @@ __global__ void __launch_bounds__(256) finish_kernel(const Call p, int copy) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// The three products on CTA pairs (tcgen05 cta_group::2, tiles of 256 x 256; the
+// pair protocol of gemm2sm.cuh), for all matrices of a turn at once:
+//   GRAM    A = X X^T (X^T X)          X from both sides
+//   POLY    B = b A + c A A
+//   UPDATE  X = a X + B X (X B)
+// A and B are symmetric: only tiles on and below the diagonal are made, each
+// written twice, as it is and turned over.
+//
+// What a product adds to (A for POLY, X for UPDATE) comes into an epilogue
+// warp's own boxes of 32 x 32 by tensor copies, one box ahead, and the result leaves from
+// there.  X X^T of wide matrices and products with A or B read K-major
+// tiles; X^T X and the X of B X lie the other way and are read as they lie.
+// ---------------------------------------------------------------------------
 enum Kind { GRAM, POLY, UPDATE };
-// One 64 x 64 tile of a product, 16 x 16 threads of 4 x 4
+constexpr int EPI_WARPS = 8;  // two per TMEM lane quarter, each with half of a tile's columns
+constexpr int THREADS = 32 * (2 + EPI_WARPS);
+constexpr int RING = 5;
+constexpr int OPERANDS = A_BYTES + B_BYTES;  // of a stage
+constexpr int BOX = 32 * 64;                 // 32 rows of 32 fp16
+constexpr int CTRL = 512;
+constexpr int SMEM = 1024 + RING * OPERANDS + EPI_WARPS * 4 * BOX + CTRL;
+
+struct Maps {
+  CUtensorMap a[2], b[2];     // operands: hi, lo
+  CUtensorMap in[2], out[2];  // what is added to, the result: hi, lo (out[0] of the last step: the user's)
+};
+struct Prod {
+  char *work;  // of the turn's first matrix
+  size_t stride, diag, mirror[2];  // between matrices; where the diagonal and the turned tiles go (GRAM, POLY) or come from
+  size_t diag_in;
+  int64_t ld_mirror;
+  int M, N, K, tiles_m, tiles, count, tall;
+  int passes;  // 1: hi hi;  3: and hi lo, lo hi
+  int last;    // the result is the user's: 1 bf16, 2 fp16
+  int by_tma;  // ... by tensor copies
+  char *user;
+  int64_t user_stride, user_ld;
+  float a, b, c, scale;
+  int32_t *status;
+  uint32_t tmo;
+};
+
+struct Tile {
+  int z, i, j;
+};
 template <int KIND>
-__global__ void __launch_bounds__(256) product_kernel(const Call p, int copy) {
-  __shared__ float as[16][65], bs[16][65];
-  const State s = state_of(p, blockIdx.z, copy), to = state_of(p, blockIdx.z, copy ^ 1);
-  const int64_t lx = p.l.ld_x, la = p.l.ld_a;
-  const int M = KIND == UPDATE ? p.rows : p.m, N = KIND == UPDATE ? p.cols : p.m;
-  const int K = KIND == GRAM ? (p.tall ? p.rows : p.cols) : p.m;
-  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-  auto left = [&](int i, int k) {
-    if (KIND == GRAM) return p.tall ? s.hi[k * lx + i] : s.hi[i * lx + k];
-    if (KIND == POLY) return s.A[i * la + k];
-    return p.tall ? s.hi[i * lx + k] : s.B[i * la + k];
-  };
-  auto right = [&](int k, int j) {
-    if (KIND == GRAM) return p.tall ? s.hi[k * lx + j] : s.hi[j * lx + k];
-    if (KIND == POLY) return s.A[k * la + j];
-    return p.tall ? s.B[k * la + j] : s.hi[k * lx + j];
-  };
-  float acc[4][4] = {};
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    for (int e = threadIdx.x; e < 1024; e += 256) {
-      const int k = e % 16, i = e / 16;
-      as[k][i] = i0 + i < M && k0 + k < K ? __half2float(left(i0 + i, k0 + k)) : 0.f;
-      bs[e / 64][e % 64] = j0 + e % 64 < N && k0 + e / 64 < K ? __half2float(right(k0 + e / 64, j0 + e % 64)) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += as[k][ty * 4 + i] * bs[k][tx * 4 + j];
-    __syncthreads();
+__device__ __forceinline__ Tile tile_of(const Prod &p, int t) {
+  Tile ti;
+  ti.z = t / p.tiles;
+  const int k = t - ti.z * p.tiles;
+  if (KIND == UPDATE) {  // consecutive tiles share columns
+    ti.j = k / p.tiles_m;
+    ti.i = k - ti.j * p.tiles_m;
+  } else {  // row i of the lower triangle holds tiles [i (i + 1) / 2, ...)
+    int i = (int)((sqrtf(8.f * k + 1.f) - 1.f) * 0.5f);
+    while (i * (i + 1) / 2 > k) --i;
+    while ((i + 1) * (i + 2) / 2 <= k) ++i;
+    ti.i = i;
+    ti.j = k - i * (i + 1) / 2;
   }
-  for (int u = 0; u < 4; ++u)
-    for (int v = 0; v < 4; ++v) {
-      const int i = i0 + ty * 4 + u, j = j0 + tx * 4 + v;
-      if (i >= M || j >= N) continue;
-      if (KIND == GRAM) {
-        const float r = acc[u][v] / (X_SCALE * X_SCALE);
-        if (i == j) s.da[i] = r;
-        s.A[i * la + j] = __float2half_rn(i == j ? 0.f : r * A_SCALE);
-      } else if (KIND == POLY) {
-        const float oo = acc[u][v] / (A_SCALE * A_SCALE), o = __half2float(s.A[i * la + j]) / A_SCALE, di = s.da[i], dj = s.da[j];
-        if (i == j) s.db[i] = p.b * di + p.c * (di * di + oo);
-        s.B[i * la + j] = __float2half_rn(i == j ? 0.f : B_SCALE * ((p.b + p.c * (di + dj)) * o + p.c * oo));
-      } else {
-        const float x = __half2float(s.hi[i * lx + j]) + __half2float(s.lo[i * lx + j]);
-        split((p.a + s.db[p.tall ? j : i]) * x + acc[u][v] / B_SCALE, to.hi + i * lx + j, to.lo + i * lx + j);
+  return ti;
+}
+
+// This lane's row of a box (64-byte swizzle: 16-byte word w of row r at w ^ (r / 2 mod 4))
+__device__ __forceinline__ uint4 *box_word(uint8_t *box, int lane, int w) {
+  return reinterpret_cast<uint4 *>(box + lane * 64 + ((w ^ ((lane >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ void add_box(uint8_t *box, int lane, float (&x)[32]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    float f[8];
+    unpack<__half, 8>(*box_word(box, lane, w), f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[8 * w + k] += f[k];
+  }
+}
+// v rounded to T; with TWO what is left of it into the second box
+template <typename T, bool TWO>
+__device__ __forceinline__ void put_boxes(uint8_t *box, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = v[8 * w + k];
+    const uint4 hi = pack<T, 8>(f);
+    *box_word(box, lane, w) = hi;
+    if (TWO) {
+      float g[8];
+      unpack<T, 8>(hi, g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] -= g[k];
+      *box_word(box + BOX, lane, w) = pack<T, 8>(f);
+    }
+  }
+}
+
+template <int KIND, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    product_kernel(const Prod p, const __grid_constant__ Maps maps) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *boxes = smem + (size_t)RING * OPERANDS;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(boxes + EPI_WARPS * 4 * BOX);
+  uint64_t *acc_full = bars + 2 * RING, *acc_empty = acc_full + 2, *box_in = acc_full + 4;  // [EPI_WARPS][2]
+  uint64_t *drained = box_in + 2 * EPI_WARPS;
+  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(drained + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base_s + 1);
+  const int wid = warp_id(), lane = lane_id();
+  const uint32_t rank = cta_rank();
+  const int pair_id = (int)cluster_id_x(), npairs = (int)num_clusters_x();
+  const Ctl ctl{abort_flag, p.status, p.tmo};
+  RingOf<RING> rg{smem, bars, bars + RING};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < RING; ++s) {
+      mbar_init(&rg.full[s], 1);
+      mbar_init(&rg.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * EPI_WARPS);
+    }
+    for (int b = 0; b < 2 * EPI_WARPS; ++b) mbar_init(&box_in[b], 1);
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.a[0]);
+    tma_prefetch_desc(&maps.b[0]);
+  }
+  if (wid == 1) {
+    tmem_alloc2(tmem_base_s, TMEM_COLS);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_s;
+  const int nk = (p.K + BK - 1) / BK, total = p.tiles * p.count;
+
+  if (wid == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      const uint32_t full_leader = map_to(rg.full, 0);
+      bool ok = true;
+      for (int n = 0, t; ok && (t = pair_tile(n, pair_id, npairs)) < total; ++n) {
+        const Tile ti = tile_of<KIND>(p, t);
+        const int m0 = ti.i * 256 + (int)rank * 128, n0 = ti.j * 256 + (int)rank * 128;
+        for (int pass = 0; ok && pass < p.passes; ++pass) {
+          const CUtensorMap *ma = &maps.a[pass == 2], *mb = &maps.b[pass == 1];
+          for (int kb = 0; kb < nk; ++kb) {
+            if (!(ok = bar_wait(&rg.empty[rg.stage], rg.phase ^ 1u, ctl))) break;
+            uint8_t *sb = rg.base + (size_t)rg.stage * OPERANDS;
+            const uint32_t bar = full_leader + (uint32_t)(rg.stage * sizeof(uint64_t));
+            if (rank == 0) mbar_arrive_expect_tx(&rg.full[rg.stage], 2u * OPERANDS);  // both CTAs'
+            if (A_MN) {
+              tma_load_3d_pair(sb, ma, bar, m0, kb * BK, ti.z);
+              tma_load_3d_pair(sb + CHUNK_BYTES, ma, bar, m0 + 64, kb * BK, ti.z);
+            } else {
+              tma_load_3d_pair(sb, ma, bar, kb * BK, m0, ti.z);
+            }
+            if (B_MN) {
+              tma_load_3d_pair(sb + A_BYTES, mb, bar, n0, kb * BK, ti.z);
+              tma_load_3d_pair(sb + A_BYTES + CHUNK_BYTES, mb, bar, n0 + 64, kb * BK, ti.z);
+            } else {
+              tma_load_3d_pair(sb + A_BYTES, mb, bar, kb * BK, n0, ti.z);
+            }
+            rg.next();
+          }
+        }
       }
     }
+  } else if (wid == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---------------------------------------------------- MMA issuer (leader)
+      constexpr uint64_t astep = A_MN ? MN_STEP : K_STEP, bstep = B_MN ? MN_STEP : K_STEP;
+      const uint32_t id = idesc(true, A_MN, B_MN, 256);
+      uint32_t ne[2] = {0, 0};
+      int b = 0;
+      bool ok = true;
+      for (int n = 0, t; ok && (t = pair_tile(n, pair_id, npairs)) < total; ++n, b ^= 1) {
+        if (!(ok = bar_wait(&acc_empty[b], (ne[b]++ & 1u) ^ 1u, ctl))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(b * ACC_COLS);
+        for (int kb = 0; kb < nk * p.passes; ++kb) {
+          if (!(ok = bar_wait(&rg.full[rg.stage], rg.phase, ctl))) break;
+          tc_fence_after();
+          uint8_t *sb = rg.base + (size_t)rg.stage * OPERANDS;
+          const uint64_t da = A_MN ? smem_desc_mn(sb) : smem_desc_sw128(sb);
+          const uint64_t db = B_MN ? smem_desc_mn(sb + A_BYTES) : smem_desc_sw128(sb + A_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < BK / UK; ++kk) mma2(d, da + kk * astep, db + kk * bstep, id, (kb > 0 || kk > 0) ? 1u : 0u);
+          commit2_both(&rg.empty[rg.stage]);
+          rg.next();
+        }
+        if (ok) commit2_both(&acc_full[b]);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int q = wid & 3, half = (wid - 2) / 4;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    uint8_t *my_boxes = boxes + (size_t)(wid - 2) * 4 * BOX;  // [2][hi, lo]
+    uint64_t *in = box_in + 2 * (wid - 2);
+    const int two_in = KIND == UPDATE || p.passes > 1, two_out = KIND == UPDATE ? !p.last : p.passes > 1;
+    uint32_t used[2] = {0, 0}, boxno = 0;
+    int b = 0;
+    bool ok = true;
+    for (int n = 0, t; ok && (t = pair_tile(n, pair_id, npairs)) < total; ++n, b ^= 1) {
+      const Tile ti = tile_of<KIND>(p, t);
+      const int row0 = ti.i * 256 + (int)rank * 128 + q * 32, row = row0 + lane, col0 = ti.j * 256 + half * 128;
+      const int chunks = row0 < p.M ? min(4, (p.N - col0 + 31) / 32) : 0;  // (negative: none)
+      char *w = p.work + ti.z * p.stride;
+      float *diag = reinterpret_cast<float *>(w + p.diag);
+      const float *diag_in = reinterpret_cast<const float *>(w + p.diag_in);
+      auto fetch = [&](int c) {  // box c of the tile's chunks as box number boxno + c
+        if (KIND == GRAM || lane != 0) return;
+        const uint32_t k = (boxno + c) & 1u;
+        bulk_wait_read<0>();  // the last result has left it
+        mbar_arrive_expect_tx(&in[k], two_in ? 2 * BOX : BOX);
+        tma_load_3d(my_boxes + k * 2 * BOX, &maps.in[0], &in[k], col0 + 32 * c, row0, ti.z);
+        if (two_in) tma_load_3d(my_boxes + k * 2 * BOX + BOX, &maps.in[1], &in[k], col0 + 32 * c, row0, ti.z);
+      };
+      if (chunks > 0) fetch(0);
+      const float d_row = KIND != GRAM && row < p.M && !(KIND == UPDATE && p.tall) ? diag_in[row] : 0.f;
+      if (!(ok = __all_sync(0xffffffffu, bar_wait(&acc_full[b], used[b]++ & 1u, ctl)))) break;
+      tc_fence_after();
+      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS + half * 128);
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        const int col = col0 + 32 * c;
+        uint8_t *box = my_boxes + ((boxno + c) & 1u) * 2 * BOX;
+        if (c + 1 < chunks) fetch(c + 1);
+        uint32_t v[32];
+        float x[32];
+        tmem_ld32(acc + 32 * c, v);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = 0.f;
+        if (KIND != GRAM) {
+          if (!(ok = __all_sync(0xffffffffu, bar_wait(&in[(boxno + c) & 1u], ((boxno + c) >> 1) & 1u, ctl)))) break;
+          add_box(box, lane, x);
+          if (two_in) add_box(box + BOX, lane, x);
+        } else {
+          if (lane == 0) bulk_wait_read<0>();
+        }
+        tmem_ld_wait();
+        __syncwarp();  // the boxes have been read (GRAM: have left) before they are written
+        if (KIND == GRAM) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]) * (A_SCALE / (X_SCALE * X_SCALE));
+        } else if (KIND == POLY) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 dj = *reinterpret_cast<const float4 *>(diag_in + col + k);
+            const float d4[4] = {dj.x, dj.y, dj.z, dj.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              x[k + u] = (p.b + p.c * (d_row + d4[u])) * (x[k + u] * (B_SCALE / A_SCALE)) +
+                         p.c * (__uint_as_float(v[k + u]) * (B_SCALE / (A_SCALE * A_SCALE)));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float e = p.tall ? __ldg(diag_in + col + k) : d_row;
+            x[k] = (p.a + e) * x[k] + __uint_as_float(v[k]) * (1.f / B_SCALE);
+          }
+        }
+        if (KIND != UPDATE && row0 == col) {  // 32 elements of the diagonal, one for each lane
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (k == lane) {
+              // (POLY: A's own part of x is zero here)
+              if (row < p.M)
+                diag[row] = KIND == GRAM ? x[k] * (1.f / A_SCALE)
+                                         : d_row * (p.b + p.c * d_row) + x[k] * (1.f / B_SCALE);
+              x[k] = 0.f;
+            }
+        }
+        if (KIND == UPDATE && p.last) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] *= p.scale / X_SCALE;
+          if (p.by_tma) {
+            if (p.last == 1) put_boxes<__nv_bfloat16, false>(box, lane, x);
+            else put_boxes<__half, false>(box, lane, x);
+          } else if (row < p.M) {
+            uint16_t *to = reinterpret_cast<uint16_t *>(p.user) + ti.z * p.user_stride + row * p.user_ld + col;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (col + k < p.N) to[k] = p.last == 1 ? to_bf16(x[k]) : to_half(x[k]);
+          }
+        } else if (two_out) {
+          put_boxes<__half, true>(box, lane, x);
+        } else {
+          put_boxes<__half, false>(box, lane, x);
+        }
+        if (KIND != UPDATE || !p.last || p.by_tma) {
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&maps.out[0], box, col, row0, ti.z);
+            if (two_out) tma_store_3d(&maps.out[1], box + BOX, col, row0, ti.z);
+            bulk_commit();
+          }
+        }
+        if (KIND != UPDATE && ti.i != ti.j && row < p.M) {  // turned over: a warp's lanes side by side
+          uint16_t *hi = reinterpret_cast<uint16_t *>(w + p.mirror[0]) + col * p.ld_mirror + row;
+          uint16_t *lo = reinterpret_cast<uint16_t *>(w + p.mirror[1]) + col * p.ld_mirror + row;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (col + k < p.N) {
+              const uint16_t h = to_half(x[k]);
+              hi[k * p.ld_mirror] = h;
+              if (two_out) lo[k * p.ld_mirror] = to_half(x[k] - widen(true, h));
+            }
+        }
+      }
+      if (!ok) break;
+      boxno += (uint32_t)max(chunks, 0);
+      give_back(&acc_empty[b], rank, lane);
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) settle(drained, wid == 1 && lane == 0 && rank == 0);
+  __syncwarp();
+  cluster_sync();
+  tc_fence_after();
+  if (wid == 1) tmem_dealloc2(tmem, TMEM_COLS);
 }
 
 }  // namespace orth
@@ -193,16 +473,18 @@ void orthogonalize_workspace(int count, int rows, int cols, int, size_t *least, 
   *best = *least * std::max(count, 1);
 }
 
-cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int, cudaStream_t st) {
+cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaStream_t st) {
   using namespace orth;
   Call p{};
-  p.l = layout_of(o.rows, o.cols);
+  const Layout l = p.l = layout_of(o.rows, o.cols);
   p.g_stride = o.g_stride, p.ldg = o.ld_g, p.out_stride = o.out_stride, p.ld_out = o.ld_out;
   p.work = reinterpret_cast<char *>(o.work);
   p.rows = o.rows, p.cols = o.cols, p.m = std::min(o.rows, o.cols), p.tall = o.rows > o.cols;
   p.a = o.coeffs[0], p.b = o.coeffs[1], p.c = o.coeffs[2], p.eps = o.eps, p.scale = o.scale;
-  const int each = (int)std::min<uint64_t>(o.work_bytes / p.l.total, o.count);
-  const int64_t gs = o.g_dtype == SYM_FP32 ? 4 : 2;
+  const int each = (int)std::min<uint64_t>(o.work_bytes / l.total, o.count), m = p.m;
+  const int64_t gs = o.g_dtype == SYM_FP32 ? 4 : 2, between = l.total / 2;
+  const uint64_t work = reinterpret_cast<uint64_t>(o.work);
+  cudaError_t err = cudaSuccess;
   for (int at = 0; at < o.count; at += each) {
     const unsigned n = std::min(each, o.count - at);
     p.g = reinterpret_cast<const char *>(o.g) + at * o.g_stride * gs;
@@ -216,16 +498,81 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int, cudaStream_t s
     if (o.g_dtype == SYM_BF16) start(__nv_bfloat16());
     else if (o.g_dtype == SYM_FP16) start(__half());
     else start(float());
-    const unsigned tm = (p.m + 63) / 64, tr = (p.rows + 63) / 64, tc = (p.cols + 63) / 64;
-    for (int i = 0; i < o.steps; ++i) {
-      product_kernel<GRAM><<<dim3(tm, tm, n), 256, 0, st>>>(p, i & 1);
-      product_kernel<POLY><<<dim3(tm, tm, n), 256, 0, st>>>(p, i & 1);
-      product_kernel<UPDATE><<<dim3(tc, tr, n), 256, 0, st>>>(p, i & 1);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+
+    // maps of an array's rows: operands, K-major (64 columns of 128 rows) or as they
+    // lie (64 of 64), and the epilogue's boxes
+    bool ok = true;
+    auto map = [&](size_t at_, int rows, int cols, int64_t ld, uint32_t b0, uint32_t b1) {
+      CUtensorMap t;
+      ok = encode(&t, work + at_, cols, rows, n, ld, between, b0, b1, false,
+                  b0 == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) && ok;
+      return t;
+    };
+    auto both = [&](CUtensorMap(&t)[2], size_t hi, size_t lo, int rows, int cols, int64_t ld, uint32_t b0, uint32_t b1) {
+      t[0] = map(hi, rows, cols, ld, b0, b1);
+      t[1] = map(lo, rows, cols, ld, b0, b1);
+    };
+    const size_t a_lo = l.a + l.a_bytes, b_lo = l.b + l.a_bytes;
+    Prod q{};
+    q.work = p.work, q.stride = l.total, q.count = n, q.tall = p.tall, q.ld_mirror = l.ld_a;
+    q.a = p.a, q.b = p.b, q.c = p.c, q.scale = p.scale, q.status = o.status;
+    q.tmo = o.wait_timeout_us ? o.wait_timeout_us : 2000000u;
+    q.user = reinterpret_cast<char *>(p.out), q.user_stride = o.out_stride, q.user_ld = o.ld_out;
+    const int tm = (m + 255) / 256;
+    Maps gram[2], poly, update[2], final_maps;
+    for (int k = 0; k < 2; ++k) {  // from copy k of X
+      const size_t hi = l.hi + k * l.x_bytes, lo = l.lo + k * l.x_bytes, hi2 = l.hi + (k ^ 1) * l.x_bytes, lo2 = l.lo + (k ^ 1) * l.x_bytes;
+      both(gram[k].a, hi, lo, p.rows, p.cols, l.ld_x, 64, p.tall ? 64 : 128);
+      gram[k].b[0] = gram[k].a[0], gram[k].b[1] = gram[k].a[1];
+      both(gram[k].out, l.a, a_lo, m, m, l.ld_a, 32, 32);
+      gram[k].in[0] = gram[k].out[0], gram[k].in[1] = gram[k].out[1];
+      CUtensorMap x[2], sq[2];
+      both(x, hi, lo, p.rows, p.cols, l.ld_x, 64, p.tall ? 128 : 64);
+      both(sq, l.b, b_lo, m, m, l.ld_a, 64, 128);
+      for (int h = 0; h < 2; ++h) {
+        update[k].a[h] = p.tall ? x[h] : sq[h];
+        update[k].b[h] = p.tall ? sq[h] : x[h];
+      }
+      both(update[k].in, hi, lo, p.rows, p.cols, l.ld_x, 32, 32);
+      both(update[k].out, hi2, lo2, p.rows, p.cols, l.ld_x, 32, 32);
     }
-    if (o.out_dtype == SYM_BF16) finish_kernel<__nv_bfloat16><<<lines, 256, 0, st>>>(p, o.steps & 1);
-    else finish_kernel<__half><<<lines, 256, 0, st>>>(p, o.steps & 1);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    both(poly.a, l.a, a_lo, m, m, l.ld_a, 64, 128);
+    poly.b[0] = poly.a[0], poly.b[1] = poly.a[1];
+    both(poly.in, l.a, a_lo, m, m, l.ld_a, 32, 32);
+    both(poly.out, l.b, b_lo, m, m, l.ld_a, 32, 32);
+    const int by_tma = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && o.ld_out % 8 == 0 && (n == 1 || o.out_stride % 8 == 0);
+    final_maps = update[(o.steps + 1) & 1];
+    if (by_tma)
+      ok = encode(&final_maps.out[0], reinterpret_cast<uint64_t>(p.out), p.cols, p.rows, n, std::max<int64_t>(o.ld_out, (p.cols + 7) / 8 * 8),
+                  n > 1 ? o.out_stride : (int64_t)p.rows * std::max<int64_t>(o.ld_out, (p.cols + 7) / 8 * 8), 32, 32, false,
+                  CU_TENSOR_MAP_SWIZZLE_64B) && ok;
+    if (!ok) return cudaErrorInvalidValue;
+    for (int i = 0; i < o.steps; ++i) {
+      const int k = i & 1;
+      q.passes = o.out_dtype == SYM_FP16 && i >= o.steps - PRECISE_STEPS ? 3 : 1;
+      q.M = q.N = m, q.K = std::max(p.rows, p.cols), q.tiles_m = tm, q.tiles = tm * (tm + 1) / 2;
+      q.diag = l.diag_a, q.mirror[0] = l.a, q.mirror[1] = a_lo;
+      err = p.tall ? launch_pairs(product_kernel<GRAM, true, true>, THREADS, SMEM, num_sms, st, q, gram[k])
+                   : launch_pairs(product_kernel<GRAM, false, false>, THREADS, SMEM, num_sms, st, q, gram[k]);
+      if (err != cudaSuccess) return err;
+      q.K = m, q.diag_in = l.diag_a, q.diag = l.diag_b, q.mirror[0] = l.b, q.mirror[1] = b_lo;
+      err = launch_pairs(product_kernel<POLY, false, false>, THREADS, SMEM, num_sms, st, q, poly);
+      if (err != cudaSuccess) return err;
+      q.M = p.rows, q.N = p.cols, q.diag_in = l.diag_b;
+      q.tiles_m = (p.rows + 255) / 256, q.tiles = q.tiles_m * ((p.cols + 255) / 256);
+      q.last = i + 1 < o.steps ? 0 : o.out_dtype == SYM_BF16 ? 1 : 2, q.by_tma = q.last && by_tma;
+      const Maps &mp = q.last ? final_maps : update[k];
+      err = p.tall ? launch_pairs(product_kernel<UPDATE, false, false>, THREADS, SMEM, num_sms, st, q, mp)
+                   : launch_pairs(product_kernel<UPDATE, false, true>, THREADS, SMEM, num_sms, st, q, mp);
+      if (err != cudaSuccess) return err;
+      q.last = q.by_tma = 0;
+    }
+    if (o.steps == 0) {
+      if (o.out_dtype == SYM_BF16) finish_kernel<__nv_bfloat16><<<lines, 256, 0, st>>>(p, 0);
+      else finish_kernel<__half><<<lines, 256, 0, st>>>(p, 0);
+      if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
   }
   return cudaSuccess;
 }

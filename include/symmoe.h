@@ -730,17 +730,23 @@ int moe_layer_norm_workspace(int64_t rows, int32_t cols, uint64_t *bytes);
  *   time to fill the device where they are large (work_bytes), and the least the
  *   call takes (least_bytes): the matrices go through in as many turns as the
  *   workspace makes them.  Contents do not matter before or after.
+ *   status: device word that SYM_STATUS_TIMEOUT is OR-ed into where one of the
+ *   products' internal waits runs out (wait_timeout_us each, 0: 2,000,000), or NULL.
  * X is held in 22 bits (two fp16 numbers) and enters the products as its first
- * 11; a Gram matrix is held as its diagonal in fp32 and the rest in fp16;
- * products accumulate in fp32.  Against exact arithmetic the result is off by a few
- * times 1e-4 of its norm before its rounding, whatever g's scale.
+ * 11 (fp16 results: as both in the last three steps); a Gram matrix is held as its
+ * diagonal in fp32 and the rest in fp16; products accumulate in fp32 on the tensor
+ * cores.  Against exact arithmetic the result is off by a few times 1e-4 of its norm
+ * before its rounding (1e-4 for fp16 results; rows of very few elements by up to 1e-3),
+ * whatever g's scale, as long as |g| is not far below eps and X's elements stay
+ * below 8 in all steps, which they do where the polynomial keeps [0, 1] below it.
  */
 typedef struct sym_orthogonalize {
   int32_t count, rows, cols, steps;
   int32_t g_dtype, out_dtype;
   float coeffs[3];
   float eps, scale;
-  uint32_t reserved;
+  uint32_t wait_timeout_us;
+  int32_t *status;
   const void *g;
   void *out;
   int64_t g_stride, ld_g, out_stride, ld_out;
