@@ -5,10 +5,10 @@
 //   h = silu(x Wg^T) * (x Wu^T);  out[t] = sum_j w[t][j] h[t, j] Wd^T
 //
 // All of it is a read of the chosen experts' weights, so both products are built
-// as a stream of them: one block an SM, whose warps cut the contraction in slices of 64
+// as a stream of them: two blocks an SM, whose warps cut the contraction in slices of 64
 // elements.  A warp's slices of 16 weight rows go from memory to the registers of
 // warp-wide products (mma.sync: a few rows need a hundredth of the tensor cores'
-// rate), four or six of them on their way; the rows that they multiply come along.  The
+// rate), two or three of them on their way; the rows that they multiply come along.  The
 // block's share is a run of features, cut to a feature and not to a tile, so that all
 // SMs end together, and the stream does not stop between tiles or experts.
 //
@@ -18,7 +18,7 @@
 //
 // The logits are read, and the tokens routed, by every block for itself: that takes
 // about a microsecond and saves a launch and its results' way through memory.  The
-// second product's blocks start beside the first's (programmatic launch): their first
+// second product's blocks start as the first's end (programmatic launch): their first
 // slices are there when the last h is written.
 //
 // h goes between the two in two numbers of the weights' type, hi + lo, as two
@@ -38,10 +38,15 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int SLICE = 64;   // contraction elements of a warp's step
 constexpr int W_ROWS = 16;  // weight rows of a tile
 constexpr int MOST_TOKENS = 32, MOST_EXPERTS = 1024, MOST_PAIRS = 32 * MOST_TOKENS;
-// Up to 8 tokens: products of 8 rows of x, and of 4 of h (hi and lo side by side), so
-// that four slices on their way fit 128 registers and two blocks an SM.  More tokens:
-// 16 and 8, six slices, one block.
-constexpr int FEW = 8;
+constexpr int BLOCKS = 2;   // an SM
+// A product's rows of x: 8 NB (and of h 4 NB, hi and lo side by side); an expert's rows
+// beyond those take its weights again, out of L2.  NB = 1 up to a row for each expert on
+// average, else 2, with three and two slices on their way, what 128 registers hold.  NB 1 / 2
+// in us (bytes at the copy rate): eight experts of 4096 x 14336, two a token, 1 token 114 / 124 (105), 4 tokens
+// 324 / 291 (287), 8 tokens 422 / 388 (378), 32 tokens 741 / 541 (420); 256 experts of 7168 x 2048,
+// eight a token, 1 token 124 / 132 (105), 8 tokens 802 / 832 (755), 32 tokens 2243 / 2310 (2143).
+// (Two slices instead of three with NB = 1: 118, 366, 126, 765 and 2173.  One block of twice
+// the slices: 130 and 2373; three blocks of two: 117, 351, 119, 780 and 2357.)
 
 struct Args {
   const uint16_t *x, *wg, *wu, *wd, *wr;
@@ -403,7 +408,7 @@ struct UpTiles {
 };
 
 template <typename T, int NB, int DEPTH>
-__global__ void __launch_bounds__(THREADS, NB == 1 ? 2 : 1) up_kernel(const Args p) {
+__global__ void __launch_bounds__(THREADS, BLOCKS) up_kernel(const Args p) {
   __shared__ Routes r;
   __shared__ float part[2][8 * NB][WARPS][W_ROWS];  // the warps' sums, of two tiles in turn
   pdl_wait();               // the router's logits
@@ -484,7 +489,7 @@ struct DownTiles {
 };
 
 template <typename T, int NB, int DEPTH>
-__global__ void __launch_bounds__(THREADS, NB == 1 ? 2 : 1) down_kernel(const Args p) {
+__global__ void __launch_bounds__(THREADS, BLOCKS) down_kernel(const Args p) {
   __shared__ Routes r;
   extern __shared__ float sums[];  // [WARPS][T][16]
   route(p, r, false);
@@ -532,13 +537,13 @@ template <typename T, int NB, int DEPTH>
 static cudaError_t products(const Args &p, int num_sms, cudaStream_t st) {
   cudaError_t err;
   if (p.wr) {
-    err = launch_pdl(up_kernel<T, NB, DEPTH>, dim3(num_sms), dim3(THREADS), 0, st, p);
+    err = launch_pdl(up_kernel<T, NB, DEPTH>, dim3(BLOCKS * num_sms), dim3(THREADS), 0, st, p);
   } else {
-    up_kernel<T, NB, DEPTH><<<num_sms, THREADS, 0, st>>>(p);
+    up_kernel<T, NB, DEPTH><<<BLOCKS * num_sms, THREADS, 0, st>>>(p);
     err = cudaGetLastError();
   }
   if (err != cudaSuccess) return err;
-  return launch_pdl(down_kernel<T, NB, DEPTH>, dim3(num_sms), dim3(THREADS), WARPS * p.T * DOWN_FEATURES * 4, st, p);
+  return launch_pdl(down_kernel<T, NB, DEPTH>, dim3(BLOCKS * num_sms), dim3(THREADS), WARPS * p.T * DOWN_FEATURES * 4, st, p);
 }
 template <typename T>
 static cudaError_t run(const Args &p, int num_sms, cudaStream_t st) {
@@ -547,7 +552,7 @@ static cudaError_t run(const Args &p, int num_sms, cudaStream_t st) {
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
-  return p.T <= FEW ? products<T, 1, 4>(p, num_sms, st) : products<T, 2, 6>(p, num_sms, st);
+  return p.T * p.k <= p.E ? products<T, 1, 3>(p, num_sms, st) : products<T, 2, 2>(p, num_sms, st);
 }
 
 }  // namespace few_tokens
