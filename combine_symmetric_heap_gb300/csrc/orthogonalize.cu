@@ -41,9 +41,13 @@ struct Layout {
   int64_t ld_x, ld_a;                      // rows of X, of A and B: multiples of 64 elements
   size_t x_bytes, a_bytes;                 // one copy of X's hi or lo, of A or B
   // offsets: two copies of X's hi and lo; A's and B's (b: B's, a: A's, each hi, lo)
-  size_t hi, lo, a, b, diag_a, diag_b, sums, total;
+  size_t hi, lo, a, b, diag_a, diag_b, sums, parts, total;
+  int splits;  // parts that a Gram product's K axis may be cut into
 };
-constexpr int SUMS = 64;  // partial sums of squares
+constexpr int SUMS = 256;  // partial sums of squares
+// A Gram matrix of few tiles with a long K axis is made of parts (joined in their
+// order): of one tile, a pair of SMs takes 0.37 us for each 64 columns of X.
+constexpr int MOST_SPLITS = 16, SPLIT_SIDE = 512, SPLIT_K = 512;
 static Layout layout_of(int rows, int cols) {
   Layout l;
   const int m = std::min(rows, cols);
@@ -52,7 +56,9 @@ static Layout layout_of(int rows, int cols) {
   l.x_bytes = up((size_t)rows * l.ld_x * 2, 256), l.a_bytes = up((size_t)m * l.ld_a * 2, 256);
   l.hi = 0, l.lo = 2 * l.x_bytes, l.a = 4 * l.x_bytes, l.b = l.a + 2 * l.a_bytes;
   l.diag_a = l.b + 2 * l.a_bytes, l.diag_b = l.diag_a + up((size_t)m * 4, 256);
-  l.sums = l.diag_b + up((size_t)m * 4, 256), l.total = l.sums + SUMS * 8;
+  l.sums = l.diag_b + up((size_t)m * 4, 256), l.parts = l.sums + SUMS * 8;
+  l.splits = m > SPLIT_SIDE ? 1 : std::max(1, std::min(MOST_SPLITS, std::max(rows, cols) / SPLIT_K));
+  l.total = up(l.parts + (l.splits > 1 ? (size_t)l.splits * m * l.ld_a * 4 : 0), 256);
   return l;
 }
 
@@ -73,18 +79,53 @@ __device__ __forceinline__ State state_of(const Call &p, int matrix, int copy) {
   return State{reinterpret_cast<__half *>(w + p.l.hi + copy * p.l.x_bytes), reinterpret_cast<__half *>(w + p.l.lo + copy * p.l.x_bytes)};
 }
 
-// Partial sums of squares, grid (SUMS, matrices), in 64 bits: any fp32 values
-// can be squared in them.
-template <typename T>
+// Eight columns of a row, those past the end zeros
+template <typename T, bool VEC>
+__device__ __forceinline__ void eight(const T *row, int c, int cols, float (&f)[8]) {
+  if (VEC && c + 8 <= cols) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = *reinterpret_cast<const float4 *>(row + c), b = *reinterpret_cast<const float4 *>(row + c + 4);
+      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
+      unpack<T, 8>(*reinterpret_cast<const uint4 *>(row + c), f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? Elem<T>::get(row[c + i]) : 0.f;
+  }
+}
+// Partial sums of squares, grid (SUMS, matrices): eight at a time in 32 bits where they
+// stay in range there, in 64 bits where not; added up in 64 bits.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) squares_kernel(const Call p) {
   __shared__ double part[8];
+  pdl_launch_dependents();
   const T *g = reinterpret_cast<const T *>(p.g) + blockIdx.y * p.g_stride;
+  // (a block takes every SUMS-th row, or where there are fewer rows a piece of one)
+  const int pieces = max(1, SUMS / p.rows), piece = blockIdx.x % pieces;
+  const int lines = SUMS / pieces;
   double s = 0;
-  for (int r = blockIdx.x; r < p.rows; r += SUMS)
-    for (int c = threadIdx.x; c < p.cols; c += 256) {
-      const double v = Elem<T>::get(g[r * p.ldg + c]);
-      s += v * v;
+  for (int r = blockIdx.x / pieces; r < p.rows; r += lines) {  // (with pieces lines are at least the rows)
+    float run = 0.f;
+    int held = 0;
+#pragma unroll 4
+    for (int c = (piece * 256 + (int)threadIdx.x) * 8; c < p.cols; c += pieces * 256 * 8) {
+      float f[8], q = 0.f, most = 0.f;
+      eight<T, VEC>(g + r * p.ldg, c, p.cols, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        q += f[i] * f[i];
+        most = fmaxf(most, fabsf(f[i]));
+      }
+      if (most <= 1e15f && (most >= 1e-15f || most == 0.f) && q == q) {
+        run += q;
+        if (++held == 8) s += run, run = 0.f, held = 0;
+      } else {
+        for (int i = 0; i < 8; ++i) s += (double)f[i] * f[i];
+      }
     }
+    s += run;
+  }
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = s;
@@ -94,37 +135,52 @@ __global__ void __launch_bounds__(256) squares_kernel(const Call p) {
     reinterpret_cast<double *>(p.work + blockIdx.y * p.l.total + p.l.sums)[blockIdx.x] = s;
   }
 }
-__device__ __forceinline__ void split(float v, __half *hi, __half *lo) {
-  const __half h = __float2half_rn(v);
-  *hi = h;
-  *lo = __float2half_rn(v - __half2float(h));
-}
 // X_SCALE / (|g| + eps) as two factors, the first a power of two that brings the
-// largest g into range
+// largest g into range; by the whole block of SUMS threads
 __device__ __forceinline__ float2 normaliser(const double *sums, float eps) {
-  double s = 0;
-  for (int i = 0; i < SUMS; ++i) s += sums[i];
+  __shared__ double part[SUMS / 32];
+  double s = sums[threadIdx.x];
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = s;
+  __syncthreads();
+  s = 0;
+  for (int i = 0; i < SUMS / 32; ++i) s += part[i];
   const double norm = sqrt(s) + (double)eps;
   if (norm == 0) return make_float2(1.f, 0.f);
   if (!(norm <= 1.7e308)) return make_float2(1.f, NAN);
   const int e = max(-126, min(126, -ilogb(norm)));
   return make_float2(ldexpf(1.f, e), (float)(X_SCALE / ldexp(norm, e)));
 }
-template <typename T>
-__global__ void __launch_bounds__(256) start_kernel(const Call p) {
-  __shared__ float2 f;
+// The first X, grid (groups of rows, matrices).  (What lies past a row's end, up to
+// its pitch, may be written: nothing reads it.)
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(SUMS) start_kernel(const Call p) {
+  pdl_launch_dependents();
   const T *g = reinterpret_cast<const T *>(p.g) + blockIdx.y * p.g_stride;
-  if (threadIdx.x == 0) f = normaliser(reinterpret_cast<const double *>(p.work + blockIdx.y * p.l.total + p.l.sums), p.eps);
-  __syncthreads();
   const State s = state_of(p, blockIdx.y, 0);
-  for (int r = blockIdx.x; r < p.rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < p.cols; c += 256)
-      split(Elem<T>::get(g[r * p.ldg + c]) * f.x * f.y, s.hi + r * p.l.ld_x + c, s.lo + r * p.l.ld_x + c);
+  pdl_wait();
+  const float2 f = normaliser(reinterpret_cast<const double *>(p.work + blockIdx.y * p.l.total + p.l.sums), p.eps);
+  const int each = (p.cols + 7) / 8;  // eights of a row
+  for (int64_t i = (int64_t)blockIdx.x * SUMS + threadIdx.x; i < (int64_t)p.rows * each; i += (int64_t)gridDim.x * SUMS) {
+    const int r = (int)(i / each), c = (int)(i - (int64_t)r * each) * 8;
+    float v[8], h[8];
+    eight<T, VEC>(g + r * p.ldg, c, p.cols, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = v[k] * f.x * f.y;
+    const uint4 hi = pack<__half, 8>(v);
+    unpack<__half, 8>(hi, h);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] -= h[k];
+    *reinterpret_cast<uint4 *>(s.hi + r * p.l.ld_x + c) = hi;
+    *reinterpret_cast<uint4 *>(s.lo + r * p.l.ld_x + c) = pack<__half, 8>(v);
+  }
 }
 template <typename T>
 __global__ void __launch_bounds__(256) finish_kernel(const Call p, int copy) {
   T *out = reinterpret_cast<T *>(p.out) + blockIdx.y * p.out_stride;
   const State s = state_of(p, blockIdx.y, copy);
+  pdl_wait();
   for (int r = blockIdx.x; r < p.rows; r += gridDim.x)
     for (int c = threadIdx.x; c < p.cols; c += 256) {
       const int64_t i = r * p.l.ld_x + c;
@@ -142,18 +198,20 @@ __global__ void __launch_bounds__(256) finish_kernel(const Call p, int copy) {
 // written twice, as it is and turned over.
 //
 // What a product adds to (A for POLY, X for UPDATE) comes into an epilogue
-// warp's own boxes of 32 x 32 by tensor copies, one box ahead, and the result leaves from
-// there.  X X^T of wide matrices and products with A or B read K-major
+// warp's own boxes of 32 x 32 by tensor copies, two boxes ahead, and the result leaves
+// from there (four boxes for each of four warps; two for each of eight, one ahead, left
+// a box waiting for the copy out before it: 8 x 2048 x 7168 UPDATE 335 us instead of NEW).  X X^T of wide matrices and products with A or B read K-major
 // tiles; X^T X and the X of B X lie the other way and are read as they lie.
 // ---------------------------------------------------------------------------
 enum Kind { GRAM, POLY, UPDATE };
-constexpr int EPI_WARPS = 8;  // two per TMEM lane quarter, each with half of a tile's columns
+constexpr int EPI_WARPS = 4;  // one per TMEM lane quarter
+constexpr int BUFS = 4;       // boxes (hi and lo) of an epilogue warp
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
 constexpr int RING = 5;
 constexpr int OPERANDS = A_BYTES + B_BYTES;  // of a stage
 constexpr int BOX = 32 * 64;                 // 32 rows of 32 fp16
 constexpr int CTRL = 512;
-constexpr int SMEM = 1024 + RING * OPERANDS + EPI_WARPS * 4 * BOX + CTRL;
+constexpr int SMEM = 1024 + RING * OPERANDS + EPI_WARPS * BUFS * 2 * BOX + CTRL;
 
 struct Maps {
   CUtensorMap a[2], b[2];     // operands: hi, lo
@@ -165,6 +223,9 @@ struct Prod {
   size_t diag_in;
   int64_t ld_mirror;
   int M, N, K, tiles_m, tiles, count, tall;
+  int tile_n;  // columns of a tile: 256, or 128 where that still leaves a pair a tile at most
+  int splits, split_kb;  // GRAM: parts of the K axis, K blocks of one (parts: where their sums go)
+  size_t parts;
   int passes;  // 1: hi hi;  3: and hi lo, lo hi
   int last;    // the result is the user's: 1 bf16, 2 fp16
   int by_tma;  // ... by tensor copies
@@ -176,22 +237,33 @@ struct Prod {
 };
 
 struct Tile {
-  int z, i, j;
+  int z, i, j, part;
+  bool turned;  // also written turned over
 };
 template <int KIND>
 __device__ __forceinline__ Tile tile_of(const Prod &p, int t) {
   Tile ti;
+  ti.part = 0;
+  if (KIND == GRAM && p.splits > 1) {
+    ti.part = t % p.splits;
+    t /= p.splits;
+  }
   ti.z = t / p.tiles;
-  const int k = t - ti.z * p.tiles;
+  int k = t - ti.z * p.tiles;
   if (KIND == UPDATE) {  // consecutive tiles share columns
     ti.j = k / p.tiles_m;
     ti.i = k - ti.j * p.tiles_m;
-  } else {  // row i of the lower triangle holds tiles [i (i + 1) / 2, ...)
+    ti.turned = false;
+  } else {  // row i of the lower triangle holds squares [i (i + 1) / 2, ...), of one or two tiles
+    const int in_square = 256 / p.tile_n, first = k % in_square;
+    k /= in_square;
     int i = (int)((sqrtf(8.f * k + 1.f) - 1.f) * 0.5f);
     while (i * (i + 1) / 2 > k) --i;
     while ((i + 1) * (i + 2) / 2 <= k) ++i;
+    const int j = k - i * (i + 1) / 2;
     ti.i = i;
-    ti.j = k - i * (i + 1) / 2;
+    ti.j = j * in_square + first;
+    ti.turned = i != j;
   }
   return ti;
 }
@@ -235,9 +307,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *boxes = smem + (size_t)RING * OPERANDS;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(boxes + EPI_WARPS * 4 * BOX);
-  uint64_t *acc_full = bars + 2 * RING, *acc_empty = acc_full + 2, *box_in = acc_full + 4;  // [EPI_WARPS][2]
-  uint64_t *drained = box_in + 2 * EPI_WARPS;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(boxes + EPI_WARPS * BUFS * 2 * BOX);
+  uint64_t *acc_full = bars + 2 * RING, *acc_empty = acc_full + 2, *box_in = acc_full + 4;  // [EPI_WARPS][BUFS]
+  uint64_t *drained = box_in + BUFS * EPI_WARPS;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base_s + 1);
   const int wid = warp_id(), lane = lane_id();
@@ -255,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * EPI_WARPS);
     }
-    for (int b = 0; b < 2 * EPI_WARPS; ++b) mbar_init(&box_in[b], 1);
+    for (int b = 0; b < BUFS * EPI_WARPS; ++b) mbar_init(&box_in[b], 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -271,7 +343,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
-  const int nk = (p.K + BK - 1) / BK, total = p.tiles * p.count;
+  const int nk = (p.K + BK - 1) / BK, total = p.tiles * p.count * p.splits, tile_n = p.tile_n;
+  pdl_launch_dependents();
+  pdl_wait();           // the kernel before this one has written what this one reads,
+  fence_proxy_async();  // some of it by plain stores
+  auto blocks = [&](const Tile &ti, int &kb0, int &kb1) {  // K blocks of a tile
+    kb0 = ti.part * p.split_kb;
+    kb1 = min(nk, kb0 + p.split_kb);
+  };
 
   if (wid == 0) {
     if (lane == 0) {
@@ -280,14 +359,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       for (int n = 0, t; ok && (t = pair_tile(n, pair_id, npairs)) < total; ++n) {
         const Tile ti = tile_of<KIND>(p, t);
-        const int m0 = ti.i * 256 + (int)rank * 128, n0 = ti.j * 256 + (int)rank * 128;
+        const int m0 = ti.i * 256 + (int)rank * 128, n0 = ti.j * tile_n + (int)rank * (tile_n / 2);
+        int kb0, kb1;
+        blocks(ti, kb0, kb1);
         for (int pass = 0; ok && pass < p.passes; ++pass) {
           const CUtensorMap *ma = &maps.a[pass == 2], *mb = &maps.b[pass == 1];
-          for (int kb = 0; kb < nk; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!(ok = bar_wait(&rg.empty[rg.stage], rg.phase ^ 1u, ctl))) break;
             uint8_t *sb = rg.base + (size_t)rg.stage * OPERANDS;
             const uint32_t bar = full_leader + (uint32_t)(rg.stage * sizeof(uint64_t));
-            if (rank == 0) mbar_arrive_expect_tx(&rg.full[rg.stage], 2u * OPERANDS);  // both CTAs'
+            if (rank == 0) mbar_arrive_expect_tx(&rg.full[rg.stage], 2u * A_BYTES + (uint32_t)tile_n * BK * 2);  // both CTAs'
             if (A_MN) {
               tma_load_3d_pair(sb, ma, bar, m0, kb * BK, ti.z);
               tma_load_3d_pair(sb + CHUNK_BYTES, ma, bar, m0 + 64, kb * BK, ti.z);
@@ -296,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
             if (B_MN) {
               tma_load_3d_pair(sb + A_BYTES, mb, bar, n0, kb * BK, ti.z);
-              tma_load_3d_pair(sb + A_BYTES + CHUNK_BYTES, mb, bar, n0 + 64, kb * BK, ti.z);
+              if (tile_n > 128) tma_load_3d_pair(sb + A_BYTES + CHUNK_BYTES, mb, bar, n0 + 64, kb * BK, ti.z);
             } else {
               tma_load_3d_pair(sb + A_BYTES, mb, bar, kb * BK, n0, ti.z);
             }
@@ -309,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (lane == 0 && rank == 0) {
       // ---------------------------------------------------- MMA issuer (leader)
       constexpr uint64_t astep = A_MN ? MN_STEP : K_STEP, bstep = B_MN ? MN_STEP : K_STEP;
-      const uint32_t id = idesc(true, A_MN, B_MN, 256);
+      const uint32_t id = idesc(true, A_MN, B_MN, tile_n);
       uint32_t ne[2] = {0, 0};
       int b = 0;
       bool ok = true;
@@ -317,7 +398,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!(ok = bar_wait(&acc_empty[b], (ne[b]++ & 1u) ^ 1u, ctl))) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(b * ACC_COLS);
-        for (int kb = 0; kb < nk * p.passes; ++kb) {
+        int kb0, kb1;
+        blocks(tile_of<KIND>(p, t), kb0, kb1);
+        for (int kb = 0; kb < (kb1 - kb0) * p.passes; ++kb) {
           if (!(ok = bar_wait(&rg.full[rg.stage], rg.phase, ctl))) break;
           tc_fence_after();
           uint8_t *sb = rg.base + (size_t)rg.stage * OPERANDS;
@@ -333,53 +416,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    const int q = wid & 3, half = (wid - 2) / 4;
+    const int q = wid & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    uint8_t *my_boxes = boxes + (size_t)(wid - 2) * 4 * BOX;  // [2][hi, lo]
-    uint64_t *in = box_in + 2 * (wid - 2);
+    uint8_t *my_boxes = boxes + (size_t)(wid - 2) * BUFS * 2 * BOX;  // [BUFS][hi, lo]
+    uint64_t *in = box_in + BUFS * (wid - 2);
     const int two_in = KIND == UPDATE || p.passes > 1, two_out = KIND == UPDATE ? !p.last : p.passes > 1;
     uint32_t used[2] = {0, 0}, boxno = 0;
     int b = 0;
     bool ok = true;
     for (int n = 0, t; ok && (t = pair_tile(n, pair_id, npairs)) < total; ++n, b ^= 1) {
       const Tile ti = tile_of<KIND>(p, t);
-      const int row0 = ti.i * 256 + (int)rank * 128 + q * 32, row = row0 + lane, col0 = ti.j * 256 + half * 128;
-      const int chunks = row0 < p.M ? min(4, (p.N - col0 + 31) / 32) : 0;  // (negative: none)
+      const int row0 = ti.i * 256 + (int)rank * 128 + q * 32, row = row0 + lane, col0 = ti.j * tile_n;
+      const int chunks = row0 < p.M ? min(tile_n / 32, (p.N - col0 + 31) / 32) : 0;  // (negative: none)
       char *w = p.work + ti.z * p.stride;
       float *diag = reinterpret_cast<float *>(w + p.diag);
       const float *diag_in = reinterpret_cast<const float *>(w + p.diag_in);
       auto fetch = [&](int c) {  // box c of the tile's chunks as box number boxno + c
         if (KIND == GRAM || lane != 0) return;
-        const uint32_t k = (boxno + c) & 1u;
-        bulk_wait_read<0>();  // the last result has left it
+        const uint32_t k = (boxno + c) % BUFS;
+        bulk_wait_read<1>();  // all results but the newest have left: this box's is older
         mbar_arrive_expect_tx(&in[k], two_in ? 2 * BOX : BOX);
         tma_load_3d(my_boxes + k * 2 * BOX, &maps.in[0], &in[k], col0 + 32 * c, row0, ti.z);
         if (two_in) tma_load_3d(my_boxes + k * 2 * BOX + BOX, &maps.in[1], &in[k], col0 + 32 * c, row0, ti.z);
       };
       if (chunks > 0) fetch(0);
+      if (chunks > 1) fetch(1);
       const float d_row = KIND != GRAM && row < p.M && !(KIND == UPDATE && p.tall) ? diag_in[row] : 0.f;
       if (!(ok = __all_sync(0xffffffffu, bar_wait(&acc_full[b], used[b]++ & 1u, ctl)))) break;
       tc_fence_after();
-      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS + half * 128);
+      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS);
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const int col = col0 + 32 * c;
-        uint8_t *box = my_boxes + ((boxno + c) & 1u) * 2 * BOX;
-        if (c + 1 < chunks) fetch(c + 1);
+        const uint32_t bn = (boxno + c) % BUFS;
+        uint8_t *box = my_boxes + bn * 2 * BOX;
+        if (c + 2 < chunks) fetch(c + 2);
         uint32_t v[32];
         float x[32];
         tmem_ld32(acc + 32 * c, v);
 #pragma unroll
         for (int k = 0; k < 32; ++k) x[k] = 0.f;
         if (KIND != GRAM) {
-          if (!(ok = __all_sync(0xffffffffu, bar_wait(&in[(boxno + c) & 1u], ((boxno + c) >> 1) & 1u, ctl)))) break;
+          if (!(ok = __all_sync(0xffffffffu, bar_wait(&in[bn], ((boxno + c) / BUFS) & 1u, ctl)))) break;
           add_box(box, lane, x);
           if (two_in) add_box(box + BOX, lane, x);
         } else {
-          if (lane == 0) bulk_wait_read<0>();
+          if (lane == 0) bulk_wait_read<BUFS - 1>();
         }
         tmem_ld_wait();
         __syncwarp();  // the boxes have been read (GRAM: have left) before they are written
+        if (KIND == GRAM && p.splits > 1) {  // a part's sums, for join_kernel
+          if (row < p.M) {
+            float *to = reinterpret_cast<float *>(w + p.parts) + ((int64_t)ti.part * p.M + row) * p.ld_mirror + col;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4 *>(to + k) = make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]),
+                                                                __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+          }
+          continue;
+        }
         if (KIND == GRAM) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]) * (A_SCALE / (X_SCALE * X_SCALE));
@@ -437,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             bulk_commit();
           }
         }
-        if (KIND != UPDATE && ti.i != ti.j && row < p.M) {  // turned over: a warp's lanes side by side
+        if (ti.turned && row < p.M) {  // turned over: a warp's lanes side by side
           uint16_t *hi = reinterpret_cast<uint16_t *>(w + p.mirror[0]) + col * p.ld_mirror + row;
           uint16_t *lo = reinterpret_cast<uint16_t *>(w + p.mirror[1]) + col * p.ld_mirror + row;
 #pragma unroll
@@ -465,6 +560,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (wid == 1) tmem_dealloc2(tmem, TMEM_COLS);
 }
 
+// A Gram matrix of its parts, grid (rows, matrices)
+__global__ void __launch_bounds__(128) join_kernel(const Prod p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  char *w = p.work + blockIdx.y * p.stride;
+  const int i = blockIdx.x, end = min(p.M, (i / 256 + 1) * 256);  // the squares below the diagonal's, and that
+  const float *part = reinterpret_cast<const float *>(w + p.parts);
+  auto put = [&](int r, int c, float x) {
+    const int64_t at = r * p.ld_mirror + c;
+    const uint16_t h = to_half(x);
+    reinterpret_cast<uint16_t *>(w + p.mirror[0])[at] = h;
+    if (p.passes > 1) reinterpret_cast<uint16_t *>(w + p.mirror[1])[at] = to_half(x - widen(true, h));
+  };
+  for (int j = threadIdx.x; j < end; j += 128) {
+    float v = 0.f;
+    for (int k = 0; k < p.splits; ++k) v += part[((int64_t)k * p.M + i) * p.ld_mirror + j];
+    float x = v * (A_SCALE / (X_SCALE * X_SCALE));
+    if (i == j) {
+      reinterpret_cast<float *>(w + p.diag)[i] = x * (1.f / A_SCALE);
+      x = 0.f;
+    }
+    put(i, j, x);
+    if (j / 256 < i / 256) put(j, i, x);
+  }
+}
+
+// A launch that may begin while the kernel before it ends
+template <typename Kern, typename... Args>
+static cudaError_t launch_product(Kern kern, int num_sms, cudaStream_t st, const Args &...args) {
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (err != cudaSuccess) return err;
+  const int grid = 2 * max_resident_pairs((const void *)kern, THREADS, SMEM, num_sms);
+  if (grid <= 0) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kern, dim3(grid), dim3(THREADS), SMEM, st, args...);
+}
+
 }  // namespace orth
 
 // (bytes of one matrix, bytes that the call runs best with)
@@ -489,16 +620,20 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
     const unsigned n = std::min(each, o.count - at);
     p.g = reinterpret_cast<const char *>(o.g) + at * o.g_stride * gs;
     p.out = reinterpret_cast<char *>(o.out) + at * o.out_stride * 2;
-    const dim3 lines(std::min(o.rows, 1024), n);
-    auto start = [&](auto t) {
+    // 16-byte vectors of g where every row starts on their boundary
+    const bool vec = reinterpret_cast<uintptr_t>(p.g) % 16 == 0 && (o.rows == 1 || o.ld_g * gs % 16 == 0) && (n == 1 || o.g_stride * gs % 16 == 0);
+    auto start = [&](auto t, auto v) {
       using T = decltype(t);
-      squares_kernel<T><<<dim3(SUMS, n), 256, 0, st>>>(p);
-      start_kernel<T><<<lines, 256, 0, st>>>(p);
+      constexpr bool VEC = decltype(v)::value;
+      squares_kernel<T, VEC><<<dim3(SUMS, n), 256, 0, st>>>(p);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      const int64_t blocks = ((int64_t)o.rows * ((o.cols + 7) / 8) + 4 * SUMS - 1) / (4 * SUMS);  // four eights a thread
+      return launch_pdl(start_kernel<T, VEC>, dim3((unsigned)std::min<int64_t>(blocks, 16384), n), dim3(SUMS), 0, st, p);
     };
-    if (o.g_dtype == SYM_BF16) start(__nv_bfloat16());
-    else if (o.g_dtype == SYM_FP16) start(__half());
-    else start(float());
-    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    auto typed = [&](auto t) { return vec ? start(t, std::true_type()) : start(t, std::false_type()); };
+    err = o.g_dtype == SYM_BF16 ? typed(__nv_bfloat16()) : o.g_dtype == SYM_FP16 ? typed(__half()) : typed(float());
+    if (err != cudaSuccess) return err;
 
     // maps of an array's rows: operands, K-major (64 columns of 128 rows) or as they
     // lie (64 of 64), and the epilogue's boxes
@@ -519,17 +654,27 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
     q.a = p.a, q.b = p.b, q.c = p.c, q.scale = p.scale, q.status = o.status;
     q.tmo = o.wait_timeout_us ? o.wait_timeout_us : 2000000u;
     q.user = reinterpret_cast<char *>(p.out), q.user_stride = o.out_stride, q.user_ld = o.ld_out;
-    const int tm = (m + 255) / 256;
+    const int tm = (m + 255) / 256, pairs = num_sms / 2;
+    const int squares = tm * (tm + 1) / 2, tr = (p.rows + 255) / 256;
+    // 128 columns a tile where that leaves a pair one tile at most (a tile of 256 by
+    // itself is bound by what its pair of SMs can take in)
+    const int sq_n = 2 * squares * (int)n <= pairs ? 128 : 256;
+    const int up_n = (int64_t)tr * ((p.cols + 127) / 128) * n <= pairs ? 128 : 256;
+    const int sq_tiles = squares * (256 / sq_n), up_tiles = tr * ((p.cols + up_n - 1) / up_n);
+    const int nk = (std::max(p.rows, p.cols) + BK - 1) / BK;
+    int splits = std::max(1, std::min(l.splits, pairs / (sq_tiles * (int)std::min<unsigned>(n, 4096))));
+    const int split_kb = (nk + splits - 1) / splits;
+    splits = (nk + split_kb - 1) / split_kb;  // none without K blocks
     Maps gram[2], poly, update[2], final_maps;
     for (int k = 0; k < 2; ++k) {  // from copy k of X
       const size_t hi = l.hi + k * l.x_bytes, lo = l.lo + k * l.x_bytes, hi2 = l.hi + (k ^ 1) * l.x_bytes, lo2 = l.lo + (k ^ 1) * l.x_bytes;
       both(gram[k].a, hi, lo, p.rows, p.cols, l.ld_x, 64, p.tall ? 64 : 128);
-      gram[k].b[0] = gram[k].a[0], gram[k].b[1] = gram[k].a[1];
+      both(gram[k].b, hi, lo, p.rows, p.cols, l.ld_x, 64, p.tall ? 64 : sq_n / 2);
       both(gram[k].out, l.a, a_lo, m, m, l.ld_a, 32, 32);
       gram[k].in[0] = gram[k].out[0], gram[k].in[1] = gram[k].out[1];
       CUtensorMap x[2], sq[2];
       both(x, hi, lo, p.rows, p.cols, l.ld_x, 64, p.tall ? 128 : 64);
-      both(sq, l.b, b_lo, m, m, l.ld_a, 64, 128);
+      both(sq, l.b, b_lo, m, m, l.ld_a, 64, p.tall ? up_n / 2 : 128);
       for (int h = 0; h < 2; ++h) {
         update[k].a[h] = p.tall ? x[h] : sq[h];
         update[k].b[h] = p.tall ? sq[h] : x[h];
@@ -538,7 +683,7 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
       both(update[k].out, hi2, lo2, p.rows, p.cols, l.ld_x, 32, 32);
     }
     both(poly.a, l.a, a_lo, m, m, l.ld_a, 64, 128);
-    poly.b[0] = poly.a[0], poly.b[1] = poly.a[1];
+    both(poly.b, l.a, a_lo, m, m, l.ld_a, 64, sq_n / 2);
     both(poly.in, l.a, a_lo, m, m, l.ld_a, 32, 32);
     both(poly.out, l.b, b_lo, m, m, l.ld_a, 32, 32);
     const int by_tma = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && o.ld_out % 8 == 0 && (n == 1 || o.out_stride % 8 == 0);
@@ -551,27 +696,31 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
     for (int i = 0; i < o.steps; ++i) {
       const int k = i & 1;
       q.passes = o.out_dtype == SYM_FP16 && i >= o.steps - PRECISE_STEPS ? 3 : 1;
-      q.M = q.N = m, q.K = std::max(p.rows, p.cols), q.tiles_m = tm, q.tiles = tm * (tm + 1) / 2;
+      q.M = q.N = m, q.K = std::max(p.rows, p.cols), q.tiles_m = tm, q.tiles = sq_tiles, q.tile_n = sq_n;
       q.diag = l.diag_a, q.mirror[0] = l.a, q.mirror[1] = a_lo;
-      err = p.tall ? launch_pairs(product_kernel<GRAM, true, true>, THREADS, SMEM, num_sms, st, q, gram[k])
-                   : launch_pairs(product_kernel<GRAM, false, false>, THREADS, SMEM, num_sms, st, q, gram[k]);
+      q.splits = splits, q.split_kb = split_kb, q.parts = l.parts;
+      err = p.tall ? launch_product(product_kernel<GRAM, true, true>, num_sms, st, q, gram[k])
+                   : launch_product(product_kernel<GRAM, false, false>, num_sms, st, q, gram[k]);
+      if (err == cudaSuccess && splits > 1) err = launch_pdl(join_kernel, dim3(m, n), dim3(128), 0, st, q);
       if (err != cudaSuccess) return err;
+      q.splits = 1, q.split_kb = 1 << 30;
       q.K = m, q.diag_in = l.diag_a, q.diag = l.diag_b, q.mirror[0] = l.b, q.mirror[1] = b_lo;
-      err = launch_pairs(product_kernel<POLY, false, false>, THREADS, SMEM, num_sms, st, q, poly);
+      err = launch_product(product_kernel<POLY, false, false>, num_sms, st, q, poly);
       if (err != cudaSuccess) return err;
       q.M = p.rows, q.N = p.cols, q.diag_in = l.diag_b;
-      q.tiles_m = (p.rows + 255) / 256, q.tiles = q.tiles_m * ((p.cols + 255) / 256);
+      q.tiles_m = tr, q.tiles = up_tiles, q.tile_n = up_n;
       q.last = i + 1 < o.steps ? 0 : o.out_dtype == SYM_BF16 ? 1 : 2, q.by_tma = q.last && by_tma;
       const Maps &mp = q.last ? final_maps : update[k];
-      err = p.tall ? launch_pairs(product_kernel<UPDATE, false, false>, THREADS, SMEM, num_sms, st, q, mp)
-                   : launch_pairs(product_kernel<UPDATE, false, true>, THREADS, SMEM, num_sms, st, q, mp);
+      err = p.tall ? launch_product(product_kernel<UPDATE, false, false>, num_sms, st, q, mp)
+                   : launch_product(product_kernel<UPDATE, false, true>, num_sms, st, q, mp);
       if (err != cudaSuccess) return err;
       q.last = q.by_tma = 0;
     }
     if (o.steps == 0) {
-      if (o.out_dtype == SYM_BF16) finish_kernel<__nv_bfloat16><<<lines, 256, 0, st>>>(p, 0);
-      else finish_kernel<__half><<<lines, 256, 0, st>>>(p, 0);
-      if ((err = cudaGetLastError()) != cudaSuccess) return err;
+      const dim3 lines(std::min(o.rows, 1024), n);
+      err = o.out_dtype == SYM_BF16 ? launch_pdl(finish_kernel<__nv_bfloat16>, lines, dim3(256), 0, st, p, 0)
+                                    : launch_pdl(finish_kernel<__half>, lines, dim3(256), 0, st, p, 0);
+      if (err != cudaSuccess) return err;
     }
   }
   return cudaSuccess;

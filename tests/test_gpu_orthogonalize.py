@@ -29,7 +29,8 @@ def check(g, out, steps=5, coeffs=COEFFS, eps=1e-7, scale=1.0):
 
 
 SIZES = [(1, 1, 1), (2, 1, 9), (2, 9, 1), (3, 8, 8), (1, 31, 33), (2, 64, 64), (2, 65, 130), (1, 200, 72), (3, 128, 512),
-         (2, 256, 256), (1, 257, 255), (2, 300, 1000), (1, 1031, 519), (1, 520, 1032), (1, 640, 2049), (30, 72, 136)]
+         (2, 256, 256), (1, 257, 255), (2, 300, 1000), (1, 1031, 519), (1, 520, 1032), (1, 640, 2049), (30, 72, 136),
+         (1, 72, 4100), (2, 4100, 72), (1, 300, 2100), (1, 2100, 500), (3, 1300, 1288)]
 
 
 @pytest.mark.parametrize("count,rows,cols", SIZES)
