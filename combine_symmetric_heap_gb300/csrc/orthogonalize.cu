@@ -94,6 +94,7 @@ __device__ __forceinline__ void eight(const T *row, int c, int cols, float (&f)[
     for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? Elem<T>::get(row[c + i]) : 0.f;
   }
 }
+constexpr int AT_ONCE = 4;  // eights that a thread has in flight
 // Partial sums of squares, grid (SUMS, matrices): eight at a time in 32 bits where they
 // stay in range there, in 64 bits where not; added up in 64 bits.
 template <typename T, bool VEC>
@@ -101,27 +102,31 @@ __global__ void __launch_bounds__(256) squares_kernel(const Call p) {
   __shared__ double part[8];
   pdl_launch_dependents();
   const T *g = reinterpret_cast<const T *>(p.g) + blockIdx.y * p.g_stride;
-  // (a block takes every SUMS-th row, or where there are fewer rows a piece of one)
-  const int pieces = max(1, SUMS / p.rows), piece = blockIdx.x % pieces;
-  const int lines = SUMS / pieces;
+  const uint32_t each = (p.cols + 7) / 8, all = p.rows * each, step = SUMS * 256;  // eights of a row, of the matrix
   double s = 0;
-  for (int r = blockIdx.x / pieces; r < p.rows; r += lines) {  // (with pieces lines are at least the rows)
-    float run = 0.f;
-    int held = 0;
-#pragma unroll 4
-    for (int c = (piece * 256 + (int)threadIdx.x) * 8; c < p.cols; c += pieces * 256 * 8) {
-      float f[8], q = 0.f, most = 0.f;
-      eight<T, VEC>(g + r * p.ldg, c, p.cols, f);
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < all; i += AT_ONCE * step) {
+    float f[AT_ONCE][8], run = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        q += f[i] * f[i];
-        most = fmaxf(most, fabsf(f[i]));
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const uint32_t k = i + u * step, r = k / each, c = (k - r * each) * 8;
+      if (k < all) eight<T, VEC>(g + r * p.ldg, c, p.cols, f[u]);
+      else
+#pragma unroll
+        for (int v = 0; v < 8; ++v) f[u][v] = 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      float q = 0.f, most = 0.f;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        q += f[u][v] * f[u][v];
+        most = fmaxf(most, fabsf(f[u][v]));
       }
       if (most <= 1e15f && (most >= 1e-15f || most == 0.f) && q == q) {
         run += q;
-        if (++held == 8) s += run, run = 0.f, held = 0;
       } else {
-        for (int i = 0; i < 8; ++i) s += (double)f[i] * f[i];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) s += (double)f[u][v] * f[u][v];
       }
     }
     s += run;
@@ -161,19 +166,28 @@ __global__ void __launch_bounds__(SUMS) start_kernel(const Call p) {
   const State s = state_of(p, blockIdx.y, 0);
   pdl_wait();
   const float2 f = normaliser(reinterpret_cast<const double *>(p.work + blockIdx.y * p.l.total + p.l.sums), p.eps);
-  const int each = (p.cols + 7) / 8;  // eights of a row
-  for (int64_t i = (int64_t)blockIdx.x * SUMS + threadIdx.x; i < (int64_t)p.rows * each; i += (int64_t)gridDim.x * SUMS) {
-    const int r = (int)(i / each), c = (int)(i - (int64_t)r * each) * 8;
-    float v[8], h[8];
-    eight<T, VEC>(g + r * p.ldg, c, p.cols, v);
+  const uint32_t each = (p.cols + 7) / 8, all = p.rows * each, step = gridDim.x * SUMS;
+  for (uint32_t i = blockIdx.x * SUMS + threadIdx.x; i < all; i += AT_ONCE * step) {
+    float v[AT_ONCE][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = v[k] * f.x * f.y;
-    const uint4 hi = pack<__half, 8>(v);
-    unpack<__half, 8>(hi, h);
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const uint32_t k = i + u * step, r = k / each, c = (k - r * each) * 8;
+      if (k < all) eight<T, VEC>(g + r * p.ldg, c, p.cols, v[u]);
+    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] -= h[k];
-    *reinterpret_cast<uint4 *>(s.hi + r * p.l.ld_x + c) = hi;
-    *reinterpret_cast<uint4 *>(s.lo + r * p.l.ld_x + c) = pack<__half, 8>(v);
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const uint32_t k = i + u * step, r = k / each, c = (k - r * each) * 8;
+      if (k >= all) break;
+      float h[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v[u][w] = v[u][w] * f.x * f.y;
+      const uint4 hi = pack<__half, 8>(v[u]);
+      unpack<__half, 8>(hi, h);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v[u][w] -= h[w];
+      *reinterpret_cast<uint4 *>(s.hi + r * p.l.ld_x + c) = hi;
+      *reinterpret_cast<uint4 *>(s.lo + r * p.l.ld_x + c) = pack<__half, 8>(v[u]);
+    }
   }
 }
 template <typename T>
@@ -198,14 +212,16 @@ __global__ void __launch_bounds__(256) finish_kernel(const Call p, int copy) {
 // written twice, as it is and turned over.
 //
 // What a product adds to (A for POLY, X for UPDATE) comes into an epilogue
-// warp's own boxes of 32 x 32 by tensor copies, two boxes ahead, and the result leaves
-// from there (four boxes for each of four warps; two for each of eight, one ahead, left
-// a box waiting for the copy out before it: 8 x 2048 x 7168 UPDATE 335 us instead of NEW).  X X^T of wide matrices and products with A or B read K-major
+// warp's own boxes of 32 x 32 one box ahead (cp.async), is turned there from rows of
+// memory to rows of a lane, and the result back the same way.  Tensor copies of the
+// boxes were no faster where products are large (8 x 2048 x 7168 UPDATE 308 to 335 us, 316
+// to 328 now; four warps with three boxes ahead 316) and slower where they are small, each issued by
+// one lane while the others wait (POLY 75 us, now 61; 5 x 1031 x 519 370 us in all, now 312).  X X^T of wide matrices and products with A or B read K-major
 // tiles; X^T X and the X of B X lie the other way and are read as they lie.
 // ---------------------------------------------------------------------------
 enum Kind { GRAM, POLY, UPDATE };
-constexpr int EPI_WARPS = 4;  // one per TMEM lane quarter
-constexpr int BUFS = 4;       // boxes (hi and lo) of an epilogue warp
+constexpr int EPI_WARPS = 8;  // two per TMEM lane quarter, each with half of a tile's columns
+constexpr int BUFS = 2;       // boxes (hi and lo) of an epilogue warp
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
 constexpr int RING = 5;
 constexpr int OPERANDS = A_BYTES + B_BYTES;  // of a stage
@@ -214,21 +230,21 @@ constexpr int CTRL = 512;
 constexpr int SMEM = 1024 + RING * OPERANDS + EPI_WARPS * BUFS * 2 * BOX + CTRL;
 
 struct Maps {
-  CUtensorMap a[2], b[2];     // operands: hi, lo
-  CUtensorMap in[2], out[2];  // what is added to, the result: hi, lo (out[0] of the last step: the user's)
+  CUtensorMap a[2], b[2];  // operands: hi, lo
 };
 struct Prod {
   char *work;  // of the turn's first matrix
-  size_t stride, diag, mirror[2];  // between matrices; where the diagonal and the turned tiles go (GRAM, POLY) or come from
-  size_t diag_in;
-  int64_t ld_mirror;
+  size_t stride;        // between matrices
+  size_t in[2], out[2]; // what is added to and the result: hi, lo
+  size_t diag_in, diag; // B's and A's diagonals
+  int64_t ld;           // of those rows
   int M, N, K, tiles_m, tiles, count, tall;
   int tile_n;  // columns of a tile: 256, or 128 where that still leaves a pair a tile at most
   int splits, split_kb;  // GRAM: parts of the K axis, K blocks of one (parts: where their sums go)
   size_t parts;
   int passes;  // 1: hi hi;  3: and hi lo, lo hi
   int last;    // the result is the user's: 1 bf16, 2 fp16
-  int by_tma;  // ... by tensor copies
+  int vec;     // ... with rows of 16-byte vectors
   char *user;
   int64_t user_stride, user_ld;
   float a, b, c, scale;
@@ -308,8 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *boxes = smem + (size_t)RING * OPERANDS;
   uint64_t *bars = reinterpret_cast<uint64_t *>(boxes + EPI_WARPS * BUFS * 2 * BOX);
-  uint64_t *acc_full = bars + 2 * RING, *acc_empty = acc_full + 2, *box_in = acc_full + 4;  // [EPI_WARPS][BUFS]
-  uint64_t *drained = box_in + BUFS * EPI_WARPS;
+  uint64_t *acc_full = bars + 2 * RING, *acc_empty = acc_full + 2, *drained = acc_full + 4;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base_s + 1);
   const int wid = warp_id(), lane = lane_id();
@@ -327,7 +342,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * EPI_WARPS);
     }
-    for (int b = 0; b < BUFS * EPI_WARPS; ++b) mbar_init(&box_in[b], 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -416,58 +430,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    const int q = wid & 3;
+    constexpr int SHARES = EPI_WARPS / 4;  // of a tile's columns
+    const int q = wid & 3, share = (wid - 2) / 4;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     uint8_t *my_boxes = boxes + (size_t)(wid - 2) * BUFS * 2 * BOX;  // [BUFS][hi, lo]
-    uint64_t *in = box_in + BUFS * (wid - 2);
     const int two_in = KIND == UPDATE || p.passes > 1, two_out = KIND == UPDATE ? !p.last : p.passes > 1;
-    uint32_t used[2] = {0, 0}, boxno = 0;
+    // memory's rows: lane 4r + w has word w of rows r, 8 + r, ...
+    const int r8 = lane >> 2, w4 = lane & 3;
+    auto in_box = [&](uint8_t *box, int r) { return reinterpret_cast<uint4 *>(box + r * 64 + ((w4 ^ ((r >> 1) & 3)) << 4)); };
+    uint32_t used[2] = {0, 0};
+    uint32_t boxno = 0;
     int b = 0;
     bool ok = true;
     for (int n = 0, t; ok && (t = pair_tile(n, pair_id, npairs)) < total; ++n, b ^= 1) {
       const Tile ti = tile_of<KIND>(p, t);
-      const int row0 = ti.i * 256 + (int)rank * 128 + q * 32, row = row0 + lane, col0 = ti.j * tile_n;
-      const int chunks = row0 < p.M ? min(tile_n / 32, (p.N - col0 + 31) / 32) : 0;  // (negative: none)
+      const int row0 = ti.i * 256 + (int)rank * 128 + q * 32, row = row0 + lane, col0 = ti.j * tile_n + share * (tile_n / SHARES);
+      const int chunks = row0 < p.M ? min(tile_n / SHARES / 32, (p.N - col0 + 31) / 32) : 0;  // (negative: none)
       char *w = p.work + ti.z * p.stride;
       float *diag = reinterpret_cast<float *>(w + p.diag);
       const float *diag_in = reinterpret_cast<const float *>(w + p.diag_in);
-      auto fetch = [&](int c) {  // box c of the tile's chunks as box number boxno + c
-        if (KIND == GRAM || lane != 0) return;
-        const uint32_t k = (boxno + c) % BUFS;
-        bulk_wait_read<1>();  // all results but the newest have left: this box's is older
-        mbar_arrive_expect_tx(&in[k], two_in ? 2 * BOX : BOX);
-        tma_load_3d(my_boxes + k * 2 * BOX, &maps.in[0], &in[k], col0 + 32 * c, row0, ti.z);
-        if (two_in) tma_load_3d(my_boxes + k * 2 * BOX + BOX, &maps.in[1], &in[k], col0 + 32 * c, row0, ti.z);
+      const bool by_column = KIND == POLY || (KIND == UPDATE && p.tall);
+      auto fetch = [&](int c) {  // the tile's box c
+        if (KIND == GRAM) return;
+        if (c >= chunks) {
+          cp_async_commit();
+          return;
+        }
+        uint8_t *box = my_boxes + (boxno + c) % BUFS * 2 * BOX;
+        const int64_t at = (int64_t)(row0 + r8) * p.ld + col0 + 32 * c + 8 * w4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row0 + 8 * i + r8 < p.M) {
+            cp_async16(in_box(box, 8 * i + r8), reinterpret_cast<const __half *>(w + p.in[0]) + at + 8 * i * p.ld);
+            if (two_in) cp_async16(in_box(box + BOX, 8 * i + r8), reinterpret_cast<const __half *>(w + p.in[1]) + at + 8 * i * p.ld);
+          }
+        cp_async_commit();
       };
-      if (chunks > 0) fetch(0);
-      if (chunks > 1) fetch(1);
+#pragma unroll
+      for (int c = 0; c < BUFS - 1; ++c) fetch(c);
+      // the next box's columns' diagonal elements, one a lane (padded to whole boxes)
+      float d_next = by_column && chunks > 0 ? diag_in[col0 + lane] : 0.f;
       const float d_row = KIND != GRAM && row < p.M && !(KIND == UPDATE && p.tall) ? diag_in[row] : 0.f;
       if (!(ok = __all_sync(0xffffffffu, bar_wait(&acc_full[b], used[b]++ & 1u, ctl)))) break;
       tc_fence_after();
-      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS);
+      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS + share * (tile_n / SHARES));
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const int col = col0 + 32 * c;
-        const uint32_t bn = (boxno + c) % BUFS;
-        uint8_t *box = my_boxes + bn * 2 * BOX;
-        if (c + 2 < chunks) fetch(c + 2);
+        uint8_t *box = my_boxes + (boxno + c) % BUFS * 2 * BOX;
+        const float d_col = d_next;
+        if (by_column && c + 1 < chunks) d_next = diag_in[col + 32 + lane];
         uint32_t v[32];
         float x[32];
         tmem_ld32(acc + 32 * c, v);
 #pragma unroll
         for (int k = 0; k < 32; ++k) x[k] = 0.f;
         if (KIND != GRAM) {
-          if (!(ok = __all_sync(0xffffffffu, bar_wait(&in[bn], ((boxno + c) / BUFS) & 1u, ctl)))) break;
+          fetch(c + BUFS - 1);
+          cp_async_wait<BUFS - 1>();
+          __syncwarp();
           add_box(box, lane, x);
           if (two_in) add_box(box + BOX, lane, x);
-        } else {
-          if (lane == 0) bulk_wait_read<BUFS - 1>();
         }
         tmem_ld_wait();
-        __syncwarp();  // the boxes have been read (GRAM: have left) before they are written
         if (KIND == GRAM && p.splits > 1) {  // a part's sums, for join_kernel
           if (row < p.M) {
-            float *to = reinterpret_cast<float *>(w + p.parts) + ((int64_t)ti.part * p.M + row) * p.ld_mirror + col;
+            float *to = reinterpret_cast<float *>(w + p.parts) + ((int64_t)ti.part * p.M + row) * p.ld + col;
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
               *reinterpret_cast<float4 *>(to + k) = make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]),
@@ -480,20 +508,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]) * (A_SCALE / (X_SCALE * X_SCALE));
         } else if (KIND == POLY) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 dj = *reinterpret_cast<const float4 *>(diag_in + col + k);
-            const float d4[4] = {dj.x, dj.y, dj.z, dj.w};
+          for (int k = 0; k < 32; ++k)
+            x[k] = (p.b + p.c * (d_row + __shfl_sync(0xffffffffu, d_col, k))) * (x[k] * (B_SCALE / A_SCALE)) +
+                   p.c * (__uint_as_float(v[k]) * (B_SCALE / (A_SCALE * A_SCALE)));
+        } else if (p.tall) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              x[k + u] = (p.b + p.c * (d_row + d4[u])) * (x[k + u] * (B_SCALE / A_SCALE)) +
-                         p.c * (__uint_as_float(v[k + u]) * (B_SCALE / (A_SCALE * A_SCALE)));
-          }
+          for (int k = 0; k < 32; ++k)
+            x[k] = (p.a + __shfl_sync(0xffffffffu, d_col, k)) * x[k] + __uint_as_float(v[k]) * (1.f / B_SCALE);
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float e = p.tall ? __ldg(diag_in + col + k) : d_row;
-            x[k] = (p.a + e) * x[k] + __uint_as_float(v[k]) * (1.f / B_SCALE);
-          }
+          for (int k = 0; k < 32; ++k) x[k] = (p.a + d_row) * x[k] + __uint_as_float(v[k]) * (1.f / B_SCALE);
         }
         if (KIND != UPDATE && row0 == col) {  // 32 elements of the diagonal, one for each lane
 #pragma unroll
@@ -506,49 +530,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               x[k] = 0.f;
             }
         }
-        if (KIND == UPDATE && p.last) {
+        const bool users = KIND == UPDATE && p.last;
+        if (users) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] *= p.scale / X_SCALE;
-          if (p.by_tma) {
-            if (p.last == 1) put_boxes<__nv_bfloat16, false>(box, lane, x);
-            else put_boxes<__half, false>(box, lane, x);
-          } else if (row < p.M) {
-            uint16_t *to = reinterpret_cast<uint16_t *>(p.user) + ti.z * p.user_stride + row * p.user_ld + col;
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (col + k < p.N) to[k] = p.last == 1 ? to_bf16(x[k]) : to_half(x[k]);
-          }
+          if (p.last == 1) put_boxes<__nv_bfloat16, false>(box, lane, x);
+          else put_boxes<__half, false>(box, lane, x);
         } else if (two_out) {
           put_boxes<__half, true>(box, lane, x);
         } else {
           put_boxes<__half, false>(box, lane, x);
         }
-        if (KIND != UPDATE || !p.last || p.by_tma) {
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&maps.out[0], box, col, row0, ti.z);
-            if (two_out) tma_store_3d(&maps.out[1], box + BOX, col, row0, ti.z);
-            bulk_commit();
-          }
+        __syncwarp();
+        if (!users) {  // (whole words: rows' pitches are whole boxes)
+          const int64_t at = (int64_t)(row0 + r8) * p.ld + col + 8 * w4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row0 + 8 * i + r8 < p.M) {
+              *reinterpret_cast<uint4 *>(reinterpret_cast<__half *>(w + p.out[0]) + at + 8 * i * p.ld) = *in_box(box, 8 * i + r8);
+              if (two_out)
+                *reinterpret_cast<uint4 *>(reinterpret_cast<__half *>(w + p.out[1]) + at + 8 * i * p.ld) = *in_box(box + BOX, 8 * i + r8);
+            }
+        } else if (p.vec && col + 32 <= p.N) {
+          uint16_t *to = reinterpret_cast<uint16_t *>(p.user) + ti.z * p.user_stride + (row0 + r8) * p.user_ld + col + 8 * w4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row0 + 8 * i + r8 < p.M) *reinterpret_cast<uint4 *>(to + 8 * i * p.user_ld) = *in_box(box, 8 * i + r8);
+        } else if (col + lane < p.N) {  // a row at a time, a column a lane
+          uint16_t *to = reinterpret_cast<uint16_t *>(p.user) + ti.z * p.user_stride + row0 * p.user_ld + col + lane;
+#pragma unroll 8
+          for (int r = 0; r < min(32, p.M - row0); ++r)
+            to[r * p.user_ld] =
+                *reinterpret_cast<const uint16_t *>(box + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
         }
+        __syncwarp();  // the box has been read
         if (ti.turned && row < p.M) {  // turned over: a warp's lanes side by side
-          uint16_t *hi = reinterpret_cast<uint16_t *>(w + p.mirror[0]) + col * p.ld_mirror + row;
-          uint16_t *lo = reinterpret_cast<uint16_t *>(w + p.mirror[1]) + col * p.ld_mirror + row;
+          uint16_t *hi = reinterpret_cast<uint16_t *>(w + p.out[0]) + col * p.ld + row;
+          uint16_t *lo = reinterpret_cast<uint16_t *>(w + p.out[1]) + col * p.ld + row;
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (col + k < p.N) {
               const uint16_t h = to_half(x[k]);
-              hi[k * p.ld_mirror] = h;
-              if (two_out) lo[k * p.ld_mirror] = to_half(x[k] - widen(true, h));
+              hi[k * p.ld] = h;
+              if (two_out) lo[k * p.ld] = to_half(x[k] - widen(true, h));
             }
         }
       }
-      if (!ok) break;
       boxno += (uint32_t)max(chunks, 0);
       give_back(&acc_empty[b], rank, lane);
     }
-    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -568,14 +598,14 @@ __global__ void __launch_bounds__(128) join_kernel(const Prod p) {
   const int i = blockIdx.x, end = min(p.M, (i / 256 + 1) * 256);  // the squares below the diagonal's, and that
   const float *part = reinterpret_cast<const float *>(w + p.parts);
   auto put = [&](int r, int c, float x) {
-    const int64_t at = r * p.ld_mirror + c;
+    const int64_t at = r * p.ld + c;
     const uint16_t h = to_half(x);
-    reinterpret_cast<uint16_t *>(w + p.mirror[0])[at] = h;
-    if (p.passes > 1) reinterpret_cast<uint16_t *>(w + p.mirror[1])[at] = to_half(x - widen(true, h));
+    reinterpret_cast<uint16_t *>(w + p.out[0])[at] = h;
+    if (p.passes > 1) reinterpret_cast<uint16_t *>(w + p.out[1])[at] = to_half(x - widen(true, h));
   };
   for (int j = threadIdx.x; j < end; j += 128) {
     float v = 0.f;
-    for (int k = 0; k < p.splits; ++k) v += part[((int64_t)k * p.M + i) * p.ld_mirror + j];
+    for (int k = 0; k < p.splits; ++k) v += part[((int64_t)k * p.M + i) * p.ld + j];
     float x = v * (A_SCALE / (X_SCALE * X_SCALE));
     if (i == j) {
       reinterpret_cast<float *>(w + p.diag)[i] = x * (1.f / A_SCALE);
@@ -628,20 +658,21 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
       squares_kernel<T, VEC><<<dim3(SUMS, n), 256, 0, st>>>(p);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
-      const int64_t blocks = ((int64_t)o.rows * ((o.cols + 7) / 8) + 4 * SUMS - 1) / (4 * SUMS);  // four eights a thread
-      return launch_pdl(start_kernel<T, VEC>, dim3((unsigned)std::min<int64_t>(blocks, 16384), n), dim3(SUMS), 0, st, p);
+      const int64_t blocks = ((int64_t)o.rows * ((o.cols + 7) / 8) + AT_ONCE * SUMS - 1) / (AT_ONCE * SUMS);
+      // (each block adds up the partial sums for itself: no more blocks than keep the SMs full)
+      const int64_t most = std::max<int64_t>(1, 16 * num_sms / n);
+      return launch_pdl(start_kernel<T, VEC>, dim3((unsigned)std::min(blocks, most), n), dim3(SUMS), 0, st, p);
     };
     auto typed = [&](auto t) { return vec ? start(t, std::true_type()) : start(t, std::false_type()); };
     err = o.g_dtype == SYM_BF16 ? typed(__nv_bfloat16()) : o.g_dtype == SYM_FP16 ? typed(__half()) : typed(float());
     if (err != cudaSuccess) return err;
 
-    // maps of an array's rows: operands, K-major (64 columns of 128 rows) or as they
-    // lie (64 of 64), and the epilogue's boxes
+    // maps of the operands' rows: K-major (64 columns of 128 rows, or of half a tile's)
+    // or as they lie (64 of 64)
     bool ok = true;
     auto map = [&](size_t at_, int rows, int cols, int64_t ld, uint32_t b0, uint32_t b1) {
       CUtensorMap t;
-      ok = encode(&t, work + at_, cols, rows, n, ld, between, b0, b1, false,
-                  b0 == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) && ok;
+      ok = encode(&t, work + at_, cols, rows, n, ld, between, b0, b1) && ok;
       return t;
     };
     auto both = [&](CUtensorMap(&t)[2], size_t hi, size_t lo, int rows, int cols, int64_t ld, uint32_t b0, uint32_t b1) {
@@ -650,7 +681,7 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
     };
     const size_t a_lo = l.a + l.a_bytes, b_lo = l.b + l.a_bytes;
     Prod q{};
-    q.work = p.work, q.stride = l.total, q.count = n, q.tall = p.tall, q.ld_mirror = l.ld_a;
+    q.work = p.work, q.stride = l.total, q.count = n, q.tall = p.tall;
     q.a = p.a, q.b = p.b, q.c = p.c, q.scale = p.scale, q.status = o.status;
     q.tmo = o.wait_timeout_us ? o.wait_timeout_us : 2000000u;
     q.user = reinterpret_cast<char *>(p.out), q.user_stride = o.out_stride, q.user_ld = o.ld_out;
@@ -665,13 +696,11 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
     int splits = std::max(1, std::min(l.splits, pairs / (sq_tiles * (int)std::min<unsigned>(n, 4096))));
     const int split_kb = (nk + splits - 1) / splits;
     splits = (nk + split_kb - 1) / split_kb;  // none without K blocks
-    Maps gram[2], poly, update[2], final_maps;
+    Maps gram[2], poly, update[2];
     for (int k = 0; k < 2; ++k) {  // from copy k of X
-      const size_t hi = l.hi + k * l.x_bytes, lo = l.lo + k * l.x_bytes, hi2 = l.hi + (k ^ 1) * l.x_bytes, lo2 = l.lo + (k ^ 1) * l.x_bytes;
+      const size_t hi = l.hi + k * l.x_bytes, lo = l.lo + k * l.x_bytes;
       both(gram[k].a, hi, lo, p.rows, p.cols, l.ld_x, 64, p.tall ? 64 : 128);
       both(gram[k].b, hi, lo, p.rows, p.cols, l.ld_x, 64, p.tall ? 64 : sq_n / 2);
-      both(gram[k].out, l.a, a_lo, m, m, l.ld_a, 32, 32);
-      gram[k].in[0] = gram[k].out[0], gram[k].in[1] = gram[k].out[1];
       CUtensorMap x[2], sq[2];
       both(x, hi, lo, p.rows, p.cols, l.ld_x, 64, p.tall ? 128 : 64);
       both(sq, l.b, b_lo, m, m, l.ld_a, 64, p.tall ? up_n / 2 : 128);
@@ -679,42 +708,35 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
         update[k].a[h] = p.tall ? x[h] : sq[h];
         update[k].b[h] = p.tall ? sq[h] : x[h];
       }
-      both(update[k].in, hi, lo, p.rows, p.cols, l.ld_x, 32, 32);
-      both(update[k].out, hi2, lo2, p.rows, p.cols, l.ld_x, 32, 32);
     }
     both(poly.a, l.a, a_lo, m, m, l.ld_a, 64, 128);
     both(poly.b, l.a, a_lo, m, m, l.ld_a, 64, sq_n / 2);
-    both(poly.in, l.a, a_lo, m, m, l.ld_a, 32, 32);
-    both(poly.out, l.b, b_lo, m, m, l.ld_a, 32, 32);
-    const int by_tma = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && o.ld_out % 8 == 0 && (n == 1 || o.out_stride % 8 == 0);
-    final_maps = update[(o.steps + 1) & 1];
-    if (by_tma)
-      ok = encode(&final_maps.out[0], reinterpret_cast<uint64_t>(p.out), p.cols, p.rows, n, std::max<int64_t>(o.ld_out, (p.cols + 7) / 8 * 8),
-                  n > 1 ? o.out_stride : (int64_t)p.rows * std::max<int64_t>(o.ld_out, (p.cols + 7) / 8 * 8), 32, 32, false,
-                  CU_TENSOR_MAP_SWIZZLE_64B) && ok;
+    const int user_vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && (p.rows == 1 || o.ld_out % 8 == 0) && (n == 1 || o.out_stride % 8 == 0);
     if (!ok) return cudaErrorInvalidValue;
     for (int i = 0; i < o.steps; ++i) {
       const int k = i & 1;
       q.passes = o.out_dtype == SYM_FP16 && i >= o.steps - PRECISE_STEPS ? 3 : 1;
       q.M = q.N = m, q.K = std::max(p.rows, p.cols), q.tiles_m = tm, q.tiles = sq_tiles, q.tile_n = sq_n;
-      q.diag = l.diag_a, q.mirror[0] = l.a, q.mirror[1] = a_lo;
+      q.diag = l.diag_a, q.out[0] = l.a, q.out[1] = a_lo, q.ld = l.ld_a;
       q.splits = splits, q.split_kb = split_kb, q.parts = l.parts;
       err = p.tall ? launch_product(product_kernel<GRAM, true, true>, num_sms, st, q, gram[k])
                    : launch_product(product_kernel<GRAM, false, false>, num_sms, st, q, gram[k]);
       if (err == cudaSuccess && splits > 1) err = launch_pdl(join_kernel, dim3(m, n), dim3(128), 0, st, q);
       if (err != cudaSuccess) return err;
       q.splits = 1, q.split_kb = 1 << 30;
-      q.K = m, q.diag_in = l.diag_a, q.diag = l.diag_b, q.mirror[0] = l.b, q.mirror[1] = b_lo;
+      q.K = m, q.diag_in = l.diag_a, q.diag = l.diag_b;
+      q.in[0] = l.a, q.in[1] = a_lo, q.out[0] = l.b, q.out[1] = b_lo;
       err = launch_product(product_kernel<POLY, false, false>, num_sms, st, q, poly);
       if (err != cudaSuccess) return err;
       q.M = p.rows, q.N = p.cols, q.diag_in = l.diag_b;
       q.tiles_m = tr, q.tiles = up_tiles, q.tile_n = up_n;
-      q.last = i + 1 < o.steps ? 0 : o.out_dtype == SYM_BF16 ? 1 : 2, q.by_tma = q.last && by_tma;
-      const Maps &mp = q.last ? final_maps : update[k];
-      err = p.tall ? launch_product(product_kernel<UPDATE, false, false>, num_sms, st, q, mp)
-                   : launch_product(product_kernel<UPDATE, false, true>, num_sms, st, q, mp);
+      q.last = i + 1 < o.steps ? 0 : o.out_dtype == SYM_BF16 ? 1 : 2, q.vec = user_vec;
+      q.in[0] = l.hi + k * l.x_bytes, q.in[1] = l.lo + k * l.x_bytes, q.ld = l.ld_x;
+      q.out[0] = l.hi + (k ^ 1) * l.x_bytes, q.out[1] = l.lo + (k ^ 1) * l.x_bytes;
+      err = p.tall ? launch_product(product_kernel<UPDATE, false, false>, num_sms, st, q, update[k])
+                   : launch_product(product_kernel<UPDATE, false, true>, num_sms, st, q, update[k]);
       if (err != cudaSuccess) return err;
-      q.last = q.by_tma = 0;
+      q.last = 0;
     }
     if (o.steps == 0) {
       const dim3 lines(std::min(o.rows, 1024), n);
