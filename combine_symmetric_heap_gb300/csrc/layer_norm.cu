@@ -158,6 +158,210 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(const Fwd p) {
   }
 }
 
+// Forward for rows that fit the registers: a thread holds NV vectors of V columns, so the
+// row is read once.  WARP: a warp has a row (four rows a block), else a block.
+template <typename T, int V, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? 128 : 1024) layer_norm_held_kernel(const Fwd p) {
+  __shared__ float buf[2 * 32];
+  const int warps = WARP ? 1 : blockDim.x / 32, warp = WARP ? 0 : threadIdx.x / 32;
+  const int thread = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
+  const int each = WARP ? blockDim.x / 32 : 1;
+  const float inv = 1.f / p.cols;
+  int turn = 0;
+  for (int r = blockIdx.x * each + (WARP ? (int)threadIdx.x / 32 : 0); r < p.rows; r += gridDim.x * each) {
+    const T *x = at<T>(p.x, r, p.ldx), *add = p.add ? at<T>(p.add, r, p.ld_add) : nullptr;
+    float s[NV][V], m[1] = {0.f}, v[1] = {0.f};
+    auto column = [&](int j) { return (thread + j * threads) * V; };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (column(j) < p.cols) {
+        load<T, V>(x + column(j), s[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[j][i] = 0.f;
+      }
+    }
+    if (add) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (column(j) < p.cols) {
+          float t[V];
+          load<T, V>(add + column(j), t);
+#pragma unroll
+          for (int i = 0; i < V; ++i) s[j][i] += t[i];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) m[0] += s[j][i];
+    group_sums<1>(m, buf, warp, warps, turn);
+    auto squares = [&](float mean, float scale) {  // of the distances, scaled
+      v[0] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (column(j) < p.cols)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float d = s[j][i] * scale - mean;
+            v[0] += d * d;
+          }
+      group_sums<1>(v, buf, warp, warps, turn);
+    };
+    float mean = m[0] * inv;
+    squares(mean, 1.f);
+    float rstd = rsqrtf(v[0] * inv + p.eps);
+    if (!squares_hold(v[0], inv, p.eps)) {
+      float largest = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) largest = fmaxf(largest, fabsf(s[j][i]));
+      const int e = max(-126, min(126, row_exponent(largest, buf, warp, warps, turn)));
+      const float scale = ldexpf(1.f, -e);
+      m[0] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) m[0] += s[j][i] * scale;
+      group_sums<1>(m, buf, warp, warps, turn);
+      squares(m[0] * inv, scale);
+      mean = ldexpf(m[0] * inv, e);
+      rstd = scaled_rstd(v[0], e, inv, p.eps);
+    }
+    if (thread == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = column(j);
+      if (c >= p.cols) continue;
+      if (p.sum) store<T, V>(at<T>(p.sum, r, p.ld_sum) + c, s[j]);
+      if (!p.h) continue;
+      float t[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[j][i] = (s[j][i] - mean) * rstd;
+      if (p.w) {
+        load<T, V>(reinterpret_cast<const T *>(p.w) + c, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[j][i] *= t[i];
+      }
+      if (p.b) {
+        load<T, V>(reinterpret_cast<const T *>(p.b) + c, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[j][i] += t[i];
+      }
+      store<T, V>(at<T>(p.h, r, p.ldh) + c, s[j]);
+    }
+  }
+}
+
+// Backward for rows of up to 8192 columns, everything in one pass: a block walks its rows, a
+// thread has the same NV vectors of V columns of each and keeps their two column sums in
+// registers.  AHEAD: the next row's vectors are loaded before this row's sums.
+template <typename T, int V, int NV, bool AHEAD>
+__global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_bwd_kernel(const Bwd p) {
+  __shared__ float buf[2 * 32 * 2];
+  using Raw = typename std::conditional<V == 1, T, uint4>::type;
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
+  const float inv = 1.f / p.cols;
+  int turn = 0;
+  auto column = [&](int j) { return ((int)threadIdx.x + j * (int)blockDim.x) * V; };
+  struct Row {
+    Raw dh[NV], s[NV], dsum[NV];
+    float mean, rstd;
+  };
+  auto fetch = [&](Row &row, int r) {
+    row.mean = p.mean[r], row.rstd = p.rstd[r];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = column(j);
+      if (c >= p.cols) continue;
+      row.dh[j] = *reinterpret_cast<const Raw *>(at<T>(p.dh, r, p.ld_dh) + c);
+      row.s[j] = *reinterpret_cast<const Raw *>(at<T>(p.s, r, p.ld_s) + c);
+      if (p.dsum) row.dsum[j] = *reinterpret_cast<const Raw *>(at<T>(p.dsum, r, p.ld_dsum) + c);
+    }
+  };
+  auto values = [&](const Raw &q, float(&f)[V]) {
+    if constexpr (V == 1) f[0] = Elem<T>::get(q);
+    else unpack<T, V>(q, f);
+  };
+  Raw w[NV];
+  float sum_w[NV][V], sum_b[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (p.w && column(j) < p.cols) w[j] = *reinterpret_cast<const Raw *>(reinterpret_cast<const T *>(p.w) + column(j));
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum_w[j][i] = sum_b[j][i] = 0.f;
+  }
+  Row now;
+  if (AHEAD && (int)blockIdx.x < p.rows) fetch(now, blockIdx.x);
+  for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    Row next;
+    if (!AHEAD) fetch(now, r);
+    else if (r + (int)gridDim.x < p.rows) fetch(next, r + gridDim.x);
+    float v[2] = {0.f, 0.f};
+    auto g_and_n = [&](int j, float(&h)[V], float(&g)[V], float(&n)[V]) {
+      values(now.dh[j], h);
+      values(now.s[j], n);
+      if (p.w) {
+        values(w[j], g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] *= h[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = h[i];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) n[i] = (n[i] - now.mean) * now.rstd;
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (column(j) >= p.cols) continue;
+      float h[V], g[V], n[V];
+      g_and_n(j, h, g, n);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[0] += g[i];
+        v[1] += g[i] * n[i];
+        sum_w[j][i] += h[i] * n[i];
+        sum_b[j][i] += h[i];
+      }
+    }
+    if (p.dx) {
+      group_sums<2>(v, buf, warp, warps, turn);
+      const float mg = v[0] * inv, mgn = v[1] * inv;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (column(j) >= p.cols) continue;
+        float h[V], g[V], n[V];
+        g_and_n(j, h, g, n);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = now.rstd * (g[i] - mg - n[i] * mgn);
+        if (p.dsum) {
+          values(now.dsum[j], h);
+#pragma unroll
+          for (int i = 0; i < V; ++i) g[i] += h[i];
+        }
+        store<T, V>(at<T>(p.dx, r, p.ld_dx) + column(j), g);
+      }
+    }
+    if (AHEAD) now = next;
+  }
+  if (!p.dw && !p.db) return;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (column(j) >= p.cols) continue;
+    float *to = p.ws + (int64_t)blockIdx.x * 2 * p.cols + column(j);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      to[i] = sum_w[j][i];
+      to[p.cols + i] = sum_b[j][i];
+    }
+  }
+}
+
 // dx for rows of any length
 template <typename T, int V>
 __global__ void __launch_bounds__(512) layer_norm_dx_kernel(const Bwd p) {
@@ -271,23 +475,51 @@ static bool vec_ok(std::initializer_list<const void *> ptrs, std::initializer_li
   return cols * es % 16 == 0;
 }
 static int threads_of(int cols, int v) { return std::min(512, std::max(32, (cols / v + 31) / 32 * 32)); }
-// rows' parts of the column sums
+// rows' parts of the column sums in the general kernels
 static int parts_of(int64_t rows, int num_sms) { return (int)std::max<int64_t>(1, std::min<int64_t>((rows + 63) / 64, num_sms)); }
+
+// The one-pass backward: columns a thread (16 in vectors of 16-bit types, whose raw rows take
+// few registers, else 8), threads, and blocks: what the SMs hold, with some rows each
+// so that the partial sums stay few.
+constexpr int FUSED_COLS = 8192;
+struct BwdShape {
+  int threads, blocks;
+};
+static BwdShape bwd_shape(int64_t rows, int cols, int each, int num_sms) {
+  const int threads = (cols + 32 * each - 1) / (32 * each) * 32, resident = (each == 16 ? 512 : 1024) / threads;
+  return {threads, (int)std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, (int64_t)num_sms * std::max(1, std::min(resident, 16))))};
+}
 
 template <typename T, int V>
 static cudaError_t fwd(const Fwd &p, int num_sms, cudaStream_t st) {
-  layer_norm_kernel<T, V><<<std::min(p.rows, num_sms * 8), threads_of(p.cols, V), 0, st>>>(p);
+  constexpr int NV = V == 8 ? 4 : V == 4 ? 8 : 32, EACH = NV * V;  // 32 columns a thread
+  if (p.cols <= 32 * EACH) {
+    const int blocks = (p.rows + 3) / 4;
+    layer_norm_held_kernel<T, V, NV, true><<<blocks, 128, 0, st>>>(p);
+  } else if (p.cols <= 1024 * EACH) {
+    layer_norm_held_kernel<T, V, NV, false><<<p.rows, (p.cols + 32 * EACH - 1) / (32 * EACH) * 32, 0, st>>>(p);
+  } else {
+    layer_norm_kernel<T, V><<<std::min(p.rows, num_sms * 8), threads_of(p.cols, V), 0, st>>>(p);
+  }
   return cudaGetLastError();
 }
 template <typename T, int V>
 static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
+  const bool sums = p.dw || p.db;
+  auto join = [&]() { return launch_pdl(layer_norm_join_kernel<T>, dim3((p.cols + 31) / 32, 2), dim3(1024), 0, st, p); };
+  if (p.cols <= FUSED_COLS) {
+    const BwdShape s = bwd_shape(p.rows, p.cols, V == 8 ? 16 : 8, num_sms);
+    p.parts = s.blocks;
+    layer_norm_bwd_kernel<T, V, V == 1 ? 8 : 2, V == 8><<<s.blocks, s.threads, 0, st>>>(p);
+    const cudaError_t err = cudaGetLastError();
+    return err != cudaSuccess || !sums ? err : join();
+  }
   // (the column sums first: dx may be dh or s)
-  if (p.dw || p.db) {
+  if (sums) {
     p.parts = parts_of(p.rows, num_sms);
     layer_norm_columns_kernel<T, V><<<dim3((p.cols + 32 * V - 1) / (32 * V), p.parts), 32 * SUM_WARPS, 0, st>>>(p);
     cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    err = launch_pdl(layer_norm_join_kernel<T>, dim3((p.cols + 31) / 32, 2), dim3(1024), 0, st, p);
+    if (err == cudaSuccess) err = join();
     if (err != cudaSuccess) return err;
   }
   if (!p.dx) return cudaSuccess;
@@ -298,7 +530,10 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
 }  // namespace layer
 
 size_t layer_norm_workspace(int64_t rows, int cols, int num_sms) {
-  return (size_t)layer::parts_of(rows, num_sms) * 2 * cols * sizeof(float);
+  using namespace layer;
+  int parts = parts_of(rows, num_sms);
+  if (cols <= FUSED_COLS) parts = std::max(bwd_shape(rows, cols, 16, num_sms).blocks, bwd_shape(rows, cols, 8, num_sms).blocks);
+  return (size_t)parts * 2 * cols * sizeof(float);
 }
 
 cudaError_t launch_layer_norm(const sym_layer_norm &a, int num_sms, cudaStream_t st) {
