@@ -362,6 +362,136 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_bwd_kernel(cons
   }
 }
 
+// The same for rows in 16-byte vectors whose tensors fit shared memory four rows deep: two rows
+// at a time, so that both take one block reduction, and the rows after them on their
+// way (cp.async, each thread into its own shared memory: no barrier guards the copies).
+// With one row at a time out of registers a row's chain (read, reduce, finish) bounds it:
+// 8192 x 7168 114 us, NEW so.
+template <typename T, int NV>
+__global__ void __launch_bounds__(512) layer_norm_bwd_staged_kernel(const Bwd p, int pairs, int arrays) {
+  constexpr int V = Elem<T>::VEC;
+  extern __shared__ __align__(16) uint4 rows_smem[];
+  __shared__ float buf[2 * 128];
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, threads = blockDim.x;
+  const float inv = 1.f / p.cols;
+  int turn = 0;
+  auto column = [&](int j) { return ((int)threadIdx.x + j * threads) * V; };
+  // vector j of array a (dh, s, dsum) of row q of pair slot k
+  auto place = [&](int k, int q, int a, int j) { return rows_smem + ((((k * 2 + q) * arrays + a) * NV + j) * threads + threadIdx.x); };
+  int ahead = blockIdx.x, put = 0;
+  const int step = gridDim.x;
+  auto fetch = [&]() {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r = ahead + q * step;
+      if (r >= p.rows) break;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = column(j);
+        if (c >= p.cols) continue;
+        cp_async16(place(put, q, 0, j), at<T>(p.dh, r, p.ld_dh) + c);
+        cp_async16(place(put, q, 1, j), at<T>(p.s, r, p.ld_s) + c);
+        if (arrays > 2) cp_async16(place(put, q, 2, j), at<T>(p.dsum, r, p.ld_dsum) + c);
+      }
+    }
+    cp_async_commit();
+    ahead += 2 * step;
+    put = put + 1 == pairs ? 0 : put + 1;
+  };
+  uint4 w[NV];
+  float sum_w[NV][V], sum_b[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (p.w && column(j) < p.cols) w[j] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.w) + column(j));
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum_w[j][i] = sum_b[j][i] = 0.f;
+  }
+  float mean[2], rstd[2];  // of the next pair
+  auto statistics = [&](int r) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (r + q * step < p.rows) mean[q] = p.mean[r + q * step], rstd[q] = p.rstd[r + q * step];
+  };
+  for (int k = 0; k + 1 < pairs; ++k) fetch();
+  statistics(blockIdx.x);
+  int take = 0;
+  for (int r = blockIdx.x; r < p.rows; r += 2 * step) {
+    fetch();
+    if (pairs == 2) cp_async_wait<1>();
+    else cp_async_wait<2>();
+    const bool two = r + step < p.rows;
+    const float m[2] = {mean[0], mean[1]}, rs[2] = {rstd[0], rstd[1]};
+    statistics(r + 2 * step);
+    auto g_and_n = [&](int q, int j, float(&h)[V], float(&g)[V], float(&n)[V]) {
+      unpack<T, V>(*place(take, q, 0, j), h);
+      unpack<T, V>(*place(take, q, 1, j), n);
+      if (p.w) {
+        unpack<T, V>(w[j], g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] *= h[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = h[i];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) n[i] = (n[i] - m[q]) * rs[q];
+    };
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (q && !two) break;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (column(j) >= p.cols) continue;
+        float h[V], g[V], n[V];
+        g_and_n(q, j, h, g, n);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          v[2 * q] += g[i];
+          v[2 * q + 1] += g[i] * n[i];
+          sum_w[j][i] += h[i] * n[i];
+          sum_b[j][i] += h[i];
+        }
+      }
+    }
+    if (p.dx) {
+      block_sums4(v, buf, warp, warps, turn);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (q && !two) break;
+        const float mg = v[2 * q] * inv, mgn = v[2 * q + 1] * inv;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (column(j) >= p.cols) continue;
+          float h[V], g[V], n[V];
+          g_and_n(q, j, h, g, n);
+#pragma unroll
+          for (int i = 0; i < V; ++i) g[i] = rs[q] * (g[i] - mg - n[i] * mgn);
+          if (arrays > 2) {
+            unpack<T, V>(*place(take, q, 2, j), h);
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[i] += h[i];
+          }
+          store<T, V>(at<T>(p.dx, r + q * step, p.ld_dx) + column(j), g);
+        }
+      }
+    }
+    take = take + 1 == pairs ? 0 : take + 1;
+  }
+  cp_async_wait<0>();
+  if (!p.dw && !p.db) return;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (column(j) >= p.cols) continue;
+    float *to = p.ws + (int64_t)blockIdx.x * 2 * p.cols + column(j);
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      *reinterpret_cast<float4 *>(to + i) = make_float4(sum_w[j][i], sum_w[j][i + 1], sum_w[j][i + 2], sum_w[j][i + 3]);
+      *reinterpret_cast<float4 *>(to + p.cols + i) = make_float4(sum_b[j][i], sum_b[j][i + 1], sum_b[j][i + 2], sum_b[j][i + 3]);
+    }
+  }
+}
+
 // dx for rows of any length
 template <typename T, int V>
 __global__ void __launch_bounds__(512) layer_norm_dx_kernel(const Bwd p) {
@@ -458,6 +588,7 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const Bwd p) {
   pdl_wait();
   float s = 0.f;
   if (c < p.cols)
+#pragma unroll 8
     for (int i = warp; i < p.parts; i += 32) s += p.ws[((int64_t)i * 2 + k) * p.cols + c];
   part[warp][lane] = s;
   __syncthreads();
@@ -490,6 +621,23 @@ static BwdShape bwd_shape(int64_t rows, int cols, int each, int num_sms) {
   return {threads, (int)std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, (int64_t)num_sms * std::max(1, std::min(resident, 16))))};
 }
 
+// The staged form of it: 16 columns a thread, two or three pairs of rows in shared memory
+constexpr int STAGED_SMEM = 220 * 1024;
+struct StagedShape {
+  int threads, blocks, pairs;  // pairs 0: does not fit
+  size_t smem;
+};
+static StagedShape staged_shape(int64_t rows, int cols, int size, int arrays, int num_sms) {
+  StagedShape s = {(cols + 511) / 512 * 32, 0, 0, 0};
+  const size_t pair = (size_t)2 * arrays * s.threads * 16 * size;
+  if (s.threads > 512 || 2 * pair > STAGED_SMEM) return s;
+  const int resident = std::max(1, std::min({512 / s.threads, 16, (int)(STAGED_SMEM / (2 * pair))}));
+  s.pairs = STAGED_SMEM / resident >= 3 * pair + 2048 ? 3 : 2;
+  s.smem = s.pairs * pair;
+  s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>((rows + 7) / 8, (int64_t)num_sms * resident));
+  return s;
+}
+
 template <typename T, int V>
 static cudaError_t fwd(const Fwd &p, int num_sms, cudaStream_t st) {
   constexpr int NV = V == 8 ? 4 : V == 4 ? 8 : 32, EACH = NV * V;  // 32 columns a thread
@@ -507,6 +655,19 @@ template <typename T, int V>
 static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
   const bool sums = p.dw || p.db;
   auto join = [&]() { return launch_pdl(layer_norm_join_kernel<T>, dim3((p.cols + 31) / 32, 2), dim3(1024), 0, st, p); };
+  if constexpr (V > 1) {
+    const int arrays = p.dsum ? 3 : 2;
+    const StagedShape s = staged_shape(p.rows, p.cols, sizeof(T), arrays, num_sms);
+    if (s.pairs) {
+      auto kern = layer_norm_bwd_staged_kernel<T, 16 / V>;
+      cudaError_t err = allow_smem(kern, STAGED_SMEM);
+      if (err != cudaSuccess) return err;
+      p.parts = s.blocks;
+      kern<<<s.blocks, s.threads, s.smem, st>>>(p, s.pairs, arrays);
+      err = cudaGetLastError();
+      return err != cudaSuccess || !sums ? err : join();
+    }
+  }
   if (p.cols <= FUSED_COLS) {
     const BwdShape s = bwd_shape(p.rows, p.cols, V == 8 ? 16 : 8, num_sms);
     p.parts = s.blocks;
@@ -532,7 +693,9 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
 size_t layer_norm_workspace(int64_t rows, int cols, int num_sms) {
   using namespace layer;
   int parts = parts_of(rows, num_sms);
-  if (cols <= FUSED_COLS) parts = std::max(bwd_shape(rows, cols, 16, num_sms).blocks, bwd_shape(rows, cols, 8, num_sms).blocks);
+  for (int size : {2, 4})
+    for (int arrays : {2, 3}) parts = std::max(parts, staged_shape(rows, cols, size, arrays, num_sms).blocks);
+  if (cols <= FUSED_COLS) parts = std::max({parts, bwd_shape(rows, cols, 16, num_sms).blocks, bwd_shape(rows, cols, 8, num_sms).blocks});
   return (size_t)parts * 2 * cols * sizeof(float);
 }
 
