@@ -141,21 +141,27 @@ __global__ void __launch_bounds__(256) squares_kernel(const Call p) {
   }
 }
 // X_SCALE / (|g| + eps) as two factors, the first a power of two that brings the
-// largest g into range; by the whole block of SUMS threads
+// largest g into range; by the whole block of SUMS threads (one of them does what
+// runs in 64 bits: a block's would keep the few units for that busy for microseconds)
 __device__ __forceinline__ float2 normaliser(const double *sums, float eps) {
   __shared__ double part[SUMS / 32];
+  __shared__ float2 f;
   double s = sums[threadIdx.x];
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = s;
   __syncthreads();
-  s = 0;
-  for (int i = 0; i < SUMS / 32; ++i) s += part[i];
-  const double norm = sqrt(s) + (double)eps;
-  if (norm == 0) return make_float2(1.f, 0.f);
-  if (!(norm <= 1.7e308)) return make_float2(1.f, NAN);
-  const int e = max(-126, min(126, -ilogb(norm)));
-  return make_float2(ldexpf(1.f, e), (float)(X_SCALE / ldexp(norm, e)));
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < SUMS / 32; ++i) s += part[i];
+    const double norm = sqrt(s) + (double)eps;
+    f = make_float2(1.f, norm == 0 ? 0.f : NAN);
+    if (norm > 0 && norm <= 1.7e308) {
+      const int e = max(-126, min(126, -ilogb(norm)));
+      f = make_float2(ldexpf(1.f, e), (float)(X_SCALE / ldexp(norm, e)));
+    }
+  }
+  __syncthreads();
+  return f;
 }
 // The first X, grid (groups of rows, matrices).  (What lies past a row's end, up to
 // its pitch, may be written: nothing reads it.)
@@ -221,13 +227,21 @@ __global__ void __launch_bounds__(256) finish_kernel(const Call p, int copy) {
 // ---------------------------------------------------------------------------
 enum Kind { GRAM, POLY, UPDATE };
 constexpr int EPI_WARPS = 8;  // two per TMEM lane quarter, each with half of a tile's columns
-constexpr int BUFS = 2;       // boxes (hi and lo) of an epilogue warp
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
-constexpr int RING = 5;
-constexpr int OPERANDS = A_BYTES + B_BYTES;  // of a stage
-constexpr int BOX = 32 * 64;                 // 32 rows of 32 fp16
+constexpr int BOX = 32 * 64;  // 32 rows of 32 fp16
 constexpr int CTRL = 512;
-constexpr int SMEM = 1024 + RING * OPERANDS + EPI_WARPS * BUFS * 2 * BOX + CTRL;
+// Tiles of 256 columns, or 128 where that leaves a pair of SMs one tile at most.  Such small
+// products' blocks take half of an SM's shared memory and TMEM, so that the next one's
+// start up beside them.
+template <bool SMALL>
+struct Shape {
+  static constexpr int TILE_N = SMALL ? 128 : 256;
+  static constexpr int RING = SMALL ? 3 : 5;
+  static constexpr int BUFS = SMALL ? 1 : 2;  // boxes (hi and lo) of an epilogue warp
+  static constexpr int OPERANDS = A_BYTES + TILE_N / 2 * BK * 2;  // of a stage
+  static constexpr int SMEM = 1024 + RING * OPERANDS + EPI_WARPS * BUFS * 2 * BOX + CTRL;
+};
+static_assert(Shape<true>::SMEM <= 113 * 1024 && Shape<false>::SMEM <= 227 * 1024, "blocks an SM");
 
 struct Maps {
   CUtensorMap a[2], b[2];  // operands: hi, lo
@@ -239,7 +253,6 @@ struct Prod {
   size_t diag_in, diag; // B's and A's diagonals
   int64_t ld;           // of those rows
   int M, N, K, tiles_m, tiles, count, tall;
-  int tile_n;  // columns of a tile: 256, or 128 where that still leaves a pair a tile at most
   int splits, split_kb;  // GRAM: parts of the K axis, K blocks of one (parts: where their sums go)
   size_t parts;
   int passes;  // 1: hi hi;  3: and hi lo, lo hi
@@ -256,7 +269,7 @@ struct Tile {
   int z, i, j, part;
   bool turned;  // also written turned over
 };
-template <int KIND>
+template <int KIND, int TILE_N>
 __device__ __forceinline__ Tile tile_of(const Prod &p, int t) {
   Tile ti;
   ti.part = 0;
@@ -271,7 +284,8 @@ __device__ __forceinline__ Tile tile_of(const Prod &p, int t) {
     ti.i = k - ti.j * p.tiles_m;
     ti.turned = false;
   } else {  // row i of the lower triangle holds squares [i (i + 1) / 2, ...), of one or two tiles
-    const int in_square = 256 / p.tile_n, first = k % in_square;
+    constexpr int in_square = 256 / TILE_N;
+    const int first = k % in_square;
     k /= in_square;
     int i = (int)((sqrtf(8.f * k + 1.f) - 1.f) * 0.5f);
     while (i * (i + 1) / 2 > k) --i;
@@ -288,38 +302,19 @@ __device__ __forceinline__ Tile tile_of(const Prod &p, int t) {
 __device__ __forceinline__ uint4 *box_word(uint8_t *box, int lane, int w) {
   return reinterpret_cast<uint4 *>(box + lane * 64 + ((w ^ ((lane >> 1) & 3)) << 4));
 }
-__device__ __forceinline__ void add_box(uint8_t *box, int lane, float (&x)[32]) {
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    float f[8];
-    unpack<__half, 8>(*box_word(box, lane, w), f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[8 * w + k] += f[k];
-  }
-}
-// v rounded to T; with TWO what is left of it into the second box
-template <typename T, bool TWO>
-__device__ __forceinline__ void put_boxes(uint8_t *box, int lane, const float (&v)[32]) {
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    float f[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = v[8 * w + k];
-    const uint4 hi = pack<T, 8>(f);
-    *box_word(box, lane, w) = hi;
-    if (TWO) {
-      float g[8];
-      unpack<T, 8>(hi, g);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] -= g[k];
-      *box_word(box + BOX, lane, w) = pack<T, 8>(f);
-    }
-  }
+// 8 consecutive fp32 columns of this thread's TMEM lane (as tmem_ld32)
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
 }
 
-template <int KIND, bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+template <int KIND, bool A_MN, bool B_MN, bool SMALL>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 : 1)
     product_kernel(const Prod p, const __grid_constant__ Maps maps) {
+  using S = Shape<SMALL>;
+  constexpr int RING = S::RING, BUFS = S::BUFS, OPERANDS = S::OPERANDS, tile_n = S::TILE_N;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *boxes = smem + (size_t)RING * OPERANDS;
@@ -349,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&maps.b[0]);
   }
   if (wid == 1) {
-    tmem_alloc2(tmem_base_s, TMEM_COLS);
+    tmem_alloc2(tmem_base_s, 2 * tile_n);
     tmem_relinquish2();
   }
   tc_fence_before();
@@ -357,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
-  const int nk = (p.K + BK - 1) / BK, total = p.tiles * p.count * p.splits, tile_n = p.tile_n;
+  const int nk = (p.K + BK - 1) / BK, total = p.tiles * p.count * p.splits;
   pdl_launch_dependents();
   pdl_wait();           // the kernel before this one has written what this one reads,
   fence_proxy_async();  // some of it by plain stores
@@ -372,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const uint32_t full_leader = map_to(rg.full, 0);
       bool ok = true;
       for (int n = 0, t; ok && (t = pair_tile(n, pair_id, npairs)) < total; ++n) {
-        const Tile ti = tile_of<KIND>(p, t);
+        const Tile ti = tile_of<KIND, tile_n>(p, t);
         const int m0 = ti.i * 256 + (int)rank * 128, n0 = ti.j * tile_n + (int)rank * (tile_n / 2);
         int kb0, kb1;
         blocks(ti, kb0, kb1);
@@ -411,9 +406,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int n = 0, t; ok && (t = pair_tile(n, pair_id, npairs)) < total; ++n, b ^= 1) {
         if (!(ok = bar_wait(&acc_empty[b], (ne[b]++ & 1u) ^ 1u, ctl))) break;
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(b * ACC_COLS);
+        const uint32_t d = tmem + (uint32_t)(b * tile_n);
         int kb0, kb1;
-        blocks(tile_of<KIND>(p, t), kb0, kb1);
+        blocks(tile_of<KIND, tile_n>(p, t), kb0, kb1);
         for (int kb = 0; kb < (kb1 - kb0) * p.passes; ++kb) {
           if (!(ok = bar_wait(&rg.full[rg.stage], rg.phase, ctl))) break;
           tc_fence_after();
@@ -443,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int b = 0;
     bool ok = true;
     for (int n = 0, t; ok && (t = pair_tile(n, pair_id, npairs)) < total; ++n, b ^= 1) {
-      const Tile ti = tile_of<KIND>(p, t);
+      const Tile ti = tile_of<KIND, tile_n>(p, t);
       const int row0 = ti.i * 256 + (int)rank * 128 + q * 32, row = row0 + lane, col0 = ti.j * tile_n + share * (tile_n / SHARES);
       const int chunks = row0 < p.M ? min(tile_n / SHARES / 32, (p.N - col0 + 31) / 32) : 0;  // (negative: none)
       char *w = p.work + ti.z * p.stride;
@@ -467,80 +462,106 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         cp_async_commit();
       };
 #pragma unroll
-      for (int c = 0; c < BUFS - 1; ++c) fetch(c);
+      for (int c = 0; c < max(1, BUFS - 1); ++c) fetch(c);
       // the next box's columns' diagonal elements, one a lane (padded to whole boxes)
       float d_next = by_column && chunks > 0 ? diag_in[col0 + lane] : 0.f;
       const float d_row = KIND != GRAM && row < p.M && !(KIND == UPDATE && p.tall) ? diag_in[row] : 0.f;
       if (!(ok = __all_sync(0xffffffffu, bar_wait(&acc_full[b], used[b]++ & 1u, ctl)))) break;
       tc_fence_after();
-      const uint32_t acc = lanes + (uint32_t)(b * ACC_COLS + share * (tile_n / SHARES));
+      const uint32_t acc = lanes + (uint32_t)(b * tile_n + share * (tile_n / SHARES));
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const int col = col0 + 32 * c;
         uint8_t *box = my_boxes + (boxno + c) % BUFS * 2 * BOX;
         const float d_col = d_next;
         if (by_column && c + 1 < chunks) d_next = diag_in[col + 32 + lane];
-        uint32_t v[32];
-        float x[32];
-        tmem_ld32(acc + 32 * c, v);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = 0.f;
         if (KIND != GRAM) {
-          fetch(c + BUFS - 1);
+          if (BUFS > 1 || c > 0) fetch(c + BUFS - 1);
           cp_async_wait<BUFS - 1>();
           __syncwarp();
-          add_box(box, lane, x);
-          if (two_in) add_box(box + BOX, lane, x);
-        }
-        tmem_ld_wait();
-        if (KIND == GRAM && p.splits > 1) {  // a part's sums, for join_kernel
-          if (row < p.M) {
-            float *to = reinterpret_cast<float *>(w + p.parts) + ((int64_t)ti.part * p.M + row) * p.ld + col;
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4 *>(to + k) = make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]),
-                                                                __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-          }
-          continue;
-        }
-        if (KIND == GRAM) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]) * (A_SCALE / (X_SCALE * X_SCALE));
-        } else if (KIND == POLY) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            x[k] = (p.b + p.c * (d_row + __shfl_sync(0xffffffffu, d_col, k))) * (x[k] * (B_SCALE / A_SCALE)) +
-                   p.c * (__uint_as_float(v[k]) * (B_SCALE / (A_SCALE * A_SCALE)));
-        } else if (p.tall) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            x[k] = (p.a + __shfl_sync(0xffffffffu, d_col, k)) * x[k] + __uint_as_float(v[k]) * (1.f / B_SCALE);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = (p.a + d_row) * x[k] + __uint_as_float(v[k]) * (1.f / B_SCALE);
-        }
-        if (KIND != UPDATE && row0 == col) {  // 32 elements of the diagonal, one for each lane
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (k == lane) {
-              // (POLY: A's own part of x is zero here)
-              if (row < p.M)
-                diag[row] = KIND == GRAM ? x[k] * (1.f / A_SCALE)
-                                         : d_row * (p.b + p.c * d_row) + x[k] * (1.f / B_SCALE);
-              x[k] = 0.f;
-            }
         }
         const bool users = KIND == UPDATE && p.last;
-        if (users) {
+        // Eight columns at a time in a loop that is not unrolled: a tile runs this code a few
+        // times, and small products are bound by its way to the SM (with 32 columns unrolled the
+        // three kernels of a step took 7.6 us each for one 64 x 64 tile, now 4.6).
+#pragma unroll 1
+        for (int o = 0; o < 4; ++o) {
+          uint32_t v[8];
+          float x[8];
+          tmem_ld8(acc + 32 * c + 8 * o, v);
+          uint4 *const hi_word = box_word(box, lane, o), *const lo_word = box_word(box + BOX, lane, o);
+          if (KIND != GRAM) {
+            unpack<__half, 8>(*hi_word, x);
+            if (two_in) {
+              float l[8];
+              unpack<__half, 8>(*lo_word, l);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] *= p.scale / X_SCALE;
-          if (p.last == 1) put_boxes<__nv_bfloat16, false>(box, lane, x);
-          else put_boxes<__half, false>(box, lane, x);
-        } else if (two_out) {
-          put_boxes<__half, true>(box, lane, x);
-        } else {
-          put_boxes<__half, false>(box, lane, x);
+              for (int k = 0; k < 8; ++k) x[k] += l[k];
+            }
+          }
+          tmem_ld_wait();
+          const int at = col + 8 * o;
+          if (KIND == GRAM && p.splits > 1) {  // a part's sums, for join_kernel
+            if (row < p.M) {
+              float *to = reinterpret_cast<float *>(w + p.parts) + ((int64_t)ti.part * p.M + row) * p.ld + at;
+#pragma unroll
+              for (int k = 0; k < 8; k += 4)
+                *reinterpret_cast<float4 *>(to + k) = make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]),
+                                                                  __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+            }
+            continue;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float sum = __uint_as_float(v[k]);
+            const float d = by_column ? __shfl_sync(0xffffffffu, d_col, 8 * o + k) : 0.f;
+            if (KIND == GRAM) x[k] = sum * (A_SCALE / (X_SCALE * X_SCALE));
+            else if (KIND == POLY)
+              x[k] = (p.b + p.c * (d_row + d)) * (x[k] * (B_SCALE / A_SCALE)) + p.c * (sum * (B_SCALE / (A_SCALE * A_SCALE)));
+            else x[k] = (p.a + (p.tall ? d : d_row)) * x[k] + sum * (1.f / B_SCALE);
+          }
+          if (KIND != UPDATE && row0 == col) {  // 32 elements of the diagonal, one for each lane
+            float own = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (8 * o + k == lane) {
+                own = x[k];
+                x[k] = 0.f;
+              }
+            // (POLY: A's own part of x is zero here)
+            if (lane / 8 == o && row < p.M)
+              diag[row] = KIND == GRAM ? own * (1.f / A_SCALE) : d_row * (p.b + p.c * d_row) + own * (1.f / B_SCALE);
+          }
+          if (users) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] *= p.scale / X_SCALE;
+            *hi_word = p.last == 1 ? pack<__nv_bfloat16, 8>(x) : pack<__half, 8>(x);
+            continue;
+          }
+          const uint4 hi = pack<__half, 8>(x);
+          uint4 lo = make_uint4(0u, 0u, 0u, 0u);
+          *hi_word = hi;
+          if (two_out) {
+            float h[8];
+            unpack<__half, 8>(hi, h);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] -= h[k];
+            lo = pack<__half, 8>(x);
+            *lo_word = lo;
+          }
+          if (ti.turned && row < p.M) {  // turned over: a warp's lanes side by side
+            const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+            uint16_t *th = reinterpret_cast<uint16_t *>(w + p.out[0]) + at * p.ld + row;
+            uint16_t *tl = reinterpret_cast<uint16_t *>(w + p.out[1]) + at * p.ld + row;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (at + k < p.N) {
+                th[k * p.ld] = (uint16_t)(hw[k / 2] >> (16 * (k & 1)));
+                if (two_out) tl[k * p.ld] = (uint16_t)(lw[k / 2] >> (16 * (k & 1)));
+              }
+          }
         }
+        if (KIND == GRAM && p.splits > 1) continue;
         __syncwarp();
         if (!users) {  // (whole words: rows' pitches are whole boxes)
           const int64_t at = (int64_t)(row0 + r8) * p.ld + col + 8 * w4;
@@ -564,17 +585,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 *reinterpret_cast<const uint16_t *>(box + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
         }
         __syncwarp();  // the box has been read
-        if (ti.turned && row < p.M) {  // turned over: a warp's lanes side by side
-          uint16_t *hi = reinterpret_cast<uint16_t *>(w + p.out[0]) + col * p.ld + row;
-          uint16_t *lo = reinterpret_cast<uint16_t *>(w + p.out[1]) + col * p.ld + row;
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (col + k < p.N) {
-              const uint16_t h = to_half(x[k]);
-              hi[k * p.ld] = h;
-              if (two_out) lo[k * p.ld] = to_half(x[k] - widen(true, h));
-            }
-        }
       }
       boxno += (uint32_t)max(chunks, 0);
       give_back(&acc_empty[b], rank, lane);
@@ -587,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __syncwarp();
   cluster_sync();
   tc_fence_after();
-  if (wid == 1) tmem_dealloc2(tmem, TMEM_COLS);
+  if (wid == 1) tmem_dealloc2(tmem, 2 * tile_n);
 }
 
 // A Gram matrix of its parts, grid (rows, matrices)
@@ -605,6 +615,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Prod p) {
   };
   for (int j = threadIdx.x; j < end; j += 128) {
     float v = 0.f;
+#pragma unroll 8
     for (int k = 0; k < p.splits; ++k) v += part[((int64_t)k * p.M + i) * p.ld + j];
     float x = v * (A_SCALE / (X_SCALE * X_SCALE));
     if (i == j) {
@@ -617,13 +628,23 @@ __global__ void __launch_bounds__(128) join_kernel(const Prod p) {
 }
 
 // A launch that may begin while the kernel before it ends
-template <typename Kern, typename... Args>
-static cudaError_t launch_product(Kern kern, int num_sms, cudaStream_t st, const Args &...args) {
+template <int KIND, bool A_MN, bool B_MN, bool SMALL>
+static cudaError_t launch_product(int num_sms, cudaStream_t st, const Prod &p, const Maps &maps) {
+  constexpr int SMEM = Shape<SMALL>::SMEM;
+  auto kern = product_kernel<KIND, A_MN, B_MN, SMALL>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (err != cudaSuccess) return err;
-  const int grid = 2 * max_resident_pairs((const void *)kern, THREADS, SMEM, num_sms);
-  if (grid <= 0) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kern, dim3(grid), dim3(THREADS), SMEM, st, args...);
+  // No more pairs than tiles: the next kernel's blocks find room sooner.  (All large
+  // products have the same shared memory and threads: one of them is asked for its resident pairs.)
+  const int pairs = SMALL ? num_sms / 2
+                          : max_resident_pairs((const void *)product_kernel<POLY, false, false, false>, THREADS, SMEM, num_sms);
+  const int64_t tiles = (int64_t)p.tiles * p.count * p.splits;
+  if (pairs <= 0) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kern, dim3(2 * (unsigned)std::min<int64_t>(pairs, tiles)), dim3(THREADS), SMEM, st, p, maps);
+}
+template <int KIND, bool A_MN, bool B_MN>
+static cudaError_t launch_product(bool small, int num_sms, cudaStream_t st, const Prod &p, const Maps &maps) {
+  return small ? launch_product<KIND, A_MN, B_MN, true>(num_sms, st, p, maps) : launch_product<KIND, A_MN, B_MN, false>(num_sms, st, p, maps);
 }
 
 }  // namespace orth
@@ -687,10 +708,9 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
     q.user = reinterpret_cast<char *>(p.out), q.user_stride = o.out_stride, q.user_ld = o.ld_out;
     const int tm = (m + 255) / 256, pairs = num_sms / 2;
     const int squares = tm * (tm + 1) / 2, tr = (p.rows + 255) / 256;
-    // 128 columns a tile where that leaves a pair one tile at most (a tile of 256 by
-    // itself is bound by what its pair of SMs can take in)
-    const int sq_n = 2 * squares * (int)n <= pairs ? 128 : 256;
-    const int up_n = (int64_t)tr * ((p.cols + 127) / 128) * n <= pairs ? 128 : 256;
+    // which products are small (Shape)
+    const bool sq_small = (int64_t)2 * squares * n <= pairs, up_small = (int64_t)tr * ((p.cols + 127) / 128) * n <= pairs;
+    const int sq_n = sq_small ? 128 : 256, up_n = up_small ? 128 : 256;
     const int sq_tiles = squares * (256 / sq_n), up_tiles = tr * ((p.cols + up_n - 1) / up_n);
     const int nk = (std::max(p.rows, p.cols) + BK - 1) / BK;
     int splits = std::max(1, std::min(l.splits, pairs / (sq_tiles * (int)std::min<unsigned>(n, 4096))));
@@ -716,25 +736,25 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
     for (int i = 0; i < o.steps; ++i) {
       const int k = i & 1;
       q.passes = o.out_dtype == SYM_FP16 && i >= o.steps - PRECISE_STEPS ? 3 : 1;
-      q.M = q.N = m, q.K = std::max(p.rows, p.cols), q.tiles_m = tm, q.tiles = sq_tiles, q.tile_n = sq_n;
+      q.M = q.N = m, q.K = std::max(p.rows, p.cols), q.tiles_m = tm, q.tiles = sq_tiles;
       q.diag = l.diag_a, q.out[0] = l.a, q.out[1] = a_lo, q.ld = l.ld_a;
       q.splits = splits, q.split_kb = split_kb, q.parts = l.parts;
-      err = p.tall ? launch_product(product_kernel<GRAM, true, true>, num_sms, st, q, gram[k])
-                   : launch_product(product_kernel<GRAM, false, false>, num_sms, st, q, gram[k]);
+      err = p.tall ? launch_product<GRAM, true, true>(sq_small, num_sms, st, q, gram[k])
+                   : launch_product<GRAM, false, false>(sq_small, num_sms, st, q, gram[k]);
       if (err == cudaSuccess && splits > 1) err = launch_pdl(join_kernel, dim3(m, n), dim3(128), 0, st, q);
       if (err != cudaSuccess) return err;
       q.splits = 1, q.split_kb = 1 << 30;
       q.K = m, q.diag_in = l.diag_a, q.diag = l.diag_b;
       q.in[0] = l.a, q.in[1] = a_lo, q.out[0] = l.b, q.out[1] = b_lo;
-      err = launch_product(product_kernel<POLY, false, false>, num_sms, st, q, poly);
+      err = launch_product<POLY, false, false>(sq_small, num_sms, st, q, poly);
       if (err != cudaSuccess) return err;
       q.M = p.rows, q.N = p.cols, q.diag_in = l.diag_b;
-      q.tiles_m = tr, q.tiles = up_tiles, q.tile_n = up_n;
+      q.tiles_m = tr, q.tiles = up_tiles;
       q.last = i + 1 < o.steps ? 0 : o.out_dtype == SYM_BF16 ? 1 : 2, q.vec = user_vec;
       q.in[0] = l.hi + k * l.x_bytes, q.in[1] = l.lo + k * l.x_bytes, q.ld = l.ld_x;
       q.out[0] = l.hi + (k ^ 1) * l.x_bytes, q.out[1] = l.lo + (k ^ 1) * l.x_bytes;
-      err = p.tall ? launch_product(product_kernel<UPDATE, false, false>, num_sms, st, q, update[k])
-                   : launch_product(product_kernel<UPDATE, false, true>, num_sms, st, q, update[k]);
+      err = p.tall ? launch_product<UPDATE, false, false>(up_small, num_sms, st, q, update[k])
+                   : launch_product<UPDATE, false, true>(up_small, num_sms, st, q, update[k]);
       if (err != cudaSuccess) return err;
       q.last = 0;
     }
