@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -162,12 +163,12 @@ def lib() -> ctypes.CDLL:
         L.moe_block_norm.argtypes = [P(SymBlockNorm), _vp]
         L.moe_block_norm_bwd.argtypes = [P(SymBlockNorm), P(SymBlockNormGrad), _vp]
         L.moe_block_norm_workspace.argtypes = [_i64, _i32, _i64, P(_u64)]
-        L.moe_layer_norm.argtypes = [P(SymLayerNorm), _vp]
-        L.moe_layer_norm_bwd.argtypes = [P(SymLayerNormGrad), _vp]
+        L.moe_layer_norm.argtypes = [_vp, _vp]
+        L.moe_layer_norm_bwd.argtypes = [_vp, _vp]
         L.moe_layer_norm_workspace.argtypes = [_i64, _i32, P(_u64)]
-        L.moe_orthogonalize.argtypes = [P(SymOrthogonalize), _vp]
+        L.moe_orthogonalize.argtypes = [_vp, _vp]
         L.moe_orthogonalize_workspace.argtypes = [_i32, _i32, _i32, P(_u64), P(_u64)]
-        L.moe_few_tokens.argtypes = [P(SymFewTokens), _vp]
+        L.moe_few_tokens.argtypes = [_vp, _vp]
         L.moe_few_tokens_workspace.argtypes = [_i32, _i32, _i32, P(_u64)]
         L.sym_strerror.argtypes = [ctypes.c_int]
         L.sym_strerror.restype = ctypes.c_char_p
@@ -595,23 +596,91 @@ def moe_block_norm_bwd(dy=None, dh=None, y=None, o=None, w_post=None, gate=None,
 
 
 # ------------------------------------------------------------------ layer norm
+# These calls are also made for single tokens, where they cost the host more than
+# the GPU: every attribute is read once, texts are made only for an error, and the
+# argument struct is packed into bytes (a ctypes struct takes several times that).
+
+def _packer(cls):
+    codes = {_i32: "i", _u32: "I", _i64: "q", _u64: "Q", ctypes.c_float: "f", ctypes.c_float * 3: "3f"}
+    s = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_))
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_layer_norm, _pack_layer_norm_grad = _packer(SymLayerNorm), _packer(SymLayerNormGrad)
+_pack_orthogonalize, _pack_few_tokens = _packer(SymOrthogonalize), _packer(SymFewTokens)
+
+
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _at(t, shape: tuple, dtype, dev: int, where: str) -> int:
+    """The address of a tensor of this shape and type on the device; 0 for none."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _need(False, where, "tensors of the current CUDA device are wanted")
+    if t.shape != shape or t.dtype != dtype:
+        _need(False, where, f"{list(shape)} {dtype} is wanted, not {list(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def _mat(t, shape: tuple, dtype, dev: int, where: str):
+    """(address, elements between rows) of a matrix, whose columns are side by side."""
+    if t is None:
+        return 0, 0
+    p = _at(t, shape, dtype, dev, where)
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        _need(False, where, "rows have to be contiguous")
+    return p, (ld if shape[0] > 1 else (shape[1] + 7) // 8 * 8)
+
+
+def _line(t, n: int, dtype, dev: int, where: str) -> int:
+    p = _at(t, (n,), dtype, dev, where)
+    if p and n > 1 and t.stride()[0] != 1:
+        _need(False, where, "vectors have to be contiguous")
+    return p
+
+
+def _work(work, dev: int, where: str):
+    if work is None:
+        return 0, 0
+    if not isinstance(work, torch.Tensor) or work.get_device() != dev or not work.is_contiguous():
+        _need(False, where, "work is a contiguous tensor of the current CUDA device")
+    return work.data_ptr(), work.numel() * work.element_size()
+
+
+def _word(t, dev: int, where: str) -> int:
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != torch.int32 or t.numel() < 1:
+        _need(False, where, "status is an int32 word of the current CUDA device")
+    return t.data_ptr()
+
+
+def _is_matrix(t, where: str) -> None:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        _need(False, where, "a tensor [rows, cols] is wanted")
+
 
 def moe_layer_norm(x, h=None, w=None, b=None, add=None, sum=None, mean=None, rstd=None, eps: float = 1e-5,
                    stream=None) -> None:
     """h = (s - mean) * rstd * w + b over the rows [R, C] of s = x + add (or x);
     sum takes s.  mean, rstd: float32 [R], kept for the backward."""
     where = "moe_layer_norm"
-    dev = _on_device(where, x, h, w, b, add, sum, mean, rstd)
-    _need(x.dim() == 2, where, "x is [rows, cols]")
-    (rows, cols), dt = x.shape, x.dtype
-    xp, xl = _plain(x, rows, cols, dt, where)
-    ap, al = _plain(add, rows, cols, dt, where)
-    sp, sl = _plain(sum, rows, cols, dt, where)
-    hp, hl = _plain(h, rows, cols, dt, where)
-    a = SymLayerNorm(rows, cols, _DTYPES.get(dt, -1), xp, ap, _vector(w, cols, dt, where), _vector(b, cols, dt, where), sp,
-                     hp, _vector(mean, rows, torch.float32, where), _vector(rstd, rows, torch.float32, where), xl, al, sl,
-                     hl, eps, 0)
-    _check(lib().moe_layer_norm(ctypes.byref(a), _stream_of(stream, dev)), where)
+    _is_matrix(x, where)
+    dev, dt, shape = _device(), x.dtype, x.shape
+    rows, cols = shape
+    f32 = torch.float32
+    xp, xl = _mat(x, shape, dt, dev, where)
+    ap, al = _mat(add, shape, dt, dev, where)
+    sp, sl = _mat(sum, shape, dt, dev, where)
+    hp, hl = _mat(h, shape, dt, dev, where)
+    a = _pack_layer_norm(rows, cols, _DTYPES.get(dt, -1), xp, ap, _line(w, cols, dt, dev, where), _line(b, cols, dt, dev, where),
+                         sp, hp, _line(mean, rows, f32, dev, where), _line(rstd, rows, f32, dev, where), xl, al, sl, hl, eps, 0)
+    _check(lib().moe_layer_norm(a, _stream_of(stream, dev)), where)
 
 
 def moe_layer_norm_workspace(rows: int, cols: int) -> int:
@@ -621,41 +690,35 @@ def moe_layer_norm_workspace(rows: int, cols: int) -> int:
     return out.value
 
 
-def _work(work, where: str):
-    if work is None:
-        return 0, 0
-    _need(work.is_contiguous(), where, "work is contiguous")
-    return work.data_ptr(), work.numel() * work.element_size()
-
-
 def moe_layer_norm_bwd(dh, s, mean, rstd, dx=None, w=None, dsum=None, dw=None, db=None, work=None, stream=None) -> None:
     """Gradients of moe_layer_norm from dh (of h) and dsum (of s, from elsewhere),
     with the forward's s, mean and rstd.  Every output may be left out.  work (for
     dw and db): a uint8 tensor of moe_layer_norm_workspace bytes."""
     where = "moe_layer_norm_bwd"
-    dev = _on_device(where, dh, s, mean, rstd, dx, w, dsum, dw, db, work)
-    _need(dh is not None and dh.dim() == 2 and s is not None, where, "dh and s, [rows, cols], are wanted")
-    (rows, cols), dt = dh.shape, dh.dtype
-    hp, hl = _plain(dh, rows, cols, dt, where)
-    sp, sl = _plain(s, rows, cols, dt, where)
-    dp, dl = _plain(dsum, rows, cols, dt, where)
-    xp, xl = _plain(dx, rows, cols, dt, where)
-    wp, wn = _work(work, where)
-    a = SymLayerNormGrad(rows, cols, _DTYPES.get(dt, -1), hp, sp, dp, _vector(w, cols, dt, where),
-                         _vector(mean, rows, torch.float32, where), _vector(rstd, rows, torch.float32, where), xp,
-                         _vector(dw, cols, dt, where), _vector(db, cols, dt, where), hl, sl, dl, xl, wp, wn)
-    _check(lib().moe_layer_norm_bwd(ctypes.byref(a), _stream_of(stream, dev)), where)
+    _is_matrix(dh, where)
+    dev, dt, shape = _device(), dh.dtype, dh.shape
+    rows, cols = shape
+    f32 = torch.float32
+    hp, hl = _mat(dh, shape, dt, dev, where)
+    sp, sl = _mat(s, shape, dt, dev, where)
+    gp, gl = _mat(dsum, shape, dt, dev, where)
+    xp, xl = _mat(dx, shape, dt, dev, where)
+    wp, wn = _work(work, dev, where)
+    a = _pack_layer_norm_grad(rows, cols, _DTYPES.get(dt, -1), hp, sp, gp, _line(w, cols, dt, dev, where),
+                              _line(mean, rows, f32, dev, where), _line(rstd, rows, f32, dev, where), xp,
+                              _line(dw, cols, dt, dev, where), _line(db, cols, dt, dev, where), hl, sl, gl, xl, wp, wn)
+    _check(lib().moe_layer_norm_bwd(a, _stream_of(stream, dev)), where)
 
 
 # ------------------------------------------------------------------ updates of the experts' matrices
 
 def _batch(t, where: str):
-    """(matrices, rows, columns, stride of a matrix, of a row) of [F, C] or [E, F, C]."""
-    _need(t.dim() in (2, 3), where, "matrices [F, C] or [E, F, C] are wanted")
-    count = t.shape[0] if t.dim() == 3 else 1
-    f, c = t.shape[-2:]
-    _need(c <= 1 or t.stride(-1) == 1, where, "the last dimension has to be contiguous")
-    return count, f, c, (t.stride(0) if count > 1 else f * c), (t.stride(-2) if f > 1 else c)
+    """(stride of a matrix, of a row) of [F, C] or [E, F, C]."""
+    shape, stride = t.shape, t.stride()
+    f, c = shape[-2:]
+    if c > 1 and stride[-1] != 1:
+        _need(False, where, "the last dimension has to be contiguous")
+    return (stride[0] if len(shape) == 3 and shape[0] > 1 else f * c), (stride[-2] if f > 1 else c)
 
 
 def moe_orthogonalize_workspace(count: int, rows: int, cols: int, least: bool = False) -> int:
@@ -673,17 +736,17 @@ def moe_orthogonalize(g, out, work, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0
     [E, F, C] (bf16, fp16 or float32; out bf16 or fp16).  work: a uint8 tensor; status: an
     int32 word that SYM_STATUS_TIMEOUT is set in if an internal wait runs out."""
     where = "moe_orthogonalize"
-    dev = _on_device(where, g, out, work, status)
-    _need(status is None or (status.dtype == torch.int32 and status.numel() >= 1), where, "status is an int32 word")
-    _need(g.shape == out.shape, where, "g and out have one shape")
-    _need(len(coeffs) == 3, where, "three coefficients are wanted")
-    count, f, c, gs, gl = _batch(g, where)
-    os_, ol = _batch(out, where)[3:]
-    wp, wn = _work(work, where)
-    a = SymOrthogonalize(count, f, c, steps, _DTYPES.get(g.dtype, -1), _DTYPES.get(out.dtype, -1),
-                         (ctypes.c_float * 3)(*coeffs), eps, scale, 0,
-                         0 if status is None else status.data_ptr(), g.data_ptr(), out.data_ptr(), gs, gl, os_, ol, wp, wn)
-    _check(lib().moe_orthogonalize(ctypes.byref(a), _stream_of(stream, dev)), where)
+    if not isinstance(g, torch.Tensor) or not isinstance(out, torch.Tensor) or g.dim() not in (2, 3) or len(coeffs) != 3:
+        _need(False, where, "tensors [F, C] or [E, F, C] and three coefficients are wanted")
+    dev, shape = _device(), g.shape
+    gp, op = _at(g, shape, g.dtype, dev, where), _at(out, shape, out.dtype, dev, where)
+    gs, gl = _batch(g, where)
+    os_, ol = _batch(out, where)
+    wp, wn = _work(work, dev, where)
+    a = _pack_orthogonalize(shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], steps, _DTYPES.get(g.dtype, -1),
+                            _DTYPES.get(out.dtype, -1), *coeffs, eps, scale, 0, _word(status, dev, where), gp, op, gs, gl, os_, ol,
+                            wp, wn)
+    _check(lib().moe_orthogonalize(a, _stream_of(stream, dev)), where)
 
 
 # ------------------------------------------------------------------ a few tokens
@@ -695,31 +758,41 @@ def moe_few_tokens_workspace(tokens: int, inter: int, topk: int) -> int:
     return out.value
 
 
+def _experts(t, shape: tuple, dtype, dev: int, where: str):
+    """(address, stride of an expert, of a row) of one matrix for each expert."""
+    p = _at(t, shape, dtype, dev, where)
+    group, ld, inner = t.stride()
+    if inner != 1 and shape[2] > 1:
+        _need(False, where, "rows have to be contiguous")
+    return p, group, (ld if shape[1] > 1 else (shape[2] + 7) // 8 * 8)
+
+
 def moe_few_tokens(x, w_gate, w_up, w_down, logits, idx, w, out, work, w_router=None, stream=None) -> None:
     """A whole MoE layer for up to 32 tokens x [T, H]: logits [T, E] (float32; made
     from w_router [E, H] where that is given), idx and w [T, k] of each token's k
     experts, out = their SwiGLU's sum.  w_gate, w_up [E, I, H], w_down [E, H, I];
     bf16 or fp16.  work: a uint8 tensor of moe_few_tokens_workspace bytes."""
     where = "moe_few_tokens"
-    dev = _on_device(where, x, w_gate, w_up, w_down, logits, idx, w, out, work, w_router)
-    _need(x.dim() == 2 and logits.dim() == 2 and idx.dim() == 2 and w_gate.dim() == 3, where,
-          "x [T, H], logits [T, E], idx [T, k] and w_gate [E, I, H] are wanted")
-    (tokens, hidden), experts, topk, inter, dt = x.shape, logits.shape[1], idx.shape[1], w_gate.shape[1], x.dtype
-    xp, xl = _plain(x, tokens, hidden, dt, where)
-    op, ol = _plain(out, tokens, hidden, dt, where)
-    for t, n, kind in ((logits, experts, torch.float32), (idx, topk, torch.int32), (w, topk, torch.float32)):
-        _need(t.shape == (tokens, n) and t.dtype == kind and t.is_contiguous(), where,
-              f"[{tokens}, {n}] {kind}, contiguous, is wanted")
-    _need(w_gate.dtype == dt and w_up.dtype == dt and w_down.dtype == dt, where, "x and the weights have one type")
-    gg, gl = _matrices(w_gate, experts, (inter, hidden), where)
-    ug, ul = _matrices(w_up, experts, (inter, hidden), where)
-    dg, dl = _matrices(w_down, experts, (hidden, inter), where)
-    rp, rl = _plain(w_router, experts, hidden, dt, where)
-    wp, wn = _work(work, where)
-    a = SymFewTokens(tokens, hidden, inter, experts, topk, _DTYPES.get(dt, -1), xp, w_gate.data_ptr(), w_up.data_ptr(),
-                     w_down.data_ptr(), rp, logits.data_ptr(), idx.data_ptr(), w.data_ptr(), op, xl, ol, gg, gl, ug, ul, dg,
-                     dl, rl, wp, wn)
-    _check(lib().moe_few_tokens(ctypes.byref(a), _stream_of(stream, dev)), where)
+    _is_matrix(x, where)
+    _is_matrix(logits, where)
+    _is_matrix(idx, where)
+    if not all(isinstance(t, torch.Tensor) for t in (w_gate, w_up, w_down, w, out, work)) or w_gate.dim() != 3:
+        _need(False, where, "tensors w_gate, w_up [E, I, H], w_down, w, out and work are wanted")
+    dev, dt, shape, f32 = _device(), x.dtype, x.shape, torch.float32
+    (tokens, hidden), experts, chosen, inter = shape, logits.shape[1], idx.shape, w_gate.shape[1]
+    gp, gg, gl = _experts(w_gate, (experts, inter, hidden), dt, dev, where)
+    up, ug, ul = _experts(w_up, (experts, inter, hidden), dt, dev, where)
+    dp, dg, dl = _experts(w_down, (experts, hidden, inter), dt, dev, where)
+    wp, wn = _work(work, dev, where)
+    if chosen[0] != tokens or not (logits.is_contiguous() and idx.is_contiguous() and w.is_contiguous()):
+        _need(False, where, "logits [T, E], idx [T, k] and w [T, k] are contiguous")
+    xp, xl = _mat(x, shape, dt, dev, where)
+    op, ol = _mat(out, shape, dt, dev, where)
+    rp, rl = _mat(w_router, (experts, hidden), dt, dev, where)
+    a = _pack_few_tokens(tokens, hidden, inter, experts, chosen[1], _DTYPES.get(dt, -1), xp, gp, up, dp, rp,
+                         _at(logits, (tokens, experts), f32, dev, where), _at(idx, chosen, torch.int32, dev, where),
+                         _at(w, chosen, f32, dev, where), op, xl, ol, gg, gl, ug, ul, dg, dl, rl, wp, wn)
+    _check(lib().moe_few_tokens(a, _stream_of(stream, dev)), where)
 
 
 # ------------------------------------------------------------------ heap owner
