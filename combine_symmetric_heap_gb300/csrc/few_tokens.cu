@@ -361,6 +361,30 @@ struct Stream {
     }
   }
 };
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// all threads of the cluster's blocks
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// the same variable of the cluster's block `rank`
+__device__ __forceinline__ float load_from(const float *p, int rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(smem_u32(p)), "r"(rank)
+               : "memory");
+  return v;
+}
+
 // (asm: the warps come to it from several places in the code)
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
 
@@ -369,7 +393,7 @@ __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0;" ::: "m
 // rows are the product's rows 0..7 and their up rows 8..15, so that a lane ends
 // with both of a feature.
 // ---------------------------------------------------------------------------
-constexpr int UP_FEATURES = 8, DOWN_FEATURES = 16;
+constexpr int UP_FEATURES = 8, DOWN_FEATURES = 16, MOST_CLUSTER = 8;
 
 // This block's features of all live experts, counted through; `MOST` rows at a time
 template <int MOST>
@@ -446,36 +470,41 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) up_kernel(const Args p) {
 }
 
 // ---------------------------------------------------------------------------
-// out = sum of w h Wd^T.  A block takes a run of features, 16 at a time, through all live
-// experts; every warp adds its part of the contraction to sums of its own for each
-// token, joined at the end in the warps' order.  The product's columns are four rows
-// of h's hi and the same four of lo, for each eight of NB.
+// out = sum of w h Wd^T.  A cluster of blocks takes a run of features, 16 at a time, and
+// each of its blocks every size-th live expert; every warp adds its part of the
+// contraction to sums of its own for each token, joined at the end in the warps' and
+// the blocks' order (distributed shared memory).  One block a cluster where the features
+// alone keep the SMs busy; with fewer of them a block's way through all experts
+// bounds the call (7 tokens, 24 experts of 1032 x 520: the layer 32 us, 27 with four blocks a cluster).
+// The product's columns are four rows of h's hi and the same four of lo, for each eight of NB.
 // ---------------------------------------------------------------------------
 template <int MOST>
 struct DownTiles {
   const Args &p;
   const Routes &r;
-  int begin, features, tiles, i;
+  int begin, features, tiles, rank, size, i;
   int f, nf, l, first, n;  // feature, features, expert's slot, first row, rows
-  __device__ DownTiles(const Args &p_, const Routes &r_) : p(p_), r(r_), i(0), l(0) {
-    begin = (int)((int64_t)p.H * blockIdx.x / gridDim.x);
-    features = (int)((int64_t)p.H * (blockIdx.x + 1) / gridDim.x) - begin;
-    tiles = r.experts > 0 ? (features + DOWN_FEATURES - 1) / DOWN_FEATURES : 0;
+  __device__ DownTiles(const Args &p_, const Routes &r_, int rank_, int size_) : p(p_), r(r_), rank(rank_), size(size_), i(0), l(rank_) {
+    const int cluster = blockIdx.x / size, clusters = gridDim.x / size;
+    begin = (int)((int64_t)p.H * cluster / clusters);
+    features = (int)((int64_t)p.H * (cluster + 1) / clusters) - begin;
+    tiles = (features + DOWN_FEATURES - 1) / DOWN_FEATURES;
     open();
   }
-  __device__ __forceinline__ bool live() const { return i < tiles; }
+  __device__ __forceinline__ bool live() const { return i < tiles && rank < r.experts; }
+  __device__ __forceinline__ void cut() { f = begin + features * i / tiles, nf = begin + features * (i + 1) / tiles - f; }  // evenly
   __device__ __forceinline__ void open() {
     if (!live()) return;
-    f = begin + features * i / tiles, nf = begin + features * (i + 1) / tiles - f;  // cut evenly
+    cut();
     first = r.first[l];
     n = min(MOST, r.first[l + 1] - first);
   }
-  __device__ __forceinline__ bool last() const { return l + 1 == r.experts && first + n == r.first[l + 1]; }  // of its features
+  __device__ __forceinline__ bool last() const { return l + size >= r.experts && first + n == r.first[l + 1]; }  // of its features
   __device__ __forceinline__ void next() {
     first += n;
     n = min(MOST, r.first[l + 1] - first);
     if (n > 0) return;
-    if (++l == r.experts) l = 0, ++i;
+    if ((l += size) >= r.experts) l = rank, ++i;
     open();
   }
   __device__ __forceinline__ const uint16_t *weight(int j) const {
@@ -491,7 +520,7 @@ struct DownTiles {
 template <typename T, int NB, int DEPTH>
 __global__ void __launch_bounds__(THREADS, BLOCKS) down_kernel(const Args p) {
   __shared__ Routes r;
-  extern __shared__ float sums[];  // [WARPS][T][16]
+  extern __shared__ float sums[];  // [WARPS][T][16], and the block's [T][16]
   route(p, r, false);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   const int warp_floats = p.T * DOWN_FEATURES;
@@ -499,8 +528,15 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) down_kernel(const Args p) {
   for (int i = lane; i < warp_floats; i += 32) mine[i] = 0.f;
   __syncwarp();
   using Tiles = DownTiles<4 * NB>;
-  Tiles now(p, r);
+  const int rank = (int)cluster_rank(), size = (int)cluster_size();
+  Tiles now(p, r, rank, size);
+  float *block_sum = sums + WARPS * warp_floats;
   auto store = [&](int f, int nf) {
+    auto put = [&](int i, float v) {
+      const int to = i / DOWN_FEATURES, c = i % DOWN_FEATURES;
+      const T o = Elem<T>::put(v);
+      if (c < nf) p.out[to * p.ld_out + f + c] = *reinterpret_cast<const uint16_t *>(&o);
+    };
     block_sync();
     for (int i = threadIdx.x; i < warp_floats; i += THREADS) {
       float v = 0.f;
@@ -509,11 +545,20 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) down_kernel(const Args p) {
         v += sums[j * warp_floats + i];
         sums[j * warp_floats + i] = 0.f;
       }
-      const int to = i / DOWN_FEATURES, c = i % DOWN_FEATURES;
-      const T o = Elem<T>::put(v);
-      if (c < nf) p.out[to * p.ld_out + f + c] = *reinterpret_cast<const uint16_t *>(&o);
+      if (size == 1) put(i, v);
+      else block_sum[i] = v;
     }
-    block_sync();
+    if (size == 1) {
+      block_sync();
+      return;
+    }
+    cluster_barrier();
+    for (int i = rank * THREADS + threadIdx.x; i < warp_floats; i += size * THREADS) {  // this block's share of the joining
+      float v = 0.f;
+      for (int q = 0; q < size; ++q) v += load_from(block_sum + i, q);
+      put(i, v);
+    }
+    cluster_barrier();
   };
   Stream<T, NB, DEPTH, Tiles> w(now, p.I);
   w.run(now, [] { pdl_wait(); },  // for the first product's h (and out may be its x)
@@ -529,8 +574,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) down_kernel(const Args p) {
           __syncwarp();
           if (now.last()) store(now.f, now.nf);
         });
-  if (r.experts == 0)  // every expert of every token is masked
-    for (int f = now.begin; f < now.begin + now.features; f += DOWN_FEATURES) store(f, min(DOWN_FEATURES, now.begin + now.features - f));
+  if (rank >= r.experts)  // none for this block (every expert of every token may be masked): the others wait for it
+    for (; now.i < now.tiles; ++now.i) {
+      now.cut();
+      store(now.f, now.nf);
+    }
 }
 
 template <typename T, int NB, int DEPTH>
@@ -543,7 +591,23 @@ static cudaError_t products(const Args &p, int num_sms, cudaStream_t st) {
     err = cudaGetLastError();
   }
   if (err != cudaSuccess) return err;
-  return launch_pdl(down_kernel<T, NB, DEPTH>, dim3(BLOCKS * num_sms), dim3(THREADS), WARPS * p.T * DOWN_FEATURES * 4, st, p);
+  // blocks of a cluster: as many as leave each cluster 16 features, no more than experts may be live
+  const int blocks = BLOCKS * num_sms, runs = (p.H + DOWN_FEATURES - 1) / DOWN_FEATURES;
+  int size = 1;
+  while (2 * size <= MOST_CLUSTER && 2 * size * runs <= blocks && 2 * size <= std::min(p.E, p.T * p.k)) size *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks / size * size);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = (WARPS + 1) * p.T * DOWN_FEATURES * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = size, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, down_kernel<T, NB, DEPTH>, p);
 }
 template <typename T>
 static cudaError_t run(const Args &p, int num_sms, cudaStream_t st) {
