@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_bwd_kernel(cons
 // at a time, so that both take one block reduction, and the rows after them on their
 // way (cp.async, each thread into its own shared memory: no barrier guards the copies).
 // With one row at a time out of registers a row's chain (read, reduce, finish) bounds it:
-// 8192 x 7168 114 us, NEW so.
+// 8192 x 7168 114 us, 91 so.
 template <typename T, int NV>
 __global__ void __launch_bounds__(512) layer_norm_bwd_staged_kernel(const Bwd p, int pairs, int arrays) {
   constexpr int V = Elem<T>::VEC;
@@ -609,10 +609,11 @@ static int threads_of(int cols, int v) { return std::min(512, std::max(32, (cols
 // rows' parts of the column sums in the general kernels
 static int parts_of(int64_t rows, int num_sms) { return (int)std::max<int64_t>(1, std::min<int64_t>((rows + 63) / 64, num_sms)); }
 
-// The one-pass backward: columns a thread (16 in vectors of 16-bit types, whose raw rows take
-// few registers, else 8), threads, and blocks: what the SMs hold, with some rows each
-// so that the partial sums stay few.
-constexpr int FUSED_COLS = 8192;
+// The one-pass backward out of registers: columns a thread (16 in vectors of 16-bit types, whose
+// raw rows take few registers; 8 in fp32 vectors; single elements 8, or 4 in rows of up to
+// 4096: 4099 x 1001 in fp32 16 us instead of 24), threads, and blocks: what the SMs hold, with
+// some rows each so that the partial sums stay few.
+constexpr int FUSED_COLS = 8192, FOUR_COLS = 4096;
 struct BwdShape {
   int threads, blocks;
 };
@@ -669,9 +670,11 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
     }
   }
   if (p.cols <= FUSED_COLS) {
-    const BwdShape s = bwd_shape(p.rows, p.cols, V == 8 ? 16 : 8, num_sms);
+    const bool four = V == 1 && p.cols <= FOUR_COLS;
+    const BwdShape s = bwd_shape(p.rows, p.cols, V == 8 ? 16 : four ? 4 : 8, num_sms);
     p.parts = s.blocks;
-    layer_norm_bwd_kernel<T, V, V == 1 ? 8 : 2, V == 8><<<s.blocks, s.threads, 0, st>>>(p);
+    if (four) layer_norm_bwd_kernel<T, V, V == 1 ? 4 : 2, V == 8><<<s.blocks, s.threads, 0, st>>>(p);
+    else layer_norm_bwd_kernel<T, V, V == 1 ? 8 : 2, V == 8><<<s.blocks, s.threads, 0, st>>>(p);
     const cudaError_t err = cudaGetLastError();
     return err != cudaSuccess || !sums ? err : join();
   }
@@ -695,7 +698,9 @@ size_t layer_norm_workspace(int64_t rows, int cols, int num_sms) {
   int parts = parts_of(rows, num_sms);
   for (int size : {2, 4})
     for (int arrays : {2, 3}) parts = std::max(parts, staged_shape(rows, cols, size, arrays, num_sms).blocks);
-  if (cols <= FUSED_COLS) parts = std::max({parts, bwd_shape(rows, cols, 16, num_sms).blocks, bwd_shape(rows, cols, 8, num_sms).blocks});
+  if (cols <= FUSED_COLS) 
+    for (int each : {4, 8, 16})
+      if (each > 4 || cols <= FOUR_COLS) parts = std::max(parts, bwd_shape(rows, cols, each, num_sms).blocks);
   return (size_t)parts * 2 * cols * sizeof(float);
 }
 

@@ -1,6 +1,7 @@
 """Training steps of one MoE block on the symmetric heap.
 
     python examples/train_moe_block.py [--steps 20] [--config tiny|mixtral] [--tokens-per-slot 512] [--inter 4096]
+                                       [--update plain|orthogonal]
 
 The block is  y = x + scale * drop(tanh(gate) * norm(MoE(norm(x)))).  Its
 forward dispatches the normalised tokens over the heap, runs the experts as
@@ -8,6 +9,10 @@ grouped products with the routing weight inside the SwiGLU, and combines
 without weights.  Its backward is made of the same pieces turned around: the
 combine's backward is a dispatch of the output's gradient (same routing, so the
 same rows), the dispatch's backward is an unweighted combine.
+
+--update orthogonal gives the experts' and the router's matrices orthogonalised
+updates.  At the end the trained block answers a few tokens by themselves (no heap,
+no dispatch).
 """
 import argparse
 import os
@@ -110,10 +115,41 @@ class MoeBlock:
         sm.moe_block_norm_bwd(dy=dy, dh=self.dh, y=self.x, w_pre=q["norm_in"], rstd_pre=self.rstd_in, dx=dx,
                               dw_pre=d["norm_in"], work=self.work)
 
-    def update(self, lr: float):
+    def update(self, lr: float, orthogonal_lr: float = 0.0):
+        """A step down the gradients.  With orthogonal_lr the matrices (the router's, and
+        every expert's gate, up and down) take that much of their gradient's
+        orthogonalisation instead, times the root of the sides' ratio where it is above 1."""
+        I = self.cfg["inter"]
+        matrices = {}
+        if orthogonal_lr:
+            q, d = self.params, self.grads
+            matrices = {"router": [(q["router"], d["router"])], "down": [(q["down"], d["down"])],
+                        "gate_up": [(q["gate_up"][:, :I], d["gate_up"][:, :I]), (q["gate_up"][:, I:], d["gate_up"][:, I:])]}
         for name, t in self.params.items():
-            t -= lr * self.grads[name]
+            if name not in matrices:
+                t -= lr * self.grads[name]
+                continue
+            for w, g in matrices[name]:
+                rows, cols = g.shape[-2:]
+                way = torch.empty_like(g, memory_format=torch.contiguous_format)
+                work = torch.empty(sm.moe_orthogonalize_workspace(g.shape[0] if g.dim() == 3 else 1, rows, cols),
+                                   dtype=torch.uint8, device=g.device)
+                sm.moe_orthogonalize(g, way, work, scale=-orthogonal_lr * max(1.0, rows / cols) ** 0.5)
+                w += way
         self.step += 1  # another dropout mask
+
+    def answer(self, x, y):
+        """The block for up to 32 tokens by themselves, without dropout: y from x [T, H]."""
+        q, cfg, bf = self.params, self.cfg, dict(device=x.device, dtype=torch.bfloat16)
+        (tokens, H), I, E = x.shape, cfg["inter"], cfg["num_experts"]
+        h, out = torch.empty(tokens, H, **bf), torch.empty(tokens, H, **bf)
+        logits, w = torch.empty(tokens, E, device=x.device), torch.empty(tokens, self.k, device=x.device)
+        idx = torch.empty(tokens, self.k, dtype=torch.int32, device=x.device)
+        work = torch.empty(sm.moe_few_tokens_workspace(tokens, I, self.k), dtype=torch.uint8, device=x.device)
+        sm.moe_block_norm(x, w_pre=q["norm_in"], h=h)
+        sm.moe_few_tokens(h, q["gate_up"][:, :I], q["gate_up"][:, I:], q["down"], logits, idx, w, out, work,
+                          w_router=q["router"])
+        sm.moe_block_norm(x, o=out, w_post=q["norm_out"], gate=q["gate"], gate_act="tanh", scale=self.scale, y=y)
 
 
 def main():
@@ -123,6 +159,7 @@ def main():
     ap.add_argument("--tokens-per-slot", type=int, help="instead of the configuration's")
     ap.add_argument("--inter", type=int, help="expert intermediate size, instead of the configuration's")
     ap.add_argument("--lr", type=float, default=0.5)
+    ap.add_argument("--update", default="plain", choices=("plain", "orthogonal"))
     a = ap.parse_args()
     cfg = ms.shape_of(ms.CONFIGS[a.config])
     cfg.update({k: v for k, v in (("tokens_per_slot", a.tokens_per_slot), ("inter", a.inter)) if v})
@@ -142,9 +179,17 @@ def main():
         # the gradient of the mean, times the tokens: one learning rate for every size
         block.backward((2 / x.shape[1] * diff).bfloat16(), dx)
         end.record()
-        block.update(a.lr / x.shape[0])
+        block.update(a.lr / x.shape[0], 0.002 if a.update == "orthogonal" else 0.0)
         first = float(loss) if first is None else first
         print(f"step {step}: loss {float(loss):.5f}, forward and backward {start.elapsed_time(end):.3f} ms")
+    few = torch.empty(min(4, x.shape[0]), x.shape[1], device=dev, dtype=torch.bfloat16)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    block.answer(x[:len(few)], few)
+    start.record()
+    block.answer(x[:len(few)], few)
+    end.record()
+    torch.cuda.synchronize()
+    print(f"{len(few)} tokens by themselves: {start.elapsed_time(end):.3f} ms")
     assert block.heap.status() == 0 and block.grad_heap.status() == 0
     return first, float(loss)
 
