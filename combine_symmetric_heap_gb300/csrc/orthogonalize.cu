@@ -615,7 +615,6 @@ __global__ void __launch_bounds__(128) join_kernel(const Prod p) {
   };
   for (int j = threadIdx.x; j < end; j += 128) {
     float v = 0.f;
-#pragma unroll 8
     for (int k = 0; k < p.splits; ++k) v += part[((int64_t)k * p.M + i) * p.ld + j];
     float x = v * (A_SCALE / (X_SCALE * X_SCALE));
     if (i == j) {
