@@ -222,8 +222,15 @@ __global__ void __launch_bounds__(256) finish_kernel(const Call p, int copy) {
 // memory to rows of a lane, and the result back the same way.  Tensor copies of the
 // boxes were no faster where products are large (8 x 2048 x 7168 UPDATE 308 to 335 us, 316
 // to 328 now; four warps with three boxes ahead 316) and slower where they are small, each issued by
-// one lane while the others wait (POLY 75 us, now 61; 5 x 1031 x 519 370 us in all, now 312).  X X^T of wide matrices and products with A or B read K-major
-// tiles; X^T X and the X of B X lie the other way and are read as they lie.
+// one lane while the others wait (POLY 75 us, now 61; 5 x 1031 x 519 370 us in all, now 300).
+//
+// X X^T of wide matrices and products with A or B read K-major tiles; X^T X and the X of
+// B X lie the other way and are read as they lie.
+//
+// What bounds them (8 x 2048 x 7168): a CTA takes in 32 KB for each 64 of K, 64 bytes a
+// cycle at the tensor cores' full rate, which is what an SM takes in at most.  GRAM 160 us
+// (1.69 PFLOP/s of the tiles it makes, tensor pipe 82% busy), UPDATE 316 (1.52, 67%): its
+// X in and out, 8 bytes an element, shares that way (without either half of it 216); POLY 61.
 // ---------------------------------------------------------------------------
 enum Kind { GRAM, POLY, UPDATE };
 constexpr int EPI_WARPS = 8;  // two per TMEM lane quarter, each with half of a tile's columns
@@ -648,10 +655,13 @@ static cudaError_t launch_product(bool small, int num_sms, cudaStream_t st, cons
 
 }  // namespace orth
 
-// (bytes of one matrix, bytes that the call runs best with)
-void orthogonalize_workspace(int count, int rows, int cols, int, size_t *least, size_t *best) {
+// (bytes of one matrix, bytes that the call runs best with: all matrices, or as many as make
+// eight waves of the square products' tiles, and any number up to a gigabyte)
+void orthogonalize_workspace(int count, int rows, int cols, int num_sms, size_t *least, size_t *best) {
   *least = orth::layout_of(rows, cols).total;
-  *best = *least * std::max(count, 1);
+  const int64_t tm = (std::min(rows, cols) + 255) / 256, squares = tm * (tm + 1) / 2;
+  const int64_t enough = std::max<int64_t>((4 * num_sms + squares - 1) / squares, (int64_t(1) << 30) / (int64_t)*least);
+  *best = *least * (size_t)std::max<int64_t>(1, std::min<int64_t>(count, enough));
 }
 
 cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaStream_t st) {
