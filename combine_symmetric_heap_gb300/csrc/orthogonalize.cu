@@ -360,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
   const int nk = (p.K + BK - 1) / BK, total = p.tiles * p.count * p.splits;
-  pdl_launch_dependents();
+  if (KIND != UPDATE || !p.last) pdl_launch_dependents();  // (what follows the call waits for all of it)
   pdl_wait();           // the kernel before this one has written what this one reads,
   fence_proxy_async();  // some of it by plain stores
   auto blocks = [&](const Tile &ti, int &kb0, int &kb1) {  // K blocks of a tile

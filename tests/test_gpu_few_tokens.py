@@ -59,7 +59,8 @@ class Layer:
 SIZES = [(1, 8, 8, 1, 1), (1, 128, 256, 4, 2), (2, 64, 8, 3, 3), (3, 8, 72, 5, 2), (4, 136, 264, 4, 2), (5, 1032, 520, 24, 3),
          (7, 520, 1032, 9, 4), (8, 512, 512, 8, 2), (9, 256, 512, 1, 1), (16, 640, 384, 2, 2), (17, 264, 136, 3, 2),
          (32, 256, 256, 4, 1), (32, 512, 128, 256, 8), (32, 128, 128, 1, 1), (31, 136, 200, 2, 1), (6, 2048, 1408, 60, 6),
-         (1, 4096, 1544, 8, 2), (2, 7168, 264, 33, 32), (32, 1096, 72, 40, 32), (1, 72, 4104, 1024, 4)]
+         (1, 4096, 1544, 8, 2), (2, 7168, 264, 33, 32), (32, 1096, 72, 40, 32), (1, 72, 4104, 1024, 4),
+         (32, 72, 40, 1024, 32), (3, 16384, 24, 2, 1)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", SIZES)
@@ -213,3 +214,28 @@ def test_no_tokens():
     layer = Layer(1, 64, 64, 4, 2)
     layer.x, layer.logits = layer.x[:0], layer.logits[:0]
     layer.call()
+
+
+def test_refusals():
+    layer = Layer(4, 64, 72, 6, 2)
+    T, k = 4, 2
+    idx, w, out = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda"), torch.empty_like(layer.x)
+    work = torch.empty(sm.moe_few_tokens_workspace(T, 72, k), dtype=torch.uint8, device="cuda")
+    good = dict(x=layer.x, w_gate=layer.wg, w_up=layer.wu, w_down=layer.wd, logits=layer.logits, idx=idx, w=w, out=out, work=work,
+                w_router=layer.wr)
+    sm.moe_few_tokens(**good)
+    many = torch.zeros(33, 64, device="cuda", dtype=BF)
+    bad = [dict(x=layer.x.half()), dict(x=layer.x[:3]), dict(x=layer.x.cpu()), dict(x=layer.x[0]), dict(w_gate=layer.wg[:5]),
+           dict(w_up=layer.wu[:, :64]), dict(w_down=layer.wg), dict(w_down=layer.wd.half()), dict(w_gate=layer.wg.transpose(1, 2)),
+           dict(logits=layer.logits.half()), dict(logits=layer.logits.t().contiguous().t()), dict(idx=idx.long()), dict(idx=idx[:3]),
+           dict(w=w[:, :1]), dict(w=w.double()), dict(out=out.float()), dict(out=out[:, :32]), dict(w_router=layer.wr[:5]),
+           dict(work=work.cpu()), dict(work=None), dict(w=None),
+           dict(x=many, out=many.clone(), logits=torch.zeros(33, 6, device="cuda"), idx=idx.new_empty(33, k), w=w.new_empty(33, k)),
+           dict(idx=idx.new_empty(T, 7), w=w.new_empty(T, 7))]
+    for i, kw in enumerate(bad):
+        with pytest.raises(sm.SymmoeError) as e:
+            sm.moe_few_tokens(**dict(good, **kw))
+        assert e.value.code == sm.SYM_EINVAL, i
+    with pytest.raises(sm.SymmoeError) as e:
+        sm.moe_few_tokens(**dict(good, work=work[:work.numel() - 16]))
+    assert e.value.code == sm.SYM_ENOSPACE

@@ -128,7 +128,7 @@ def test_edges(dt, cols):
 
 @pytest.mark.parametrize("dt,size", [(torch.float32, 1e30), (torch.float32, 1e-30), (torch.bfloat16, 1e30), (torch.bfloat16, 1e-30),
                                      (torch.float16, 2e4), (torch.float16, 1e-6)])
-@pytest.mark.parametrize("cols", [100, 1001, 4096, 9000])
+@pytest.mark.parametrize("cols", [100, 1001, 4096, 9000, 40000])
 def test_range(dt, size, cols):
     """Squares beyond the range of 32 bits; eps 0, so that the scale does not matter."""
     x = (make(4, cols, torch.float32) * size).to(dt)
@@ -226,3 +226,37 @@ def test_no_rows():
     sm.moe_layer_norm(e, e, w=w)
     sm.moe_layer_norm_bwd(e, e, none, none, dx=e, w=w, dw=dw, db=db)
     assert not dw.any() and not db.any()
+
+
+def test_parts_of_the_forward():
+    """Every output may be left out; what is there is the same."""
+    x, add, w = make(5, 1000, torch.bfloat16), make(5, 1000, torch.bfloat16, seed=1), make(1, 1000, torch.bfloat16, seed=2)[0]
+    full = {"h": like(x), "sum": like(x), "mean": torch.empty(5, device="cuda"), "rstd": torch.empty(5, device="cuda")}
+    sm.moe_layer_norm(x, w=w, add=add, **full)
+    for name in full:
+        one = torch.empty_like(full[name])
+        sm.moe_layer_norm(x, w=w, add=add, **{name: one})
+        assert torch.equal(one, full[name]), name
+
+
+def test_refusals():
+    x, w = make(4, 64, torch.bfloat16), make(1, 64, torch.bfloat16)[0]
+    h, st = like(x), torch.empty(4, device="cuda")
+    work = torch.empty(sm.moe_layer_norm_workspace(4, 64), dtype=torch.uint8, device="cuda")
+    bad = [lambda: sm.moe_layer_norm(x), lambda: sm.moe_layer_norm(x, h[:3]), lambda: sm.moe_layer_norm(x, h.float()),
+           lambda: sm.moe_layer_norm(x, h, w=w[:63]), lambda: sm.moe_layer_norm(x, h, w=w.float()), lambda: sm.moe_layer_norm(x, h, mean=st[:3]),
+           lambda: sm.moe_layer_norm(x, h, sum=h), lambda: sm.moe_layer_norm(x.cpu(), h), lambda: sm.moe_layer_norm(x, h.cpu()),
+           lambda: sm.moe_layer_norm(x[0], h[0]), lambda: sm.moe_layer_norm(x.t(), h.t()), lambda: sm.moe_layer_norm(x, h, eps=-1.0),
+           lambda: sm.moe_layer_norm(x.double(), h.double()), lambda: sm.moe_layer_norm(x[:1].expand(4, 64), h),
+           lambda: sm.moe_layer_norm_bwd(x, x, st, st), lambda: sm.moe_layer_norm_bwd(x, x, None, st, dx=h),
+           lambda: sm.moe_layer_norm_bwd(x, None, st, st, dx=h), lambda: sm.moe_layer_norm_bwd(x, x, st, st[:2], dx=h),
+           lambda: sm.moe_layer_norm_bwd(x, x, st, st, dw=w, work=work.cpu())]
+    for i, call in enumerate(bad):
+        with pytest.raises(sm.SymmoeError) as e:
+            call()
+        assert e.value.code == sm.SYM_EINVAL, i
+    for short in (None, work[:work.numel() - 16]):
+        with pytest.raises(sm.SymmoeError) as e:
+            sm.moe_layer_norm_bwd(x, x, st, st, dw=torch.empty_like(w), work=short)
+        assert e.value.code == sm.SYM_ENOSPACE
+    sm.moe_layer_norm_bwd(x, x, st, st, dx=h)  # dx alone wants no workspace

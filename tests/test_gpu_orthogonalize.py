@@ -1,4 +1,6 @@
 """Orthogonalised updates against the definition in 64 bits."""
+import ctypes
+
 import pytest
 import torch
 
@@ -30,7 +32,8 @@ def check(g, out, steps=5, coeffs=COEFFS, eps=1e-7, scale=1.0):
 
 SIZES = [(1, 1, 1), (2, 1, 9), (2, 9, 1), (3, 8, 8), (1, 31, 33), (2, 64, 64), (2, 65, 130), (1, 200, 72), (3, 128, 512),
          (2, 256, 256), (1, 257, 255), (2, 300, 1000), (1, 1031, 519), (1, 520, 1032), (1, 640, 2049), (30, 72, 136),
-         (1, 72, 4100), (2, 4100, 72), (1, 300, 2100), (1, 2100, 500), (3, 1300, 1288)]
+         (1, 72, 4100), (2, 4100, 72), (1, 300, 2100), (1, 2100, 500), (3, 1300, 1288),
+         (1, 33000, 40), (1, 24, 20000)]
 
 
 @pytest.mark.parametrize("count,rows,cols", SIZES)
@@ -158,3 +161,55 @@ def test_capture_and_streams():
 def test_no_matrices():
     e = torch.empty(0, 8, 8, device="cuda", dtype=torch.bfloat16)
     sm.moe_orthogonalize(e, e, torch.empty(0, dtype=torch.uint8, device="cuda"))
+
+
+def test_refusals():
+    g = gradient(2, 40, 72)
+    out, work = torch.empty_like(g), work_for(2, 40, 72)
+    bad = [lambda: sm.moe_orthogonalize(g, out[:1], work), lambda: sm.moe_orthogonalize(g, out.float(), work),
+           lambda: sm.moe_orthogonalize(g.cpu(), out, work), lambda: sm.moe_orthogonalize(g, out, work.cpu()),
+           lambda: sm.moe_orthogonalize(g.transpose(1, 2), out.transpose(1, 2), work), lambda: sm.moe_orthogonalize(g[0, 0], out[0, 0], work),
+           lambda: sm.moe_orthogonalize(g, out, work, steps=65), lambda: sm.moe_orthogonalize(g, out, work, steps=-1),
+           lambda: sm.moe_orthogonalize(g, out, work, eps=-1.0), lambda: sm.moe_orthogonalize(g, out, work, coeffs=(1.0, 2.0)),
+           lambda: sm.moe_orthogonalize(g, out, work[128:]), lambda: sm.moe_orthogonalize(g, out, work, status=out),
+           lambda: sm.moe_orthogonalize(g[:1].expand(2, 40, 72), out, work), lambda: sm.moe_orthogonalize(g, out[:1].expand(2, 40, 72), work)]
+    for i, call in enumerate(bad):
+        with pytest.raises(sm.SymmoeError) as e:
+            call()
+        assert e.value.code == sm.SYM_EINVAL, i
+    least = sm.moe_orthogonalize_workspace(2, 40, 72, least=True)
+    with pytest.raises(sm.SymmoeError) as e:
+        sm.moe_orthogonalize(g, out, work[:least - 256])
+    assert e.value.code == sm.SYM_ENOSPACE
+
+
+def test_workspace_fills_the_device_and_no_more():
+    """Many large matrices go through in turns; few or small ones side by side."""
+    one = sm.moe_orthogonalize_workspace(256, 2048, 7168, least=True)
+    assert one == sm.moe_orthogonalize_workspace(1, 2048, 7168)
+    assert sm.moe_orthogonalize_workspace(8, 2048, 7168) == 8 * one
+    assert sm.moe_orthogonalize_workspace(256, 2048, 7168) < 4 << 30
+    small = sm.moe_orthogonalize_workspace(1, 64, 64)
+    assert sm.moe_orthogonalize_workspace(100, 64, 64) == 100 * small
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """Waits limited to 20 us where a tile's K axis takes about a millisecond (the limit is
+    looked at every sixteenth poll, and a poll can take some microseconds): the kernels
+    give up, say so, and leave the device as they found it."""
+    rows, cols = 600, 65536
+    g = gradient(1, rows, cols, torch.float16, scale=1e-1)
+    out, work, status = torch.empty_like(g), work_for(1, rows, cols), torch.zeros(1, dtype=torch.int32, device="cuda")
+    sm.moe_orthogonalize(g, out, work, status=status)
+    want = out.clone()
+    assert int(status) == 0
+    a = sm.SymOrthogonalize(1, rows, cols, 1, sm.SYM_FP16, sm.SYM_FP16, (ctypes.c_float * 3)(*COEFFS), 1e-7, 1.0, 20,
+                            status.data_ptr(), g.data_ptr(), out.data_ptr(), rows * cols, cols, rows * cols, cols, work.data_ptr(),
+                            work.numel())
+    assert sm.lib().moe_orthogonalize(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == sm.SYM_OK
+    torch.cuda.synchronize()
+    assert int(status) & sm.SYM_STATUS_TIMEOUT
+    status.zero_()
+    out.zero_()
+    sm.moe_orthogonalize(g, out, work, status=status)
+    assert int(status) == 0 and torch.equal(out, want)
