@@ -16,6 +16,14 @@
 //     rest belongs to one element each.  As X comes near to orthogonality the
 //     diagonals come near to constants and the rests to zero, and so does what
 //     their rounding leaves.
+// The first two steps of matrices that are wider than tall (or the other way) share one
+// update: with P = a I + B, the second's Gram matrix is A' = P A P, and X goes to P' P X.  All
+// of these commute and are symmetric, and their products, of the shorter side, cost less than an update and a Gram
+// matrix.  It is for the first two only: what rounding leaves in A is taken times P
+// squared, up to a^2 = 12, where singular values are small; beside an A of at most one
+// that is nothing yet (relative error of a result 4.2e-4 either way; with the third
+// and fourth step so too, 3e-3).
+//
 // All are held times a power of two that keeps them in fp16's range: X (entries at
 // most its largest singular value; 1 / sqrt(m n) at first) times 2^13, A times 2^10, B
 // times 2^8.
@@ -41,7 +49,7 @@ struct Layout {
   int64_t ld_x, ld_a;                      // rows of X, of A and B: multiples of 64 elements
   size_t x_bytes, a_bytes;                 // one copy of X's hi or lo, of A or B
   // offsets: two copies of X's hi and lo; A's and B's (b: B's, a: A's, each hi, lo)
-  size_t hi, lo, a, b, diag_a, diag_b, sums, parts, total;
+  size_t hi, lo, a, b, diag_a, diag_b, diag_a2, diag_b2, sums, parts, total;
   int splits;  // parts that a Gram product's K axis may be cut into
 };
 constexpr int SUMS = 256;  // partial sums of squares
@@ -56,7 +64,8 @@ static Layout layout_of(int rows, int cols) {
   l.x_bytes = up((size_t)rows * l.ld_x * 2, 256), l.a_bytes = up((size_t)m * l.ld_a * 2, 256);
   l.hi = 0, l.lo = 2 * l.x_bytes, l.a = 4 * l.x_bytes, l.b = l.a + 2 * l.a_bytes;
   l.diag_a = l.b + 2 * l.a_bytes, l.diag_b = l.diag_a + up((size_t)m * 4, 256);
-  l.sums = l.diag_b + up((size_t)m * 4, 256), l.parts = l.sums + SUMS * 8;
+  l.diag_a2 = l.diag_b + up((size_t)m * 4, 256), l.diag_b2 = l.diag_a2 + up((size_t)m * 4, 256);
+  l.sums = l.diag_b2 + up((size_t)m * 4, 256), l.parts = l.sums + SUMS * 8;
   l.splits = m > SPLIT_SIDE ? 1 : std::max(1, std::min(MOST_SPLITS, std::max(rows, cols) / SPLIT_K));
   l.total = up(l.parts + (l.splits > 1 ? (size_t)l.splits * m * l.ld_a * 4 : 0), 256);
   return l;
@@ -214,7 +223,8 @@ __global__ void __launch_bounds__(256) finish_kernel(const Call p, int copy) {
 //   GRAM    A = X X^T (X^T X)          X from both sides
 //   POLY    B = b A + c A A
 //   UPDATE  X = a X + B X (X B)
-// A and B are symmetric: only tiles on and below the diagonal are made, each
+//   MIX     the product of two symmetric matrices that commute
+// All but X are symmetric: only tiles on and below the diagonal are made, each
 // written twice, as it is and turned over.
 //
 // What a product adds to (A for POLY, X for UPDATE) comes into an epilogue
@@ -232,7 +242,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const Call p, int copy) {
 // (1.69 PFLOP/s of the tiles it makes, tensor pipe 82% busy), UPDATE 316 (1.52, 67%): its
 // X in and out, 8 bytes an element, shares that way (without either half of it 216); POLY 61.
 // ---------------------------------------------------------------------------
-enum Kind { GRAM, POLY, UPDATE };
+enum Kind { GRAM, POLY, UPDATE, MIX };
 constexpr int EPI_WARPS = 8;  // two per TMEM lane quarter, each with half of a tile's columns
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
 constexpr int BOX = 32 * 64;  // 32 rows of 32 fp16
@@ -257,7 +267,10 @@ struct Prod {
   char *work;  // of the turn's first matrix
   size_t stride;        // between matrices
   size_t in[2], out[2]; // what is added to and the result: hi, lo
-  size_t diag_in, diag; // B's and A's diagonals
+  size_t diag_in, diag; // the diagonals: of what is multiplied, of the result
+  size_t diag_in2;      // MIX: the second factor's
+  float shift, shift2;  // added to them
+  float f0, f1, f2;     // MIX: scales of the factors' elements and of the sums in the result's
   int64_t ld;           // of those rows
   int M, N, K, tiles_m, tiles, count, tall;
   int splits, split_kb;  // GRAM: parts of the K axis, K blocks of one (parts: where their sums go)
@@ -436,7 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
     const int q = wid & 3, share = (wid - 2) / 4;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     uint8_t *my_boxes = boxes + (size_t)(wid - 2) * BUFS * 2 * BOX;  // [BUFS][hi, lo]
-    const int two_in = KIND == UPDATE || p.passes > 1, two_out = KIND == UPDATE ? !p.last : p.passes > 1;
+    // two boxes in: hi and lo of one matrix (MIX: both factors'); out: hi and lo
+    const int two_in = KIND == UPDATE || KIND == MIX || p.passes > 1, two_out = KIND == UPDATE ? !p.last : p.passes > 1;
     // memory's rows: lane 4r + w has word w of rows r, 8 + r, ...
     const int r8 = lane >> 2, w4 = lane & 3;
     auto in_box = [&](uint8_t *box, int r) { return reinterpret_cast<uint4 *>(box + r * 64 + ((w4 ^ ((r >> 1) & 3)) << 4)); };
@@ -451,7 +465,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
       char *w = p.work + ti.z * p.stride;
       float *diag = reinterpret_cast<float *>(w + p.diag);
       const float *diag_in = reinterpret_cast<const float *>(w + p.diag_in);
-      const bool by_column = KIND == POLY || (KIND == UPDATE && p.tall);
+      const bool by_column = KIND == POLY || KIND == MIX || (KIND == UPDATE && p.tall);
+      const float *diag_col = KIND == MIX ? reinterpret_cast<const float *>(w + p.diag_in2) : diag_in;
       auto fetch = [&](int c) {  // the tile's box c
         if (KIND == GRAM) return;
         if (c >= chunks) {
@@ -471,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
 #pragma unroll
       for (int c = 0; c < max(1, BUFS - 1); ++c) fetch(c);
       // the next box's columns' diagonal elements, one a lane (padded to whole boxes)
-      float d_next = by_column && chunks > 0 ? diag_in[col0 + lane] : 0.f;
+      float d_next = by_column && chunks > 0 ? diag_col[col0 + lane] : 0.f;
       const float d_row = KIND != GRAM && row < p.M && !(KIND == UPDATE && p.tall) ? diag_in[row] : 0.f;
       if (!(ok = __all_sync(0xffffffffu, bar_wait(&acc_full[b], used[b]++ & 1u, ctl)))) break;
       tc_fence_after();
@@ -481,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
         const int col = col0 + 32 * c;
         uint8_t *box = my_boxes + (boxno + c) % BUFS * 2 * BOX;
         const float d_col = d_next;
-        if (by_column && c + 1 < chunks) d_next = diag_in[col + 32 + lane];
+        if (by_column && c + 1 < chunks) d_next = diag_col[col + 32 + lane];
         if (KIND != GRAM) {
           if (BUFS > 1 || c > 0) fetch(c + BUFS - 1);
           cp_async_wait<BUFS - 1>();
@@ -494,16 +509,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
 #pragma unroll 1
         for (int o = 0; o < 4; ++o) {
           uint32_t v[8];
-          float x[8];
+          float x[8], l[8];
           tmem_ld8(acc + 32 * c + 8 * o, v);
           uint4 *const hi_word = box_word(box, lane, o), *const lo_word = box_word(box + BOX, lane, o);
           if (KIND != GRAM) {
             unpack<__half, 8>(*hi_word, x);
             if (two_in) {
-              float l[8];
               unpack<__half, 8>(*lo_word, l);
+              if (KIND != MIX)
 #pragma unroll
-              for (int k = 0; k < 8; ++k) x[k] += l[k];
+                for (int k = 0; k < 8; ++k) x[k] += l[k];
             }
           }
           tmem_ld_wait();
@@ -523,6 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
             const float sum = __uint_as_float(v[k]);
             const float d = by_column ? __shfl_sync(0xffffffffu, d_col, 8 * o + k) : 0.f;
             if (KIND == GRAM) x[k] = sum * (A_SCALE / (X_SCALE * X_SCALE));
+            else if (KIND == MIX) x[k] = (d_row + p.shift) * (l[k] * p.f1) + (d + p.shift2) * (x[k] * p.f0) + sum * p.f2;
             else if (KIND == POLY)
               x[k] = (p.b + p.c * (d_row + d)) * (x[k] * (B_SCALE / A_SCALE)) + p.c * (sum * (B_SCALE / (A_SCALE * A_SCALE)));
             else x[k] = (p.a + (p.tall ? d : d_row)) * x[k] + sum * (1.f / B_SCALE);
@@ -535,9 +551,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
                 own = x[k];
                 x[k] = 0.f;
               }
-            // (POLY: A's own part of x is zero here)
+            // (the factors' own parts of x are zero here)
             if (lane / 8 == o && row < p.M)
-              diag[row] = KIND == GRAM ? own * (1.f / A_SCALE) : d_row * (p.b + p.c * d_row) + own * (1.f / B_SCALE);
+              diag[row] = KIND == GRAM  ? own * (1.f / A_SCALE)
+                          : KIND == MIX ? (d_row + p.shift) * (d_col + p.shift2) + own / (p.f0 * p.f1 / p.f2)
+                                        : d_row * (p.b + p.c * d_row) + own * (1.f / B_SCALE);
           }
           if (users) {
 #pragma unroll
@@ -725,7 +743,7 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
     int splits = std::max(1, std::min(l.splits, pairs / (sq_tiles * (int)std::min<unsigned>(n, 4096))));
     const int split_kb = (nk + splits - 1) / splits;
     splits = (nk + split_kb - 1) / split_kb;  // none without K blocks
-    Maps gram[2], poly, update[2];
+    Maps gram[2], poly, update[2], mix[3], update2;
     for (int k = 0; k < 2; ++k) {  // from copy k of X
       const size_t hi = l.hi + k * l.x_bytes, lo = l.lo + k * l.x_bytes;
       both(gram[k].a, hi, lo, p.rows, p.cols, l.ld_x, 64, p.tall ? 64 : 128);
@@ -738,12 +756,28 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
         update[k].b[h] = p.tall ? sq[h] : x[h];
       }
     }
+    // Two steps with one update (their low parts' places are free: they are not the precise
+    // ones): an update and a Gram matrix, 3 m^2 n operations, against three products of 3 m^3.
+    // One launch more, so small products only where n is far from m.  With / without, us: 8 x 2048 x
+    // 7168 3017 / 3300, 4096 x 14336 2634 / 2900, 256 x 7168 154 / 160; 256 x 1024 137 / 126, 5 x 1031 x 519 219 / 209.
+    const int n_side = std::max(p.rows, p.cols);
+    const bool twice = (sq_small ? n_side >= 8 * (int64_t)m : n_side * 2 >= 3 * m) &&
+                       o.steps >= (o.out_dtype == SYM_FP16 ? 2 + PRECISE_STEPS : 2);
+    if (twice) {
+      const size_t left[3] = {l.a, a_lo, b_lo};
+      for (int k = 0; k < 3; ++k) {
+        both(mix[k].a, left[k], left[k], m, m, l.ld_a, 64, 128);
+        both(mix[k].b, l.b, l.b, m, m, l.ld_a, 64, sq_n / 2);
+      }
+      update2 = update[0];
+      both(p.tall ? update2.b : update2.a, l.a, a_lo, m, m, l.ld_a, 64, p.tall ? up_n / 2 : 128);
+    }
     both(poly.a, l.a, a_lo, m, m, l.ld_a, 64, 128);
     both(poly.b, l.a, a_lo, m, m, l.ld_a, 64, sq_n / 2);
     const int user_vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && (p.rows == 1 || o.ld_out % 8 == 0) && (n == 1 || o.out_stride % 8 == 0);
     if (!ok) return cudaErrorInvalidValue;
-    for (int i = 0; i < o.steps; ++i) {
-      const int k = i & 1;
+    for (int i = 0, k = 0; i < o.steps; k ^= 1) {
+      const bool both_steps = i == 0 && twice;
       q.passes = o.out_dtype == SYM_FP16 && i >= o.steps - PRECISE_STEPS ? 3 : 1;
       q.M = q.N = m, q.K = std::max(p.rows, p.cols), q.tiles_m = tm, q.tiles = sq_tiles;
       q.diag = l.diag_a, q.out[0] = l.a, q.out[1] = a_lo, q.ld = l.ld_a;
@@ -757,15 +791,35 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
       q.in[0] = l.a, q.in[1] = a_lo, q.out[0] = l.b, q.out[1] = b_lo;
       err = launch_product<POLY, false, false>(sq_small, num_sms, st, q, poly);
       if (err != cudaSuccess) return err;
-      q.M = p.rows, q.N = p.cols, q.diag_in = l.diag_b;
+      q.a = p.a;
+      if (both_steps) {
+        // W = A P, A' = W P over A, P' from A', P' P over A'
+        auto mix_of = [&](int which, size_t first, size_t first_diag, float shift, float first_scale, size_t to, size_t to_diag, float scale) {
+          q.in[0] = first, q.in[1] = l.b, q.diag_in = first_diag, q.diag_in2 = l.diag_b, q.shift = shift, q.shift2 = p.a;
+          q.out[0] = to, q.diag = to_diag;
+          q.f0 = scale / first_scale, q.f1 = scale / B_SCALE, q.f2 = scale / (first_scale * B_SCALE);
+          return launch_product<MIX, false, false>(sq_small, num_sms, st, q, mix[which]);
+        };
+        if ((err = mix_of(0, l.a, l.diag_a, 0.f, A_SCALE, a_lo, l.diag_a2, A_SCALE)) != cudaSuccess ||
+            (err = mix_of(1, a_lo, l.diag_a2, 0.f, A_SCALE, l.a, l.diag_a, A_SCALE)) != cudaSuccess)
+          return err;
+        q.in[0] = l.a, q.diag_in = l.diag_a, q.out[0] = b_lo, q.diag = l.diag_b2;
+        if ((err = launch_product<POLY, false, false>(sq_small, num_sms, st, q, poly)) != cudaSuccess ||
+            (err = mix_of(2, b_lo, l.diag_b2, p.a, B_SCALE, l.a, l.diag_a, B_SCALE)) != cudaSuccess)
+          return err;
+        q.a = 0.f;  // (P' P has all of it)
+      }
+      i += both_steps ? 2 : 1;
+      q.M = p.rows, q.N = p.cols, q.diag_in = both_steps ? l.diag_a : l.diag_b;
       q.tiles_m = tr, q.tiles = up_tiles;
-      q.last = i + 1 < o.steps ? 0 : o.out_dtype == SYM_BF16 ? 1 : 2, q.vec = user_vec;
+      q.last = i < o.steps ? 0 : o.out_dtype == SYM_BF16 ? 1 : 2, q.vec = user_vec;
       q.in[0] = l.hi + k * l.x_bytes, q.in[1] = l.lo + k * l.x_bytes, q.ld = l.ld_x;
       q.out[0] = l.hi + (k ^ 1) * l.x_bytes, q.out[1] = l.lo + (k ^ 1) * l.x_bytes;
-      err = p.tall ? launch_product<UPDATE, false, false>(up_small, num_sms, st, q, update[k])
-                   : launch_product<UPDATE, false, true>(up_small, num_sms, st, q, update[k]);
+      const Maps &maps = both_steps ? update2 : update[k];
+      err = p.tall ? launch_product<UPDATE, false, false>(up_small, num_sms, st, q, maps)
+                   : launch_product<UPDATE, false, true>(up_small, num_sms, st, q, maps);
       if (err != cudaSuccess) return err;
-      q.last = 0;
+      q.last = 0, q.a = p.a;
     }
     if (o.steps == 0) {
       const dim3 lines(std::min(o.rows, 1024), n);

@@ -729,7 +729,8 @@ int moe_layer_norm_workspace(int64_t rows, int32_t cols, uint64_t *bytes);
  *   all matrices go side by side where they are small, and enough of them at a
  *   time to fill the device where they are large (work_bytes), and the least the
  *   call takes (least_bytes): the matrices go through in as many turns as the
- *   workspace makes them.  Contents do not matter before or after.
+ *   workspace makes them.  Contents do not matter before or after.  (Products are cut
+ *   up by the number of matrices in a turn: another one can change last bits.)
  *   status: device word that SYM_STATUS_TIMEOUT is OR-ed into where one of the
  *   products' internal waits runs out (wait_timeout_us each, 0: 2,000,000), or NULL.
  * X is held in 22 bits (two fp16 numbers) and enters the products as its first

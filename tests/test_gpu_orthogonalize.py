@@ -55,7 +55,18 @@ def test_steps_and_coefficients(rows, cols, steps, coeffs):
     check(g, out, steps, coeffs, scale=-0.25)
 
 
-@pytest.mark.parametrize("rows,cols", [(64, 200), (200, 64), (300, 300)])
+@pytest.mark.parametrize("count,rows,cols", [(40, 72, 136), (40, 136, 72), (8, 600, 1000), (8, 1000, 600), (1, 40, 400), (2, 700, 64)])
+@pytest.mark.parametrize("out_dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("steps", [2, 5, 6])
+def test_first_two_steps_with_one_update(count, rows, cols, out_dt, steps):
+    """Shapes whose first two steps go through one update."""
+    g = gradient(count, rows, cols, torch.float32)
+    out = torch.empty(count, rows, cols, device="cuda", dtype=out_dt)
+    sm.moe_orthogonalize(g, out, work_for(count, rows, cols), steps=steps)
+    check(g[:3], out[:3], steps)
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 200), (200, 64), (300, 300), (16, 300)])
 def test_orthogonal_rows_take_the_scalar_recursion(rows, cols):
     """One entry in each row and column: every Gram matrix is diagonal, held in 32
     bits, and the entries go through the polynomial one by one."""
