@@ -103,7 +103,9 @@ __device__ __forceinline__ void eight(const T *row, int c, int cols, float (&f)[
     for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? Elem<T>::get(row[c + i]) : 0.f;
   }
 }
-constexpr int AT_ONCE = 4;  // eights that a thread has in flight
+// Eights that a thread has in flight; the SMs are full of threads (2 / 4 / 8: squares of 4 x 2048 x 7168
+// 32 / 45 / 62 us, the first X 60 / 67 / 105).
+constexpr int AT_ONCE = 2;
 // Partial sums of squares, grid (SUMS, matrices): eight at a time in 32 bits where they
 // stay in range there, in 64 bits where not; added up in 64 bits.
 template <typename T, bool VEC>
@@ -321,6 +323,26 @@ __device__ __forceinline__ Tile tile_of(const Prod &p, int t) {
 // This lane's row of a box (64-byte swizzle: 16-byte word w of row r at w ^ (r / 2 mod 4))
 __device__ __forceinline__ uint4 *box_word(uint8_t *box, int lane, int w) {
   return reinterpret_cast<uint4 *>(box + lane * 64 + ((w ^ ((lane >> 1) & 3)) << 4));
+}
+// Eight lanes' rows of eight 16-bit columns turned over among them: lane i's result is column
+// i mod 8 of its eight lanes' rows.  (Stores of 2 bytes, a column at a time, instead: POLY
+// 38 us at 4 x 2048 x 7168, 31 without them, 35 so.)
+__device__ __forceinline__ uint4 turned8(const uint4 &q, int lane) {
+  uint32_t t[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // lanes 1 apart: columns 2j (even lanes) or 2j + 1 of two rows
+    const uint32_t o = __shfl_xor_sync(0xffffffffu, t[j], 1);
+    t[j] = lane & 1 ? __byte_perm(o, t[j], 0x7632) : __byte_perm(t[j], o, 0x5410);
+  }
+  const bool b = lane & 2, c = lane & 4;
+  // lanes 2 apart: j = b and j = 2 + b, of four rows
+  const uint32_t r0 = __shfl_xor_sync(0xffffffffu, b ? t[0] : t[1], 2), r1 = __shfl_xor_sync(0xffffffffu, b ? t[2] : t[3], 2);
+  const uint32_t k0 = b ? t[1] : t[0], k1 = b ? t[3] : t[2];
+  const uint32_t u[2][2] = {{b ? r0 : k0, b ? k0 : r0}, {b ? r1 : k1, b ? k1 : r1}};
+  // lanes 4 apart: one of the two, of eight rows
+  const uint32_t s0 = __shfl_xor_sync(0xffffffffu, c ? u[0][0] : u[1][0], 4), s1 = __shfl_xor_sync(0xffffffffu, c ? u[0][1] : u[1][1], 4);
+  const uint32_t m0 = c ? u[1][0] : u[0][0], m1 = c ? u[1][1] : u[0][1];
+  return c ? make_uint4(s0, s1, m0, m1) : make_uint4(m0, m1, s0, s1);
 }
 // 8 consecutive fp32 columns of this thread's TMEM lane (as tmem_ld32)
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -574,16 +596,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
             lo = pack<__half, 8>(x);
             *lo_word = lo;
           }
-          if (ti.turned && row < p.M) {  // turned over: a warp's lanes side by side
-            const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
-            uint16_t *th = reinterpret_cast<uint16_t *>(w + p.out[0]) + at * p.ld + row;
-            uint16_t *tl = reinterpret_cast<uint16_t *>(w + p.out[1]) + at * p.ld + row;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (at + k < p.N) {
-                th[k * p.ld] = (uint16_t)(hw[k / 2] >> (16 * (k & 1)));
-                if (two_out) tl[k * p.ld] = (uint16_t)(lw[k / 2] >> (16 * (k & 1)));
-              }
+          if (ti.turned) {  // turned over: a lane has a column of eight rows (past the last row: the pitch's end)
+            const int64_t to = (int64_t)(at + (lane & 7)) * p.ld + row0 + (lane & ~7);
+            const bool there = at + (lane & 7) < p.N;
+            const uint4 th = turned8(hi, lane);
+            if (there) *reinterpret_cast<uint4 *>(reinterpret_cast<__half *>(w + p.out[0]) + to) = th;
+            if (two_out) {
+              const uint4 tl = turned8(lo, lane);
+              if (there) *reinterpret_cast<uint4 *>(reinterpret_cast<__half *>(w + p.out[1]) + to) = tl;
+            }
           }
         }
         if (KIND == GRAM && p.splits > 1) continue;
