@@ -158,9 +158,52 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(const Fwd p) {
   }
 }
 
+// Bytes [n, n + 16) of a and b behind one another; n even, up to 16
+__device__ __forceinline__ uint4 turned(const uint4 &a, const uint4 &b, int n) {
+  if (n & 16) return b;
+  uint32_t t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) t[i] = n & 8 ? t[i + 2] : t[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) t[i] = n & 4 ? t[i + 1] : t[i];
+  const int bits = n & 2 ? 16 : 0;
+  return make_uint4(__funnelshift_r(t[0], t[1], bits), __funnelshift_r(t[1], t[2], bits),
+                    __funnelshift_r(t[2], t[3], bits), __funnelshift_r(t[3], t[4], bits));
+}
+
+// Columns [c, c + V) of a row of any alignment, zeros outside [0, cols): two words on 16-byte
+// boundaries where both are the row's own, else single elements
+template <typename T, int V>
+__device__ __forceinline__ uint4 load_turned(const T *row, int c, int cols) {
+  const int bytes = (int)(reinterpret_cast<uintptr_t>(row + c) & 15), first = c - bytes / (int)sizeof(T);
+  if (first >= 0 && first + 2 * V <= cols) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(row + first);
+    return turned(q[0], q[1], bytes);
+  }
+  float f[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = c + i >= 0 && c + i < cols ? Elem<T>::get(row[c + i]) : 0.f;
+  return pack<T, V>(f);
+}
+
+// Whether the 16 bytes from column c of row r on lie between a tensor's first and last
+// element.  A row's first and last word may hold elements of the rows beside it, which
+// another block may be writing: they are read and not used.
+template <typename T>
+__device__ __forceinline__ bool word_inside(const void *from, int64_t ld, int rows, int cols, int r, int c) {
+  if (r >= 8 && r + 8 < rows) return true;  // (at least as many elements on both sides)
+  const int64_t word = reinterpret_cast<int64_t>(at<T>(from, r, ld)) + c * (int64_t)sizeof(T);
+  return word >= reinterpret_cast<int64_t>(from) && word + 16 <= reinterpret_cast<int64_t>(at<T>(from, rows - 1, ld) + cols);
+}
+
 // Forward for rows that fit the registers: a thread holds NV vectors of V columns, so the
-// row is read once.  WARP: a warp has a row (four rows a block), else a block.
-template <typename T, int V, int NV, bool WARP>
+// row is read once.  WARP: a warp has a row (four rows a block), else a block.  SHIFT: the
+// rows start off 16-byte boundaries, all tensors' by as much: vectors lie on the
+// boundaries, the first and last of a row with elements that are not its own, the weights
+// turned to them (16384 x 4095 bf16 with the sum 177 us, 414 with single elements; 60000 x
+// 1001 199 and 251; 16384 x 999 without it 43 and 38).  What is left over whole vectors' 85 us
+// are instructions, 1.7 times as many.
+template <typename T, int V, int NV, bool WARP, bool SHIFT>
 __global__ void __launch_bounds__(WARP ? 128 : 1024) layer_norm_held_kernel(const Fwd p) {
   __shared__ float buf[2 * 32];
   const int warps = WARP ? 1 : blockDim.x / 32, warp = WARP ? 0 : threadIdx.x / 32;
@@ -171,22 +214,35 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) layer_norm_held_kernel(cons
   for (int r = blockIdx.x * each + (WARP ? (int)threadIdx.x / 32 : 0); r < p.rows; r += gridDim.x * each) {
     const T *x = at<T>(p.x, r, p.ldx), *add = p.add ? at<T>(p.add, r, p.ld_add) : nullptr;
     float s[NV][V], m[1] = {0.f}, v[1] = {0.f};
-    auto column = [&](int j) { return (thread + j * threads) * V; };
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (column(j) < p.cols) {
-        load<T, V>(x + column(j), s[j]);
+    const int off = SHIFT ? (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T)) : 0;
+    auto column = [&](int j) { return (thread + j * threads) * V - off; };
+    auto whole = [&](int c) { return !SHIFT || (c >= 0 && c + V <= p.cols); };
+    auto get = [&](const T *row, int c, float(&f)[V]) {  // zeros past the row's ends
+      if (SHIFT) {
+        load_part<T, V>(row, c, p.cols, f);
+      } else if (c < p.cols) {
+        load<T, V>(row + c, f);
       } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[j][i] = 0.f;
+        for (int i = 0; i < V; ++i) f[i] = 0.f;
       }
-    }
+    };
+    auto weights = [&](const void *q, int c, float(&f)[V]) {
+      if (SHIFT) unpack<T, V>(load_turned<T, V>(reinterpret_cast<const T *>(q), c, p.cols), f);
+      else load<T, V>(reinterpret_cast<const T *>(q) + c, f);
+    };
+    auto put = [&](T *row, int c, const float(&f)[V]) {
+      if (SHIFT) store_part<T, V>(row, c, p.cols, f);
+      else store<T, V>(row + c, f);
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) get(x, column(j), s[j]);
     if (add) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (column(j) < p.cols) {
           float t[V];
-          load<T, V>(add + column(j), t);
+          get(add, column(j), t);
 #pragma unroll
           for (int i = 0; i < V; ++i) s[j][i] += t[i];
         }
@@ -204,7 +260,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) layer_norm_held_kernel(cons
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const float d = s[j][i] * scale - mean;
-            v[0] += d * d;
+            if (whole(column(j)) || (column(j) + i >= 0 && column(j) + i < p.cols)) v[0] += d * d;
           }
       group_sums<1>(v, buf, warp, warps, turn);
     };
@@ -237,31 +293,31 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) layer_norm_held_kernel(cons
     for (int j = 0; j < NV; ++j) {
       const int c = column(j);
       if (c >= p.cols) continue;
-      if (p.sum) store<T, V>(at<T>(p.sum, r, p.ld_sum) + c, s[j]);
+      if (p.sum) put(at<T>(p.sum, r, p.ld_sum), c, s[j]);
       if (!p.h) continue;
       float t[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) s[j][i] = (s[j][i] - mean) * rstd;
       if (p.w) {
-        load<T, V>(reinterpret_cast<const T *>(p.w) + c, t);
+        weights(p.w, c, t);
 #pragma unroll
         for (int i = 0; i < V; ++i) s[j][i] *= t[i];
       }
       if (p.b) {
-        load<T, V>(reinterpret_cast<const T *>(p.b) + c, t);
+        weights(p.b, c, t);
 #pragma unroll
         for (int i = 0; i < V; ++i) s[j][i] += t[i];
       }
-      store<T, V>(at<T>(p.h, r, p.ldh) + c, s[j]);
+      put(at<T>(p.h, r, p.ldh), c, s[j]);
     }
   }
 }
 
 // Backward for rows of up to 8192 columns, everything in one pass: a block walks its rows, a
 // thread has the same NV vectors of V columns of each and keeps their two column sums in
-// registers.  AHEAD: the next row's vectors are loaded before this row's sums.
-template <typename T, int V, int NV, bool AHEAD>
-__global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_bwd_kernel(const Bwd p) {
+// registers.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(1024) layer_norm_bwd_kernel(const Bwd p) {
   __shared__ float buf[2 * 32 * 2];
   using Raw = typename std::conditional<V == 1, T, uint4>::type;
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
@@ -296,11 +352,8 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_bwd_kernel(cons
     for (int i = 0; i < V; ++i) sum_w[j][i] = sum_b[j][i] = 0.f;
   }
   Row now;
-  if (AHEAD && (int)blockIdx.x < p.rows) fetch(now, blockIdx.x);
   for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
-    Row next;
-    if (!AHEAD) fetch(now, r);
-    else if (r + (int)gridDim.x < p.rows) fetch(next, r + gridDim.x);
+    fetch(now, r);
     float v[2] = {0.f, 0.f};
     auto g_and_n = [&](int j, float(&h)[V], float(&g)[V], float(&n)[V]) {
       values(now.dh[j], h);
@@ -347,7 +400,6 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_bwd_kernel(cons
         store<T, V>(at<T>(p.dx, r, p.ld_dx) + column(j), g);
       }
     }
-    if (AHEAD) now = next;
   }
   if (!p.dw && !p.db) return;
 #pragma unroll
@@ -362,22 +414,41 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_bwd_kernel(cons
   }
 }
 
-// The same for rows in 16-byte vectors whose tensors fit shared memory four rows deep: two rows
+// The same with 16-byte vectors, for rows whose tensors fit shared memory four rows deep: two rows
 // at a time, so that both take one block reduction, and the rows after them on their
 // way (cp.async, each thread into its own shared memory: no barrier guards the copies).
 // With one row at a time out of registers a row's chain (read, reduce, finish) bounds it:
 // 8192 x 7168 114 us, 91 so.
-template <typename T, int NV>
-__global__ void __launch_bounds__(512) layer_norm_bwd_staged_kernel(const Bwd p, int pairs, int arrays) {
+// SHIFT: the rows start off 16-byte boundaries, all tensors' by as much; the grid is a
+// multiple of the rows after which that repeats, so that a block's rows start alike and its
+// threads keep their columns: vectors on the boundaries, the first and last of a row with
+// elements that are not its own.  Those are copied all the same (a wait for single elements
+// costs more than all the rest) and taken as zeros, but not past the first and last row.
+// 16384 x 4095 bf16 130 us, 273 with single elements; 8192 x 7167 134 and 400; 60000 x 1001
+// 177 and 215.  (At most 96 registers: 9 warps twice on an SM; with 101 it was 196 us.)
+template <typename T, int NV, bool SHIFT>
+__global__ void __launch_bounds__(SHIFT ? 640 : 512) layer_norm_bwd_staged_kernel(const Bwd p, int pairs, int arrays) {
   constexpr int V = Elem<T>::VEC;
   extern __shared__ __align__(16) uint4 rows_smem[];
   __shared__ float buf[2 * 128];
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, threads = blockDim.x;
   const float inv = 1.f / p.cols;
   int turn = 0;
-  auto column = [&](int j) { return ((int)threadIdx.x + j * threads) * V; };
+  const int off = SHIFT ? (int)((reinterpret_cast<uintptr_t>(at<T>(p.dh, blockIdx.x, p.ld_dh)) & 15) / sizeof(T)) : 0;
+  auto column = [&](int j) { return ((int)threadIdx.x + j * threads) * V - off; };
+  auto whole = [&](int c) { return !SHIFT || (c >= 0 && c + V <= p.cols); };
   // vector j of array a (dh, s, dsum) of row q of pair slot k
   auto place = [&](int k, int q, int a, int j) { return rows_smem + ((((k * 2 + q) * arrays + a) * NV + j) * threads + threadIdx.x); };
+  auto copy = [&](uint4 *to, const void *from, int64_t ld, int r, int c) {
+    const T *row = at<T>(from, r, ld);
+    if (whole(c) || word_inside<T>(from, ld, p.rows, p.cols, r, c)) {
+      cp_async16(to, row + c);
+    } else {
+      float f[V];
+      load_part<T, V>(row, c, p.cols, f);
+      *to = pack<T, V>(f);
+    }
+  };
   int ahead = blockIdx.x, put = 0;
   const int step = gridDim.x;
   auto fetch = [&]() {
@@ -389,9 +460,9 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_staged_kernel(const Bwd p,
       for (int j = 0; j < NV; ++j) {
         const int c = column(j);
         if (c >= p.cols) continue;
-        cp_async16(place(put, q, 0, j), at<T>(p.dh, r, p.ld_dh) + c);
-        cp_async16(place(put, q, 1, j), at<T>(p.s, r, p.ld_s) + c);
-        if (arrays > 2) cp_async16(place(put, q, 2, j), at<T>(p.dsum, r, p.ld_dsum) + c);
+        copy(place(put, q, 0, j), p.dh, p.ld_dh, r, c);
+        copy(place(put, q, 1, j), p.s, p.ld_s, r, c);
+        if (arrays > 2) copy(place(put, q, 2, j), p.dsum, p.ld_dsum, r, c);
       }
     }
     cp_async_commit();
@@ -402,7 +473,11 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_staged_kernel(const Bwd p,
   float sum_w[NV][V], sum_b[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (p.w && column(j) < p.cols) w[j] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.w) + column(j));
+    if (p.w && column(j) < p.cols) {
+      const T *from = reinterpret_cast<const T *>(p.w);
+      if (SHIFT) w[j] = load_turned<T, V>(from, column(j), p.cols);
+      else w[j] = *reinterpret_cast<const uint4 *>(from + column(j));
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) sum_w[j][i] = sum_b[j][i] = 0.f;
   }
@@ -419,6 +494,22 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_staged_kernel(const Bwd p,
     fetch();
     if (pairs == 2) cp_async_wait<1>();
     else cp_async_wait<2>();
+    if constexpr (SHIFT) {  // the other rows' elements to zeros (so is w beside its columns)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = column(j);
+        if (whole(c) || c >= p.cols) continue;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            T *word = reinterpret_cast<T *>(place(take, q, a, j));
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (c + i < 0 || c + i >= p.cols) word[i] = Elem<T>::put(0.f);
+          }
+      }
+    }
     const bool two = r + step < p.rows;
     const float m[2] = {mean[0], mean[1]}, rs[2] = {rstd[0], rstd[1]};
     statistics(r + 2 * step);
@@ -472,7 +563,9 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_staged_kernel(const Bwd p,
 #pragma unroll
             for (int i = 0; i < V; ++i) g[i] += h[i];
           }
-          store<T, V>(at<T>(p.dx, r + q * step, p.ld_dx) + column(j), g);
+          T *to = at<T>(p.dx, r + q * step, p.ld_dx);
+          if (SHIFT) store_part<T, V>(to, column(j), p.cols, g);
+          else store<T, V>(to + column(j), g);
         }
       }
     }
@@ -484,10 +577,16 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_staged_kernel(const Bwd p,
   for (int j = 0; j < NV; ++j) {
     if (column(j) >= p.cols) continue;
     float *to = p.ws + (int64_t)blockIdx.x * 2 * p.cols + column(j);
+    if constexpr (SHIFT) {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      *reinterpret_cast<float4 *>(to + i) = make_float4(sum_w[j][i], sum_w[j][i + 1], sum_w[j][i + 2], sum_w[j][i + 3]);
-      *reinterpret_cast<float4 *>(to + p.cols + i) = make_float4(sum_b[j][i], sum_b[j][i + 1], sum_b[j][i + 2], sum_b[j][i + 3]);
+      for (int i = 0; i < V; ++i)
+        if (column(j) + i >= 0 && column(j) + i < p.cols) to[i] = sum_w[j][i], to[p.cols + i] = sum_b[j][i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        *reinterpret_cast<float4 *>(to + i) = make_float4(sum_w[j][i], sum_w[j][i + 1], sum_w[j][i + 2], sum_w[j][i + 3]);
+        *reinterpret_cast<float4 *>(to + p.cols + i) = make_float4(sum_b[j][i], sum_b[j][i + 1], sum_b[j][i + 2], sum_b[j][i + 3]);
+      }
     }
   }
 }
@@ -609,16 +708,15 @@ static int threads_of(int cols, int v) { return std::min(512, std::max(32, (cols
 // rows' parts of the column sums in the general kernels
 static int parts_of(int64_t rows, int num_sms) { return (int)std::max<int64_t>(1, std::min<int64_t>((rows + 63) / 64, num_sms)); }
 
-// The one-pass backward out of registers: columns a thread (16 in vectors of 16-bit types, whose
-// raw rows take few registers; 8 in fp32 vectors; single elements 8, or 4 in rows of up to
-// 4096: 4099 x 1001 in fp32 16 us instead of 24), threads, and blocks: what the SMs hold, with
-// some rows each so that the partial sums stay few.
+// The one-pass backward out of registers: columns a thread (8, or 4 single elements in rows of
+// up to 4096: 4099 x 1001 in fp32 16 us instead of 24), threads, and blocks: what the SMs hold,
+// with some rows each so that the partial sums stay few.
 constexpr int FUSED_COLS = 8192, FOUR_COLS = 4096;
 struct BwdShape {
   int threads, blocks;
 };
 static BwdShape bwd_shape(int64_t rows, int cols, int each, int num_sms) {
-  const int threads = (cols + 32 * each - 1) / (32 * each) * 32, resident = (each == 16 ? 512 : 1024) / threads;
+  const int threads = (cols + 32 * each - 1) / (32 * each) * 32, resident = 1024 / threads;
   return {threads, (int)std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, (int64_t)num_sms * std::max(1, std::min(resident, 16))))};
 }
 
@@ -628,40 +726,46 @@ struct StagedShape {
   int threads, blocks, pairs;  // pairs 0: does not fit
   size_t smem;
 };
-static StagedShape staged_shape(int64_t rows, int cols, int size, int arrays, int num_sms) {
-  StagedShape s = {(cols + 511) / 512 * 32, 0, 0, 0};
+static StagedShape staged_shape(int64_t rows, int cols, int size, int arrays, bool shift, int num_sms) {
+  const int alike = shift ? 16 / size : 1;  // rows after which the starts repeat
+  StagedShape s = {(cols + alike - 1 + 511) / 512 * 32, 0, 0, 0};
   const size_t pair = (size_t)2 * arrays * s.threads * 16 * size;
   if (s.threads > 512 || 2 * pair > STAGED_SMEM) return s;
-  const int resident = std::max(1, std::min({512 / s.threads, 16, (int)(STAGED_SMEM / (2 * pair))}));
+  const int resident = std::max(1, std::min({(shift ? 576 : 512) / s.threads, 16, (int)(STAGED_SMEM / (2 * pair))}));
   s.pairs = STAGED_SMEM / resident >= 3 * pair + 2048 ? 3 : 2;
   s.smem = s.pairs * pair;
   s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>((rows + 7) / 8, (int64_t)num_sms * resident));
+  s.blocks = std::max(alike, s.blocks / alike * alike);
   return s;
 }
 
-template <typename T, int V>
+constexpr int HELD_COLS = 32768;  // of a row in a block's registers, 32 a thread
+template <typename T, int V, bool SHIFT>
 static cudaError_t fwd(const Fwd &p, int num_sms, cudaStream_t st) {
-  constexpr int NV = V == 8 ? 4 : V == 4 ? 8 : 32, EACH = NV * V;  // 32 columns a thread
-  if (p.cols <= 32 * EACH) {
+  constexpr int NV = V == 8 ? 4 : V == 4 ? 8 : 32, EACH = NV * V;
+  static_assert(1024 * EACH == HELD_COLS, "columns of a block");
+  const int cols = SHIFT ? p.cols + V - 1 : p.cols;  // with what may lie before a row
+  if (cols <= 32 * EACH) {
     const int blocks = (p.rows + 3) / 4;
-    layer_norm_held_kernel<T, V, NV, true><<<blocks, 128, 0, st>>>(p);
-  } else if (p.cols <= 1024 * EACH) {
-    layer_norm_held_kernel<T, V, NV, false><<<p.rows, (p.cols + 32 * EACH - 1) / (32 * EACH) * 32, 0, st>>>(p);
+    layer_norm_held_kernel<T, V, NV, true, SHIFT><<<blocks, 128, 0, st>>>(p);
+  } else if (SHIFT || cols <= HELD_COLS) {
+    layer_norm_held_kernel<T, V, NV, false, SHIFT><<<p.rows, (cols + 32 * EACH - 1) / (32 * EACH) * 32, 0, st>>>(p);
   } else {
     layer_norm_kernel<T, V><<<std::min(p.rows, num_sms * 8), threads_of(p.cols, V), 0, st>>>(p);
   }
   return cudaGetLastError();
 }
-template <typename T, int V>
+template <typename T, int V, bool SHIFT>
 static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
   const bool sums = p.dw || p.db;
   auto join = [&]() { return launch_pdl(layer_norm_join_kernel<T>, dim3((p.cols + 31) / 32, 2), dim3(1024), 0, st, p); };
-  if constexpr (V > 1) {
+  if constexpr (V > 1 || SHIFT) {
     const int arrays = p.dsum ? 3 : 2;
-    const StagedShape s = staged_shape(p.rows, p.cols, sizeof(T), arrays, num_sms);
+    const StagedShape s = staged_shape(p.rows, p.cols, sizeof(T), arrays, SHIFT, num_sms);
     if (s.pairs) {
-      auto kern = layer_norm_bwd_staged_kernel<T, 16 / V>;
+      auto kern = layer_norm_bwd_staged_kernel<T, 16 / Elem<T>::VEC, SHIFT>;
       cudaError_t err = allow_smem(kern, STAGED_SMEM);
+      if (err == cudaSuccess) err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (err != cudaSuccess) return err;
       p.parts = s.blocks;
       kern<<<s.blocks, s.threads, s.smem, st>>>(p, s.pairs, arrays);
@@ -671,10 +775,12 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
   }
   if (p.cols <= FUSED_COLS) {
     const bool four = V == 1 && p.cols <= FOUR_COLS;
-    const BwdShape s = bwd_shape(p.rows, p.cols, V == 8 ? 16 : four ? 4 : 8, num_sms);
+    const BwdShape s = bwd_shape(p.rows, p.cols, four ? 4 : 8, num_sms);
     p.parts = s.blocks;
-    if (four) layer_norm_bwd_kernel<T, V, V == 1 ? 4 : 2, V == 8><<<s.blocks, s.threads, 0, st>>>(p);
-    else layer_norm_bwd_kernel<T, V, V == 1 ? 8 : 2, V == 8><<<s.blocks, s.threads, 0, st>>>(p);
+    if constexpr (V != 8) {  // (16-bit vectors of so many columns fit shared memory)
+      if (four) layer_norm_bwd_kernel<T, V, V == 1 ? 4 : 2><<<s.blocks, s.threads, 0, st>>>(p);
+      else layer_norm_bwd_kernel<T, V, V == 1 ? 8 : 2><<<s.blocks, s.threads, 0, st>>>(p);
+    }
     const cudaError_t err = cudaGetLastError();
     return err != cudaSuccess || !sums ? err : join();
   }
@@ -697,9 +803,10 @@ size_t layer_norm_workspace(int64_t rows, int cols, int num_sms) {
   using namespace layer;
   int parts = parts_of(rows, num_sms);
   for (int size : {2, 4})
-    for (int arrays : {2, 3}) parts = std::max(parts, staged_shape(rows, cols, size, arrays, num_sms).blocks);
+    for (int arrays : {2, 3})
+      for (bool shift : {false, true}) parts = std::max(parts, staged_shape(rows, cols, size, arrays, shift, num_sms).blocks);
   if (cols <= FUSED_COLS) 
-    for (int each : {4, 8, 16})
+    for (int each : {4, 8})
       if (each > 4 || cols <= FOUR_COLS) parts = std::max(parts, bwd_shape(rows, cols, each, num_sms).blocks);
   return (size_t)parts * 2 * cols * sizeof(float);
 }
@@ -712,9 +819,17 @@ cudaError_t launch_layer_norm(const sym_layer_norm &a, int num_sms, cudaStream_t
   const bool vec = vec_ok({p.x, p.add, p.w, p.b, p.sum, p.h},
                           {one ? 0 : p.ldx, p.add && !one ? p.ld_add : 0, p.sum && !one ? p.ld_sum : 0, p.h && !one ? p.ldh : 0},
                           p.cols, es);
-  if (a.dtype == SYM_BF16) return vec ? fwd<__nv_bfloat16, 8>(p, num_sms, st) : fwd<__nv_bfloat16, 1>(p, num_sms, st);
-  if (a.dtype == SYM_FP16) return vec ? fwd<__half, 8>(p, num_sms, st) : fwd<__half, 1>(p, num_sms, st);
-  return vec ? fwd<float, 4>(p, num_sms, st) : fwd<float, 1>(p, num_sms, st);
+  // every row of all tensors as far off a boundary as x's
+  auto like_x = [&](const void *q, int64_t ld) {
+    return !q || ((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p.x)) % 16 == 0 && (one || (ld - p.ldx) * es % 16 == 0));
+  };
+  const bool shift = !vec && p.cols + 16 / es - 1 <= HELD_COLS && like_x(p.add, p.ld_add) && like_x(p.sum, p.ld_sum) && like_x(p.h, p.ldh);
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    constexpr int V = Elem<T>::VEC;
+    return vec ? fwd<T, V, false>(p, num_sms, st) : shift ? fwd<T, V, true>(p, num_sms, st) : fwd<T, 1, false>(p, num_sms, st);
+  };
+  return a.dtype == SYM_BF16 ? go(__nv_bfloat16()) : a.dtype == SYM_FP16 ? go(__half()) : go(float());
 }
 
 cudaError_t launch_layer_norm_bwd(const sym_layer_norm_grad &a, int num_sms, cudaStream_t st) {
@@ -726,9 +841,19 @@ cudaError_t launch_layer_norm_bwd(const sym_layer_norm_grad &a, int num_sms, cud
   const bool vec = vec_ok({p.dh, p.s, p.dsum, p.w, p.dx, p.dw, p.db},
                           {one ? 0 : p.ld_dh, one ? 0 : p.ld_s, p.dsum && !one ? p.ld_dsum : 0, p.dx && !one ? p.ld_dx : 0},
                           p.cols, es);
-  if (a.dtype == SYM_BF16) return vec ? bwd<__nv_bfloat16, 8>(p, num_sms, st) : bwd<__nv_bfloat16, 1>(p, num_sms, st);
-  if (a.dtype == SYM_FP16) return vec ? bwd<__half, 8>(p, num_sms, st) : bwd<__half, 1>(p, num_sms, st);
-  return vec ? bwd<float, 4>(p, num_sms, st) : bwd<float, 1>(p, num_sms, st);
+  // every row of all tensors as far off a boundary as dh's (not for 32 bits, where single
+  // elements do as well: 8192 x 4095 151 us so and 155, 4099 x 1001 29 and 22)
+  auto like_dh = [&](const void *q, int64_t ld) {
+    return !q || ((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p.dh)) % 16 == 0 && (one || (ld - p.ld_dh) * es % 16 == 0));
+  };
+  const bool shift = !vec && es == 2 && like_dh(p.s, p.ld_s) && like_dh(p.dsum, p.ld_dsum) && like_dh(p.dx, p.ld_dx);
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    if constexpr (sizeof(T) == 2)
+      if (shift) return bwd<T, 1, true>(p, num_sms, st);
+    return vec ? bwd<T, Elem<T>::VEC, false>(p, num_sms, st) : bwd<T, 1, false>(p, num_sms, st);
+  };
+  return a.dtype == SYM_BF16 ? go(__nv_bfloat16()) : a.dtype == SYM_FP16 ? go(__half()) : go(float());
 }
 
 }  // namespace symmoe

@@ -163,6 +163,44 @@ def test_in_place(dt, cols):
         assert torch.equal(t[into], out["dx"]) and torch.equal(dw, out["dw"]) and torch.equal(db, out["db"]), into
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("pad,shift", [(0, 0), (2, 3), (7, 1), (8, 5)])
+@pytest.mark.parametrize("cols", [1, 5, 33, 501, 1017, 4095, 8185, 8187])
+def test_rows_alike_off_boundaries(cols, pad, shift, dt):
+    """All tensors with the same rows' starts; NaN between the rows and in one of them reaches no other."""
+    rows, bad = 60, 20
+    good = [r for r in range(rows) if r != bad]
+
+    def walled(t):
+        out = torch.full((rows * (cols + pad) + shift,), float("nan"), device="cuda", dtype=dt)[shift:].as_strided((rows, cols), t.stride())
+        return out.copy_(t)
+
+    x, add, dh, dsum = (walled(make(rows, cols, dt, pad, shift, seed=i)) for i in range(4))
+    w, b = make(1, cols, dt, 0, 1, seed=5)[0], make(1, cols, dt, 0, 0, seed=6)[0]
+    h, total, dx = like(x), like(x), like(x)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    sm.moe_layer_norm(x, h, w=w, b=b, add=add, sum=total, mean=mean, rstd=rstd)
+    ref = ref_layer_norm(x, w, b, add, 1e-5)
+    for name, got in (("h", h), ("sum", total), ("mean", mean), ("rstd", rstd)):
+        assert_within(got, *ref[name], name)
+    assert untouched(h) and untouched(total)
+    s = walled(total)
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    work = torch.empty(sm.moe_layer_norm_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+    sm.moe_layer_norm_bwd(dh, s, mean, rstd, dx=dx, w=w, dsum=dsum, dw=dw, db=db, work=work)
+    ref = ref_layer_norm_bwd(dh, s, mean, rstd, w, dsum)
+    for name, got in (("dx", dx), ("dw", dw), ("db", db)):
+        assert_within(got, *ref[name], name)
+    assert untouched(dx)
+
+    clean = {"h": h[good], "sum": total[good], "dx": dx[good]}
+    x[bad], dh[bad] = float("nan"), float("nan")
+    sm.moe_layer_norm(x, h, w=w, b=b, add=add, sum=total)
+    assert torch.equal(h[good], clean["h"]) and torch.equal(total[good], clean["sum"]) and bool(h[bad].isnan().all())
+    sm.moe_layer_norm_bwd(dh, s, mean, rstd, dx=dh, w=w, dsum=dsum)  # over its own input
+    assert torch.equal(dh[good], clean["dx"]) and bool(dh[bad].isnan().all())
+
+
 def test_gradient_against_differences():
     """In 32 bits: a step along a direction changes the loss by the gradient's share of it."""
     rows, cols = 5, 192
