@@ -426,16 +426,22 @@ __global__ void __launch_bounds__(1024) layer_norm_bwd_kernel(const Bwd p) {
 // costs more than all the rest) and taken as zeros, but not past the first and last row.
 // 16384 x 4095 bf16 130 us, 273 with single elements; 8192 x 7167 134 and 400; 60000 x 1001
 // 177 and 215.  (At most 96 registers: 9 warps twice on an SM; with 101 it was 196 us.)
-template <typename T, int NV, bool SHIFT>
+// CLUSTER: the blocks of a cluster share rows too long for one, each a run of columns; they
+// read one another's four sums (buffers in turn: one barrier a pair).  4096 x 16383 bf16 187
+// us, 414 with single elements read twice, 2048 x 16383 fp32 184 and 254; not for aligned rows,
+// which are faster read twice (2048 x 16384 fp32 191 us so and 160, 8000 x 8400 bf16 188 and 146).
+template <typename T, int NV, bool SHIFT, bool CLUSTER>
 __global__ void __launch_bounds__(SHIFT ? 640 : 512) layer_norm_bwd_staged_kernel(const Bwd p, int pairs, int arrays) {
   constexpr int V = Elem<T>::VEC;
   extern __shared__ __align__(16) uint4 rows_smem[];
-  __shared__ float buf[2 * 128];
+  __shared__ float buf[2 * 128], cross[2 * 4];
+  const int ranks = CLUSTER ? (int)cluster_size() : 1, rank = CLUSTER ? (int)cluster_rank() : 0;
+  const int unit = blockIdx.x / ranks, step = gridDim.x / ranks;
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, threads = blockDim.x;
   const float inv = 1.f / p.cols;
-  int turn = 0;
-  const int off = SHIFT ? (int)((reinterpret_cast<uintptr_t>(at<T>(p.dh, blockIdx.x, p.ld_dh)) & 15) / sizeof(T)) : 0;
-  auto column = [&](int j) { return ((int)threadIdx.x + j * threads) * V - off; };
+  int turn = 0, cross_turn = 0;
+  const int off = SHIFT ? (int)((reinterpret_cast<uintptr_t>(at<T>(p.dh, unit, p.ld_dh)) & 15) / sizeof(T)) : 0;
+  auto column = [&](int j) { return ((int)threadIdx.x + (rank * NV + j) * threads) * V - off; };
   auto whole = [&](int c) { return !SHIFT || (c >= 0 && c + V <= p.cols); };
   // vector j of array a (dh, s, dsum) of row q of pair slot k
   auto place = [&](int k, int q, int a, int j) { return rows_smem + ((((k * 2 + q) * arrays + a) * NV + j) * threads + threadIdx.x); };
@@ -449,8 +455,7 @@ __global__ void __launch_bounds__(SHIFT ? 640 : 512) layer_norm_bwd_staged_kerne
       *to = pack<T, V>(f);
     }
   };
-  int ahead = blockIdx.x, put = 0;
-  const int step = gridDim.x;
+  int ahead = unit, put = 0;
   auto fetch = [&]() {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -488,9 +493,9 @@ __global__ void __launch_bounds__(SHIFT ? 640 : 512) layer_norm_bwd_staged_kerne
       if (r + q * step < p.rows) mean[q] = p.mean[r + q * step], rstd[q] = p.rstd[r + q * step];
   };
   for (int k = 0; k + 1 < pairs; ++k) fetch();
-  statistics(blockIdx.x);
+  statistics(unit);
   int take = 0;
-  for (int r = blockIdx.x; r < p.rows; r += 2 * step) {
+  for (int r = unit; r < p.rows; r += 2 * step) {
     fetch();
     if (pairs == 2) cp_async_wait<1>();
     else cp_async_wait<2>();
@@ -547,6 +552,20 @@ __global__ void __launch_bounds__(SHIFT ? 640 : 512) layer_norm_bwd_staged_kerne
     }
     if (p.dx) {
       block_sums4(v, buf, warp, warps, turn);
+      if constexpr (CLUSTER) {
+        const int lane = threadIdx.x & 31;
+        float *mine = cross + cross_turn * 4;
+        cross_turn ^= 1;
+        if (threadIdx.x == 0)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mine[k] = v[k];
+        cluster_barrier();
+        float sum = lane < 4 * ranks ? load_from(mine + (lane & 3), lane >> 2) : 0.f;
+#pragma unroll
+        for (int d = 16; d > 2; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(~0u, sum, k);
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         if (q && !two) break;
@@ -572,11 +591,12 @@ __global__ void __launch_bounds__(SHIFT ? 640 : 512) layer_norm_bwd_staged_kerne
     take = take + 1 == pairs ? 0 : take + 1;
   }
   cp_async_wait<0>();
+  if (CLUSTER) cluster_barrier();  // nobody leaves before its sums are read
   if (!p.dw && !p.db) return;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     if (column(j) >= p.cols) continue;
-    float *to = p.ws + (int64_t)blockIdx.x * 2 * p.cols + column(j);
+    float *to = p.ws + (int64_t)unit * 2 * p.cols + column(j);
     if constexpr (SHIFT) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -720,21 +740,28 @@ static BwdShape bwd_shape(int64_t rows, int cols, int each, int num_sms) {
   return {threads, (int)std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, (int64_t)num_sms * std::max(1, std::min(resident, 16))))};
 }
 
-// The staged form of it: 16 columns a thread, two or three pairs of rows in shared memory
+// The staged form of it: 16 columns a thread, two or three pairs of rows in shared memory; rows
+// off 16-byte boundaries that are longer than the register form's are shared by two to eight blocks
 constexpr int STAGED_SMEM = 220 * 1024;
 struct StagedShape {
-  int threads, blocks, pairs;  // pairs 0: does not fit
+  int threads, ranks, blocks, pairs;  // blocks: times ranks; pairs 0: does not fit
   size_t smem;
 };
 static StagedShape staged_shape(int64_t rows, int cols, int size, int arrays, bool shift, int num_sms) {
   const int alike = shift ? 16 / size : 1;  // rows after which the starts repeat
-  StagedShape s = {(cols + alike - 1 + 511) / 512 * 32, 0, 0, 0};
-  const size_t pair = (size_t)2 * arrays * s.threads * 16 * size;
-  if (s.threads > 512 || 2 * pair > STAGED_SMEM) return s;
+  StagedShape s = {0, 1, 0, 0};
+  size_t pair;
+  for (;; s.ranks *= 2) {
+    const int each = (cols + alike - 1 + s.ranks - 1) / s.ranks;
+    s.threads = (each + 511) / 512 * 32;
+    pair = (size_t)2 * arrays * s.threads * 16 * size;
+    if (s.threads <= 512 && 2 * pair <= STAGED_SMEM) break;
+    if (!shift || cols <= FUSED_COLS || s.ranks == 8) return s;
+  }
   const int resident = std::max(1, std::min({(shift ? 576 : 512) / s.threads, 16, (int)(STAGED_SMEM / (2 * pair))}));
   s.pairs = STAGED_SMEM / resident >= 3 * pair + 2048 ? 3 : 2;
   s.smem = s.pairs * pair;
-  s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>((rows + 7) / 8, (int64_t)num_sms * resident));
+  s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>((rows + 7) / 8, (int64_t)num_sms * resident / s.ranks));
   s.blocks = std::max(alike, s.blocks / alike * alike);
   return s;
 }
@@ -763,13 +790,27 @@ static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
     const int arrays = p.dsum ? 3 : 2;
     const StagedShape s = staged_shape(p.rows, p.cols, sizeof(T), arrays, SHIFT, num_sms);
     if (s.pairs) {
-      auto kern = layer_norm_bwd_staged_kernel<T, 16 / Elem<T>::VEC, SHIFT>;
-      cudaError_t err = allow_smem(kern, STAGED_SMEM);
-      if (err == cudaSuccess) err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-      if (err != cudaSuccess) return err;
       p.parts = s.blocks;
-      kern<<<s.blocks, s.threads, s.smem, st>>>(p, s.pairs, arrays);
-      err = cudaGetLastError();
+      auto launch = [&](auto kern) {
+        cudaError_t err = allow_smem(kern, STAGED_SMEM);
+        if (err != cudaSuccess) return err;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(s.blocks * s.ranks);
+        cfg.blockDim = dim3(s.threads);
+        cfg.dynamicSmemBytes = s.smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = s.ranks, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = s.ranks > 1;
+        return cudaLaunchKernelEx(&cfg, kern, p, (int)s.pairs, (int)arrays);
+      };
+      cudaError_t err = cudaSuccess;
+      if constexpr (SHIFT)
+        if (s.ranks > 1) err = launch(layer_norm_bwd_staged_kernel<T, 16 / Elem<T>::VEC, true, true>);
+      if constexpr (!SHIFT || sizeof(T) == 2)
+        if (s.ranks == 1) err = launch(layer_norm_bwd_staged_kernel<T, 16 / Elem<T>::VEC, SHIFT, false>);
       return err != cudaSuccess || !sums ? err : join();
     }
   }
@@ -841,17 +882,15 @@ cudaError_t launch_layer_norm_bwd(const sym_layer_norm_grad &a, int num_sms, cud
   const bool vec = vec_ok({p.dh, p.s, p.dsum, p.w, p.dx, p.dw, p.db},
                           {one ? 0 : p.ld_dh, one ? 0 : p.ld_s, p.dsum && !one ? p.ld_dsum : 0, p.dx && !one ? p.ld_dx : 0},
                           p.cols, es);
-  // every row of all tensors as far off a boundary as dh's (not for 32 bits, where single
+  // every row of all tensors as far off a boundary as dh's (in 32 bits of long rows alone: of others single
   // elements do as well: 8192 x 4095 151 us so and 155, 4099 x 1001 29 and 22)
   auto like_dh = [&](const void *q, int64_t ld) {
     return !q || ((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p.dh)) % 16 == 0 && (one || (ld - p.ld_dh) * es % 16 == 0));
   };
-  const bool shift = !vec && es == 2 && like_dh(p.s, p.ld_s) && like_dh(p.dsum, p.ld_dsum) && like_dh(p.dx, p.ld_dx);
+  const bool shift = !vec && (es == 2 || p.cols > FUSED_COLS) && like_dh(p.s, p.ld_s) && like_dh(p.dsum, p.ld_dsum) && like_dh(p.dx, p.ld_dx);
   auto go = [&](auto t) {
     using T = decltype(t);
-    if constexpr (sizeof(T) == 2)
-      if (shift) return bwd<T, 1, true>(p, num_sms, st);
-    return vec ? bwd<T, Elem<T>::VEC, false>(p, num_sms, st) : bwd<T, 1, false>(p, num_sms, st);
+    return vec ? bwd<T, Elem<T>::VEC, false>(p, num_sms, st) : shift ? bwd<T, 1, true>(p, num_sms, st) : bwd<T, 1, false>(p, num_sms, st);
   };
   return a.dtype == SYM_BF16 ? go(__nv_bfloat16()) : a.dtype == SYM_FP16 ? go(__half()) : go(float());
 }

@@ -201,6 +201,20 @@ def test_rows_alike_off_boundaries(cols, pad, shift, dt):
     assert torch.equal(dh[good], clean["dx"]) and bool(dh[bad].isnan().all())
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("rows,cols", [(40, 8193), (37, 16384), (50, 9001), (20, 20001), (18, 65536), (9, 65535), (5, 40000), (700, 8200)])
+def test_gradient_of_long_rows(rows, cols, dt):
+    """Rows that several blocks share, or that are walked again."""
+    test_backward(rows, cols, dt)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("pad,shift", [(0, 0), (7, 1)])
+@pytest.mark.parametrize("cols", [8200, 16381, 33001])
+def test_long_rows_alike_off_boundaries(cols, pad, shift, dt):
+    test_rows_alike_off_boundaries(cols, pad, shift, dt)
+
+
 def test_gradient_against_differences():
     """In 32 bits: a step along a direction changes the loss by the gradient's share of it."""
     rows, cols = 5, 192
