@@ -197,55 +197,108 @@ __device__ __forceinline__ bool word_inside(const void *from, int64_t ld, int ro
 }
 
 // Forward for rows that fit the registers: a thread holds NV vectors of V columns, so the
-// row is read once.  WARP: a warp has a row (four rows a block), else a block.  SHIFT: the
-// rows start off 16-byte boundaries, all tensors' by as much: vectors lie on the
-// boundaries, the first and last of a row with elements that are not its own, the weights
-// turned to them (16384 x 4095 bf16 with the sum 177 us, 414 with single elements; 60000 x
-// 1001 199 and 251; 16384 x 999 without it 43 and 38).  What is left over whole vectors' 85 us
-// are instructions, 1.7 times as many.
+// row is read once.  WARP: a warp has a row (four rows a block), else a block.
+//
+// SHIFT: the rows start off 16-byte boundaries, all tensors' by as much; the grid is a multiple
+// of the rows after which that repeats, so that a block's (a warp's) rows start alike.  Vectors
+// lie on the boundaries, the first and last of a row with elements that are not its own.  They
+// are read all the same, but not past the first and last row, and all words of a row before the
+// first is looked at: with a branch around each read a row's latencies add up (16384 x 4095 bf16
+// with the sum 174 us, 60000 x 1001 195).  The weights are turned to the vectors once, into
+// shared memory.  So 16384 x 4095 140 us, 414 with single elements; 8192 x 7167 110 and 392;
+// 60000 x 1001 118 and 251; fp32 8192 x 4095 112 and 219, 4099 x 1001 18 and 19.  Whole vectors
+// take 85 us: what is left are instructions and the registers (the most threads with little
+// spilled; with 1024 and 64 registers 131, 109 and fp32 143 us, with 640 137, 132 and 101).
+constexpr int SHIFT_THREADS = 768;
 template <typename T, int V, int NV, bool WARP, bool SHIFT>
-__global__ void __launch_bounds__(WARP ? 128 : 1024) layer_norm_held_kernel(const Fwd p) {
+__global__ void __launch_bounds__(WARP ? 128 : SHIFT ? SHIFT_THREADS : 1024, WARP && SHIFT ? 4 : 1) layer_norm_held_kernel(const Fwd p) {
   __shared__ float buf[2 * 32];
+  extern __shared__ __align__(16) uint4 weights_smem[];
   const int warps = WARP ? 1 : blockDim.x / 32, warp = WARP ? 0 : threadIdx.x / 32;
   const int thread = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
   const int each = WARP ? blockDim.x / 32 : 1;
   const float inv = 1.f / p.cols;
   int turn = 0;
-  for (int r = blockIdx.x * each + (WARP ? (int)threadIdx.x / 32 : 0); r < p.rows; r += gridDim.x * each) {
+  const int first = blockIdx.x * each + (WARP ? (int)threadIdx.x / 32 : 0);
+  const int off = SHIFT ? (int)((reinterpret_cast<uintptr_t>(at<T>(p.x, first, p.ldx)) & 15) / sizeof(T)) : 0;
+  auto column = [&](int j) { return (thread + j * threads) * V - off; };
+  auto whole = [&](int c) { return !SHIFT || (c >= 0 && c + V <= p.cols); };
+  auto own = [&](int c) { return c >= 0 && c < p.cols; };
+  auto mine = [&](int k, int j) { return weights_smem + (k * NV + j) * (int)blockDim.x + threadIdx.x; };
+  if (SHIFT) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (column(j) >= p.cols) continue;
+      if (p.w) *mine(0, j) = load_turned<T, V>(reinterpret_cast<const T *>(p.w), column(j), p.cols);
+      if (p.b) *mine(1, j) = load_turned<T, V>(reinterpret_cast<const T *>(p.b), column(j), p.cols);
+    }
+  }
+  for (int r = first; r < p.rows; r += gridDim.x * each) {
     const T *x = at<T>(p.x, r, p.ldx), *add = p.add ? at<T>(p.add, r, p.ld_add) : nullptr;
     float s[NV][V], m[1] = {0.f}, v[1] = {0.f};
-    const int off = SHIFT ? (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T)) : 0;
-    auto column = [&](int j) { return (thread + j * threads) * V - off; };
-    auto whole = [&](int c) { return !SHIFT || (c >= 0 && c + V <= p.cols); };
-    auto get = [&](const T *row, int c, float(&f)[V]) {  // zeros past the row's ends
-      if (SHIFT) {
-        load_part<T, V>(row, c, p.cols, f);
-      } else if (c < p.cols) {
-        load<T, V>(row + c, f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = 0.f;
-      }
-    };
-    auto weights = [&](const void *q, int c, float(&f)[V]) {
-      if (SHIFT) unpack<T, V>(load_turned<T, V>(reinterpret_cast<const T *>(q), c, p.cols), f);
-      else load<T, V>(reinterpret_cast<const T *>(q) + c, f);
+    auto weights = [&](int k, int j, float(&f)[V]) {
+      if constexpr (SHIFT) unpack<T, V>(*mine(k, j), f);
+      else load<T, V>(reinterpret_cast<const T *>(k ? p.b : p.w) + column(j), f);
     };
     auto put = [&](T *row, int c, const float(&f)[V]) {
       if (SHIFT) store_part<T, V>(row, c, p.cols, f);
       else store<T, V>(row + c, f);
     };
+    if constexpr (SHIFT) {  // words first, all of them under way, then their elements
+      uint4 raw[NV];
+      auto fetch = [&](const T *row) {
+        if (r >= 8 && r + 8 < p.rows) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) get(x, column(j), s[j]);
-    if (add) {
+          for (int j = 0; j < NV; ++j)
+            raw[j] = column(j) < p.cols ? *reinterpret_cast<const uint4 *>(row + column(j)) : make_uint4(0, 0, 0, 0);
+        } else {  // (a word may reach past the tensor)
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (column(j) < p.cols) {
+          for (int j = 0; j < NV; ++j) {
+            float f[V];
+            load_part<T, V>(row, column(j), p.cols, f);
+            raw[j] = pack<T, V>(f);
+          }
+        }
+      };
+      auto values = [&](int j, float(&f)[V]) {
+        unpack<T, V>(raw[j], f);
+        if (!whole(column(j)))
+#pragma unroll
+          for (int i = 0; i < V; ++i) f[i] = own(column(j) + i) ? f[i] : 0.f;
+      };
+      fetch(x);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) values(j, s[j]);
+      if (add) {
+        fetch(add);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
           float t[V];
-          get(add, column(j), t);
+          values(j, t);
 #pragma unroll
           for (int i = 0; i < V; ++i) s[j][i] += t[i];
         }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (column(j) < p.cols) {
+          load<T, V>(x + column(j), s[j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) s[j][i] = 0.f;
+        }
+      }
+      if (add) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (column(j) < p.cols) {
+            float t[V];
+            load<T, V>(add + column(j), t);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[j][i] += t[i];
+          }
+      }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -260,7 +313,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) layer_norm_held_kernel(cons
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const float d = s[j][i] * scale - mean;
-            if (whole(column(j)) || (column(j) + i >= 0 && column(j) + i < p.cols)) v[0] += d * d;
+            if (whole(column(j)) || own(column(j) + i)) v[0] += d * d;
           }
       group_sums<1>(v, buf, warp, warps, turn);
     };
@@ -299,12 +352,12 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) layer_norm_held_kernel(cons
 #pragma unroll
       for (int i = 0; i < V; ++i) s[j][i] = (s[j][i] - mean) * rstd;
       if (p.w) {
-        weights(p.w, c, t);
+        weights(0, j, t);
 #pragma unroll
         for (int i = 0; i < V; ++i) s[j][i] *= t[i];
       }
       if (p.b) {
-        weights(p.b, c, t);
+        weights(1, j, t);
 #pragma unroll
         for (int i = 0; i < V; ++i) s[j][i] += t[i];
       }
@@ -767,20 +820,33 @@ static StagedShape staged_shape(int64_t rows, int cols, int size, int arrays, bo
 }
 
 constexpr int HELD_COLS = 32768;  // of a row in a block's registers, 32 a thread
+// ... and off 16-byte boundaries, whose turned weights take 64 elements a thread of shared memory
+static int shifted_cols(int size) { return std::min(SHIFT_THREADS, STAGED_SMEM / (64 * size) / 32 * 32) * 32 - (16 / size - 1); }
 template <typename T, int V, bool SHIFT>
 static cudaError_t fwd(const Fwd &p, int num_sms, cudaStream_t st) {
   constexpr int NV = V == 8 ? 4 : V == 4 ? 8 : 32, EACH = NV * V;
   static_assert(1024 * EACH == HELD_COLS, "columns of a block");
   const int cols = SHIFT ? p.cols + V - 1 : p.cols;  // with what may lie before a row
-  if (cols <= 32 * EACH) {
-    const int blocks = (p.rows + 3) / 4;
-    layer_norm_held_kernel<T, V, NV, true, SHIFT><<<blocks, 128, 0, st>>>(p);
-  } else if (SHIFT || cols <= HELD_COLS) {
-    layer_norm_held_kernel<T, V, NV, false, SHIFT><<<p.rows, (cols + 32 * EACH - 1) / (32 * EACH) * 32, 0, st>>>(p);
-  } else {
+  const bool warp = cols <= 32 * EACH;
+  if (!SHIFT && cols > HELD_COLS) {
     layer_norm_kernel<T, V><<<std::min(p.rows, num_sms * 8), threads_of(p.cols, V), 0, st>>>(p);
+    return cudaGetLastError();
   }
-  return cudaGetLastError();
+  const int threads = warp ? 128 : (cols + 32 * EACH - 1) / (32 * EACH) * 32;
+  int blocks = warp ? (p.rows + 3) / 4 : p.rows;
+  size_t smem = 0;
+  auto launch = [&](auto kern) {
+    if (SHIFT) {
+      smem = (size_t)2 * NV * threads * 16;
+      const cudaError_t err = allow_smem(kern, STAGED_SMEM);
+      if (err != cudaSuccess) return err;
+      const int resident = std::max(1, std::min({(warp ? 1024 : SHIFT_THREADS) / threads, 16, (int)(STAGED_SMEM / smem)}));
+      blocks = std::min(blocks, std::max(8, num_sms * resident / 8 * 8));  // (starts repeat after 8 rows or fewer)
+    }
+    kern<<<blocks, threads, smem, st>>>(p);
+    return cudaGetLastError();
+  };
+  return warp ? launch(layer_norm_held_kernel<T, V, NV, true, SHIFT>) : launch(layer_norm_held_kernel<T, V, NV, false, SHIFT>);
 }
 template <typename T, int V, bool SHIFT>
 static cudaError_t bwd(Bwd p, int num_sms, cudaStream_t st) {
@@ -864,7 +930,7 @@ cudaError_t launch_layer_norm(const sym_layer_norm &a, int num_sms, cudaStream_t
   auto like_x = [&](const void *q, int64_t ld) {
     return !q || ((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p.x)) % 16 == 0 && (one || (ld - p.ldx) * es % 16 == 0));
   };
-  const bool shift = !vec && p.cols + 16 / es - 1 <= HELD_COLS && like_x(p.add, p.ld_add) && like_x(p.sum, p.ld_sum) && like_x(p.h, p.ldh);
+  const bool shift = !vec && p.cols <= shifted_cols((int)es) && like_x(p.add, p.ld_add) && like_x(p.sum, p.ld_sum) && like_x(p.h, p.ldh);
   auto go = [&](auto t) {
     using T = decltype(t);
     constexpr int V = Elem<T>::VEC;

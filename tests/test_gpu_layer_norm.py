@@ -215,6 +215,14 @@ def test_long_rows_alike_off_boundaries(cols, pad, shift, dt):
     test_rows_alike_off_boundaries(cols, pad, shift, dt)
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("rows,cols", [(12000, 129), (9001, 1033), (7000, 2051)])
+def test_many_rows_off_boundaries(rows, cols, dt):
+    """More rows than blocks: each block walks several."""
+    test_forward(rows, cols, dt)
+    test_backward(rows, cols, dt)
+
+
 def test_gradient_against_differences():
     """In 32 bits: a step along a direction changes the loss by the gradient's share of it."""
     rows, cols = 5, 192
