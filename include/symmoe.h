@@ -665,8 +665,9 @@ int moe_block_norm_workspace(int64_t rows, int32_t cols, int64_t gate_rows, uint
  *   w, b [cols]: NULL = ones, zeros.  mean, rstd: device fp32 [rows], out (kept
  *   for the backward), each may be NULL.  h may be NULL.
  * All tensors have the type dtype; rows ld_* elements apart; 16-byte vectors are
- * used where a row of every tensor starts on a 16-byte boundary.  h or sum may be
- * x or add, but sum is not h.
+ * used where a row starts on a 16-byte boundary in every tensor, or equally far from
+ * one (what lies between a tensor's rows may then be read, and is not used).  h or sum
+ * may be x or add, but sum is not h.
  * The variance is the mean of the squared distances from the mean, all in fp32.
  * rows < 2^30, cols <= 65536; eps >= 0.  A row whose s holds an infinity or NaN,
  * and only that row, has results that are NaN.
