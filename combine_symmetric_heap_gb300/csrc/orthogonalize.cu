@@ -10,8 +10,8 @@
 // 1.7e-3).  What a product multiplies may be rounded; what is carried from step to
 // step may not, since small singular values grow by a = 3.4 a step and errors
 // beside them likewise:
-//   - X is hi + lo, two fp16 numbers (22 bits): a X is taken of both, B X of hi;
-//   - A and B are their diagonal in fp32 and the rest in fp16.  With D and O for
+//   - X is hi + lo, two fp16 numbers (22 bits): a X is taken of both, B X of hi or of both;
+//   - A and B are their diagonal in fp32 and the rest in fp16, one number or two.  With D and O for
 //     the two, A A = D D + D O + O D + O O: only O O is a product of matrices, the
 //     rest belongs to one element each.  As X comes near to orthogonality the
 //     diagonals come near to constants and the rests to zero, and so does what
@@ -21,8 +21,8 @@
 // of these commute and are symmetric, and their products, of the shorter side, cost less than an update and a Gram
 // matrix.  It is for the first two only: what rounding leaves in A is taken times P
 // squared, up to a^2 = 12, where singular values are small; beside an A of at most one
-// that is nothing yet (relative error of a result 4.2e-4 either way; with the third
-// and fourth step so too, 3e-3).
+// that adds 2e-4 of a result's norm or less (with the third and fourth step so too the error
+// is 3e-3).  Not where products take both parts (PRECISE_SIDE): the shared factors are rounded to 11 bits.
 //
 // All are held times a power of two that keeps them in fp16's range: X (entries at
 // most its largest singular value; 1 / sqrt(m n) at first) times 2^13, A times 2^10, B
@@ -38,10 +38,16 @@ namespace orth {
 using namespace rows;
 using namespace pair;
 
-// A bf16 result rounds by 1.7e-3 of its norm; products of 11-bit operands add 4e-4 to
-// 5e-4.  An fp16 result rounds by 2.1e-4: there the last steps' products are taken of
-// both parts (hi hi + hi lo + lo hi), which leaves the first steps' 1e-4 or less.
-constexpr int PRECISE_STEPS = 3;
+// A bf16 result rounds by 1.7e-3 of its norm, an fp16 result by 2.1e-4; products of 11-bit
+// operands add 3e-4 to 6e-4 where a gradient has a broad rest.  Beside strong directions with little else
+// they add more: what they leave in the other directions, like everything small, grows 3.4 times
+// a step, 480 times in five.  Of a gradient of rank one (the worst) 3e-2 of the norm at a shorter side of 8,
+// 1.1e-2 at 40, 5e-3 at 64, 2e-3 at 256, 8e-4 at 512, 7e-4 at 700.  So products are taken of both parts
+// (hi hi + hi lo + lo hi) in all steps for fp16 results, and for bf16 results of a shorter side up
+// to PRECISE_SIDE in all but the last two, whose errors grow little.  With / without, us: bf16 1 x 256 x
+// 7168 196 / 155, 24 x 512 x 2048 653 / 450, 24 x 512 x 7168 1679 / 997; fp16 (without: in the last three
+// steps) 5 x 1031 x 519 344 / 289, 8 x 2048 x 7168 8011 / 5560.
+constexpr int PRECISE_SIDE = 512, ROUGH_STEPS = 2;
 constexpr float X_SCALE = 8192.f, A_SCALE = 1024.f, B_SCALE = 256.f;
 
 // A matrix' part of the workspace
@@ -277,7 +283,10 @@ struct Prod {
   int M, N, K, tiles_m, tiles, count, tall;
   int splits, split_kb;  // GRAM: parts of the K axis, K blocks of one (parts: where their sums go)
   size_t parts;
-  int passes;  // 1: hi hi;  3: and hi lo, lo hi
+  // 1: hi hi;  3: and hi lo, lo hi before it: the accumulator drops what is below its last
+  // bit at every 16 of K, so the small sums come first (2048 x 7168 of rank one, fp16: off by
+  // 3e-4 of the norm, with hi hi first 1.1e-3)
+  int passes;
   int last;    // the result is the user's: 1 bf16, 2 fp16
   int vec;     // ... with rows of 16-byte vectors
   char *user;
@@ -413,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, SMALL ? 2 :
         const int m0 = ti.i * 256 + (int)rank * 128, n0 = ti.j * tile_n + (int)rank * (tile_n / 2);
         int kb0, kb1;
         blocks(ti, kb0, kb1);
-        for (int pass = 0; ok && pass < p.passes; ++pass) {
+        for (int pass = p.passes; ok && pass-- > 0;) {  // lo hi, hi lo, and hi hi last (Prod::passes)
           const CUtensorMap *ma = &maps.a[pass == 2], *mb = &maps.b[pass == 1];
           for (int kb = kb0; kb < kb1; ++kb) {
             if (!(ok = bar_wait(&rg.empty[rg.stage], rg.phase ^ 1u, ctl))) break;
@@ -777,13 +786,15 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
         update[k].b[h] = p.tall ? sq[h] : x[h];
       }
     }
-    // Two steps with one update (their low parts' places are free: they are not the precise
-    // ones): an update and a Gram matrix, 3 m^2 n operations, against three products of 3 m^3.
+    // products of both parts (PRECISE_SIDE)
+    auto passes_of = [&](int i) { return o.out_dtype == SYM_FP16 || (m <= PRECISE_SIDE && i + ROUGH_STEPS < o.steps) ? 3 : 1; };
+    // Two steps with one update (of single parts: the low ones' places are free): an update and a
+    // Gram matrix, 3 m^2 n operations, against three products of 3 m^3.
     // One launch more, so small products only where n is far from m.  With / without, us: 8 x 2048 x
-    // 7168 3017 / 3300, 4096 x 14336 2634 / 2900, 256 x 7168 154 / 160; 256 x 1024 137 / 126, 5 x 1031 x 519 219 / 209.
+    // 7168 2792 / 3190, 4096 x 14336 2500 / 2843, 3 x 600 x 6000 367 / 399, 520 x 7168 314 / 337; 5 x 1031 x 519 219 / 209.
     const int n_side = std::max(p.rows, p.cols);
     const bool twice = (sq_small ? n_side >= 8 * (int64_t)m : n_side * 2 >= 3 * m) &&
-                       o.steps >= (o.out_dtype == SYM_FP16 ? 2 + PRECISE_STEPS : 2);
+                       o.steps >= 2 && passes_of(0) == 1;
     if (twice) {
       const size_t left[3] = {l.a, a_lo, b_lo};
       for (int k = 0; k < 3; ++k) {
@@ -799,7 +810,7 @@ cudaError_t launch_orthogonalize(const sym_orthogonalize &o, int num_sms, cudaSt
     if (!ok) return cudaErrorInvalidValue;
     for (int i = 0, k = 0; i < o.steps; k ^= 1) {
       const bool both_steps = i == 0 && twice;
-      q.passes = o.out_dtype == SYM_FP16 && i >= o.steps - PRECISE_STEPS ? 3 : 1;
+      q.passes = passes_of(i);
       q.M = q.N = m, q.K = std::max(p.rows, p.cols), q.tiles_m = tm, q.tiles = sq_tiles;
       q.diag = l.diag_a, q.out[0] = l.a, q.out[1] = a_lo, q.ld = l.ld_a;
       q.splits = splits, q.split_kb = split_kb, q.parts = l.parts;

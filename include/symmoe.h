@@ -734,13 +734,19 @@ int moe_layer_norm_workspace(int64_t rows, int32_t cols, uint64_t *bytes);
  *   up by the number of matrices in a turn: another one can change last bits.)
  *   status: device word that SYM_STATUS_TIMEOUT is OR-ed into where one of the
  *   products' internal waits runs out (wait_timeout_us each, 0: 2,000,000), or NULL.
- * X is held in 22 bits (two fp16 numbers) and enters the products as its first
- * 11 (fp16 results: as both in the last three steps); a Gram matrix is held as its
- * diagonal in fp32 and the rest in fp16; products accumulate in fp32 on the tensor
- * cores.  Against exact arithmetic the result is off by a few times 1e-4 of its norm
- * before its rounding (1e-4 for fp16 results; rows of very few elements by up to 1e-3),
- * whatever g's scale, as long as |g| is not far below eps and X's elements stay
- * below 8 in all steps, which they do where the polynomial keeps [0, 1] below it.
+ * X is held in 22 bits (two fp16 numbers); a Gram matrix and its polynomial are held as
+ * their diagonals in fp32 and the rest in fp16; products accumulate in fp32 on the tensor
+ * cores.  Products take 11 bits of an operand, and 22 (of X, and of the Gram matrices' rest) in
+ * all steps for fp16 results and in all but the last two for matrices with a side of 512 or less.
+ * Against exact arithmetic, five steps with (3.4445, -4.7750, 2.0315) are off, before the
+ * result's rounding (1.7e-3 of its norm in bf16, 2.1e-4 in fp16), by
+ *   fp16 results: 2e-4 of the norm; gradients of a few directions with next to nothing (1e-3
+ *   or less) beside them, where errors grow 480 times in five steps, 6e-4 (with a shorter
+ *   side above 2048 in proportion to it);
+ *   bf16 results: 3e-4 to 6e-4, where a gradient has a few directions alone or few
+ *   elements 1.2e-3; matrices with a side below 16 up to 2e-3.
+ * This holds whatever g's scale, as long as |g| is not far below eps and the coefficients
+ * keep the singular values of X below 3.
  */
 typedef struct sym_orthogonalize {
   int32_t count, rows, cols, steps;
