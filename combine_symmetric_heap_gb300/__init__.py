@@ -730,11 +730,13 @@ def moe_orthogonalize_workspace(count: int, rows: int, cols: int, least: bool = 
 
 
 def moe_orthogonalize(g, out, work, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
-                      scale: float = 1.0, status=None, stream=None) -> None:
+                      scale: float = 1.0, status=None, stream=None, wait_timeout_us: int = 0) -> None:
     """out = scale * X after `steps` Newton-Schulz products, X = a X + (b A + c A A) X
     with A = X X^T, from X = g / (norm of g + eps), for every matrix of g [F, C] or
-    [E, F, C] (bf16, fp16 or float32; out bf16 or fp16).  work: a uint8 tensor; status: an
-    int32 word that SYM_STATUS_TIMEOUT is set in if an internal wait runs out."""
+    [E, F, C] (bf16, fp16 or float32; out bf16 or fp16).  work: a uint8 tensor.
+    status: an int32 word that SYM_STATUS_TIMEOUT is set in if an internal wait runs out
+    (wait_timeout_us each, 0: two seconds).  Nothing else tells of it: out is then undefined,
+    so read the word before out is relied on."""
     where = "moe_orthogonalize"
     if not isinstance(g, torch.Tensor) or not isinstance(out, torch.Tensor) or g.dim() not in (2, 3) or len(coeffs) != 3:
         _need(False, where, "tensors [F, C] or [E, F, C] and three coefficients are wanted")
@@ -744,8 +746,8 @@ def moe_orthogonalize(g, out, work, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0
     os_, ol = _batch(out, where)
     wp, wn = _work(work, dev, where)
     a = _pack_orthogonalize(shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], steps, _DTYPES.get(g.dtype, -1),
-                            _DTYPES.get(out.dtype, -1), *coeffs, eps, scale, 0, _word(status, dev, where), gp, op, gs, gl, os_, ol,
-                            wp, wn)
+                            _DTYPES.get(out.dtype, -1), *coeffs, eps, scale, wait_timeout_us, _word(status, dev, where), gp, op, gs, gl,
+                            os_, ol, wp, wn)
     _check(lib().moe_orthogonalize(a, _stream_of(stream, dev)), where)
 
 

@@ -134,7 +134,8 @@ class MoeBlock:
                 way = torch.empty_like(g, memory_format=torch.contiguous_format)
                 work = torch.empty(sm.moe_orthogonalize_workspace(g.shape[0] if g.dim() == 3 else 1, rows, cols),
                                    dtype=torch.uint8, device=g.device)
-                sm.moe_orthogonalize(g, way, work, scale=-orthogonal_lr * max(1.0, rows / cols) ** 0.5)
+                sm.moe_orthogonalize(g, way, work, scale=-orthogonal_lr * max(1.0, rows / cols) ** 0.5,
+                                     status=self.heap.status_word())  # looked at where the heap's is
                 w += way
         self.step += 1  # another dropout mask
 
@@ -180,6 +181,7 @@ def main():
         block.backward((2 / x.shape[1] * diff).bfloat16(), dx)
         end.record()
         block.update(a.lr / x.shape[0], 0.002 if a.update == "orthogonal" else 0.0)
+        assert block.heap.status() == 0  # no product's wait ran out, the updates' among them
         first = float(loss) if first is None else first
         print(f"step {step}: loss {float(loss):.5f}, forward and backward {start.elapsed_time(end):.3f} ms")
     few = torch.empty(min(4, x.shape[0]), x.shape[1], device=dev, dtype=torch.bfloat16)

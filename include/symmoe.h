@@ -733,7 +733,8 @@ int moe_layer_norm_workspace(int64_t rows, int32_t cols, uint64_t *bytes);
  *   workspace makes them.  Contents do not matter before or after.  (Products are cut
  *   up by the number of matrices in a turn: another one can change last bits.)
  *   status: device word that SYM_STATUS_TIMEOUT is OR-ed into where one of the
- *   products' internal waits runs out (wait_timeout_us each, 0: 2,000,000), or NULL.
+ *   products' internal waits runs out (wait_timeout_us each, 0: 2,000,000), or NULL.  Out is
+ *   undefined then, and nothing else tells of it.
  * X is held in 22 bits (two fp16 numbers); a Gram matrix and its polynomial are held as
  * their diagonals in fp32 and the rest in fp16; products accumulate in fp32 on the tensor
  * cores.  Products take 11 bits of an operand, and 22 (of X, and of the Gram matrices' rest) in
