@@ -23,7 +23,9 @@
 //
 // h goes between the two in two numbers of the weights' type, hi + lo, as two
 // rows of the second product: rounded to one it would cost the result as much again as its
-// own rounding.
+// own rounding.  In fp16 lo is held times 2^11, which brings it to hi's range: as it is it
+// would be a subnormal number, or nothing, beside an h below 0.1 (of an h of about 2e-6 the
+// result was off by twenty times its rounding).
 #include <algorithm>
 
 #include "rows_dev.cuh"
@@ -47,6 +49,10 @@ constexpr int BLOCKS = 2;   // an SM
 // eight a token, 1 token 124 / 132 (105), 8 tokens 802 / 832 (755), 32 tokens 2243 / 2310 (2143).
 // (Two slices instead of three with NB = 1: 118, 366, 126, 765 and 2173.  One block of twice
 // the slices: 130 and 2373; three blocks of two: 117, 351, 119, 780 and 2357.)
+
+// h - hi is at most 2^-11 of hi, so that this many times of it is no larger; bf16 has fp32's range
+template <typename T>
+constexpr float LO_SCALE = std::is_same<T, __half>::value ? 2048.f : 1.f;
 
 struct Args {
   const uint16_t *x, *wg, *wu, *wd, *wr;
@@ -436,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) up_kernel(const Args p) {
       const float h = gate / (1.f + expf(-gate)) * up;
       const T hi = Elem<T>::put(h);
       const float back = Elem<T>::get(hi);
-      const T lo = Elem<T>::put(fabsf(back) <= 3.4028235e38f ? h - back : 0.f);  // (beyond the type's range hi alone is infinite)
+      const T lo = Elem<T>::put(fabsf(back) <= 3.4028235e38f ? (h - back) * LO_SCALE<T> : 0.f);  // (beyond the type's range hi alone is infinite)
       uint16_t *to = p.h + (int64_t)(now.first + row) * p.I + now.c + c;
       to[0] = *reinterpret_cast<const uint16_t *>(&hi);
       to[(int64_t)p.T * p.k * p.I] = *reinterpret_cast<const uint16_t *>(&lo);
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) down_kernel(const Args p) {
           for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float v = acc[j][i] + __shfl_xor_sync(0xffffffffu, acc[j][i], 2);  // hi + lo: columns 4 apart
+              const float v = acc[j][i] + __shfl_xor_sync(0xffffffffu, acc[j][i], 2) * (1.f / LO_SCALE<T>);  // hi + lo: columns 4 apart (lanes t < 2 have hi)
               const int row = 4 * j + 2 * t + (i & 1);
               if (t < 2 && row < now.n) mine[r.token[now.first + row] * DOWN_FEATURES + g + 8 * (i >> 1)] += r.weight[now.first + row] * v;
             }

@@ -789,8 +789,8 @@ int moe_orthogonalize_workspace(int32_t count, int32_t rows, int32_t cols, uint6
  *   not matter before or after.
  * tokens in [0, 32], hidden and inter multiples of 8 up to 65536, num_experts <= 1024,
  * topk <= min(num_experts, 32).  Products accumulate in fp32; h is held in two
- * numbers of dtype (bf16: 16 bits; fp16: 22, and infinite beyond its range); out is
- * rounded once.  Only the chosen experts' weights are read.
+ * numbers of dtype (bf16: 16 bits; fp16: 22, or to 2^-36 where it is below 2^-14, and
+ * infinite beyond its range); out is rounded once.  Only the chosen experts' weights are read.
  */
 typedef struct sym_few_tokens {
   int32_t tokens, hidden, inter, num_experts, topk, dtype;
