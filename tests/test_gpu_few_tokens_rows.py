@@ -50,3 +50,34 @@ class Layer:
 def test_small_values_between_the_products(T, H, I, E, k, dt, x):
     """h far below one, down to what fp16 cannot hold; down weights that bring the rows back up."""
     Layer(T, H, I, E, k, dt, x, down=min(100.0, x ** -1.5)).check()
+
+
+# long contractions (the most slices, the deepest pipelines), many experts a token, blocks that share experts, odd slices
+SIZES = [(1, 4096, 1544, 8, 2), (3, 16384, 24, 2, 1), (1, 24, 16384, 2, 2), (2, 7168, 264, 33, 32), (6, 2048, 1408, 60, 6), (5, 1032, 520, 24, 3),
+         (9, 520, 1032, 9, 4), (32, 1096, 72, 40, 32), (1, 72, 4104, 1024, 4), (32, 512, 4096, 4, 2), (17, 264, 136, 3, 2), (2, 14336, 512, 4, 2),
+         (1, 128, 2048, 64, 8), (32, 7168, 2048, 16, 2)]
+
+
+@pytest.mark.parametrize("T,H,I,E,k", SIZES)
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_rows_are_off_by_their_rounding(T, H, I, E, k, dt):
+    Layer(T, H, I, E, k, dt).check()
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_where_the_high_parts_cancel(dt):
+    """Down weights of -1 and 1 over two features whose h differ by an eighth of the high part's last
+    place: what is left is the low parts' difference (a power of two, so it is exact)."""
+    T, H, I = 1, 64, 64
+    layer = Layer(T, H, I, 1, 1, dt)
+    layer.x.zero_()
+    layer.x[0, 0], layer.x[0, 1] = 8.0, 1.0
+    layer.wg.zero_(), layer.wu.zero_(), layer.wd.zero_()
+    layer.wg[0, :2, 0] = 4.0  # silu(32): 32 to fp32's last place
+    layer.wu[0, 0, 0] = layer.wu[0, 1, 0] = 1.0 / 8
+    step = 2.0 ** -7 if dt == BF else 2.0 ** -10  # hi's last place, of 1
+    layer.wu[0, 1, 1] = step / 8
+    layer.wd[0, :, 0], layer.wd[0, :, 1] = -1.0, 1.0
+    out = layer.call()[2].double()
+    want = 32 * step / 8
+    assert bool(((out - want).abs() <= want * 2.0 ** -12).all()), (out[0, :4].tolist(), want)
