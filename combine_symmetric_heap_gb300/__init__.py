@@ -678,8 +678,11 @@ def moe_layer_norm(x, h=None, w=None, b=None, add=None, sum=None, mean=None, rst
     ap, al = _mat(add, shape, dt, dev, where)
     sp, sl = _mat(sum, shape, dt, dev, where)
     hp, hl = _mat(h, shape, dt, dev, where)
-    a = _pack_layer_norm(rows, cols, _DTYPES.get(dt, -1), xp, ap, _line(w, cols, dt, dev, where), _line(b, cols, dt, dev, where),
-                         sp, hp, _line(mean, rows, f32, dev, where), _line(rstd, rows, f32, dev, where), xl, al, sl, hl, eps, 0)
+    try:
+        a = _pack_layer_norm(rows, cols, _DTYPES.get(dt, -1), xp, ap, _line(w, cols, dt, dev, where), _line(b, cols, dt, dev, where),
+                             sp, hp, _line(mean, rows, f32, dev, where), _line(rstd, rows, f32, dev, where), xl, al, sl, hl, eps, 0)
+    except struct.error as e:  # a number that its field does not hold, or none
+        _need(False, where, str(e))
     _check(lib().moe_layer_norm(a, _stream_of(stream, dev)), where)
 
 
@@ -704,9 +707,12 @@ def moe_layer_norm_bwd(dh, s, mean, rstd, dx=None, w=None, dsum=None, dw=None, d
     gp, gl = _mat(dsum, shape, dt, dev, where)
     xp, xl = _mat(dx, shape, dt, dev, where)
     wp, wn = _work(work, dev, where)
-    a = _pack_layer_norm_grad(rows, cols, _DTYPES.get(dt, -1), hp, sp, gp, _line(w, cols, dt, dev, where),
-                              _line(mean, rows, f32, dev, where), _line(rstd, rows, f32, dev, where), xp,
-                              _line(dw, cols, dt, dev, where), _line(db, cols, dt, dev, where), hl, sl, gl, xl, wp, wn)
+    try:
+        a = _pack_layer_norm_grad(rows, cols, _DTYPES.get(dt, -1), hp, sp, gp, _line(w, cols, dt, dev, where),
+                                  _line(mean, rows, f32, dev, where), _line(rstd, rows, f32, dev, where), xp,
+                                  _line(dw, cols, dt, dev, where), _line(db, cols, dt, dev, where), hl, sl, gl, xl, wp, wn)
+    except struct.error as e:  # a number that its field does not hold, or none
+        _need(False, where, str(e))
     _check(lib().moe_layer_norm_bwd(a, _stream_of(stream, dev)), where)
 
 
@@ -745,9 +751,12 @@ def moe_orthogonalize(g, out, work, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0
     gs, gl = _batch(g, where)
     os_, ol = _batch(out, where)
     wp, wn = _work(work, dev, where)
-    a = _pack_orthogonalize(shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], steps, _DTYPES.get(g.dtype, -1),
-                            _DTYPES.get(out.dtype, -1), *coeffs, eps, scale, wait_timeout_us, _word(status, dev, where), gp, op, gs, gl,
-                            os_, ol, wp, wn)
+    try:
+        a = _pack_orthogonalize(shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], steps, _DTYPES.get(g.dtype, -1),
+                                _DTYPES.get(out.dtype, -1), *coeffs, eps, scale, wait_timeout_us, _word(status, dev, where), gp, op, gs, gl,
+                                os_, ol, wp, wn)
+    except struct.error as e:  # a number that its field does not hold, or none
+        _need(False, where, str(e))
     _check(lib().moe_orthogonalize(a, _stream_of(stream, dev)), where)
 
 
@@ -791,9 +800,12 @@ def moe_few_tokens(x, w_gate, w_up, w_down, logits, idx, w, out, work, w_router=
     xp, xl = _mat(x, shape, dt, dev, where)
     op, ol = _mat(out, shape, dt, dev, where)
     rp, rl = _mat(w_router, (experts, hidden), dt, dev, where)
-    a = _pack_few_tokens(tokens, hidden, inter, experts, chosen[1], _DTYPES.get(dt, -1), xp, gp, up, dp, rp,
-                         _at(logits, (tokens, experts), f32, dev, where), _at(idx, chosen, torch.int32, dev, where),
-                         _at(w, chosen, f32, dev, where), op, xl, ol, gg, gl, ug, ul, dg, dl, rl, wp, wn)
+    try:
+        a = _pack_few_tokens(tokens, hidden, inter, experts, chosen[1], _DTYPES.get(dt, -1), xp, gp, up, dp, rp,
+                             _at(logits, (tokens, experts), f32, dev, where), _at(idx, chosen, torch.int32, dev, where),
+                             _at(w, chosen, f32, dev, where), op, xl, ol, gg, gl, ug, ul, dg, dl, rl, wp, wn)
+    except struct.error as e:  # a number that its field does not hold, or none
+        _need(False, where, str(e))
     _check(lib().moe_few_tokens(a, _stream_of(stream, dev)), where)
 
 
