@@ -207,8 +207,10 @@ __device__ __forceinline__ bool word_inside(const void *from, int64_t ld, int ro
 // with the sum 174 us, 60000 x 1001 195).  The weights are turned to the vectors once, into
 // shared memory.  So 16384 x 4095 140 us, 414 with single elements; 8192 x 7167 110 and 392;
 // 60000 x 1001 118 and 251; fp32 8192 x 4095 112 and 219, 4099 x 1001 18 and 19.  Whole vectors
-// take 85 us: what is left are instructions and the registers (the most threads with little
-// spilled; with 1024 and 64 registers 131, 109 and fp32 143 us, with 640 137, 132 and 101).
+// take 85 us; without the sum 16384 x 4095 96 us, 60000 x 1001 77, 16384 x 4096 52.  What is left is latency: 20 warps
+// an SM, each of which reads, reduces twice and stores a row before it asks for the next (issue slots
+// half used, DRAM 46% busy, 3.7 of the 9.8 cycles between a warp's instructions a wait for loads).  The
+// threads are the most with little spilled; with 1024 and 64 registers 131, 109 and fp32 143 us, with 640 137, 132 and 101.
 constexpr int SHIFT_THREADS = 768;
 template <typename T, int V, int NV, bool WARP, bool SHIFT>
 __global__ void __launch_bounds__(WARP ? 128 : SHIFT ? SHIFT_THREADS : 1024, WARP && SHIFT ? 4 : 1) layer_norm_held_kernel(const Fwd p) {
@@ -794,7 +796,8 @@ static BwdShape bwd_shape(int64_t rows, int cols, int each, int num_sms) {
 }
 
 // The staged form of it: 16 columns a thread, two or three pairs of rows in shared memory; rows
-// off 16-byte boundaries that are longer than the register form's are shared by two to eight blocks
+// off 16-byte boundaries that are longer than the register form's are shared by two to eight blocks.
+// Aligned fp32 rows, of those with the stream's gradient: 8192 x 4608 93 us (floor 90), x 6144 165 (120), x 8192 196 (160).
 constexpr int STAGED_SMEM = 220 * 1024;
 struct StagedShape {
   int threads, ranks, blocks, pairs;  // blocks: times ranks; pairs 0: does not fit

@@ -669,8 +669,9 @@ int moe_block_norm_workspace(int64_t rows, int32_t cols, int64_t gate_rows, uint
  * one (what lies between a tensor's rows may then be read, and is not used).  h or sum
  * may be x or add, but sum is not h.
  * The variance is the mean of the squared distances from the mean, all in fp32.
- * rows < 2^30, cols <= 65536; eps >= 0.  A row whose s holds an infinity or NaN,
- * and only that row, has results that are NaN.
+ * rows < 2^30, cols <= 65536; eps >= 0; |s| up to 1.7e38 (half of fp32's range: distances
+ * from the mean are taken in it).  A row whose s holds an infinity or NaN, and only that
+ * row, has an rstd and an h of NaN (its mean is what its sum gives).
  */
 typedef struct sym_layer_norm {
   int64_t rows;
